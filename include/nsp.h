@@ -7,7 +7,10 @@
  *     stream, forward and backward, with grouped-query heads;
  *   - the chunk-partial attention of ring-style sequence parallelism (a query
  *     range against a key range) and the log-sum-exp merge of such partials;
- *   - the Ulysses seq-sharded -> head-sharded layout permutation.
+ *   - the Ulysses seq-sharded -> head-sharded layout permutation;
+ *   - a differential attention layer's operators: rotary positions, the
+ *     learned difference weight, differential attention forward and backward,
+ *     and the norm of each head's output.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -542,6 +545,165 @@ int32_t nsp_seq2head_permute_validate(const void* in, const void* out, int64_t T
 int32_t nsp_seq2head_permute_groups(const void* in, void* out, int32_t B, int64_t L, int32_t H,
                                     int32_t d, int32_t K, int32_t elem_bytes, int32_t inverse,
                                     nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The operators between the projections of a differential attention layer
+ * on a packed stream.  No page has a counterpart of them; they follow the
+ * conventions above (caller-owned buffers, caller stream, nothing allocated,
+ * host errors before anything is enqueued).
+ *
+ * Rotary positions
+ * ----------------
+ * Every head of every token is rotated by angles that grow with the token's
+ * position inside its own document.  With rot rotated columns of a head's d,
+ * pair i < rot / 2 is columns (i, i + rot / 2) (interleaved = 0) or
+ * (2 i, 2 i + 1) (interleaved = 1), and for x_a, x_b of the pair
+ *   angle = position * freqs[i],
+ *   y_a = mscale (x_a cos - x_b sin),  y_b = mscale (x_a sin + x_b cos);
+ * columns [rot, d) are copied.  inverse = 1 rotates by -angle (times mscale
+ * as well): the transpose, which takes gradients of y to gradients of x.
+ *
+ *   tensors: HOST array of n (1..4) descriptors, read during the call: in and
+ *     out device [len, heads, d] of io_dtype, tokens in_stride / out_stride
+ *     elements apart (0: heads * d), so that in or out can be columns of a
+ *     fused projection's tensor.  in and out may be the same buffer with the
+ *     same stride (in place); any other overlap of an input or an output with
+ *     an output is NSP_ERR_INVALID.  groups = P > 1: the rotated side (out,
+ *     or in when inverse = 1) is in the head-group-major layout
+ *     [P][len][heads / P][d] of nsp_attn_fwd_headgroups, packed.
+ *   positions: device int32 [len], or NULL: row r is then global token
+ *     start + r of the stream, its position the distance from its document's
+ *     start in cu_seqlens (device int32 [ndoc + 1]; unused, may be NULL, when
+ *     positions is given).  Rows at or past cu_seqlens[ndoc] are not written.
+ *     The contents of cu_seqlens are not checked here (there is no status
+ *     word); they never lead outside the buffers.
+ *   freqs: device float64 [rot / 2], radians per position.  The angle's whole
+ *     turns are taken off in integer arithmetic: it is exact to 2^-32 turns
+ *     at any position.
+ *   d in 2..1024; rot even, 2..d; sums and products in float32.  Pointers
+ *     need their element's alignment; 16-byte aligned ones with strides, d
+ *     and rot (halves: rot / 2) of whole 16-byte pieces are several times
+ *     faster.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t in_stride, out_stride;
+  int32_t heads, groups;
+} nsp_rope_tensor_t;
+
+int32_t nsp_rope(const nsp_rope_tensor_t* tensors, int32_t n, const int32_t* cu_seqlens,
+                 int32_t ndoc, const int32_t* positions, int64_t start, int64_t len, int32_t d,
+                 int32_t rot, const double* freqs, int32_t interleaved, float mscale,
+                 int32_t inverse, int32_t io_dtype, nsp_stream_t stream);
+
+/* Frequencies for nsp_rope, written to HOST freqs_host [rot / 2]:
+ *   f_i = base^(-2 i / rot), and for contexts longer than the trained one
+ *   NSP_ROPE_LINEAR: f_i / factor;
+ *   NSP_ROPE_BASE:   base * factor^(rot / (rot - 2)) in place of base (the
+ *                    slowest pair slows by factor, the fastest stays);
+ *   NSP_ROPE_PARTS:  k f_i + (1 - k) f_i / factor, where pair i turns
+ *                    n_i = orig_len f_i / 2 pi times over the trained context
+ *                    and k = clamp((n_i - low) / (high - low), 0, 1).
+ * factor >= 1; unused arguments of a kind are ignored.  Host only. */
+typedef enum {
+  NSP_ROPE_PLAIN = 0, NSP_ROPE_LINEAR = 1, NSP_ROPE_BASE = 2, NSP_ROPE_PARTS = 3
+} nsp_rope_scaling;
+
+int32_t nsp_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double low,
+                       double high, double orig_len, double* freqs_host);
+
+/* ------------------------------------------------------------------------
+ * Weight of the second map, from four learned vectors of each head:
+ *   lambda[h] = exp(<q1, k1>) - exp(<q2, k2>) + init.
+ *   q1, k1, q2, k2: device [n][dl] of io_dtype, n = heads, or n = 1: one set
+ *   that every head shares.  lambda: device [heads] of io_dtype.
+ * The backward writes dq1 = g e1 k1, dk1 = g e1 q1, dq2 = -g e2 k2,
+ * dk2 = -g e2 q2 ([n][dl], io_dtype), e1, e2 the two exponentials and g =
+ * dlambda[h] (io_dtype), or its sum over the heads when n = 1.  Sums in
+ * float32.  Pointers need their element's alignment.
+ * ---------------------------------------------------------------------- */
+int32_t nsp_diff_lambda_fwd(const void* q1, const void* k1, const void* q2, const void* k2,
+                            int32_t n, int32_t dl, int32_t heads, float init, int32_t io_dtype,
+                            void* lambda, nsp_stream_t stream);
+
+int32_t nsp_diff_lambda_bwd(const void* dlambda, const void* q1, const void* k1, const void* q2,
+                            const void* k2, int32_t n, int32_t dl, int32_t heads,
+                            int32_t io_dtype, void* dq1, void* dk1, void* dq2, void* dk2,
+                            nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Differential attention of a whole packed stream, document-masked as
+ * nsp_attn_fwd with q_start = kv_start = 0, q_len = kv_len = T.  Columns
+ * [0, d/2) of a head's q and k are its first map, [d/2, d) its second:
+ *   x^m_j = scale <q^m[t,h], k^m[j,g]>,  lse[h,m,t] = ln sum_j exp(x^m_j),
+ *   o^m[t,h] = sum_j exp(x^m_j - lse[h,m,t]) v[j,g],
+ *   out = o^1 - lambda o^2,                       g = h / (Hq / Hkv).
+ *   q, out, out2: device [T, Hq, d]; k, v: device [T, Hkv, d]; d in {64, 128}.
+ *   lambda: device [Hq][n_lambda] of io_dtype; n_lambda = 1 (one of each
+ *     head) or T (one of each head and token).
+ *   out2: o^2, or NULL when no backward follows.  lse: device float32
+ *     [Hq][2][T], or NULL likewise.  out and out2 are of io_dtype.
+ * All pointers 16-byte aligned, bf16 out and out2 32-byte aligned.  Errors
+ * and the status word as nsp_attn_fwd.  A non-finite value in one document's
+ * v may reach rows of documents that share a 128-token tile with it (the
+ * product with a zero probability is not finite).
+ * ---------------------------------------------------------------------- */
+size_t nsp_diff_attn_fwd_workspace_size(int64_t T);
+
+int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const void* lambda,
+                          int64_t n_lambda, const int32_t* cu_seqlens, int32_t ndoc, int64_t T,
+                          int32_t Hq, int32_t Hkv, int32_t d, float scale, int32_t causal,
+                          int32_t io_dtype, void* out, void* out2, float* lse, void* workspace,
+                          size_t workspace_bytes, nsp_stream_t stream);
+
+/* Its backward.  out, out2 and lse as the forward wrote them; dout and dq
+ * device [T, Hq, d], dk and dv [T, Hkv, d], dlambda [Hq][n_lambda], all of
+ * io_dtype.  With p^m the probabilities recomputed from lse,
+ * delta^m = <dout, o^m> and dp_j = <dout, v_j>:
+ *   ds^1 = p^1 (dp - delta^1),  ds^2 = -lambda p^2 (dp - delta^2),
+ *   dq^m = scale sum_j ds^m_j k^m_j,  dk^m = scale sum_t ds^m_t q^m_t,
+ *   dv = sum_t (p^1_t - lambda p^2_t) dout_t  (dk, dv over the group's heads),
+ *   dlambda = -delta^2 of each token, or its sum over the tokens.
+ * Every output is written whole, and sums run in one fixed order: results are
+ * the same bits on every run. */
+size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t d);
+
+int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const void* lambda,
+                          int64_t n_lambda, const void* out, const void* out2, const void* dout,
+                          const float* lse, const int32_t* cu_seqlens, int32_t ndoc, int64_t T,
+                          int32_t Hq, int32_t Hkv, int32_t d, float scale, int32_t causal,
+                          int32_t io_dtype, void* dq, void* dk, void* dv, void* dlambda,
+                          void* workspace, size_t workspace_bytes, nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of every head's row (the difference of two maps is
+ * normed head by head before the output projection; q and k before the
+ * rotation), scaled and optionally gated:
+ *   y = scale * weight * x / sqrt(mean(x^2) + eps) [* sigmoid(gate)].
+ *   x: device [tokens, heads, d], tokens x_stride elements apart (0:
+ *     heads * d); weight: device [d] or NULL (ones); gate: device
+ *     [tokens, heads, d] or NULL; y: device [tokens, heads, d]; all of
+ *     io_dtype, statistics and products in float32.
+ *   d <= 512 with whole 16-byte pieces (bf16: a multiple of 8, float32: of 4),
+ *     other d are NSP_ERR_UNSUPPORTED; eps > 0.  Pointers 16-byte aligned,
+ *     x_stride a multiple of 16 bytes.  y may be gate's or a packed x's
+ *     buffer.
+ * The backward writes dx (packed), dgate (required with a gate) and, unless
+ * NULL, dweight [d]; dweight needs nsp_head_norm_bwd_workspace_size bytes of
+ * workspace and is summed in one fixed order.  dx may be dy's buffer, dgate
+ * gate's.
+ * ---------------------------------------------------------------------- */
+int32_t nsp_head_norm_fwd(const void* x, int64_t x_stride, const void* weight, const void* gate,
+                          int64_t tokens, int32_t heads, int32_t d, float eps, float scale,
+                          int32_t io_dtype, void* y, nsp_stream_t stream);
+
+size_t nsp_head_norm_bwd_workspace_size(int64_t tokens, int32_t heads, int32_t d);
+
+int32_t nsp_head_norm_bwd(const void* x, int64_t x_stride, const void* weight, const void* gate,
+                          const void* dy, int64_t tokens, int32_t heads, int32_t d, float eps,
+                          float scale, int32_t io_dtype, void* dx, void* dgate, void* dweight,
+                          void* workspace, size_t workspace_bytes, nsp_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Status word of the last call that used `workspace`.  Synchronises `stream`

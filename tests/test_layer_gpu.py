@@ -1,0 +1,576 @@
+"""Differential attention layer on the GPU against the float64 oracle.
+
+Tolerances are derived, element by element, from roundings: u is half a step
+of the output's type (bf16 2^-8, float32 2^-24, relative to the value), e =
+2^-24 that of the float32 arithmetic in between.  A product with bf16
+probabilities or dS (the tensor-core path rounds both once) is off by at most
+u times the sum of the terms' magnitudes, plus the float32 terms.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import oracle.layer as L
+
+pytestmark = pytest.mark.gpu
+
+E = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def half_step(dt):
+    return torch.finfo(dt).eps / 2
+
+
+def f64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+def randn(seed, *shape, dt=BF16, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dt).cuda()
+
+
+def cu_of(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def assert_within(got, ref, tol, what):
+    got = f64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    assert np.isfinite(got).all(), what
+    over = np.abs(got - ref) - tol
+    i = np.unravel_index(int(np.argmax(over)), over.shape)
+    assert over[i] <= 0, f"{what} at {i}: {got[i]} against {ref[i]}, off by more than {np.broadcast_to(tol, ref.shape)[i]}"
+
+
+# ----------------------------------------------------------------------------- rotary positions
+
+def check_rope(got, x, angles, rot, inter, m, inverse, dt, what, angle_err=0.0):
+    x = f64(x) if isinstance(x, torch.Tensor) else x
+    ref = L.rope(x, angles, rot, inter, m, inverse)
+    # sine and cosine: 2 ulp of sincospi, the angle's float32 rounding (pi e) and
+    # its 2^-32 turns; the factor, two products and the sum: 16 e in all of m (|a| + |b|)
+    a = np.abs(x)
+    pair = a.copy()
+    ia = np.arange(0, rot, 2) if inter else np.arange(rot // 2)
+    ib = ia + 1 if inter else ia + rot // 2
+    pair[..., ia] = pair[..., ib] = a[..., ia] + a[..., ib]
+    pair[..., rot:] = 0
+    assert_within(got, ref, half_step(dt) * np.abs(ref) + (16 * E + angle_err) * abs(m) * pair, what)
+    if rot < x.shape[-1]:
+        np.testing.assert_array_equal(f64(got)[..., rot:], x[..., rot:])
+
+
+LENS = [3, 0, 1, 70, 0, 26]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("d,rot,hq,hkv", [(128, 128, 8, 2), (64, 32, 3, 1), (96, 96, 2, 2), (128, 64, 33, 4),
+                                          (64, 64, 1, 1), (80, 20, 2, 1), (7, 6, 3, 2)])
+def test_rope(nsp, dt, inter, inverse, d, rot, hq, hkv):
+    T = sum(LENS)
+    q, k = randn(1, T, hq, d, dt=dt), randn(2, T, hkv, d, dt=dt)
+    fr = nsp.rope_freqs(rot, base=500.0, device="cuda")
+    cu = cu_of(LENS)
+    a = L.rope_angles(L.rope_positions(cu.cpu().numpy(), T), fr.cpu().numpy())
+    qo, ko = nsp.rope(q, k, cu, fr, layout="interleaved" if inter else "half", mscale=1.25,
+                      inverse=inverse)
+    check_rope(qo, q, a, rot, inter, 1.25, inverse, dt, "q")
+    check_rope(ko, k, a, rot, inter, 1.25, inverse, dt, "k")
+
+
+def test_rope_far_positions(nsp):
+    """Explicit positions to the end of int32, negative ones too: the angle
+    error is that of the float64 frequency (2^-52 turns a turn) alone."""
+    pos = torch.tensor([0, 1, 399999, 2 ** 30 + 7, 2 ** 31 - 1, -1, -2 ** 31], dtype=torch.int32, device="cuda")
+    fr = nsp.rope_freqs(64, base=1e6, device="cuda")
+    x = randn(3, 7, 2, 64, dt=F32)
+    got, none = nsp.rope(x, None, None, fr, positions=pos)
+    assert none is None
+    err = np.abs(pos.cpu().numpy().astype(np.float64))[:, None] * fr.cpu().numpy() * 2.0 ** -51
+    err = np.concatenate([err, err], -1)[:, None]
+    check_rope(got, x, L.rope_angles(pos.cpu().numpy(), fr.cpu().numpy()), 64, False, 1.0, False, F32,
+               "far", err)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_fused_views_in_place_groups(nsp, inter):
+    """Columns of a fused projection in, packed, head-grouped and in-place out;
+    every form the same bits; the columns in between untouched."""
+    T, hq, hkv, d = sum(LENS), 8, 2, 128
+    lay = "interleaved" if inter else "half"
+    cu, fr = cu_of(LENS), nsp.rope_freqs(d, device="cuda")
+    qkv = randn(4, T, hq + 2 * hkv, d)
+    q, k = qkv[:, :hq], qkv[:, hq:hq + hkv]
+    ref_q, ref_k = nsp.rope(q.contiguous(), k.contiguous(), cu, fr, layout=lay)
+    got_q, got_k = nsp.rope(q, k, cu, fr, layout=lay)
+    assert torch.equal(got_q, ref_q) and torch.equal(got_k, ref_k)
+    for p in (2, 4):
+        gq, _ = nsp.rope(q, k, cu, fr, layout=lay, q_groups=p)
+        assert torch.equal(gq, nsp.seq2head(ref_q, p))
+        back, _ = nsp.rope(gq, ref_k, cu, fr, layout=lay, q_groups=p, inverse=True)
+        plain, _ = nsp.rope(ref_q, ref_k, cu, fr, layout=lay, inverse=True)
+        assert torch.equal(back, plain)
+    before = qkv.clone()
+    nsp.rope(q, k, cu, fr, layout=lay, out=(q, k))
+    assert torch.equal(qkv[:, :hq], ref_q) and torch.equal(qkv[:, hq:hq + hkv], ref_k)
+    assert torch.equal(qkv[:, hq + hkv:], before[:, hq + hkv:])
+
+
+def test_rope_odd_addresses(nsp):
+    """Strides and addresses that are no whole 16 bytes give the same bits."""
+    T, h, d = 29, 3, 64
+    cu, fr = cu_of([29]), nsp.rope_freqs(d, device="cuda")
+    x = randn(5, T, h, d)
+    ref, _ = nsp.rope(x, None, cu, fr)
+    wide = torch.zeros((T, h * d + 3), dtype=BF16, device="cuda")
+    view = wide[:, 1:1 + h * d].unflatten(1, (h, d))
+    view.copy_(x)
+    got, _ = nsp.rope(view, None, cu, fr)
+    assert torch.equal(got, ref)
+
+
+def test_rope_rows_behind_the_last_document_and_shards(nsp):
+    T, h, d = 100, 4, 64
+    cu, fr = cu_of([40, 30]), nsp.rope_freqs(d, device="cuda")
+    x = randn(6, T, h, d)
+    out = torch.full_like(x, 7.0)
+    nsp.rope(x, None, cu, fr, out=(out, None))
+    assert (out[70:] == 7).all()
+    ref, _ = nsp.rope(x[:70].contiguous(), None, cu, fr)
+    assert torch.equal(out[:70], ref)
+    for s, e in ((0, 33), (33, 70)):                 # a sequence shard's own rows
+        part, _ = nsp.rope(x[s:e], None, cu, fr, start=s)
+        assert torch.equal(part, ref[s:e])
+    one, _ = nsp.rope(x[:1], None, cu, fr)
+    assert torch.equal(one, ref[:1])
+    none, _ = nsp.rope(x[:0], None, cu, fr)
+    assert none.shape == (0, h, d)
+
+
+# ----------------------------------------------------------------------------- difference weight
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("n,heads,dl", [(1, 1, 1), (1, 37, 64), (16, 16, 64), (5, 5, 33), (3, 3, 300)])
+def test_diff_lambda(nsp, dt, n, heads, dl):
+    vec = [randn(10 + i, n, dl, dt=dt, scale=0.1) for i in range(4)]
+    ref = [f64(x) for x in vec]
+    lam = nsp.diff_lambda(*vec, heads=heads, lambda_init=0.8)
+    # a dot product of dl terms and exp (2 ulp): the exponentials are off by
+    # (dl + 4) e of themselves at most
+    e1, e2 = (np.exp((ref[2 * i] * ref[2 * i + 1]).sum(-1)) for i in range(2))
+    dot = sum(np.abs(ref[2 * i] * ref[2 * i + 1]).sum(-1) for i in range(2)) * dl + 6
+    want = L.diff_lambda(*ref, heads, 0.8)
+    assert_within(lam, want, half_step(dt) * np.abs(want) + E * dot * (e1 + e2 + 1), "lambda")
+    g = randn(20, heads, dt=dt)
+    grads = nsp.diff_lambda_bwd(g, *vec)
+    gs = np.abs(f64(g)).sum() if n == 1 else np.abs(f64(g))
+    for i, (a, b) in enumerate(zip(grads, L.diff_lambda_bwd(f64(g), *ref))):
+        other = np.abs(ref[i ^ 1]) * ((e1, e2)[i // 2] * gs * (dot + heads + 4))[:, None]
+        assert_within(a, b, half_step(dt) * np.abs(b) + E * other, f"gradient {i}")
+        assert a.shape == vec[i].shape
+
+
+# ----------------------------------------------------------------------------- head norm
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("gate,weight", [(True, True), (False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("tokens,heads,d", [(1, 1, 128), (37, 3, 64), (129, 5, 128), (300, 2, 512), (11, 7, 8),
+                                            (50, 4, 96), (1000, 16, 256)])
+def test_head_norm(nsp, dt, gate, weight, tokens, heads, d):
+    x, dy = randn(30, tokens, heads, d, dt=dt), randn(31, tokens, heads, d, dt=dt)
+    g = randn(32, tokens, heads, d, dt=dt) if gate else None
+    w = randn(33, d, dt=dt) if weight else None
+    kw = dict(eps=1e-5, scale=0.2)
+    rx, rdy = f64(x), f64(dy)
+    rw, rg = (None if t is None else f64(t) for t in (w, g))
+    y = nsp.head_norm(x, w, g, **kw)
+    ref = L.head_norm(rx, rw, rg, 1e-5, 0.2)
+    # the sum of d squares (16 partial sums and 5 shuffles at most: 40 e), rsqrt
+    # 2 ulp, sigmoid (exp 2 + 1.2 |g| ulp, sum, quotient) and four products
+    c = (64 + 4 * (np.abs(rg).max() if gate else 0)) * E
+    assert_within(y, ref, (half_step(dt) + c) * np.abs(ref), "y")
+    dx, dw, dg = nsp.head_norm_bwd(x, dy, w, g, **kw)
+    rdx, rdw, rdg = L.head_norm_bwd(rx, rdy, rw, rg, 1e-5, 0.2)
+    r = 1 / np.sqrt((rx * rx).mean(-1, keepdims=True) + 1e-5)
+    s = 1.0 if rg is None else 1 / (1 + np.exp(-rg))
+    u = np.abs(0.2 * rdy * (1.0 if rw is None else rw) * s)
+    n = np.abs(rx * r)
+    terms = r * (u + n * (u * n).mean(-1, keepdims=True))
+    assert_within(dx, rdx, half_step(dt) * np.abs(rdx) + c * terms, "dx")
+    if weight:
+        # a column's terms pass through at most 32 + 16 + 76 + 8 sums here
+        mag = (np.abs(0.2 * rdy * rx * r) * s).sum((0, 1))
+        assert_within(dw, rdw, half_step(dt) * np.abs(rdw) + (c + 132 * E) * mag, "dw")
+    else:
+        assert dw is None
+    if gate:
+        # 1 - sigmoid of a large gate keeps only sigmoid's absolute error
+        big = np.abs(0.2 * rdy * rx * r * (1.0 if rw is None else rw)) * s
+        assert_within(dg, rdg, half_step(dt) * np.abs(rdg) + c * big, "dgate")
+    else:
+        assert dg is None
+
+
+def test_head_norm_views_and_edges(nsp):
+    """Columns of a fused tensor; zero rows and extreme gates; no rows; results
+    the same bits twice."""
+    qkv = randn(40, 65, 10, 64)
+    x, w = qkv[:, 2:6], randn(41, 64)
+    dy, g = randn(42, 65, 4, 64), randn(43, 65, 4, 64)
+    assert torch.equal(nsp.head_norm(x, w, g), nsp.head_norm(x.contiguous(), w, g))
+    for a, b in zip(nsp.head_norm_bwd(x, dy, w, g), nsp.head_norm_bwd(x.contiguous(), dy, w, g)):
+        assert torch.equal(a, b)
+    z = torch.zeros(3, 2, 64, device="cuda")
+    far = torch.full_like(z, 200.0)
+    assert (nsp.head_norm(z) == 0).all() and (nsp.head_norm(z + 1, gate=-far) == 0).all()
+    np.testing.assert_allclose(f64(nsp.head_norm(z + 1, gate=far, eps=1e-12)), 1, rtol=1e-6)
+    dx, _, dg = nsp.head_norm_bwd(z + 1, z + 1, gate=far)
+    assert torch.isfinite(dx).all() and (dg == 0).all()
+    e = x[:0]
+    assert nsp.head_norm(e, w).shape == (0, 4, 64)
+    dx, dw, _ = nsp.head_norm_bwd(e, dy[:0], w)
+    assert dx.shape == (0, 4, 64) and (dw == 0).all()
+
+
+# ----------------------------------------------------------------------------- differential attention
+
+def diff_inputs(seed, lens, hq, hkv, d, dt, tokens, scale=1.0):
+    T = sum(lens)
+    g = torch.Generator().manual_seed(seed)
+    lam = (torch.rand((hq, T if tokens else 1), generator=g) * 1.2 - 0.3).to(dt).cuda()
+    return (randn(seed + 1, T, hq, d, dt=dt, scale=scale), randn(seed + 2, T, hkv, d, dt=dt, scale=scale),
+            randn(seed + 3, T, hkv, d, dt=dt), lam, randn(seed + 4, T, hq, d, dt=dt), cu_of(lens))
+
+
+def diff_bounds(q, k, v, lam, do, cu, scale, causal, dt):
+    """The oracle's results and how far each may be off, element by element."""
+    T, Hq, d = q.shape
+    G = Hq // k.shape[1]
+    P, lse = L.diff_maps(q, k, cu, scale, causal)
+    out, out2, _ = L.diff_attn_fwd(q, k, v, lam, cu, scale, causal)
+    w = np.broadcast_to(lam, (Hq, T))
+    V, K = np.repeat(v, G, 1), np.repeat(k, G, 1)
+    h = half_step(dt)
+    u = h if dt == BF16 else 0.0                      # one rounding of P and of dS
+    # a score is off by d/2 + 2 float32 roundings of its terms' magnitudes; exp
+    # turns that into a relative error of P
+    mag = np.zeros((Hq, 2, T))
+    for m in range(2):
+        c = slice(m * d // 2, (m + 1) * d // 2)
+        s = scale * np.einsum("ihc,jhc->hij", np.abs(q[..., c]), np.abs(K[..., c]))
+        mag[:, m] = np.where(P[m] > 0, s, 0).max(-1)
+    rel = E * ((d // 2 + 2) * mag + 64)               # of P, per row
+    tol_lse = rel + 4 * E * np.abs(lse)
+    A1, A2 = (np.einsum("hij,jhd->ihd", P[m], np.abs(V)) for m in range(2))
+    r1, r2 = rel[:, 0].T[..., None], rel[:, 1].T[..., None]
+    lw = np.abs(w).T[..., None]
+    # a row's sum of exponentials adds as much again, float32 sums over the keys e each
+    acc = T * E
+    tol_o2 = (u + 2 * r2 + acc) * A2 + h * np.abs(out2)
+    tol_out = (u + 2 * r1 + acc) * A1 + lw * (u + 2 * r2 + acc) * A2 + h * np.abs(out)
+    if do is None:
+        return (out, out2, lse), (tol_out, tol_o2, tol_lse)
+    grads = L.diff_attn_bwd(q, k, v, lam, do, cu, scale, causal)
+    ado = np.abs(do)
+    d2_err = (ado * (tol_o2 + d * E * np.abs(out2))).sum(-1).T                # [Hq, T]
+    d1_err = (ado * (tol_out + d * E * np.abs(out))).sum(-1).T + np.abs(w) * d2_err
+    tq, tk, tv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    for hh in range(Hq):
+        g = hh // G
+        dp = do[:, hh] @ v[:, g].T
+        dp_err = d * E * ado[:, hh] @ np.abs(v[:, g]).T
+        pc = (u + acc) * (P[0, hh] + np.abs(w[hh])[:, None] * P[1, hh])
+        pc += rel[hh, 0][:, None] * P[0, hh] + (rel[hh, 1] * np.abs(w[hh]))[:, None] * P[1, hh]
+        tv[:, g] += pc.T @ ado[:, hh]
+        for m, sign, derr in ((0, np.ones(T), d1_err[hh]), (1, np.abs(w[hh]), d2_err[hh])):
+            c = slice(m * d // 2, (m + 1) * d // 2)
+            diff = np.abs(dp - (P[m, hh] * dp).sum(-1, keepdims=True))
+            # P's own error, P and dS rounded (u each), delta's and dP's errors
+            es = sign[:, None] * P[m, hh] * ((2 * u + 2 * rel[hh, m][:, None] + acc) * diff
+                                             + derr[:, None] + dp_err)
+            tq[:, hh, c] += scale * es @ np.abs(k[:, g, c])
+            tk[:, g, c] += scale * es.T @ np.abs(q[:, hh, c])
+    tl = d2_err + T * E * np.abs(out2 * do).sum(-1).T
+    if grads[3].shape[1] != T or T == 1:
+        tl = tl.sum(-1, keepdims=True)
+    tols = [t + h * np.abs(g) for t, g in zip((tq, tk, tv, tl), grads)]
+    return (out, out2, lse) + tuple(grads), (tol_out, tol_o2, tol_lse) + tuple(tols)
+
+
+DIFF_CASES = [
+    ([1], 1, 1, 128), ([1], 2, 1, 64), ([5, 0, 1, 130], 4, 2, 128), ([128, 129], 2, 2, 64),
+    ([127, 1, 128, 2], 6, 2, 128), ([33] * 9, 5, 1, 64), ([300], 3, 3, 128), ([40, 0, 0, 333, 27], 4, 1, 128),
+]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("tokens", [False, True])
+@pytest.mark.parametrize("lens,hq,hkv,d", DIFF_CASES)
+def test_diff_attention(nsp, dt, causal, tokens, lens, hq, hkv, d):
+    q, k, v, lam, do, cu = diff_inputs(50, lens, hq, hkv, d, dt, tokens)
+    scale = (d // 2) ** -0.5
+    ref, tol = diff_bounds(*(f64(t) for t in (q, k, v, lam, do)), cu.cpu().numpy(), scale, causal, dt)
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, causal=causal, save=True)
+    assert torch.equal(out, nsp.diff_attn_fwd(q, k, v, lam, cu, causal=causal))
+    grads = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu, causal=causal)
+    for name, a, b, t in zip(("out", "out2", "lse", "dq", "dk", "dv", "dlam"),
+                             (out, out2, lse) + grads, ref, tol):
+        assert_within(a, b, t, name)
+        # as a whole within the library's bar for gradients, where roundings do
+        # not outweigh the result: one token alone has P = 1 and dP = delta, so
+        # its dq and dk are zero and what comes out is delta's rounding (within
+        # the elements' tolerance above, which no multiple of zero can be)
+        if np.linalg.norm(b) > np.linalg.norm(t):
+            assert np.linalg.norm(f64(a) - b) <= 1e-2 * np.linalg.norm(b), name
+    for a, b in zip(grads, nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu, causal=causal)):
+        assert torch.equal(a, b)                      # one fixed order of sums
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_diff_attention_growing_scores(nsp, dt):
+    """Scores that climb along the document (the running maximum is replaced
+    again and again) and lambda of both signs."""
+    lens, d = [700], 128
+    q, k, v, lam, do, cu = diff_inputs(60, lens, 2, 1, d, dt, True)
+    ramp = torch.linspace(0, 6, 700, device="cuda")[:, None]
+    k[:, :, 0] = (k[:, :, 0].float() + 4 * ramp).to(dt)
+    k[:, :, 64] = (k[:, :, 64].float() - 4 * ramp).to(dt)
+    q[:, :, 0] = (q[:, :, 0].float().abs() + 1).to(dt)
+    q[:, :, 64] = (q[:, :, 64].float().abs() + 1).to(dt)
+    ref, tol = diff_bounds(*(f64(t) for t in (q, k, v, lam, do)), [0, 700], 0.125, True, dt)
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    grads = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+    for name, a, b, t in zip(("out", "out2", "lse", "dq", "dk", "dv", "dlam"),
+                             (out, out2, lse) + grads, ref, tol):
+        assert_within(a, b, t, name)
+
+
+def test_diff_attention_equals_attention(nsp):
+    """lambda = 0 leaves the first map: ordinary attention of 64-column heads
+    on v's column halves."""
+    lens = [200, 3, 57]
+    q, k, v, lam, do, cu = diff_inputs(70, lens, 4, 2, 128, BF16, False)
+    out = nsp.diff_attn_fwd(q, k, v, torch.zeros_like(lam), cu)
+    for half in range(2):
+        o, _ = nsp.attn_fwd(q[..., :64].contiguous(), k[..., :64].contiguous(),
+                            v[..., 64 * half:64 * half + 64].contiguous(), cu, scale=0.125)
+        # both round P (u each) and the result
+        assert (f64(out[..., 64 * half:64 * half + 64]) - f64(o)).max() <= 4 * 2.0 ** -8 * 4
+
+
+def test_diff_attention_differences(nsp):
+    """Directional differences of the float32 forward: the step h leaves an
+    h^2 / 6 third-derivative term (third derivatives of this loss along a unit
+    direction are below its norm), the two losses e of their terms' sum."""
+    lens = [40, 0, 77]
+    q, k, v, lam, do, cu = diff_inputs(80, lens, 4, 2, 64, F32, True)
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    grads = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+    for i, g in enumerate(grads):
+        dirn = randn(90 + i, *g.shape, dt=F32)
+        dirn /= dirn.norm()
+        step, f = 1e-2, []
+        for e in (step, -step):
+            x = [q, k, v, lam]
+            x[i] = x[i] + e * dirn
+            o = nsp.diff_attn_fwd(*x, cu)
+            f.append((o.double() * do.double()).sum().item())
+        noise = 64 * E * (out.double() * do.double()).norm().item() / step
+        want = (g.double() * dirn.double()).sum().item()
+        assert abs((f[0] - f[1]) / (2 * step) - want) <= noise + step ** 2 * g.norm().item(), i
+
+
+def test_diff_attention_status(nsp):
+    """cu_seqlens shorter than the stream, or decreasing: recorded, nothing written."""
+    q, k, v, lam, do, _ = diff_inputs(100, [100], 2, 1, 64, BF16, False)
+    good = cu_of([100])
+    _, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, good, save=True)
+    for bad in ([0, 60], [0, 70, 50, 100], [1, 100]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        ws = torch.empty(nsp.load().nsp_diff_attn_fwd_workspace_size(100), dtype=torch.uint8, device="cuda")
+        nsp.diff_attn_fwd(q, k, v, lam, cu, workspace=ws)
+        assert nsp.nsp_status_query(ws) == nsp.NSP_ERR_INVALID
+        ws = torch.empty(nsp.load().nsp_diff_attn_bwd_workspace_size(100, 2, 64), dtype=torch.uint8,
+                         device="cuda")
+        nsp.diff_attn_bwd(q, k, v, lam, q, out2, do, lse, cu, workspace=ws)
+        assert nsp.nsp_status_query(ws) == nsp.NSP_ERR_INVALID
+    # a longer cu_seqlens: the stream is the start of it
+    cu = torch.tensor([0, 30, 170], dtype=torch.int32, device="cuda")
+    a = nsp.diff_attn_fwd(q, k, v, lam, cu, causal=False)
+    assert torch.equal(a, nsp.diff_attn_fwd(q, k, v, lam, cu_of([30, 70]), causal=False))
+
+
+def test_diff_attention_empty_stream(nsp):
+    q, k, v, lam, do, _ = diff_inputs(110, [0], 2, 1, 64, BF16, False)
+    cu = cu_of([0])
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    assert out.shape == (0, 2, 64) and lse.shape == (2, 2, 0)
+    dq, dk, dv, dl = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+    assert dq.shape == (0, 2, 64) and (dl == 0).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_diff_attention_guard_zones(nsp, dt):
+    """Nothing around the outputs and the workspaces is written."""
+    lens, hq, hkv, d = [70, 1, 130], 4, 2, 128
+    q, k, v, lam, do, cu = diff_inputs(120, lens, hq, hkv, d, dt, False)
+    T, lib = sum(lens), nsp.load()
+    pad = 4096
+
+    def guarded(nbytes):
+        buf = torch.full((pad + (nbytes + 255) // 256 * 256 + pad,), 0xA5, dtype=torch.uint8, device="cuda")
+        return buf, buf[pad:pad + nbytes]
+
+    def check(buf, n):
+        assert (buf[:pad] == 0xA5).all() and (buf[pad + n:] == 0xA5).all()
+
+    es = q.element_size()
+    sizes = [T * hq * d * es, T * hq * d * es, hq * 2 * T * 4, lib.nsp_diff_attn_fwd_workspace_size(T),
+             T * hq * d * es, T * hkv * d * es, T * hkv * d * es, hq * es,
+             lib.nsp_diff_attn_bwd_workspace_size(T, hq, d)]
+    bufs = [guarded(n) for n in sizes]
+    p = [b[1].data_ptr() for b in bufs]
+    io, st = nsp._DTYPES[dt], torch.cuda.current_stream().cuda_stream
+    assert lib.nsp_diff_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), 1, cu.data_ptr(),
+                                 len(lens), T, hq, hkv, d, 0.125, 1, io, p[0], p[1], p[2], p[3], sizes[3],
+                                 st) == 0
+    assert lib.nsp_diff_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), 1, p[0], p[1],
+                                 do.data_ptr(), p[2], cu.data_ptr(), len(lens), T, hq, hkv, d, 0.125, 1, io,
+                                 p[4], p[5], p[6], p[7], p[8], sizes[8], st) == 0
+    torch.cuda.synchronize()
+    for (buf, _), n in zip(bufs, sizes):
+        check(buf, n)
+
+
+# ----------------------------------------------------------------------------- together
+
+def layer_forward(nsp, x, cu, fr):
+    q, k = nsp.rope(x["q"], x["k"], cu, fr)
+    lam = nsp.diff_lambda(*x["vec"], heads=q.shape[1], lambda_init=0.5)
+    out, out2, lse = nsp.diff_attn_fwd(q, k, x["v"], lam, cu, save=True)
+    return q, k, lam, out, out2, lse, nsp.head_norm(out, x["w"], x["gate"], scale=0.5)
+
+
+def layer_backward(nsp, x, saved, dy, cu, fr):
+    q, k, lam, out, out2, lse, _ = saved
+    dout, dw, dg = nsp.head_norm_bwd(out, dy, x["w"], x["gate"], scale=0.5)
+    dq, dk, dv, dl = nsp.diff_attn_bwd(q, k, x["v"], lam, out, out2, dout, lse, cu)
+    dvec = nsp.diff_lambda_bwd(dl, *x["vec"])
+    dq, dk = nsp.rope(dq, dk, cu, fr, inverse=True)
+    return (dq, dk, dv, dw, dg) + dvec
+
+
+def layer_inputs(lens, hq, hkv, d, dt):
+    T = sum(lens)
+    qkv = randn(200, T, hq + 2 * hkv, d, dt=dt)
+    return {"q": qkv[:, :hq], "k": qkv[:, hq:hq + hkv], "v": qkv[:, hq + hkv:].contiguous(),
+            "vec": [randn(201 + i, hq, d // 2, dt=dt, scale=0.1) for i in range(4)],
+            "w": randn(210, d, dt=dt), "gate": randn(211, T, hq, d, dt=dt)}
+
+
+def test_layer_forward_and_gradients(nsp):
+    """The whole layer in float32 against the oracle's chain: the gradients
+    pass five operators, each within a few e of its terms; 2e-5 of each
+    tensor's norm leaves a factor of ten over the measured float32 chains of
+    the separate tests."""
+    lens, hq, hkv, d = [50, 0, 1, 90], 4, 2, 64
+    x, cu = layer_inputs(lens, hq, hkv, d, F32), cu_of(lens)
+    fr = nsp.rope_freqs(d, device="cuda")
+    saved = layer_forward(nsp, x, cu, fr)
+    dy = randn(220, sum(lens), hq, d, dt=F32)
+    got = (saved[-1],) + layer_backward(nsp, x, saved, dy, cu, fr)
+
+    c = cu.cpu().numpy()
+    a = L.rope_angles(L.rope_positions(c, sum(lens)), fr.cpu().numpy())
+    rq, rk = (L.rope(f64(x[n]), a, d) for n in ("q", "k"))
+    vec, v, w, g = [f64(t) for t in x["vec"]], f64(x["v"]), f64(x["w"]), f64(x["gate"])
+    lam = L.diff_lambda(*vec, hq, 0.5)[:, None]
+    s = (d // 2) ** -0.5
+    out, _, _ = L.diff_attn_fwd(rq, rk, v, lam, c, s)
+    y = L.head_norm(out, w, g, 1e-6, 0.5)
+    dout, dw, dg = L.head_norm_bwd(out, f64(dy), w, g, 1e-6, 0.5)
+    dq, dk, dv, dl = L.diff_attn_bwd(rq, rk, v, lam, dout, c, s)
+    ref = (y, L.rope(dq, a, d, inverse=True), L.rope(dk, a, d, inverse=True), dv, dw, dg) + \
+        L.diff_lambda_bwd(dl, *vec)
+    for i, (p, r) in enumerate(zip(got, ref)):
+        assert np.linalg.norm(f64(p) - r) <= 2e-5 * np.linalg.norm(r), i
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_layer_captured_and_on_another_stream(nsp, dt):
+    """Captured into a graph and replayed on new inputs, and run on a side
+    stream: the same bits as eager calls."""
+    lens, hq, hkv, d = [64, 3, 150], 4, 2, 128
+    x, cu = layer_inputs(lens, hq, hkv, d, dt), cu_of(lens)
+    fr = nsp.rope_freqs(d, device="cuda")
+    dy = randn(230, sum(lens), hq, d, dt=dt)
+
+    def step():
+        saved = layer_forward(nsp, x, cu, fr)
+        return (saved[-1],) + layer_backward(nsp, x, saved, dy, cu, fr)
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    y = nsp.head_norm(x["gate"], x["w"], stream=side)
+    side.synchronize()
+    for a, b in zip(want, other):
+        assert torch.equal(a, b)
+    assert torch.equal(y, nsp.head_norm(x["gate"], x["w"]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    x["v"].mul_(-0.5)
+    x["gate"].neg_()
+    want = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_layer_refusals_on_the_gpu(nsp):
+    q, k, v, lam, do, cu = diff_inputs(240, [20], 4, 2, 64, BF16, False)
+    with pytest.raises(ValueError):
+        nsp.diff_attn_fwd(q.transpose(0, 1), k, v, lam, cu)
+    with pytest.raises(ValueError):
+        nsp.diff_attn_fwd(q, k, v[:-1], lam, cu)
+    with pytest.raises(TypeError):
+        nsp.diff_attn_fwd(q, k.float(), v, lam, cu)
+    with pytest.raises(TypeError):
+        nsp.diff_attn_fwd(q, k, v, lam, cu.long())
+    with pytest.raises(ValueError):
+        nsp.diff_attn_fwd(q, k, v, lam[:2], cu)
+    with pytest.raises(ValueError):
+        nsp.diff_attn_fwd(q, k, v, lam.cpu(), cu)
+    with pytest.raises(nsp.NspError):
+        nsp.diff_attn_fwd(q, k, v, lam, cu, scale=-1.0)
+    with pytest.raises(nsp.NspError):
+        nsp.diff_attn_fwd(q, k, v, lam, cu, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    fr = nsp.rope_freqs(64, device="cuda")
+    with pytest.raises(ValueError):
+        nsp.rope(q, k, None, fr)
+    with pytest.raises(ValueError):
+        nsp.rope(q, k, cu, fr, q_groups=3)
+    with pytest.raises(TypeError):
+        nsp.rope(q, k, cu, fr.float())
+    with pytest.raises(ValueError):
+        nsp.rope(q.transpose(1, 2), k, cu, fr)
+    with pytest.raises(nsp.NspError):                 # overlapping, not in place
+        nsp.rope(q[:-1], None, cu, fr, out=(q[1:], None))
+    with pytest.raises(nsp.NspError):
+        nsp.head_norm(q, eps=0.0)
+    with pytest.raises(ValueError):
+        nsp.head_norm(q, weight=lam[:, 0])

@@ -1,0 +1,458 @@
+// Differential attention on the CUDA cores, in true float32 arithmetic (no
+// TF32).
+//
+// Per document of the packed stream, with map m of a head reading columns
+// [m D/2, (m + 1) D/2) of q and k:
+//   P_m = softmax over the visible keys of scale q_m k_m^T,  O_m = P_m V,
+//   out = O_1 - lambda O_2.
+// Backward, with delta_m = <dout, O_m> and dP = dout V^T (one product for both
+// maps):
+//   dS_1 = P_1 (dP - delta_1),  dS_2 = -lambda P_2 (dP - delta_2),
+//   dQ_m = scale dS_m K_m,  dK_m = scale dS_m^T Q_m,  dV = (P_1 - lambda P_2)^T dout.
+//
+// Bound: the FP32 pipes and shared-memory reads.  Every product is tiled in
+// registers over 256 threads (16 x 16) from float32 tiles in shared memory,
+// rows padded by 4 floats so that 16 rows read at one column fall into
+// different banks.  Forward: 64 query rows by 32 keys; both maps' scores,
+// online softmax (Milakov and Gimelshein) and outputs stay in the registers of
+// one thread row.  Backward: one kernel over key tiles (dK, dV), one over
+// query tiles (dQ), each recomputing both maps' P and dP, so every gradient
+// is summed in one fixed order without atomics.
+#include "layer.cuh"
+
+namespace nsp {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float4 fma4(float s, const float4& x, const float4& y) {
+  return make_float4(fmaf(s, x.x, y.x), fmaf(s, x.y, y.y), fmaf(s, x.z, y.z), fmaf(s, x.w, y.w));
+}
+__device__ __forceinline__ float4 scaled(float s, const float4& x) {
+  return make_float4(s * x.x, s * x.y, s * x.z, s * x.w);
+}
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float acc) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, acc))));
+}
+
+__device__ __forceinline__ float4 ld4(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void st4(float* p, const float4& x) {
+  *reinterpret_cast<float4*>(p) = x;
+}
+__device__ __forceinline__ void st4(__nv_bfloat16* p, const float4& x) {
+  st_out(p, x.x); st_out(p + 1, x.y); st_out(p + 2, x.z); st_out(p + 3, x.w);
+}
+
+// ROWS rows of one head (row stride `stride` elements) into padded shared
+// rows; rows at or past `end` read as zero.
+template <int D, int ROWS, typename E>
+__device__ __forceinline__ void load_tile(float (*dst)[D + 4], const E* src, int64_t stride,
+                                          int64_t row0, int64_t end) {
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row0 + r < end) x = ld4(src + (row0 + r) * stride + c);
+    *reinterpret_cast<float4*>(&dst[r][c]) = x;
+  }
+}
+
+// Visible keys [lo, hi) of stream row t.
+__device__ __forceinline__ void visible(const AttnProblem& p, int64_t t, int& lo, int& hi) {
+  const int b = doc_of(p.cu, p.ndoc, t);
+  lo = __ldg(p.cu + b);
+  hi = p.causal ? (int)t + 1 : (int)min((int64_t)__ldg(p.cu + b + 1), p.kv_len);
+}
+
+template <typename E>
+__device__ __forceinline__ float lambda_of(const DiffProblem& a, int h, int64_t t) {
+  const int64_t i = (int64_t)h * a.n_lambda + (a.n_lambda > 1 ? t : 0);
+  return to_f(reinterpret_cast<const E*>(a.lambda)[i]);
+}
+
+// ---------------------------------------------------------------- forward
+
+constexpr int kFwdM = 64, kFwdN = 32;
+
+template <int D>
+struct FwdSmem {
+  float q[kFwdM][D + 4];
+  float k[kFwdN][D + 4];
+  float v[kFwdN][D + 4];
+  float p[2][kFwdM][kFwdN + 4];
+  int lo[kFwdM], hi[kFwdM];
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProblem a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem_raw);
+  const AttnProblem& p = a.p;
+  if (status_bad(p.hdr)) return;
+  constexpr int kCols = D / 64;                    // float4 columns of a thread
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int h = blockIdx.y, g = h / (p.Hq / p.Hkv);
+  // longest rows first: causal tiles late in the stream see the most keys
+  const int64_t row0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * kFwdM;
+  const int64_t T = p.q_len;
+  const E* Q = reinterpret_cast<const E*>(p.q) + (int64_t)h * D;
+  const E* K = reinterpret_cast<const E*>(p.k) + (int64_t)g * D;
+  const E* V = reinterpret_cast<const E*>(p.v) + (int64_t)g * D;
+  const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
+
+  load_tile<D, kFwdM>(sm.q, Q, qs, row0, T);
+  if (threadIdx.x < kFwdM) {
+    int lo = 0, hi = 0;
+    if (row0 + threadIdx.x < T) visible(p, row0 + threadIdx.x, lo, hi);
+    sm.lo[threadIdx.x] = lo;
+    sm.hi[threadIdx.x] = hi;
+  }
+  __syncthreads();
+  // the tile's keys: from its first row's document to its last row's end
+  const int last = (int)min((int64_t)kFwdM, T - row0) - 1;
+  const int key_lo = sm.lo[0] / kFwdN * kFwdN;
+  const int key_hi = sm.hi[last];
+  int lo[4], hi[4];
+  float m[2][4], l[2][4];
+  float4 o[2][4][kCols];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = sm.lo[ty * 4 + i];
+    hi[i] = sm.hi[ty * 4 + i];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      m[t][i] = -INFINITY;
+      l[t][i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[t][i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  const float sl2 = p.scale * kLog2e;
+
+  for (int j0 = key_lo; j0 < key_hi; j0 += kFwdN) {
+    __syncthreads();
+    load_tile<D, kFwdN>(sm.k, K, ks, j0, p.kv_len);
+    load_tile<D, kFwdN>(sm.v, V, ks, j0, p.kv_len);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      // scores of rows 4 ty .. + 3 against keys tx and tx + 16
+      float s[4][2] = {};
+#pragma unroll 4
+      for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 4) {
+        const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
+        const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][c]);
+          s[i][0] = dot4(x, k0, s[i][0]);
+          s[i][1] = dot4(x, k1, s[i][1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = j0 + tx;
+        float s0 = key >= lo[i] && key < hi[i] ? s[i][0] * sl2 : -INFINITY;
+        float s1 = key + 16 >= lo[i] && key + 16 < hi[i] ? s[i][1] * sl2 : -INFINITY;
+        float mx = fmaxf(s0, s1);
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float mn = fmaxf(m[t][i], mx);
+        const float mb = mn == -INFINITY ? 0.f : mn;
+        const float corr = exp2f(m[t][i] - mb);
+        s0 = exp2f(s0 - mb);
+        s1 = exp2f(s1 - mb);
+        m[t][i] = mn;
+        l[t][i] = l[t][i] * corr + (s0 + s1);      // this thread's two key columns only
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[t][i][c] = scaled(corr, o[t][i][c]);
+        sm.p[t][ty * 4 + i][tx] = s0;
+        sm.p[t][ty * 4 + i][tx + 16] = s1;
+      }
+    }
+    __syncwarp();                                   // a row's P is written and read by one half warp
+#pragma unroll 2
+    for (int j = 0; j < kFwdN; j += 4) {
+      float4 v[4][kCols];
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          v[jj][c] = *reinterpret_cast<const float4*>(&sm.v[j + jj][c * 64 + tx * 4]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 w = *reinterpret_cast<const float4*>(&sm.p[t][ty * 4 + i][j]);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            o[t][i][c] = fma4(w.w, v[3][c], fma4(w.z, v[2][c], fma4(w.y, v[1][c],
+                              fma4(w.x, v[0][c], o[t][i][c]))));
+        }
+    }
+  }
+
+  E* O = reinterpret_cast<E*>(p.out);
+  E* O2 = reinterpret_cast<E*>(a.out2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + ty * 4 + i;
+    float inv[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], w);
+      inv[t] = l[t][i] > 0.f ? 1.f / l[t][i] : 0.f;
+      if (row < T && tx == 0 && p.lse != nullptr)
+        p.lse[((int64_t)h * 2 + t) * T + row] = (m[t][i] + log2f(l[t][i])) * kLn2;
+    }
+    if (row >= T) continue;
+    const float lam = lambda_of<E>(a, h, row);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      const int64_t off = row * qs + (int64_t)h * D + c * 64 + tx * 4;
+      const float4 x = o[0][i][c], y = o[1][i][c];
+      const float4 o2 = make_float4(y.x * inv[1], y.y * inv[1], y.z * inv[1], y.w * inv[1]);
+      st4(O + off, make_float4(x.x * inv[0] - lam * o2.x, x.y * inv[0] - lam * o2.y,
+                               x.z * inv[0] - lam * o2.z, x.w * inv[0] - lam * o2.w));
+      if (O2 != nullptr) st4(O2 + off, o2);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+constexpr int kBwdTile = 32;          // query rows and keys of a tile
+
+template <int D>
+struct BwdSmem {
+  float q[kBwdTile][D + 4], dout[kBwdTile][D + 4];
+  float k[kBwdTile][D + 4], v[kBwdTile][D + 4];
+  float ds[2][kBwdTile][kBwdTile + 4];            // [map][row of the output][summed index]
+  float pc[kBwdTile][kBwdTile + 4];               // (P_1 - lambda P_2)^T: [key][query]
+  float nlse2[2][kBwdTile], delta[2][kBwdTile], coef[kBwdTile];
+  int lo[kBwdTile], hi[kBwdTile];
+};
+
+// P and dS of a 32 x 32 tile, written for the product that follows: KEY puts
+// dS and P_1 - lambda P_2 in rows of keys (dK, dV), otherwise dS in rows of
+// queries (dQ).  Threads take rows 2 ty, 2 ty + 1 and keys tx, tx + 16.
+template <int D, bool KEY>
+__device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  float s[2][2][2] = {}, dp[2][2] = {};
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll 4
+    for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 4) {
+      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
+      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
+      const float4 v0 = *reinterpret_cast<const float4*>(&sm.v[tx][c]);
+      const float4 v1 = *reinterpret_cast<const float4*>(&sm.v[tx + 16][c]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * 2 + i][c]);
+        const float4 y = *reinterpret_cast<const float4*>(&sm.dout[ty * 2 + i][c]);
+        s[t][i][0] = dot4(x, k0, s[t][i][0]);
+        s[t][i][1] = dot4(x, k1, s[t][i][1]);
+        dp[i][0] = dot4(y, v0, dp[i][0]);
+        dp[i][1] = dot4(y, v1, dp[i][1]);
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = ty * 2 + i;
+    const float coef = sm.coef[r];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int kk = tx + 16 * j;
+      const int64_t key = key0 + kk;
+      const bool vis = key >= sm.lo[r] && key < sm.hi[r];
+      const float p1 = vis ? exp2f(fmaf(s[0][i][j], sl2, sm.nlse2[0][r])) : 0.f;
+      const float p2 = vis ? coef * exp2f(fmaf(s[1][i][j], sl2, sm.nlse2[1][r])) : 0.f;
+      const float d1 = vis ? p1 * (dp[i][j] - sm.delta[0][r]) : 0.f;
+      const float d2 = vis ? p2 * (dp[i][j] - sm.delta[1][r]) : 0.f;
+      if constexpr (KEY) {
+        sm.ds[0][kk][r] = d1;
+        sm.ds[1][kk][r] = d2;
+        sm.pc[kk][r] = p1 + p2;
+      } else {
+        sm.ds[0][r][kk] = d1;
+        sm.ds[1][r][kk] = d2;
+      }
+    }
+  }
+}
+
+// acc[i][c] += sum_j w[2 ty + i][j] x[j][col + 64 c]: a 32 x D product of a
+// 32 x 32 tile in shared memory; map_of picks the tile of the column's map.
+template <int D, typename W>
+__device__ __forceinline__ void tile_product(float4 (&acc)[2][(D + 63) / 64], W&& w_of,
+                                             float (*x)[D + 4]) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll 2
+  for (int j = 0; j < kBwdTile; j += 4) {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const int col = c * 64 + tx * 4;
+      float4 b[4];
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) b[jj] = *reinterpret_cast<const float4*>(&x[j + jj][col]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 w = *reinterpret_cast<const float4*>(w_of(col) + (ty * 2 + i) * (kBwdTile + 4) + j);
+        acc[i][c] = fma4(w.w, b[3], fma4(w.z, b[2], fma4(w.y, b[1], fma4(w.x, b[0], acc[i][c]))));
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_rows(BwdSmem<D>& sm, const DiffProblem& a, int h, int64_t row0) {
+  const AttnProblem& p = a.p;
+  const int r = threadIdx.x;
+  if (r >= kBwdTile) return;
+  const int64_t t = row0 + r;
+  int lo = 0, hi = 0;
+  if (t < p.q_len) {
+    visible(p, t, lo, hi);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      sm.nlse2[m][r] = a.nlse2[((int64_t)h * 2 + m) * a.Tp + t];
+      sm.delta[m][r] = a.delta[((int64_t)h * 2 + m) * a.Tp + t];
+    }
+    sm.coef[r] = a.coef[(int64_t)h * a.Tp + t];
+  }
+  sm.lo[r] = lo;
+  sm.hi[r] = hi;
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const DiffProblem a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
+  const AttnProblem& p = a.p;
+  if (status_bad(p.hdr)) return;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int g = blockIdx.y, G = p.Hq / p.Hkv;
+  const int64_t T = p.q_len, key0 = (int64_t)blockIdx.x * kBwdTile;
+  const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
+  load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const E*>(p.k) + (int64_t)g * D, ks, key0, T);
+  load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const E*>(p.v) + (int64_t)g * D, ks, key0, T);
+  const int64_t key1 = min(key0 + kBwdTile, T) - 1;
+  const int b0 = doc_of(p.cu, p.ndoc, key0), b1 = doc_of(p.cu, p.ndoc, key1);
+  const int64_t r_lo = p.causal ? key0 : (int64_t)__ldg(p.cu + b0);
+  const int64_t r_hi = min((int64_t)__ldg(p.cu + b1 + 1), T);
+  float4 dk[2][D / 64] = {}, dv[2][D / 64] = {};
+  for (int hh = 0; hh < G; ++hh) {
+    const int h = g * G + hh;
+    for (int64_t r0 = r_lo; r0 < r_hi; r0 += kBwdTile) {
+      __syncthreads();
+      load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const E*>(p.q) + (int64_t)h * D, qs, r0, T);
+      load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const E*>(a.dout) + (int64_t)h * D, qs, r0, T);
+      load_rows<D>(sm, a, h, r0);
+      __syncthreads();
+      tile_ds<D, true>(sm, key0, p.scale * kLog2e);
+      __syncthreads();
+      tile_product<D>(dk, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.q);
+      tile_product<D>(dv, [&](int) { return &sm.pc[0][0]; }, sm.dout);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t key = key0 + ty * 2 + i;
+    if (key >= T) continue;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const int64_t off = key * ks + (int64_t)g * D + c * 64 + tx * 4;
+      st4(reinterpret_cast<E*>(a.dk) + off, scaled(p.scale, dk[i][c]));
+      st4(reinterpret_cast<E*>(a.dv) + off, dv[i][c]);
+    }
+  }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffProblem a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
+  const AttnProblem& p = a.p;
+  if (status_bad(p.hdr)) return;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int h = blockIdx.y, g = h / (p.Hq / p.Hkv);
+  const int64_t T = p.q_len, row0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * kBwdTile;
+  const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
+  load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const E*>(p.q) + (int64_t)h * D, qs, row0, T);
+  load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const E*>(a.dout) + (int64_t)h * D, qs, row0, T);
+  load_rows<D>(sm, a, h, row0);
+  __syncthreads();
+  const int last = (int)min((int64_t)kBwdTile, T - row0) - 1;
+  const int key_lo = sm.lo[0] / kBwdTile * kBwdTile, key_hi = sm.hi[last];
+  float4 dq[2][D / 64] = {};
+  for (int j0 = key_lo; j0 < key_hi; j0 += kBwdTile) {
+    __syncthreads();
+    load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const E*>(p.k) + (int64_t)g * D, ks, j0, T);
+    load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const E*>(p.v) + (int64_t)g * D, ks, j0, T);
+    __syncthreads();
+    tile_ds<D, false>(sm, j0, p.scale * kLog2e);
+    __syncthreads();
+    tile_product<D>(dq, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.k);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = row0 + ty * 2 + i;
+    if (row >= T) continue;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      st4(reinterpret_cast<E*>(a.dq) + row * qs + (int64_t)h * D + c * 64 + tx * 4,
+          scaled(p.scale, dq[i][c]));
+  }
+}
+
+template <typename K>
+cudaError_t launch(K kern, dim3 grid, size_t smem, const DiffProblem& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, smem, s>>>(a);
+  count_launches(1);
+  count_path(false);
+  return cudaGetLastError();
+}
+
+template <typename E, int D>
+cudaError_t fwd(const DiffProblem& a, cudaStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.p.q_len, kFwdM), a.p.Hq);
+  return launch(diff_fwd_simt_kernel<E, D>, grid, sizeof(FwdSmem<D>), a, s);
+}
+
+template <typename E, int D>
+cudaError_t bwd(const DiffProblem& a, cudaStream_t s) {
+  const unsigned tiles = (unsigned)ceil_div(a.p.q_len, kBwdTile);
+  cudaError_t e =
+      launch(diff_bwd_dkdv_simt_kernel<E, D>, dim3(tiles, a.p.Hkv), sizeof(BwdSmem<D>), a, s);
+  if (e != cudaSuccess) return e;
+  return launch(diff_bwd_dq_simt_kernel<E, D>, dim3(tiles, a.p.Hq), sizeof(BwdSmem<D>), a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s) {
+  using bf = __nv_bfloat16;
+  if (a.p.io_dtype == NSP_BF16) return a.p.d == 128 ? fwd<bf, 128>(a, s) : fwd<bf, 64>(a, s);
+  return a.p.d == 128 ? fwd<float, 128>(a, s) : fwd<float, 64>(a, s);
+}
+
+cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s) {
+  using bf = __nv_bfloat16;
+  if (a.p.io_dtype == NSP_BF16) return a.p.d == 128 ? bwd<bf, 128>(a, s) : bwd<bf, 64>(a, s);
+  return a.p.d == 128 ? bwd<float, 128>(a, s) : bwd<float, 64>(a, s);
+}
+
+}  // namespace nsp

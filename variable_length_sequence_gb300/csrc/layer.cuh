@@ -1,0 +1,133 @@
+// Declarations of the operators around differential attention (rotary
+// positions, the difference weight, the head norm, differential attention
+// itself) and the vector loads and stores their streaming kernels share.
+#pragma once
+
+#include "nsp_internal.cuh"
+
+namespace nsp {
+
+// ---- rotary positions (rope.cu)
+constexpr int kRopeMaxTensors = 4;
+constexpr int kRopeMaxDim = 1024;
+
+struct RopeTensor {
+  const void* in;
+  void* out;
+  int64_t in_stride, out_stride;     // elements between tokens
+  int32_t heads;
+  int32_t in_groups, out_groups;     // > 1: head-group-major [P][len][heads / P][d]
+};
+
+struct RopeArgs {
+  RopeTensor t[kRopeMaxTensors];
+  int32_t n;
+  const int32_t* cu;
+  int32_t ndoc;
+  const int32_t* positions;
+  int64_t start, len;
+  int32_t d, rot, interleaved, inverse;
+  const double* freqs;
+  float mscale;
+};
+cudaError_t launch_rope(const RopeArgs& a, int32_t io_dtype, cudaStream_t s);
+
+// ---- difference weight (diff_lambda.cu)
+cudaError_t launch_diff_lambda(const void* const* v, int32_t n, int32_t dl, int32_t heads,
+                               float init, int32_t io_dtype, void* lambda, cudaStream_t s);
+cudaError_t launch_diff_lambda_bwd(const void* dlambda, const void* const* v, int32_t n, int32_t dl,
+                                   int32_t heads, int32_t io_dtype, void* const* dvec,
+                                   cudaStream_t s);
+
+// ---- head norm (head_norm.cu)
+constexpr int kNormMaxDim = 512;
+
+struct NormArgs {
+  const void *x, *gate, *weight, *dy;
+  void *y, *dx, *dgate, *dweight;
+  int64_t x_stride;                  // elements between tokens of x
+  int64_t tokens;
+  int32_t heads, d;
+  float eps, scale;
+  float* partial;                    // backward: [norm_bwd_blocks][d] weight gradient sums
+};
+int norm_bwd_blocks(int64_t rows);   // upper bound of the backward's grid, whatever the device
+cudaError_t launch_head_norm(const NormArgs& a, int32_t io_dtype, cudaStream_t s);
+cudaError_t launch_head_norm_bwd(const NormArgs& a, int32_t io_dtype, cudaStream_t s);
+
+// ---- differential attention (diff_simt.cu, diff_fwd_tc.cu, diff_bwd_tc.cu)
+// Whole packed stream of T tokens.  q, out, out2, dout, dq: [T, Hq, d]; k, v,
+// dk, dv: [T, Hkv, d]; map m of a head is columns [m d/2, (m + 1) d/2) of q
+// and k; lse: [Hq][2][T]; lambda: [Hq][n_lambda], n_lambda 1 or T.
+struct DiffProblem {
+  AttnProblem p;                     // q, k, v, cu, ranges (the whole stream), heads, header
+  const void* lambda;
+  int64_t n_lambda;
+  void* out2;                        // second map's output (forward: may be null)
+  const void *fout, *dout;           // backward
+  void *dq, *dk, *dv, *dlambda;
+  float *delta, *nlse2, *coef;       // backward workspace: [2 Hq][Tp], [2 Hq][Tp], [Hq][Tp]
+  int64_t Tp;
+};
+cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s);
+cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s);
+// delta, nlse2 and coef of the backward, and dlambda of each token
+cudaError_t launch_diff_prep(const DiffProblem& a, cudaStream_t s);
+// dlambda of each head (n_lambda = 1), from delta
+cudaError_t launch_diff_dlambda(const DiffProblem& a, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// 16 bytes of T as float32 values, and back (round to nearest even).
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  __device__ static __forceinline__ void unpack(const uint4& u, float (&x)[N]) {
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+  }
+  __device__ static __forceinline__ uint4 pack(const float (&x)[N]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
+  }
+};
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ static __forceinline__ void unpack(const uint4& u, float (&x)[N]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static __forceinline__ uint4 pack(const float (&x)[N]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// Data touched once: loaded and stored past L1.  (Not the non-coherent load:
+// an operator may write the buffer it reads.)
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_once(void* p, const uint4& v) {
+  asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+#endif  // __CUDACC__
+
+}  // namespace nsp

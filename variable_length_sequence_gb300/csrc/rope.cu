@@ -1,0 +1,230 @@
+// Rotary positions of a packed stream: every token's heads rotated by angles
+// that grow with the token's position inside its own document.
+//
+// With f_i the frequency of pair i (radians per position) and a = pos f_i,
+//   u = m (x_a cos a - x_b sin a),  w = m (x_a sin a + x_b cos a),
+// and, inverse, the transpose (a -> -a): the backward of the rotation.
+//
+// Angles.  A far position times a frequency near 1 needs more bits than
+// float32 has (position 400000: an angle error of 0.03).  The frequency is
+// converted once per block to a fixed-point fraction of a turn, 2^-64 turns
+// per unit, so that position x frequency is one integer product whose wrap
+// modulo 2^64 is the reduction modulo whole turns, exactly; its top 32 bits,
+// signed, are the angle in [-1/2, 1/2) turns, off by at most 2^-32 turns (and
+// by the float64 frequency's own 2^-53 relative error).
+//
+// Bound: HBM, one read and one write of every element.  A team of threads
+// owns one token and a 16-byte piece of a head each (both pieces of the pair
+// with halves), computes the sines and cosines of its pairs once and walks
+// the token's heads with four heads' loads in flight.  With few tokens the
+// heads of one token are split over several teams, so that a single token
+// still spreads over the GPU.
+#include <algorithm>
+
+#include "layer.cuh"
+
+namespace nsp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeadsInFlight = 4;
+
+// The row of head h at range row t: packed (token stride), or head-group-major.
+__device__ __forceinline__ int64_t row_offset(int64_t t, int h, int64_t stride, int heads,
+                                              int groups, int64_t len, int d) {
+  if (groups <= 1) return t * stride + (int64_t)h * d;
+  const int hpg = heads / groups, g = h / hpg;
+  return (((int64_t)g * len + t) * hpg + (h - g * hpg)) * d;
+}
+
+__device__ __forceinline__ uint64_t fixed_turns(double f) {
+  double x = f * 0.15915494309189533576888;          // 1 / (2 pi)
+  x -= floor(x);
+  return __double2ull_rn(x * 18446744073709551616.0);
+}
+
+__device__ __forceinline__ void turn(int64_t pos, uint64_t fx, float m, bool inverse, float& c,
+                                     float& s) {
+  const int32_t hi = (int32_t)(((uint64_t)pos * fx) >> 32);
+  sincospif((float)hi * 4.656612873077393e-10f, &s, &c);       // 2^-31: half turns
+  c *= m;
+  s *= inverse ? -m : m;
+}
+
+// Position of range row t; false for a row past the last document.
+__device__ __forceinline__ bool position_of(const RopeArgs& a, int64_t t, int64_t& pos) {
+  if (a.positions != nullptr) {
+    pos = __ldg(a.positions + t);
+    return true;
+  }
+  const int64_t g = a.start + t;
+  if (g >= (int64_t)__ldg(a.cu + a.ndoc)) return false;
+  pos = g - (int64_t)__ldg(a.cu + doc_of(a.cu, a.ndoc, g));
+  return true;
+}
+
+// Pieces of one head: INTERLEAVED: rot / N rotated vectors of whole pairs;
+// halves: rot / 2 / N pairs of vectors; then the (d - rot) / N unrotated
+// vectors, copied.
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a,
+                                                        int pieces, int rotated, int total_heads,
+                                                        int hsplit) {
+  constexpr int N = Vec<T>::N;
+  constexpr int kPairs = INTERLEAVED ? N / 2 : N;    // pairs of one rotated piece
+  __shared__ uint64_t s_fx[kRopeMaxDim / 2];
+  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) s_fx[i] = fixed_turns(a.freqs[i]);
+  __syncthreads();
+  const int teams = kThreads / pieces;
+  const int team = threadIdx.x / pieces, u = threadIdx.x - team * pieces;
+  if (team >= teams) return;
+  const int64_t items = a.len * hsplit;
+  const int per = (total_heads + hsplit - 1) / hsplit;
+  const int half = a.rot / 2;
+  for (int64_t item = (int64_t)blockIdx.x * teams + team; item < items;
+       item += (int64_t)gridDim.x * teams) {
+    const int64_t t = item / hsplit;
+    const int part = (int)(item - t * hsplit);
+    int64_t pos;
+    if (!position_of(a, t, pos)) continue;
+    const bool rot = u < rotated;
+    float c[kPairs], s[kPairs];
+    // column of the piece's first vector
+    const int col = rot ? u * N : a.rot + (u - rotated) * N;
+    if (rot) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+        turn(pos, s_fx[u * kPairs + i], a.mscale, a.inverse != 0, c[i], s[i]);
+    }
+    const int h_end = min((part + 1) * per, total_heads);
+    for (int h0 = part * per; h0 < h_end; h0 += kHeadsInFlight) {
+      uint4 x[kHeadsInFlight], y[kHeadsInFlight];
+      T* dst[kHeadsInFlight];
+#pragma unroll
+      for (int i = 0; i < kHeadsInFlight; ++i) {
+        int h = h0 + i, k = 0;
+        if (h >= h_end) break;
+        while (h >= a.t[k].heads) h -= a.t[k++].heads;
+        const RopeTensor& r = a.t[k];
+        const T* src = reinterpret_cast<const T*>(r.in) + col +
+                       row_offset(t, h, r.in_stride, r.heads, r.in_groups, a.len, a.d);
+        dst[i] = reinterpret_cast<T*>(r.out) + col +
+                 row_offset(t, h, r.out_stride, r.heads, r.out_groups, a.len, a.d);
+        x[i] = ld_once(src);
+        if (!INTERLEAVED && rot) y[i] = ld_once(src + half);
+      }
+#pragma unroll
+      for (int i = 0; i < kHeadsInFlight; ++i) {
+        if (h0 + i >= h_end) break;
+        if (!rot) {
+          st_once(dst[i], x[i]);
+          continue;
+        }
+        float p[N], q[N];
+        Vec<T>::unpack(x[i], p);
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j) {
+            q[2 * j] = p[2 * j] * c[j] - p[2 * j + 1] * s[j];
+            q[2 * j + 1] = p[2 * j] * s[j] + p[2 * j + 1] * c[j];
+          }
+          st_once(dst[i], Vec<T>::pack(q));
+        } else {
+          Vec<T>::unpack(y[i], q);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float b = q[j];
+            q[j] = p[j] * s[j] + b * c[j];
+            p[j] = p[j] * c[j] - b * s[j];
+          }
+          st_once(dst[i], Vec<T>::pack(p));
+          st_once(dst[i] + half, Vec<T>::pack(q));
+        }
+      }
+    }
+  }
+}
+
+// Sizes, strides or addresses that do not allow 16-byte pieces: one pair (or
+// one unrotated element) per thread.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_element_kernel(const __grid_constant__ RopeArgs a,
+                                                                int total_heads) {
+  const int half = a.rot / 2, units = half + a.d - a.rot;
+  const int64_t n = a.len * total_heads * units;
+  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n;
+       e += (int64_t)gridDim.x * kThreads) {
+    const int64_t th = e / units, t = th / total_heads;
+    const int u = (int)(e - th * units);
+    int h = (int)(th - t * total_heads), k = 0;
+    int64_t pos;
+    if (!position_of(a, t, pos)) continue;
+    while (h >= a.t[k].heads) h -= a.t[k++].heads;
+    const RopeTensor& r = a.t[k];
+    const T* src = reinterpret_cast<const T*>(r.in) +
+                   row_offset(t, h, r.in_stride, r.heads, r.in_groups, a.len, a.d);
+    T* dst = reinterpret_cast<T*>(r.out) +
+             row_offset(t, h, r.out_stride, r.heads, r.out_groups, a.len, a.d);
+    if (u >= half) {
+      dst[a.rot + u - half] = src[a.rot + u - half];
+      continue;
+    }
+    const int ia = a.interleaved ? 2 * u : u, ib = a.interleaved ? 2 * u + 1 : u + half;
+    float c, s;
+    turn(pos, fixed_turns(a.freqs[u]), a.mscale, a.inverse != 0, c, s);
+    const float xa = to_f(src[ia]), xb = to_f(src[ib]);
+    st_out(dst + ia, xa * c - xb * s);
+    st_out(dst + ib, xa * s + xb * c);
+  }
+}
+
+template <typename T>
+bool vector_ok(const RopeArgs& a) {
+  constexpr int N = 16 / (int)sizeof(T);
+  if (a.d % N != 0 || (a.interleaved ? a.rot : a.rot / 2) % N != 0) return false;
+  for (int i = 0; i < a.n; ++i) {
+    const RopeTensor& r = a.t[i];
+    if (((reinterpret_cast<uintptr_t>(r.in) | reinterpret_cast<uintptr_t>(r.out)) & 15) != 0)
+      return false;
+    if (r.in_stride % N != 0 || r.out_stride % N != 0) return false;
+  }
+  return true;
+}
+
+template <typename T>
+cudaError_t launch_typed(const RopeArgs& a, cudaStream_t s) {
+  int heads = 0;
+  for (int i = 0; i < a.n; ++i) heads += a.t[i].heads;
+  const int64_t nsm = num_sms();
+  if (!vector_ok<T>(a)) {
+    const int64_t n = a.len * heads * (a.d - a.rot / 2);
+    const int64_t blocks = std::min<int64_t>(ceil_div(n, kThreads), nsm * 16);
+    rope_element_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(a, heads);
+  } else {
+    constexpr int N = 16 / (int)sizeof(T);
+    const int rotated = (a.interleaved ? a.rot : a.rot / 2) / N;
+    const int pieces = rotated + (a.d - a.rot) / N;
+    const int teams = kThreads / pieces;
+    // teams to fill the GPU (8 blocks of an SM), from splitting a token's heads
+    // when there are too few tokens
+    int64_t hsplit = ceil_div(nsm * 8 * teams, a.len);
+    hsplit = std::min<int64_t>(hsplit, heads);
+    const int64_t blocks = std::min<int64_t>(ceil_div(a.len * hsplit, teams), nsm * 8);
+    if (a.interleaved)
+      rope_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a, pieces, rotated, heads,
+                                                                 (int)hsplit);
+    else
+      rope_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a, pieces, rotated, heads,
+                                                                  (int)hsplit);
+  }
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, int32_t io_dtype, cudaStream_t s) {
+  return io_dtype == NSP_BF16 ? launch_typed<__nv_bfloat16>(a, s) : launch_typed<float>(a, s);
+}
+
+}  // namespace nsp

@@ -26,6 +26,7 @@ NSP_F32, NSP_BF16 = 0, 1
 _lib: Optional[C.CDLL] = None
 
 _vp, _i32, _i64, _f32, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
+_f64 = C.c_double
 
 _SIGNATURES = {
     "nsp_status_str": (C.c_char_p, [_i32]),
@@ -69,6 +70,23 @@ _SIGNATURES = {
     "nsp_seq2head_permute_validate": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _i32]),
     "nsp_seq2head_permute_groups": (_i32, [_vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _i32,
                                            _vp]),
+    "nsp_rope": (_i32, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _vp, _i32, _f32, _i32,
+                        _i32, _vp]),
+    "nsp_rope_freqs": (_i32, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp]),
+    "nsp_diff_lambda_fwd": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _i32, _vp, _vp]),
+    "nsp_diff_lambda_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                   _vp, _vp]),
+    "nsp_diff_attn_fwd_workspace_size": (_sz, [_i64]),
+    "nsp_diff_attn_fwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i32, _i32, _i32, _f32,
+                                 _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nsp_diff_attn_bwd_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "nsp_diff_attn_bwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32,
+                                 _i32, _i32, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nsp_head_norm_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _i32, _vp,
+                                 _vp]),
+    "nsp_head_norm_bwd_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "nsp_head_norm_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _i32, _vp,
+                                 _vp, _vp, _vp, _sz, _vp]),
     "nsp_status_query": (_i32, [_vp, _vp]),
     "nsp_attn_bwd_ds_cache_size": (_sz, [_vp, _i32, _i32, _i32]),
     "nsp_attn_bwd_blocks_ds_cache_size": (_sz, [_vp, _i32, _i32, _vp, _i32, _i32]),
@@ -89,6 +107,12 @@ class Range(C.Structure):
     """nsp_range_t: one (query range, key range) block of a batched backward."""
     _fields_ = [("q_start", C.c_int64), ("q_len", C.c_int64), ("kv_start", C.c_int64),
                 ("kv_len", C.c_int64)]
+
+
+class RopeTensor(C.Structure):
+    """nsp_rope_tensor_t: one tensor of a rotation."""
+    _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("in_stride", C.c_int64),
+                ("out_stride", C.c_int64), ("heads", C.c_int32), ("groups", C.c_int32)]
 
 
 class AttnCost(C.Structure):
@@ -609,3 +633,313 @@ def head2seq(y, stream=None):
     out = torch.empty((T, P * h, d), dtype=y.dtype, device=y.device)
     nsp_seq2head_permute(y, out, T, P * h, d, P, True, stream)
     return out
+
+
+# ----------------------------------------------------------------------------- differential attention layer
+
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
+_DTYPES = {torch.bfloat16: NSP_BF16, torch.float32: NSP_F32}
+
+
+def _check_tensors(fn: str, dtype, **tensors) -> None:
+    """Every given tensor is on the current CUDA device and of `dtype` (or its
+    name's own): the library takes bare pointers."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: {name} is not on a CUDA device")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on device {t.get_device()}, the current one is {dev}")
+        want = _INDEX_DTYPES.get(name, dtype)
+        if t.dtype != want:
+            raise TypeError(f"{fn}: {name} is {t.dtype}, expected {want}")
+
+
+_INDEX_DTYPES = {"cu_seqlens": torch.int32, "positions": torch.int32, "freqs": torch.float64,
+                 "lse": torch.float32, "workspace": torch.uint8}
+
+
+def _check_io(fn: str, dtype) -> int:
+    if dtype not in _DTYPES:
+        raise TypeError(f"{fn}: unsupported dtype {dtype}")
+    return _DTYPES[dtype]
+
+
+def _check_shape(fn: str, name: str, t, shape) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+class _OnStream:
+    """Tensors allocated inside belong to `stream` (None: the current one)."""
+
+    def __init__(self, stream):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        self.ctx = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _token_stride(fn: str, name: str, t) -> int:
+    """Elements between tokens of [tokens, heads, d] whose heads are packed."""
+    T, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{fn}: the heads of {name} are not packed")
+    if T <= 1:
+        return H * d
+    if t.stride(0) < H * d:
+        raise ValueError(f"{fn}: the tokens of {name} overlap")
+    return t.stride(0)
+
+
+def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, low=1.0, high=32.0, orig_len=0,
+               device=None):
+    """Rotary frequencies [rot / 2], float64 (radians per position), on
+    `device`: base^(-2 i / rot), scaled for long contexts by `scaling` (None,
+    "linear", "base" or "parts", see nsp_rope_freqs)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"rope_freqs: unknown scaling {scaling!r}")
+    out = torch.empty(max(int(rot) // 2, 0), dtype=torch.float64)
+    st = load().nsp_rope_freqs(int(rot), float(base), ROPE_SCALINGS[scaling], float(factor),
+                               float(low), float(high), float(orig_len), out.data_ptr() or None)
+    _check("nsp_rope_freqs", st)
+    return out if device is None else out.to(device)
+
+
+def nsp_rope(tensors, cu_seqlens, ndoc, positions, start, length, d, rot, freqs, interleaved,
+             mscale, inverse, io_dtype, stream=None) -> int:
+    """tensors: sequence of (in, out, in_stride, out_stride, heads, groups)
+    with in and out as addresses."""
+    arr = (RopeTensor * len(tensors))()
+    for i, t in enumerate(tensors):
+        arr[i] = RopeTensor(*t)
+    st = load().nsp_rope(C.addressof(arr), len(tensors), _ptr(cu_seqlens), int(ndoc),
+                         _ptr(positions), int(start), int(length), int(d), int(rot), _ptr(freqs),
+                         int(interleaved), float(mscale), int(inverse), int(io_dtype),
+                         _stream(stream))
+    return _check("nsp_rope", st)
+
+
+def rope(q, k, cu_seqlens, freqs, layout="half", mscale=1.0, inverse=False, start=0,
+         positions=None, q_groups=1, out=None, stream=None):
+    """Rotate q [T, Hq, d] and k [T, Hkv, d] (k may be None) by their tokens'
+    positions: those of row start + t in its document of cu_seqlens, or
+    `positions` (int32 [T]; cu_seqlens may then be None).
+
+    freqs: rope_freqs(rot): the first rot = 2 len(freqs) columns of a head are
+    rotated, as halves or as interleaved pairs (layout "half", "interleaved").
+    q and k may have tokens any stride apart (columns of a fused projection).
+    q_groups = P > 1: the rotated q is returned as [P, T, Hq / P, d], the
+    layout attn_fwd_headgroups takes; with inverse=True q is given in it.
+    inverse=True is the backward: it takes gradients of the rotated q and k to
+    gradients of q and k.  out: (q_out, k_out) to write (q and k themselves to
+    rotate in place), default new tensors.  Rows at or past cu_seqlens[-1] are
+    not written."""
+    io = _check_io("rope", q.dtype)
+    qo, ko = out if out is not None else (None, None)
+    _check_tensors("rope", q.dtype, q=q, k=k, cu_seqlens=cu_seqlens, positions=positions,
+                   freqs=freqs, q_out=qo, k_out=ko)
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"rope: unknown layout {layout!r}")
+    P = int(q_groups)
+    grouped_in = inverse and P > 1
+    if q.dim() != (4 if grouped_in else 3) or P < 1:
+        raise ValueError("rope: q is [T, Hq, d], or [P, T, Hq / P, d] for the inverse of a grouped q")
+    if grouped_in:
+        if q.shape[0] != P:
+            raise ValueError("rope: q has another number of head groups than q_groups")
+        T, Hq, d = q.shape[1], P * q.shape[2], q.shape[3]
+    else:
+        T, Hq, d = q.shape
+        if Hq % P != 0:
+            raise ValueError("rope: q_groups does not divide the heads")
+    if k is not None:
+        _check_shape("rope", "k", k, (T, k.shape[1] if k.dim() == 3 else -1, d))
+    _check_shape("rope", "positions", positions, (T,))
+    if positions is None and (cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
+        raise ValueError("rope: cu_seqlens [documents + 1] or positions are needed")
+    q_shape = (P, T, Hq // P, d) if P > 1 and not inverse else (T, Hq, d)
+    with _OnStream(stream):
+        if qo is None:
+            qo = torch.empty(q_shape, dtype=q.dtype, device=q.device)
+        if ko is None and k is not None:
+            ko = torch.empty((T, k.shape[1], d), dtype=q.dtype, device=q.device)
+    _check_shape("rope", "q_out", qo, q_shape)
+    _check_shape("rope", "k_out", ko, k.shape if k is not None else ())
+    tensors = [(_ptr(q) if grouped_in else q.data_ptr(),
+                _ptr(qo) if len(q_shape) == 4 else qo.data_ptr(),
+                0 if grouped_in else _token_stride("rope", "q", q),
+                0 if len(q_shape) == 4 else _token_stride("rope", "q_out", qo), Hq, P)]
+    if k is not None:
+        tensors.append((k.data_ptr(), ko.data_ptr(), _token_stride("rope", "k", k),
+                        _token_stride("rope", "k_out", ko), k.shape[1], 1))
+    nsp_rope(tensors, cu_seqlens, cu_seqlens.numel() - 1 if cu_seqlens is not None else 0,
+             positions, start, T, d, 2 * freqs.numel(), freqs, layout == "interleaved", mscale,
+             bool(inverse), io, stream)
+    return qo, ko
+
+
+def _lambda_shape(fn, q1, k1, q2, k2):
+    io = _check_io(fn, q1.dtype)
+    if q1.dim() != 2:
+        raise ValueError(f"{fn}: the vectors are [n, dl]")
+    for name, t in (("k1", k1), ("q2", q2), ("k2", k2)):
+        _check_shape(fn, name, t, q1.shape)
+    return io, q1.shape[0], q1.shape[1]
+
+
+def diff_lambda(q1, k1, q2, k2, heads, lambda_init, stream=None):
+    """lambda [heads] = exp(<q1, k1>) - exp(<q2, k2>) + lambda_init of vectors
+    [n, dl], n = heads, or 1 for one set shared by every head."""
+    io, n, dl = _lambda_shape("diff_lambda", q1, k1, q2, k2)
+    _check_tensors("diff_lambda", q1.dtype, q1=q1, k1=k1, q2=q2, k2=k2)
+    with _OnStream(stream):
+        lam = torch.empty(int(heads), dtype=q1.dtype, device=q1.device)
+    st = load().nsp_diff_lambda_fwd(_ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), n, dl, int(heads),
+                                    float(lambda_init), io, lam.data_ptr() or None,
+                                    _stream(stream))
+    _check("nsp_diff_lambda_fwd", st)
+    return lam
+
+
+def diff_lambda_bwd(dlam, q1, k1, q2, k2, stream=None):
+    """Gradients of q1, k1, q2, k2 from dlam [heads] (or [heads, 1])."""
+    io, n, dl = _lambda_shape("diff_lambda_bwd", q1, k1, q2, k2)
+    _check_tensors("diff_lambda_bwd", q1.dtype, dlam=dlam, q1=q1, k1=k1, q2=q2, k2=k2)
+    with _OnStream(stream):
+        g = torch.empty((4, n, dl), dtype=q1.dtype, device=q1.device)
+    p, step = g.data_ptr(), n * dl * g.element_size()
+    st = load().nsp_diff_lambda_bwd(_ptr(dlam), _ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), n, dl,
+                                    dlam.numel(), io, p or None, (p + step) if p else None,
+                                    (p + 2 * step) if p else None, (p + 3 * step) if p else None,
+                                    _stream(stream))
+    _check("nsp_diff_lambda_bwd", st)
+    return g[0], g[1], g[2], g[3]
+
+
+def _diff_shapes(fn, q, k, v, lam, cu_seqlens, stream_rows, **more):
+    io = _check_io(fn, q.dtype)
+    _check_tensors(fn, q.dtype, q=q, k=k, v=v, lam=lam, cu_seqlens=cu_seqlens, **more)
+    if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1:
+        raise ValueError(f"{fn}: q is [T, Hq, d], k and v [T, Hkv, d], cu_seqlens [documents + 1]")
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    _check_shape(fn, "k", k, (T, Hkv, d))
+    _check_shape(fn, "v", v, (T, Hkv, d))
+    n = lam.numel() // Hq if Hq > 0 else 0
+    if lam.dim() not in (1, 2) or lam.shape[0] != Hq or n not in (1, T):
+        raise ValueError(f"{fn}: lam is [Hq], [Hq, 1] or [Hq, T]")
+    for name in stream_rows:
+        _check_shape(fn, name, more[name], (T, Hq, d))
+    return io, T, Hq, Hkv, d, n
+
+
+def diff_attn_fwd(q, k, v, lam, cu_seqlens, scale=None, causal=True, save=False, workspace=None,
+                  stream=None):
+    """Differential attention of a packed stream: q [T, Hq, d], k and v
+    [T, Hkv, d], map m of a head in columns [m d/2, (m + 1) d/2) of q and k,
+    lam [Hq], [Hq, 1] or [Hq, T].  Returns out [T, Hq, d]; with save=True
+    (out, out2, lse), what diff_attn_bwd needs."""
+    io, T, Hq, Hkv, d, n = _diff_shapes("diff_attn_fwd", q, k, v, lam, cu_seqlens, (),
+                                        workspace=workspace)
+    scale = (d // 2) ** -0.5 if scale is None else scale
+    lib = load()
+    out2 = lse = None
+    with _OnStream(stream):
+        out = torch.empty_like(q)
+        if save:
+            out2 = torch.empty_like(q)
+            lse = torch.empty((Hq, 2, T), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(lib.nsp_diff_attn_fwd_workspace_size(T), dtype=torch.uint8,
+                                    device=q.device)
+    st = lib.nsp_diff_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), n, _ptr(cu_seqlens),
+                               cu_seqlens.numel() - 1, T, Hq, Hkv, d, float(scale),
+                               int(bool(causal)), io, _ptr(out), _ptr(out2), _ptr(lse),
+                               _ptr(workspace), workspace.numel(), _stream(stream))
+    _check("nsp_diff_attn_fwd", st)
+    return (out, out2, lse) if save else out
+
+
+def diff_attn_bwd(q, k, v, lam, out, out2, dout, lse, cu_seqlens, scale=None, causal=True,
+                  workspace=None, stream=None):
+    """Gradients (dq, dk, dv, dlam) of diff_attn_fwd(save=True); dlam has
+    lam's shape ([Hq] as [Hq, 1])."""
+    io, T, Hq, Hkv, d, n = _diff_shapes("diff_attn_bwd", q, k, v, lam, cu_seqlens,
+                                        ("out", "out2", "dout"), out=out, out2=out2, dout=dout,
+                                        lse=lse, workspace=workspace)
+    _check_shape("diff_attn_bwd", "lse", lse, (Hq, 2, T))
+    scale = (d // 2) ** -0.5 if scale is None else scale
+    lib = load()
+    with _OnStream(stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dlam = torch.empty((Hq, n), dtype=q.dtype, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(lib.nsp_diff_attn_bwd_workspace_size(T, Hq, d),
+                                    dtype=torch.uint8, device=q.device)
+    st = lib.nsp_diff_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), n, _ptr(out), _ptr(out2),
+                               _ptr(dout), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T,
+                               Hq, Hkv, d, float(scale), int(bool(causal)), io, _ptr(dq), _ptr(dk),
+                               _ptr(dv), _ptr(dlam), _ptr(workspace), workspace.numel(),
+                               _stream(stream))
+    _check("nsp_diff_attn_bwd", st)
+    return dq, dk, dv, dlam
+
+
+def _norm_shapes(fn, x, weight, gate, **more):
+    io = _check_io(fn, x.dtype)
+    _check_tensors(fn, x.dtype, x=x, weight=weight, gate=gate, **more)
+    if x.dim() != 3:
+        raise ValueError(f"{fn}: x is [tokens, heads, d]")
+    _check_shape(fn, "weight", weight, x.shape[2:])
+    _check_shape(fn, "gate", gate, x.shape)
+    return io, _token_stride(fn, "x", x)
+
+
+def head_norm(x, weight=None, gate=None, eps=1e-6, scale=1.0, stream=None):
+    """scale * weight * x / sqrt(mean(x^2) + eps) [* sigmoid(gate)] of every
+    head's row of x [tokens, heads, d] (tokens any stride apart); weight [d]."""
+    io, stride = _norm_shapes("head_norm", x, weight, gate)
+    with _OnStream(stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    T, H, d = x.shape
+    st = load().nsp_head_norm_fwd(x.data_ptr() or None, stride, _ptr(weight), _ptr(gate), T, H, d,
+                                  float(eps), float(scale), io, _ptr(y), _stream(stream))
+    _check("nsp_head_norm_fwd", st)
+    return y
+
+
+def head_norm_bwd(x, dy, weight=None, gate=None, eps=1e-6, scale=1.0, workspace=None, stream=None):
+    """Gradients (dx, dweight, dgate) of head_norm; None for a weight or gate
+    that is not there."""
+    io, stride = _norm_shapes("head_norm_bwd", x, weight, gate, dy=dy, workspace=workspace)
+    _check_shape("head_norm_bwd", "dy", dy, x.shape)
+    T, H, d = x.shape
+    lib = load()
+    dw = dg = None
+    with _OnStream(stream):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if weight is not None:
+            dw = torch.empty(d, dtype=x.dtype, device=x.device)
+            if workspace is None:
+                workspace = torch.empty(lib.nsp_head_norm_bwd_workspace_size(T, H, d),
+                                        dtype=torch.uint8, device=x.device)
+        if gate is not None:
+            dg = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    st = lib.nsp_head_norm_bwd(x.data_ptr() or None, stride, _ptr(weight), _ptr(gate), _ptr(dy), T,
+                               H, d, float(eps), float(scale), io, _ptr(dx), _ptr(dg), _ptr(dw),
+                               _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                               _stream(stream))
+    _check("nsp_head_norm_bwd", st)
+    return dx, dw, dg
