@@ -1,0 +1,503 @@
+// Differential attention forward on the 5th-generation tensor cores (tcgen05,
+// TMEM accumulators, TMA loads): bf16 inputs, float32 scores, softmax and
+// accumulation, head dimension D = 128 or 64 (two maps of D / 2 columns).
+//
+//   P_m = softmax(scale q_m k_m^T) over a row's visible keys,  O_m = P_m V,
+//   out = O_1 - lambda O_2,  with the online softmax of Milakov and Gimelshein.
+//
+// Work item: one 128-row query tile of one head, in the schedule kernel's
+// order (most keys first), taken from an atomic counter by a persistent grid
+// of one CTA per SM.  Both maps read the same Q, K and V tiles: map m is the
+// m-th half of the columns of Q and K (an offset into the same shared-memory
+// tile), V is shared whole, and the difference is formed in the epilogue, so
+// no map's output goes to memory (out2 only when a backward follows).
+//
+// CTA roles (384 threads, three warpgroups):
+//   warps 0-3   softmax of map 1 (one query row a thread, TMEM lanes 0-127)
+//   warps 4-7   softmax of map 2
+//   warp 8      TMA producer and work fetch
+//   warp 9      TMEM allocation and the single MMA-issuing thread
+//   warps 10-11 idle (they complete the control warpgroup)
+// Registers are moved from the control warpgroup to the softmax warpgroups
+// (launched at 168: 384 x 168 = 64512; 256 x 192 + 128 x 112 = 63488), enough
+// to hold a 128-column row of S.
+// TMEM (512 columns): S_1 [0,128) S_2 [128,256) O_1 [256,384) O_2 [384,512);
+// P (bf16 pairs) over the first 64 columns of its S, read from there by P V.
+// The tensor core alternates between the maps, so that one map's softmax
+// runs under the other's products.
+//
+// Rounding: P is rounded to bf16 as the product's operand; the row sums use
+// the unrounded float32 values.  The running output is rescaled only when a
+// row's maximum has grown by more than 2^8 (exact either way: numerator and
+// denominator share the reference).
+#include <cudaTypedefs.h>
+
+#include "layer.cuh"
+#include "tc_ptx.cuh"
+
+namespace nsp {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128, BN = 128;
+constexpr int NSTAGE = 2;
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 192, kRegsControl = 112;
+constexpr int kWarpProducer = 8, kWarpMma = 9;
+constexpr uint32_t kColBlock = 128 * 64 * 2;              // 128 rows x 64 bf16 (one swizzle span)
+constexpr uint32_t kTile = 2 * kColBlock;
+__host__ __device__ constexpr uint32_t col_s(int m) { return m == 0 ? 0u : 128u; }
+__host__ __device__ constexpr uint32_t col_o(int m) { return m == 0 ? 256u : 384u; }
+constexpr float kRescaleThreshold = 8.0f;                 // log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Item {
+  int qtile, h, g, j_lo, n_kv;         // n_kv 128-key tiles from j_lo; -1 stops
+  int pad[3];
+};
+
+struct __align__(1024) Smem {
+  uint8_t q[2][kTile];                 // this item's and the next one's
+  uint8_t k[NSTAGE][kTile];
+  uint8_t v[NSTAGE][kTile];
+  float inv[2][2][BM];                 // [item parity][map][row]: 1 / row sum
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[NSTAGE], k_empty[NSTAGE], v_full[NSTAGE], v_empty[NSTAGE];
+  uint64_t s_full[2], p_full[2], o_full, o_free, inv_full;
+  uint64_t item_full[2], item_empty[2];
+  Item items[2];
+  uint64_t mma_drain_bar;
+  uint32_t tmem_base;
+  WaitCtl wait;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;        // + alignment slack
+static_assert(kSmemBytes <= 232448, "forward tile set exceeds shared memory");
+
+struct FwdArgs {
+  AttnProblem p;
+  const __nv_bfloat16* lambda;
+  int64_t n_lambda;
+  __nv_bfloat16* out2;
+  const int2* tiles;
+  const int* order;
+};
+
+// S_m = Q_m K_m^T: D / 32 products of K = 16 over the map's half of the
+// columns.  Both operands K-major with 128-byte swizzle; 16 columns are 32
+// bytes of a row, 64 columns one column block.
+template <int D>
+__device__ __forceinline__ void issue_qk(int m, uint32_t d_tmem, uint32_t q_saddr, uint32_t k_saddr) {
+  constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, false);
+  const uint64_t qd = smem_desc_sw128(q_saddr, 16, 1024);
+  const uint64_t kd = smem_desc_sw128(k_saddr, 16, 1024);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int kk = m * (D / 32) + i;
+    const uint32_t off = ((kk >> 2) * kColBlock + (kk & 3) * 32) >> 4;
+    mma_ss(d_tmem, qd + off, kd + off, idesc, i > 0 ? 1u : 0u);
+  }
+}
+
+// O (+)= P V: P from TMEM, 8 columns per 16 keys; V MN-major (keys along K).
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_saddr,
+                                         bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(BM, D, true);
+  const uint64_t vd = smem_desc_sw128(v_saddr, kColBlock, 1024);
+#pragma unroll
+  for (int kk = 0; kk < BN / 16; ++kk)
+    mma_ts(d_tmem, p_tmem + kk * 8, vd + ((kk * 2048) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ FwdArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AttnProblem& p = a.p;
+  WsHeader* hdr = p.hdr;
+  grid_dep_wait();                          // the schedule kernel's lists and status
+  if (status_bad(hdr)) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.q_full[s], 1);
+      mbar_init(&sm.q_empty[s], 1);
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 128);
+      mbar_init(&sm.item_full[s], 1);
+      mbar_init(&sm.item_empty[s], 1 + 8);
+    }
+    for (int s = 0; s < NSTAGE; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_free, 8);
+    mbar_init(&sm.inv_full, 8);
+    mbar_init(&sm.mma_drain_bar, 1);
+    wait_ctl_init(&sm.wait, p.wait_budget);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == kWarpProducer && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem = sm.tmem_base;
+  WaitCtl* const wc = &sm.wait;
+  const int G = p.Hq / p.Hkv;
+  const int n_items = hdr->n_items * p.Hq;
+  constexpr int kBlocks = D / 64;                               // 64-column blocks of a row
+  constexpr uint32_t kLoadBytes = kBlocks * kColBlock;          // one Q, K or V tile
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == kWarpProducer && lane == 0) {
+      // ------------------------------------------------------------ producer
+      uint32_t it_count = 0, kv_count = 0;
+      bool ok = true;
+      while (ok) {
+        const int idx = atomicAdd(&hdr->counter, 1);
+        Item it = {};
+        it.n_kv = -1;
+        if (idx < n_items) {
+          const int qt = a.order[idx / p.Hq];
+          const int2 tr = a.tiles[qt];
+          it.qtile = qt;
+          it.h = idx % p.Hq;
+          it.g = it.h / G;
+          it.j_lo = tr.x;
+          it.n_kv = tr.y - tr.x + 1;
+        }
+        // items alternate over two slots of the queue and of Q
+        const uint32_t slot = it_count & 1, use = it_count >> 1;
+        if (use >= 1 && !mbar_wait(&sm.item_empty[slot], (use - 1) & 1, wc, hdr)) break;
+        sm.items[slot] = it;
+        mbar_arrive(&sm.item_full[slot]);
+        if (it.n_kv < 0) break;
+        if (use >= 1 && !mbar_wait(&sm.q_empty[slot], (use - 1) & 1, wc, hdr)) break;
+        mbar_arrive_expect_tx(&sm.q_full[slot], kLoadBytes);
+#pragma unroll
+        for (int cb = 0; cb < kBlocks; ++cb)
+          tma_load_2d(sm.q[slot] + cb * kColBlock, &tm_q, &sm.q_full[slot], it.h * D + cb * 64,
+                      it.qtile * BM);
+        ++it_count;
+        for (int jj = 0; jj < it.n_kv; ++jj) {
+          const uint32_t st = kv_count % NSTAGE, n = kv_count / NSTAGE;
+          const int key0 = (it.j_lo + jj) * BN;
+          if (n >= 1 && !mbar_wait(&sm.k_empty[st], (n - 1) & 1, wc, hdr)) { ok = false; break; }
+          mbar_arrive_expect_tx(&sm.k_full[st], kLoadBytes);
+#pragma unroll
+          for (int cb = 0; cb < kBlocks; ++cb)
+            tma_load_2d(sm.k[st] + cb * kColBlock, &tm_k, &sm.k_full[st], it.g * D + cb * 64, key0);
+          if (n >= 1 && !mbar_wait(&sm.v_empty[st], (n - 1) & 1, wc, hdr)) {
+            drain_wait(&sm.k_full[st], n & 1);      // the K copy just issued is in flight
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&sm.v_full[st], kLoadBytes);
+#pragma unroll
+          for (int cb = 0; cb < kBlocks; ++cb)
+            tma_load_2d(sm.v[st] + cb * kColBlock, &tm_v, &sm.v_full[st], it.g * D + cb * 64, key0);
+          ++kv_count;
+        }
+      }
+      // leaving, normally or on an abort: every issued copy lands first
+      for (uint32_t j = it_count > 2 ? it_count - 2 : 0; j < it_count; ++j)
+        drain_wait(&sm.q_full[j & 1], (j >> 1) & 1);
+      for (uint32_t j = kv_count > NSTAGE ? kv_count - NSTAGE : 0; j < kv_count; ++j) {
+        drain_wait(&sm.k_full[j % NSTAGE], (j / NSTAGE) & 1);
+        drain_wait(&sm.v_full[j % NSTAGE], (j / NSTAGE) & 1);
+      }
+    } else if (warp == kWarpMma && lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      uint32_t it_count = 0, kv_count = 0, p_count = 0;
+      while (true) {
+        const uint32_t slot = it_count & 1, use = it_count >> 1;
+        if (!mbar_wait(&sm.item_full[slot], use & 1, wc, hdr)) break;
+        const Item it = sm.items[slot];
+        mbar_arrive(&sm.item_empty[slot]);
+        if (it.n_kv < 0) break;
+        if (!mbar_wait(&sm.q_full[slot], use & 1, wc, hdr)) break;
+        const uint32_t qs = smem_u32(sm.q[slot]);
+        bool ok = true;
+        {
+          const uint32_t st = kv_count % NSTAGE, n = kv_count / NSTAGE;
+          if (!mbar_wait(&sm.k_full[st], n & 1, wc, hdr)) break;
+          tc_fence_after();
+          const uint32_t ks = smem_u32(sm.k[st]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            issue_qk<D>(m, tmem + col_s(m), qs, ks);
+            mma_commit(&sm.s_full[m]);
+          }
+          mma_commit(&sm.k_empty[st]);
+          if (it.n_kv == 1) mma_commit(&sm.q_empty[slot]);
+        }
+        for (int jj = 0; jj < it.n_kv && ok; ++jj) {
+          const uint32_t st = (kv_count + jj) % NSTAGE, n = (kv_count + jj) / NSTAGE;
+          const bool has_next = jj + 1 < it.n_kv;
+          const uint32_t stn = (kv_count + jj + 1) % NSTAGE, nn = (kv_count + jj + 1) / NSTAGE;
+          if (!mbar_wait(&sm.v_full[st], n & 1, wc, hdr)) { ok = false; break; }
+          // the first product overwrites O: read by the previous item's epilogue
+          if (jj == 0 && it_count >= 1 && !mbar_wait(&sm.o_free, (it_count - 1) & 1, wc, hdr)) {
+            ok = false;
+            break;
+          }
+          const uint32_t vs = smem_u32(sm.v[st]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (!ok) continue;
+            if (!mbar_wait(&sm.p_full[m], p_count & 1, wc, hdr)) { ok = false; continue; }
+            tc_fence_after();
+            issue_pv<D>(tmem + col_o(m), tmem + col_s(m), vs, jj > 0);
+            if (m == 1) mma_commit(&sm.v_empty[st]);
+            if (!has_next) {
+              if (m == 1) mma_commit(&sm.o_full);
+              continue;
+            }
+            if (m == 0) {
+              if (!mbar_wait(&sm.k_full[stn], nn & 1, wc, hdr)) { ok = false; continue; }
+              tc_fence_after();
+            }
+            issue_qk<D>(m, tmem + col_s(m), qs, smem_u32(sm.k[stn]));
+            mma_commit(&sm.s_full[m]);
+            if (m == 1) {
+              mma_commit(&sm.k_empty[stn]);
+              if (jj + 2 == it.n_kv) mma_commit(&sm.q_empty[slot]);
+            }
+          }
+          ++p_count;
+        }
+        if (!ok) break;
+        kv_count += it.n_kv;
+        ++it_count;
+      }
+      mma_drain(&sm.mma_drain_bar);        // every product done before TMEM is freed
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------ softmax
+    const int m_ = warp >> 2;              // map
+    const int wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + col_s(m_);
+    const uint32_t o_tm = tmem + lane_base + col_o(m_);
+    const float sl2 = p.scale * kLog2e;
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    uint32_t it_count = 0, s_count = 0;
+    while (true) {
+      const uint32_t slot = it_count & 1;
+      if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+      const Item it = sm.items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      if (it.n_kv < 0) break;
+      const int64_t row = (int64_t)it.qtile * BM + r;
+      const bool valid = row < p.q_len;
+      int lo = 0, hi = 0;                                      // visible keys [lo, hi)
+      float lam = 0.f;
+      if (valid) {
+        const int b = doc_of(p.cu, p.ndoc, row);
+        lo = __ldg(p.cu + b);
+        hi = p.causal ? (int)row + 1 : (int)min((int64_t)__ldg(p.cu + b + 1), p.kv_len);
+        lam = __bfloat162float(a.lambda[(int64_t)it.h * a.n_lambda + (a.n_lambda > 1 ? row : 0)]);
+      }
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int jj = 0; jj < it.n_kv; ++jj) {
+        if (!mbar_wait_warp(&sm.s_full[m_], s_count & 1, wc, hdr)) { ok = false; break; }
+        ++s_count;
+        tc_fence_after();
+        const int key0 = (it.j_lo + jj) * BN;
+        // visible columns are [c0, c0 + span): one unsigned compare per column;
+        // a warp whose rows all see the whole tile skips the mask
+        const int c0 = lo - key0;
+        const uint32_t span = (uint32_t)(hi - lo);
+        const bool full_w = __all_sync(0xffffffffu, lo <= key0 && key0 + BN <= hi);
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, sr[c]);
+        tmem_wait_ld();
+        if (!full_w) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((uint32_t)(c * 32 + i - c0) >= span) sr[c][i] = 0xff800000u;   // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = max3f(__uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]), __uint_as_float(sr[c][2]));
+#pragma unroll
+          for (int i = 3; i < 31; i += 2)
+            mx[c] = max3f(mx[c], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+          mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][31]));
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float m_new = fmaxf(m, mt * sl2);
+        const bool need = (m != -INFINITY) && (m_new > m + kRescaleThreshold);
+        const float corr = need ? ex2(m - m_new) : 1.f;
+        if (need || m == -INFINITY) m = m_new;
+        const float mb = (m == -INFINITY) ? 0.f : m;
+        const uint64_t nm2 = f2_pack(-mb, -mb);
+        uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])),
+                             sl2x2, nm2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            ls[i & 3] = f2_add(ls[i & 3], f2_pack(p0, p1));
+            pk[i] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(s_tm + c * 16, pk);
+        }
+        float l0, l1;
+        f2_unpack(f2_add(f2_add(ls[0], ls[1]), f2_add(ls[2], ls[3])), l0, l1);
+        l = l * corr + (l0 + l1);
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t orow[32];
+            tmem_ld32(o_tm + c * 32, orow);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) orow[i] = __float_as_uint(__uint_as_float(orow[i]) * corr);
+            tmem_st32(o_tm + c * 32, orow);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[m_]);
+      }
+      if (!ok) break;
+      // ---- epilogue: out = O_1 / l_1 - lambda O_2 / l_2; the warpgroups swap
+      // their row sums and take half of the columns of both accumulators each
+      sm.inv[slot][m_][r] = l > 0.f ? 1.f / l : 0.f;
+      if (valid && p.lse != nullptr)
+        p.lse[((int64_t)it.h * 2 + m_) * p.q_len + row] = (m + __log2f(l)) * kLn2;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.inv_full);
+      if (!mbar_wait_warp(&sm.inv_full, it_count & 1, wc, hdr)) break;
+      if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
+      tc_fence_after();
+      const float i0 = sm.inv[slot][0][r], i1 = sm.inv[slot][1][r];
+      const int64_t off = (row * p.Hq + it.h) * D + m_ * (D / 2);
+      __nv_bfloat16* const out = reinterpret_cast<__nv_bfloat16*>(p.out) + off;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[32], y[32];
+        tmem_ld32(tmem + lane_base + col_o(0) + m_ * (D / 2) + c * 32, x);
+        tmem_ld32(tmem + lane_base + col_o(1) + m_ * (D / 2) + c * 32, y);
+        tmem_wait_ld();
+        if (c == D / 64 - 1) {             // both accumulators read: the next item may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.o_free);
+        }
+        if (!valid) continue;
+        uint32_t w[16], w2[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float a0 = __uint_as_float(y[2 * i]) * i1, a1 = __uint_as_float(y[2 * i + 1]) * i1;
+          w[i] = pack_bf16x2(fmaf(__uint_as_float(x[2 * i]), i0, -lam * a0),
+                             fmaf(__uint_as_float(x[2 * i + 1]), i0, -lam * a1));
+          w2[i] = pack_bf16x2(a0, a1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          st_global_v8(out + c * 32 + 16 * i, w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                       w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
+          if (a.out2 != nullptr)
+            st_global_v8(a.out2 + off + c * 32 + 16 * i, w2[8 * i], w2[8 * i + 1], w2[8 * i + 2],
+                         w2[8 * i + 3], w2[8 * i + 4], w2[8 * i + 5], w2[8 * i + 6], w2[8 * i + 7]);
+        }
+      }
+      ++it_count;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const FwdArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, cudaStream_t s) {
+  auto kern = diff_fwd_tc_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(persistent_grid()), dim3(kThreads), kSmemBytes, s, mq, mk, mv, a);
+  count_launches(1);
+  count_path(true);
+  return e;
+}
+
+}  // namespace
+
+// [rows, cols] bf16 row-major, box = 64 columns x 128 rows, 128-byte swizzle.
+bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(cols * 2)};
+  const cuuint32_t box[2] = {64, 128}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_diff_fwd_tc(const DiffProblem& d, const FwdWsLayout& L, char* ws, cudaStream_t s) {
+  const AttnProblem& p = d.p;
+  CUtensorMap mq, mk, mv;
+  if (!diff_tile_map(&mq, p.q, p.q_len, (int64_t)p.Hq * p.d) ||
+      !diff_tile_map(&mk, p.k, p.kv_len, (int64_t)p.Hkv * p.d) ||
+      !diff_tile_map(&mv, p.v, p.kv_len, (int64_t)p.Hkv * p.d))
+    return cudaErrorNotSupported;
+  FwdArgs a;
+  a.p = p;
+  a.lambda = reinterpret_cast<const __nv_bfloat16*>(d.lambda);
+  a.n_lambda = d.n_lambda;
+  a.out2 = reinterpret_cast<__nv_bfloat16*>(d.out2);
+  a.tiles = reinterpret_cast<const int2*>(ws + L.tiles);
+  a.order = reinterpret_cast<const int*>(ws + L.order);
+  return p.d == 128 ? launch_d<128>(a, mq, mk, mv, s) : launch_d<64>(a, mq, mk, mv, s);
+}
+
+}  // namespace nsp

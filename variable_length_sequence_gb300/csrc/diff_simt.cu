@@ -444,8 +444,6 @@ cudaError_t bwd(const DiffProblem& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s) {
-  using bf = __nv_bfloat16;
-  if (a.p.io_dtype == NSP_BF16) return a.p.d == 128 ? fwd<bf, 128>(a, s) : fwd<bf, 64>(a, s);
   return a.p.d == 128 ? fwd<float, 128>(a, s) : fwd<float, 64>(a, s);
 }
 

@@ -3,6 +3,8 @@
 // itself) and the vector loads and stores their streaming kernels share.
 #pragma once
 
+#include <cuda.h>
+
 #include "nsp_internal.cuh"
 
 namespace nsp {
@@ -69,6 +71,10 @@ struct DiffProblem {
   float *delta, *nlse2, *coef;       // backward workspace: [2 Hq][Tp], [2 Hq][Tp], [Hq][Tp]
   int64_t Tp;
 };
+cudaError_t launch_diff_fwd_tc(const DiffProblem& a, const FwdWsLayout& L, char* ws, cudaStream_t s);
+// A map of [rows, cols] bf16 whose copies are 128 rows of 64 columns, 128-byte
+// swizzled; false without tensor-map support in the driver.
+bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols);
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s);
 cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s);
 // delta, nlse2 and coef of the backward, and dlambda of each token

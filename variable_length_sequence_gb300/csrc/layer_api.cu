@@ -283,7 +283,9 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
   a.out2 = out2;
   if (launch_fwd_schedule(a.p, L, ws, s) != cudaSuccess) return NSP_ERR_CUDA;
   if (T == 0) return NSP_OK;
-  return launch_diff_fwd_simt(a, s) == cudaSuccess ? NSP_OK : NSP_ERR_CUDA;
+  const cudaError_t e =
+      io_dtype == NSP_BF16 ? launch_diff_fwd_tc(a, L, ws, s) : launch_diff_fwd_simt(a, s);
+  return e == cudaSuccess ? NSP_OK : NSP_ERR_CUDA;
 }
 
 // Backward workspace: the attention backward's layout for 2 Hq rows of delta
