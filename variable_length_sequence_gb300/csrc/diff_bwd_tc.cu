@@ -1,0 +1,1014 @@
+// Differential attention backward on the tcgen05 tensor cores: bf16 inputs,
+// float32 scores and accumulation, head dimension D = 128 or 64 (two maps of
+// D / 2 columns), two persistent kernels without atomics.
+//
+// With P_m recomputed from the forward's lse, delta_m = <dout, O_m>, c = -lambda
+// (per query row; delta, -lse log2 e and c are prepared by diff_prep_kernel in
+// padded rows):
+//   dP = dOut V^T (one product for both maps),
+//   dS_1 = P_1 (dP - delta_1),  dS_2 = c P_2 (dP - delta_2),
+//   dV = (P_1 + c P_2)^T dOut,  dK_m = scale dS_m^T Q_m,  dQ_m = scale dS_m K_m.
+//
+// dK/dV kernel (key-stationary).  Work item: one 128-key tile of one KV head;
+// it walks every pair (query head of the group, 128-row query tile that can
+// see the keys).  A pair costs four 128 x 128 x 128 products' worth: S_1 and
+// S_2 (half the columns each), dP, dV (both maps in one product, their
+// combination is its operand), dK_1 and dK_2 (half the columns each); treating
+// the maps as two heads would cost six.  TMEM: two 128-column regions [0,256),
+// dV [256,256+D), dK_1 | dK_2 [384,384+D).  Pair n puts S_1^T in region A = n & 1,
+// dP^T in the other one, B; S_2^T follows into A when the softmax warps have
+// read S_1, P^T (bf16, the dV operand) over S_2 when they have read that.  The
+// next pair swaps the regions, so its S_1 is computed (into B, read by then)
+// while the softmax is on this pair's second map.
+//   Softmax warps hold P_1 between the two steps as fp16 (the registers do not
+//   hold it in float32 beside dP), times 2^15 so that probabilities down to
+//   2^-29 keep fp16's 11 bits: an error of 2^-12 beside the 2^-9 of the bf16
+//   operand.  The factor rides in the exponent and is taken off dK_1 at the end.
+//
+// dQ kernel (query-stationary).  Work item: one 128-row query tile of one head.
+// TMEM: S_1 [0,128), S_2 [128,256), dP [256,384), dQ_1 | dQ_2 [384,384+D).  dS_m
+// (bf16) goes over S_m and is read from TMEM.  The softmax keeps dP of a tile
+// in registers for both maps; while it is on one map the tensor core does the
+// other map's dQ, the next S, and the next dP.
+//
+// Roles, dK/dV: 16 softmax warps (four column groups of four lane quadrants),
+// warp 16 producer of tiles, warps 17 and 18 one MMA stream each (S and dP;
+// dK and dV: products of one thread run in order, so those that wait for the
+// softmax must not hold up the others), warp 19 producer of the row vectors.
+// dQ: 8 softmax warps, warp 8 producer, warp 9 MMA.  All waits are bounded.
+#include <cuda_fp16.h>
+
+#include "layer.cuh"
+#include "tc_ptx.cuh"
+
+namespace nsp {
+namespace {
+
+using namespace tc;
+
+constexpr uint32_t kBlk = 128 * 64 * 2;               // 128 rows x 64 bf16 column block
+constexpr uint32_t kTile = 2 * kBlk;                   // 128 x 128 bf16
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr size_t kSmemLimit = 232448;
+
+struct BwdArgs {
+  AttnProblem p;
+  const float *nlse2, *delta;       // [2 Hq][Tp]
+  const float* coef;                // [Hq][Tp]
+  int64_t Tp;
+  __nv_bfloat16 *dq, *dk, *dv;
+  const int2* qtiles;               // per 128-row query tile: first/last 128-key tile
+  const int* qorder;
+  const int2* ktiles;               // per 128-key tile: first/last 128-row query tile
+  const int* korder;
+};
+
+// D = A B^T over columns [m HK, (m + 1) HK) of K-major 128-row tiles.
+template <int HK>
+__device__ __forceinline__ void mma_kk(int m, uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+  const uint64_t ad = smem_desc_sw128(a_saddr, 16, 1024);
+  const uint64_t bd = smem_desc_sw128(b_saddr, 16, 1024);
+#pragma unroll
+  for (int i = 0; i < HK / 16; ++i) {
+    const int kk = m * (HK / 16) + i;
+    const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
+    mma_ss(d_tmem, ad + off, bd + off, idesc, i > 0 ? 1u : 0u);
+  }
+}
+
+// Address of column n0 (a multiple of 32) of an MN-major tile's first rows.
+__device__ __forceinline__ uint32_t mn_offset(int n0) {
+  return (uint32_t)(n0 >> 6) * kBlk + (uint32_t)(n0 & 63) * 2;
+}
+
+// D (+)= A B, A (128 x 128) from TMEM in groups of QPG K-columns (group j at
+// columns a_tmem + j QPG + [0, QPG / 2), bf16 pairs), B MN-major columns
+// [n0, n0 + N) of a 128-row tile.
+template <int QPG, int N>
+__device__ __forceinline__ void mma_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_saddr, int n0,
+                                          bool accumulate) {
+  constexpr int kSteps = QPG / 16;
+  const uint64_t bd = smem_desc_sw128(b_saddr + mn_offset(n0), kBlk, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(d_tmem, a_tmem + (kk / kSteps) * QPG + (kk % kSteps) * 8, bd + ((kk * 2048) >> 4),
+           idesc_bf16_f32(128, N, true, false), (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// The same with A K-major in shared memory.
+template <int N>
+__device__ __forceinline__ void mma_ss_mn(uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr, int n0,
+                                          bool accumulate) {
+  const uint64_t ad = smem_desc_sw128(a_saddr, 16, 1024);
+  const uint64_t bd = smem_desc_sw128(b_saddr + mn_offset(n0), kBlk, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ss(d_tmem, ad + (((kk >> 2) * kBlk + (kk & 3) * 32) >> 4), bd + ((kk * 2048) >> 4),
+           idesc_bf16_f32(128, N, true, false), (accumulate || kk > 0) ? 1u : 0u);
+}
+
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&v)[32], float scale) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * scale, __uint_as_float(v[2 * i + 1]) * scale);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    st_global_v8(dst + 16 * i, w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3], w[8 * i + 4],
+                 w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
+}
+
+// 1024-aligned view of dynamic shared memory, or nullptr (error recorded)
+// when the aligned structure would not fit in the launch's allocation.
+template <typename S>
+__device__ __forceinline__ S* smem_view(uint8_t* raw, WsHeader* hdr) {
+  uint32_t dyn_bytes;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
+  const uint32_t base = smem_u32(raw);
+  if (((base + 1023u) & ~1023u) - base + sizeof(S) > dyn_bytes) {
+    if (threadIdx.x == 0) atomicExch(&hdr->status, (int)NSP_ERR_UNSUPPORTED);
+    return nullptr;
+  }
+  return reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                              ~static_cast<uintptr_t>(1023));
+}
+
+template <typename S>
+constexpr size_t smem_bytes() {
+  return sizeof(S) + 1024 <= kSmemLimit ? sizeof(S) + 1024 : kSmemLimit;
+}
+
+// ================================================================ dK / dV
+
+constexpr int kKvThreads = 640;
+constexpr int kKvSoftmaxWarps = 16;
+constexpr int kKvWarpTiles = 16, kKvWarpMma1 = 17, kKvWarpMma2 = 18, kKvWarpRows = 19;
+constexpr int kKvRegsControl = 64, kKvRegsSoftmax = 104;   // 128 x 64 + 512 x 104 = 640 x 96
+constexpr float kShift = 15.f, kUnshift = 1.f / 32768.f;    // exponent of P_1, see above
+
+struct KvItem {
+  int ktile, g, i_lo, n_q, pairs, pad[3];    // pairs = heads * n_q; -1 stops
+};
+
+struct __align__(1024) SmemKV {
+  uint8_t k[kTile];
+  uint8_t v[kTile];
+  // Q of pair j in slot j % 4, dOut in slot (j + 2) % 4, the (j / 2)-th fill
+  // of their slots: Q of pair j + 2 takes the slot that dOut of pair j frees
+  uint8_t qd[4][kTile];
+  uint8_t ds[kTile];                         // dS_m^T, [q-block][key][64 q], 128-byte swizzle
+  float first[2][128];                       // map 1: -lse log2 e, delta
+  float second[3][128];                      // map 2: -lse log2 e, delta, c
+  uint64_t kv_full, kv_empty;
+  uint64_t slot_full[4], slot_empty[4];
+  uint64_t first_full, first_empty, second_full, second_empty;
+  uint64_t s1_full, s1_free, s2_full, dp_full, dp_free, p_ready, dv_done, ds_ready, dk_done;
+  uint64_t dkv_full, dkv_empty;
+  uint64_t item_full[2], item_empty[2];
+  KvItem items[2];
+  uint64_t drain1, drain2;
+  uint32_t tmem_base;
+  WaitCtl wait;
+};
+static_assert(sizeof(SmemKV) <= kSmemLimit, "dK/dV tile set exceeds shared memory");
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads, 1)
+    diff_bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                            const __grid_constant__ CUtensorMap tm_do,
+                            const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ BwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const AttnProblem& p = a.p;
+  WsHeader* hdr = p.hdr;
+  grid_dep_wait();                          // the prepared row vectors
+  grid_dep_trigger();                       // the dQ kernel may launch on SMs this one frees
+  if (status_bad(hdr)) return;
+  SmemKV* smp = smem_view<SmemKV>(smem_raw, hdr);
+  if (smp == nullptr) return;
+  SmemKV& sm = *smp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.kv_full, 1);
+    mbar_init(&sm.kv_empty, 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sm.slot_full[s], 1);
+      mbar_init(&sm.slot_empty[s], 2);       // one commit of each stream
+    }
+    mbar_init(&sm.first_full, 1);
+    mbar_init(&sm.first_empty, kKvSoftmaxWarps);
+    mbar_init(&sm.second_full, 1);
+    mbar_init(&sm.second_empty, kKvSoftmaxWarps);
+    mbar_init(&sm.s1_full, 1);
+    mbar_init(&sm.s1_free, kKvSoftmaxWarps);
+    mbar_init(&sm.s2_full, 1);
+    mbar_init(&sm.dp_full, 1);
+    mbar_init(&sm.dp_free, kKvSoftmaxWarps);
+    mbar_init(&sm.p_ready, kKvSoftmaxWarps);
+    mbar_init(&sm.dv_done, 1);
+    mbar_init(&sm.ds_ready, kKvSoftmaxWarps);
+    mbar_init(&sm.dk_done, 1);
+    mbar_init(&sm.dkv_full, 1);
+    mbar_init(&sm.dkv_empty, kKvSoftmaxWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.item_full[s], 1);
+      mbar_init(&sm.item_empty[s], 3 + kKvSoftmaxWarps);
+    }
+    mbar_init(&sm.drain1, 1);
+    mbar_init(&sm.drain2, 1);
+    wait_ctl_init(&sm.wait, p.wait_budget);
+    fence_mbar_init();
+  }
+  if (warp == kKvWarpMma1) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == kKvWarpTiles && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem = sm.tmem_base;
+  WaitCtl* const wc = &sm.wait;
+  const int G = p.Hq / p.Hkv;
+  const int n_items = hdr->n_items2 * p.Hkv;
+  constexpr int kBlocks = D / 64;                        // 64-column blocks of a row
+  constexpr uint32_t kLoad = kBlocks * kBlk;             // one Q, dOut, K or V tile
+
+  if (warp >= kKvSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kKvRegsControl));
+    if (warp == kKvWarpTiles && lane == 0) {
+      // ------------------------------------------------------------ producer: items, tiles
+      uint32_t it_count = 0, kv_count = 0, qc = 0, loads = 0;
+      bool ok = true;
+      while (ok) {
+        const int idx = atomicAdd(&hdr->counter2, 1);
+        KvItem it = {};
+        it.pairs = -1;
+        if (idx < n_items) {
+          const int kt = a.korder[idx / p.Hkv];
+          const int2 tr = a.ktiles[kt];
+          it.ktile = kt;
+          it.g = idx % p.Hkv;
+          it.i_lo = tr.x;
+          it.n_q = tr.y - tr.x + 1;
+          it.pairs = G * it.n_q;
+        }
+        const uint32_t slot = it_count & 1;
+        if (it_count >= 2 && !mbar_wait(&sm.item_empty[slot], ((it_count >> 1) - 1) & 1, wc, hdr))
+          break;
+        sm.items[slot] = it;
+        mbar_arrive(&sm.item_full[slot]);
+        ++it_count;
+        if (it.pairs < 0) break;
+        if (kv_count >= 1 && !mbar_wait(&sm.kv_empty, (kv_count - 1) & 1, wc, hdr)) break;
+        mbar_arrive_expect_tx(&sm.kv_full, 2 * kLoad);
+#pragma unroll
+        for (int cb = 0; cb < kBlocks; ++cb) {
+          tma_load_2d(sm.k + cb * kBlk, &tm_k, &sm.kv_full, it.g * D + cb * 64, it.ktile * 128);
+          tma_load_2d(sm.v + cb * kBlk, &tm_v, &sm.kv_full, it.g * D + cb * 64, it.ktile * 128);
+        }
+        ++kv_count;
+        int h = it.g * G, i = it.i_lo;
+        for (int n = 0; n < it.pairs && ok; ++n) {
+          const uint32_t fill = qc >> 1;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {                  // Q, then dOut
+            const uint32_t s = (qc + 2 * t) & 3;
+            if (!ok) continue;
+            if (fill >= 1 && !mbar_wait(&sm.slot_empty[s], (fill - 1) & 1, wc, hdr)) {
+              ok = false;
+              continue;
+            }
+            mbar_arrive_expect_tx(&sm.slot_full[s], kLoad);
+#pragma unroll
+            for (int cb = 0; cb < kBlocks; ++cb)
+              tma_load_2d(sm.qd[s] + cb * kBlk, t == 0 ? &tm_q : &tm_do, &sm.slot_full[s],
+                          h * D + cb * 64, i * 128);
+            ++loads;
+          }
+          ++qc;
+          if (++i == it.i_lo + it.n_q) { i = it.i_lo; ++h; }
+        }
+      }
+      // leaving, normally or on an abort: every issued copy lands first
+      if (kv_count >= 1) drain_wait(&sm.kv_full, (kv_count - 1) & 1);
+      for (uint32_t l = (loads > 4 ? loads - 4 : 0); l < loads; ++l) {
+        const uint32_t j = l >> 1;                        // load l: pair l / 2, Q or dOut
+        drain_wait(&sm.slot_full[(l & 1) ? ((j + 2) & 3) : (j & 3)], (j >> 1) & 1);
+      }
+    } else if (warp == kKvWarpRows && lane == 0) {
+      // ------------------------------------------------------------ producer: row vectors
+      // One buffer for each map: the first map's is free in the middle of a pair
+      // and wanted at the start of the next one, the second's the other way round.
+      uint32_t it_count = 0, n1 = 0, n2 = 0;
+      bool ok = true;
+      while (ok) {
+        const uint32_t slot = it_count & 1;
+        if (!mbar_wait(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+        const KvItem it = sm.items[slot];
+        mbar_arrive(&sm.item_empty[slot]);
+        ++it_count;
+        if (it.pairs < 0) break;
+        int h = it.g * G, i = it.i_lo;
+        for (int n = 0; n < it.pairs; ++n) {
+          const int64_t r1 = (int64_t)(2 * h) * a.Tp + (int64_t)i * 128, r2 = r1 + a.Tp;
+          if (n1 >= 1 && !mbar_wait(&sm.first_empty, (n1 - 1) & 1, wc, hdr)) { ok = false; break; }
+          mbar_arrive_expect_tx(&sm.first_full, 2 * 512);
+          bulk_load(sm.first[0], a.nlse2 + r1, 512, &sm.first_full);
+          bulk_load(sm.first[1], a.delta + r1, 512, &sm.first_full);
+          ++n1;
+          if (n2 >= 1 && !mbar_wait(&sm.second_empty, (n2 - 1) & 1, wc, hdr)) { ok = false; break; }
+          mbar_arrive_expect_tx(&sm.second_full, 3 * 512);
+          bulk_load(sm.second[0], a.nlse2 + r2, 512, &sm.second_full);
+          bulk_load(sm.second[1], a.delta + r2, 512, &sm.second_full);
+          bulk_load(sm.second[2], a.coef + (int64_t)h * a.Tp + (int64_t)i * 128, 512, &sm.second_full);
+          ++n2;
+          if (++i == it.i_lo + it.n_q) { i = it.i_lo; ++h; }
+        }
+      }
+      if (n1 >= 1) drain_wait(&sm.first_full, (n1 - 1) & 1);
+      if (n2 >= 1) drain_wait(&sm.second_full, (n2 - 1) & 1);
+    } else if (warp == kKvWarpMma1 && lane == 0) {
+      // ------------------------------------------------------------ stream 1: S_1, dP, S_2
+      const uint32_t k_s = smem_u32(sm.k), v_s = smem_u32(sm.v);
+      uint32_t it_count = 0, items_done = 0, qc = 0;
+      bool ok = true;
+      while (ok) {
+        const uint32_t slot = it_count & 1;
+        if (!mbar_wait(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+        const KvItem it = sm.items[slot];
+        mbar_arrive(&sm.item_empty[slot]);
+        ++it_count;
+        if (it.pairs < 0) break;
+        if (!mbar_wait(&sm.kv_full, items_done & 1, wc, hdr)) break;
+        for (int n = 0; n < it.pairs; ++n) {
+          const uint32_t sq = qc & 3, sd = (qc + 2) & 3, fp = (qc >> 1) & 1, rb = qc & 1;
+          const uint32_t ra = tmem + 128 * rb, rbb = tmem + 128 * (rb ^ 1);
+          if (!mbar_wait(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
+          // A held the previous pair's dP: free once the softmax has read it
+          if (qc >= 1 && !mbar_wait(&sm.dp_free, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
+          tc_fence_after();
+          mma_kk<D / 2>(0, ra, k_s, smem_u32(sm.qd[sq]));                 // S_1^T = K_1 Q_1^T
+          mma_commit(&sm.s1_full);
+          if (!mbar_wait(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
+          // B held the previous pair's P: free once dV has read it
+          if (qc >= 1 && !mbar_wait(&sm.dv_done, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
+          tc_fence_after();
+          mma_kk<D>(0, rbb, v_s, smem_u32(sm.qd[sd]));                    // dP^T = V dOut^T
+          mma_commit(&sm.dp_full);
+          mma_commit(&sm.slot_empty[sd]);
+          if (!mbar_wait(&sm.s1_free, qc & 1, wc, hdr)) { ok = false; break; }
+          tc_fence_after();
+          mma_kk<D / 2>(1, ra, k_s, smem_u32(sm.qd[sq]));                 // S_2^T = K_2 Q_2^T
+          mma_commit(&sm.s2_full);
+          mma_commit(&sm.slot_empty[sq]);
+          ++qc;
+        }
+        if (!ok) break;
+        mma_commit(&sm.kv_empty);
+        ++items_done;
+      }
+      mma_drain(&sm.drain1);              // every product done before TMEM is freed
+    } else if (warp == kKvWarpMma2 && lane == 0) {
+      // ------------------------------------------------------------ stream 2: dK_1, dV, dK_2
+      const uint32_t ds_s = smem_u32(sm.ds);
+      uint32_t it_count = 0, items_done = 0, qc = 0;
+      bool ok = true;
+      while (ok) {
+        const uint32_t slot = it_count & 1;
+        if (!mbar_wait(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+        const KvItem it = sm.items[slot];
+        mbar_arrive(&sm.item_empty[slot]);
+        ++it_count;
+        if (it.pairs < 0) break;
+        for (int n = 0; n < it.pairs; ++n) {
+          const uint32_t sq = qc & 3, sd = (qc + 2) & 3, fp = (qc >> 1) & 1, rb = qc & 1;
+          const uint32_t q_s = smem_u32(sm.qd[sq]);
+          if (!mbar_wait(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
+          if (!mbar_wait(&sm.ds_ready, 0, wc, hdr)) { ok = false; break; }
+          // the accumulators hold the previous item until its epilogue has read them
+          if (n == 0 && items_done > 0 &&
+              !mbar_wait(&sm.dkv_empty, (items_done - 1) & 1, wc, hdr)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          mma_ss_mn<D / 2>(tmem + 384, ds_s, q_s, 0, n > 0);              // dK_1 += dS_1^T Q_1
+          mma_commit(&sm.dk_done);
+          if (!mbar_wait(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
+          if (!mbar_wait(&sm.p_ready, qc & 1, wc, hdr)) { ok = false; break; }
+          tc_fence_after();
+          mma_ts_mn<32, D>(tmem + 256, tmem + 128 * rb, smem_u32(sm.qd[sd]), 0, n > 0);   // dV += P^T dOut
+          mma_commit(&sm.dv_done);
+          mma_commit(&sm.slot_empty[sd]);
+          if (!mbar_wait(&sm.ds_ready, 1, wc, hdr)) { ok = false; break; }
+          tc_fence_after();
+          mma_ss_mn<D / 2>(tmem + 384 + D / 2, ds_s, q_s, D / 2, n > 0);  // dK_2 += dS_2^T Q_2
+          mma_commit(&sm.dk_done);
+          mma_commit(&sm.slot_empty[sq]);
+          ++qc;
+        }
+        if (!ok) break;
+        mma_commit(&sm.dkv_full);
+        ++items_done;
+      }
+      mma_drain(&sm.drain2);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kKvRegsSoftmax));
+    // ------------------------------------------------------------ softmax + dK/dV epilogue
+    // Warp (cg, wq) covers TMEM lane quadrant wq (32 keys) and query columns
+    // 32 cg .. 32 cg + 31, as 16-lane fragments: thread t holds key rows wq 32 +
+    // t/4 + 8 i (i = 0..3) at columns 8 j + 2 (t % 4) + {0, 1} (j = 0..3).
+    // Register pair k = 8 h + 2 j + e is row 16 h + 8 e + t/4.
+    const int cg = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;                          // epilogue: TMEM lane = key row
+    const int tr = lane >> 2, tc2 = 2 * (lane & 3);
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const float sl2 = p.scale * kLog2e;
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    const uint64_t shift2 = f2_pack(kShift, kShift);
+    // dS^T tile: query block cg / 2, 16-byte chunks 4 (cg & 1) + j, swizzled
+    // by key & 7 (= tr for every fragment row)
+    const uint32_t ds_base = smem_u32(sm.ds) + (cg >> 1) * kBlk + (wq * 32 + tr) * 128 + 2 * tc2;
+    const float* const vec1 = sm.first[0] + cg * 32 + tc2;
+    const float* const vec2 = sm.second[0] + cg * 32 + tc2;
+    uint32_t it_count = 0, items_done = 0, qc = 0;
+    bool ok = true;
+    while (ok) {
+      const uint32_t slot = it_count & 1;
+      if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+      const KvItem it = sm.items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      ++it_count;
+      if (it.pairs < 0) break;
+      int qlo[4], qhi[4];                                  // queries that see fragment row i
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t key = (int64_t)it.ktile * 128 + wq * 32 + tr + 8 * i;
+        qlo[i] = qhi[i] = 0;
+        if (key < p.kv_len) {
+          const int b = doc_of(p.cu, p.ndoc, key);
+          qlo[i] = p.causal ? (int)key : __ldg(p.cu + b);
+          qhi[i] = (int)min((int64_t)__ldg(p.cu + b + 1), p.q_len);
+        }
+      }
+      int n_in = 0;                                        // query tile of the pair, 0 .. n_q - 1
+      for (int n = 0; n < it.pairs; ++n) {
+        const int q0 = (it.i_lo + n_in) * 128 + cg * 32;
+        if (++n_in == it.n_q) n_in = 0;
+        const uint32_t rb = qc & 1;
+        const uint32_t s_tm = tmem + lane_base + 128 * rb + cg * 32;
+        const uint32_t dp_tm = tmem + lane_base + 128 * (rb ^ 1) + cg * 32;
+        bool full = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) full = full && qlo[i] <= q0 && q0 + 32 <= qhi[i];
+        const bool full_w = __all_sync(0xffffffffu, full);
+        // ---- first map: P_1 2^15 and dS_1 2^15
+        if (!mbar_wait_warp(&sm.first_full, qc & 1, wc, hdr)) { ok = false; break; }
+        if (!mbar_wait_warp(&sm.s1_full, qc & 1, wc, hdr)) { ok = false; break; }
+        tc_fence_after();
+        uint64_t pp[16];
+        {
+          uint32_t x[32];
+          tmem_ld16x256_x4(s_tm, x);
+          tmem_ld16x256_x4(s_tm + (16u << 16), x + 16);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s1_free);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t nl = f2_add(*reinterpret_cast<const uint64_t*>(vec1 + 8 * j), shift2);
+#pragma unroll
+            for (int he = 0; he < 4; ++he) {
+              const int k = 8 * (he >> 1) + 2 * j + (he & 1);
+              float u0, u1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sl2x2,
+                               nl), u0, u1);
+              if (!full_w) {
+                const int q = q0 + 8 * j + tc2;
+                if (q < qlo[he] || q >= qhi[he]) u0 = -INFINITY;
+                if (q + 1 < qlo[he] || q + 1 >= qhi[he]) u1 = -INFINITY;
+              }
+              pp[k] = f2_pack(ex2(u0), ex2(u1));
+            }
+          }
+        }
+        if (!mbar_wait_warp(&sm.dp_full, qc & 1, wc, hdr)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t y[32];
+        tmem_ld16x256_x4(dp_tm, y);
+        tmem_ld16x256_x4(dp_tm + (16u << 16), y + 16);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.dp_free);
+        // the dS^T buffer is free once dK_2 of the previous pair has read it
+        if (qc >= 1 && !mbar_wait_warp(&sm.dk_done, 1, wc, hdr)) { ok = false; break; }
+        uint32_t ph[16];                                    // P_1 2^15, fp16 pairs
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t dl = *reinterpret_cast<const uint64_t*>(vec1 + 128 + 8 * j);
+          const int chunk = (cg & 1) * 4 + j;               // 8 query columns per 16 bytes
+#pragma unroll
+          for (int he = 0; he < 4; ++he) {
+            const int k = 8 * (he >> 1) + 2 * j + (he & 1);
+            const int rowoff = 16 * (he >> 1) + 8 * (he & 1);
+            float u0, u1;
+            f2_unpack(pp[k], u0, u1);
+            const __half2 hp = __floats2half2_rn(u0, u1);
+            ph[k] = *reinterpret_cast<const uint32_t*>(&hp);
+            f2_unpack(f2_mul(pp[k], f2_sub(f2_pack(__uint_as_float(y[2 * k]),
+                                                   __uint_as_float(y[2 * k + 1])), dl)), u0, u1);
+            st_shared_u32(ds_base + rowoff * 128 + ((chunk ^ tr) << 4), pack_bf16x2(u0, u1));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.ds_ready);
+          mbar_arrive(&sm.first_empty);
+        }
+        // ---- second map: P = P_1 + c P_2 (the dV operand, over S_2) and dS_2
+        if (!mbar_wait_warp(&sm.second_full, qc & 1, wc, hdr)) { ok = false; break; }
+        if (!mbar_wait_warp(&sm.s2_full, qc & 1, wc, hdr)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t ds2[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16], pk[8];
+          tmem_ld16x256_x4(s_tm + ((uint32_t)(16 * h) << 16), x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t nl = *reinterpret_cast<const uint64_t*>(vec2 + 8 * j);
+            const uint64_t dl = *reinterpret_cast<const uint64_t*>(vec2 + 128 + 8 * j);
+            const uint64_t cc = *reinterpret_cast<const uint64_t*>(vec2 + 256 + 8 * j);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int kk = 2 * j + e, k = 8 * h + kk;
+              float u0, u1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * kk]), __uint_as_float(x[2 * kk + 1])),
+                               sl2x2, nl), u0, u1);
+              if (!full_w) {
+                const int q = q0 + 8 * j + tc2, i = 2 * h + e;
+                if (q < qlo[i] || q >= qhi[i]) u0 = -INFINITY;
+                if (q + 1 < qlo[i] || q + 1 >= qhi[i]) u1 = -INFINITY;
+              }
+              const uint64_t p2 = f2_mul(f2_pack(ex2(u0), ex2(u1)), cc);
+              const float2 p1 = __half22float2(*reinterpret_cast<const __half2*>(&ph[k]));
+              f2_unpack(f2_fma(f2_pack(p1.x, p1.y), f2_pack(kUnshift, kUnshift), p2), u0, u1);
+              pk[kk] = pack_bf16x2(u0, u1);
+              f2_unpack(f2_mul(p2, f2_sub(f2_pack(__uint_as_float(y[2 * k]),
+                                                  __uint_as_float(y[2 * k + 1])), dl)), u0, u1);
+              ds2[k] = pack_bf16x2(u0, u1);
+            }
+          }
+          // pk[2 j + e] is (row 16 h + 8 e + t/4, packed column 4 j + t % 4): the
+          // 16x128b register order
+          tmem_st16x128_x4(s_tm + ((uint32_t)(16 * h) << 16), pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.p_ready);
+          mbar_arrive(&sm.second_empty);
+        }
+        if (!mbar_wait_warp(&sm.dk_done, 0, wc, hdr)) { ok = false; break; }   // dK_1 has read dS_1
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int chunk = (cg & 1) * 4 + ((k >> 1) & 3);
+          const int rowoff = 16 * (k >> 3) + 8 * (k & 1);
+          st_shared_u32(ds_base + rowoff * 128 + ((chunk ^ tr) << 4), ds2[k]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ds_ready);
+        ++qc;
+      }
+      if (!ok) break;
+      // item epilogue: column groups 0-1 write dV, 2-3 dK (64 columns each)
+      if (!mbar_wait_warp(&sm.dkv_full, items_done & 1, wc, hdr)) break;
+      tc_fence_after();
+      const int c0 = (cg & 1) * 64;
+      if (c0 < D) {
+        const int64_t key = (int64_t)it.ktile * 128 + r;
+        const bool is_dk = cg >= 2;
+        __nv_bfloat16* dst = (is_dk ? a.dk : a.dv) + (key * p.Hkv + it.g) * D + c0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_base + (is_dk ? 384u : 256u) + c0 + c * 32, v);
+          tmem_wait_ld();
+          const bool map1 = c0 + c * 32 < D / 2;
+          if (key < p.kv_len)
+            store_row32(dst + c * 32, v, is_dk ? (map1 ? p.scale * kUnshift : p.scale) : 1.f);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.dkv_empty);
+      ++items_done;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kKvWarpMma1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ================================================================ dQ
+
+constexpr int kQThreads = 320;
+constexpr int kQWarpProducer = 8, kQWarpMma = 9;
+constexpr int K_NS = 2;
+
+struct QItem {
+  int qtile, h, g, j_lo, n_kv, pad[3];     // n_kv 128-key tiles; -1 stops
+};
+
+struct __align__(1024) SmemQ {
+  uint8_t q[2][kTile], dout[2][kTile];     // this item's and the next one's
+  uint8_t k[K_NS][kTile];
+  uint8_t v[kTile];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[K_NS], k_empty[K_NS], v_full, v_empty;
+  uint64_t s_full[2], p_full[2], dp_full, dp_free, o_full, o_free;
+  uint64_t item_full[2], item_empty[2];
+  QItem items[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  WaitCtl wait;
+};
+static_assert(sizeof(SmemQ) <= kSmemLimit, "dQ tile set exceeds shared memory");
+
+template <int D>
+__global__ void __launch_bounds__(kQThreads, 1)
+    diff_bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_do,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ BwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const AttnProblem& p = a.p;
+  WsHeader* hdr = p.hdr;
+  // Launched behind the dK/dV kernel, which triggers only after its own wait:
+  // everything this kernel reads is complete.  It starts on the SMs that kernel
+  // frees and waits for it only before it exits, so that what follows in the
+  // stream follows both.
+  if (status_bad(hdr)) {
+    grid_dep_wait();
+    return;
+  }
+  SmemQ* smp = smem_view<SmemQ>(smem_raw, hdr);
+  if (smp == nullptr) {
+    grid_dep_wait();
+    return;
+  }
+  SmemQ& sm = *smp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.q_full[s], 1);
+      mbar_init(&sm.q_empty[s], 1);
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 8);
+      mbar_init(&sm.item_full[s], 1);
+      mbar_init(&sm.item_empty[s], 1 + 8);
+    }
+    for (int s = 0; s < K_NS; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+    }
+    mbar_init(&sm.v_full, 1);
+    mbar_init(&sm.v_empty, 1);
+    mbar_init(&sm.dp_full, 1);
+    mbar_init(&sm.dp_free, 8);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_free, 8);
+    mbar_init(&sm.drain, 1);
+    wait_ctl_init(&sm.wait, p.wait_budget);
+    fence_mbar_init();
+  }
+  if (warp == kQWarpMma) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == kQWarpProducer && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem = sm.tmem_base;
+  WaitCtl* const wc = &sm.wait;
+  const int G = p.Hq / p.Hkv;
+  const int n_items = hdr->n_items * p.Hq;
+  constexpr int kBlocks = D / 64;
+  constexpr uint32_t kLoad = kBlocks * kBlk;
+
+  if (warp == kQWarpProducer) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t it_count = 0, k_count = 0, v_count = 0;
+      bool ok = true;
+      while (ok) {
+        const int idx = atomicAdd(&hdr->counter, 1);
+        QItem it = {};
+        it.n_kv = -1;
+        if (idx < n_items) {
+          const int qt = a.qorder[idx / p.Hq];
+          const int2 tr = a.qtiles[qt];
+          it.qtile = qt;
+          it.h = idx % p.Hq;
+          it.g = it.h / G;
+          it.j_lo = tr.x;
+          it.n_kv = tr.y - tr.x + 1;
+        }
+        const uint32_t slot = it_count & 1, use = it_count >> 1;
+        if (use >= 1 && !mbar_wait(&sm.item_empty[slot], (use - 1) & 1, wc, hdr)) break;
+        sm.items[slot] = it;
+        mbar_arrive(&sm.item_full[slot]);
+        if (it.n_kv < 0) break;
+        if (use >= 1 && !mbar_wait(&sm.q_empty[slot], (use - 1) & 1, wc, hdr)) break;
+        mbar_arrive_expect_tx(&sm.q_full[slot], 2 * kLoad);
+#pragma unroll
+        for (int cb = 0; cb < kBlocks; ++cb) {
+          tma_load_2d(sm.q[slot] + cb * kBlk, &tm_q, &sm.q_full[slot], it.h * D + cb * 64, it.qtile * 128);
+          tma_load_2d(sm.dout[slot] + cb * kBlk, &tm_do, &sm.q_full[slot], it.h * D + cb * 64,
+                      it.qtile * 128);
+        }
+        ++it_count;
+        for (int jj = 0; jj < it.n_kv; ++jj) {
+          const int key0 = (it.j_lo + jj) * 128;
+          const uint32_t st = k_count % K_NS, n = k_count / K_NS;
+          if (n >= 1 && !mbar_wait(&sm.k_empty[st], (n - 1) & 1, wc, hdr)) { ok = false; break; }
+          mbar_arrive_expect_tx(&sm.k_full[st], kLoad);
+#pragma unroll
+          for (int cb = 0; cb < kBlocks; ++cb)
+            tma_load_2d(sm.k[st] + cb * kBlk, &tm_k, &sm.k_full[st], it.g * D + cb * 64, key0);
+          ++k_count;
+          if (v_count >= 1 && !mbar_wait(&sm.v_empty, (v_count - 1) & 1, wc, hdr)) { ok = false; break; }
+          mbar_arrive_expect_tx(&sm.v_full, kLoad);
+#pragma unroll
+          for (int cb = 0; cb < kBlocks; ++cb)
+            tma_load_2d(sm.v + cb * kBlk, &tm_v, &sm.v_full, it.g * D + cb * 64, key0);
+          ++v_count;
+        }
+      }
+      // leaving, normally or on an abort: every issued copy lands first
+      for (uint32_t j = it_count > 2 ? it_count - 2 : 0; j < it_count; ++j)
+        drain_wait(&sm.q_full[j & 1], (j >> 1) & 1);
+      for (uint32_t j = k_count > K_NS ? k_count - K_NS : 0; j < k_count; ++j)
+        drain_wait(&sm.k_full[j % K_NS], (j / K_NS) & 1);
+      if (v_count >= 1) drain_wait(&sm.v_full, (v_count - 1) & 1);
+    }
+  } else if (warp == kQWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    // Products run in issue order, so S_m of the next tile may follow dQ_m,
+    // which reads dS_m from the same columns, without a wait.
+    if (lane == 0) {
+      uint32_t it_count = 0, jc = 0;
+      while (true) {
+        const uint32_t slot = it_count & 1, use = it_count >> 1;
+        if (!mbar_wait(&sm.item_full[slot], use & 1, wc, hdr)) break;
+        const QItem it = sm.items[slot];
+        mbar_arrive(&sm.item_empty[slot]);
+        if (it.n_kv < 0) break;
+        if (!mbar_wait(&sm.q_full[slot], use & 1, wc, hdr)) break;
+        const uint32_t q_s = smem_u32(sm.q[slot]), do_s = smem_u32(sm.dout[slot]);
+        bool ok = true;
+        // dP and S_1 of tile t are issued before dQ_2 of tile t - 1, S_2 after it
+        auto issue_dp_s1 = [&](uint32_t t) {
+          if (!mbar_wait(&sm.v_full, t & 1, wc, hdr)) return false;
+          if (t >= 1 && !mbar_wait(&sm.dp_free, (t - 1) & 1, wc, hdr)) return false;
+          tc_fence_after();
+          mma_kk<D>(0, tmem + 256, do_s, smem_u32(sm.v));                   // dP = dOut V^T
+          mma_commit(&sm.dp_full);
+          mma_commit(&sm.v_empty);
+          if (!mbar_wait(&sm.k_full[t % K_NS], (t / K_NS) & 1, wc, hdr)) return false;
+          tc_fence_after();
+          mma_kk<D / 2>(0, tmem, q_s, smem_u32(sm.k[t % K_NS]));            // S_1 = Q_1 K_1^T
+          mma_commit(&sm.s_full[0]);
+          return true;
+        };
+        auto issue_s2 = [&](uint32_t t) {
+          mma_kk<D / 2>(1, tmem + 128, q_s, smem_u32(sm.k[t % K_NS]));
+          mma_commit(&sm.s_full[1]);
+        };
+        if (!issue_dp_s1(jc)) break;
+        issue_s2(jc);
+        for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
+          const uint32_t k_s = smem_u32(sm.k[jc % K_NS]);
+          const bool has_next = jj + 1 < it.n_kv;
+          if (!mbar_wait(&sm.p_full[0], jc & 1, wc, hdr)) { ok = false; break; }
+          // the first product overwrites dQ: read by the previous item's epilogue
+          if (jj == 0 && it_count >= 1 && !mbar_wait(&sm.o_free, (it_count - 1) & 1, wc, hdr)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          mma_ts_mn<64, D / 2>(tmem + 384, tmem, k_s, 0, jj > 0);           // dQ_1 += dS_1 K_1
+          if (has_next && !issue_dp_s1(jc + 1)) { ok = false; break; }
+          if (!mbar_wait(&sm.p_full[1], jc & 1, wc, hdr)) { ok = false; break; }
+          tc_fence_after();
+          mma_ts_mn<64, D / 2>(tmem + 384 + D / 2, tmem + 128, k_s, D / 2, jj > 0);   // dQ_2 += dS_2 K_2
+          mma_commit(&sm.k_empty[jc % K_NS]);
+          if (has_next) issue_s2(jc + 1);
+        }
+        if (!ok) break;
+        mma_commit(&sm.q_empty[slot]);
+        mma_commit(&sm.o_full);
+        ++it_count;
+      }
+      mma_drain(&sm.drain);               // every product done before TMEM is freed
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + dQ epilogue
+    const int wg = warp >> 2, wq = warp & 3;              // key columns 64 wg .. 64 wg + 63
+    const int r = wq * 32 + lane;                          // TMEM lane = query row
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const float sl2 = p.scale * kLog2e;
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    uint32_t it_count = 0, jc = 0;
+    bool ok = true;
+    while (ok) {
+      const uint32_t slot = it_count & 1;
+      if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+      const QItem it = sm.items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      if (it.n_kv < 0) break;
+      const int64_t row = (int64_t)it.qtile * 128 + r;
+      const bool valid = row < p.q_len;
+      int lo = 0, hi = 0;                                    // visible keys [lo, hi)
+      float nl[2] = {0.f, 0.f}, dl[2] = {0.f, 0.f}, c = 0.f;
+      if (valid) {
+        const int b = doc_of(p.cu, p.ndoc, row);
+        lo = __ldg(p.cu + b);
+        hi = p.causal ? (int)row + 1 : (int)min((int64_t)__ldg(p.cu + b + 1), p.kv_len);
+        const int64_t v1 = (int64_t)(2 * it.h) * a.Tp + row;
+        nl[0] = __ldg(a.nlse2 + v1);
+        nl[1] = __ldg(a.nlse2 + v1 + a.Tp);
+        dl[0] = __ldg(a.delta + v1);
+        dl[1] = __ldg(a.delta + v1 + a.Tp);
+        c = __ldg(a.coef + (int64_t)it.h * a.Tp + row);
+      }
+      for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
+        const int key0 = (it.j_lo + jj) * 128 + wg * 64;
+        const int c0 = lo - key0;
+        const uint32_t span = (uint32_t)(hi - lo);
+        const bool full_w = __all_sync(0xffffffffu, lo <= key0 && key0 + 64 <= hi);
+        uint32_t dp[64];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t s_tm = tmem + lane_base + 128 * m + wg * 64;
+          if (!ok) continue;
+          if (!mbar_wait_warp(&sm.s_full[m], jc & 1, wc, hdr)) { ok = false; continue; }
+          tc_fence_after();
+          uint32_t x[64];
+          tmem_ld32(s_tm, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld32(s_tm + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+          tmem_wait_ld();
+          const uint64_t nl2 = f2_pack(nl[m], nl[m]);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float u0, u1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2x2,
+                             nl2), u0, u1);
+            if (!full_w) {
+              if ((uint32_t)(2 * e - c0) >= span) u0 = -INFINITY;
+              if ((uint32_t)(2 * e + 1 - c0) >= span) u1 = -INFINITY;
+            }
+            x[2 * e] = __float_as_uint(ex2(u0));
+            x[2 * e + 1] = __float_as_uint(ex2(u1));
+          }
+          if (m == 0) {
+            if (!mbar_wait_warp(&sm.dp_full, jc & 1, wc, hdr)) { ok = false; continue; }
+            tc_fence_after();
+            const uint32_t dp_tm = tmem + lane_base + 256 + wg * 64;
+            tmem_ld32(dp_tm, *reinterpret_cast<uint32_t(*)[32]>(dp));
+            tmem_ld32(dp_tm + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.dp_free);
+          }
+          // dS over the S columns this warp has read; the second map's factor c
+          // is taken in with dP - delta: c dP - c delta
+          const float f = m == 0 ? 1.f : c, g = -f * dl[m];
+          const uint64_t f2 = f2_pack(f, f), g2 = f2_pack(g, g);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int i = 32 * cc + 2 * e;
+              float u0, u1;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                               f2_fma(f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])), f2,
+                                      g2)), u0, u1);
+              w[e] = pack_bf16x2(u0, u1);
+            }
+            tmem_st16(s_tm + cc * 16, w);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[m]);
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+      // epilogue: map wg of the row's gradient
+      if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
+      tc_fence_after();
+      __nv_bfloat16* dst = a.dq + (row * p.Hq + it.h) * D + wg * (D / 2);
+#pragma unroll
+      for (int cc = 0; cc < D / 64; ++cc) {
+        uint32_t v[32];
+        tmem_ld32(tmem + lane_base + 384 + wg * (D / 2) + cc * 32, v);
+        tmem_wait_ld();
+        if (cc == D / 64 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.o_free);
+        }
+        if (valid) store_row32(dst + cc * 32, v, p.scale);
+      }
+      ++it_count;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kQWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  grid_dep_wait();
+}
+
+template <typename K>
+cudaError_t launch_one(K kern, int threads, size_t smem, const CUtensorMap& mq, const CUtensorMap& mdo,
+                       const CUtensorMap& mk, const CUtensorMap& mv, const BwdArgs& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(persistent_grid()), dim3(threads), smem, s, mq, mdo, mk, mv, a);
+  count_launches(1);
+  count_path(true);
+  return e;
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
+                     const CUtensorMap& mv, const BwdArgs& a, cudaStream_t s) {
+  const cudaError_t e = launch_one(diff_bwd_dkdv_tc_kernel<D>, kKvThreads, smem_bytes<SmemKV>(), mq,
+                                   mdo, mk, mv, a, s);
+  if (e != cudaSuccess) return e;
+  return launch_one(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), mq, mdo, mk, mv, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char* ws, cudaStream_t s) {
+  const AttnProblem& p = d.p;
+  CUtensorMap mq, mdo, mk, mv;
+  const int64_t qc = (int64_t)p.Hq * p.d, kc = (int64_t)p.Hkv * p.d;
+  if (!diff_tile_map(&mq, p.q, p.q_len, qc) || !diff_tile_map(&mdo, d.dout, p.q_len, qc) ||
+      !diff_tile_map(&mk, p.k, p.kv_len, kc) || !diff_tile_map(&mv, p.v, p.kv_len, kc))
+    return cudaErrorNotSupported;
+  BwdArgs a;
+  a.p = p;
+  a.nlse2 = d.nlse2; a.delta = d.delta; a.coef = d.coef; a.Tp = d.Tp;
+  a.dq = reinterpret_cast<__nv_bfloat16*>(d.dq);
+  a.dk = reinterpret_cast<__nv_bfloat16*>(d.dk);
+  a.dv = reinterpret_cast<__nv_bfloat16*>(d.dv);
+  a.qtiles = reinterpret_cast<const int2*>(ws + L.qtiles);
+  a.qorder = reinterpret_cast<const int*>(ws + L.qorder);
+  a.ktiles = reinterpret_cast<const int2*>(ws + L.ktiles);
+  a.korder = reinterpret_cast<const int*>(ws + L.korder);
+  return p.d == 128 ? launch_d<128>(mq, mdo, mk, mv, a, s) : launch_d<64>(mq, mdo, mk, mv, a, s);
+}
+
+}  // namespace nsp

@@ -1,5 +1,5 @@
-// Differential attention on the CUDA cores, in true float32 arithmetic (no
-// TF32).
+// Differential attention on the CUDA cores: the path of float32 inputs, in
+// true float32 arithmetic (no TF32).
 //
 // Per document of the packed stream, with map m of a head reading columns
 // [m D/2, (m + 1) D/2) of q and k:
@@ -40,22 +40,14 @@ __device__ __forceinline__ float dot4(const float4& a, const float4& b, float ac
 __device__ __forceinline__ float4 ld4(const float* p) {
   return __ldg(reinterpret_cast<const float4*>(p));
 }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
 __device__ __forceinline__ void st4(float* p, const float4& x) {
   *reinterpret_cast<float4*>(p) = x;
-}
-__device__ __forceinline__ void st4(__nv_bfloat16* p, const float4& x) {
-  st_out(p, x.x); st_out(p + 1, x.y); st_out(p + 2, x.z); st_out(p + 3, x.w);
 }
 
 // ROWS rows of one head (row stride `stride` elements) into padded shared
 // rows; rows at or past `end` read as zero.
-template <int D, int ROWS, typename E>
-__device__ __forceinline__ void load_tile(float (*dst)[D + 4], const E* src, int64_t stride,
+template <int D, int ROWS>
+__device__ __forceinline__ void load_tile(float (*dst)[D + 4], const float* src, int64_t stride,
                                           int64_t row0, int64_t end) {
   for (int e = threadIdx.x; e < ROWS * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c = (e % (D / 4)) * 4;
@@ -72,10 +64,9 @@ __device__ __forceinline__ void visible(const AttnProblem& p, int64_t t, int& lo
   hi = p.causal ? (int)t + 1 : (int)min((int64_t)__ldg(p.cu + b + 1), p.kv_len);
 }
 
-template <typename E>
 __device__ __forceinline__ float lambda_of(const DiffProblem& a, int h, int64_t t) {
   const int64_t i = (int64_t)h * a.n_lambda + (a.n_lambda > 1 ? t : 0);
-  return to_f(reinterpret_cast<const E*>(a.lambda)[i]);
+  return reinterpret_cast<const float*>(a.lambda)[i];
 }
 
 // ---------------------------------------------------------------- forward
@@ -91,7 +82,7 @@ struct FwdSmem {
   int lo[kFwdM], hi[kFwdM];
 };
 
-template <typename E, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem_raw);
@@ -103,9 +94,9 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
   // longest rows first: causal tiles late in the stream see the most keys
   const int64_t row0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * kFwdM;
   const int64_t T = p.q_len;
-  const E* Q = reinterpret_cast<const E*>(p.q) + (int64_t)h * D;
-  const E* K = reinterpret_cast<const E*>(p.k) + (int64_t)g * D;
-  const E* V = reinterpret_cast<const E*>(p.v) + (int64_t)g * D;
+  const float* Q = reinterpret_cast<const float*>(p.q) + (int64_t)h * D;
+  const float* K = reinterpret_cast<const float*>(p.k) + (int64_t)g * D;
+  const float* V = reinterpret_cast<const float*>(p.v) + (int64_t)g * D;
   const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
 
   load_tile<D, kFwdM>(sm.q, Q, qs, row0, T);
@@ -200,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
     }
   }
 
-  E* O = reinterpret_cast<E*>(p.out);
-  E* O2 = reinterpret_cast<E*>(a.out2);
+  float* O = reinterpret_cast<float*>(p.out);
+  float* O2 = reinterpret_cast<float*>(a.out2);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t row = row0 + ty * 4 + i;
@@ -215,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
         p.lse[((int64_t)h * 2 + t) * T + row] = (m[t][i] + log2f(l[t][i])) * kLn2;
     }
     if (row >= T) continue;
-    const float lam = lambda_of<E>(a, h, row);
+    const float lam = lambda_of(a, h, row);
 #pragma unroll
     for (int c = 0; c < kCols; ++c) {
       const int64_t off = row * qs + (int64_t)h * D + c * 64 + tx * 4;
@@ -335,7 +326,7 @@ __device__ __forceinline__ void load_rows(BwdSmem<D>& sm, const DiffProblem& a, 
   sm.hi[r] = hi;
 }
 
-template <typename E, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
@@ -345,8 +336,8 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const Diff
   const int g = blockIdx.y, G = p.Hq / p.Hkv;
   const int64_t T = p.q_len, key0 = (int64_t)blockIdx.x * kBwdTile;
   const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
-  load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const E*>(p.k) + (int64_t)g * D, ks, key0, T);
-  load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const E*>(p.v) + (int64_t)g * D, ks, key0, T);
+  load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, key0, T);
+  load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const float*>(p.v) + (int64_t)g * D, ks, key0, T);
   const int64_t key1 = min(key0 + kBwdTile, T) - 1;
   const int b0 = doc_of(p.cu, p.ndoc, key0), b1 = doc_of(p.cu, p.ndoc, key1);
   const int64_t r_lo = p.causal ? key0 : (int64_t)__ldg(p.cu + b0);
@@ -356,8 +347,8 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const Diff
     const int h = g * G + hh;
     for (int64_t r0 = r_lo; r0 < r_hi; r0 += kBwdTile) {
       __syncthreads();
-      load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const E*>(p.q) + (int64_t)h * D, qs, r0, T);
-      load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const E*>(a.dout) + (int64_t)h * D, qs, r0, T);
+      load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const float*>(p.q) + (int64_t)h * D, qs, r0, T);
+      load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, r0, T);
       load_rows<D>(sm, a, h, r0);
       __syncthreads();
       tile_ds<D, true>(sm, key0, p.scale * kLog2e);
@@ -373,13 +364,13 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const Diff
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int64_t off = key * ks + (int64_t)g * D + c * 64 + tx * 4;
-      st4(reinterpret_cast<E*>(a.dk) + off, scaled(p.scale, dk[i][c]));
-      st4(reinterpret_cast<E*>(a.dv) + off, dv[i][c]);
+      st4(reinterpret_cast<float*>(a.dk) + off, scaled(p.scale, dk[i][c]));
+      st4(reinterpret_cast<float*>(a.dv) + off, dv[i][c]);
     }
   }
 }
 
-template <typename E, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
@@ -389,8 +380,8 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffPr
   const int h = blockIdx.y, g = h / (p.Hq / p.Hkv);
   const int64_t T = p.q_len, row0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * kBwdTile;
   const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
-  load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const E*>(p.q) + (int64_t)h * D, qs, row0, T);
-  load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const E*>(a.dout) + (int64_t)h * D, qs, row0, T);
+  load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const float*>(p.q) + (int64_t)h * D, qs, row0, T);
+  load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, row0, T);
   load_rows<D>(sm, a, h, row0);
   __syncthreads();
   const int last = (int)min((int64_t)kBwdTile, T - row0) - 1;
@@ -398,8 +389,8 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffPr
   float4 dq[2][D / 64] = {};
   for (int j0 = key_lo; j0 < key_hi; j0 += kBwdTile) {
     __syncthreads();
-    load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const E*>(p.k) + (int64_t)g * D, ks, j0, T);
-    load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const E*>(p.v) + (int64_t)g * D, ks, j0, T);
+    load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, j0, T);
+    load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const float*>(p.v) + (int64_t)g * D, ks, j0, T);
     __syncthreads();
     tile_ds<D, false>(sm, j0, p.scale * kLog2e);
     __syncthreads();
@@ -411,7 +402,7 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffPr
     if (row >= T) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      st4(reinterpret_cast<E*>(a.dq) + row * qs + (int64_t)h * D + c * 64 + tx * 4,
+      st4(reinterpret_cast<float*>(a.dq) + row * qs + (int64_t)h * D + c * 64 + tx * 4,
           scaled(p.scale, dq[i][c]));
   }
 }
@@ -426,31 +417,29 @@ cudaError_t launch(K kern, dim3 grid, size_t smem, const DiffProblem& a, cudaStr
   return cudaGetLastError();
 }
 
-template <typename E, int D>
+template <int D>
 cudaError_t fwd(const DiffProblem& a, cudaStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.p.q_len, kFwdM), a.p.Hq);
-  return launch(diff_fwd_simt_kernel<E, D>, grid, sizeof(FwdSmem<D>), a, s);
+  return launch(diff_fwd_simt_kernel<D>, grid, sizeof(FwdSmem<D>), a, s);
 }
 
-template <typename E, int D>
+template <int D>
 cudaError_t bwd(const DiffProblem& a, cudaStream_t s) {
   const unsigned tiles = (unsigned)ceil_div(a.p.q_len, kBwdTile);
   cudaError_t e =
-      launch(diff_bwd_dkdv_simt_kernel<E, D>, dim3(tiles, a.p.Hkv), sizeof(BwdSmem<D>), a, s);
+      launch(diff_bwd_dkdv_simt_kernel<D>, dim3(tiles, a.p.Hkv), sizeof(BwdSmem<D>), a, s);
   if (e != cudaSuccess) return e;
-  return launch(diff_bwd_dq_simt_kernel<E, D>, dim3(tiles, a.p.Hq), sizeof(BwdSmem<D>), a, s);
+  return launch(diff_bwd_dq_simt_kernel<D>, dim3(tiles, a.p.Hq), sizeof(BwdSmem<D>), a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s) {
-  return a.p.d == 128 ? fwd<float, 128>(a, s) : fwd<float, 64>(a, s);
+  return a.p.d == 128 ? fwd<128>(a, s) : fwd<64>(a, s);
 }
 
 cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s) {
-  using bf = __nv_bfloat16;
-  if (a.p.io_dtype == NSP_BF16) return a.p.d == 128 ? bwd<bf, 128>(a, s) : bwd<bf, 64>(a, s);
-  return a.p.d == 128 ? bwd<float, 128>(a, s) : bwd<float, 64>(a, s);
+  return a.p.d == 128 ? bwd<128>(a, s) : bwd<64>(a, s);
 }
 
 }  // namespace nsp

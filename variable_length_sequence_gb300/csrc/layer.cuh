@@ -76,6 +76,7 @@ cudaError_t launch_diff_fwd_tc(const DiffProblem& a, const FwdWsLayout& L, char*
 // swizzled; false without tensor-map support in the driver.
 bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols);
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s);
+cudaError_t launch_diff_bwd_tc(const DiffProblem& a, const BwdWsLayout& L, char* ws, cudaStream_t s);
 cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s);
 // delta, nlse2 and coef of the backward, and dlambda of each token
 cudaError_t launch_diff_prep(const DiffProblem& a, cudaStream_t s);

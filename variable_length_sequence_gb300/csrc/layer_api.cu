@@ -336,9 +336,10 @@ int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const voi
       return NSP_ERR_CUDA;
     return NSP_OK;
   }
-  if (launch_diff_prep(a, s) != cudaSuccess || launch_diff_bwd_simt(a, s) != cudaSuccess ||
-      launch_diff_dlambda(a, s) != cudaSuccess)
-    return NSP_ERR_CUDA;
+  if (launch_diff_prep(a, s) != cudaSuccess) return NSP_ERR_CUDA;
+  const cudaError_t e =
+      io_dtype == NSP_BF16 ? launch_diff_bwd_tc(a, L, ws, s) : launch_diff_bwd_simt(a, s);
+  if (e != cudaSuccess || launch_diff_dlambda(a, s) != cudaSuccess) return NSP_ERR_CUDA;
   return NSP_OK;
 }
 
