@@ -119,6 +119,24 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
                  w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
 }
 
+// Bits [lo, hi) of 32 columns (bounds relative to the first one, any value).
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
+  lo = min(max(lo, 0), 32);
+  hi = min(max(hi, 0), 32);
+  return hi <= lo ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+}
+
+// Masks of 16-bit pairs from column bits: pair j of the result covers bits
+// 8 j and 8 j + 1 of `bits`, 0xffff or 0 in each half.  A masked pair of
+// results is cleared whatever it holds (infinities and NaN included).
+__device__ __forceinline__ void pair_masks(uint32_t bits, uint32_t (&mask)[4]) {
+  const uint32_t even = bits << 7, odd = bits << 6;       // the bit at each byte's sign
+  asm("prmt.b32 %0, %1, %2, 0xcc88;" : "=r"(mask[0]) : "r"(even), "r"(odd));
+  asm("prmt.b32 %0, %1, %2, 0xdd99;" : "=r"(mask[1]) : "r"(even), "r"(odd));
+  asm("prmt.b32 %0, %1, %2, 0xeeaa;" : "=r"(mask[2]) : "r"(even), "r"(odd));
+  asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(mask[3]) : "r"(even), "r"(odd));
+}
+
 // 1024-aligned view of dynamic shared memory, or nullptr (error recorded)
 // when the aligned structure would not fit in the launch's allocation.
 template <typename S>
@@ -172,6 +190,17 @@ struct __align__(1024) SmemKV {
   WaitCtl wait;
 };
 static_assert(sizeof(SmemKV) <= kSmemLimit, "dK/dV tile set exceeds shared memory");
+
+// A warp's 32 x 32 fragment of dS^T (bf16 pairs k = 8 h + 2 j + e, see below)
+// into the swizzled shared tile.
+__device__ __forceinline__ void store_ds(uint32_t base, int cg, int tr, const uint32_t (&ds)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int chunk = (cg & 1) * 4 + ((k >> 1) & 3);      // 8 query columns per 16 bytes
+    const int row = 16 * (k >> 3) + 8 * (k & 1);
+    st_shared_u32(base + row * 128 + ((chunk ^ tr) << 4), ds[k]);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kKvThreads, 1)
@@ -496,11 +525,6 @@ __global__ void __launch_bounds__(kKvThreads, 1)
               float u0, u1;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sl2x2,
                                nl), u0, u1);
-              if (!full_w) {
-                const int q = q0 + 8 * j + tc2;
-                if (q < qlo[he] || q >= qhi[he]) u0 = -INFINITY;
-                if (q + 1 < qlo[he] || q + 1 >= qhi[he]) u1 = -INFINITY;
-              }
               pp[k] = f2_pack(ex2(u0), ex2(u1));
             }
           }
@@ -514,26 +538,38 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.dp_free);
-        // the dS^T buffer is free once dK_2 of the previous pair has read it
-        if (qc >= 1 && !mbar_wait_warp(&sm.dk_done, 1, wc, hdr)) { ok = false; break; }
-        uint32_t ph[16];                                    // P_1 2^15, fp16 pairs
+        uint32_t ph[16], ds[16];                            // P_1 2^15 (fp16 pairs), dS (bf16 pairs)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint64_t dl = *reinterpret_cast<const uint64_t*>(vec1 + 128 + 8 * j);
-          const int chunk = (cg & 1) * 4 + j;               // 8 query columns per 16 bytes
 #pragma unroll
           for (int he = 0; he < 4; ++he) {
             const int k = 8 * (he >> 1) + 2 * j + (he & 1);
-            const int rowoff = 16 * (he >> 1) + 8 * (he & 1);
             float u0, u1;
             f2_unpack(pp[k], u0, u1);
             const __half2 hp = __floats2half2_rn(u0, u1);
             ph[k] = *reinterpret_cast<const uint32_t*>(&hp);
             f2_unpack(f2_mul(pp[k], f2_sub(f2_pack(__uint_as_float(y[2 * k]),
                                                    __uint_as_float(y[2 * k + 1])), dl)), u0, u1);
-            st_shared_u32(ds_base + rowoff * 128 + ((chunk ^ tr) << 4), pack_bf16x2(u0, u1));
+            ds[k] = pack_bf16x2(u0, u1);
           }
         }
+        if (!full_w) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t mask[4];
+            pair_masks(column_bits(qlo[i] - q0, qhi[i] - q0) >> tc2, mask);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int k = 8 * (i >> 1) + 2 * j + (i & 1);
+              ph[k] &= mask[j];
+              ds[k] &= mask[j];
+            }
+          }
+        }
+        // the dS^T buffer is free once dK_2 of the previous pair has read it
+        if (qc >= 1 && !mbar_wait_warp(&sm.dk_done, 1, wc, hdr)) { ok = false; break; }
+        store_ds(ds_base, cg, tr, ds);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -544,7 +580,6 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (!mbar_wait_warp(&sm.second_full, qc & 1, wc, hdr)) { ok = false; break; }
         if (!mbar_wait_warp(&sm.s2_full, qc & 1, wc, hdr)) { ok = false; break; }
         tc_fence_after();
-        uint32_t ds2[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t x[16], pk[8];
@@ -561,18 +596,25 @@ __global__ void __launch_bounds__(kKvThreads, 1)
               float u0, u1;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * kk]), __uint_as_float(x[2 * kk + 1])),
                                sl2x2, nl), u0, u1);
-              if (!full_w) {
-                const int q = q0 + 8 * j + tc2, i = 2 * h + e;
-                if (q < qlo[i] || q >= qhi[i]) u0 = -INFINITY;
-                if (q + 1 < qlo[i] || q + 1 >= qhi[i]) u1 = -INFINITY;
-              }
               const uint64_t p2 = f2_mul(f2_pack(ex2(u0), ex2(u1)), cc);
               const float2 p1 = __half22float2(*reinterpret_cast<const __half2*>(&ph[k]));
               f2_unpack(f2_fma(f2_pack(p1.x, p1.y), f2_pack(kUnshift, kUnshift), p2), u0, u1);
               pk[kk] = pack_bf16x2(u0, u1);
               f2_unpack(f2_mul(p2, f2_sub(f2_pack(__uint_as_float(y[2 * k]),
                                                   __uint_as_float(y[2 * k + 1])), dl)), u0, u1);
-              ds2[k] = pack_bf16x2(u0, u1);
+              ds[k] = pack_bf16x2(u0, u1);
+            }
+          }
+          if (!full_w) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t mask[4];
+              pair_masks(column_bits(qlo[2 * h + e] - q0, qhi[2 * h + e] - q0) >> tc2, mask);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                pk[2 * j + e] &= mask[j];
+                ds[8 * h + 2 * j + e] &= mask[j];
+              }
             }
           }
           // pk[2 j + e] is (row 16 h + 8 e + t/4, packed column 4 j + t % 4): the
@@ -587,12 +629,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           mbar_arrive(&sm.second_empty);
         }
         if (!mbar_wait_warp(&sm.dk_done, 0, wc, hdr)) { ok = false; break; }   // dK_1 has read dS_1
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int chunk = (cg & 1) * 4 + ((k >> 1) & 3);
-          const int rowoff = 16 * (k >> 3) + 8 * (k & 1);
-          st_shared_u32(ds_base + rowoff * 128 + ((chunk ^ tr) << 4), ds2[k]);
-        }
+        store_ds(ds_base, cg, tr, ds);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.ds_ready);
@@ -876,8 +913,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
       }
       for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
         const int key0 = (it.j_lo + jj) * 128 + wg * 64;
-        const int c0 = lo - key0;
-        const uint32_t span = (uint32_t)(hi - lo);
         const bool full_w = __all_sync(0xffffffffu, lo <= key0 && key0 + 64 <= hi);
         uint32_t dp[64];
 #pragma unroll
@@ -896,10 +931,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
             float u0, u1;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2x2,
                              nl2), u0, u1);
-            if (!full_w) {
-              if ((uint32_t)(2 * e - c0) >= span) u0 = -INFINITY;
-              if ((uint32_t)(2 * e + 1 - c0) >= span) u1 = -INFINITY;
-            }
             x[2 * e] = __float_as_uint(ex2(u0));
             x[2 * e + 1] = __float_as_uint(ex2(u1));
           }
@@ -929,6 +960,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
                                f2_fma(f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])), f2,
                                       g2)), u0, u1);
               w[e] = pack_bf16x2(u0, u1);
+            }
+            if (!full_w) {
+              const uint32_t bits = column_bits(lo - key0 - 32 * cc, hi - key0 - 32 * cc);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {                // pairs of columns 8 j + 2 i
+                uint32_t mask[4];
+                pair_masks(bits >> (2 * i), mask);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[4 * j + i] &= mask[j];
+              }
             }
             tmem_st16(s_tm + cc * 16, w);
           }
