@@ -17,13 +17,13 @@
 // the maps as two heads would cost six.  TMEM: two 128-column regions [0,256),
 // dV [256,256+D), dK_1 | dK_2 [384,384+D).  Pair n puts S_1^T in region A = n & 1,
 // dP^T in the other one, B; S_2^T follows into A when the softmax warps have
-// read S_1, P^T (bf16, the dV operand) over S_2 when they have read that.  The
-// next pair swaps the regions, so its S_1 is computed (into B, read by then)
-// while the softmax is on this pair's second map.
-//   Softmax warps hold P_1 between the two steps as fp16 (the registers do not
-//   hold it in float32 beside dP), times 2^15 so that probabilities down to
-//   2^-29 keep fp16's 11 bits: an error of 2^-12 beside the 2^-9 of the bf16
-//   operand.  The factor rides in the exponent and is taken off dK_1 at the end.
+// read S_1.  dS_1^T (bf16) goes to shared memory; P^T = (P_1 + c P_2)^T and dS_2^T
+// (bf16) over S_2, 16 columns each of every 32: both are operands read from
+// TMEM, which spares shared memory's bandwidth (the kernel's tightest resource:
+// the operands of S, dP and dK_1, the tiles' copies and dS_1 take about 2900
+// cycles of it a pair against 2100 of the tensor core).  The next pair swaps the
+// regions, so its S_1 is computed into B, while the softmax is on this pair's
+// second map.
 //
 // dQ kernel (query-stationary).  Work item: one 128-row query tile of one head.
 // TMEM: S_1 [0,128), S_2 [128,256), dP [256,384), dQ_1 | dQ_2 [384,384+D).  dS_m
@@ -31,29 +31,22 @@
 // in registers for both maps; while it is on one map the tensor core does the
 // other map's dQ, the next S, and the next dP.
 //
-// Roles, dK/dV: 16 softmax warps (four column groups of four lane quadrants),
-// warp 16 producer of tiles, warps 17 and 18 one MMA stream each (S and dP;
+// Roles, dK/dV: 16 softmax warps (four column groups of four lane quadrants;
+// with 8 warps of 64 columns the loop is 18 KB of instructions and waits for
+// them), warp 16 producer of tiles, warps 17 and 18 one MMA stream each (S and dP;
 // dK and dV: products of one thread run in order, so those that wait for the
 // softmax must not hold up the others), warp 19 producer of the row vectors.
 // dQ: 8 softmax warps, warp 8 producer, warp 9 MMA.  All waits are bounded.
-#include <cuda_fp16.h>
-
-#include "layer.cuh"
-#include "tc_ptx.cuh"
+#include "diff_tc.cuh"
 
 namespace nsp {
 namespace {
 
 using namespace tc;
 
-constexpr uint32_t kBlk = 128 * 64 * 2;               // 128 rows x 64 bf16 column block
-constexpr uint32_t kTile = 2 * kBlk;                   // 128 x 128 bf16
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr size_t kSmemLimit = 232448;
-
 struct BwdArgs {
   AttnProblem p;
-  const float *nlse2, *delta;       // [2 Hq][Tp]
+  const float *nlse2, *ndelta;      // [2 Hq][Tp]
   const float* coef;                // [Hq][Tp]
   int64_t Tp;
   __nv_bfloat16 *dq, *dk, *dv;
@@ -63,107 +56,12 @@ struct BwdArgs {
   const int* korder;
 };
 
-// D = A B^T over columns [m HK, (m + 1) HK) of K-major 128-row tiles.
-template <int HK>
-__device__ __forceinline__ void mma_kk(int m, uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-  const uint64_t ad = smem_desc_sw128(a_saddr, 16, 1024);
-  const uint64_t bd = smem_desc_sw128(b_saddr, 16, 1024);
-#pragma unroll
-  for (int i = 0; i < HK / 16; ++i) {
-    const int kk = m * (HK / 16) + i;
-    const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
-    mma_ss(d_tmem, ad + off, bd + off, idesc, i > 0 ? 1u : 0u);
-  }
-}
-
-// Address of column n0 (a multiple of 32) of an MN-major tile's first rows.
-__device__ __forceinline__ uint32_t mn_offset(int n0) {
-  return (uint32_t)(n0 >> 6) * kBlk + (uint32_t)(n0 & 63) * 2;
-}
-
-// D (+)= A B, A (128 x 128) from TMEM in groups of QPG K-columns (group j at
-// columns a_tmem + j QPG + [0, QPG / 2), bf16 pairs), B MN-major columns
-// [n0, n0 + N) of a 128-row tile.
-template <int QPG, int N>
-__device__ __forceinline__ void mma_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_saddr, int n0,
-                                          bool accumulate) {
-  constexpr int kSteps = QPG / 16;
-  const uint64_t bd = smem_desc_sw128(b_saddr + mn_offset(n0), kBlk, 1024);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_ts(d_tmem, a_tmem + (kk / kSteps) * QPG + (kk % kSteps) * 8, bd + ((kk * 2048) >> 4),
-           idesc_bf16_f32(128, N, true, false), (accumulate || kk > 0) ? 1u : 0u);
-}
-
-// The same with A K-major in shared memory.
-template <int N>
-__device__ __forceinline__ void mma_ss_mn(uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr, int n0,
-                                          bool accumulate) {
-  const uint64_t ad = smem_desc_sw128(a_saddr, 16, 1024);
-  const uint64_t bd = smem_desc_sw128(b_saddr + mn_offset(n0), kBlk, 1024);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_ss(d_tmem, ad + (((kk >> 2) * kBlk + (kk & 3) * 32) >> 4), bd + ((kk * 2048) >> 4),
-           idesc_bf16_f32(128, N, true, false), (accumulate || kk > 0) ? 1u : 0u);
-}
-
-__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&v)[32], float scale) {
-  uint32_t w[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * scale, __uint_as_float(v[2 * i + 1]) * scale);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    st_global_v8(dst + 16 * i, w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3], w[8 * i + 4],
-                 w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
-}
-
-// Bits [lo, hi) of 32 columns (bounds relative to the first one, any value).
-__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
-  lo = min(max(lo, 0), 32);
-  hi = min(max(hi, 0), 32);
-  return hi <= lo ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
-}
-
-// Masks of 16-bit pairs from column bits: pair j of the result covers bits
-// 8 j and 8 j + 1 of `bits`, 0xffff or 0 in each half.  A masked pair of
-// results is cleared whatever it holds (infinities and NaN included).
-__device__ __forceinline__ void pair_masks(uint32_t bits, uint32_t (&mask)[4]) {
-  const uint32_t even = bits << 7, odd = bits << 6;       // the bit at each byte's sign
-  asm("prmt.b32 %0, %1, %2, 0xcc88;" : "=r"(mask[0]) : "r"(even), "r"(odd));
-  asm("prmt.b32 %0, %1, %2, 0xdd99;" : "=r"(mask[1]) : "r"(even), "r"(odd));
-  asm("prmt.b32 %0, %1, %2, 0xeeaa;" : "=r"(mask[2]) : "r"(even), "r"(odd));
-  asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(mask[3]) : "r"(even), "r"(odd));
-}
-
-// 1024-aligned view of dynamic shared memory, or nullptr (error recorded)
-// when the aligned structure would not fit in the launch's allocation.
-template <typename S>
-__device__ __forceinline__ S* smem_view(uint8_t* raw, WsHeader* hdr) {
-  uint32_t dyn_bytes;
-  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
-  const uint32_t base = smem_u32(raw);
-  if (((base + 1023u) & ~1023u) - base + sizeof(S) > dyn_bytes) {
-    if (threadIdx.x == 0) atomicExch(&hdr->status, (int)NSP_ERR_UNSUPPORTED);
-    return nullptr;
-  }
-  return reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
-                              ~static_cast<uintptr_t>(1023));
-}
-
-template <typename S>
-constexpr size_t smem_bytes() {
-  return sizeof(S) + 1024 <= kSmemLimit ? sizeof(S) + 1024 : kSmemLimit;
-}
-
 // ================================================================ dK / dV
 
 constexpr int kKvThreads = 640;
 constexpr int kKvSoftmaxWarps = 16;
 constexpr int kKvWarpTiles = 16, kKvWarpMma1 = 17, kKvWarpMma2 = 18, kKvWarpRows = 19;
 constexpr int kKvRegsControl = 64, kKvRegsSoftmax = 104;   // 128 x 64 + 512 x 104 = 640 x 96
-constexpr float kShift = 15.f, kUnshift = 1.f / 32768.f;    // exponent of P_1, see above
 
 struct KvItem {
   int ktile, g, i_lo, n_q, pairs, pad[3];    // pairs = heads * n_q; -1 stops
@@ -175,13 +73,13 @@ struct __align__(1024) SmemKV {
   // Q of pair j in slot j % 4, dOut in slot (j + 2) % 4, the (j / 2)-th fill
   // of their slots: Q of pair j + 2 takes the slot that dOut of pair j frees
   uint8_t qd[4][kTile];
-  uint8_t ds[kTile];                         // dS_m^T, [q-block][key][64 q], 128-byte swizzle
-  float first[2][128];                       // map 1: -lse log2 e, delta
-  float second[3][128];                      // map 2: -lse log2 e, delta, c
+  uint8_t ds[kTile];                         // dS_1^T, [q-block][key][64 q], 128-byte swizzle
+  float first[2][128];                       // map 1: -lse log2 e, -delta
+  float second[3][128];                      // map 2: -lse log2 e, -delta, c
   uint64_t kv_full, kv_empty;
   uint64_t slot_full[4], slot_empty[4];
-  uint64_t first_full, first_empty, second_full, second_empty;
-  uint64_t s1_full, s1_free, s2_full, dp_full, dp_free, p_ready, dv_done, ds_ready, dk_done;
+  uint64_t first_full, second_full;
+  uint64_t s1_full, s1_free, s2_full, dp_full, dp_free, ds_ready, p_ready, p_done;
   uint64_t dkv_full, dkv_empty;
   uint64_t item_full[2], item_empty[2];
   KvItem items[2];
@@ -191,15 +89,16 @@ struct __align__(1024) SmemKV {
 };
 static_assert(sizeof(SmemKV) <= kSmemLimit, "dK/dV tile set exceeds shared memory");
 
-// A warp's 32 x 32 fragment of dS^T (bf16 pairs k = 8 h + 2 j + e, see below)
-// into the swizzled shared tile.
-__device__ __forceinline__ void store_ds(uint32_t base, int cg, int tr, const uint32_t (&ds)[16]) {
+// Clears the masked pairs of a 16-lane fragment: rows e = 0 and 1 (pairs 2 j + e)
+// keep columns [lo_e, hi_e).
+__device__ __forceinline__ void mask_rows(uint32_t (&w)[8], int lo0, int hi0, int lo1, int hi1, int tc2) {
+  uint32_t mask[4];
+  pair_masks(column_bits(lo0, hi0) >> tc2, mask);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int chunk = (cg & 1) * 4 + ((k >> 1) & 3);      // 8 query columns per 16 bytes
-    const int row = 16 * (k >> 3) + 8 * (k & 1);
-    st_shared_u32(base + row * 128 + ((chunk ^ tr) << 4), ds[k]);
-  }
+  for (int j = 0; j < 4; ++j) w[2 * j] &= mask[j];
+  pair_masks(column_bits(lo1, hi1) >> tc2, mask);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[2 * j + 1] &= mask[j];
 }
 
 template <int D>
@@ -228,18 +127,15 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       mbar_init(&sm.slot_empty[s], 2);       // one commit of each stream
     }
     mbar_init(&sm.first_full, 1);
-    mbar_init(&sm.first_empty, kKvSoftmaxWarps);
     mbar_init(&sm.second_full, 1);
-    mbar_init(&sm.second_empty, kKvSoftmaxWarps);
     mbar_init(&sm.s1_full, 1);
     mbar_init(&sm.s1_free, kKvSoftmaxWarps);
     mbar_init(&sm.s2_full, 1);
     mbar_init(&sm.dp_full, 1);
     mbar_init(&sm.dp_free, kKvSoftmaxWarps);
     mbar_init(&sm.p_ready, kKvSoftmaxWarps);
-    mbar_init(&sm.dv_done, 1);
     mbar_init(&sm.ds_ready, kKvSoftmaxWarps);
-    mbar_init(&sm.dk_done, 1);
+    mbar_init(&sm.p_done, 1);
     mbar_init(&sm.dkv_full, 1);
     mbar_init(&sm.dkv_empty, kKvSoftmaxWarps);
     for (int s = 0; s < 2; ++s) {
@@ -337,7 +233,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     } else if (warp == kKvWarpRows && lane == 0) {
       // ------------------------------------------------------------ producer: row vectors
       // One buffer for each map: the first map's is free in the middle of a pair
-      // and wanted at the start of the next one, the second's the other way round.
+      // (all of dS_1 written) and wanted at the start of the next one, the
+      // second's the other way round.
       uint32_t it_count = 0, n1 = 0, n2 = 0;
       bool ok = true;
       while (ok) {
@@ -350,16 +247,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         int h = it.g * G, i = it.i_lo;
         for (int n = 0; n < it.pairs; ++n) {
           const int64_t r1 = (int64_t)(2 * h) * a.Tp + (int64_t)i * 128, r2 = r1 + a.Tp;
-          if (n1 >= 1 && !mbar_wait(&sm.first_empty, (n1 - 1) & 1, wc, hdr)) { ok = false; break; }
+          if (n1 >= 1 && !mbar_wait(&sm.ds_ready, (n1 - 1) & 1, wc, hdr)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.first_full, 2 * 512);
           bulk_load(sm.first[0], a.nlse2 + r1, 512, &sm.first_full);
-          bulk_load(sm.first[1], a.delta + r1, 512, &sm.first_full);
+          bulk_load(sm.first[1], a.ndelta + r1, 512, &sm.first_full);
           ++n1;
-          if (n2 >= 1 && !mbar_wait(&sm.second_empty, (n2 - 1) & 1, wc, hdr)) { ok = false; break; }
+          if (n2 >= 1 && !mbar_wait(&sm.p_ready, (n2 - 1) & 1, wc, hdr)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.second_full, 3 * 512);
           bulk_load(sm.second[0], a.nlse2 + r2, 512, &sm.second_full);
-          bulk_load(sm.second[1], a.delta + r2, 512, &sm.second_full);
-          bulk_load(sm.second[2], a.coef + (int64_t)h * a.Tp + (int64_t)i * 128, 512, &sm.second_full);
+          bulk_load(sm.second[1], a.ndelta + r2, 512, &sm.second_full);
+          bulk_load(sm.second[2], a.coef + (int64_t)h * a.Tp + (int64_t)i * 128, 512,
+                    &sm.second_full);
           ++n2;
           if (++i == it.i_lo + it.n_q) { i = it.i_lo; ++h; }
         }
@@ -383,14 +281,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           const uint32_t sq = qc & 3, sd = (qc + 2) & 3, fp = (qc >> 1) & 1, rb = qc & 1;
           const uint32_t ra = tmem + 128 * rb, rbb = tmem + 128 * (rb ^ 1);
           if (!mbar_wait(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
-          // A held the previous pair's dP: free once the softmax has read it
+          // A held the previous pair's dP: free once the softmax has read it twice
           if (qc >= 1 && !mbar_wait(&sm.dp_free, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           mma_kk<D / 2>(0, ra, k_s, smem_u32(sm.qd[sq]));                 // S_1^T = K_1 Q_1^T
           mma_commit(&sm.s1_full);
           if (!mbar_wait(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
-          // B held the previous pair's P: free once dV has read it
-          if (qc >= 1 && !mbar_wait(&sm.dv_done, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
+          // B held the previous pair's P and dS_2: free once dV and dK_2 have read them
+          if (qc >= 1 && !mbar_wait(&sm.p_done, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           mma_kk<D>(0, rbb, v_s, smem_u32(sm.qd[sd]));                    // dP^T = V dOut^T
           mma_commit(&sm.dp_full);
@@ -423,7 +321,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           const uint32_t sq = qc & 3, sd = (qc + 2) & 3, fp = (qc >> 1) & 1, rb = qc & 1;
           const uint32_t q_s = smem_u32(sm.qd[sq]);
           if (!mbar_wait(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
-          if (!mbar_wait(&sm.ds_ready, 0, wc, hdr)) { ok = false; break; }
+          if (!mbar_wait(&sm.ds_ready, qc & 1, wc, hdr)) { ok = false; break; }
           // the accumulators hold the previous item until its epilogue has read them
           if (n == 0 && items_done > 0 &&
               !mbar_wait(&sm.dkv_empty, (items_done - 1) & 1, wc, hdr)) {
@@ -432,17 +330,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           }
           tc_fence_after();
           mma_ss_mn<D / 2>(tmem + 384, ds_s, q_s, 0, n > 0);              // dK_1 += dS_1^T Q_1
-          mma_commit(&sm.dk_done);
           if (!mbar_wait(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
           if (!mbar_wait(&sm.p_ready, qc & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
-          mma_ts_mn<32, D>(tmem + 256, tmem + 128 * rb, smem_u32(sm.qd[sd]), 0, n > 0);   // dV += P^T dOut
-          mma_commit(&sm.dv_done);
+          const uint32_t a_tm = tmem + 128 * rb;
+          mma_ts_mn<32, D>(tmem + 256, a_tm, smem_u32(sm.qd[sd]), 0, n > 0);       // dV += P^T dOut
           mma_commit(&sm.slot_empty[sd]);
-          if (!mbar_wait(&sm.ds_ready, 1, wc, hdr)) { ok = false; break; }
-          tc_fence_after();
-          mma_ss_mn<D / 2>(tmem + 384 + D / 2, ds_s, q_s, D / 2, n > 0);  // dK_2 += dS_2^T Q_2
-          mma_commit(&sm.dk_done);
+          mma_ts_mn<32, D / 2>(tmem + 384 + D / 2, a_tm + 16, q_s, D / 2, n > 0);  // dK_2 += dS_2^T Q_2
+          mma_commit(&sm.p_done);
           mma_commit(&sm.slot_empty[sq]);
           ++qc;
         }
@@ -458,14 +353,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     // Warp (cg, wq) covers TMEM lane quadrant wq (32 keys) and query columns
     // 32 cg .. 32 cg + 31, as 16-lane fragments: thread t holds key rows wq 32 +
     // t/4 + 8 i (i = 0..3) at columns 8 j + 2 (t % 4) + {0, 1} (j = 0..3).
-    // Register pair k = 8 h + 2 j + e is row 16 h + 8 e + t/4.
+    // Register pair k = 8 h + 2 j + e is row i = 2 h + e, columns of j.
     const int cg = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;                          // epilogue: TMEM lane = key row
     const int tr = lane >> 2, tc2 = 2 * (lane & 3);
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const float sl2 = p.scale * kLog2e;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
-    const uint64_t shift2 = f2_pack(kShift, kShift);
     // dS^T tile: query block cg / 2, 16-byte chunks 4 (cg & 1) + j, swizzled
     // by key & 7 (= tr for every fragment row)
     const uint32_t ds_base = smem_u32(sm.ds) + (cg >> 1) * kBlk + (wq * 32 + tr) * 128 + 2 * tc2;
@@ -477,8 +371,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       const uint32_t slot = it_count & 1;
       if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
       const KvItem it = sm.items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      mbar_arrive_warp(&sm.item_empty[slot], lane);
       ++it_count;
       if (it.pairs < 0) break;
       int qlo[4], qhi[4];                                  // queries that see fragment row i
@@ -503,9 +396,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) full = full && qlo[i] <= q0 && q0 + 32 <= qhi[i];
         const bool full_w = __all_sync(0xffffffffu, full);
-        // ---- first map: P_1 2^15 and dS_1 2^15
-        if (!mbar_wait_warp(&sm.first_full, qc & 1, wc, hdr)) { ok = false; break; }
-        if (!mbar_wait_warp(&sm.s1_full, qc & 1, wc, hdr)) { ok = false; break; }
+        // ---- first map: P_1 (kept for the second) and dS_1
+        if (!wait_warp(&sm.first_full, qc & 1, wc, hdr)) { ok = false; break; }
+        if (!wait_warp(&sm.s1_full, qc & 1, wc, hdr)) { ok = false; break; }
         tc_fence_after();
         uint64_t pp[16];
         {
@@ -514,14 +407,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           tmem_ld16x256_x4(s_tm + (16u << 16), x + 16);
           tmem_wait_ld();
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s1_free);
+          mbar_arrive_warp(&sm.s1_free, lane);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint64_t nl = f2_add(*reinterpret_cast<const uint64_t*>(vec1 + 8 * j), shift2);
+            const uint64_t nl = *reinterpret_cast<const uint64_t*>(vec1 + 8 * j);
 #pragma unroll
-            for (int he = 0; he < 4; ++he) {
-              const int k = 8 * (he >> 1) + 2 * j + (he & 1);
+            for (int i = 0; i < 4; ++i) {
+              const int k = 8 * (i >> 1) + 2 * j + (i & 1);
               float u0, u1;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sl2x2,
                                nl), u0, u1);
@@ -529,110 +421,82 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             }
           }
         }
-        if (!mbar_wait_warp(&sm.dp_full, qc & 1, wc, hdr)) { ok = false; break; }
+        if (!wait_warp(&sm.dp_full, qc & 1, wc, hdr)) { ok = false; break; }
         tc_fence_after();
-        uint32_t y[32];
-        tmem_ld16x256_x4(dp_tm, y);
-        tmem_ld16x256_x4(dp_tm + (16u << 16), y + 16);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.dp_free);
-        uint32_t ph[16], ds[16];                            // P_1 2^15 (fp16 pairs), dS (bf16 pairs)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t dl = *reinterpret_cast<const uint64_t*>(vec1 + 128 + 8 * j);
-#pragma unroll
-          for (int he = 0; he < 4; ++he) {
-            const int k = 8 * (he >> 1) + 2 * j + (he & 1);
-            float u0, u1;
-            f2_unpack(pp[k], u0, u1);
-            const __half2 hp = __floats2half2_rn(u0, u1);
-            ph[k] = *reinterpret_cast<const uint32_t*>(&hp);
-            f2_unpack(f2_mul(pp[k], f2_sub(f2_pack(__uint_as_float(y[2 * k]),
-                                                   __uint_as_float(y[2 * k + 1])), dl)), u0, u1);
-            ds[k] = pack_bf16x2(u0, u1);
-          }
-        }
-        if (!full_w) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t mask[4];
-            pair_masks(column_bits(qlo[i] - q0, qhi[i] - q0) >> tc2, mask);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int k = 8 * (i >> 1) + 2 * j + (i & 1);
-              ph[k] &= mask[j];
-              ds[k] &= mask[j];
-            }
-          }
-        }
-        // the dS^T buffer is free once dK_2 of the previous pair has read it
-        if (qc >= 1 && !mbar_wait_warp(&sm.dk_done, 1, wc, hdr)) { ok = false; break; }
-        store_ds(ds_base, cg, tr, ds);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.ds_ready);
-          mbar_arrive(&sm.first_empty);
-        }
-        // ---- second map: P = P_1 + c P_2 (the dV operand, over S_2) and dS_2
-        if (!mbar_wait_warp(&sm.second_full, qc & 1, wc, hdr)) { ok = false; break; }
-        if (!mbar_wait_warp(&sm.s2_full, qc & 1, wc, hdr)) { ok = false; break; }
-        tc_fence_after();
+        // (dP of this pair follows dK_1 of the previous one, so dS_1's buffer is free)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t x[16], pk[8];
-          tmem_ld16x256_x4(s_tm + ((uint32_t)(16 * h) << 16), x);
+          uint32_t y[16], ds[8];
+          tmem_ld16x256_x4(dp_tm + ((uint32_t)(16 * h) << 16), y);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            const uint64_t nd = *reinterpret_cast<const uint64_t*>(vec1 + 128 + 8 * j);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int kk = 2 * j + e;
+              float u0, u1;
+              f2_unpack(f2_mul(pp[8 * h + kk], f2_add(f2_pack(__uint_as_float(y[2 * kk]),
+                                                              __uint_as_float(y[2 * kk + 1])), nd)),
+                        u0, u1);
+              ds[kk] = pack_bf16x2(u0, u1);
+            }
+          }
+          if (!full_w) mask_rows(ds, qlo[2 * h] - q0, qhi[2 * h] - q0, qlo[2 * h + 1] - q0,
+                                 qhi[2 * h + 1] - q0, tc2);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const int chunk = (cg & 1) * 4 + (kk >> 1);      // 8 query columns per 16 bytes
+            st_shared_u32(ds_base + (16 * h + 8 * (kk & 1)) * 128 + ((chunk ^ tr) << 4), ds[kk]);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(&sm.ds_ready, lane);
+        // ---- second map: P = P_1 + c P_2 and dS_2, the operands of dV and dK_2
+        if (!wait_warp(&sm.second_full, qc & 1, wc, hdr)) { ok = false; break; }
+        if (!wait_warp(&sm.s2_full, qc & 1, wc, hdr)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16], y[16], pk[8], ds[8];
+          tmem_ld16x256_x4(s_tm + ((uint32_t)(16 * h) << 16), x);
+          tmem_ld16x256_x4(dp_tm + ((uint32_t)(16 * h) << 16), y);
+          tmem_wait_ld();
+          if (h == 1) {
+            tc_fence_before();
+            mbar_arrive_warp(&sm.dp_free, lane);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
             const uint64_t nl = *reinterpret_cast<const uint64_t*>(vec2 + 8 * j);
-            const uint64_t dl = *reinterpret_cast<const uint64_t*>(vec2 + 128 + 8 * j);
+            const uint64_t nd = *reinterpret_cast<const uint64_t*>(vec2 + 128 + 8 * j);
             const uint64_t cc = *reinterpret_cast<const uint64_t*>(vec2 + 256 + 8 * j);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int kk = 2 * j + e, k = 8 * h + kk;
+              const int kk = 2 * j + e;
               float u0, u1;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * kk]), __uint_as_float(x[2 * kk + 1])),
                                sl2x2, nl), u0, u1);
               const uint64_t p2 = f2_mul(f2_pack(ex2(u0), ex2(u1)), cc);
-              const float2 p1 = __half22float2(*reinterpret_cast<const __half2*>(&ph[k]));
-              f2_unpack(f2_fma(f2_pack(p1.x, p1.y), f2_pack(kUnshift, kUnshift), p2), u0, u1);
+              f2_unpack(f2_add(pp[8 * h + kk], p2), u0, u1);
               pk[kk] = pack_bf16x2(u0, u1);
-              f2_unpack(f2_mul(p2, f2_sub(f2_pack(__uint_as_float(y[2 * k]),
-                                                  __uint_as_float(y[2 * k + 1])), dl)), u0, u1);
-              ds[k] = pack_bf16x2(u0, u1);
+              f2_unpack(f2_mul(p2, f2_add(f2_pack(__uint_as_float(y[2 * kk]),
+                                                  __uint_as_float(y[2 * kk + 1])), nd)), u0, u1);
+              ds[kk] = pack_bf16x2(u0, u1);
             }
           }
           if (!full_w) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t mask[4];
-              pair_masks(column_bits(qlo[2 * h + e] - q0, qhi[2 * h + e] - q0) >> tc2, mask);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                pk[2 * j + e] &= mask[j];
-                ds[8 * h + 2 * j + e] &= mask[j];
-              }
-            }
+            mask_rows(pk, qlo[2 * h] - q0, qhi[2 * h] - q0, qlo[2 * h + 1] - q0, qhi[2 * h + 1] - q0, tc2);
+            mask_rows(ds, qlo[2 * h] - q0, qhi[2 * h] - q0, qlo[2 * h + 1] - q0, qhi[2 * h + 1] - q0, tc2);
           }
-          // pk[2 j + e] is (row 16 h + 8 e + t/4, packed column 4 j + t % 4): the
+          // pair 2 j + e is (row 16 h + 8 e + t/4, packed column 4 j + t % 4): the
           // 16x128b register order
           tmem_st16x128_x4(s_tm + ((uint32_t)(16 * h) << 16), pk);
+          tmem_st16x128_x4(s_tm + 16 + ((uint32_t)(16 * h) << 16), ds);
         }
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.p_ready);
-          mbar_arrive(&sm.second_empty);
-        }
-        if (!mbar_wait_warp(&sm.dk_done, 0, wc, hdr)) { ok = false; break; }   // dK_1 has read dS_1
-        store_ds(ds_base, cg, tr, ds);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ds_ready);
+        mbar_arrive_warp(&sm.p_ready, lane);
         ++qc;
       }
       if (!ok) break;
@@ -649,14 +513,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           uint32_t v[32];
           tmem_ld32(tmem + lane_base + (is_dk ? 384u : 256u) + c0 + c * 32, v);
           tmem_wait_ld();
-          const bool map1 = c0 + c * 32 < D / 2;
-          if (key < p.kv_len)
-            store_row32(dst + c * 32, v, is_dk ? (map1 ? p.scale * kUnshift : p.scale) : 1.f);
+          if (key < p.kv_len) store_row32(dst + c * 32, v, is_dk ? p.scale : 1.f);
         }
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.dkv_empty);
+      mbar_arrive_warp(&sm.dkv_empty, lane);
       ++items_done;
     }
   }
@@ -835,25 +696,25 @@ __global__ void __launch_bounds__(kQThreads, 1)
         if (!mbar_wait(&sm.q_full[slot], use & 1, wc, hdr)) break;
         const uint32_t q_s = smem_u32(sm.q[slot]), do_s = smem_u32(sm.dout[slot]);
         bool ok = true;
-        // dP and S_1 of tile t are issued before dQ_2 of tile t - 1, S_2 after it
-        auto issue_dp_s1 = [&](uint32_t t) {
+        // S_1 and dP of tile t are issued before dQ_2 of tile t - 1, S_2 after it
+        auto issue_s1_dp = [&](uint32_t t) {
+          if (!mbar_wait(&sm.k_full[t % K_NS], (t / K_NS) & 1, wc, hdr)) return false;
+          tc_fence_after();
+          mma_kk<D / 2>(0, tmem, q_s, smem_u32(sm.k[t % K_NS]));            // S_1 = Q_1 K_1^T
+          mma_commit(&sm.s_full[0]);
           if (!mbar_wait(&sm.v_full, t & 1, wc, hdr)) return false;
           if (t >= 1 && !mbar_wait(&sm.dp_free, (t - 1) & 1, wc, hdr)) return false;
           tc_fence_after();
           mma_kk<D>(0, tmem + 256, do_s, smem_u32(sm.v));                   // dP = dOut V^T
           mma_commit(&sm.dp_full);
           mma_commit(&sm.v_empty);
-          if (!mbar_wait(&sm.k_full[t % K_NS], (t / K_NS) & 1, wc, hdr)) return false;
-          tc_fence_after();
-          mma_kk<D / 2>(0, tmem, q_s, smem_u32(sm.k[t % K_NS]));            // S_1 = Q_1 K_1^T
-          mma_commit(&sm.s_full[0]);
           return true;
         };
         auto issue_s2 = [&](uint32_t t) {
           mma_kk<D / 2>(1, tmem + 128, q_s, smem_u32(sm.k[t % K_NS]));
           mma_commit(&sm.s_full[1]);
         };
-        if (!issue_dp_s1(jc)) break;
+        if (!issue_s1_dp(jc)) break;
         issue_s2(jc);
         for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
           const uint32_t k_s = smem_u32(sm.k[jc % K_NS]);
@@ -866,7 +727,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
           tc_fence_after();
           mma_ts_mn<64, D / 2>(tmem + 384, tmem, k_s, 0, jj > 0);           // dQ_1 += dS_1 K_1
-          if (has_next && !issue_dp_s1(jc + 1)) { ok = false; break; }
+          if (has_next && !issue_s1_dp(jc + 1)) { ok = false; break; }
           if (!mbar_wait(&sm.p_full[1], jc & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           mma_ts_mn<64, D / 2>(tmem + 384 + D / 2, tmem + 128, k_s, D / 2, jj > 0);   // dQ_2 += dS_2 K_2
@@ -893,8 +754,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const uint32_t slot = it_count & 1;
       if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
       const QItem it = sm.items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      mbar_arrive_warp(&sm.item_empty[slot], lane);
       if (it.n_kv < 0) break;
       const int64_t row = (int64_t)it.qtile * 128 + r;
       const bool valid = row < p.q_len;
@@ -907,8 +767,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
         const int64_t v1 = (int64_t)(2 * it.h) * a.Tp + row;
         nl[0] = __ldg(a.nlse2 + v1);
         nl[1] = __ldg(a.nlse2 + v1 + a.Tp);
-        dl[0] = __ldg(a.delta + v1);
-        dl[1] = __ldg(a.delta + v1 + a.Tp);
+        dl[0] = __ldg(a.ndelta + v1);
+        dl[1] = __ldg(a.ndelta + v1 + a.Tp);
         c = __ldg(a.coef + (int64_t)it.h * a.Tp + row);
       }
       for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
@@ -919,7 +779,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         for (int m = 0; m < 2; ++m) {
           const uint32_t s_tm = tmem + lane_base + 128 * m + wg * 64;
           if (!ok) continue;
-          if (!mbar_wait_warp(&sm.s_full[m], jc & 1, wc, hdr)) { ok = false; continue; }
+          if (!wait_warp(&sm.s_full[m], jc & 1, wc, hdr)) { ok = false; continue; }
           tc_fence_after();
           uint32_t x[64];
           tmem_ld32(s_tm, *reinterpret_cast<uint32_t(*)[32]>(x));
@@ -935,19 +795,18 @@ __global__ void __launch_bounds__(kQThreads, 1)
             x[2 * e + 1] = __float_as_uint(ex2(u1));
           }
           if (m == 0) {
-            if (!mbar_wait_warp(&sm.dp_full, jc & 1, wc, hdr)) { ok = false; continue; }
+            if (!wait_warp(&sm.dp_full, jc & 1, wc, hdr)) { ok = false; continue; }
             tc_fence_after();
             const uint32_t dp_tm = tmem + lane_base + 256 + wg * 64;
             tmem_ld32(dp_tm, *reinterpret_cast<uint32_t(*)[32]>(dp));
             tmem_ld32(dp_tm + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
             tmem_wait_ld();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.dp_free);
+            mbar_arrive_warp(&sm.dp_free, lane);
           }
           // dS over the S columns this warp has read; the second map's factor c
           // is taken in with dP - delta: c dP - c delta
-          const float f = m == 0 ? 1.f : c, g = -f * dl[m];
+          const float f = m == 0 ? 1.f : c, g = f * dl[m];
           const uint64_t f2 = f2_pack(f, f), g2 = f2_pack(g, g);
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
@@ -975,8 +834,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
           tmem_wait_st();
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_full[m]);
+          mbar_arrive_warp(&sm.p_full[m], lane);
         }
         if (!ok) break;
       }
@@ -992,8 +850,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         tmem_wait_ld();
         if (cc == D / 64 - 1) {
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.o_free);
+          mbar_arrive_warp(&sm.o_free, lane);
         }
         if (valid) store_row32(dst + cc * 32, v, p.scale);
       }
@@ -1041,7 +898,7 @@ cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char*
     return cudaErrorNotSupported;
   BwdArgs a;
   a.p = p;
-  a.nlse2 = d.nlse2; a.delta = d.delta; a.coef = d.coef; a.Tp = d.Tp;
+  a.nlse2 = d.nlse2; a.ndelta = d.ndelta; a.coef = d.coef; a.Tp = d.Tp;
   a.dq = reinterpret_cast<__nv_bfloat16*>(d.dq);
   a.dk = reinterpret_cast<__nv_bfloat16*>(d.dk);
   a.dv = reinterpret_cast<__nv_bfloat16*>(d.dv);

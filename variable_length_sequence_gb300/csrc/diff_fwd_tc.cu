@@ -32,8 +32,7 @@
 // denominator share the reference).
 #include <cudaTypedefs.h>
 
-#include "layer.cuh"
-#include "tc_ptx.cuh"
+#include "diff_tc.cuh"
 
 namespace nsp {
 namespace {
@@ -45,13 +44,9 @@ constexpr int NSTAGE = 2;
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 192, kRegsControl = 112;
 constexpr int kWarpProducer = 8, kWarpMma = 9;
-constexpr uint32_t kColBlock = 128 * 64 * 2;              // 128 rows x 64 bf16 (one swizzle span)
-constexpr uint32_t kTile = 2 * kColBlock;
 __host__ __device__ constexpr uint32_t col_s(int m) { return m == 0 ? 0u : 128u; }
 __host__ __device__ constexpr uint32_t col_o(int m) { return m == 0 ? 256u : 384u; }
 constexpr float kRescaleThreshold = 8.0f;                 // log2 units
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct Item {
   int qtile, h, g, j_lo, n_kv;         // n_kv 128-key tiles from j_lo; -1 stops
@@ -73,7 +68,7 @@ struct __align__(1024) Smem {
   WaitCtl wait;
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;        // + alignment slack
-static_assert(kSmemBytes <= 232448, "forward tile set exceeds shared memory");
+static_assert(kSmemBytes <= kSmemLimit, "forward tile set exceeds shared memory");
 
 struct FwdArgs {
   AttnProblem p;
@@ -83,33 +78,6 @@ struct FwdArgs {
   const int2* tiles;
   const int* order;
 };
-
-// S_m = Q_m K_m^T: D / 32 products of K = 16 over the map's half of the
-// columns.  Both operands K-major with 128-byte swizzle; 16 columns are 32
-// bytes of a row, 64 columns one column block.
-template <int D>
-__device__ __forceinline__ void issue_qk(int m, uint32_t d_tmem, uint32_t q_saddr, uint32_t k_saddr) {
-  constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, false);
-  const uint64_t qd = smem_desc_sw128(q_saddr, 16, 1024);
-  const uint64_t kd = smem_desc_sw128(k_saddr, 16, 1024);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int kk = m * (D / 32) + i;
-    const uint32_t off = ((kk >> 2) * kColBlock + (kk & 3) * 32) >> 4;
-    mma_ss(d_tmem, qd + off, kd + off, idesc, i > 0 ? 1u : 0u);
-  }
-}
-
-// O (+)= P V: P from TMEM, 8 columns per 16 keys; V MN-major (keys along K).
-template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_saddr,
-                                         bool accumulate) {
-  constexpr uint32_t idesc = idesc_bf16_f32(BM, D, true);
-  const uint64_t vd = smem_desc_sw128(v_saddr, kColBlock, 1024);
-#pragma unroll
-  for (int kk = 0; kk < BN / 16; ++kk)
-    mma_ts(d_tmem, p_tmem + kk * 8, vd + ((kk * 2048) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -165,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = p.Hq / p.Hkv;
   const int n_items = hdr->n_items * p.Hq;
   constexpr int kBlocks = D / 64;                               // 64-column blocks of a row
-  constexpr uint32_t kLoadBytes = kBlocks * kColBlock;          // one Q, K or V tile
+  constexpr uint32_t kLoadBytes = kBlocks * kBlk;          // one Q, K or V tile
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
@@ -196,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&sm.q_full[slot], kLoadBytes);
 #pragma unroll
         for (int cb = 0; cb < kBlocks; ++cb)
-          tma_load_2d(sm.q[slot] + cb * kColBlock, &tm_q, &sm.q_full[slot], it.h * D + cb * 64,
+          tma_load_2d(sm.q[slot] + cb * kBlk, &tm_q, &sm.q_full[slot], it.h * D + cb * 64,
                       it.qtile * BM);
         ++it_count;
         for (int jj = 0; jj < it.n_kv; ++jj) {
@@ -206,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&sm.k_full[st], kLoadBytes);
 #pragma unroll
           for (int cb = 0; cb < kBlocks; ++cb)
-            tma_load_2d(sm.k[st] + cb * kColBlock, &tm_k, &sm.k_full[st], it.g * D + cb * 64, key0);
+            tma_load_2d(sm.k[st] + cb * kBlk, &tm_k, &sm.k_full[st], it.g * D + cb * 64, key0);
           if (n >= 1 && !mbar_wait(&sm.v_empty[st], (n - 1) & 1, wc, hdr)) {
             drain_wait(&sm.k_full[st], n & 1);      // the K copy just issued is in flight
             ok = false;
@@ -215,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&sm.v_full[st], kLoadBytes);
 #pragma unroll
           for (int cb = 0; cb < kBlocks; ++cb)
-            tma_load_2d(sm.v[st] + cb * kColBlock, &tm_v, &sm.v_full[st], it.g * D + cb * 64, key0);
+            tma_load_2d(sm.v[st] + cb * kBlk, &tm_v, &sm.v_full[st], it.g * D + cb * 64, key0);
           ++kv_count;
         }
       }
@@ -245,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ks = smem_u32(sm.k[st]);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            issue_qk<D>(m, tmem + col_s(m), qs, ks);
+            mma_kk<D / 2>(m, tmem + col_s(m), qs, ks);              // S_m = Q_m K_m^T
             mma_commit(&sm.s_full[m]);
           }
           mma_commit(&sm.k_empty[st]);
@@ -267,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) continue;
             if (!mbar_wait(&sm.p_full[m], p_count & 1, wc, hdr)) { ok = false; continue; }
             tc_fence_after();
-            issue_pv<D>(tmem + col_o(m), tmem + col_s(m), vs, jj > 0);
+            mma_ts_mn<128, D>(tmem + col_o(m), tmem + col_s(m), vs, 0, jj > 0);   // O_m += P_m V
             if (m == 1) mma_commit(&sm.v_empty[st]);
             if (!has_next) {
               if (m == 1) mma_commit(&sm.o_full);
@@ -277,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!mbar_wait(&sm.k_full[stn], nn & 1, wc, hdr)) { ok = false; continue; }
               tc_fence_after();
             }
-            issue_qk<D>(m, tmem + col_s(m), qs, smem_u32(sm.k[stn]));
+            mma_kk<D / 2>(m, tmem + col_s(m), qs, smem_u32(sm.k[stn]));
             mma_commit(&sm.s_full[m]);
             if (m == 1) {
               mma_commit(&sm.k_empty[stn]);
@@ -308,8 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t slot = it_count & 1;
       if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
       const Item it = sm.items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      mbar_arrive_warp(&sm.item_empty[slot], lane);
       if (it.n_kv < 0) break;
       const int64_t row = (int64_t)it.qtile * BM + r;
       const bool valid = row < p.q_len;
@@ -324,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int jj = 0; jj < it.n_kv; ++jj) {
-        if (!mbar_wait_warp(&sm.s_full[m_], s_count & 1, wc, hdr)) { ok = false; break; }
+        if (!wait_warp(&sm.s_full[m_], s_count & 1, wc, hdr)) { ok = false; break; }
         ++s_count;
         tc_fence_after();
         const int key0 = (it.j_lo + jj) * BN;
@@ -400,8 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.inv[slot][m_][r] = l > 0.f ? 1.f / l : 0.f;
       if (valid && p.lse != nullptr)
         p.lse[((int64_t)it.h * 2 + m_) * p.q_len + row] = (m + __log2f(l)) * kLn2;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.inv_full);
+      mbar_arrive_warp(&sm.inv_full, lane);
       if (!mbar_wait_warp(&sm.inv_full, it_count & 1, wc, hdr)) break;
       if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
       tc_fence_after();
@@ -416,8 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         if (c == D / 64 - 1) {             // both accumulators read: the next item may start
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.o_free);
+          mbar_arrive_warp(&sm.o_free, lane);
         }
         if (!valid) continue;
         uint32_t w[16], w2[16];

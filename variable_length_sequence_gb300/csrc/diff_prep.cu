@@ -5,7 +5,7 @@
 // O_2 saved by the forward:
 //   delta_2 = <dout, out2>,  delta_1 = <dout, out> + lambda delta_2,
 //   dlambda = -delta_2 (of each token), or its sum over the tokens.
-// Written as [2 Hq][Tp] rows (delta, -lse log2 e) and [Hq][Tp] (-lambda, the
+// Written as [2 Hq][Tp] rows (-delta, -lse log2 e) and [Hq][Tp] (-lambda, the
 // factor of the second map's probabilities), padded with zeros to whole
 // 128-row tiles.  Bound: HBM, one read of out, out2 and dout.
 #include <algorithm>
@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
       const int h = (int)(r - t * p.Hq);
       const float lam = to_f(L[(int64_t)h * a.n_lambda + (a.n_lambda > 1 ? t : 0)]);
       const int64_t v1 = (int64_t)h * 2 * a.Tp + t, v2 = v1 + a.Tp;
-      a.delta[v1] = fmaf(lam, d2, d0);
-      a.delta[v2] = d2;
+      a.ndelta[v1] = -fmaf(lam, d2, d0);
+      a.ndelta[v2] = -d2;
       a.nlse2[v1] = -kLog2e * __ldg(p.lse + (int64_t)h * 2 * T_ + t);
       a.nlse2[v2] = -kLog2e * __ldg(p.lse + ((int64_t)h * 2 + 1) * T_ + t);
       a.coef[(int64_t)h * a.Tp + t] = -lam;
@@ -83,20 +83,20 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
   const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   for (int64_t e = tid; e < (int64_t)pad * p.Hq; e += (int64_t)gridDim.x * kThreads) {
     const int64_t h = e / pad, t = T_ + (e - h * pad);
-    a.delta[h * 2 * a.Tp + t] = a.delta[(h * 2 + 1) * a.Tp + t] = 0.f;
+    a.ndelta[h * 2 * a.Tp + t] = a.ndelta[(h * 2 + 1) * a.Tp + t] = 0.f;
     a.nlse2[h * 2 * a.Tp + t] = a.nlse2[(h * 2 + 1) * a.Tp + t] = 0.f;
     a.coef[h * a.Tp + t] = 0.f;
   }
 }
 
-// dlambda[h] = -sum_t delta_2, one block of a head, in one fixed order.
+// dlambda[h] = sum_t -delta_2, one block of a head, in one fixed order.
 template <typename T>
-__global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restrict__ delta,
+__global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restrict__ ndelta,
                                                             int64_t tokens, int64_t Tp, T* dlambda,
                                                             const WsHeader* hdr) {
   __shared__ float s[32];
   if (status_bad(hdr)) return;
-  const float* row = delta + ((int64_t)blockIdx.x * 2 + 1) * Tp;
+  const float* row = ndelta + ((int64_t)blockIdx.x * 2 + 1) * Tp;
   float x = 0.f;
   for (int64_t t = threadIdx.x; t < tokens; t += 1024) x += __ldcg(row + t);
 #pragma unroll
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restr
   x = s[threadIdx.x];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if (threadIdx.x == 0) st_out(dlambda + blockIdx.x, -x);
+  if (threadIdx.x == 0) st_out(dlambda + blockIdx.x, x);
 }
 
 template <typename T>
@@ -124,7 +124,7 @@ cudaError_t prep(const DiffProblem& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t dlambda(const DiffProblem& a, cudaStream_t s) {
-  diff_dlambda_kernel<T><<<a.p.Hq, 1024, 0, s>>>(a.delta, a.p.q_len, a.Tp,
+  diff_dlambda_kernel<T><<<a.p.Hq, 1024, 0, s>>>(a.ndelta, a.p.q_len, a.Tp,
                                                  reinterpret_cast<T*>(a.dlambda), a.p.hdr);
   count_launches(1);
   return cudaGetLastError();

@@ -229,7 +229,7 @@ struct BwdSmem {
   float k[kBwdTile][D + 4], v[kBwdTile][D + 4];
   float ds[2][kBwdTile][kBwdTile + 4];            // [map][row of the output][summed index]
   float pc[kBwdTile][kBwdTile + 4];               // (P_1 - lambda P_2)^T: [key][query]
-  float nlse2[2][kBwdTile], delta[2][kBwdTile], coef[kBwdTile];
+  float nlse2[2][kBwdTile], ndelta[2][kBwdTile], coef[kBwdTile];
   int lo[kBwdTile], hi[kBwdTile];
 };
 
@@ -269,8 +269,8 @@ __device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2)
       const bool vis = key >= sm.lo[r] && key < sm.hi[r];
       const float p1 = vis ? exp2f(fmaf(s[0][i][j], sl2, sm.nlse2[0][r])) : 0.f;
       const float p2 = vis ? coef * exp2f(fmaf(s[1][i][j], sl2, sm.nlse2[1][r])) : 0.f;
-      const float d1 = vis ? p1 * (dp[i][j] - sm.delta[0][r]) : 0.f;
-      const float d2 = vis ? p2 * (dp[i][j] - sm.delta[1][r]) : 0.f;
+      const float d1 = vis ? p1 * (dp[i][j] + sm.ndelta[0][r]) : 0.f;
+      const float d2 = vis ? p2 * (dp[i][j] + sm.ndelta[1][r]) : 0.f;
       if constexpr (KEY) {
         sm.ds[0][kk][r] = d1;
         sm.ds[1][kk][r] = d2;
@@ -318,7 +318,7 @@ __device__ __forceinline__ void load_rows(BwdSmem<D>& sm, const DiffProblem& a, 
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       sm.nlse2[m][r] = a.nlse2[((int64_t)h * 2 + m) * a.Tp + t];
-      sm.delta[m][r] = a.delta[((int64_t)h * 2 + m) * a.Tp + t];
+      sm.ndelta[m][r] = a.ndelta[((int64_t)h * 2 + m) * a.Tp + t];
     }
     sm.coef[r] = a.coef[(int64_t)h * a.Tp + t];
   }

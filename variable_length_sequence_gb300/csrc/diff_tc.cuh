@@ -1,0 +1,139 @@
+// What the tensor-core kernels of differential attention share.
+#pragma once
+
+#include "layer.cuh"
+#include "tc_ptx.cuh"
+
+namespace nsp {
+namespace tc {
+
+constexpr uint32_t kBlk = 128 * 64 * 2;               // 128 rows x 64 bf16 column block
+constexpr uint32_t kTile = 2 * kBlk;                   // 128 x 128 bf16
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr size_t kSmemLimit = 232448;
+
+// One arrival of the warp, by lane 0, without a branch.  The caller's
+// __syncwarp orders the other lanes' accesses before it.
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar, int lane) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lane)
+      : "memory");
+}
+
+// mbar_wait_warp with a first look that neither suspends the warp nor reads
+// the wait's bound: most waits of a softmax warp find their phase complete.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, WaitCtl* wc, WsHeader* hdr) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok != 0)) return true;
+  return mbar_wait_warp(bar, parity, wc, hdr);
+}
+
+// D = A B^T over columns [m HK, (m + 1) HK) of K-major 128-row tiles (128-byte
+// swizzle: 16 columns are 32 bytes of a row, 64 columns one column block).
+template <int HK>
+__device__ __forceinline__ void mma_kk(int m, uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+  const uint64_t ad = smem_desc_sw128(a_saddr, 16, 1024);
+  const uint64_t bd = smem_desc_sw128(b_saddr, 16, 1024);
+#pragma unroll
+  for (int i = 0; i < HK / 16; ++i) {
+    const int kk = m * (HK / 16) + i;
+    const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
+    mma_ss(d_tmem, ad + off, bd + off, idesc, i > 0 ? 1u : 0u);
+  }
+}
+
+// Address of column n0 (a multiple of 32) of an MN-major tile's first rows.
+__device__ __forceinline__ uint32_t mn_offset(int n0) {
+  return (uint32_t)(n0 >> 6) * kBlk + (uint32_t)(n0 & 63) * 2;
+}
+
+// D (+)= A B, A (128 x 128) from TMEM in groups of QPG K-columns (group j at
+// columns a_tmem + j QPG + [0, QPG / 2), bf16 pairs), B MN-major columns
+// [n0, n0 + N) of a 128-row tile (16 rows are 2048 bytes).
+template <int QPG, int N>
+__device__ __forceinline__ void mma_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_saddr, int n0,
+                                          bool accumulate) {
+  constexpr int kSteps = QPG / 16;
+  const uint64_t bd = smem_desc_sw128(b_saddr + mn_offset(n0), kBlk, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(d_tmem, a_tmem + (kk / kSteps) * QPG + (kk % kSteps) * 8, bd + ((kk * 2048) >> 4),
+           idesc_bf16_f32(128, N, true, false), (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// The same with A K-major in shared memory.
+template <int N>
+__device__ __forceinline__ void mma_ss_mn(uint32_t d_tmem, uint32_t a_saddr, uint32_t b_saddr, int n0,
+                                          bool accumulate) {
+  const uint64_t ad = smem_desc_sw128(a_saddr, 16, 1024);
+  const uint64_t bd = smem_desc_sw128(b_saddr + mn_offset(n0), kBlk, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ss(d_tmem, ad + (((kk >> 2) * kBlk + (kk & 3) * 32) >> 4), bd + ((kk * 2048) >> 4),
+           idesc_bf16_f32(128, N, true, false), (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// Bits [lo, hi) of 32 columns (bounds relative to the first one, any value).
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
+  lo = min(max(lo, 0), 32);
+  hi = min(max(hi, 0), 32);
+  return hi <= lo ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+}
+
+// Masks of 16-bit pairs from column bits: pair j of the result covers bits
+// 8 j and 8 j + 1 of `bits`, 0xffff or 0 in each half.  A masked pair of
+// results is cleared whatever it holds (infinities and NaN included).
+__device__ __forceinline__ void pair_masks(uint32_t bits, uint32_t (&mask)[4]) {
+  const uint32_t even = bits << 7, odd = bits << 6;       // the bit at each byte's sign
+  asm("prmt.b32 %0, %1, %2, 0xcc88;" : "=r"(mask[0]) : "r"(even), "r"(odd));
+  asm("prmt.b32 %0, %1, %2, 0xdd99;" : "=r"(mask[1]) : "r"(even), "r"(odd));
+  asm("prmt.b32 %0, %1, %2, 0xeeaa;" : "=r"(mask[2]) : "r"(even), "r"(odd));
+  asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(mask[3]) : "r"(even), "r"(odd));
+}
+
+// dst[0..31] = scale * v (raw float32 bits) in bf16.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&v)[32], float scale) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * scale, __uint_as_float(v[2 * i + 1]) * scale);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    st_global_v8(dst + 16 * i, w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3], w[8 * i + 4],
+                 w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
+}
+
+// 1024-aligned view of dynamic shared memory, or nullptr (error recorded)
+// when the aligned structure would not fit in the launch's allocation.
+template <typename S>
+__device__ __forceinline__ S* smem_view(uint8_t* raw, WsHeader* hdr) {
+  uint32_t dyn_bytes;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
+  const uint32_t base = smem_u32(raw);
+  if (((base + 1023u) & ~1023u) - base + sizeof(S) > dyn_bytes) {
+    if (threadIdx.x == 0) atomicExch(&hdr->status, (int)NSP_ERR_UNSUPPORTED);
+    return nullptr;
+  }
+  return reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                              ~static_cast<uintptr_t>(1023));
+}
+
+template <typename S>
+constexpr size_t smem_bytes() {
+  return sizeof(S) + 1024 <= kSmemLimit ? sizeof(S) + 1024 : kSmemLimit;
+}
+
+}  // namespace tc
+}  // namespace nsp

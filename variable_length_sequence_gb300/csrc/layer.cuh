@@ -68,7 +68,7 @@ struct DiffProblem {
   void* out2;                        // second map's output (forward: may be null)
   const void *fout, *dout;           // backward
   void *dq, *dk, *dv, *dlambda;
-  float *delta, *nlse2, *coef;       // backward workspace: [2 Hq][Tp], [2 Hq][Tp], [Hq][Tp]
+  float *ndelta, *nlse2, *coef;      // backward workspace: [2 Hq][Tp], [2 Hq][Tp], [Hq][Tp]
   int64_t Tp;
 };
 cudaError_t launch_diff_fwd_tc(const DiffProblem& a, const FwdWsLayout& L, char* ws, cudaStream_t s);
@@ -78,9 +78,9 @@ bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols)
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s);
 cudaError_t launch_diff_bwd_tc(const DiffProblem& a, const BwdWsLayout& L, char* ws, cudaStream_t s);
 cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s);
-// delta, nlse2 and coef of the backward, and dlambda of each token
+// ndelta, nlse2 and coef of the backward, and dlambda of each token
 cudaError_t launch_diff_prep(const DiffProblem& a, cudaStream_t s);
-// dlambda of each head (n_lambda = 1), from delta
+// dlambda of each head (n_lambda = 1), from ndelta
 cudaError_t launch_diff_dlambda(const DiffProblem& a, cudaStream_t s);
 
 #ifdef __CUDACC__

@@ -324,7 +324,7 @@ int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const voi
   a.p.lse = const_cast<float*>(lse);
   a.fout = out; a.out2 = const_cast<void*>(out2); a.dout = dout;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dlambda = dlambda;
-  a.delta = reinterpret_cast<float*>(ws + L.delta);
+  a.ndelta = reinterpret_cast<float*>(ws + L.delta);
   a.nlse2 = reinterpret_cast<float*>(ws + L.nlse2);
   a.coef = reinterpret_cast<float*>(ws + L.total);
   a.Tp = L.Tp;
