@@ -271,29 +271,29 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       bool ok = true;
       while (ok) {
         const uint32_t slot = it_count & 1;
-        if (!mbar_wait(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+        if (!wait_one(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
         const KvItem it = sm.items[slot];
         mbar_arrive(&sm.item_empty[slot]);
         ++it_count;
         if (it.pairs < 0) break;
-        if (!mbar_wait(&sm.kv_full, items_done & 1, wc, hdr)) break;
+        if (!wait_one(&sm.kv_full, items_done & 1, wc, hdr)) break;
         for (int n = 0; n < it.pairs; ++n) {
           const uint32_t sq = qc & 3, sd = (qc + 2) & 3, fp = (qc >> 1) & 1, rb = qc & 1;
           const uint32_t ra = tmem + 128 * rb, rbb = tmem + 128 * (rb ^ 1);
-          if (!mbar_wait(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
           // A held the previous pair's dP: free once the softmax has read it twice
-          if (qc >= 1 && !mbar_wait(&sm.dp_free, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
+          if (qc >= 1 && !wait_one(&sm.dp_free, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           mma_kk<D / 2>(0, ra, k_s, smem_u32(sm.qd[sq]));                 // S_1^T = K_1 Q_1^T
           mma_commit(&sm.s1_full);
-          if (!mbar_wait(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
           // B held the previous pair's P and dS_2: free once dV and dK_2 have read them
-          if (qc >= 1 && !mbar_wait(&sm.p_done, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
+          if (qc >= 1 && !wait_one(&sm.p_done, (qc - 1) & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           mma_kk<D>(0, rbb, v_s, smem_u32(sm.qd[sd]));                    // dP^T = V dOut^T
           mma_commit(&sm.dp_full);
           mma_commit(&sm.slot_empty[sd]);
-          if (!mbar_wait(&sm.s1_free, qc & 1, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.s1_free, qc & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           mma_kk<D / 2>(1, ra, k_s, smem_u32(sm.qd[sq]));                 // S_2^T = K_2 Q_2^T
           mma_commit(&sm.s2_full);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       bool ok = true;
       while (ok) {
         const uint32_t slot = it_count & 1;
-        if (!mbar_wait(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+        if (!wait_one(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
         const KvItem it = sm.items[slot];
         mbar_arrive(&sm.item_empty[slot]);
         ++it_count;
@@ -320,18 +320,18 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         for (int n = 0; n < it.pairs; ++n) {
           const uint32_t sq = qc & 3, sd = (qc + 2) & 3, fp = (qc >> 1) & 1, rb = qc & 1;
           const uint32_t q_s = smem_u32(sm.qd[sq]);
-          if (!mbar_wait(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
-          if (!mbar_wait(&sm.ds_ready, qc & 1, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.slot_full[sq], fp, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.ds_ready, qc & 1, wc, hdr)) { ok = false; break; }
           // the accumulators hold the previous item until its epilogue has read them
           if (n == 0 && items_done > 0 &&
-              !mbar_wait(&sm.dkv_empty, (items_done - 1) & 1, wc, hdr)) {
+              !wait_one(&sm.dkv_empty, (items_done - 1) & 1, wc, hdr)) {
             ok = false;
             break;
           }
           tc_fence_after();
           mma_ss_mn<D / 2>(tmem + 384, ds_s, q_s, 0, n > 0);              // dK_1 += dS_1^T Q_1
-          if (!mbar_wait(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
-          if (!mbar_wait(&sm.p_ready, qc & 1, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.slot_full[sd], fp, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.p_ready, qc & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_tm = tmem + 128 * rb;
           mma_ts_mn<32, D>(tmem + 256, a_tm, smem_u32(sm.qd[sd]), 0, n > 0);       // dV += P^T dOut
@@ -689,21 +689,21 @@ __global__ void __launch_bounds__(kQThreads, 1)
       uint32_t it_count = 0, jc = 0;
       while (true) {
         const uint32_t slot = it_count & 1, use = it_count >> 1;
-        if (!mbar_wait(&sm.item_full[slot], use & 1, wc, hdr)) break;
+        if (!wait_one(&sm.item_full[slot], use & 1, wc, hdr)) break;
         const QItem it = sm.items[slot];
         mbar_arrive(&sm.item_empty[slot]);
         if (it.n_kv < 0) break;
-        if (!mbar_wait(&sm.q_full[slot], use & 1, wc, hdr)) break;
+        if (!wait_one(&sm.q_full[slot], use & 1, wc, hdr)) break;
         const uint32_t q_s = smem_u32(sm.q[slot]), do_s = smem_u32(sm.dout[slot]);
         bool ok = true;
         // S_1 and dP of tile t are issued before dQ_2 of tile t - 1, S_2 after it
         auto issue_s1_dp = [&](uint32_t t) {
-          if (!mbar_wait(&sm.k_full[t % K_NS], (t / K_NS) & 1, wc, hdr)) return false;
+          if (!wait_one(&sm.k_full[t % K_NS], (t / K_NS) & 1, wc, hdr)) return false;
           tc_fence_after();
           mma_kk<D / 2>(0, tmem, q_s, smem_u32(sm.k[t % K_NS]));            // S_1 = Q_1 K_1^T
           mma_commit(&sm.s_full[0]);
-          if (!mbar_wait(&sm.v_full, t & 1, wc, hdr)) return false;
-          if (t >= 1 && !mbar_wait(&sm.dp_free, (t - 1) & 1, wc, hdr)) return false;
+          if (!wait_one(&sm.v_full, t & 1, wc, hdr)) return false;
+          if (t >= 1 && !wait_one(&sm.dp_free, (t - 1) & 1, wc, hdr)) return false;
           tc_fence_after();
           mma_kk<D>(0, tmem + 256, do_s, smem_u32(sm.v));                   // dP = dOut V^T
           mma_commit(&sm.dp_full);
@@ -719,16 +719,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
         for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
           const uint32_t k_s = smem_u32(sm.k[jc % K_NS]);
           const bool has_next = jj + 1 < it.n_kv;
-          if (!mbar_wait(&sm.p_full[0], jc & 1, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.p_full[0], jc & 1, wc, hdr)) { ok = false; break; }
           // the first product overwrites dQ: read by the previous item's epilogue
-          if (jj == 0 && it_count >= 1 && !mbar_wait(&sm.o_free, (it_count - 1) & 1, wc, hdr)) {
+          if (jj == 0 && it_count >= 1 && !wait_one(&sm.o_free, (it_count - 1) & 1, wc, hdr)) {
             ok = false;
             break;
           }
           tc_fence_after();
           mma_ts_mn<64, D / 2>(tmem + 384, tmem, k_s, 0, jj > 0);           // dQ_1 += dS_1 K_1
           if (has_next && !issue_s1_dp(jc + 1)) { ok = false; break; }
-          if (!mbar_wait(&sm.p_full[1], jc & 1, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.p_full[1], jc & 1, wc, hdr)) { ok = false; break; }
           tc_fence_after();
           mma_ts_mn<64, D / 2>(tmem + 384 + D / 2, tmem + 128, k_s, D / 2, jj > 0);   // dQ_2 += dS_2 K_2
           mma_commit(&sm.k_empty[jc % K_NS]);

@@ -199,16 +199,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it_count = 0, kv_count = 0, p_count = 0;
       while (true) {
         const uint32_t slot = it_count & 1, use = it_count >> 1;
-        if (!mbar_wait(&sm.item_full[slot], use & 1, wc, hdr)) break;
+        if (!wait_one(&sm.item_full[slot], use & 1, wc, hdr)) break;
         const Item it = sm.items[slot];
         mbar_arrive(&sm.item_empty[slot]);
         if (it.n_kv < 0) break;
-        if (!mbar_wait(&sm.q_full[slot], use & 1, wc, hdr)) break;
+        if (!wait_one(&sm.q_full[slot], use & 1, wc, hdr)) break;
         const uint32_t qs = smem_u32(sm.q[slot]);
         bool ok = true;
         {
           const uint32_t st = kv_count % NSTAGE, n = kv_count / NSTAGE;
-          if (!mbar_wait(&sm.k_full[st], n & 1, wc, hdr)) break;
+          if (!wait_one(&sm.k_full[st], n & 1, wc, hdr)) break;
           tc_fence_after();
           const uint32_t ks = smem_u32(sm.k[st]);
 #pragma unroll
@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t st = (kv_count + jj) % NSTAGE, n = (kv_count + jj) / NSTAGE;
           const bool has_next = jj + 1 < it.n_kv;
           const uint32_t stn = (kv_count + jj + 1) % NSTAGE, nn = (kv_count + jj + 1) / NSTAGE;
-          if (!mbar_wait(&sm.v_full[st], n & 1, wc, hdr)) { ok = false; break; }
+          if (!wait_one(&sm.v_full[st], n & 1, wc, hdr)) { ok = false; break; }
           // the first product overwrites O: read by the previous item's epilogue
-          if (jj == 0 && it_count >= 1 && !mbar_wait(&sm.o_free, (it_count - 1) & 1, wc, hdr)) {
+          if (jj == 0 && it_count >= 1 && !wait_one(&sm.o_free, (it_count - 1) & 1, wc, hdr)) {
             ok = false;
             break;
           }
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (!ok) continue;
-            if (!mbar_wait(&sm.p_full[m], p_count & 1, wc, hdr)) { ok = false; continue; }
+            if (!wait_one(&sm.p_full[m], p_count & 1, wc, hdr)) { ok = false; continue; }
             tc_fence_after();
             mma_ts_mn<128, D>(tmem + col_o(m), tmem + col_s(m), vs, 0, jj > 0);   // O_m += P_m V
             if (m == 1) mma_commit(&sm.v_empty[st]);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             if (m == 0) {
-              if (!mbar_wait(&sm.k_full[stn], nn & 1, wc, hdr)) { ok = false; continue; }
+              if (!wait_one(&sm.k_full[stn], nn & 1, wc, hdr)) { ok = false; continue; }
               tc_fence_after();
             }
             mma_kk<D / 2>(m, tmem + col_s(m), qs, smem_u32(sm.k[stn]));
