@@ -667,7 +667,8 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
  *   dlambda = -delta^2 of each token, or its sum over the tokens.
  * Every output is written whole, and sums run in one fixed order: results are
  * the same bits on every run. */
-size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t d);
+size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                                        int32_t io_dtype);
 
 int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const void* lambda,
                           int64_t n_lambda, const void* out, const void* out2, const void* dout,

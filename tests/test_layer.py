@@ -233,7 +233,7 @@ def test_norm_backward_refusals(lib):
 
 
 def _diff(lib, back, **kw):
-    n = (lib.nsp_diff_attn_bwd_workspace_size(300, 4, 128) if back
+    n = (lib.nsp_diff_attn_bwd_workspace_size(300, 4, 2, 128, nsp.NSP_F32) if back
          else lib.nsp_diff_attn_fwd_workspace_size(300))
     a = dict(q=A, k=A + (1 << 20), v=A + (2 << 20), lam=A + (3 << 20), n_lambda=1, cu=A + (4 << 20),
              ndoc=3, T=300, Hq=4, Hkv=2, d=128, scale=0.125, causal=1, io=nsp.NSP_BF16,
@@ -273,8 +273,8 @@ def test_diff_output_alignment(lib):
         assert _diff(lib, True, **{name: None}) == INVALID
     assert _diff(lib, False, out=None) == INVALID
     assert lib.nsp_diff_attn_fwd_workspace_size(-1) == 0
-    assert lib.nsp_diff_attn_bwd_workspace_size(10, 0, 128) == 0
-    assert lib.nsp_diff_attn_bwd_workspace_size((1 << 30) + 1, 4, 128) == 0
+    assert lib.nsp_diff_attn_bwd_workspace_size(10, 0, 1, 128, 1) == 0
+    assert lib.nsp_diff_attn_bwd_workspace_size((1 << 30) + 1, 4, 4, 128, 1) == 0
 
 
 def test_binding_refuses_host_tensors():

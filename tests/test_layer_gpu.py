@@ -396,7 +396,7 @@ def test_diff_attention_status(nsp):
         ws = torch.empty(nsp.load().nsp_diff_attn_fwd_workspace_size(100), dtype=torch.uint8, device="cuda")
         nsp.diff_attn_fwd(q, k, v, lam, cu, workspace=ws)
         assert nsp.nsp_status_query(ws) == nsp.NSP_ERR_INVALID
-        ws = torch.empty(nsp.load().nsp_diff_attn_bwd_workspace_size(100, 2, 64), dtype=torch.uint8,
+        ws = torch.empty(nsp.load().nsp_diff_attn_bwd_workspace_size(100, 2, 1, 64, nsp.NSP_BF16), dtype=torch.uint8,
                          device="cuda")
         nsp.diff_attn_bwd(q, k, v, lam, q, out2, do, lse, cu, workspace=ws)
         assert nsp.nsp_status_query(ws) == nsp.NSP_ERR_INVALID
@@ -433,7 +433,7 @@ def test_diff_attention_guard_zones(nsp, dt):
     es = q.element_size()
     sizes = [T * hq * d * es, T * hq * d * es, hq * 2 * T * 4, lib.nsp_diff_attn_fwd_workspace_size(T),
              T * hq * d * es, T * hkv * d * es, T * hkv * d * es, hq * es,
-             lib.nsp_diff_attn_bwd_workspace_size(T, hq, d)]
+             lib.nsp_diff_attn_bwd_workspace_size(T, hq, hkv, d, nsp._DTYPES[dt])]
     bufs = [guarded(n) for n in sizes]
     p = [b[1].data_ptr() for b in bufs]
     io, st = nsp._DTYPES[dt], torch.cuda.current_stream().cuda_stream

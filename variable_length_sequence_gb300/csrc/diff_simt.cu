@@ -10,14 +10,16 @@
 //   dS_1 = P_1 (dP - delta_1),  dS_2 = -lambda P_2 (dP - delta_2),
 //   dQ_m = scale dS_m K_m,  dK_m = scale dS_m^T Q_m,  dV = (P_1 - lambda P_2)^T dout.
 //
-// Bound: the FP32 pipes and shared-memory reads.  Every product is tiled in
-// registers over 256 threads (16 x 16) from float32 tiles in shared memory,
-// rows padded by 4 floats so that 16 rows read at one column fall into
-// different banks.  Forward: 64 query rows by 32 keys; both maps' scores,
+// Bound: shared-memory reads beside the FP32 pipes.  Every product is tiled in
+// registers over 256 threads (16 x 16; 4 x 4 results of a thread and 8 FMAs for
+// each 16-byte read: 2 x 2 with 4 took twice as long) from float32 tiles in
+// shared memory, rows padded by 4 floats so that 16 rows read at one column fall
+// into different banks.  Forward: 64 query rows by 64 keys; both maps' scores,
 // online softmax (Milakov and Gimelshein) and outputs stay in the registers of
-// one thread row.  Backward: one kernel over key tiles (dK, dV), one over
-// query tiles (dQ), each recomputing both maps' P and dP, so every gradient
-// is summed in one fixed order without atomics.
+// one thread row.  Backward: one kernel over key tiles and query heads (dK, dV of
+// the head; a small kernel sums a group's heads), one over query tiles (dQ),
+// each recomputing both maps' P and dP, so every gradient is summed in one
+// fixed order without atomics.
 #include "layer.cuh"
 
 namespace nsp {
@@ -71,7 +73,7 @@ __device__ __forceinline__ float lambda_of(const DiffProblem& a, int h, int64_t 
 
 // ---------------------------------------------------------------- forward
 
-constexpr int kFwdM = 64, kFwdN = 32;
+constexpr int kFwdM = 64, kFwdN = 64, kFwdKeys = kFwdN / 16;    // keys of a thread: tx + 16 j
 
 template <int D>
 struct FwdSmem {
@@ -135,38 +137,45 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      // scores of rows 4 ty .. + 3 against keys tx and tx + 16
-      float s[4][2] = {};
-#pragma unroll 4
+      // scores of rows 4 ty .. + 3 against keys tx + 16 j
+      float s[4][kFwdKeys] = {};
+#pragma unroll 2
       for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 4) {
-        const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
-        const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
+        float4 kk[kFwdKeys];
+#pragma unroll
+        for (int j = 0; j < kFwdKeys; ++j)
+          kk[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][c]);
-          s[i][0] = dot4(x, k0, s[i][0]);
-          s[i][1] = dot4(x, k1, s[i][1]);
+#pragma unroll
+          for (int j = 0; j < kFwdKeys; ++j) s[i][j] = dot4(x, kk[j], s[i][j]);
         }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int key = j0 + tx;
-        float s0 = key >= lo[i] && key < hi[i] ? s[i][0] * sl2 : -INFINITY;
-        float s1 = key + 16 >= lo[i] && key + 16 < hi[i] ? s[i][1] * sl2 : -INFINITY;
-        float mx = fmaxf(s0, s1);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kFwdKeys; ++j) {
+          const int key = j0 + tx + 16 * j;
+          s[i][j] = key >= lo[i] && key < hi[i] ? s[i][j] * sl2 : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
 #pragma unroll
         for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
         const float mn = fmaxf(m[t][i], mx);
         const float mb = mn == -INFINITY ? 0.f : mn;
         const float corr = exp2f(m[t][i] - mb);
-        s0 = exp2f(s0 - mb);
-        s1 = exp2f(s1 - mb);
         m[t][i] = mn;
-        l[t][i] = l[t][i] * corr + (s0 + s1);      // this thread's two key columns only
+        l[t][i] *= corr;                           // this thread's key columns only
+#pragma unroll
+        for (int j = 0; j < kFwdKeys; ++j) {
+          const float e = exp2f(s[i][j] - mb);
+          l[t][i] += e;
+          sm.p[t][ty * 4 + i][tx + 16 * j] = e;
+        }
 #pragma unroll
         for (int c = 0; c < kCols; ++c) o[t][i][c] = scaled(corr, o[t][i][c]);
-        sm.p[t][ty * 4 + i][tx] = s0;
-        sm.p[t][ty * 4 + i][tx + 16] = s1;
       }
     }
     __syncwarp();                                   // a row's P is written and read by one half warp
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
 
 // ---------------------------------------------------------------- backward
 
-constexpr int kBwdTile = 32;          // query rows and keys of a tile
+constexpr int kBwdTile = 64;          // query rows and keys of a tile: 4 x 4 a thread
 
 template <int D>
 struct BwdSmem {
@@ -233,61 +242,65 @@ struct BwdSmem {
   int lo[kBwdTile], hi[kBwdTile];
 };
 
-// P and dS of a 32 x 32 tile, written for the product that follows: KEY puts
-// dS and P_1 - lambda P_2 in rows of keys (dK, dV), otherwise dS in rows of
-// queries (dQ).  Threads take rows 2 ty, 2 ty + 1 and keys tx, tx + 16.
+// P and dS of a tile, written for the product that follows: KEY puts dS and
+// P_1 - lambda P_2 in rows of keys (dK, dV), otherwise dS in rows of queries
+// (dQ).  Threads take rows 4 ty + i and keys tx + 16 j.
 template <int D, bool KEY>
 __device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  float s[2][2][2] = {}, dp[2][2] = {};
+  float s[2][4][4] = {}, dp[4][4] = {};
 #pragma unroll
   for (int t = 0; t < 2; ++t)
-#pragma unroll 4
+#pragma unroll 2
     for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 4) {
-      const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[tx][c]);
-      const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[tx + 16][c]);
-      const float4 v0 = *reinterpret_cast<const float4*>(&sm.v[tx][c]);
-      const float4 v1 = *reinterpret_cast<const float4*>(&sm.v[tx + 16][c]);
+      float4 kk[4], vv[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * 2 + i][c]);
-        const float4 y = *reinterpret_cast<const float4*>(&sm.dout[ty * 2 + i][c]);
-        s[t][i][0] = dot4(x, k0, s[t][i][0]);
-        s[t][i][1] = dot4(x, k1, s[t][i][1]);
-        dp[i][0] = dot4(y, v0, dp[i][0]);
-        dp[i][1] = dot4(y, v1, dp[i][1]);
+      for (int j = 0; j < 4; ++j) {
+        kk[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
+        vv[j] = *reinterpret_cast<const float4*>(&sm.v[tx + 16 * j][c]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][c]);
+        const float4 y = *reinterpret_cast<const float4*>(&sm.dout[ty * 4 + i][c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[t][i][j] = dot4(x, kk[j], s[t][i][j]);
+          dp[i][j] = dot4(y, vv[j], dp[i][j]);
+        }
       }
     }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = ty * 2 + i;
-    const float coef = sm.coef[r];
+  for (int j = 0; j < 4; ++j) {
+    const int kk = tx + 16 * j;
+    const int64_t key = key0 + kk;
+    float d1[4], d2[4], pc[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int kk = tx + 16 * j;
-      const int64_t key = key0 + kk;
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
       const bool vis = key >= sm.lo[r] && key < sm.hi[r];
       const float p1 = vis ? exp2f(fmaf(s[0][i][j], sl2, sm.nlse2[0][r])) : 0.f;
-      const float p2 = vis ? coef * exp2f(fmaf(s[1][i][j], sl2, sm.nlse2[1][r])) : 0.f;
-      const float d1 = vis ? p1 * (dp[i][j] + sm.ndelta[0][r]) : 0.f;
-      const float d2 = vis ? p2 * (dp[i][j] + sm.ndelta[1][r]) : 0.f;
-      if constexpr (KEY) {
-        sm.ds[0][kk][r] = d1;
-        sm.ds[1][kk][r] = d2;
-        sm.pc[kk][r] = p1 + p2;
-      } else {
-        sm.ds[0][r][kk] = d1;
-        sm.ds[1][r][kk] = d2;
+      const float p2 = vis ? sm.coef[r] * exp2f(fmaf(s[1][i][j], sl2, sm.nlse2[1][r])) : 0.f;
+      d1[i] = vis ? p1 * (dp[i][j] + sm.ndelta[0][r]) : 0.f;
+      d2[i] = vis ? p2 * (dp[i][j] + sm.ndelta[1][r]) : 0.f;
+      pc[i] = p1 + p2;
+      if constexpr (!KEY) {
+        sm.ds[0][r][kk] = d1[i];
+        sm.ds[1][r][kk] = d2[i];
       }
+    }
+    if constexpr (KEY) {
+      st4(&sm.ds[0][kk][ty * 4], make_float4(d1[0], d1[1], d1[2], d1[3]));
+      st4(&sm.ds[1][kk][ty * 4], make_float4(d2[0], d2[1], d2[2], d2[3]));
+      st4(&sm.pc[kk][ty * 4], make_float4(pc[0], pc[1], pc[2], pc[3]));
     }
   }
 }
 
-// acc[i][c] += sum_j w[2 ty + i][j] x[j][col + 64 c]: a 32 x D product of a
-// 32 x 32 tile in shared memory; map_of picks the tile of the column's map.
+// acc[i][c] += sum_j w[4 ty + i][j] x[j][col + 64 c]: a kBwdTile x D product of
+// a square tile in shared memory; w_of picks the tile of the column's map.
 template <int D, typename W>
-__device__ __forceinline__ void tile_product(float4 (&acc)[2][(D + 63) / 64], W&& w_of,
-                                             float (*x)[D + 4]) {
+__device__ __forceinline__ void tile_product(float4 (&acc)[4][D / 64], W&& w_of, float (*x)[D + 4]) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll 2
   for (int j = 0; j < kBwdTile; j += 4) {
@@ -298,8 +311,8 @@ __device__ __forceinline__ void tile_product(float4 (&acc)[2][(D + 63) / 64], W&
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) b[jj] = *reinterpret_cast<const float4*>(&x[j + jj][col]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 w = *reinterpret_cast<const float4*>(w_of(col) + (ty * 2 + i) * (kBwdTile + 4) + j);
+      for (int i = 0; i < 4; ++i) {
+        const float4 w = *reinterpret_cast<const float4*>(w_of(col) + (ty * 4 + i) * (kBwdTile + 4) + j);
         acc[i][c] = fma4(w.w, b[3], fma4(w.z, b[2], fma4(w.y, b[1], fma4(w.x, b[0], acc[i][c]))));
       }
     }
@@ -326,6 +339,9 @@ __device__ __forceinline__ void load_rows(BwdSmem<D>& sm, const DiffProblem& a, 
   sm.hi[r] = hi;
 }
 
+// One query head's share of dK and dV for a key tile: summed over the group's
+// heads by diff_group_sum_kernel (one block a head, so that few key tiles still
+// fill the GPU), or written at once when the group is one head.
 template <int D>
 __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -333,7 +349,7 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const Diff
   const AttnProblem& p = a.p;
   if (status_bad(p.hdr)) return;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int g = blockIdx.y, G = p.Hq / p.Hkv;
+  const int h = blockIdx.y, G = p.Hq / p.Hkv, g = h / G;
   const int64_t T = p.q_len, key0 = (int64_t)blockIdx.x * kBwdTile;
   const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
   load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, key0, T);
@@ -342,31 +358,47 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const Diff
   const int b0 = doc_of(p.cu, p.ndoc, key0), b1 = doc_of(p.cu, p.ndoc, key1);
   const int64_t r_lo = p.causal ? key0 : (int64_t)__ldg(p.cu + b0);
   const int64_t r_hi = min((int64_t)__ldg(p.cu + b1 + 1), T);
-  float4 dk[2][D / 64] = {}, dv[2][D / 64] = {};
-  for (int hh = 0; hh < G; ++hh) {
-    const int h = g * G + hh;
-    for (int64_t r0 = r_lo; r0 < r_hi; r0 += kBwdTile) {
-      __syncthreads();
-      load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const float*>(p.q) + (int64_t)h * D, qs, r0, T);
-      load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, r0, T);
-      load_rows<D>(sm, a, h, r0);
-      __syncthreads();
-      tile_ds<D, true>(sm, key0, p.scale * kLog2e);
-      __syncthreads();
-      tile_product<D>(dk, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.q);
-      tile_product<D>(dv, [&](int) { return &sm.pc[0][0]; }, sm.dout);
-    }
+  float4 dk[4][D / 64] = {}, dv[4][D / 64] = {};
+  for (int64_t r0 = r_lo; r0 < r_hi; r0 += kBwdTile) {
+    __syncthreads();
+    load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const float*>(p.q) + (int64_t)h * D, qs, r0, T);
+    load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, r0, T);
+    load_rows<D>(sm, a, h, r0);
+    __syncthreads();
+    tile_ds<D, true>(sm, key0, p.scale * kLog2e);
+    __syncthreads();
+    tile_product<D>(dk, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.q);
+    tile_product<D>(dv, [&](int) { return &sm.pc[0][0]; }, sm.dout);
   }
+  float* const DK = G > 1 ? a.dk_heads : reinterpret_cast<float*>(a.dk);
+  float* const DV = G > 1 ? a.dv_heads : reinterpret_cast<float*>(a.dv);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t key = key0 + ty * 2 + i;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t key = key0 + ty * 4 + i;
     if (key >= T) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const int64_t off = key * ks + (int64_t)g * D + c * 64 + tx * 4;
-      st4(reinterpret_cast<float*>(a.dk) + off, scaled(p.scale, dk[i][c]));
-      st4(reinterpret_cast<float*>(a.dv) + off, dv[i][c]);
+      const int64_t off = key * qs + (int64_t)h * D + c * 64 + tx * 4;
+      st4(DK + off, scaled(p.scale, dk[i][c]));
+      st4(DV + off, dv[i][c]);
     }
+  }
+}
+
+// dk, dv [T, Hkv, d] = sums over each group's G heads of [T, Hq, d], in order.
+__global__ void __launch_bounds__(kThreads) diff_group_sum_kernel(const DiffProblem a) {
+  const AttnProblem& p = a.p;
+  if (status_bad(p.hdr)) return;
+  const int G = p.Hq / p.Hkv, d4 = p.d / 4;
+  const int64_t n = p.q_len * p.Hkv * d4;
+  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < 2 * n;
+       e += (int64_t)gridDim.x * kThreads) {
+    const bool is_v = e >= n;
+    const int64_t i = is_v ? e - n : e, tg = i / d4;
+    const float* src = (is_v ? a.dv_heads : a.dk_heads) + (tg * G * d4 + (i - tg * d4)) * 4;
+    float4 x = ld4(src);
+    for (int h = 1; h < G; ++h) x = fma4(1.f, ld4(src + (int64_t)h * p.d), x);
+    st4(reinterpret_cast<float*>(is_v ? a.dv : a.dk) + i * 4, x);
   }
 }
 
@@ -386,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffPr
   __syncthreads();
   const int last = (int)min((int64_t)kBwdTile, T - row0) - 1;
   const int key_lo = sm.lo[0] / kBwdTile * kBwdTile, key_hi = sm.hi[last];
-  float4 dq[2][D / 64] = {};
+  float4 dq[4][D / 64] = {};
   for (int j0 = key_lo; j0 < key_hi; j0 += kBwdTile) {
     __syncthreads();
     load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, j0, T);
@@ -397,8 +429,8 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffPr
     tile_product<D>(dq, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.k);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = row0 + ty * 2 + i;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + ty * 4 + i;
     if (row >= T) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
@@ -425,11 +457,18 @@ cudaError_t fwd(const DiffProblem& a, cudaStream_t s) {
 
 template <int D>
 cudaError_t bwd(const DiffProblem& a, cudaStream_t s) {
-  const unsigned tiles = (unsigned)ceil_div(a.p.q_len, kBwdTile);
-  cudaError_t e =
-      launch(diff_bwd_dkdv_simt_kernel<D>, dim3(tiles, a.p.Hkv), sizeof(BwdSmem<D>), a, s);
+  const dim3 grid((unsigned)ceil_div(a.p.q_len, kBwdTile), a.p.Hq);
+  cudaError_t e = launch(diff_bwd_dkdv_simt_kernel<D>, grid, sizeof(BwdSmem<D>), a, s);
   if (e != cudaSuccess) return e;
-  return launch(diff_bwd_dq_simt_kernel<D>, dim3(tiles, a.p.Hq), sizeof(BwdSmem<D>), a, s);
+  if (a.p.Hq > a.p.Hkv) {
+    const int64_t n = 2 * a.p.q_len * a.p.Hkv * (D / 4);
+    const int64_t blocks = ceil_div(n, kThreads), most = (int64_t)num_sms() * 8;
+    diff_group_sum_kernel<<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, s>>>(a);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return launch(diff_bwd_dq_simt_kernel<D>, grid, sizeof(BwdSmem<D>), a, s);
 }
 
 }  // namespace

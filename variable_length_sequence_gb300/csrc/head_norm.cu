@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+// exp and the quotient to 2 ulp each (IEEE division costs as much as the rest)
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 __device__ __forceinline__ float group_sum(float x, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const NormArgs a, i
 }
 
 template <typename T, int V, int ROWS>
-__global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(const NormArgs a, int lanes) {
+__global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 1) head_norm_bwd_kernel(const NormArgs a, int lanes) {
   constexpr int N = Vec<T>::N;
   extern __shared__ float s_dw[];                 // [groups][d]
   grid_dep_trigger();
@@ -153,40 +154,36 @@ __global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(const NormArgs 
       const int64_t row = r0 + k * groups + group;
       // sums of x^2 and of x u (n and u scale out of the second one)
       float ss = 0.f, su = 0.f;
+      float t[V][N], u[V][N], sg[V][N];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float t[N], u[N], q[N];
-        Vec<T>::unpack(x[k][v], t);
-        Vec<T>::unpack(y[k][v], u);
-        if (G != nullptr) Vec<T>::unpack(g[k][v], q);
+        Vec<T>::unpack(x[k][v], t[v]);
+        Vec<T>::unpack(y[k][v], u[v]);
+        if (G != nullptr) Vec<T>::unpack(g[k][v], sg[v]);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          float c = u[i] * w[v][i];
-          if (G != nullptr) c *= sigmoid(q[i]);
-          ss = fmaf(t[i], t[i], ss);
-          su = fmaf(t[i], c, su);
+          sg[v][i] = G != nullptr ? sigmoid(sg[v][i]) : 1.f;
+          ss = fmaf(t[v][i], t[v][i], ss);
+          su = fmaf(t[v][i], u[v][i] * w[v][i] * sg[v][i], su);
         }
       }
       const float r = rsqrtf(fmaf(group_sum(ss, lanes), inv_d, a.eps));
       const float mean = group_sum(su, lanes) * r * inv_d;      // mean(u n) / s
+      const float sr = a.scale * r;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = lane + v * lanes;
         if (row >= rows || c >= nvec) continue;
-        float t[N], u[N], q[N];
-        Vec<T>::unpack(x[k][v], t);
-        Vec<T>::unpack(y[k][v], u);
-        if (G != nullptr) Vec<T>::unpack(g[k][v], q);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float n = t[i] * r, sg = G != nullptr ? sigmoid(q[i]) : 1.f;
-          const float dyn = a.scale * u[i] * n;                 // s dy n
-          dw[v][i] = fmaf(dyn, sg, dw[v][i]);
-          q[i] = dyn * w[v][i] * sg * (1.f - sg);
-          t[i] = a.scale * r * (u[i] * w[v][i] * sg - n * mean);
+          const float n = t[v][i] * r, us = u[v][i] * sg[v][i];
+          const float dyn = a.scale * n * us;                   // s dy n sigmoid
+          dw[v][i] += dyn;
+          t[v][i] = sr * fmaf(us, w[v][i], -n * mean);
+          u[v][i] = dyn * w[v][i] * (1.f - sg[v][i]);
         }
-        st_once(DX + row * a.d + c * N, Vec<T>::pack(t));
-        if (G != nullptr) st_once(DG + row * a.d + c * N, Vec<T>::pack(q));
+        st_once(DX + row * a.d + c * N, Vec<T>::pack(t[v]));
+        if (G != nullptr) st_once(DG + row * a.d + c * N, Vec<T>::pack(u[v]));
       }
     }
   }
@@ -206,24 +203,27 @@ __global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(const NormArgs 
   }
 }
 
-// dw[c] = sum of the blocks' partial sums; 32 columns of a block, 8 warps
-// taking every eighth partial row.
+// dw[c] = sum of the blocks' partial sums; 32 columns of a block, 32 warps
+// taking every 32nd partial row.
+constexpr int kSumThreads = 1024;
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_weight_grad_kernel(const float* __restrict__ partial,
-                                                                    int n, int d, T* dw) {
-  __shared__ float s[kThreads / 32][32];
+__global__ void __launch_bounds__(kSumThreads) norm_weight_grad_kernel(
+    const float* __restrict__ partial, int n, int d, T* dw) {
+  __shared__ float s[32][33];
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float x = 0.f;
-  if (c < d)
-    for (int k = warp; k < n; k += kThreads / 32) x += __ldcg(partial + (int64_t)k * d + c);
+  if (c < d) {
+#pragma unroll 4
+    for (int k = warp; k < n; k += 32) x += __ldcg(partial + (int64_t)k * d + c);
+  }
   s[warp][lane] = x;
   __syncthreads();
-  if (warp == 0 && c < d) {
+  // column `warp` of the block: its 32 sums are one warp's lanes now
+  x = s[lane][warp];
 #pragma unroll
-    for (int k = 1; k < kThreads / 32; ++k) x += s[k][lane];
-    st_out(dw + c, x);
-  }
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < d) st_out(dw + blockIdx.x * 32 + warp, x);
 }
 
 // Lanes of a row (a power of two) and vectors of a lane.
@@ -270,7 +270,7 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
   count_launches(1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.partial) return e;
-  e = launch_dependent(norm_weight_grad_kernel<T>, dim3((a.d + 31) / 32), dim3(kThreads), 0, s,
+  e = launch_dependent(norm_weight_grad_kernel<T>, dim3((a.d + 31) / 32), dim3(kSumThreads), 0, s,
                        (const float*)a.partial, (int)blocks, (int)a.d,
                        reinterpret_cast<T*>(a.dweight));
   count_launches(1);

@@ -70,6 +70,7 @@ struct DiffProblem {
   void *dq, *dk, *dv, *dlambda;
   float *ndelta, *nlse2, *coef;      // backward workspace: [2 Hq][Tp], [2 Hq][Tp], [Hq][Tp]
   int64_t Tp;
+  float *dk_heads, *dv_heads;        // float32 backward, Hq > Hkv: [T, Hq, d] shares of the heads
 };
 cudaError_t launch_diff_fwd_tc(const DiffProblem& a, const FwdWsLayout& L, char* ws, cudaStream_t s);
 // A map of [rows, cols] bf16 whose copies are 128 rows of 64 columns, 128-byte

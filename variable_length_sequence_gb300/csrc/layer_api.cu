@@ -288,15 +288,30 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
   return e == cudaSuccess ? NSP_OK : NSP_ERR_CUDA;
 }
 
-// Backward workspace: the attention backward's layout for 2 Hq rows of delta
-// and -lse log2 e, then -lambda [Hq, Tp].
-static size_t diff_bwd_total(const BwdWsLayout& L, int32_t Hq) {
-  return align_up(L.total + sizeof(float) * (size_t)Hq * (size_t)L.Tp, 256);
+// Backward workspace: the attention backward's layout for 2 Hq rows of -delta
+// and -lse log2 e, then -lambda [Hq, Tp], and for float32 with grouped heads each
+// query head's share of dk and dv.
+struct DiffBwdLayout {
+  BwdWsLayout attn;
+  size_t coef, heads, total;
+};
+static DiffBwdLayout diff_bwd_layout(int64_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                                     int32_t io_dtype) {
+  DiffBwdLayout L;
+  L.attn = bwd_ws_layout(T, T, 2 * Hq, d, false);
+  L.coef = L.attn.total;
+  L.heads = align_up(L.coef + sizeof(float) * (size_t)Hq * (size_t)L.attn.Tp, 256);
+  const bool shares = io_dtype == NSP_F32 && Hq > Hkv;
+  L.total = L.heads + (shares ? 2 * sizeof(float) * (size_t)T * (size_t)Hq * (size_t)d : 0);
+  return L;
 }
 
-size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t d) {
-  if (T < 0 || T > kMaxTokens || Hq < 1 || Hq > kMaxHeads || d < 1) return 0;
-  return diff_bwd_total(bwd_ws_layout(T, T, 2 * Hq, d, false), Hq);
+size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                                        int32_t io_dtype) {
+  if (T < 0 || T > kMaxTokens || Hq < 1 || Hq > kMaxHeads || Hkv < 1 || d < 1 || d > 128 ||
+      !dtype_ok(io_dtype))
+    return 0;
+  return diff_bwd_layout(T, Hq, Hkv, d, io_dtype).total;
 }
 
 int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const void* lambda,
@@ -314,8 +329,9 @@ int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const voi
   }
   if (io_dtype == NSP_BF16 && (!aligned(dq, 32) || !aligned(dk, 32) || !aligned(dv, 32)))
     return NSP_ERR_ALIGN;
-  const BwdWsLayout L = bwd_ws_layout(T, T, 2 * Hq, d, false);
-  if (!workspace || workspace_bytes < diff_bwd_total(L, Hq)) return NSP_ERR_WORKSPACE;
+  const DiffBwdLayout W = diff_bwd_layout(T, Hq, Hkv, d, io_dtype);
+  const BwdWsLayout& L = W.attn;
+  if (!workspace || workspace_bytes < W.total) return NSP_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return NSP_ERR_ALIGN;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* ws = reinterpret_cast<char*>(workspace);
@@ -326,7 +342,9 @@ int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const voi
   a.dq = dq; a.dk = dk; a.dv = dv; a.dlambda = dlambda;
   a.ndelta = reinterpret_cast<float*>(ws + L.delta);
   a.nlse2 = reinterpret_cast<float*>(ws + L.nlse2);
-  a.coef = reinterpret_cast<float*>(ws + L.total);
+  a.coef = reinterpret_cast<float*>(ws + W.coef);
+  a.dk_heads = reinterpret_cast<float*>(ws + W.heads);
+  a.dv_heads = a.dk_heads + (size_t)T * (size_t)Hq * (size_t)d;
   a.Tp = L.Tp;
   if (launch_bwd_schedules(a.p, L, ws, s) != cudaSuccess) return NSP_ERR_CUDA;
   if (T == 0) {

@@ -209,7 +209,9 @@ cudaError_t launch_typed(const RopeArgs& a, cudaStream_t s) {
     // when there are too few tokens
     int64_t hsplit = ceil_div(nsm * 8 * teams, a.len);
     hsplit = std::min<int64_t>(hsplit, heads);
-    const int64_t blocks = std::min<int64_t>(ceil_div(a.len * hsplit, teams), nsm * 8);
+    // (one item a team where 64 blocks of an SM allow it: no block is left with one
+    // more item than the others at the end)
+    const int64_t blocks = std::min<int64_t>(ceil_div(a.len * hsplit, teams), nsm * 64);
     if (a.interleaved)
       rope_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a, pieces, rotated, heads,
                                                                  (int)hsplit);

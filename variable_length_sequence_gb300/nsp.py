@@ -79,7 +79,7 @@ _SIGNATURES = {
     "nsp_diff_attn_fwd_workspace_size": (_sz, [_i64]),
     "nsp_diff_attn_fwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i32, _i32, _i32, _f32,
                                  _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
-    "nsp_diff_attn_bwd_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "nsp_diff_attn_bwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32]),
     "nsp_diff_attn_bwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32,
                                  _i32, _i32, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "nsp_head_norm_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _i32, _vp,
@@ -636,64 +636,73 @@ def head2seq(y, stream=None):
 
 
 # ----------------------------------------------------------------------------- differential attention layer
+#
+# These calls are short enough on the GPU for the host's share to matter, so
+# each tensor is looked at once and the common case takes no detours.
 
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
 _DTYPES = {torch.bfloat16: NSP_BF16, torch.float32: NSP_F32}
+_Rope1, _Rope2 = RopeTensor * 1, RopeTensor * 2
 
 
-def _check_tensors(fn: str, dtype, **tensors) -> None:
-    """Every given tensor is on the current CUDA device and of `dtype` (or its
-    name's own): the library takes bare pointers."""
-    dev = None
+def _io(fn: str, dtype) -> int:
+    io = _DTYPES.get(dtype)
+    if io is None:
+        raise TypeError(f"{fn}: unsupported dtype {dtype}")
+    return io
+
+
+def _on_device(fn: str, dtype, **tensors) -> int:
+    """Every given tensor is of `dtype` and on the current CUDA device (the
+    library takes bare pointers).  Returns that device's index."""
+    dev = -2
     for name, t in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: {name} is not on a CUDA device")
-        if dev is None:
+        at = t.get_device()
+        if at != dev:
+            if at < 0:
+                raise ValueError(f"{fn}: {name} is not on a CUDA device")
             dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} is on device {t.get_device()}, the current one is {dev}")
-        want = _INDEX_DTYPES.get(name, dtype)
-        if t.dtype != want:
-            raise TypeError(f"{fn}: {name} is {t.dtype}, expected {want}")
+            if at != dev:
+                raise ValueError(f"{fn}: {name} is on device {at}, the current one is {dev}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
+    return dev
 
 
-_INDEX_DTYPES = {"cu_seqlens": torch.int32, "positions": torch.int32, "freqs": torch.float64,
-                 "lse": torch.float32, "workspace": torch.uint8}
-
-
-def _check_io(fn: str, dtype) -> int:
-    if dtype not in _DTYPES:
-        raise TypeError(f"{fn}: unsupported dtype {dtype}")
-    return _DTYPES[dtype]
-
-
-def _check_shape(fn: str, name: str, t, shape) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _shape(fn: str, name: str, t, shape) -> None:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-class _OnStream:
-    """Tensors allocated inside belong to `stream` (None: the current one)."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __init__(self, stream):
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+
+def _stream_of(stream, dev: int) -> int:
+    """The address of `stream`, or of the current stream of device `dev`."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _new(stream, like, *shapes, dtype=None):
+    """New tensors of the shapes (None: None), beside `like`, that belong to
+    `stream` (None: the current one)."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream))
-        self.ctx = torch.cuda.stream(stream) if stream is not None else None
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        with torch.cuda.stream(stream):
+            return _new(None, like, *shapes, dtype=dtype)
+    dtype = dtype or like.dtype
+    return tuple(None if s is None else like.new_empty(s, dtype=dtype) for s in shapes)
 
 
 def _token_stride(fn: str, name: str, t) -> int:
     """Elements between tokens of [tokens, heads, d] whose heads are packed."""
     T, H, d = t.shape
+    if t.is_contiguous():
+        return H * d
     if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
         raise ValueError(f"{fn}: the heads of {name} are not packed")
     if T <= 1:
@@ -717,20 +726,6 @@ def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, low=1.0, high=32.0, 
     return out if device is None else out.to(device)
 
 
-def nsp_rope(tensors, cu_seqlens, ndoc, positions, start, length, d, rot, freqs, interleaved,
-             mscale, inverse, io_dtype, stream=None) -> int:
-    """tensors: sequence of (in, out, in_stride, out_stride, heads, groups)
-    with in and out as addresses."""
-    arr = (RopeTensor * len(tensors))()
-    for i, t in enumerate(tensors):
-        arr[i] = RopeTensor(*t)
-    st = load().nsp_rope(C.addressof(arr), len(tensors), _ptr(cu_seqlens), int(ndoc),
-                         _ptr(positions), int(start), int(length), int(d), int(rot), _ptr(freqs),
-                         int(interleaved), float(mscale), int(inverse), int(io_dtype),
-                         _stream(stream))
-    return _check("nsp_rope", st)
-
-
 def rope(q, k, cu_seqlens, freqs, layout="half", mscale=1.0, inverse=False, start=0,
          positions=None, q_groups=1, out=None, stream=None):
     """Rotate q [T, Hq, d] and k [T, Hkv, d] (k may be None) by their tokens'
@@ -746,103 +741,126 @@ def rope(q, k, cu_seqlens, freqs, layout="half", mscale=1.0, inverse=False, star
     gradients of q and k.  out: (q_out, k_out) to write (q and k themselves to
     rotate in place), default new tensors.  Rows at or past cu_seqlens[-1] are
     not written."""
-    io = _check_io("rope", q.dtype)
+    fn, dt = "rope", q.dtype
+    io = _io(fn, dt)
     qo, ko = out if out is not None else (None, None)
-    _check_tensors("rope", q.dtype, q=q, k=k, cu_seqlens=cu_seqlens, positions=positions,
-                   freqs=freqs, q_out=qo, k_out=ko)
+    dev = _on_device(fn, dt, q=q, k=k, q_out=qo, k_out=ko)
+    _on_device(fn, torch.int32, cu_seqlens=cu_seqlens, positions=positions)
+    _on_device(fn, torch.float64, freqs=freqs)
     if layout not in ("half", "interleaved"):
         raise ValueError(f"rope: unknown layout {layout!r}")
     P = int(q_groups)
-    grouped_in = inverse and P > 1
+    grouped_in, grouped_out = inverse and P > 1, not inverse and P > 1
     if q.dim() != (4 if grouped_in else 3) or P < 1:
         raise ValueError("rope: q is [T, Hq, d], or [P, T, Hq / P, d] for the inverse of a grouped q")
     if grouped_in:
         if q.shape[0] != P:
             raise ValueError("rope: q has another number of head groups than q_groups")
-        T, Hq, d = q.shape[1], P * q.shape[2], q.shape[3]
+        _, T, hpg, d = q.shape
+        Hq = P * hpg
     else:
         T, Hq, d = q.shape
         if Hq % P != 0:
             raise ValueError("rope: q_groups does not divide the heads")
+    Hkv = 0
     if k is not None:
-        _check_shape("rope", "k", k, (T, k.shape[1] if k.dim() == 3 else -1, d))
-    _check_shape("rope", "positions", positions, (T,))
+        Hkv = k.shape[1] if k.dim() == 3 else -1
+        _shape(fn, "k", k, (T, Hkv, d))
+    _shape(fn, "positions", positions, (T,))
+    if freqs.dim() != 1:
+        raise ValueError("rope: freqs is [rot / 2]")
     if positions is None and (cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
         raise ValueError("rope: cu_seqlens [documents + 1] or positions are needed")
-    q_shape = (P, T, Hq // P, d) if P > 1 and not inverse else (T, Hq, d)
-    with _OnStream(stream):
-        if qo is None:
-            qo = torch.empty(q_shape, dtype=q.dtype, device=q.device)
-        if ko is None and k is not None:
-            ko = torch.empty((T, k.shape[1], d), dtype=q.dtype, device=q.device)
-    _check_shape("rope", "q_out", qo, q_shape)
-    _check_shape("rope", "k_out", ko, k.shape if k is not None else ())
-    tensors = [(_ptr(q) if grouped_in else q.data_ptr(),
-                _ptr(qo) if len(q_shape) == 4 else qo.data_ptr(),
-                0 if grouped_in else _token_stride("rope", "q", q),
-                0 if len(q_shape) == 4 else _token_stride("rope", "q_out", qo), Hq, P)]
-    if k is not None:
-        tensors.append((k.data_ptr(), ko.data_ptr(), _token_stride("rope", "k", k),
-                        _token_stride("rope", "k_out", ko), k.shape[1], 1))
-    nsp_rope(tensors, cu_seqlens, cu_seqlens.numel() - 1 if cu_seqlens is not None else 0,
-             positions, start, T, d, 2 * freqs.numel(), freqs, layout == "interleaved", mscale,
-             bool(inverse), io, stream)
+    q_shape = (P, T, Hq // P, d) if grouped_out else (T, Hq, d)
+    if qo is None:
+        qo, = _new(stream, q, q_shape)
+    else:
+        _shape(fn, "q_out", qo, q_shape)
+    if k is None:
+        ko = None
+    elif ko is None:
+        ko, = _new(stream, k, (T, Hkv, d))
+    else:
+        _shape(fn, "k_out", ko, (T, Hkv, d))
+    one = (_ptr(q) if grouped_in else q.data_ptr(), _ptr(qo) if grouped_out else qo.data_ptr(),
+           0 if grouped_in else _token_stride(fn, "q", q),
+           0 if grouped_out else _token_stride(fn, "q_out", qo), Hq, P)
+    if k is None:
+        n, arr = 1, _Rope1(one)
+    else:
+        n, arr = 2, _Rope2(one, (k.data_ptr(), ko.data_ptr(), _token_stride(fn, "k", k),
+                                 _token_stride(fn, "k_out", ko), Hkv, 1))
+    st = load().nsp_rope(C.addressof(arr), n, _ptr(cu_seqlens),
+                         0 if cu_seqlens is None else cu_seqlens.numel() - 1, _ptr(positions),
+                         int(start), T, d, 2 * freqs.numel(), _ptr(freqs), layout == "interleaved",
+                         mscale, bool(inverse), io, _stream_of(stream, dev))
+    _check("nsp_rope", st)
     return qo, ko
 
 
-def _lambda_shape(fn, q1, k1, q2, k2):
-    io = _check_io(fn, q1.dtype)
+def _vectors(fn, q1, k1, q2, k2):
     if q1.dim() != 2:
         raise ValueError(f"{fn}: the vectors are [n, dl]")
-    for name, t in (("k1", k1), ("q2", q2), ("k2", k2)):
-        _check_shape(fn, name, t, q1.shape)
-    return io, q1.shape[0], q1.shape[1]
+    s = q1.shape
+    if k1.shape != s or q2.shape != s or k2.shape != s:
+        raise ValueError(f"{fn}: the vectors are of different shapes")
+    return s[0], s[1]
 
 
 def diff_lambda(q1, k1, q2, k2, heads, lambda_init, stream=None):
     """lambda [heads] = exp(<q1, k1>) - exp(<q2, k2>) + lambda_init of vectors
     [n, dl], n = heads, or 1 for one set shared by every head."""
-    io, n, dl = _lambda_shape("diff_lambda", q1, k1, q2, k2)
-    _check_tensors("diff_lambda", q1.dtype, q1=q1, k1=k1, q2=q2, k2=k2)
-    with _OnStream(stream):
-        lam = torch.empty(int(heads), dtype=q1.dtype, device=q1.device)
-    st = load().nsp_diff_lambda_fwd(_ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), n, dl, int(heads),
-                                    float(lambda_init), io, lam.data_ptr() or None,
-                                    _stream(stream))
+    fn = "diff_lambda"
+    io = _io(fn, q1.dtype)
+    dev = _on_device(fn, q1.dtype, q1=q1, k1=k1, q2=q2, k2=k2)
+    n, dl = _vectors(fn, q1, k1, q2, k2)
+    heads = int(heads)
+    lam, = _new(stream, q1, (heads,))
+    st = load().nsp_diff_lambda_fwd(_ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), n, dl, heads,
+                                    lambda_init, io, _ptr(lam), _stream_of(stream, dev))
     _check("nsp_diff_lambda_fwd", st)
     return lam
 
 
 def diff_lambda_bwd(dlam, q1, k1, q2, k2, stream=None):
     """Gradients of q1, k1, q2, k2 from dlam [heads] (or [heads, 1])."""
-    io, n, dl = _lambda_shape("diff_lambda_bwd", q1, k1, q2, k2)
-    _check_tensors("diff_lambda_bwd", q1.dtype, dlam=dlam, q1=q1, k1=k1, q2=q2, k2=k2)
-    with _OnStream(stream):
-        g = torch.empty((4, n, dl), dtype=q1.dtype, device=q1.device)
+    fn = "diff_lambda_bwd"
+    io = _io(fn, q1.dtype)
+    dev = _on_device(fn, q1.dtype, dlam=dlam, q1=q1, k1=k1, q2=q2, k2=k2)
+    n, dl = _vectors(fn, q1, k1, q2, k2)
+    g, = _new(stream, q1, (4, n, dl))
     p, step = g.data_ptr(), n * dl * g.element_size()
     st = load().nsp_diff_lambda_bwd(_ptr(dlam), _ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), n, dl,
-                                    dlam.numel(), io, p or None, (p + step) if p else None,
-                                    (p + 2 * step) if p else None, (p + 3 * step) if p else None,
-                                    _stream(stream))
+                                    dlam.numel(), io, p, p + step, p + 2 * step, p + 3 * step,
+                                    _stream_of(stream, dev))
     _check("nsp_diff_lambda_bwd", st)
-    return g[0], g[1], g[2], g[3]
+    return g.unbind(0)
 
 
-def _diff_shapes(fn, q, k, v, lam, cu_seqlens, stream_rows, **more):
-    io = _check_io(fn, q.dtype)
-    _check_tensors(fn, q.dtype, q=q, k=k, v=v, lam=lam, cu_seqlens=cu_seqlens, **more)
+def _diff_shapes(fn, q, k, v, lam, cu_seqlens, **rows):
+    """Checks of differential attention's tensors; `rows`: more of q's shape."""
+    io = _io(fn, q.dtype)
+    dev = _on_device(fn, q.dtype, q=q, k=k, v=v, lam=lam, **rows)
+    _on_device(fn, torch.int32, cu_seqlens=cu_seqlens)
     if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1:
         raise ValueError(f"{fn}: q is [T, Hq, d], k and v [T, Hkv, d], cu_seqlens [documents + 1]")
     T, Hq, d = q.shape
     Hkv = k.shape[1]
-    _check_shape(fn, "k", k, (T, Hkv, d))
-    _check_shape(fn, "v", v, (T, Hkv, d))
+    _shape(fn, "k", k, (T, Hkv, d))
+    _shape(fn, "v", v, (T, Hkv, d))
     n = lam.numel() // Hq if Hq > 0 else 0
     if lam.dim() not in (1, 2) or lam.shape[0] != Hq or n not in (1, T):
         raise ValueError(f"{fn}: lam is [Hq], [Hq, 1] or [Hq, T]")
-    for name in stream_rows:
-        _check_shape(fn, name, more[name], (T, Hq, d))
-    return io, T, Hq, Hkv, d, n
+    for name, t in rows.items():
+        _shape(fn, name, t, q.shape)
+    return io, dev, T, Hq, Hkv, d, n
+
+
+def _workspace(fn, stream, like, nbytes, workspace):
+    if workspace is None:
+        return _new(stream, like, (nbytes,), dtype=torch.uint8)[0]
+    _on_device(fn, torch.uint8, workspace=workspace)
+    return workspace
 
 
 def diff_attn_fwd(q, k, v, lam, cu_seqlens, scale=None, causal=True, save=False, workspace=None,
@@ -851,71 +869,60 @@ def diff_attn_fwd(q, k, v, lam, cu_seqlens, scale=None, causal=True, save=False,
     [T, Hkv, d], map m of a head in columns [m d/2, (m + 1) d/2) of q and k,
     lam [Hq], [Hq, 1] or [Hq, T].  Returns out [T, Hq, d]; with save=True
     (out, out2, lse), what diff_attn_bwd needs."""
-    io, T, Hq, Hkv, d, n = _diff_shapes("diff_attn_fwd", q, k, v, lam, cu_seqlens, (),
-                                        workspace=workspace)
+    fn = "diff_attn_fwd"
+    io, dev, T, Hq, Hkv, d, n = _diff_shapes(fn, q, k, v, lam, cu_seqlens)
     scale = (d // 2) ** -0.5 if scale is None else scale
     lib = load()
-    out2 = lse = None
-    with _OnStream(stream):
-        out = torch.empty_like(q)
-        if save:
-            out2 = torch.empty_like(q)
-            lse = torch.empty((Hq, 2, T), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(lib.nsp_diff_attn_fwd_workspace_size(T), dtype=torch.uint8,
-                                    device=q.device)
+    out, out2 = _new(stream, q, (T, Hq, d), (T, Hq, d) if save else None)
+    lse = _new(stream, q, (Hq, 2, T), dtype=torch.float32)[0] if save else None
+    ws = _workspace(fn, stream, q, lib.nsp_diff_attn_fwd_workspace_size(T), workspace)
     st = lib.nsp_diff_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), n, _ptr(cu_seqlens),
-                               cu_seqlens.numel() - 1, T, Hq, Hkv, d, float(scale),
-                               int(bool(causal)), io, _ptr(out), _ptr(out2), _ptr(lse),
-                               _ptr(workspace), workspace.numel(), _stream(stream))
+                               cu_seqlens.numel() - 1, T, Hq, Hkv, d, scale, bool(causal), io,
+                               _ptr(out), _ptr(out2), _ptr(lse), _ptr(ws), ws.numel(),
+                               _stream_of(stream, dev))
     _check("nsp_diff_attn_fwd", st)
     return (out, out2, lse) if save else out
 
 
 def diff_attn_bwd(q, k, v, lam, out, out2, dout, lse, cu_seqlens, scale=None, causal=True,
                   workspace=None, stream=None):
-    """Gradients (dq, dk, dv, dlam) of diff_attn_fwd(save=True); dlam has
-    lam's shape ([Hq] as [Hq, 1])."""
-    io, T, Hq, Hkv, d, n = _diff_shapes("diff_attn_bwd", q, k, v, lam, cu_seqlens,
-                                        ("out", "out2", "dout"), out=out, out2=out2, dout=dout,
-                                        lse=lse, workspace=workspace)
-    _check_shape("diff_attn_bwd", "lse", lse, (Hq, 2, T))
+    """Gradients (dq, dk, dv, dlam) of diff_attn_fwd(save=True); dlam is
+    [Hq, 1] or [Hq, T]."""
+    fn = "diff_attn_bwd"
+    io, dev, T, Hq, Hkv, d, n = _diff_shapes(fn, q, k, v, lam, cu_seqlens, out=out, out2=out2,
+                                             dout=dout)
+    _on_device(fn, torch.float32, lse=lse)
+    _shape(fn, "lse", lse, (Hq, 2, T))
     scale = (d // 2) ** -0.5 if scale is None else scale
     lib = load()
-    with _OnStream(stream):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        dlam = torch.empty((Hq, n), dtype=q.dtype, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(lib.nsp_diff_attn_bwd_workspace_size(T, Hq, d),
-                                    dtype=torch.uint8, device=q.device)
+    dq, dk, dv, dlam = _new(stream, q, (T, Hq, d), (T, Hkv, d), (T, Hkv, d), (Hq, n))
+    ws = _workspace(fn, stream, q, lib.nsp_diff_attn_bwd_workspace_size(T, Hq, Hkv, d, io), workspace)
     st = lib.nsp_diff_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), n, _ptr(out), _ptr(out2),
                                _ptr(dout), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T,
-                               Hq, Hkv, d, float(scale), int(bool(causal)), io, _ptr(dq), _ptr(dk),
-                               _ptr(dv), _ptr(dlam), _ptr(workspace), workspace.numel(),
-                               _stream(stream))
+                               Hq, Hkv, d, scale, bool(causal), io, _ptr(dq), _ptr(dk), _ptr(dv),
+                               _ptr(dlam), _ptr(ws), ws.numel(), _stream_of(stream, dev))
     _check("nsp_diff_attn_bwd", st)
     return dq, dk, dv, dlam
 
 
-def _norm_shapes(fn, x, weight, gate, **more):
-    io = _check_io(fn, x.dtype)
-    _check_tensors(fn, x.dtype, x=x, weight=weight, gate=gate, **more)
+def _norm_shapes(fn, x, weight, gate, dy=None):
+    io = _io(fn, x.dtype)
+    dev = _on_device(fn, x.dtype, x=x, weight=weight, gate=gate, dy=dy)
     if x.dim() != 3:
         raise ValueError(f"{fn}: x is [tokens, heads, d]")
-    _check_shape(fn, "weight", weight, x.shape[2:])
-    _check_shape(fn, "gate", gate, x.shape)
-    return io, _token_stride(fn, "x", x)
+    _shape(fn, "weight", weight, x.shape[2:])
+    _shape(fn, "gate", gate, x.shape)
+    return io, dev, _token_stride(fn, "x", x)
 
 
 def head_norm(x, weight=None, gate=None, eps=1e-6, scale=1.0, stream=None):
     """scale * weight * x / sqrt(mean(x^2) + eps) [* sigmoid(gate)] of every
     head's row of x [tokens, heads, d] (tokens any stride apart); weight [d]."""
-    io, stride = _norm_shapes("head_norm", x, weight, gate)
-    with _OnStream(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    io, dev, stride = _norm_shapes("head_norm", x, weight, gate)
     T, H, d = x.shape
-    st = load().nsp_head_norm_fwd(x.data_ptr() or None, stride, _ptr(weight), _ptr(gate), T, H, d,
-                                  float(eps), float(scale), io, _ptr(y), _stream(stream))
+    y, = _new(stream, x, (T, H, d))
+    st = load().nsp_head_norm_fwd(x.data_ptr(), stride, _ptr(weight), _ptr(gate), T, H, d, eps,
+                                  scale, io, _ptr(y), _stream_of(stream, dev))
     _check("nsp_head_norm_fwd", st)
     return y
 
@@ -923,23 +930,18 @@ def head_norm(x, weight=None, gate=None, eps=1e-6, scale=1.0, stream=None):
 def head_norm_bwd(x, dy, weight=None, gate=None, eps=1e-6, scale=1.0, workspace=None, stream=None):
     """Gradients (dx, dweight, dgate) of head_norm; None for a weight or gate
     that is not there."""
-    io, stride = _norm_shapes("head_norm_bwd", x, weight, gate, dy=dy, workspace=workspace)
-    _check_shape("head_norm_bwd", "dy", dy, x.shape)
+    fn = "head_norm_bwd"
+    io, dev, stride = _norm_shapes(fn, x, weight, gate, dy)
     T, H, d = x.shape
+    _shape(fn, "dy", dy, (T, H, d))
     lib = load()
-    dw = dg = None
-    with _OnStream(stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if weight is not None:
-            dw = torch.empty(d, dtype=x.dtype, device=x.device)
-            if workspace is None:
-                workspace = torch.empty(lib.nsp_head_norm_bwd_workspace_size(T, H, d),
-                                        dtype=torch.uint8, device=x.device)
-        if gate is not None:
-            dg = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    st = lib.nsp_head_norm_bwd(x.data_ptr() or None, stride, _ptr(weight), _ptr(gate), _ptr(dy), T,
-                               H, d, float(eps), float(scale), io, _ptr(dx), _ptr(dg), _ptr(dw),
-                               _ptr(workspace), workspace.numel() if workspace is not None else 0,
-                               _stream(stream))
+    dx, dw, dg = _new(stream, x, (T, H, d), None if weight is None else (d,),
+                      None if gate is None else (T, H, d))
+    ws = None
+    if weight is not None:
+        ws = _workspace(fn, stream, x, lib.nsp_head_norm_bwd_workspace_size(T, H, d), workspace)
+    st = lib.nsp_head_norm_bwd(x.data_ptr(), stride, _ptr(weight), _ptr(gate), _ptr(dy), T, H, d,
+                               eps, scale, io, _ptr(dx), _ptr(dg), _ptr(dw), _ptr(ws),
+                               0 if ws is None else ws.numel(), _stream_of(stream, dev))
     _check("nsp_head_norm_bwd", st)
     return dx, dw, dg
