@@ -867,24 +867,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
   grid_dep_wait();
 }
 
-template <typename K>
-cudaError_t launch_one(K kern, int threads, size_t smem, const CUtensorMap& mq, const CUtensorMap& mdo,
-                       const CUtensorMap& mk, const CUtensorMap& mv, const BwdArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(persistent_grid()), dim3(threads), smem, s, mq, mdo, mk, mv, a);
-  count_launches(1);
-  count_path(true);
-  return e;
-}
-
 template <int D>
 cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
                      const CUtensorMap& mv, const BwdArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_one(diff_bwd_dkdv_tc_kernel<D>, kKvThreads, smem_bytes<SmemKV>(), mq,
-                                   mdo, mk, mv, a, s);
+  const cudaError_t e = launch_persistent<2 * D>(diff_bwd_dkdv_tc_kernel<D>, kKvThreads,
+                                                 smem_bytes<SmemKV>(), s, mq, mdo, mk, mv, a);
   if (e != cudaSuccess) return e;
-  return launch_one(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), mq, mdo, mk, mv, a, s);
+  return launch_persistent<2 * D + 1>(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), s, mq,
+                                      mdo, mk, mv, a);
 }
 
 }  // namespace

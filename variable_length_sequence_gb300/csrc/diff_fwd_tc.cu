@@ -414,19 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
-cudaError_t launch_d(const FwdArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
-                     const CUtensorMap& mv, cudaStream_t s) {
-  auto kern = diff_fwd_tc_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kSmemBytes);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(persistent_grid()), dim3(kThreads), kSmemBytes, s, mq, mk, mv, a);
-  count_launches(1);
-  count_path(true);
-  return e;
-}
-
 }  // namespace
 
 // [rows, cols] bf16 row-major, box = 64 columns x 128 rows, 128-byte swizzle.
@@ -462,7 +449,8 @@ cudaError_t launch_diff_fwd_tc(const DiffProblem& d, const FwdWsLayout& L, char*
   a.out2 = reinterpret_cast<__nv_bfloat16*>(d.out2);
   a.tiles = reinterpret_cast<const int2*>(ws + L.tiles);
   a.order = reinterpret_cast<const int*>(ws + L.order);
-  return p.d == 128 ? launch_d<128>(a, mq, mk, mv, s) : launch_d<64>(a, mq, mk, mv, s);
+  return p.d == 128 ? launch_persistent<0>(diff_fwd_tc_kernel<128>, kThreads, kSmemBytes, s, mq, mk, mv, a)
+                    : launch_persistent<1>(diff_fwd_tc_kernel<64>, kThreads, kSmemBytes, s, mq, mk, mv, a);
 }
 
 }  // namespace nsp

@@ -1,6 +1,8 @@
 // What the tensor-core kernels of differential attention share.
 #pragma once
 
+#include <atomic>
+
 #include "layer.cuh"
 #include "tc_ptx.cuh"
 
@@ -142,6 +144,27 @@ __device__ __forceinline__ S* smem_view(uint8_t* raw, WsHeader* hdr) {
 template <typename S>
 constexpr size_t smem_bytes() {
   return sizeof(S) + 1024 <= kSmemLimit ? sizeof(S) + 1024 : kSmemLimit;
+}
+
+// Launches a persistent kernel behind the one before it, with `smem` bytes of
+// dynamic shared memory (allowed once for each device and kernel; ID tells the
+// file's kernels of one signature apart).
+template <int ID, typename K, typename... Args>
+static cudaError_t launch_persistent(K kern, int threads, size_t smem, cudaStream_t s, Args... args) {
+  static std::atomic<uint64_t> allowed{0};           // one bit a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  e = launch_dependent(kern, dim3(persistent_grid()), dim3(threads), smem, s, args...);
+  count_launches(1);
+  count_path(true);
+  return e;
 }
 
 }  // namespace tc

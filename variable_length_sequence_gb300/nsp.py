@@ -686,16 +686,19 @@ def _stream_of(stream, dev: int) -> int:
     return _stream(stream)
 
 
-def _new(stream, like, *shapes, dtype=None):
-    """New tensors of the shapes (None: None), beside `like`, that belong to
-    `stream` (None: the current one)."""
+def _owner(stream):
+    """A context whose new tensors belong to `stream` (not None)."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _new(stream, like, shape, dtype=None):
+    """A new tensor beside `like` that belongs to `stream` (None: the current one)."""
     if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(stream):
-            return _new(None, like, *shapes, dtype=dtype)
-    dtype = dtype or like.dtype
-    return tuple(None if s is None else like.new_empty(s, dtype=dtype) for s in shapes)
+        with _owner(stream):
+            return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def _token_stride(fn: str, name: str, t) -> int:
@@ -772,24 +775,27 @@ def rope(q, k, cu_seqlens, freqs, layout="half", mscale=1.0, inverse=False, star
     if positions is None and (cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
         raise ValueError("rope: cu_seqlens [documents + 1] or positions are needed")
     q_shape = (P, T, Hq // P, d) if grouped_out else (T, Hq, d)
+    qo_stride = ko_stride = 0                     # (0: packed)
     if qo is None:
-        qo, = _new(stream, q, q_shape)
+        qo = _new(stream, q, q_shape)
     else:
         _shape(fn, "q_out", qo, q_shape)
+        if grouped_out:
+            _ptr(qo)
+        else:
+            qo_stride = _token_stride(fn, "q_out", qo)
+    one = (_ptr(q) if grouped_in else q.data_ptr(), qo.data_ptr(),
+           0 if grouped_in else _token_stride(fn, "q", q), qo_stride, Hq, P)
     if k is None:
-        ko = None
-    elif ko is None:
-        ko, = _new(stream, k, (T, Hkv, d))
+        ko, n, arr = None, 1, _Rope1(one)
     else:
-        _shape(fn, "k_out", ko, (T, Hkv, d))
-    one = (_ptr(q) if grouped_in else q.data_ptr(), _ptr(qo) if grouped_out else qo.data_ptr(),
-           0 if grouped_in else _token_stride(fn, "q", q),
-           0 if grouped_out else _token_stride(fn, "q_out", qo), Hq, P)
-    if k is None:
-        n, arr = 1, _Rope1(one)
-    else:
-        n, arr = 2, _Rope2(one, (k.data_ptr(), ko.data_ptr(), _token_stride(fn, "k", k),
-                                 _token_stride(fn, "k_out", ko), Hkv, 1))
+        if ko is None:
+            ko = _new(stream, k, (T, Hkv, d))
+        else:
+            _shape(fn, "k_out", ko, (T, Hkv, d))
+            ko_stride = _token_stride(fn, "k_out", ko)
+        n, arr = 2, _Rope2(one, (k.data_ptr(), ko.data_ptr(), _token_stride(fn, "k", k), ko_stride,
+                                 Hkv, 1))
     st = load().nsp_rope(C.addressof(arr), n, _ptr(cu_seqlens),
                          0 if cu_seqlens is None else cu_seqlens.numel() - 1, _ptr(positions),
                          int(start), T, d, 2 * freqs.numel(), _ptr(freqs), layout == "interleaved",
@@ -799,9 +805,9 @@ def rope(q, k, cu_seqlens, freqs, layout="half", mscale=1.0, inverse=False, star
 
 
 def _vectors(fn, q1, k1, q2, k2):
-    if q1.dim() != 2:
-        raise ValueError(f"{fn}: the vectors are [n, dl]")
     s = q1.shape
+    if len(s) != 2:
+        raise ValueError(f"{fn}: the vectors are [n, dl]")
     if k1.shape != s or q2.shape != s or k2.shape != s:
         raise ValueError(f"{fn}: the vectors are of different shapes")
     return s[0], s[1]
@@ -815,9 +821,9 @@ def diff_lambda(q1, k1, q2, k2, heads, lambda_init, stream=None):
     dev = _on_device(fn, q1.dtype, q1=q1, k1=k1, q2=q2, k2=k2)
     n, dl = _vectors(fn, q1, k1, q2, k2)
     heads = int(heads)
-    lam, = _new(stream, q1, (heads,))
+    lam = _new(stream, q1, (heads,))
     st = load().nsp_diff_lambda_fwd(_ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), n, dl, heads,
-                                    lambda_init, io, _ptr(lam), _stream_of(stream, dev))
+                                    lambda_init, io, lam.data_ptr(), _stream_of(stream, dev))
     _check("nsp_diff_lambda_fwd", st)
     return lam
 
@@ -828,13 +834,14 @@ def diff_lambda_bwd(dlam, q1, k1, q2, k2, stream=None):
     io = _io(fn, q1.dtype)
     dev = _on_device(fn, q1.dtype, dlam=dlam, q1=q1, k1=k1, q2=q2, k2=k2)
     n, dl = _vectors(fn, q1, k1, q2, k2)
-    g, = _new(stream, q1, (4, n, dl))
-    p, step = g.data_ptr(), n * dl * g.element_size()
+    shape = (n, dl)
+    g = (_new(stream, q1, shape), _new(stream, q1, shape), _new(stream, q1, shape),
+         _new(stream, q1, shape))             # (less host time than views of one tensor)
     st = load().nsp_diff_lambda_bwd(_ptr(dlam), _ptr(q1), _ptr(k1), _ptr(q2), _ptr(k2), n, dl,
-                                    dlam.numel(), io, p, p + step, p + 2 * step, p + 3 * step,
-                                    _stream_of(stream, dev))
+                                    dlam.numel(), io, g[0].data_ptr(), g[1].data_ptr(),
+                                    g[2].data_ptr(), g[3].data_ptr(), _stream_of(stream, dev))
     _check("nsp_diff_lambda_bwd", st)
-    return g.unbind(0)
+    return g
 
 
 def _diff_shapes(fn, q, k, v, lam, cu_seqlens, **rows):
@@ -858,7 +865,7 @@ def _diff_shapes(fn, q, k, v, lam, cu_seqlens, **rows):
 
 def _workspace(fn, stream, like, nbytes, workspace):
     if workspace is None:
-        return _new(stream, like, (nbytes,), dtype=torch.uint8)[0]
+        return _new(stream, like, nbytes, torch.uint8)
     _on_device(fn, torch.uint8, workspace=workspace)
     return workspace
 
@@ -873,8 +880,10 @@ def diff_attn_fwd(q, k, v, lam, cu_seqlens, scale=None, causal=True, save=False,
     io, dev, T, Hq, Hkv, d, n = _diff_shapes(fn, q, k, v, lam, cu_seqlens)
     scale = (d // 2) ** -0.5 if scale is None else scale
     lib = load()
-    out, out2 = _new(stream, q, (T, Hq, d), (T, Hq, d) if save else None)
-    lse = _new(stream, q, (Hq, 2, T), dtype=torch.float32)[0] if save else None
+    out = _new(stream, q, (T, Hq, d))
+    out2 = lse = None
+    if save:
+        out2, lse = _new(stream, q, (T, Hq, d)), _new(stream, q, (Hq, 2, T), torch.float32)
     ws = _workspace(fn, stream, q, lib.nsp_diff_attn_fwd_workspace_size(T), workspace)
     st = lib.nsp_diff_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), n, _ptr(cu_seqlens),
                                cu_seqlens.numel() - 1, T, Hq, Hkv, d, scale, bool(causal), io,
@@ -895,7 +904,8 @@ def diff_attn_bwd(q, k, v, lam, out, out2, dout, lse, cu_seqlens, scale=None, ca
     _shape(fn, "lse", lse, (Hq, 2, T))
     scale = (d // 2) ** -0.5 if scale is None else scale
     lib = load()
-    dq, dk, dv, dlam = _new(stream, q, (T, Hq, d), (T, Hkv, d), (T, Hkv, d), (Hq, n))
+    dq, dk, dv = (_new(stream, q, t.shape) for t in (q, k, v))
+    dlam = _new(stream, q, (Hq, n))
     ws = _workspace(fn, stream, q, lib.nsp_diff_attn_bwd_workspace_size(T, Hq, Hkv, d, io), workspace)
     st = lib.nsp_diff_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), n, _ptr(out), _ptr(out2),
                                _ptr(dout), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T,
@@ -920,7 +930,7 @@ def head_norm(x, weight=None, gate=None, eps=1e-6, scale=1.0, stream=None):
     head's row of x [tokens, heads, d] (tokens any stride apart); weight [d]."""
     io, dev, stride = _norm_shapes("head_norm", x, weight, gate)
     T, H, d = x.shape
-    y, = _new(stream, x, (T, H, d))
+    y = _new(stream, x, (T, H, d))
     st = load().nsp_head_norm_fwd(x.data_ptr(), stride, _ptr(weight), _ptr(gate), T, H, d, eps,
                                   scale, io, _ptr(y), _stream_of(stream, dev))
     _check("nsp_head_norm_fwd", st)
@@ -935,10 +945,11 @@ def head_norm_bwd(x, dy, weight=None, gate=None, eps=1e-6, scale=1.0, workspace=
     T, H, d = x.shape
     _shape(fn, "dy", dy, (T, H, d))
     lib = load()
-    dx, dw, dg = _new(stream, x, (T, H, d), None if weight is None else (d,),
-                      None if gate is None else (T, H, d))
-    ws = None
+    dx, dw, dg, ws = _new(stream, x, (T, H, d)), None, None, None
+    if gate is not None:
+        dg = _new(stream, x, (T, H, d))
     if weight is not None:
+        dw = _new(stream, x, (d,))
         ws = _workspace(fn, stream, x, lib.nsp_head_norm_bwd_workspace_size(T, H, d), workspace)
     st = lib.nsp_head_norm_bwd(x.data_ptr(), stride, _ptr(weight), _ptr(gate), _ptr(dy), T, H, d,
                                eps, scale, io, _ptr(dx), _ptr(dg), _ptr(dw), _ptr(ws),
