@@ -760,10 +760,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const bool valid = row < p.q_len;
       int lo = 0, hi = 0;                                    // visible keys [lo, hi)
       float nl[2] = {0.f, 0.f}, dl[2] = {0.f, 0.f}, c = 0.f;
+      const Span32 doc =
+          document_of_rows(p.cu, p.ndoc, (int64_t)it.qtile * 128 + wq * 32, p.q_len, lane);
       if (valid) {
-        const int b = doc_of(p.cu, p.ndoc, row);
-        lo = __ldg(p.cu + b);
-        hi = p.causal ? (int)row + 1 : (int)min((int64_t)__ldg(p.cu + b + 1), p.kv_len);
+        lo = doc.first;
+        hi = p.causal ? (int)row + 1 : (int)min((int64_t)doc.last, p.kv_len);
         const int64_t v1 = (int64_t)(2 * it.h) * a.Tp + row;
         nl[0] = __ldg(a.nlse2 + v1);
         nl[1] = __ldg(a.nlse2 + v1 + a.Tp);

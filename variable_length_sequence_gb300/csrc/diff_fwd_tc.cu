@@ -17,7 +17,8 @@
 //   warps 4-7   softmax of map 2
 //   warp 8      TMA producer and work fetch
 //   warp 9      TMEM allocation and the single MMA-issuing thread
-//   warps 10-11 idle (they complete the control warpgroup)
+//   warp 10     stores finished tiles (TMA, from a staging buffer)
+//   warp 11     idle (completes the control warpgroup)
 // Registers are moved from the control warpgroup to the softmax warpgroups
 // (launched at 168: 384 x 168 = 64512; 256 x 192 + 128 x 112 = 63488), enough
 // to hold a 128-column row of S.
@@ -43,7 +44,7 @@ constexpr int BM = 128, BN = 128;
 constexpr int NSTAGE = 2;
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 192, kRegsControl = 112;
-constexpr int kWarpProducer = 8, kWarpMma = 9;
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpStore = 10;
 __host__ __device__ constexpr uint32_t col_s(int m) { return m == 0 ? 0u : 128u; }
 __host__ __device__ constexpr uint32_t col_o(int m) { return m == 0 ? 256u : 384u; }
 constexpr float kRescaleThreshold = 8.0f;                 // log2 units
@@ -54,44 +55,81 @@ struct Item {
 };
 
 struct __align__(1024) Smem {
-  uint8_t q[2][kTile];                 // this item's and the next one's
+  uint8_t q[2][kTile];                 // this item's and the next one's; then out2's tile
   uint8_t k[NSTAGE][kTile];
   uint8_t v[NSTAGE][kTile];
+  uint8_t out[kTile];                  // the finished tile, 128-byte swizzled, on its way out
   float inv[2][2][BM];                 // [item parity][map][row]: 1 / row sum
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[NSTAGE], k_empty[NSTAGE], v_full[NSTAGE], v_empty[NSTAGE];
-  uint64_t s_full[2], p_full[2], o_full, o_free, inv_full;
+  uint64_t s_full[2], p_full[2], o_full, o_free, inv_full, out_full, out_free;
   uint64_t item_full[2], item_empty[2];
   Item items[2];
   uint64_t mma_drain_bar;
   uint32_t tmem_base;
   WaitCtl wait;
 };
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;        // + alignment slack
-static_assert(kSmemBytes <= kSmemLimit, "forward tile set exceeds shared memory");
+static_assert(sizeof(Smem) <= kSmemLimit, "forward tile set exceeds shared memory");
 
 struct FwdArgs {
   AttnProblem p;
   const __nv_bfloat16* lambda;
   int64_t n_lambda;
-  __nv_bfloat16* out2;
   const int2* tiles;
   const int* order;
 };
 
-template <int D>
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float a = max3f(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+  float b = max3f(__uint_as_float(s[16]), __uint_as_float(s[17]), __uint_as_float(s[18]));
+#pragma unroll
+  for (int i = 3; i < 15; i += 2) {
+    a = max3f(a, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    b = max3f(b, __uint_as_float(s[16 + i]), __uint_as_float(s[17 + i]));
+  }
+  return max3f(fmaxf(a, b), __uint_as_float(s[15]), __uint_as_float(s[31]));
+}
+
+// Columns whose bit is not set become -inf.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if ((bits & (1u << i)) == 0) s[i] = 0xff800000u;
+}
+
+// p = 2^(s scale log2 e - m) of 32 columns in bf16 pairs; their float32 values
+// are added to the four pairs of sums.
+__device__ __forceinline__ void exps32(const uint32_t (&s)[32], uint64_t sl2x2, uint64_t nm2,
+                                       uint64_t (&sum)[4], uint32_t (&p)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float p0, p1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl2x2, nm2), p0,
+              p1);
+    p0 = ex2(p0);
+    p1 = ex2(p1);
+    sum[i & 3] = f2_add(sum[i & 3], f2_pack(p0, p1));
+    p[i] = pack_bf16x2(p0, p1);
+  }
+}
+
+// SAVE: out2 is stored too.
+template <int D, bool SAVE>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ FwdArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                      ~static_cast<uintptr_t>(1023));
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_out,
+                       const __grid_constant__ CUtensorMap tm_out2, const __grid_constant__ FwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttnProblem& p = a.p;
   WsHeader* hdr = p.hdr;
   grid_dep_wait();                          // the schedule kernel's lists and status
   if (status_bad(hdr)) return;
+  Smem* smp = smem_view<Smem>(smem_raw, hdr);
+  if (smp == nullptr) return;
+  Smem& sm = *smp;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -100,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_full[s], 128);
       mbar_init(&sm.item_full[s], 1);
-      mbar_init(&sm.item_empty[s], 1 + 8);
+      mbar_init(&sm.item_empty[s], 2 + 8);
     }
     for (int s = 0; s < NSTAGE; ++s) {
       mbar_init(&sm.k_full[s], 1);
@@ -111,6 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, 8);
     mbar_init(&sm.inv_full, 8);
+    mbar_init(&sm.out_full, 8);
+    mbar_init(&sm.out_free, 1);
     mbar_init(&sm.mma_drain_bar, 1);
     wait_ctl_init(&sm.wait, p.wait_budget);
     fence_mbar_init();
@@ -123,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_out);
   }
   tc_fence_before();
   __syncthreads();
@@ -217,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&sm.s_full[m]);
           }
           mma_commit(&sm.k_empty[st]);
-          if (it.n_kv == 1) mma_commit(&sm.q_empty[slot]);
+          if (it.n_kv == 1 && !SAVE) mma_commit(&sm.q_empty[slot]);
         }
         for (int jj = 0; jj < it.n_kv && ok; ++jj) {
           const uint32_t st = (kv_count + jj) % NSTAGE, n = (kv_count + jj) / NSTAGE;
@@ -249,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&sm.s_full[m]);
             if (m == 1) {
               mma_commit(&sm.k_empty[stn]);
-              if (jj + 2 == it.n_kv) mma_commit(&sm.q_empty[slot]);
+              if (jj + 2 == it.n_kv && !SAVE) mma_commit(&sm.q_empty[slot]);
             }
           }
           ++p_count;
@@ -259,6 +300,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++it_count;
       }
       mma_drain(&sm.mma_drain_bar);        // every product done before TMEM is freed
+    } else if (warp == kWarpStore && lane == 0) {
+      // ------------------------------------------------------------ store of finished tiles
+      uint32_t it_count = 0;
+      while (true) {
+        const uint32_t slot = it_count & 1;
+        if (!mbar_wait(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
+        const Item it = sm.items[slot];
+        mbar_arrive(&sm.item_empty[slot]);
+        if (it.n_kv < 0) break;
+        if (!mbar_wait(&sm.out_full, it_count & 1, wc, hdr)) break;
+#pragma unroll
+        for (int cb = 0; cb < kBlocks; ++cb) {
+          tma_store_2d(&tm_out, sm.out + cb * kBlk, it.h * D + cb * 64, it.qtile * BM);
+          if constexpr (SAVE)
+            tma_store_2d(&tm_out2, sm.q[slot] + cb * kBlk, it.h * D + cb * 64, it.qtile * BM);
+        }
+        bulk_commit();
+        bulk_wait_read_all();
+        mbar_arrive(&sm.out_free);
+        if constexpr (SAVE) mbar_arrive(&sm.q_empty[slot]);
+        ++it_count;
+      }
+      bulk_wait_all();                     // every tile is in memory before the CTA exits
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -282,10 +346,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = row < p.q_len;
       int lo = 0, hi = 0;                                      // visible keys [lo, hi)
       float lam = 0.f;
+      const Span32 doc =
+          document_of_rows(p.cu, p.ndoc, (int64_t)it.qtile * BM + wq * 32, p.q_len, lane);
       if (valid) {
-        const int b = doc_of(p.cu, p.ndoc, row);
-        lo = __ldg(p.cu + b);
-        hi = p.causal ? (int)row + 1 : (int)min((int64_t)__ldg(p.cu + b + 1), p.kv_len);
+        lo = doc.first;
+        hi = p.causal ? (int)row + 1 : (int)min((int64_t)doc.last, p.kv_len);
         lam = __bfloat162float(a.lambda[(int64_t)it.h * a.n_lambda + (a.n_lambda > 1 ? row : 0)]);
       }
       float m = -INFINITY, l = 0.f;
@@ -295,33 +360,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++s_count;
         tc_fence_after();
         const int key0 = (it.j_lo + jj) * BN;
-        // visible columns are [c0, c0 + span): one unsigned compare per column;
-        // a warp whose rows all see the whole tile skips the mask
-        const int c0 = lo - key0;
-        const uint32_t span = (uint32_t)(hi - lo);
-        const bool full_w = __all_sync(0xffffffffu, lo <= key0 && key0 + BN <= hi);
         uint32_t sr[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, sr[c]);
         tmem_wait_ld();
-        if (!full_w) {
+        // a warp whose rows all see the whole tile skips the masks (skipping single
+        // chunks that nothing sees instead costs more in branches than it saves)
+        if (!__all_sync(0xffffffffu, lo <= key0 && key0 + BN <= hi)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((uint32_t)(c * 32 + i - c0) >= span) sr[c][i] = 0xff800000u;   // -inf
+            mask32(sr[c], column_bits(lo - key0 - 32 * c, hi - key0 - 32 * c));
         }
         float mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = max3f(__uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]), __uint_as_float(sr[c][2]));
-#pragma unroll
-          for (int i = 3; i < 31; i += 2)
-            mx[c] = max3f(mx[c], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
-          mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][31]));
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float m_new = fmaxf(m, mt * sl2);
+        for (int c = 0; c < 4; ++c) mx[c] = max32(sr[c]);
+        const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2);
+        // the running output is rescaled only when the maximum grew a lot
         const bool need = (m != -INFINITY) && (m_new > m + kRescaleThreshold);
         const float corr = need ? ex2(m - m_new) : 1.f;
         if (need || m == -INFINITY) m = m_new;
@@ -331,16 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float p0, p1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])),
-                             sl2x2, nm2), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            ls[i & 3] = f2_add(ls[i & 3], f2_pack(p0, p1));
-            pk[i] = pack_bf16x2(p0, p1);
-          }
+          exps32(sr[c], sl2x2, nm2, ls, pk);
           tmem_st16(s_tm + c * 16, pk);
         }
         float l0, l1;
@@ -372,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
       tc_fence_after();
       const float i0 = sm.inv[slot][0][r], i1 = sm.inv[slot][1][r];
-      const int64_t off = (row * p.Hq + it.h) * D + m_ * (D / 2);
-      __nv_bfloat16* const out = reinterpret_cast<__nv_bfloat16*>(p.out) + off;
+      // the previous tile has left the staging buffer
+      if (it_count >= 1 && !wait_warp(&sm.out_free, (it_count - 1) & 1, wc, hdr)) break;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint32_t x[32], y[32];
@@ -384,7 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           mbar_arrive_warp(&sm.o_free, lane);
         }
-        if (!valid) continue;
         uint32_t w[16], w2[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -393,15 +437,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                              fmaf(__uint_as_float(x[2 * i + 1]), i0, -lam * a1));
           w2[i] = pack_bf16x2(a0, a1);
         }
+        // columns m D/2 + 32 c + 0..31 of the row: four 16-byte chunks of its swizzle span
+        const int col = m_ * (D / 2) + c * 32;
+        const uint32_t base = smem_u32(sm.out) + (col >> 6) * kBlk + r * 128;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          st_global_v8(out + c * 32 + 16 * i, w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
-                       w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
-          if (a.out2 != nullptr)
-            st_global_v8(a.out2 + off + c * 32 + 16 * i, w2[8 * i], w2[8 * i + 1], w2[8 * i + 2],
-                         w2[8 * i + 3], w2[8 * i + 4], w2[8 * i + 5], w2[8 * i + 6], w2[8 * i + 7]);
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(base + (((((col & 63) >> 3) + i) ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1],
+                       w[4 * i + 2], w[4 * i + 3]);
+        if constexpr (SAVE) {
+          // (every product of the item is done: its Q tile is free until it is stored)
+          const uint32_t base2 = smem_u32(sm.q[slot]) + (col >> 6) * kBlk + r * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_shared_v4(base2 + (((((col & 63) >> 3) + i) ^ (r & 7)) << 4), w2[4 * i], w2[4 * i + 1],
+                         w2[4 * i + 2], w2[4 * i + 3]);
         }
       }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(&sm.out_full, lane);
       ++it_count;
     }
   }
@@ -412,6 +465,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+template <int D, bool SAVE>
+cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                       const CUtensorMap& mo, const CUtensorMap& mo2, const FwdArgs& a,
+                       cudaStream_t s) {
+  return launch_persistent<2 * D + SAVE>(diff_fwd_tc_kernel<D, SAVE>, kThreads, smem_bytes<Smem>(), s,
+                                         mq, mk, mv, mo, mo2, a);
 }
 
 }  // namespace
@@ -437,20 +498,24 @@ bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols)
 
 cudaError_t launch_diff_fwd_tc(const DiffProblem& d, const FwdWsLayout& L, char* ws, cudaStream_t s) {
   const AttnProblem& p = d.p;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo, mo2;
   if (!diff_tile_map(&mq, p.q, p.q_len, (int64_t)p.Hq * p.d) ||
       !diff_tile_map(&mk, p.k, p.kv_len, (int64_t)p.Hkv * p.d) ||
-      !diff_tile_map(&mv, p.v, p.kv_len, (int64_t)p.Hkv * p.d))
+      !diff_tile_map(&mv, p.v, p.kv_len, (int64_t)p.Hkv * p.d) ||
+      !diff_tile_map(&mo, p.out, p.q_len, (int64_t)p.Hq * p.d) ||
+      !diff_tile_map(&mo2, d.out2 ? d.out2 : p.out, p.q_len, (int64_t)p.Hq * p.d))
     return cudaErrorNotSupported;
   FwdArgs a;
   a.p = p;
   a.lambda = reinterpret_cast<const __nv_bfloat16*>(d.lambda);
   a.n_lambda = d.n_lambda;
-  a.out2 = reinterpret_cast<__nv_bfloat16*>(d.out2);
   a.tiles = reinterpret_cast<const int2*>(ws + L.tiles);
   a.order = reinterpret_cast<const int*>(ws + L.order);
-  return p.d == 128 ? launch_persistent<0>(diff_fwd_tc_kernel<128>, kThreads, kSmemBytes, s, mq, mk, mv, a)
-                    : launch_persistent<1>(diff_fwd_tc_kernel<64>, kThreads, kSmemBytes, s, mq, mk, mv, a);
+  if (d.out2 != nullptr)
+    return p.d == 128 ? launch_fwd<128, true>(mq, mk, mv, mo, mo2, a, s)
+                      : launch_fwd<64, true>(mq, mk, mv, mo, mo2, a, s);
+  return p.d == 128 ? launch_fwd<128, false>(mq, mk, mv, mo, mo2, a, s)
+                    : launch_fwd<64, false>(mq, mk, mv, mo, mo2, a, s);
 }
 
 }  // namespace nsp

@@ -1,6 +1,8 @@
 // What the tensor-core kernels of differential attention share.
 #pragma once
 
+#include <limits.h>
+
 #include <atomic>
 
 #include "layer.cuh"
@@ -48,6 +50,43 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, WaitCtl
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, WaitCtl* wc, WsHeader* hdr) {
   if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   return mbar_wait_warp(bar, parity, wc, hdr);
+}
+
+// Document [first, last) of stream row t0 + lane, for a whole warp (rows at or
+// past `rows` get the document of the last row below): the warp narrows the
+// search 32-fold with each load, then reads the next documents' starts in one:
+// three dependent loads for a thousand documents instead of ten.
+struct Span32 {
+  int first, last;
+};
+__device__ __forceinline__ Span32 document_of_rows(const int32_t* __restrict__ cu, int ndoc, int64_t t0,
+                                                   int64_t rows, int lane) {
+  int lo = 0, m = ndoc;                              // the first row's document is in [lo, lo + m)
+  while (m > 1) {
+    const int step = (m + 31) >> 5, at = lo + lane * step;
+    const bool below = lane * step < m && (int64_t)__ldg(cu + at) <= t0;
+    const int top = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+    lo += top * step;
+    m = min(step, m - top * step);
+  }
+  const int64_t t = min(t0 + lane, rows - 1);
+  const int at = lo + lane;
+  const int start = at <= ndoc ? __ldg(cu + at) : INT_MAX;
+  int n = 0;                                         // starts passed by row t
+  for (; n < 31; ++n)
+    if (!__any_sync(0xffffffffu, __shfl_sync(0xffffffffu, start, n + 1) <= (int)t)) break;
+  // at most n of the window's starts are passed: count this row's
+  int b = 0;
+  for (int j = 1; j <= n; ++j) b += __shfl_sync(0xffffffffu, start, j) <= (int)t;
+  Span32 d;
+  d.first = __shfl_sync(0xffffffffu, start, b);
+  d.last = __shfl_sync(0xffffffffu, start, min(b + 1, 31));
+  if (n == 31 && b == 31) {                          // more documents than the window holds
+    const int x = doc_of(cu, ndoc, t);
+    d.first = __ldg(cu + x);
+    d.last = __ldg(cu + x + 1);
+  }
+  return d;
 }
 
 // D = A B^T over columns [m HK, (m + 1) HK) of K-major 128-row tiles (128-byte
@@ -144,6 +183,15 @@ __device__ __forceinline__ S* smem_view(uint8_t* raw, WsHeader* hdr) {
 template <typename S>
 constexpr size_t smem_bytes() {
   return sizeof(S) + 1024 <= kSmemLimit ? sizeof(S) + 1024 : kSmemLimit;
+}
+
+// 2-D tiled store of one box from shared memory (rows past the map's end are
+// not written), tracked by the issuing thread's bulk groups.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(smem_src)), "r"(x), "r"(y)
+               : "memory");
 }
 
 // Launches a persistent kernel behind the one before it, with `smem` bytes of
