@@ -336,22 +336,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = p.scale * kLog2e;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     uint32_t it_count = 0, s_count = 0;
-    while (true) {
+    // An item's rows are found (a search of some 1400 cycles) while the item before
+    // it waits for its last product.
+    Item it;
+    Span32 doc = {0, 0};
+    auto next_item = [&](uint32_t n) {
+      if (!wait_warp(&sm.item_full[n & 1], (n >> 1) & 1, wc, hdr)) return false;
+      it = sm.items[n & 1];
+      mbar_arrive_warp(&sm.item_empty[n & 1], lane);
+      if (it.n_kv >= 0)
+        doc = document_of_rows(p.cu, p.ndoc, (int64_t)it.qtile * BM + wq * 32, p.q_len, lane);
+      return true;
+    };
+    if (!next_item(0)) it.n_kv = -1;
+    while (it.n_kv >= 0) {
       const uint32_t slot = it_count & 1;
-      if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
-      const Item it = sm.items[slot];
-      mbar_arrive_warp(&sm.item_empty[slot], lane);
-      if (it.n_kv < 0) break;
+      const int h = it.h;
       const int64_t row = (int64_t)it.qtile * BM + r;
       const bool valid = row < p.q_len;
       int lo = 0, hi = 0;                                      // visible keys [lo, hi)
       float lam = 0.f;
-      const Span32 doc =
-          document_of_rows(p.cu, p.ndoc, (int64_t)it.qtile * BM + wq * 32, p.q_len, lane);
       if (valid) {
         lo = doc.first;
         hi = p.causal ? (int)row + 1 : (int)min((int64_t)doc.last, p.kv_len);
-        lam = __bfloat162float(a.lambda[(int64_t)it.h * a.n_lambda + (a.n_lambda > 1 ? row : 0)]);
+        lam = __bfloat162float(a.lambda[(int64_t)h * a.n_lambda + (a.n_lambda > 1 ? row : 0)]);
       }
       float m = -INFINITY, l = 0.f;
       bool ok = true;
@@ -411,8 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // their row sums and take half of the columns of both accumulators each
       sm.inv[slot][m_][r] = l > 0.f ? 1.f / l : 0.f;
       if (valid && p.lse != nullptr)
-        p.lse[((int64_t)it.h * 2 + m_) * p.q_len + row] = (m + __log2f(l)) * kLn2;
+        p.lse[((int64_t)h * 2 + m_) * p.q_len + row] = (m + __log2f(l)) * kLn2;
       mbar_arrive_warp(&sm.inv_full, lane);
+      if (!next_item(it_count + 1)) break;
       if (!mbar_wait_warp(&sm.inv_full, it_count & 1, wc, hdr)) break;
       if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
       tc_fence_after();
