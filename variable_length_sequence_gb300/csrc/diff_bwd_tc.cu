@@ -749,29 +749,34 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const float sl2 = p.scale * kLog2e;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     uint32_t it_count = 0, jc = 0;
-    bool ok = true;
-    while (ok) {
-      const uint32_t slot = it_count & 1;
-      if (!mbar_wait_warp(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
-      const QItem it = sm.items[slot];
-      mbar_arrive_warp(&sm.item_empty[slot], lane);
-      if (it.n_kv < 0) break;
-      const int64_t row = (int64_t)it.qtile * 128 + r;
-      const bool valid = row < p.q_len;
-      int lo = 0, hi = 0;                                    // visible keys [lo, hi)
-      float nl[2] = {0.f, 0.f}, dl[2] = {0.f, 0.f}, c = 0.f;
-      const Span32 doc =
-          document_of_rows(p.cu, p.ndoc, (int64_t)it.qtile * 128 + wq * 32, p.q_len, lane);
-      if (valid) {
+    // the next item's row is found, and its vectors read, under the current item
+    QItem it;
+    int lo, hi;                                              // visible keys [lo, hi)
+    float nl[2], nd[2], c;
+    auto next_item = [&](uint32_t n) {
+      if (!wait_warp(&sm.item_full[n & 1], (n >> 1) & 1, wc, hdr)) return false;
+      it = sm.items[n & 1];
+      mbar_arrive_warp(&sm.item_empty[n & 1], lane);
+      lo = hi = 0;
+      nl[0] = nl[1] = nd[0] = nd[1] = c = 0.f;
+      if (it.n_kv < 0) return true;
+      const int64_t row0 = (int64_t)it.qtile * 128 + wq * 32, row = row0 + lane;
+      const Span32 doc = document_of_rows(p.cu, p.ndoc, row0, p.q_len, lane);
+      if (row < p.q_len) {
         lo = doc.first;
         hi = p.causal ? (int)row + 1 : (int)min((int64_t)doc.last, p.kv_len);
         const int64_t v1 = (int64_t)(2 * it.h) * a.Tp + row;
         nl[0] = __ldg(a.nlse2 + v1);
         nl[1] = __ldg(a.nlse2 + v1 + a.Tp);
-        dl[0] = __ldg(a.ndelta + v1);
-        dl[1] = __ldg(a.ndelta + v1 + a.Tp);
+        nd[0] = __ldg(a.ndelta + v1);
+        nd[1] = __ldg(a.ndelta + v1 + a.Tp);
         c = __ldg(a.coef + (int64_t)it.h * a.Tp + row);
       }
+      return true;
+    };
+    if (!next_item(0)) it.n_kv = -1;
+    bool ok = true;
+    while (it.n_kv >= 0) {
       for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
         const int key0 = (it.j_lo + jj) * 128 + wg * 64;
         const bool full_w = __all_sync(0xffffffffu, lo <= key0 && key0 + 64 <= hi);
@@ -807,7 +812,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
           // dS over the S columns this warp has read; the second map's factor c
           // is taken in with dP - delta: c dP - c delta
-          const float f = m == 0 ? 1.f : c, g = f * dl[m];
+          const float f = m == 0 ? 1.f : c, g = f * nd[m];
           const uint64_t f2 = f2_pack(f, f), g2 = f2_pack(g, g);
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
@@ -841,9 +846,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
       }
       if (!ok) break;
       // epilogue: map wg of the row's gradient
+      const int64_t row = (int64_t)it.qtile * 128 + r;
+      __nv_bfloat16* const dst = a.dq + (row * p.Hq + it.h) * D + wg * (D / 2);
+      if (!next_item(it_count + 1)) break;
       if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
       tc_fence_after();
-      __nv_bfloat16* dst = a.dq + (row * p.Hq + it.h) * D + wg * (D / 2);
 #pragma unroll
       for (int cc = 0; cc < D / 64; ++cc) {
         uint32_t v[32];
@@ -853,7 +860,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           tc_fence_before();
           mbar_arrive_warp(&sm.o_free, lane);
         }
-        if (valid) store_row32(dst + cc * 32, v, p.scale);
+        if (row < p.q_len) store_row32(dst + cc * 32, v, p.scale);
       }
       ++it_count;
     }
