@@ -47,7 +47,7 @@ using namespace tc;
 struct BwdArgs {
   AttnProblem p;
   const float *nlse2, *ndelta;      // [2 Hq][Tp]
-  const float* coef;                // [Hq][Tp]
+  const float *coef, *cndelta;      // [Hq][Tp]: c, -c delta_2
   int64_t Tp;
   __nv_bfloat16 *dq, *dk, *dv;
   const int2* qtiles;               // per 128-row query tile: first/last 128-key tile
@@ -75,7 +75,7 @@ struct __align__(1024) SmemKV {
   uint8_t qd[4][kTile];
   uint8_t ds[kTile];                         // dS_1^T, [q-block][key][64 q], 128-byte swizzle
   float first[2][128];                       // map 1: -lse log2 e, -delta
-  float second[3][128];                      // map 2: -lse log2 e, -delta, c
+  float second[3][128];                      // map 2: -lse log2 e, -c delta, c
   uint64_t kv_full, kv_empty;
   uint64_t slot_full[4], slot_empty[4];
   uint64_t first_full, second_full;
@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           if (n2 >= 1 && !mbar_wait(&sm.p_ready, (n2 - 1) & 1, wc, hdr)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.second_full, 3 * 512);
           bulk_load(sm.second[0], a.nlse2 + r2, 512, &sm.second_full);
-          bulk_load(sm.second[1], a.ndelta + r2, 512, &sm.second_full);
-          bulk_load(sm.second[2], a.coef + (int64_t)h * a.Tp + (int64_t)i * 128, 512,
-                    &sm.second_full);
+          const int64_t rc = (int64_t)h * a.Tp + (int64_t)i * 128;
+          bulk_load(sm.second[1], a.cndelta + rc, 512, &sm.second_full);
+          bulk_load(sm.second[2], a.coef + rc, 512, &sm.second_full);
           ++n2;
           if (++i == it.i_lo + it.n_q) { i = it.i_lo; ++h; }
         }
@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     // dS^T tile: query block cg / 2, 16-byte chunks 4 (cg & 1) + j, swizzled
     // by key & 7 (= tr for every fragment row)
-    const uint32_t ds_base = smem_u32(sm.ds) + (cg >> 1) * kBlk + (wq * 32 + tr) * 128 + 2 * tc2;
+    const uint32_t ds_base = smem_u32(sm.ds) + (cg >> 1) * kBlk + (wq * 32 + tr) * 128 +
+                             ((((cg & 1) * 4) ^ tr) << 4) + 2 * tc2;
     const float* const vec1 = sm.first[0] + cg * 32 + tc2;
     const float* const vec2 = sm.second[0] + cg * 32 + tc2;
     uint32_t it_count = 0, items_done = 0, qc = 0;
@@ -385,6 +386,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           qhi[i] = (int)min((int64_t)__ldg(p.cu + b + 1), p.q_len);
         }
       }
+      // queries that see every row of the thread
+      const int all_lo = max(max(qlo[0], qlo[1]), max(qlo[2], qlo[3]));
+      const int all_hi = min(min(qhi[0], qhi[1]), min(qhi[2], qhi[3]));
       int n_in = 0;                                        // query tile of the pair, 0 .. n_q - 1
       for (int n = 0; n < it.pairs; ++n) {
         const int q0 = (it.i_lo + n_in) * 128 + cg * 32;
@@ -392,10 +396,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const uint32_t rb = qc & 1;
         const uint32_t s_tm = tmem + lane_base + 128 * rb + cg * 32;
         const uint32_t dp_tm = tmem + lane_base + 128 * (rb ^ 1) + cg * 32;
-        bool full = true;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) full = full && qlo[i] <= q0 && q0 + 32 <= qhi[i];
-        const bool full_w = __all_sync(0xffffffffu, full);
+        const bool full_w = __all_sync(0xffffffffu, all_lo <= q0 && q0 + 32 <= all_hi);
         // ---- first map: P_1 (kept for the second) and dS_1
         if (!wait_warp(&sm.first_full, qc & 1, wc, hdr)) { ok = false; break; }
         if (!wait_warp(&sm.s1_full, qc & 1, wc, hdr)) { ok = false; break; }
@@ -446,8 +447,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                                  qhi[2 * h + 1] - q0, tc2);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const int chunk = (cg & 1) * 4 + (kk >> 1);      // 8 query columns per 16 bytes
-            st_shared_u32(ds_base + (16 * h + 8 * (kk & 1)) * 128 + ((chunk ^ tr) << 4), ds[kk]);
+            // (8 query columns per 16 bytes; j is two bits of the chunk number)
+            st_shared_u32((ds_base ^ ((kk >> 1) << 4)) + (16 * h + 8 * (kk & 1)) * 128, ds[kk]);
           }
         }
         fence_proxy_async_smem();
@@ -477,11 +478,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
               float u0, u1;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * kk]), __uint_as_float(x[2 * kk + 1])),
                                sl2x2, nl), u0, u1);
-              const uint64_t p2 = f2_mul(f2_pack(ex2(u0), ex2(u1)), cc);
-              f2_unpack(f2_add(pp[8 * h + kk], p2), u0, u1);
+              const uint64_t p2 = f2_pack(ex2(u0), ex2(u1));
+              f2_unpack(f2_fma(p2, cc, pp[8 * h + kk]), u0, u1);
               pk[kk] = pack_bf16x2(u0, u1);
-              f2_unpack(f2_mul(p2, f2_add(f2_pack(__uint_as_float(y[2 * kk]),
-                                                  __uint_as_float(y[2 * kk + 1])), nd)), u0, u1);
+              f2_unpack(f2_mul(p2, f2_fma(f2_pack(__uint_as_float(y[2 * kk]),
+                                                  __uint_as_float(y[2 * kk + 1])), cc, nd)), u0, u1);
               ds[kk] = pack_bf16x2(u0, u1);
             }
           }
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
         nl[0] = __ldg(a.nlse2 + v1);
         nl[1] = __ldg(a.nlse2 + v1 + a.Tp);
         nd[0] = __ldg(a.ndelta + v1);
-        nd[1] = __ldg(a.ndelta + v1 + a.Tp);
+        nd[1] = __ldg(a.cndelta + (int64_t)it.h * a.Tp + row);
         c = __ldg(a.coef + (int64_t)it.h * a.Tp + row);
       }
       return true;
@@ -812,7 +813,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           }
           // dS over the S columns this warp has read; the second map's factor c
           // is taken in with dP - delta: c dP - c delta
-          const float f = m == 0 ? 1.f : c, g = f * nd[m];
+          const float f = m == 0 ? 1.f : c, g = nd[m];
           const uint64_t f2 = f2_pack(f, f), g2 = f2_pack(g, g);
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
@@ -896,7 +897,7 @@ cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char*
     return cudaErrorNotSupported;
   BwdArgs a;
   a.p = p;
-  a.nlse2 = d.nlse2; a.ndelta = d.ndelta; a.coef = d.coef; a.Tp = d.Tp;
+  a.nlse2 = d.nlse2; a.ndelta = d.ndelta; a.coef = d.coef; a.cndelta = d.cndelta; a.Tp = d.Tp;
   a.dq = reinterpret_cast<__nv_bfloat16*>(d.dq);
   a.dk = reinterpret_cast<__nv_bfloat16*>(d.dk);
   a.dv = reinterpret_cast<__nv_bfloat16*>(d.dv);

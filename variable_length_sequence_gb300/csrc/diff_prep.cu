@@ -5,8 +5,8 @@
 // O_2 saved by the forward:
 //   delta_2 = <dout, out2>,  delta_1 = <dout, out> + lambda delta_2,
 //   dlambda = -delta_2 (of each token), or its sum over the tokens.
-// Written as [2 Hq][Tp] rows (-delta, -lse log2 e) and [Hq][Tp] (-lambda, the
-// factor of the second map's probabilities), padded with zeros to whole
+// Written as [2 Hq][Tp] rows (-delta, -lse log2 e) and [Hq][Tp] (c = -lambda, the
+// factor of the second map's probabilities, and -c delta_2), padded with zeros to whole
 // 128-row tiles.  Bound: HBM, one read of out, out2 and dout.
 #include <algorithm>
 
@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
       a.nlse2[v1] = -kLog2e * __ldg(p.lse + (int64_t)h * 2 * T_ + t);
       a.nlse2[v2] = -kLog2e * __ldg(p.lse + ((int64_t)h * 2 + 1) * T_ + t);
       a.coef[(int64_t)h * a.Tp + t] = -lam;
+      a.cndelta[(int64_t)h * a.Tp + t] = lam * d2;
       if (a.n_lambda > 1) st_out(reinterpret_cast<T*>(a.dlambda) + (int64_t)h * T_ + t, -d2);
     }
   }
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
     const int64_t h = e / pad, t = T_ + (e - h * pad);
     a.ndelta[h * 2 * a.Tp + t] = a.ndelta[(h * 2 + 1) * a.Tp + t] = 0.f;
     a.nlse2[h * 2 * a.Tp + t] = a.nlse2[(h * 2 + 1) * a.Tp + t] = 0.f;
-    a.coef[h * a.Tp + t] = 0.f;
+    a.coef[h * a.Tp + t] = a.cndelta[h * a.Tp + t] = 0.f;
   }
 }
 

@@ -68,7 +68,8 @@ struct DiffProblem {
   void* out2;                        // second map's output (forward: may be null)
   const void *fout, *dout;           // backward
   void *dq, *dk, *dv, *dlambda;
-  float *ndelta, *nlse2, *coef;      // backward workspace: [2 Hq][Tp], [2 Hq][Tp], [Hq][Tp]
+  float *ndelta, *nlse2;             // backward workspace: [2 Hq][Tp]
+  float *coef, *cndelta;             // [Hq][Tp]
   int64_t Tp;
   float *dk_heads, *dv_heads;        // float32 backward, Hq > Hkv: [T, Hq, d] shares of the heads
 };
@@ -79,7 +80,7 @@ bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols)
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s);
 cudaError_t launch_diff_bwd_tc(const DiffProblem& a, const BwdWsLayout& L, char* ws, cudaStream_t s);
 cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s);
-// ndelta, nlse2 and coef of the backward, and dlambda of each token
+// ndelta, nlse2, coef and cndelta of the backward, and dlambda of each token
 cudaError_t launch_diff_prep(const DiffProblem& a, cudaStream_t s);
 // dlambda of each head (n_lambda = 1), from ndelta
 cudaError_t launch_diff_dlambda(const DiffProblem& a, cudaStream_t s);

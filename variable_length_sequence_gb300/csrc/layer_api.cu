@@ -289,7 +289,7 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
 }
 
 // Backward workspace: the attention backward's layout for 2 Hq rows of -delta
-// and -lse log2 e, then -lambda [Hq, Tp], and for float32 with grouped heads each
+// and -lse log2 e, then -lambda and lambda delta_2 [Hq, Tp], and for float32 with grouped heads each
 // query head's share of dk and dv.
 struct DiffBwdLayout {
   BwdWsLayout attn;
@@ -300,7 +300,7 @@ static DiffBwdLayout diff_bwd_layout(int64_t T, int32_t Hq, int32_t Hkv, int32_t
   DiffBwdLayout L;
   L.attn = bwd_ws_layout(T, T, 2 * Hq, d, false);
   L.coef = L.attn.total;
-  L.heads = align_up(L.coef + sizeof(float) * (size_t)Hq * (size_t)L.attn.Tp, 256);
+  L.heads = align_up(L.coef + 2 * sizeof(float) * (size_t)Hq * (size_t)L.attn.Tp, 256);
   const bool shares = io_dtype == NSP_F32 && Hq > Hkv;
   L.total = L.heads + (shares ? 2 * sizeof(float) * (size_t)T * (size_t)Hq * (size_t)d : 0);
   return L;
@@ -343,6 +343,7 @@ int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const voi
   a.ndelta = reinterpret_cast<float*>(ws + L.delta);
   a.nlse2 = reinterpret_cast<float*>(ws + L.nlse2);
   a.coef = reinterpret_cast<float*>(ws + W.coef);
+  a.cndelta = a.coef + (size_t)Hq * (size_t)L.Tp;
   a.dk_heads = reinterpret_cast<float*>(ws + W.heads);
   a.dv_heads = a.dk_heads + (size_t)T * (size_t)Hq * (size_t)d;
   a.Tp = L.Tp;
