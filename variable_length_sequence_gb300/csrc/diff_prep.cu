@@ -18,66 +18,81 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A warp takes kTokens consecutive tokens of one head (its warps the next heads'),
+// so that the values it writes are neighbours.
+template <typename T, int D>
+struct PrepShape {
+  static constexpr int TPR = D / Vec<T>::N;                       // threads of a row
+  static constexpr int RPW = 32 / TPR;                            // rows of a warp at once
+  static constexpr int ROWS = 4;                                  // rows of a thread in flight
+  static constexpr int kTokens = RPW * ROWS;
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a) {
   constexpr int N = Vec<T>::N;
-  constexpr int TPR = D / N;                       // threads of a row
-  constexpr int RPW = 32 / TPR;                    // rows of a warp
-  constexpr int ROWS = 4;                          // rows of a thread in flight
+  using S = PrepShape<T, D>;
   const AttnProblem& p = a.p;
   grid_dep_trigger();
   if (status_bad(p.hdr)) return;
-  const int lane = threadIdx.x & 31, sub = lane / TPR, part = lane % TPR;
+  const int lane = threadIdx.x & 31, sub = lane / S::TPR, part = lane % S::TPR;
   const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
-  const int64_t T_ = p.q_len, rows = T_ * p.Hq;
+  const int64_t T_ = p.q_len, units = (T_ + S::kTokens - 1) / S::kTokens * p.Hq;
   const T* O = reinterpret_cast<const T*>(a.fout);
   const T* O2 = reinterpret_cast<const T*>(a.out2);
   const T* G = reinterpret_cast<const T*>(a.dout);
   const T* L = reinterpret_cast<const T*>(a.lambda);
-  for (int64_t r0 = warp * RPW * ROWS; r0 < rows; r0 += nwarps * RPW * ROWS) {
-    uint4 x[ROWS], y[ROWS], z[ROWS];
+  for (int64_t u = warp; u < units; u += nwarps) {
+    const int64_t chunk = u / p.Hq, t0 = chunk * S::kTokens;
+    const int h = (int)(u - chunk * p.Hq);
+    uint4 x[S::ROWS], y[S::ROWS], z[S::ROWS];
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      const int64_t r = r0 + k * RPW + sub, off = r * D + part * N;
+    for (int k = 0; k < S::ROWS; ++k) {
+      const int64_t t = t0 + k * S::RPW + sub, off = (t * p.Hq + h) * D + part * N;
       x[k] = y[k] = z[k] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
+      if (t < T_) {
         x[k] = ld_once(O + off);
         y[k] = ld_once(O2 + off);
         z[k] = ld_once(G + off);
       }
     }
+    float m0 = 0.f, m2 = 0.f;                      // of token t0 + lane (lanes below kTokens)
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      float u[N], v[N], g[N];
-      Vec<T>::unpack(x[k], u);
-      Vec<T>::unpack(y[k], v);
+    for (int k = 0; k < S::ROWS; ++k) {
+      float v[N], w[N], g[N];
+      Vec<T>::unpack(x[k], v);
+      Vec<T>::unpack(y[k], w);
       Vec<T>::unpack(z[k], g);
       float d0 = 0.f, d2 = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        d0 = fmaf(g[i], u[i], d0);
-        d2 = fmaf(g[i], v[i], d2);
+        d0 = fmaf(g[i], v[i], d0);
+        d2 = fmaf(g[i], w[i], d2);
       }
 #pragma unroll
-      for (int o = TPR / 2; o > 0; o >>= 1) {
+      for (int o = S::TPR / 2; o > 0; o >>= 1) {
         d0 += __shfl_xor_sync(0xffffffffu, d0, o);
         d2 += __shfl_xor_sync(0xffffffffu, d2, o);
       }
-      const int64_t r = r0 + k * RPW + sub;
-      if (r >= rows || part != 0) continue;
-      const int64_t t = r / p.Hq;
-      const int h = (int)(r - t * p.Hq);
-      const float lam = to_f(L[(int64_t)h * a.n_lambda + (a.n_lambda > 1 ? t : 0)]);
-      const int64_t v1 = (int64_t)h * 2 * a.Tp + t, v2 = v1 + a.Tp;
-      a.ndelta[v1] = -fmaf(lam, d2, d0);
-      a.ndelta[v2] = -d2;
-      a.nlse2[v1] = -kLog2e * __ldg(p.lse + (int64_t)h * 2 * T_ + t);
-      a.nlse2[v2] = -kLog2e * __ldg(p.lse + ((int64_t)h * 2 + 1) * T_ + t);
-      a.coef[(int64_t)h * a.Tp + t] = -lam;
-      a.cndelta[(int64_t)h * a.Tp + t] = lam * d2;
-      if (a.n_lambda > 1) st_out(reinterpret_cast<T*>(a.dlambda) + (int64_t)h * T_ + t, -d2);
+      d0 = __shfl_sync(0xffffffffu, d0, (lane % S::RPW) * S::TPR);
+      d2 = __shfl_sync(0xffffffffu, d2, (lane % S::RPW) * S::TPR);
+      if (lane / S::RPW == k) {
+        m0 = d0;
+        m2 = d2;
+      }
     }
+    const int64_t t = t0 + lane;
+    if (lane >= S::kTokens || t >= T_) continue;
+    const float lam = to_f(L[(int64_t)h * a.n_lambda + (a.n_lambda > 1 ? t : 0)]);
+    const int64_t v1 = (int64_t)h * 2 * a.Tp + t, v2 = v1 + a.Tp, vc = (int64_t)h * a.Tp + t;
+    a.ndelta[v1] = -fmaf(lam, m2, m0);
+    a.ndelta[v2] = -m2;
+    a.nlse2[v1] = -kLog2e * __ldg(p.lse + (int64_t)h * 2 * T_ + t);
+    a.nlse2[v2] = -kLog2e * __ldg(p.lse + ((int64_t)h * 2 + 1) * T_ + t);
+    a.coef[vc] = -lam;
+    a.cndelta[vc] = lam * m2;
+    if (a.n_lambda > 1) st_out(reinterpret_cast<T*>(a.dlambda) + (int64_t)h * T_ + t, -m2);
   }
   // zero padding of the last tile's rows
   const int pad = (int)(a.Tp - T_);
@@ -111,16 +126,18 @@ __global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restr
   if (threadIdx.x == 0) st_out(dlambda + blockIdx.x, x);
 }
 
-template <typename T>
-cudaError_t prep(const DiffProblem& a, cudaStream_t s) {
-  const int64_t blocks = std::min<int64_t>(
-      ceil_div(a.p.q_len * a.p.Hq, kThreads / (a.p.d / Vec<T>::N) * 4), (int64_t)num_sms() * 8);
-  if (a.p.d == 128)
-    diff_prep_kernel<T, 128><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-  else
-    diff_prep_kernel<T, 64><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+template <typename T, int D>
+cudaError_t prep_d(const DiffProblem& a, cudaStream_t s) {
+  const int64_t units = ceil_div(a.p.q_len, PrepShape<T, D>::kTokens) * a.p.Hq;
+  const int64_t blocks = std::min<int64_t>(ceil_div(units, kThreads / 32), (int64_t)num_sms() * 8);
+  diff_prep_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t prep(const DiffProblem& a, cudaStream_t s) {
+  return a.p.d == 128 ? prep_d<T, 128>(a, s) : prep_d<T, 64>(a, s);
 }
 
 template <typename T>

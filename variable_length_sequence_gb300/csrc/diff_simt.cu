@@ -14,7 +14,8 @@
 // registers over 256 threads (16 x 16; 4 x 4 results of a thread and 8 FMAs for
 // each 16-byte read: 2 x 2 with 4 took twice as long) from float32 tiles in
 // shared memory, rows padded by 4 floats so that 16 rows read at one column fall
-// into different banks.  Forward: 64 query rows by 64 keys; both maps' scores,
+// into different banks.  Forward: 64 query rows by 32 keys (64 keys leave
+// room for fewer blocks: 850 us against 611); both maps' scores,
 // online softmax (Milakov and Gimelshein) and outputs stay in the registers of
 // one thread row.  Backward: one kernel over key tiles and query heads (dK, dV of
 // the head; a small kernel sums a group's heads), one over query tiles (dQ),
@@ -73,7 +74,7 @@ __device__ __forceinline__ float lambda_of(const DiffProblem& a, int h, int64_t 
 
 // ---------------------------------------------------------------- forward
 
-constexpr int kFwdM = 64, kFwdN = 64, kFwdKeys = kFwdN / 16;    // keys of a thread: tx + 16 j
+constexpr int kFwdM = 64, kFwdN = 32, kFwdKeys = kFwdN / 16;    // keys of a thread: tx + 16 j
 
 template <int D>
 struct FwdSmem {
@@ -237,16 +238,15 @@ struct BwdSmem {
   float q[kBwdTile][D + 4], dout[kBwdTile][D + 4];
   float k[kBwdTile][D + 4], v[kBwdTile][D + 4];
   float ds[2][kBwdTile][kBwdTile + 4];            // [map][row of the output][summed index]
-  float pc[kBwdTile][kBwdTile + 4];               // (P_1 - lambda P_2)^T: [key][query]
   float nlse2[2][kBwdTile], ndelta[2][kBwdTile], coef[kBwdTile];
   int lo[kBwdTile], hi[kBwdTile];
 };
 
-// P and dS of a tile, written for the product that follows: KEY puts dS and
-// P_1 - lambda P_2 in rows of keys (dK, dV), otherwise dS in rows of queries
-// (dQ).  Threads take rows 4 ty + i and keys tx + 16 j.
+// dS of a tile, written for the product that follows: KEY puts it in rows of
+// keys (dK), otherwise in rows of queries (dQ); pc: P_1 - lambda P_2 of the thread's
+// rows 4 ty + i and keys tx + 16 j.
 template <int D, bool KEY>
-__device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2) {
+__device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2, float4 (&pc)[4]) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   float s[2][4][4] = {}, dp[4][4] = {};
 #pragma unroll
@@ -274,7 +274,7 @@ __device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2)
   for (int j = 0; j < 4; ++j) {
     const int kk = tx + 16 * j;
     const int64_t key = key0 + kk;
-    float d1[4], d2[4], pc[4];
+    float d1[4], d2[4], pr[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
@@ -283,7 +283,7 @@ __device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2)
       const float p2 = vis ? sm.coef[r] * exp2f(fmaf(s[1][i][j], sl2, sm.nlse2[1][r])) : 0.f;
       d1[i] = vis ? p1 * (dp[i][j] + sm.ndelta[0][r]) : 0.f;
       d2[i] = vis ? p2 * (dp[i][j] + sm.ndelta[1][r]) : 0.f;
-      pc[i] = p1 + p2;
+      pr[i] = p1 + p2;
       if constexpr (!KEY) {
         sm.ds[0][r][kk] = d1[i];
         sm.ds[1][r][kk] = d2[i];
@@ -292,7 +292,7 @@ __device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2)
     if constexpr (KEY) {
       st4(&sm.ds[0][kk][ty * 4], make_float4(d1[0], d1[1], d1[2], d1[3]));
       st4(&sm.ds[1][kk][ty * 4], make_float4(d2[0], d2[1], d2[2], d2[3]));
-      st4(&sm.pc[kk][ty * 4], make_float4(pc[0], pc[1], pc[2], pc[3]));
+      pc[j] = make_float4(pr[0], pr[1], pr[2], pr[3]);
     }
   }
 }
@@ -343,7 +343,7 @@ __device__ __forceinline__ void load_rows(BwdSmem<D>& sm, const DiffProblem& a, 
 // heads by diff_group_sum_kernel (one block a head, so that few key tiles still
 // fill the GPU), or written at once when the group is one head.
 template <int D>
-__global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const DiffProblem a) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) diff_bwd_dkdv_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
   const AttnProblem& p = a.p;
@@ -365,10 +365,16 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dkdv_simt_kernel(const Diff
     load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, r0, T);
     load_rows<D>(sm, a, h, r0);
     __syncthreads();
-    tile_ds<D, true>(sm, key0, p.scale * kLog2e);
+    float4 pc[4];
+    tile_ds<D, true>(sm, key0, p.scale * kLog2e, pc);
     __syncthreads();
     tile_product<D>(dk, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.q);
-    tile_product<D>(dv, [&](int) { return &sm.pc[0][0]; }, sm.dout);
+    __syncthreads();
+    // P over dS (a buffer of its own would leave room for one block of an SM only)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) st4(&sm.ds[0][tx + 16 * j][ty * 4], pc[j]);
+    __syncthreads();
+    tile_product<D>(dv, [&](int) { return &sm.ds[0][0][0]; }, sm.dout);
   }
   float* const DK = G > 1 ? a.dk_heads : reinterpret_cast<float*>(a.dk);
   float* const DV = G > 1 ? a.dv_heads : reinterpret_cast<float*>(a.dv);
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) diff_group_sum_kernel(const DiffProb
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffProblem a) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) diff_bwd_dq_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
   const AttnProblem& p = a.p;
@@ -424,7 +430,8 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_dq_simt_kernel(const DiffPr
     load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, j0, T);
     load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const float*>(p.v) + (int64_t)g * D, ks, j0, T);
     __syncthreads();
-    tile_ds<D, false>(sm, j0, p.scale * kLog2e);
+    float4 pc[4];
+    tile_ds<D, false>(sm, j0, p.scale * kLog2e, pc);
     __syncthreads();
     tile_product<D>(dq, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.k);
   }
