@@ -666,7 +666,8 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
  *   dv = sum_t (p^1_t - lambda p^2_t) dout_t  (dk, dv over the group's heads),
  *   dlambda = -delta^2 of each token, or its sum over the tokens.
  * Every output is written whole, and sums run in one fixed order: results are
- * the same bits on every run. */
+ * the same bits on every run.  A non-finite value in one document's q, k or
+ * dout may reach rows of documents that share a 128-token tile with it. */
 size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t d,
                                         int32_t io_dtype);
 

@@ -448,6 +448,138 @@ def test_diff_attention_guard_zones(nsp, dt):
         check(buf, n)
 
 
+def test_diff_attention_grids(nsp, monkeypatch):
+    """1, 7 and 152 persistent blocks: the same bits (each item is computed whole
+    by one block, each sum has one order)."""
+    q, k, v, lam, do, cu = diff_inputs(130, [300, 1, 0, 77, 129, 500], 4, 2, 128, BF16, True)
+
+    def step():
+        out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+        return (out, out2, lse) + nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+
+    monkeypatch.setenv("NSP_PERSISTENT_CTAS", "152")
+    want = step()
+    for n in ("1", "7"):
+        monkeypatch.setenv("NSP_PERSISTENT_CTAS", n)
+        for a, b in zip(want, step()):
+            assert torch.equal(a, b)
+
+
+def test_diff_attention_many_documents(nsp):
+    """More documents than one look of the document search (32 starts a warp,
+    empty ones among them) against one document at a time."""
+    rng = np.random.default_rng(7)
+    lens = [int(n) for n in rng.choice([0, 0, 1, 1, 2, 3, 40], size=700)]
+    q, k, v, lam, do, cu = diff_inputs(140, lens, 2, 1, 64, BF16, False)
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    dq, dk, dv, _ = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+    ref, tol = diff_bounds(*(f64(t) for t in (q, k, v, lam, do)), cu.cpu().numpy(), 32 ** -0.5, True, BF16)
+    for name, a, i in (("out", out, 0), ("out2", out2, 1), ("lse", lse, 2), ("dq", dq, 3), ("dk", dk, 4),
+                       ("dv", dv, 5)):
+        assert_within(a, ref[i], tol[i], name)
+
+
+def test_diff_attention_masked_neighbours(nsp):
+    """Infinite and NaN keys of one document leave its neighbours in the tile as
+    they are (scores outside a row's document are dropped, not multiplied)."""
+    lens = [50, 30, 60]
+    q, k, v, lam, do, cu = diff_inputs(150, lens, 2, 1, 128, BF16, False)
+    want = nsp.diff_attn_fwd(q, k, v, lam, cu)
+    k[50:65] = float("nan")
+    k[65:80] = float("inf")
+    got = nsp.diff_attn_fwd(q, k, v, lam, cu)
+    assert torch.equal(got[:50], want[:50]) and torch.equal(got[80:], want[80:])
+    assert torch.isnan(got[50:80]).any()
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_diff_attention_timeout(nsp, backward):
+    """A wait that runs out is recorded, the context stays usable and the same
+    workspace works again."""
+    lens = [700, 300]
+    q, k, v, lam, do, cu = diff_inputs(160, lens, 8, 2, 128, BF16, False)
+    T, lib = sum(lens), nsp.load()
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    n = (lib.nsp_diff_attn_bwd_workspace_size(T, 8, 2, 128, nsp.NSP_BF16) if backward
+         else lib.nsp_diff_attn_fwd_workspace_size(T))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def call():
+        if backward:
+            return nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu, workspace=ws)
+        return nsp.diff_attn_fwd(q, k, v, lam, cu, save=True, workspace=ws)
+
+    want = call()
+    torch.cuda.synchronize()
+    old = nsp.nsp_set_wait_timeout_cycles(100)
+    try:
+        call()
+        assert nsp.nsp_status_query(ws) == nsp.NSP_ERR_TIMEOUT
+    finally:
+        nsp.nsp_set_wait_timeout_cycles(old)
+    got = call()
+    assert nsp.nsp_status_query(ws) == nsp.NSP_OK
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_two_streams_at_once(nsp):
+    """Two steps in flight at the same time on their own workspaces."""
+    ins = [diff_inputs(170 + 10 * i, [900, 33, 600], 4, 2, 128, BF16, False) for i in range(2)]
+
+    def step(x):
+        q, k, v, lam, do, cu = x
+        out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+        return (out, nsp.head_norm(out)) + nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+
+    want = [step(x) for x in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(ins[i])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits(nsp):
+    """More than 2^31 elements in q: the last documents equal the same documents
+    alone (they start on a tile's edge, so the same tiles are summed)."""
+    d, hq, n = 128, 256, 66048                        # 2.16e9 elements
+    tail = 256
+    q = torch.empty((n, hq, d), dtype=BF16, device="cuda")
+    q[:n - tail] = 0.5
+    q[n - tail:] = randn(180, tail, hq, d)
+    cu = torch.arange(0, n + 1, 64, dtype=torch.int32, device="cuda")
+    cu2 = torch.arange(0, tail + 1, 64, dtype=torch.int32, device="cuda")
+    qt = q[n - tail:].clone()
+    assert q.numel() > 2 ** 31
+    fr = nsp.rope_freqs(d, device="cuda")
+    r, _ = nsp.rope(q, None, cu, fr)
+    assert torch.equal(r[n - tail:], nsp.rope(qt, None, cu2, fr)[0])
+    del r
+    y = nsp.head_norm(q)
+    assert torch.equal(y[n - tail:], nsp.head_norm(qt))
+    del y
+    k = randn(181, n, 1, d)
+    v = randn(182, n, 1, d)
+    lam = torch.full((hq, 1), 0.5, dtype=BF16, device="cuda")
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    o, o2, l = nsp.diff_attn_fwd(qt, k[n - tail:].contiguous(), v[n - tail:].contiguous(), lam, cu2, save=True)
+    assert torch.equal(out[n - tail:], o) and torch.equal(out2[n - tail:], o2)
+    assert torch.equal(lse[:, :, n - tail:], l)
+    dq, dk, dv, _ = nsp.diff_attn_bwd(q, k, v, lam, out, out2, q, lse, cu)
+    eq, ek, ev, _ = nsp.diff_attn_bwd(qt, k[n - tail:].contiguous(), v[n - tail:].contiguous(), lam, o, o2,
+                                      qt, l, cu2)
+    assert torch.equal(dq[n - tail:], eq) and torch.equal(dk[n - tail:], ek) and torch.equal(dv[n - tail:], ev)
+    dx, _, _ = nsp.head_norm_bwd(q, dq)
+    assert torch.equal(dx[n - tail:], nsp.head_norm_bwd(qt, eq)[0])
+
+
 # ----------------------------------------------------------------------------- together
 
 def layer_forward(nsp, x, cu, fr):
