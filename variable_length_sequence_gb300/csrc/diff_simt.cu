@@ -10,17 +10,22 @@
 //   dS_1 = P_1 (dP - delta_1),  dS_2 = -lambda P_2 (dP - delta_2),
 //   dQ_m = scale dS_m K_m,  dK_m = scale dS_m^T Q_m,  dV = (P_1 - lambda P_2)^T dout.
 //
-// Bound: shared-memory reads beside the FP32 pipes.  Every product is tiled in
-// registers over 256 threads (16 x 16; 4 x 4 results of a thread and 8 FMAs for
-// each 16-byte read: 2 x 2 with 4 took twice as long) from float32 tiles in
-// shared memory, rows padded by 4 floats so that 16 rows read at one column fall
-// into different banks.  Forward: 64 query rows by 32 keys (64 keys leave
-// room for fewer blocks: 850 us against 611); both maps' scores,
-// online softmax (Milakov and Gimelshein) and outputs stay in the registers of
-// one thread row.  Backward: one kernel over key tiles and query heads (dK, dV of
-// the head; a small kernel sums a group's heads), one over query tiles (dQ),
-// each recomputing both maps' P and dP, so every gradient is summed in one
-// fixed order without atomics.
+// Bound: the 128 bytes a clock that shared memory fills registers with (a
+// 16-byte read costs a warp 4 clocks of it, broadcast or not) beside the FP32
+// pipes (a warp's FMA costs 1/4).  Every product is tiled in registers, 16
+// threads wide, from float32 tiles in shared memory, rows padded by 4 floats so
+// that 16 rows read at one column fall into different banks; a thread's 8 rows by
+// 4 keys take 12 reads for 128 FMAs (8 x 4 x d = 64; 4 x 4, 8 for 64, took 625 us
+// forward and 1707 back against 570 and 1415 at 3001 tokens, 6 heads, d = 64,
+// bidirectional).  At d = 128 registers or shared memory leave room for less:
+// 8 x 2 forward (1165 us against 1293 at 3001 tokens, 8 heads, causal documents),
+// 4 x 4 with twice the threads back (2530 us; 8 x 4 spills: 3112).  Asynchronous
+// copies fill the buffer that a product has done with while the next one runs.
+// Forward: both maps' scores, online softmax (Milakov and Gimelshein) and outputs
+// stay in the registers of one thread row, 36 TFLOP/s.  Backward: one kernel over
+// key tiles and query heads (dK, dV of the head; a small kernel sums a group's
+// heads), one over query tiles (dQ), each recomputing both maps' P and dP, so
+// every gradient is summed in one fixed order without atomics; 34 TFLOP/s.
 #include "layer.cuh"
 
 namespace nsp {
@@ -28,7 +33,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;             // forward: 8 rows of 16 threads, and the group sum's
+constexpr int kRows = 8;                  // forward: rows 8 ty + i of a thread
 
 __device__ __forceinline__ float4 fma4(float s, const float4& x, const float4& y) {
   return make_float4(fmaf(s, x.x, y.x), fmaf(s, x.y, y.y), fmaf(s, x.z, y.z), fmaf(s, x.w, y.w));
@@ -47,18 +53,22 @@ __device__ __forceinline__ void st4(float* p, const float4& x) {
   *reinterpret_cast<float4*>(p) = x;
 }
 
-// ROWS rows of one head (row stride `stride` elements) into padded shared
-// rows; rows at or past `end` read as zero.
-template <int D, int ROWS>
+// ROWS rows of one head (row stride `stride` elements) into padded shared rows,
+// by asynchronous copies that the caller waits for; rows at or past `end` read as
+// zero.
+template <int D, int ROWS, int THREADS>
 __device__ __forceinline__ void load_tile(float (*dst)[D + 4], const float* src, int64_t stride,
                                           int64_t row0, int64_t end) {
-  for (int e = threadIdx.x; e < ROWS * (D / 4); e += kThreads) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += THREADS) {
     const int r = e / (D / 4), c = (e % (D / 4)) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row0 + r < end) x = ld4(src + (row0 + r) * stride + c);
-    *reinterpret_cast<float4*>(&dst[r][c]) = x;
+    const bool in = row0 + r < end;
+    const float* from = src + (in ? row0 + r : 0) * stride + c;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(&dst[r][c]);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
   }
 }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Visible keys [lo, hi) of stream row t.
 __device__ __forceinline__ void visible(const AttnProblem& p, int64_t t, int& lo, int& hi) {
@@ -74,24 +84,32 @@ __device__ __forceinline__ float lambda_of(const DiffProblem& a, int h, int64_t 
 
 // ---------------------------------------------------------------- forward
 
-constexpr int kFwdM = 64, kFwdN = 32, kFwdKeys = kFwdN / 16;    // keys of a thread: tx + 16 j
+constexpr int kFwdM = 64;
 
+// Keys of a thread, tx + 16 j, which lie beside each other in a row of p: 4 at
+// d = 64; at d = 128 shared memory holds two blocks of an SM with 2 only.
 template <int D>
 struct FwdSmem {
+  static constexpr int kKeys = D == 64 ? 4 : 2, kN = 16 * kKeys;
   float q[kFwdM][D + 4];
-  float k[kFwdN][D + 4];
-  float v[kFwdN][D + 4];
-  float p[2][kFwdM][kFwdN + 4];
+  float k[kN][D + 4];
+  float v[kN][D + 4];
+  float p[2][kFwdM][kN + 4];
   int lo[kFwdM], hi[kFwdM];
 };
 
+// The key that column c of such a row holds.
+template <int KEYS>
+__device__ __forceinline__ int key_row(int c) { return c / KEYS + 16 * (c % KEYS); }
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProblem a) {
+__global__ void __launch_bounds__(kThreads, 2) diff_fwd_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem_raw);
   const AttnProblem& p = a.p;
   if (status_bad(p.hdr)) return;
   constexpr int kCols = D / 64;                    // float4 columns of a thread
+  constexpr int kKeys = FwdSmem<D>::kKeys, kN = FwdSmem<D>::kN;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int h = blockIdx.y, g = h / (p.Hq / p.Hkv);
   // longest rows first: causal tiles late in the stream see the most keys
@@ -102,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
   const float* V = reinterpret_cast<const float*>(p.v) + (int64_t)g * D;
   const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
 
-  load_tile<D, kFwdM>(sm.q, Q, qs, row0, T);
+  load_tile<D, kFwdM, kThreads>(sm.q, Q, qs, row0, T);
   if (threadIdx.x < kFwdM) {
     int lo = 0, hi = 0;
     if (row0 + threadIdx.x < T) visible(p, row0 + threadIdx.x, lo, hi);
@@ -112,15 +130,13 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
   __syncthreads();
   // the tile's keys: from its first row's document to its last row's end
   const int last = (int)min((int64_t)kFwdM, T - row0) - 1;
-  const int key_lo = sm.lo[0] / kFwdN * kFwdN;
+  const int key_lo = sm.lo[0] / kN * kN;
   const int key_hi = sm.hi[last];
-  int lo[4], hi[4];
-  float m[2][4], l[2][4];
-  float4 o[2][4][kCols];
+  load_tile<D, kN, kThreads>(sm.k, K, ks, key_lo, p.kv_len);
+  float m[2][kRows], l[2][kRows];
+  float4 o[2][kRows][kCols];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[i] = sm.lo[ty * 4 + i];
-    hi[i] = sm.hi[ty * 4 + i];
+  for (int i = 0; i < kRows; ++i) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       m[t][i] = -INFINITY;
@@ -131,35 +147,36 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
   }
   const float sl2 = p.scale * kLog2e;
 
-  for (int j0 = key_lo; j0 < key_hi; j0 += kFwdN) {
+  // K's buffer is filled while P V of the tile before runs, V's while S does.
+  for (int j0 = key_lo; j0 < key_hi; j0 += kN) {
+    copies_wait();
     __syncthreads();
-    load_tile<D, kFwdN>(sm.k, K, ks, j0, p.kv_len);
-    load_tile<D, kFwdN>(sm.v, V, ks, j0, p.kv_len);
-    __syncthreads();
+    load_tile<D, kN, kThreads>(sm.v, V, ks, j0, p.kv_len);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      // scores of rows 4 ty .. + 3 against keys tx + 16 j
-      float s[4][kFwdKeys] = {};
+      // scores of rows 8 ty .. + 7 against keys tx + 16 j
+      float s[kRows][kKeys] = {};
 #pragma unroll 2
       for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 4) {
-        float4 kk[kFwdKeys];
+        float4 kk[kKeys];
 #pragma unroll
-        for (int j = 0; j < kFwdKeys; ++j)
+        for (int j = 0; j < kKeys; ++j)
           kk[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][c]);
+        for (int i = 0; i < kRows; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * kRows + i][c]);
 #pragma unroll
-          for (int j = 0; j < kFwdKeys; ++j) s[i][j] = dot4(x, kk[j], s[i][j]);
+          for (int j = 0; j < kKeys; ++j) s[i][j] = dot4(x, kk[j], s[i][j]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kRows; ++i) {
+        const int lo = sm.lo[ty * kRows + i], hi = sm.hi[ty * kRows + i];
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < kFwdKeys; ++j) {
+        for (int j = 0; j < kKeys; ++j) {
           const int key = j0 + tx + 16 * j;
-          s[i][j] = key >= lo[i] && key < hi[i] ? s[i][j] * sl2 : -INFINITY;
+          s[i][j] = key >= lo && key < hi ? s[i][j] * sl2 : -INFINITY;
           mx = fmaxf(mx, s[i][j]);
         }
 #pragma unroll
@@ -170,29 +187,33 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
         m[t][i] = mn;
         l[t][i] *= corr;                           // this thread's key columns only
 #pragma unroll
-        for (int j = 0; j < kFwdKeys; ++j) {
-          const float e = exp2f(s[i][j] - mb);
-          l[t][i] += e;
-          sm.p[t][ty * 4 + i][tx + 16 * j] = e;
+        for (int j = 0; j < kKeys; ++j) {
+          s[i][j] = exp2f(s[i][j] - mb);
+          l[t][i] += s[i][j];
         }
+        float* const row = &sm.p[t][ty * kRows + i][kKeys * tx];
+        if constexpr (kKeys == 4) st4(row, make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
+        else *reinterpret_cast<float2*>(row) = make_float2(s[i][0], s[i][1]);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) o[t][i][c] = scaled(corr, o[t][i][c]);
       }
     }
-    __syncwarp();                                   // a row's P is written and read by one half warp
-#pragma unroll 2
-    for (int j = 0; j < kFwdN; j += 4) {
+    copies_wait();
+    __syncthreads();                                // V is there, K and P's rows are done with
+    if (j0 + kN < key_hi) load_tile<D, kN, kThreads>(sm.k, K, ks, j0 + kN, p.kv_len);
+#pragma unroll (D == 64 ? 4 : 2)
+    for (int j = 0; j < kN; j += 4) {
       float4 v[4][kCols];
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          v[jj][c] = *reinterpret_cast<const float4*>(&sm.v[j + jj][c * 64 + tx * 4]);
+          v[jj][c] = *reinterpret_cast<const float4*>(&sm.v[key_row<kKeys>(j + jj)][c * 64 + tx * 4]);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 w = *reinterpret_cast<const float4*>(&sm.p[t][ty * 4 + i][j]);
+        for (int i = 0; i < kRows; ++i) {
+          const float4 w = *reinterpret_cast<const float4*>(&sm.p[t][ty * kRows + i][j]);
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
             o[t][i][c] = fma4(w.w, v[3][c], fma4(w.z, v[2][c], fma4(w.y, v[1][c],
@@ -200,12 +221,13 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
         }
     }
   }
+  copies_wait();                                // a tile that sees no key has copies in flight
 
   float* O = reinterpret_cast<float*>(p.out);
   float* O2 = reinterpret_cast<float*>(a.out2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = row0 + ty * 4 + i;
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = row0 + ty * kRows + i;
     float inv[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -231,7 +253,11 @@ __global__ void __launch_bounds__(kThreads) diff_fwd_simt_kernel(const DiffProbl
 
 // ---------------------------------------------------------------- backward
 
-constexpr int kBwdTile = 64;          // query rows and keys of a tile: 4 x 4 a thread
+template <int D>
+constexpr int kBwdRows = D == 64 ? 8 : 4;          // rows of a thread, by 4 keys
+template <int D>
+constexpr int kBwdThreads = 1024 / kBwdRows<D>;
+constexpr int kBwdTile = 64;          // query rows and keys of a tile
 
 template <int D>
 struct BwdSmem {
@@ -244,14 +270,15 @@ struct BwdSmem {
 
 // dS of a tile, written for the product that follows: KEY puts it in rows of
 // keys (dK), otherwise in rows of queries (dQ); pc: P_1 - lambda P_2 of the thread's
-// rows 4 ty + i and keys tx + 16 j.
+// rows (kBwdRows ty + i) and keys tx + 16 j.  A row of queries holds a thread's
+// keys beside each other, as key_row tells.
 template <int D, bool KEY>
-__device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2, float4 (&pc)[4]) {
+__device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2, float (&pc)[4][kBwdRows<D>]) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  float s[2][4][4] = {}, dp[4][4] = {};
+  float s[2][kBwdRows<D>][4] = {}, dp[kBwdRows<D>][4] = {};
 #pragma unroll
   for (int t = 0; t < 2; ++t)
-#pragma unroll 2
+#pragma unroll 1
     for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 4) {
       float4 kk[4], vv[4];
 #pragma unroll
@@ -260,9 +287,9 @@ __device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2,
         vv[j] = *reinterpret_cast<const float4*>(&sm.v[tx + 16 * j][c]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][c]);
-        const float4 y = *reinterpret_cast<const float4*>(&sm.dout[ty * 4 + i][c]);
+      for (int i = 0; i < kBwdRows<D>; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.q[ty * kBwdRows<D> + i][c]);
+        const float4 y = *reinterpret_cast<const float4*>(&sm.dout[ty * kBwdRows<D> + i][c]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           s[t][i][j] = dot4(x, kk[j], s[t][i][j]);
@@ -271,48 +298,57 @@ __device__ __forceinline__ void tile_ds(BwdSmem<D>& sm, int64_t key0, float sl2,
       }
     }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int kk = tx + 16 * j;
-    const int64_t key = key0 + kk;
-    float d1[4], d2[4], pr[4];
+  for (int i = 0; i < kBwdRows<D>; ++i) {
+    const int r = ty * kBwdRows<D> + i;
+    const int lo = sm.lo[r], hi = sm.hi[r];
+    const float n0 = sm.nlse2[0][r], n1 = sm.nlse2[1][r], co = sm.coef[r];
+    const float e0 = sm.ndelta[0][r], e1 = sm.ndelta[1][r];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
-      const bool vis = key >= sm.lo[r] && key < sm.hi[r];
-      const float p1 = vis ? exp2f(fmaf(s[0][i][j], sl2, sm.nlse2[0][r])) : 0.f;
-      const float p2 = vis ? sm.coef[r] * exp2f(fmaf(s[1][i][j], sl2, sm.nlse2[1][r])) : 0.f;
-      d1[i] = vis ? p1 * (dp[i][j] + sm.ndelta[0][r]) : 0.f;
-      d2[i] = vis ? p2 * (dp[i][j] + sm.ndelta[1][r]) : 0.f;
-      pr[i] = p1 + p2;
-      if constexpr (!KEY) {
-        sm.ds[0][r][kk] = d1[i];
-        sm.ds[1][r][kk] = d2[i];
-      }
-    }
-    if constexpr (KEY) {
-      st4(&sm.ds[0][kk][ty * 4], make_float4(d1[0], d1[1], d1[2], d1[3]));
-      st4(&sm.ds[1][kk][ty * 4], make_float4(d2[0], d2[1], d2[2], d2[3]));
-      pc[j] = make_float4(pr[0], pr[1], pr[2], pr[3]);
+    for (int j = 0; j < 4; ++j) {
+      const int64_t key = key0 + tx + 16 * j;
+      const bool vis = key >= lo && key < hi;
+      const float p1 = vis ? exp2f(fmaf(s[0][i][j], sl2, n0)) : 0.f;
+      const float p2 = vis ? co * exp2f(fmaf(s[1][i][j], sl2, n1)) : 0.f;
+      s[0][i][j] = vis ? p1 * (dp[i][j] + e0) : 0.f;
+      s[1][i][j] = vis ? p2 * (dp[i][j] + e1) : 0.f;
+      pc[j][i] = p1 + p2;
     }
   }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    if constexpr (KEY) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int kk = tx + 16 * j;
+#pragma unroll
+        for (int i = 0; i < kBwdRows<D>; i += 4)
+          st4(&sm.ds[t][kk][ty * kBwdRows<D> + i],
+              make_float4(s[t][i][j], s[t][i + 1][j], s[t][i + 2][j], s[t][i + 3][j]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBwdRows<D>; ++i)
+        st4(&sm.ds[t][ty * kBwdRows<D> + i][4 * tx], make_float4(s[t][i][0], s[t][i][1], s[t][i][2], s[t][i][3]));
+    }
 }
 
-// acc[i][c] += sum_j w[4 ty + i][j] x[j][col + 64 c]: a kBwdTile x D product of
+// acc[i][c] += sum_j w[kBwdRows ty + i][j] x[j][col + 64 c]: a kBwdTile x D product of
 // a square tile in shared memory; w_of picks the tile of the column's map.
-template <int D, typename W>
-__device__ __forceinline__ void tile_product(float4 (&acc)[4][D / 64], W&& w_of, float (*x)[D + 4]) {
+template <int D, bool KEY, typename W>
+__device__ __forceinline__ void tile_product(float4 (&acc)[kBwdRows<D>][D / 64], W&& w_of, float (*x)[D + 4]) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-#pragma unroll 2
+#pragma unroll 4
   for (int j = 0; j < kBwdTile; j += 4) {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int col = c * 64 + tx * 4;
       float4 b[4];
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) b[jj] = *reinterpret_cast<const float4*>(&x[j + jj][col]);
+      for (int jj = 0; jj < 4; ++jj)
+        b[jj] = *reinterpret_cast<const float4*>(&x[KEY ? j + jj : key_row<4>(j + jj)][col]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 w = *reinterpret_cast<const float4*>(w_of(col) + (ty * 4 + i) * (kBwdTile + 4) + j);
+      for (int i = 0; i < kBwdRows<D>; ++i) {
+        const float4 w = *reinterpret_cast<const float4*>(w_of(col) + (ty * kBwdRows<D> + i) * (kBwdTile + 4) + j);
         acc[i][c] = fma4(w.w, b[3], fma4(w.z, b[2], fma4(w.y, b[1], fma4(w.x, b[0], acc[i][c]))));
       }
     }
@@ -343,7 +379,7 @@ __device__ __forceinline__ void load_rows(BwdSmem<D>& sm, const DiffProblem& a, 
 // heads by diff_group_sum_kernel (one block a head, so that few key tiles still
 // fill the GPU), or written at once when the group is one head.
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) diff_bwd_dkdv_simt_kernel(const DiffProblem a) {
+__global__ void __launch_bounds__(kBwdThreads<D>, D == 64 ? 2 : 1) diff_bwd_dkdv_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
   const AttnProblem& p = a.p;
@@ -352,35 +388,44 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) diff_bwd_dkdv_simt_
   const int h = blockIdx.y, G = p.Hq / p.Hkv, g = h / G;
   const int64_t T = p.q_len, key0 = (int64_t)blockIdx.x * kBwdTile;
   const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
-  load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, key0, T);
-  load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const float*>(p.v) + (int64_t)g * D, ks, key0, T);
+  load_tile<D, kBwdTile, kBwdThreads<D>>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, key0, T);
+  load_tile<D, kBwdTile, kBwdThreads<D>>(sm.v, reinterpret_cast<const float*>(p.v) + (int64_t)g * D, ks, key0, T);
   const int64_t key1 = min(key0 + kBwdTile, T) - 1;
   const int b0 = doc_of(p.cu, p.ndoc, key0), b1 = doc_of(p.cu, p.ndoc, key1);
   const int64_t r_lo = p.causal ? key0 : (int64_t)__ldg(p.cu + b0);
   const int64_t r_hi = min((int64_t)__ldg(p.cu + b1 + 1), T);
-  float4 dk[4][D / 64] = {}, dv[4][D / 64] = {};
+  float4 dk[kBwdRows<D>][D / 64] = {}, dv[kBwdRows<D>][D / 64] = {};
+  const float* const Q = reinterpret_cast<const float*>(p.q) + (int64_t)h * D;
+  load_tile<D, kBwdTile, kBwdThreads<D>>(sm.q, Q, qs, r_lo, T);
   for (int64_t r0 = r_lo; r0 < r_hi; r0 += kBwdTile) {
     __syncthreads();
-    load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const float*>(p.q) + (int64_t)h * D, qs, r0, T);
-    load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, r0, T);
+    load_tile<D, kBwdTile, kBwdThreads<D>>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, r0, T);
     load_rows<D>(sm, a, h, r0);
+    copies_wait();
     __syncthreads();
-    float4 pc[4];
+    float pc[4][kBwdRows<D>];
     tile_ds<D, true>(sm, key0, p.scale * kLog2e, pc);
     __syncthreads();
-    tile_product<D>(dk, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.q);
+    tile_product<D, true>(dk, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.q);
     __syncthreads();
+    // the next tile's queries arrive while dV's product runs
+    if (r0 + kBwdTile < r_hi) load_tile<D, kBwdTile, kBwdThreads<D>>(sm.q, Q, qs, r0 + kBwdTile, T);
     // P over dS (a buffer of its own would leave room for one block of an SM only)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) st4(&sm.ds[0][tx + 16 * j][ty * 4], pc[j]);
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < kBwdRows<D>; i += 4)
+        st4(&sm.ds[0][tx + 16 * j][ty * kBwdRows<D> + i],
+            make_float4(pc[j][i], pc[j][i + 1], pc[j][i + 2], pc[j][i + 3]));
     __syncthreads();
-    tile_product<D>(dv, [&](int) { return &sm.ds[0][0][0]; }, sm.dout);
+    tile_product<D, true>(dv, [&](int) { return &sm.ds[0][0][0]; }, sm.dout);
   }
+  copies_wait();
   float* const DK = G > 1 ? a.dk_heads : reinterpret_cast<float*>(a.dk);
   float* const DV = G > 1 ? a.dv_heads : reinterpret_cast<float*>(a.dv);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t key = key0 + ty * 4 + i;
+  for (int i = 0; i < kBwdRows<D>; ++i) {
+    const int64_t key = key0 + ty * kBwdRows<D> + i;
     if (key >= T) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
@@ -409,7 +454,7 @@ __global__ void __launch_bounds__(kThreads) diff_group_sum_kernel(const DiffProb
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) diff_bwd_dq_simt_kernel(const DiffProblem a) {
+__global__ void __launch_bounds__(kBwdThreads<D>, D == 64 ? 2 : 1) diff_bwd_dq_simt_kernel(const DiffProblem a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
   const AttnProblem& p = a.p;
@@ -418,26 +463,31 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) diff_bwd_dq_simt_ke
   const int h = blockIdx.y, g = h / (p.Hq / p.Hkv);
   const int64_t T = p.q_len, row0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * kBwdTile;
   const int64_t qs = (int64_t)p.Hq * D, ks = (int64_t)p.Hkv * D;
-  load_tile<D, kBwdTile>(sm.q, reinterpret_cast<const float*>(p.q) + (int64_t)h * D, qs, row0, T);
-  load_tile<D, kBwdTile>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, row0, T);
+  load_tile<D, kBwdTile, kBwdThreads<D>>(sm.q, reinterpret_cast<const float*>(p.q) + (int64_t)h * D, qs, row0, T);
+  load_tile<D, kBwdTile, kBwdThreads<D>>(sm.dout, reinterpret_cast<const float*>(a.dout) + (int64_t)h * D, qs, row0, T);
   load_rows<D>(sm, a, h, row0);
   __syncthreads();
   const int last = (int)min((int64_t)kBwdTile, T - row0) - 1;
   const int key_lo = sm.lo[0] / kBwdTile * kBwdTile, key_hi = sm.hi[last];
-  float4 dq[4][D / 64] = {};
+  float4 dq[kBwdRows<D>][D / 64] = {};
+  const float* const V = reinterpret_cast<const float*>(p.v) + (int64_t)g * D;
+  load_tile<D, kBwdTile, kBwdThreads<D>>(sm.v, V, ks, key_lo, T);
   for (int j0 = key_lo; j0 < key_hi; j0 += kBwdTile) {
     __syncthreads();
-    load_tile<D, kBwdTile>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, j0, T);
-    load_tile<D, kBwdTile>(sm.v, reinterpret_cast<const float*>(p.v) + (int64_t)g * D, ks, j0, T);
+    load_tile<D, kBwdTile, kBwdThreads<D>>(sm.k, reinterpret_cast<const float*>(p.k) + (int64_t)g * D, ks, j0, T);
+    copies_wait();
     __syncthreads();
-    float4 pc[4];
+    float pc[4][kBwdRows<D>];
     tile_ds<D, false>(sm, j0, p.scale * kLog2e, pc);
     __syncthreads();
-    tile_product<D>(dq, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.k);
+    // the next tile's values arrive while the product runs
+    if (j0 + kBwdTile < key_hi) load_tile<D, kBwdTile, kBwdThreads<D>>(sm.v, V, ks, j0 + kBwdTile, T);
+    tile_product<D, false>(dq, [&](int col) { return &sm.ds[col >= D / 2][0][0]; }, sm.k);
   }
+  copies_wait();                                   // of a tile that sees no key
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = row0 + ty * 4 + i;
+  for (int i = 0; i < kBwdRows<D>; ++i) {
+    const int64_t row = row0 + ty * kBwdRows<D> + i;
     if (row >= T) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
@@ -447,10 +497,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) diff_bwd_dq_simt_ke
 }
 
 template <typename K>
-cudaError_t launch(K kern, dim3 grid, size_t smem, const DiffProblem& a, cudaStream_t s) {
+cudaError_t launch(K kern, dim3 grid, int threads, size_t smem, const DiffProblem& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, smem, s>>>(a);
+  kern<<<grid, threads, smem, s>>>(a);
   count_launches(1);
   count_path(false);
   return cudaGetLastError();
@@ -459,13 +509,13 @@ cudaError_t launch(K kern, dim3 grid, size_t smem, const DiffProblem& a, cudaStr
 template <int D>
 cudaError_t fwd(const DiffProblem& a, cudaStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.p.q_len, kFwdM), a.p.Hq);
-  return launch(diff_fwd_simt_kernel<D>, grid, sizeof(FwdSmem<D>), a, s);
+  return launch(diff_fwd_simt_kernel<D>, grid, kThreads, sizeof(FwdSmem<D>), a, s);
 }
 
 template <int D>
 cudaError_t bwd(const DiffProblem& a, cudaStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.p.q_len, kBwdTile), a.p.Hq);
-  cudaError_t e = launch(diff_bwd_dkdv_simt_kernel<D>, grid, sizeof(BwdSmem<D>), a, s);
+  cudaError_t e = launch(diff_bwd_dkdv_simt_kernel<D>, grid, kBwdThreads<D>, sizeof(BwdSmem<D>), a, s);
   if (e != cudaSuccess) return e;
   if (a.p.Hq > a.p.Hkv) {
     const int64_t n = 2 * a.p.q_len * a.p.Hkv * (D / 4);
@@ -475,7 +525,7 @@ cudaError_t bwd(const DiffProblem& a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  return launch(diff_bwd_dq_simt_kernel<D>, grid, sizeof(BwdSmem<D>), a, s);
+  return launch(diff_bwd_dq_simt_kernel<D>, grid, kBwdThreads<D>, sizeof(BwdSmem<D>), a, s);
 }
 
 }  // namespace
