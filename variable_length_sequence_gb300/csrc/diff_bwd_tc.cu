@@ -19,17 +19,25 @@
 // dP^T in the other one, B; S_2^T follows into A when the softmax warps have
 // read S_1.  dS_1^T (bf16) goes to shared memory; P^T = (P_1 + c P_2)^T and dS_2^T
 // (bf16) over S_2, 16 columns each of every 32: both are operands read from
-// TMEM, which spares shared memory's bandwidth (the kernel's tightest resource:
-// the operands of S, dP and dK_1, the tiles' copies and dS_1 take about 2900
-// cycles of it a pair against 2100 of the tensor core).  The next pair swaps the
-// regions, so its S_1 is computed into B, while the softmax is on this pair's
-// second map.
+// TMEM, which spares shared memory's bandwidth (the operands of S, dP and dK_1, the
+// tiles' copies and dS_1 take about 2900 cycles of it a pair).  The next pair swaps
+// the regions, so its S_1 is computed into B, while the softmax is on this pair's
+// second map.  A pair's 40 instructions take the tensor core 2560 cycles at least
+// (64 for 128 columns, 62 for the 64 of a dK_m); it measures 5200: dS_1 waits for S_1
+// and dP, dK_2 and dV for both, and the two regions hold no third pair.  404 us for
+// 16384 tokens in 19 causal documents, 16 heads on 4, d = 128 (540 TFLOP/s of the
+// visible pairs' 8 d).
 //
 // dQ kernel (query-stationary).  Work item: one 128-row query tile of one head.
 // TMEM: S_1 [0,128), S_2 [128,256), dP [256,384), dQ_1 | dQ_2 [384,384+D).  dS_m
 // (bf16) goes over S_m and is read from TMEM.  The softmax keeps dP of a tile
 // in registers for both maps; while it is on one map the tensor core does the
-// other map's dQ, the next S, and the next dP.
+// other map's dQ, the next S, and the next dP.  The issuing thread always has a
+// product to issue: 32 instructions of a tile take 3500 cycles, 110 each, against
+// 68 to 76 of independent ones back to back (dP of the next tile between dQ_1's or
+// dQ_2's, instruction by instruction or half by half, is 2 to 4 % slower: 600 us
+// for both kernels against 581).  227 us for the same documents (720
+// TFLOP/s of their 6 d).
 //
 // Roles, dK/dV: 16 softmax warps (four column groups of four lane quadrants;
 // with 8 warps of 64 columns the loop is 18 KB of instructions and waits for

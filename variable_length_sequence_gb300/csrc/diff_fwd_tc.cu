@@ -27,6 +27,14 @@
 // The tensor core alternates between the maps, so that one map's softmax
 // runs under the other's products.
 //
+// Bound: the tensor core's issue, 24 instructions of a 128 x 128 tile of pairs and
+// both maps at about 117 cycles each.  One causal document of 20001 tokens, 8 heads
+// on 4, D = 128: 914 us, 1345 TFLOP/s of the visible pairs' 6 D; D = 64 has the same
+// number of instructions of P V at half the columns and reaches 730.  16384 tokens
+// in 19 documents, 16 heads: 190 us, 860 TFLOP/s.  454 documents of 32 to 256 tokens
+// (65536 tokens, 16 heads on 2): 295 us, 2.0 TB/s; an item has some two tiles of keys
+// there and its start, epilogue and masked half of the pairs weigh as much as they.
+//
 // Rounding: P is rounded to bf16 as the product's operand; the row sums use
 // the unrounded float32 values.  The running output is rescaled only when a
 // row's maximum has grown by more than 2^8 (exact either way: numerator and

@@ -7,7 +7,8 @@
 //   dlambda = -delta_2 (of each token), or its sum over the tokens.
 // Written as [2 Hq][Tp] rows (-delta, -lse log2 e) and [Hq][Tp] (c = -lambda, the
 // factor of the second map's probabilities, and -c delta_2), padded with zeros to whole
-// 128-row tiles.  Bound: HBM, one read of out, out2 and dout.
+// 128-row tiles.  Bound: HBM, one read of out, out2 and dout: 201 MB of 16384 tokens,
+// 16 heads, d = 128 in 37 us, 5.5 TB/s.
 #include <algorithm>
 
 #include "layer.cuh"
