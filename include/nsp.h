@@ -621,7 +621,8 @@ int32_t nsp_rope_freqs(int32_t rot, double base, int32_t scaling, double factor,
  * The backward writes dq1 = g e1 k1, dk1 = g e1 q1, dq2 = -g e2 k2,
  * dk2 = -g e2 q2 ([n][dl], io_dtype), e1, e2 the two exponentials and g =
  * dlambda[h] (io_dtype), or its sum over the heads when n = 1.  Sums in
- * float32.  Pointers need their element's alignment.
+ * float32.  Pointers need their element's alignment.  A gradient that overlaps
+ * an input or another gradient is NSP_ERR_INVALID.
  * ---------------------------------------------------------------------- */
 int32_t nsp_diff_lambda_fwd(const void* q1, const void* k1, const void* q2, const void* k2,
                             int32_t n, int32_t dl, int32_t heads, float init, int32_t io_dtype,
@@ -644,8 +645,9 @@ int32_t nsp_diff_lambda_bwd(const void* dlambda, const void* q1, const void* k1,
  *     head) or T (one of each head and token).
  *   out2: o^2, or NULL when no backward follows.  lse: device float32
  *     [Hq][2][T], or NULL likewise.  out and out2 are of io_dtype.
- * All pointers 16-byte aligned, bf16 out and out2 32-byte aligned.  Errors
- * and the status word as nsp_attn_fwd.  A non-finite value in one document's
+ * All pointers 16-byte aligned, bf16 out and out2 32-byte aligned.  Outputs
+ * must not overlap any input or one another (not checked).  Errors and the
+ * status word as nsp_attn_fwd.  A non-finite value in one document's
  * v may reach rows of documents that share a 128-token tile with it (the
  * product with a zero probability is not finite).
  * ---------------------------------------------------------------------- */
@@ -694,7 +696,8 @@ int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const voi
  * The backward writes dx (packed), dgate (required with a gate) and, unless
  * NULL, dweight [d]; dweight needs nsp_head_norm_bwd_workspace_size bytes of
  * workspace and is summed in one fixed order.  dx may be dy's buffer, dgate
- * gate's.
+ * gate's.  Any other overlap of an output (or the workspace) with another
+ * array is NSP_ERR_INVALID.
  * ---------------------------------------------------------------------- */
 int32_t nsp_head_norm_fwd(const void* x, int64_t x_stride, const void* weight, const void* gate,
                           int64_t tokens, int32_t heads, int32_t d, float eps, float scale,

@@ -232,6 +232,43 @@ def test_norm_backward_refusals(lib):
     assert call(w=None) == INVALID
 
 
+def test_norm_overlap_refusals(lib):
+    """10 tokens of 4 heads of 128 bf16 columns: 10240 bytes an array."""
+    x, w, gate, y = A, A + (1 << 20), A + (2 << 20), A + (3 << 20)
+
+    def fwd(y=y, stride=0, gate=gate):
+        return lib.nsp_head_norm_fwd(x, stride, w, gate, 10, 4, 128, 1e-6, 1.0, nsp.NSP_BF16, y, None)
+
+    # rows of x 1024 elements apart leave 1024 bytes between them: y fits none of them
+    assert fwd(y=x + 1024) == INVALID and fwd(y=gate + 1024) == INVALID and fwd(y=w) == INVALID
+    assert fwd(y=x, stride=1024) == INVALID and fwd(y=x - 10240 + 16) == INVALID
+    assert fwd(y=x + 1024, stride=1024) == INVALID
+
+    def bwd(dy=A + (5 << 20), dx=y, dg=A + (4 << 20), dw=A + (6 << 20), ws=A + (7 << 20)):
+        n = lib.nsp_head_norm_bwd_workspace_size(10, 4, 128)
+        return lib.nsp_head_norm_bwd(x, 0, w, gate, dy, 10, 4, 128, 1e-6, 1.0, nsp.NSP_BF16, dx, dg, dw,
+                                     ws, n, None)
+
+    for kw in (dict(dx=x), dict(dx=gate), dict(dx=w), dict(dg=y), dict(dg=x), dict(dg=A + (5 << 20)),
+               dict(dw=w), dict(dw=gate + 256), dict(ws=y), dict(ws=A + (6 << 20)),
+               dict(dx=A + (5 << 20) + 1024)):
+        assert bwd(**kw) == INVALID, kw
+
+
+def test_lambda_overlap_refusals(lib):
+    """4 heads of 64 bf16 columns: 512 bytes an array."""
+    a = [A + 4096 * i for i in range(9)]                # dlambda, four vectors, four gradients
+
+    def call(**kw):
+        p = list(a)
+        for i, x in kw.items():
+            p[int(i[1:])] = x
+        return lib.nsp_diff_lambda_bwd(*p[:5], 4, 64, 4, nsp.NSP_BF16, *p[5:], None)
+
+    for kw in (dict(p5=a[1]), dict(p6=a[1] + 510), dict(p7=a[0] + 6), dict(p8=a[7] - 510), dict(p8=a[5])):
+        assert call(**kw) == INVALID, kw
+
+
 def _diff(lib, back, **kw):
     n = (lib.nsp_diff_attn_bwd_workspace_size(300, 4, 2, 128, nsp.NSP_F32) if back
          else lib.nsp_diff_attn_fwd_workspace_size(300))

@@ -32,6 +32,15 @@ bool overlap(const Span& a, const Span& b) {
   return off < a.row || off + b.row > a.step;
 }
 
+bool same_rows(const Span& a, const Span& b) {
+  return a.base == b.base && a.rows == b.rows && a.step == b.step;
+}
+
+// `rows` rows of `row` bytes, one behind the other; none where p is NULL
+Span packed(const void* p, int64_t rows, int64_t row) {
+  return {reinterpret_cast<uintptr_t>(p), p ? rows : 0, row, row};
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,6 +161,14 @@ int32_t nsp_diff_lambda_bwd(const void* dlambda, const void* q1, const void* k1,
   void* g[4] = {dq1, dk1, dq2, dk2};
   st = lambda_check(g, dlambda, n, dl, heads, io_dtype);
   if (st != NSP_OK) return st;
+  const int64_t es = elem_bytes(io_dtype);
+  for (int i = 0; i < 4; ++i) {
+    const Span o = packed(g[i], n, dl * es);
+    if (overlap(o, packed(dlambda, 1, heads * es))) return NSP_ERR_INVALID;
+    for (int j = 0; j < 4; ++j)
+      if (overlap(o, packed(v[j], n, dl * es)) || (j < i && overlap(o, packed(g[j], n, dl * es))))
+        return NSP_ERR_INVALID;
+  }
   return launch_diff_lambda_bwd(dlambda, v, n, dl, heads, io_dtype, g,
                                 reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? NSP_OK
@@ -170,6 +187,26 @@ static int32_t norm_check(const NormArgs& a, int32_t io_dtype) {
   const void* ptrs[] = {a.x, a.gate, a.weight, a.dy, a.y, a.dx, a.dgate, a.dweight, a.partial};
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return NSP_ERR_ALIGN;
+  // an output shares no byte with another array, but y may take gate's or a packed
+  // x's place, dx dy's and dgate gate's: a row is read whole before it is written
+  const int64_t es = elem_bytes(io_dtype), width = a.heads * a.d * es;
+  const Span x = {reinterpret_cast<uintptr_t>(a.x), a.tokens, a.x_stride * es, width};
+  const Span gate = packed(a.gate, a.tokens, width), dy = packed(a.dy, a.tokens, width);
+  const Span w = packed(a.weight, 1, a.d * es);
+  const Span outs[] = {packed(a.y, a.tokens, width), packed(a.dx, a.tokens, width),
+                       packed(a.dgate, a.tokens, width), packed(a.dweight, 1, a.d * es),
+                       packed(a.partial, 1, (int64_t)norm_bwd_blocks(a.tokens * a.heads) * a.d *
+                                                (int64_t)sizeof(float))};
+  constexpr int kY = 0, kDx = 1, kDgate = 2;
+  for (int i = 0; i < 5; ++i) {
+    const Span& o = outs[i];
+    if (overlap(o, w) || (overlap(o, x) && !(i == kY && same_rows(o, x))) ||
+        (overlap(o, gate) && !((i == kY || i == kDgate) && same_rows(o, gate))) ||
+        (overlap(o, dy) && !(i == kDx && same_rows(o, dy))))
+      return NSP_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (overlap(o, outs[j])) return NSP_ERR_INVALID;
+  }
   return NSP_OK;
 }
 
