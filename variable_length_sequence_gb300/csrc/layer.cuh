@@ -19,6 +19,8 @@ struct RopeTensor {
   int64_t in_stride, out_stride;     // elements between tokens
   int32_t heads;
   int32_t in_groups, out_groups;     // > 1: head-group-major [P][len][heads / P][d]
+  int32_t hpg;                       // heads of a group
+  int64_t in_jump, out_jump;         // from behind a group's last head to the next one's first
 };
 
 struct RopeArgs {

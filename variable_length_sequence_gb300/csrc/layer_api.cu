@@ -104,6 +104,10 @@ int32_t nsp_rope(const nsp_rope_tensor_t* tensors, int32_t n, const int32_t* cu_
     a.t[i].heads = t.heads;
     a.t[i].in_groups = inverse ? t.groups : 1;
     a.t[i].out_groups = inverse ? 1 : t.groups;
+    a.t[i].hpg = t.heads / t.groups;
+    const int64_t jump = t.groups > 1 ? (len - 1) * a.t[i].hpg * d : 0;
+    a.t[i].in_jump = inverse ? jump : 0;
+    a.t[i].out_jump = inverse ? 0 : jump;
     in[i] = {reinterpret_cast<uintptr_t>(t.in), len, is * es, width * es};
     out[i] = {reinterpret_cast<uintptr_t>(t.out), len, os * es, width * es};
   }

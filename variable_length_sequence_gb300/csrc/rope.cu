@@ -19,9 +19,9 @@
 // the token's heads with four heads' loads in flight.  With few tokens the
 // heads of one token are split over several teams, so that a single token
 // still spreads over the GPU.  32768 tokens, 32 + 4 heads of 128 bf16 columns read
-// from the fused projection: 94 us, 6.4 TB/s; 8191 tokens, 16 + 4 heads of 64 float32
-// columns, half of them rotated in interleaved pairs: 23 us, 3.6 TB/s (84 MB: most of
-// it a launch's start and end).
+// from the fused projection: 91 us, 6.6 TB/s; 8191 tokens, 16 + 4 heads of 64 float32
+// columns, half of them rotated in interleaved pairs: 10.4 us when its 84 MB are in L2,
+// and a call takes the host 21 us.
 #include <algorithm>
 
 #include "layer.cuh"
@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeadsInFlight = 4;
+constexpr int64_t kL2Bytes = (int64_t)128 << 20;
 
 // The row of head h at range row t: packed (token stride), or head-group-major.
 __device__ __forceinline__ int64_t row_offset(int64_t t, int h, int64_t stride, int heads,
@@ -80,8 +81,7 @@ struct Cursor {
           row_offset(t, h, r.in_stride, r.heads, r.in_groups, a.len, a.d);
     dst = reinterpret_cast<T*>(r.out) + col +
           row_offset(t, h, r.out_stride, r.heads, r.out_groups, a.len, a.d);
-    const int hpg = r.heads / max(r.in_groups, r.out_groups);
-    left = hpg - h % hpg;
+    left = r.hpg - h % r.hpg;
   }
   __device__ __forceinline__ void start(const RopeArgs& a, int64_t t, int head, int col) {
     k = 0;
@@ -94,11 +94,15 @@ struct Cursor {
     src += a.d;
     dst += a.d;
     if (--left > 0) return;
-    if (h == a.t[k].heads) {
-      h = 0;
-      if (++k == a.n) return;         // past the last head
+    const RopeTensor& r = a.t[k];
+    if (h < r.heads) {                // the next head group of the same tensor
+      left = r.hpg;
+      src += r.in_jump;
+      dst += r.out_jump;
+      return;
     }
-    place(a, t, col);
+    h = 0;
+    if (++k < a.n) place(a, t, col);  // (else past the last head)
   }
 };
 
@@ -112,9 +116,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   constexpr int N = Vec<T>::N;
   constexpr int kPairs = INTERLEAVED ? N / 2 : N;    // pairs of one rotated piece
   __shared__ uint64_t s_fx[kRopeMaxDim / 2];
-  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) s_fx[i] = fixed_turns(a.freqs[i]);
+  for (int i = threadIdx.x; i < a.rot / 2; i += blockDim.x) s_fx[i] = fixed_turns(a.freqs[i]);
   __syncthreads();
-  const int teams = kThreads / pieces;
+  const int teams = blockDim.x / pieces;
   const int team = threadIdx.x / pieces, u = threadIdx.x - team * pieces;
   if (team >= teams) return;
   const int64_t items = a.len * hsplit;
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int half = a.rot / 2;
   for (int64_t item = (int64_t)blockIdx.x * teams + team; item < items;
        item += (int64_t)gridDim.x * teams) {
-    const int64_t t = item / hsplit;
+    const int64_t t = hsplit == 1 ? item : (int64_t)((uint32_t)item / (uint32_t)hsplit);
     const int part = (int)(item - t * hsplit);
     const bool rot = u < rotated;
     float c[kPairs], s[kPairs];
@@ -245,21 +249,27 @@ cudaError_t launch_typed(const RopeArgs& a, cudaStream_t s) {
     constexpr int N = 16 / (int)sizeof(T);
     const int rotated = (a.interleaved ? a.rot : a.rot / 2) / N;
     const int pieces = rotated + (a.d - a.rot) / N;
-    const int teams = kThreads / pieces;
-    // teams to fill the GPU twice (16 blocks of an SM), from splitting a token's
-    // heads when there are too few tokens: 32768 tokens of 36 heads, in two parts
-    // 97.6 us, in three 95
-    int64_t hsplit = ceil_div(nsm * 16 * teams, a.len);
+    // 128 threads, or as many pieces as a head has: with 256 a stream of few blocks
+    // waits longer for its last ones (8191 tokens, 20 heads of 64 float32: 13.6 us against
+    // 10.4; 32768 tokens, 36 heads of 128 bf16: 94.0 against 93.0)
+    const int threads = pieces > kThreads / 2 ? kThreads : kThreads / 2;
+    const int teams = threads / pieces;
+    // A token's heads are split over several teams, each with its own search and angles,
+    // for two blocks of an SM only (16 blocks: 14.6 us of the first stream above), and
+    // in parts of 12 heads or more for a stream that does not fit in L2, whose rows in flight
+    // then lie closer together (the second one: 90.4 us in three parts, 93.0 in one)
+    const int64_t bytes = 2 * a.len * heads * a.d * (int64_t)sizeof(T);
+    int64_t hsplit = ceil_div(nsm * 2 * teams, a.len);
+    if (bytes > kL2Bytes) hsplit = std::max<int64_t>(hsplit, heads / 12);
     hsplit = std::min<int64_t>(hsplit, heads);
-    // (one item a team where 64 blocks of an SM allow it: no block is left with one
+    if (a.len * hsplit > UINT32_MAX) hsplit = 1;     // the kernel divides split items in 32 bits
+    // (one item a team where 128 blocks of an SM allow it: no block is left with one
     // more item than the others at the end)
-    const int64_t blocks = std::min<int64_t>(ceil_div(a.len * hsplit, teams), nsm * 64);
+    const int64_t blocks = std::min<int64_t>(ceil_div(a.len * hsplit, teams), nsm * 128);
     if (a.interleaved)
-      rope_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(a, pieces, rotated, heads,
-                                                                 (int)hsplit);
+      rope_kernel<T, true><<<(unsigned)blocks, threads, 0, s>>>(a, pieces, rotated, heads, (int)hsplit);
     else
-      rope_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(a, pieces, rotated, heads,
-                                                                  (int)hsplit);
+      rope_kernel<T, false><<<(unsigned)blocks, threads, 0, s>>>(a, pieces, rotated, heads, (int)hsplit);
   }
   count_launches(1);
   return cudaGetLastError();
