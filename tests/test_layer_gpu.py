@@ -134,6 +134,34 @@ def test_rope_odd_addresses(nsp):
     assert torch.equal(got, ref)
 
 
+@pytest.mark.parametrize("d,rot,inter", [(1024, 8, True), (1024, 8, False), (1024, 1024, True),
+                                         (1024, 1024, False), (516, 4, True)])
+def test_rope_wide_heads(nsp, d, rot, inter):
+    """More 16-byte pieces in a head than half a block has threads."""
+    T, h = 9, 3
+    fr = nsp.rope_freqs(rot, base=500.0, device="cuda")
+    cu, x = cu_of([5, 4]), randn(30, T, h, d, dt=F32)
+    got, _ = nsp.rope(x, None, cu, fr, layout="interleaved" if inter else "half")
+    a = L.rope_angles(L.rope_positions(cu.cpu().numpy(), T), fr.cpu().numpy())
+    check_rope(got, x, a, rot, inter, 1.0, False, F32, "wide")
+
+
+@pytest.mark.parametrize("T,h,hkv,groups", [(1, 36, 4, 4), (2, 40, 1, 8), (20011, 39, 13, 3),
+                                            (700, 64, 64, 1)])
+def test_rope_parts_of_heads(nsp, T, h, hkv, groups):
+    """However a token's heads are split over the blocks, within a tensor, over
+    two and over head groups: the bits of every head alone."""
+    cu, fr = cu_of([T]), nsp.rope_freqs(64, device="cuda")
+    q, k = randn(31, T, h, 64), randn(32, T, hkv, 64)
+    whole_q, whole_k = nsp.rope(q, k, cu, fr, q_groups=groups)
+    if groups > 1:
+        whole_q = whole_q.permute(1, 0, 2, 3).reshape(T, h, 64)
+    for i in (0, h // groups - 1, h // groups % h, h // 2, h - 1):
+        assert torch.equal(whole_q[:, i:i + 1], nsp.rope(q[:, i:i + 1], None, cu, fr)[0]), i
+    for i in (0, hkv - 1):
+        assert torch.equal(whole_k[:, i:i + 1], nsp.rope(k[:, i:i + 1], None, cu, fr)[0]), i
+
+
 def test_rope_rows_behind_the_last_document_and_shards(nsp):
     T, h, d = 100, 4, 64
     cu, fr = cu_of([40, 30]), nsp.rope_freqs(d, device="cuda")
