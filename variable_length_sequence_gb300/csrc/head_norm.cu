@@ -11,19 +11,47 @@
 // The weight's gradient is summed by every thread for its own columns over
 // its rows, then over the block in shared memory, and over the blocks by a
 // second small kernel, always in the same order.  32768 x 16 rows of 128 bf16 columns
-// with gate and weight: 62.7 us, 6.4 TB/s; backward of 16383 x 16 such rows: 65.6 us,
-// 5.1 TB/s (reads with writes between them, and a third of the FP32 pipes' time).
+// with gate and weight: 61.8 us, 6.5 TB/s; backward of 16383 x 16 such rows: 56.7 us,
+// 5.9 TB/s (some 2.5 of them the second kernel).
 #include <algorithm>
 
 #include "layer.cuh"
+#include "tc_ptx.cuh"
 
 namespace nsp {
 namespace {
 
+using namespace tc;
+
 constexpr int kThreads = 256;
 
-// exp and the quotient to 2 ulp each (IEEE division costs as much as the rest)
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// exp to 2 ulp, the reciprocal to 1 (of 1 at least; the largest give zero)
+__device__ __forceinline__ float sigmoid(float g) {
+  float x;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(1.f + __expf(-g)));
+  return x;
+}
+
+// A vector's values as packed pairs: two of them an instruction.
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4& u, uint64_t (&x)[Vec<T>::N / 2]) {
+  float t[Vec<T>::N];
+  Vec<T>::unpack(u, t);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N / 2; ++i) x[i] = f2_pack(t[2 * i], t[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const uint64_t (&x)[Vec<T>::N / 2]) {
+  float t[Vec<T>::N];
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N / 2; ++i) f2_unpack(x[i], t[2 * i], t[2 * i + 1]);
+  return Vec<T>::pack(t);
+}
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  float a, b;
+  f2_unpack(g, a, b);
+  return f2_pack(sigmoid(a), sigmoid(b));
+}
 
 __device__ __forceinline__ float group_sum(float x, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -109,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const NormArgs a, i
 }
 
 template <typename T, int V, int ROWS>
-__global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 1) head_norm_bwd_kernel(const NormArgs a, int lanes) {
+__global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) head_norm_bwd_kernel(const NormArgs a, int lanes) {
   constexpr int N = Vec<T>::N;
   extern __shared__ float s_dw[];                 // [groups][d]
   grid_dep_trigger();
@@ -123,21 +151,23 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 1) head_norm_bwd_kernel
   const T* const DY = reinterpret_cast<const T*>(a.dy);
   T* const DX = reinterpret_cast<T*>(a.dx);
   T* const DG = reinterpret_cast<T*>(a.dgate);
-  float w[V][N], dw[V][N];
+  constexpr int P = N / 2;                        // pairs of a vector
+  uint64_t w[V][P], dw[V][P];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = lane + v * lanes;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      w[v][i] = 1.f;
-      dw[v][i] = 0.f;
+    for (int i = 0; i < P; ++i) {
+      w[v][i] = f2_pack(1.f, 1.f);
+      dw[v][i] = 0;
     }
     if (a.weight != nullptr && c < nvec)
-      Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(a.weight) + c), w[v]);
+      unpack2<T>(__ldg(reinterpret_cast<const uint4*>(a.weight) + c), w[v]);
   }
   const int64_t step = (int64_t)gridDim.x * groups * ROWS;
-  for (int64_t r0 = (int64_t)blockIdx.x * groups * ROWS; r0 < rows; r0 += step) {
-    uint4 x[ROWS][V], g[ROWS][V], y[ROWS][V];
+  // the next rows are on their way while these are worked on
+  uint4 nx[ROWS][V], ng[ROWS][V], ny[ROWS][V];
+  auto load = [&](int64_t r0) {
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       const int64_t row = r0 + k * groups + group;
@@ -146,46 +176,67 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 1) head_norm_bwd_kernel
       for (int v = 0; v < V; ++v) {
         const int c = lane + v * lanes;
         const bool in = row < rows && c < nvec;
-        x[k][v] = in ? ld_once(src + (int64_t)c * N) : make_uint4(0, 0, 0, 0);
-        y[k][v] = in ? ld_once(DY + row * a.d + c * N) : make_uint4(0, 0, 0, 0);
-        if (G != nullptr) g[k][v] = in ? ld_once(G + row * a.d + c * N) : make_uint4(0, 0, 0, 0);
+        nx[k][v] = in ? ld_once(src + (int64_t)c * N) : make_uint4(0, 0, 0, 0);
+        ny[k][v] = in ? ld_once(DY + row * a.d + c * N) : make_uint4(0, 0, 0, 0);
+        if (G != nullptr) ng[k][v] = in ? ld_once(G + row * a.d + c * N) : make_uint4(0, 0, 0, 0);
       }
     }
+  };
+  load((int64_t)blockIdx.x * groups * ROWS);
+  for (int64_t r0 = (int64_t)blockIdx.x * groups * ROWS; r0 < rows; r0 += step) {
+    uint4 x[ROWS][V], g[ROWS][V], y[ROWS][V];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[k][v] = nx[k][v];
+        y[k][v] = ny[k][v];
+        if (G != nullptr) g[k][v] = ng[k][v];
+      }
+    if (r0 + step < rows) load(r0 + step);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       const int64_t row = r0 + k * groups + group;
       // sums of x^2 and of x u (n and u scale out of the second one)
-      float ss = 0.f, su = 0.f;
-      float t[V][N], u[V][N], sg[V][N];
+      uint64_t ss = 0, su = 0;
+      uint64_t t[V][P], us[V][P], uw[V][P], sg[V][P];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        Vec<T>::unpack(x[k][v], t[v]);
-        Vec<T>::unpack(y[k][v], u[v]);
-        if (G != nullptr) Vec<T>::unpack(g[k][v], sg[v]);
+        unpack2<T>(x[k][v], t[v]);
+        unpack2<T>(y[k][v], us[v]);
+        if (G != nullptr) unpack2<T>(g[k][v], sg[v]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          sg[v][i] = G != nullptr ? sigmoid(sg[v][i]) : 1.f;
-          ss = fmaf(t[v][i], t[v][i], ss);
-          su = fmaf(t[v][i], u[v][i] * w[v][i] * sg[v][i], su);
+        for (int i = 0; i < P; ++i) {
+          if (G != nullptr) {
+            sg[v][i] = sigmoid2(sg[v][i]);
+            us[v][i] = f2_mul(us[v][i], sg[v][i]);
+          }
+          uw[v][i] = f2_mul(us[v][i], w[v][i]);
+          ss = f2_fma(t[v][i], t[v][i], ss);
+          su = f2_fma(t[v][i], uw[v][i], su);
         }
       }
-      const float r = rsqrtf(fmaf(group_sum(ss, lanes), inv_d, a.eps));
-      const float mean = group_sum(su, lanes) * r * inv_d;      // mean(u n) / s
+      float s0, s1, u0, u1;
+      f2_unpack(ss, s0, s1);
+      f2_unpack(su, u0, u1);
+      const float r = rsqrtf(fmaf(group_sum(s0 + s1, lanes), inv_d, a.eps));
+      const float mean = group_sum(u0 + u1, lanes) * r * inv_d;      // mean(u n) / s
       const float sr = a.scale * r;
+      const uint64_t sr2 = f2_pack(sr, sr), nm2 = f2_pack(-sr * mean * r, -sr * mean * r);
+      const uint64_t one = f2_pack(1.f, 1.f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = lane + v * lanes;
         if (row >= rows || c >= nvec) continue;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float n = t[v][i] * r, us = u[v][i] * sg[v][i];
-          const float dyn = a.scale * n * us;                   // s dy n sigmoid
-          dw[v][i] += dyn;
-          t[v][i] = sr * fmaf(us, w[v][i], -n * mean);
-          u[v][i] = dyn * w[v][i] * (1.f - sg[v][i]);
+        for (int i = 0; i < P; ++i) {
+          const uint64_t st = f2_mul(t[v][i], sr2);                  // s n
+          dw[v][i] = f2_fma(st, us[v][i], dw[v][i]);
+          if (G != nullptr) sg[v][i] = f2_mul(f2_mul(st, uw[v][i]), f2_sub(one, sg[v][i]));
+          t[v][i] = f2_fma(uw[v][i], sr2, f2_mul(t[v][i], nm2));
         }
-        st_once(DX + row * a.d + c * N, Vec<T>::pack(t[v]));
-        if (G != nullptr) st_once(DG + row * a.d + c * N, Vec<T>::pack(u[v]));
+        st_once(DX + row * a.d + c * N, pack2<T>(t[v]));
+        if (G != nullptr) st_once(DG + row * a.d + c * N, pack2<T>(sg[v]));
       }
     }
   }
@@ -195,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 1) head_norm_bwd_kernel
     const int c = lane + v * lanes;
     if (c >= nvec) continue;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s_dw[group * a.d + c * N + i] = dw[v][i];
+    for (int i = 0; i < P; ++i)
+      f2_unpack(dw[v][i], s_dw[group * a.d + c * N + 2 * i], s_dw[group * a.d + c * N + 2 * i + 1]);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < a.d; c += kThreads) {
@@ -281,11 +333,12 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// At most 456 blocks, three on each of 152 SMs, as many as fit at once (608 took
-// 87 us for 16383 x 16 x 128 with gate, 456 take 66), fewer for few rows: the size of
-// the workspace must not depend on the device.
+// At most 304 blocks, two on each of 152 SMs, as many as fit at once with two rows
+// of a group worked on and two more on their way (16383 x 16 x 128 with gate: 56.7 us;
+// three blocks without rows on their way 63.3, four blocks of one row and one 57.1),
+// fewer for few rows: the size of the workspace must not depend on the device.
 int norm_bwd_blocks(int64_t rows) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(456, ceil_div(rows, 8)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(304, ceil_div(rows, 8)));
 }
 
 cudaError_t launch_head_norm(const NormArgs& a, int32_t io_dtype, cudaStream_t s) {
