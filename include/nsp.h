@@ -648,7 +648,7 @@ int32_t nsp_diff_lambda_bwd(const void* dlambda, const void* q1, const void* k1,
  * All pointers 16-byte aligned, bf16 out and out2 32-byte aligned.  Outputs
  * must not overlap any input or one another (not checked).  Errors and the
  * status word as nsp_attn_fwd.  A non-finite value in one document's
- * v may reach rows of documents that share a 128-token tile with it (the
+ * v may reach rows of documents less than 128 tokens away from it (the
  * product with a zero probability is not finite).
  * ---------------------------------------------------------------------- */
 size_t nsp_diff_attn_fwd_workspace_size(int64_t T);

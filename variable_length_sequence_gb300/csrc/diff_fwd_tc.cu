@@ -5,12 +5,19 @@
 //   P_m = softmax(scale q_m k_m^T) over a row's visible keys,  O_m = P_m V,
 //   out = O_1 - lambda O_2,  with the online softmax of Milakov and Gimelshein.
 //
-// Work item: one 128-row query tile of one head, in the schedule kernel's
-// order (most keys first), taken from an atomic counter by a persistent grid
-// of one CTA per SM.  Both maps read the same Q, K and V tiles: map m is the
-// m-th half of the columns of Q and K (an offset into the same shared-memory
-// tile), V is shared whole, and the difference is formed in the epilogue, so
-// no map's output goes to memory (out2 only when a backward follows).
+// Work item: 128 query rows, the 2^k heads of one group at 128 / 2^k consecutive
+// tokens (k as large as the group's head count and kMaxItemHeads allow), against the
+// 128-key tiles from the start of the first token's document on.  Fewer tokens of an
+// item see fewer keys of other documents, and tiles that begin with a document waste
+// less: 10800 tiles in place of 18400 for 454 documents of 32 to 256 tokens and 8 heads
+// of a group, 14400 in place of 15900 for 19 documents around 1024 and 4 heads (whole
+// calls: 300 us of one head in an item, 280 of 4, 265 of 8; 191 and 178; one long
+// document: 921 and 909).  Items are taken from an atomic counter by a persistent grid of
+// one CTA per SM, 128-token tiles in the schedule kernel's order (most keys first).  Both
+// maps read the same Q, K and V tiles: map m is the m-th half of the columns of Q and K
+// (an offset into the same shared-memory tile), V is shared whole, and the difference is
+// formed in the epilogue, so no map's output goes to memory (out2 only when a backward
+// follows).
 //
 // CTA roles (384 threads, three warpgroups):
 //   warps 0-3   softmax of map 1 (one query row a thread, TMEM lanes 0-127)
@@ -20,20 +27,22 @@
 //   warp 10     stores finished tiles (TMA, from a staging buffer)
 //   warp 11     idle (completes the control warpgroup)
 // Registers are moved from the control warpgroup to the softmax warpgroups
-// (launched at 168: 384 x 168 = 64512; 256 x 192 + 128 x 112 = 63488), enough
-// to hold a 128-column row of S.
+// (launched at 168: 384 x 168 = 64512 = 256 x 200 + 128 x 104; with 192 and 112
+// a long document takes 909 us, not 900, with 208 and 88 short ones 292, not 265),
+// enough to hold a 128-column row of S.
 // TMEM (512 columns): S_1 [0,128) S_2 [128,256) O_1 [256,384) O_2 [384,512);
 // P (bf16 pairs) over the first 64 columns of its S, read from there by P V.
 // The tensor core alternates between the maps, so that one map's softmax
 // runs under the other's products.
 //
 // Bound: the tensor core's issue, 24 instructions of a 128 x 128 tile of pairs and
-// both maps at about 117 cycles each.  One causal document of 20001 tokens, 8 heads
-// on 4, D = 128: 914 us, 1345 TFLOP/s of the visible pairs' 6 D; D = 64 has the same
-// number of instructions of P V at half the columns and reaches 730.  16384 tokens
-// in 19 documents, 16 heads: 190 us, 860 TFLOP/s.  454 documents of 32 to 256 tokens
-// (65536 tokens, 16 heads on 2): 295 us, 2.0 TB/s; an item has some two tiles of keys
-// there and its start, epilogue and masked half of the pairs weigh as much as they.
+// both maps at about 115 cycles each.  One causal document of 20001 tokens, 8 heads
+// on 4, D = 128: 900 us, 1365 TFLOP/s of the visible pairs' 6 D; D = 64 has the same
+// number of instructions of P V at half the columns and reaches 729.  16384 tokens
+// in 19 documents, 16 heads: 178 us, 917 TFLOP/s.  454 documents of 32 to 256 tokens
+// (65536 tokens, 16 heads on 2): 265 us, 2.3 TB/s; an item has 1.3 tiles of keys there,
+// and the chain of its scores, softmax, product and epilogue, some 9000 cycles, has
+// nothing of its own CTA beside it: TMEM holds no second item's accumulators.
 //
 // Rounding: P is rounded to bf16 as the product's operand; the row sums use
 // the unrounded float32 values.  The running output is rescaled only when a
@@ -50,15 +59,16 @@ using namespace tc;
 
 constexpr int BM = 128, BN = 128;
 constexpr int NSTAGE = 2;
+constexpr int kMaxItemHeads = 8;
 constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 192, kRegsControl = 112;
+constexpr int kRegsSoftmax = 200, kRegsControl = 104;
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpStore = 10;
 __host__ __device__ constexpr uint32_t col_s(int m) { return m == 0 ? 0u : 128u; }
 __host__ __device__ constexpr uint32_t col_o(int m) { return m == 0 ? 256u : 384u; }
 constexpr float kRescaleThreshold = 8.0f;                 // log2 units
 
 struct Item {
-  int qtile, h, g, j_lo, n_kv;         // n_kv 128-key tiles from j_lo; -1 stops
+  int t0, h0, g, lo, n_kv;             // first token and head; n_kv 128-key tiles from key lo; -1 stops
   int pad[3];
 };
 
@@ -83,8 +93,8 @@ struct FwdArgs {
   AttnProblem p;
   const __nv_bfloat16* lambda;
   int64_t n_lambda;
-  const int2* tiles;
-  const int* order;
+  const int* order;                    // 128-token tiles, most keys first
+  int shift;                           // log2 of the heads of an item
 };
 
 __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
@@ -181,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   WaitCtl* const wc = &sm.wait;
   const int G = p.Hq / p.Hkv;
   const int n_items = hdr->n_items * p.Hq;
+  const int heads = 1 << a.shift, tokens = BM >> a.shift;       // of an item
   constexpr int kBlocks = D / 64;                               // 64-column blocks of a row
   constexpr uint32_t kLoadBytes = kBlocks * kBlk;          // one Q, K or V tile
 
@@ -195,13 +206,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it = {};
         it.n_kv = -1;
         if (idx < n_items) {
-          const int qt = a.order[idx / p.Hq];
-          const int2 tr = a.tiles[qt];
-          it.qtile = qt;
-          it.h = idx % p.Hq;
-          it.g = it.h / G;
-          it.j_lo = tr.x;
-          it.n_kv = tr.y - tr.x + 1;
+          const int rest = idx % p.Hq;
+          it.t0 = a.order[idx / p.Hq] * BM + (rest & (heads - 1)) * tokens;
+          if (it.t0 >= p.q_len) continue;            // (the last tile may be short)
+          it.h0 = rest & ~(heads - 1);
+          it.g = it.h0 / G;
+          const int end = (int)min((int64_t)it.t0 + tokens, p.q_len);
+          it.lo = __ldg(p.cu + doc_of(p.cu, p.ndoc, it.t0));
+          const int hi = p.causal ? end : __ldg(p.cu + doc_of(p.cu, p.ndoc, end - 1) + 1);
+          it.n_kv = (hi - it.lo + BN - 1) / BN;
         }
         // items alternate over two slots of the queue and of Q
         const uint32_t slot = it_count & 1, use = it_count >> 1;
@@ -213,12 +226,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&sm.q_full[slot], kLoadBytes);
 #pragma unroll
         for (int cb = 0; cb < kBlocks; ++cb)
-          tma_load_2d(sm.q[slot] + cb * kBlk, &tm_q, &sm.q_full[slot], it.h * D + cb * 64,
-                      it.qtile * BM);
+          tma_load_3d(sm.q[slot] + cb * kBlk, &tm_q, &sm.q_full[slot], cb * 64, it.h0, it.t0);
         ++it_count;
         for (int jj = 0; jj < it.n_kv; ++jj) {
           const uint32_t st = kv_count % NSTAGE, n = kv_count / NSTAGE;
-          const int key0 = (it.j_lo + jj) * BN;
+          const int key0 = it.lo + jj * BN;
           if (n >= 1 && !mbar_wait(&sm.k_empty[st], (n - 1) & 1, wc, hdr)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.k_full[st], kLoadBytes);
 #pragma unroll
@@ -266,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&sm.s_full[m]);
           }
           mma_commit(&sm.k_empty[st]);
-          if (it.n_kv == 1 && !SAVE) mma_commit(&sm.q_empty[slot]);
         }
         for (int jj = 0; jj < it.n_kv && ok; ++jj) {
           const uint32_t st = (kv_count + jj) % NSTAGE, n = (kv_count + jj) / NSTAGE;
@@ -296,10 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mma_kk<D / 2>(m, tmem + col_s(m), qs, smem_u32(sm.k[stn]));
             mma_commit(&sm.s_full[m]);
-            if (m == 1) {
-              mma_commit(&sm.k_empty[stn]);
-              if (jj + 2 == it.n_kv && !SAVE) mma_commit(&sm.q_empty[slot]);
-            }
+            if (m == 1) mma_commit(&sm.k_empty[stn]);
           }
           ++p_count;
         }
@@ -320,14 +328,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&sm.out_full, it_count & 1, wc, hdr)) break;
 #pragma unroll
         for (int cb = 0; cb < kBlocks; ++cb) {
-          tma_store_2d(&tm_out, sm.out + cb * kBlk, it.h * D + cb * 64, it.qtile * BM);
+          tma_store_3d(&tm_out, sm.out + cb * kBlk, cb * 64, it.h0, it.t0);
           if constexpr (SAVE)
-            tma_store_2d(&tm_out2, sm.q[slot] + cb * kBlk, it.h * D + cb * 64, it.qtile * BM);
+            tma_store_3d(&tm_out2, sm.q[slot] + cb * kBlk, cb * 64, it.h0, it.t0);
         }
         bulk_commit();
         bulk_wait_read_all();
         mbar_arrive(&sm.out_free);
-        if constexpr (SAVE) mbar_arrive(&sm.q_empty[slot]);
+        // (freed by the last product of scores instead, a long document takes 940 us, not 912)
+        mbar_arrive(&sm.q_empty[slot]);
         ++it_count;
       }
       bulk_wait_all();                     // every tile is in memory before the CTA exits
@@ -353,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       it = sm.items[n & 1];
       mbar_arrive_warp(&sm.item_empty[n & 1], lane);
       if (it.n_kv >= 0)
-        doc = document_of_rows(p.cu, p.ndoc, (int64_t)it.qtile * BM + wq * 32, p.q_len, lane);
+        doc = document_of_rows(p.cu, p.ndoc, (int64_t)it.t0 + ((wq * 32) >> a.shift), p.q_len, lane, a.shift);
       return true;
     };
     if (!next_item(0)) it.n_kv = -1;
     while (it.n_kv >= 0) {
       const uint32_t slot = it_count & 1;
-      const int h = it.h;
-      const int64_t row = (int64_t)it.qtile * BM + r;
+      const int h = it.h0 + (r & (heads - 1));
+      const int64_t row = (int64_t)it.t0 + (r >> a.shift);
       const bool valid = row < p.q_len;
       int lo = 0, hi = 0;                                      // visible keys [lo, hi)
       float lam = 0.f;
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(&sm.s_full[m_], s_count & 1, wc, hdr)) { ok = false; break; }
         ++s_count;
         tc_fence_after();
-        const int key0 = (it.j_lo + jj) * BN;
+        const int key0 = it.lo + jj * BN;
         uint32_t sr[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, sr[c]);
@@ -494,8 +503,9 @@ cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
 
 }  // namespace
 
-// [rows, cols] bf16 row-major, box = 64 columns x 128 rows, 128-byte swizzle.
-bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+namespace {
+bool encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -504,30 +514,49 @@ bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols)
       ptr = nullptr;
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   }();
-  if (!fn) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [T, H, d] bf16, box = 64 columns x `heads` heads x 128 / heads tokens, 128-byte swizzle:
+// row r of the tile is token r / heads, head r % heads.
+bool heads_map(CUtensorMap* m, const void* base, int64_t T, int64_t H, int64_t d, int heads) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)(d * 2), (cuuint64_t)(H * d * 2)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(BM / heads)};
+  return encode_map(m, base, 3, dims, strides, box);
+}
+}  // namespace
+
+// [rows, cols] bf16 row-major, box = 64 columns x 128 rows, 128-byte swizzle.
+bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(cols * 2)};
-  const cuuint32_t box[2] = {64, 128}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t box[2] = {64, 128};
+  return encode_map(m, base, 2, dims, strides, box);
 }
 
 cudaError_t launch_diff_fwd_tc(const DiffProblem& d, const FwdWsLayout& L, char* ws, cudaStream_t s) {
   const AttnProblem& p = d.p;
   CUtensorMap mq, mk, mv, mo, mo2;
-  if (!diff_tile_map(&mq, p.q, p.q_len, (int64_t)p.Hq * p.d) ||
+  // heads of an item: the group's power of two, kMaxItemHeads at most
+  int shift = 0;
+  while ((2 << shift) <= kMaxItemHeads && p.Hq / p.Hkv % (2 << shift) == 0) ++shift;
+  if (!heads_map(&mq, p.q, p.q_len, p.Hq, p.d, 1 << shift) ||
       !diff_tile_map(&mk, p.k, p.kv_len, (int64_t)p.Hkv * p.d) ||
       !diff_tile_map(&mv, p.v, p.kv_len, (int64_t)p.Hkv * p.d) ||
-      !diff_tile_map(&mo, p.out, p.q_len, (int64_t)p.Hq * p.d) ||
-      !diff_tile_map(&mo2, d.out2 ? d.out2 : p.out, p.q_len, (int64_t)p.Hq * p.d))
+      !heads_map(&mo, p.out, p.q_len, p.Hq, p.d, 1 << shift) ||
+      !heads_map(&mo2, d.out2 ? d.out2 : p.out, p.q_len, p.Hq, p.d, 1 << shift))
     return cudaErrorNotSupported;
   FwdArgs a;
   a.p = p;
   a.lambda = reinterpret_cast<const __nv_bfloat16*>(d.lambda);
   a.n_lambda = d.n_lambda;
-  a.tiles = reinterpret_cast<const int2*>(ws + L.tiles);
   a.order = reinterpret_cast<const int*>(ws + L.order);
+  a.shift = shift;
   if (d.out2 != nullptr)
     return p.d == 128 ? launch_fwd<128, true>(mq, mk, mv, mo, mo2, a, s)
                       : launch_fwd<64, true>(mq, mk, mv, mo, mo2, a, s);

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, WaitCt
   return mbar_wait_warp(bar, parity, wc, hdr);
 }
 
-// Document [first, last) of stream row t0 + lane, for a whole warp (rows at or
+// Document [first, last) of stream row t0 + (lane >> shift), for a whole warp (rows at or
 // past `rows` get the document of the last row below): the warp narrows the
 // search 32-fold with each load, then reads the next documents' starts in one:
 // three dependent loads for a thousand documents instead of ten.
@@ -60,7 +60,7 @@ struct Span32 {
   int first, last;
 };
 __device__ __forceinline__ Span32 document_of_rows(const int32_t* __restrict__ cu, int ndoc, int64_t t0,
-                                                   int64_t rows, int lane) {
+                                                   int64_t rows, int lane, int shift = 0) {
   int lo = 0, m = ndoc;                              // the first row's document is in [lo, lo + m)
   while (m > 1) {
     const int step = (m + 31) >> 5, at = lo + lane * step;
@@ -69,7 +69,7 @@ __device__ __forceinline__ Span32 document_of_rows(const int32_t* __restrict__ c
     lo += top * step;
     m = min(step, m - top * step);
   }
-  const int64_t t = min(t0 + lane, rows - 1);
+  const int64_t t = min(t0 + (lane >> shift), rows - 1);
   const int at = lo + lane;
   const int start = at <= ndoc ? __ldg(cu + at) : INT_MAX;
   int n = 0;                                         // starts passed by row t
@@ -185,12 +185,22 @@ constexpr size_t smem_bytes() {
   return sizeof(S) + 1024 <= kSmemLimit ? sizeof(S) + 1024 : kSmemLimit;
 }
 
-// 2-D tiled store of one box from shared memory (rows past the map's end are
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Tiled store of one box from shared memory (rows past the map's end are
 // not written), tracked by the issuing thread's bulk groups.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x, int y,
+                                             int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(smem_src)), "r"(x), "r"(y)
+               "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
                : "memory");
 }
 
