@@ -28,7 +28,8 @@
 // 16384 tokens in 19 causal documents, 16 heads on 4, d = 128 (540 TFLOP/s of the
 // visible pairs' 8 d).
 //
-// dQ kernel (query-stationary).  Work item: one 128-row query tile of one head.
+// dQ kernel (query-stationary).  Work item: 128 query rows, several heads of a group
+// at fewer tokens (QueryItem).
 // TMEM: S_1 [0,128), S_2 [128,256), dP [256,384), dQ_1 | dQ_2 [384,384+D).  dS_m
 // (bf16) goes over S_m and is read from TMEM.  The softmax keeps dP of a tile
 // in registers for both maps; while it is on one map the tensor core does the
@@ -58,8 +59,8 @@ struct BwdArgs {
   const float *coef, *cndelta;      // [Hq][Tp]: c, -c delta_2
   int64_t Tp;
   __nv_bfloat16 *dq, *dk, *dv;
-  const int2* qtiles;               // per 128-row query tile: first/last 128-key tile
-  const int* qorder;
+  const int* qorder;                // 128-token tiles of queries, most keys first
+  int shift;                        // log2 of the heads of a query item
   const int2* ktiles;               // per 128-key tile: first/last 128-row query tile
   const int* korder;
 };
@@ -545,10 +546,6 @@ constexpr int kQThreads = 320;
 constexpr int kQWarpProducer = 8, kQWarpMma = 9;
 constexpr int K_NS = 2;
 
-struct QItem {
-  int qtile, h, g, j_lo, n_kv, pad[3];     // n_kv 128-key tiles; -1 stops
-};
-
 struct __align__(1024) SmemQ {
   uint8_t q[2][kTile], dout[2][kTile];     // this item's and the next one's
   uint8_t k[K_NS][kTile];
@@ -557,7 +554,7 @@ struct __align__(1024) SmemQ {
   uint64_t k_full[K_NS], k_empty[K_NS], v_full, v_empty;
   uint64_t s_full[2], p_full[2], dp_full, dp_free, o_full, o_free;
   uint64_t item_full[2], item_empty[2];
-  QItem items[2];
+  QueryItem items[2];
   uint64_t drain;
   uint32_t tmem_base;
   WaitCtl wait;
@@ -629,7 +626,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
 
   const uint32_t tmem = sm.tmem_base;
   WaitCtl* const wc = &sm.wait;
-  const int G = p.Hq / p.Hkv;
   const int n_items = hdr->n_items * p.Hq;
   constexpr int kBlocks = D / 64;
   constexpr uint32_t kLoad = kBlocks * kBlk;
@@ -641,17 +637,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
       bool ok = true;
       while (ok) {
         const int idx = atomicAdd(&hdr->counter, 1);
-        QItem it = {};
+        QueryItem it = {};
         it.n_kv = -1;
-        if (idx < n_items) {
-          const int qt = a.qorder[idx / p.Hq];
-          const int2 tr = a.qtiles[qt];
-          it.qtile = qt;
-          it.h = idx % p.Hq;
-          it.g = it.h / G;
-          it.j_lo = tr.x;
-          it.n_kv = tr.y - tr.x + 1;
-        }
+        if (idx < n_items && !query_item(it, p, a.qorder, idx, a.shift)) continue;
         const uint32_t slot = it_count & 1, use = it_count >> 1;
         if (use >= 1 && !mbar_wait(&sm.item_empty[slot], (use - 1) & 1, wc, hdr)) break;
         sm.items[slot] = it;
@@ -661,13 +649,12 @@ __global__ void __launch_bounds__(kQThreads, 1)
         mbar_arrive_expect_tx(&sm.q_full[slot], 2 * kLoad);
 #pragma unroll
         for (int cb = 0; cb < kBlocks; ++cb) {
-          tma_load_2d(sm.q[slot] + cb * kBlk, &tm_q, &sm.q_full[slot], it.h * D + cb * 64, it.qtile * 128);
-          tma_load_2d(sm.dout[slot] + cb * kBlk, &tm_do, &sm.q_full[slot], it.h * D + cb * 64,
-                      it.qtile * 128);
+          tma_load_3d(sm.q[slot] + cb * kBlk, &tm_q, &sm.q_full[slot], cb * 64, it.h0, it.t0);
+          tma_load_3d(sm.dout[slot] + cb * kBlk, &tm_do, &sm.q_full[slot], cb * 64, it.h0, it.t0);
         }
         ++it_count;
         for (int jj = 0; jj < it.n_kv; ++jj) {
-          const int key0 = (it.j_lo + jj) * 128;
+          const int key0 = it.lo + jj * 128;
           const uint32_t st = k_count % K_NS, n = k_count / K_NS;
           if (n >= 1 && !mbar_wait(&sm.k_empty[st], (n - 1) & 1, wc, hdr)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.k_full[st], kLoad);
@@ -699,7 +686,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       while (true) {
         const uint32_t slot = it_count & 1, use = it_count >> 1;
         if (!wait_one(&sm.item_full[slot], use & 1, wc, hdr)) break;
-        const QItem it = sm.items[slot];
+        const QueryItem it = sm.items[slot];
         mbar_arrive(&sm.item_empty[slot]);
         if (it.n_kv < 0) break;
         if (!wait_one(&sm.q_full[slot], use & 1, wc, hdr)) break;
@@ -759,7 +746,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     uint32_t it_count = 0, jc = 0;
     // the next item's row is found, and its vectors read, under the current item
-    QItem it;
+    QueryItem it;
+    const int hr = r & ((1 << a.shift) - 1), tr = r >> a.shift;    // the row's head and token in the item
     int lo, hi;                                              // visible keys [lo, hi)
     float nl[2], nd[2], c;
     auto next_item = [&](uint32_t n) {
@@ -769,17 +757,19 @@ __global__ void __launch_bounds__(kQThreads, 1)
       lo = hi = 0;
       nl[0] = nl[1] = nd[0] = nd[1] = c = 0.f;
       if (it.n_kv < 0) return true;
-      const int64_t row0 = (int64_t)it.qtile * 128 + wq * 32, row = row0 + lane;
-      const Span32 doc = document_of_rows(p.cu, p.ndoc, row0, p.q_len, lane);
+      const int64_t row = (int64_t)it.t0 + tr;
+      const Span32 doc = document_of_rows(p.cu, p.ndoc, (int64_t)it.t0 + ((wq * 32) >> a.shift), p.q_len,
+                                          lane, a.shift);
       if (row < p.q_len) {
         lo = doc.first;
         hi = p.causal ? (int)row + 1 : (int)min((int64_t)doc.last, p.kv_len);
-        const int64_t v1 = (int64_t)(2 * it.h) * a.Tp + row;
+        const int h = it.h0 + hr;
+        const int64_t v1 = (int64_t)(2 * h) * a.Tp + row;
         nl[0] = __ldg(a.nlse2 + v1);
         nl[1] = __ldg(a.nlse2 + v1 + a.Tp);
         nd[0] = __ldg(a.ndelta + v1);
-        nd[1] = __ldg(a.cndelta + (int64_t)it.h * a.Tp + row);
-        c = __ldg(a.coef + (int64_t)it.h * a.Tp + row);
+        nd[1] = __ldg(a.cndelta + (int64_t)h * a.Tp + row);
+        c = __ldg(a.coef + (int64_t)h * a.Tp + row);
       }
       return true;
     };
@@ -787,7 +777,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     bool ok = true;
     while (it.n_kv >= 0) {
       for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
-        const int key0 = (it.j_lo + jj) * 128 + wg * 64;
+        const int key0 = it.lo + jj * 128 + wg * 64;
         const bool full_w = __all_sync(0xffffffffu, lo <= key0 && key0 + 64 <= hi);
         uint32_t dp[64];
 #pragma unroll
@@ -855,8 +845,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
       }
       if (!ok) break;
       // epilogue: map wg of the row's gradient
-      const int64_t row = (int64_t)it.qtile * 128 + r;
-      __nv_bfloat16* const dst = a.dq + (row * p.Hq + it.h) * D + wg * (D / 2);
+      const int64_t row = (int64_t)it.t0 + tr;
+      __nv_bfloat16* const dst = a.dq + (row * p.Hq + it.h0 + hr) * D + wg * (D / 2);
       if (!next_item(it_count + 1)) break;
       if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
       tc_fence_after();
@@ -885,23 +875,27 @@ __global__ void __launch_bounds__(kQThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
-                     const CUtensorMap& mv, const BwdArgs& a, cudaStream_t s) {
+cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mqh,
+                     const CUtensorMap& mdoh, const CUtensorMap& mk, const CUtensorMap& mv, const BwdArgs& a,
+                     cudaStream_t s) {
   const cudaError_t e = launch_persistent<2 * D>(diff_bwd_dkdv_tc_kernel<D>, kKvThreads,
                                                  smem_bytes<SmemKV>(), s, mq, mdo, mk, mv, a);
   if (e != cudaSuccess) return e;
-  return launch_persistent<2 * D + 1>(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), s, mq,
-                                      mdo, mk, mv, a);
+  return launch_persistent<2 * D + 1>(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), s, mqh,
+                                      mdoh, mk, mv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char* ws, cudaStream_t s) {
   const AttnProblem& p = d.p;
-  CUtensorMap mq, mdo, mk, mv;
+  CUtensorMap mq, mdo, mk, mv, mqh, mdoh;
+  const int shift = item_shift(p.Hq / p.Hkv);
   const int64_t qc = (int64_t)p.Hq * p.d, kc = (int64_t)p.Hkv * p.d;
   if (!diff_tile_map(&mq, p.q, p.q_len, qc) || !diff_tile_map(&mdo, d.dout, p.q_len, qc) ||
-      !diff_tile_map(&mk, p.k, p.kv_len, kc) || !diff_tile_map(&mv, p.v, p.kv_len, kc))
+      !diff_tile_map(&mk, p.k, p.kv_len, kc) || !diff_tile_map(&mv, p.v, p.kv_len, kc) ||
+      !diff_heads_map(&mqh, p.q, p.q_len, p.Hq, p.d, 1 << shift) ||
+      !diff_heads_map(&mdoh, d.dout, p.q_len, p.Hq, p.d, 1 << shift))
     return cudaErrorNotSupported;
   BwdArgs a;
   a.p = p;
@@ -909,11 +903,12 @@ cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char*
   a.dq = reinterpret_cast<__nv_bfloat16*>(d.dq);
   a.dk = reinterpret_cast<__nv_bfloat16*>(d.dk);
   a.dv = reinterpret_cast<__nv_bfloat16*>(d.dv);
-  a.qtiles = reinterpret_cast<const int2*>(ws + L.qtiles);
+  a.shift = shift;
   a.qorder = reinterpret_cast<const int*>(ws + L.qorder);
   a.ktiles = reinterpret_cast<const int2*>(ws + L.ktiles);
   a.korder = reinterpret_cast<const int*>(ws + L.korder);
-  return p.d == 128 ? launch_d<128>(mq, mdo, mk, mv, a, s) : launch_d<64>(mq, mdo, mk, mv, a, s);
+  return p.d == 128 ? launch_d<128>(mq, mdo, mqh, mdoh, mk, mv, a, s)
+                    : launch_d<64>(mq, mdo, mqh, mdoh, mk, mv, a, s);
 }
 
 }  // namespace nsp

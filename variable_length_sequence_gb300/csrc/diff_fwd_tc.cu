@@ -59,18 +59,12 @@ using namespace tc;
 
 constexpr int BM = 128, BN = 128;
 constexpr int NSTAGE = 2;
-constexpr int kMaxItemHeads = 8;
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 200, kRegsControl = 104;
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpStore = 10;
 __host__ __device__ constexpr uint32_t col_s(int m) { return m == 0 ? 0u : 128u; }
 __host__ __device__ constexpr uint32_t col_o(int m) { return m == 0 ? 256u : 384u; }
 constexpr float kRescaleThreshold = 8.0f;                 // log2 units
-
-struct Item {
-  int t0, h0, g, lo, n_kv;             // first token and head; n_kv 128-key tiles from key lo; -1 stops
-  int pad[3];
-};
 
 struct __align__(1024) Smem {
   uint8_t q[2][kTile];                 // this item's and the next one's; then out2's tile
@@ -82,7 +76,7 @@ struct __align__(1024) Smem {
   uint64_t k_full[NSTAGE], k_empty[NSTAGE], v_full[NSTAGE], v_empty[NSTAGE];
   uint64_t s_full[2], p_full[2], o_full, o_free, inv_full, out_full, out_free;
   uint64_t item_full[2], item_empty[2];
-  Item items[2];
+  QueryItem items[2];
   uint64_t mma_drain_bar;
   uint32_t tmem_base;
   WaitCtl wait;
@@ -189,9 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const uint32_t tmem = sm.tmem_base;
   WaitCtl* const wc = &sm.wait;
-  const int G = p.Hq / p.Hkv;
   const int n_items = hdr->n_items * p.Hq;
-  const int heads = 1 << a.shift, tokens = BM >> a.shift;       // of an item
   constexpr int kBlocks = D / 64;                               // 64-column blocks of a row
   constexpr uint32_t kLoadBytes = kBlocks * kBlk;          // one Q, K or V tile
 
@@ -203,19 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok) {
         const int idx = atomicAdd(&hdr->counter, 1);
-        Item it = {};
+        QueryItem it = {};
         it.n_kv = -1;
-        if (idx < n_items) {
-          const int rest = idx % p.Hq;
-          it.t0 = a.order[idx / p.Hq] * BM + (rest & (heads - 1)) * tokens;
-          if (it.t0 >= p.q_len) continue;            // (the last tile may be short)
-          it.h0 = rest & ~(heads - 1);
-          it.g = it.h0 / G;
-          const int end = (int)min((int64_t)it.t0 + tokens, p.q_len);
-          it.lo = __ldg(p.cu + doc_of(p.cu, p.ndoc, it.t0));
-          const int hi = p.causal ? end : __ldg(p.cu + doc_of(p.cu, p.ndoc, end - 1) + 1);
-          it.n_kv = (hi - it.lo + BN - 1) / BN;
-        }
+        if (idx < n_items && !query_item(it, p, a.order, idx, a.shift)) continue;
         // items alternate over two slots of the queue and of Q
         const uint32_t slot = it_count & 1, use = it_count >> 1;
         if (use >= 1 && !mbar_wait(&sm.item_empty[slot], (use - 1) & 1, wc, hdr)) break;
@@ -261,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (true) {
         const uint32_t slot = it_count & 1, use = it_count >> 1;
         if (!wait_one(&sm.item_full[slot], use & 1, wc, hdr)) break;
-        const Item it = sm.items[slot];
+        const QueryItem it = sm.items[slot];
         mbar_arrive(&sm.item_empty[slot]);
         if (it.n_kv < 0) break;
         if (!wait_one(&sm.q_full[slot], use & 1, wc, hdr)) break;
@@ -322,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (true) {
         const uint32_t slot = it_count & 1;
         if (!mbar_wait(&sm.item_full[slot], (it_count >> 1) & 1, wc, hdr)) break;
-        const Item it = sm.items[slot];
+        const QueryItem it = sm.items[slot];
         mbar_arrive(&sm.item_empty[slot]);
         if (it.n_kv < 0) break;
         if (!mbar_wait(&sm.out_full, it_count & 1, wc, hdr)) break;
@@ -355,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it_count = 0, s_count = 0;
     // An item's rows are found (a search of some 1400 cycles) while the item before
     // it waits for its last product.
-    Item it;
+    QueryItem it;
     Span32 doc = {0, 0};
     auto next_item = [&](uint32_t n) {
       if (!wait_warp(&sm.item_full[n & 1], (n >> 1) & 1, wc, hdr)) return false;
@@ -368,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!next_item(0)) it.n_kv = -1;
     while (it.n_kv >= 0) {
       const uint32_t slot = it_count & 1;
-      const int h = it.h0 + (r & (heads - 1));
+      const int h = it.h0 + (r & ((1 << a.shift) - 1));
       const int64_t row = (int64_t)it.t0 + (r >> a.shift);
       const bool valid = row < p.q_len;
       int lo = 0, hi = 0;                                      // visible keys [lo, hi)
@@ -503,8 +485,7 @@ cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
 
 }  // namespace
 
-namespace {
-bool encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+static bool encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                 const cuuint64_t* strides, const cuuint32_t* box) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* ptr = nullptr;
@@ -523,13 +504,12 @@ bool encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* di
 
 // [T, H, d] bf16, box = 64 columns x `heads` heads x 128 / heads tokens, 128-byte swizzle:
 // row r of the tile is token r / heads, head r % heads.
-bool heads_map(CUtensorMap* m, const void* base, int64_t T, int64_t H, int64_t d, int heads) {
+bool diff_heads_map(CUtensorMap* m, const void* base, int64_t T, int64_t H, int64_t d, int heads) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)(d * 2), (cuuint64_t)(H * d * 2)};
   const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(BM / heads)};
   return encode_map(m, base, 3, dims, strides, box);
 }
-}  // namespace
 
 // [rows, cols] bf16 row-major, box = 64 columns x 128 rows, 128-byte swizzle.
 bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
@@ -542,14 +522,12 @@ bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols)
 cudaError_t launch_diff_fwd_tc(const DiffProblem& d, const FwdWsLayout& L, char* ws, cudaStream_t s) {
   const AttnProblem& p = d.p;
   CUtensorMap mq, mk, mv, mo, mo2;
-  // heads of an item: the group's power of two, kMaxItemHeads at most
-  int shift = 0;
-  while ((2 << shift) <= kMaxItemHeads && p.Hq / p.Hkv % (2 << shift) == 0) ++shift;
-  if (!heads_map(&mq, p.q, p.q_len, p.Hq, p.d, 1 << shift) ||
+  const int shift = item_shift(p.Hq / p.Hkv);
+  if (!diff_heads_map(&mq, p.q, p.q_len, p.Hq, p.d, 1 << shift) ||
       !diff_tile_map(&mk, p.k, p.kv_len, (int64_t)p.Hkv * p.d) ||
       !diff_tile_map(&mv, p.v, p.kv_len, (int64_t)p.Hkv * p.d) ||
-      !heads_map(&mo, p.out, p.q_len, p.Hq, p.d, 1 << shift) ||
-      !heads_map(&mo2, d.out2 ? d.out2 : p.out, p.q_len, p.Hq, p.d, 1 << shift))
+      !diff_heads_map(&mo, p.out, p.q_len, p.Hq, p.d, 1 << shift) ||
+      !diff_heads_map(&mo2, d.out2 ? d.out2 : p.out, p.q_len, p.Hq, p.d, 1 << shift))
     return cudaErrorNotSupported;
   FwdArgs a;
   a.p = p;

@@ -89,6 +89,38 @@ __device__ __forceinline__ Span32 document_of_rows(const int32_t* __restrict__ c
   return d;
 }
 
+// Work item of the query-stationary kernels: 128 query rows, 2^shift heads of one
+// group at 128 >> shift consecutive tokens (row r is token t0 + (r >> shift), head
+// h0 + r % 2^shift), against n_kv 128-key tiles from key lo, the start of the first
+// token's document; n_kv = -1 stops.
+constexpr int kMaxItemHeads = 8;
+struct QueryItem {
+  int t0, h0, g, lo, n_kv;
+  int pad[3];
+};
+
+inline int item_shift(int group) {
+  int shift = 0;
+  while ((2 << shift) <= kMaxItemHeads && group % (2 << shift) == 0) ++shift;
+  return shift;
+}
+
+// Item idx (128-token tiles in `order`, Hq items each); false when its tokens lie past
+// the stream (the last tile may be short).
+__device__ __forceinline__ bool query_item(QueryItem& it, const AttnProblem& p, const int* order, int idx,
+                                           int shift) {
+  const int rest = idx % p.Hq, part = rest & ((1 << shift) - 1), tokens = 128 >> shift;
+  it.t0 = order[idx / p.Hq] * 128 + part * tokens;
+  if (it.t0 >= p.q_len) return false;
+  it.h0 = rest - part;
+  it.g = it.h0 / (p.Hq / p.Hkv);
+  const int end = (int)min((int64_t)it.t0 + tokens, p.q_len);
+  it.lo = __ldg(p.cu + doc_of(p.cu, p.ndoc, it.t0));
+  const int hi = p.causal ? end : __ldg(p.cu + doc_of(p.cu, p.ndoc, end - 1) + 1);
+  it.n_kv = (hi - it.lo + 127) / 128;
+  return true;
+}
+
 // D = A B^T over columns [m HK, (m + 1) HK) of K-major 128-row tiles (128-byte
 // swizzle: 16 columns are 32 bytes of a row, 64 columns one column block).
 template <int HK>

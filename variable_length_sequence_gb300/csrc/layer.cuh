@@ -79,6 +79,7 @@ cudaError_t launch_diff_fwd_tc(const DiffProblem& a, const FwdWsLayout& L, char*
 // A map of [rows, cols] bf16 whose copies are 128 rows of 64 columns, 128-byte
 // swizzled; false without tensor-map support in the driver.
 bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols);
+bool diff_heads_map(CUtensorMap* m, const void* base, int64_t T, int64_t H, int64_t d, int heads);
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s);
 cudaError_t launch_diff_bwd_tc(const DiffProblem& a, const BwdWsLayout& L, char* ws, cudaStream_t s);
 cudaError_t launch_diff_bwd_simt(const DiffProblem& a, cudaStream_t s);
