@@ -10,8 +10,8 @@
 //   dV = (P_1 + c P_2)^T dOut,  dK_m = scale dS_m^T Q_m,  dQ_m = scale dS_m K_m.
 //
 // dK/dV kernel (key-stationary).  Work item: one 128-key tile of one KV head;
-// it walks every pair (query head of the group, 128-row query tile that can
-// see the keys).  A pair costs four 128 x 128 x 128 products' worth: S_1 and
+// it walks every pair (2^shift query heads of the group, tile of 128 >> shift
+// tokens of them that can see the keys).  A pair costs four 128 x 128 x 128 products' worth: S_1 and
 // S_2 (half the columns each), dP, dV (both maps in one product, their
 // combination is its operand), dK_1 and dK_2 (half the columns each); treating
 // the maps as two heads would cost six.  TMEM: two 128-column regions [0,256),
@@ -55,13 +55,12 @@ using namespace tc;
 
 struct BwdArgs {
   AttnProblem p;
-  const float *nlse2, *ndelta;      // [2 Hq][Tp]
-  const float *coef, *cndelta;      // [Hq][Tp]: c, -c delta_2
+  const float *nlse2, *ndelta;      // [Hq / P][2][Tp][P], P = 2^shift
+  const float *coef, *cndelta;      // [Hq / P][Tp][P]: c, -c delta_2
   int64_t Tp;
   __nv_bfloat16 *dq, *dk, *dv;
   const int* qorder;                // 128-token tiles of queries, most keys first
   int shift;                        // log2 of the heads of a query item
-  const int2* ktiles;               // per 128-key tile: first/last 128-row query tile
   const int* korder;
 };
 
@@ -73,7 +72,9 @@ constexpr int kKvWarpTiles = 16, kKvWarpMma1 = 17, kKvWarpMma2 = 18, kKvWarpRows
 constexpr int kKvRegsControl = 64, kKvRegsSoftmax = 104;   // 128 x 64 + 512 x 104 = 640 x 96
 
 struct KvItem {
-  int ktile, g, i_lo, n_q, pairs, pad[3];    // pairs = heads * n_q; -1 stops
+  // n_q query tiles (128 >> shift tokens of 2^shift heads) from row q_lo = token << shift on;
+  // pairs = head groups * n_q; -1 stops
+  int ktile, g, q_lo, n_q, pairs, pad[3];
 };
 
 struct __align__(1024) SmemKV {
@@ -188,13 +189,16 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         KvItem it = {};
         it.pairs = -1;
         if (idx < n_items) {
-          const int kt = a.korder[idx / p.Hkv];
-          const int2 tr = a.ktiles[kt];
-          it.ktile = kt;
+          it.ktile = a.korder[idx / p.Hkv];
           it.g = idx % p.Hkv;
-          it.i_lo = tr.x;
-          it.n_q = tr.y - tr.x + 1;
-          it.pairs = G * it.n_q;
+          const int key0 = it.ktile * 128;
+          const int64_t last = min((int64_t)key0 + 128, p.kv_len) - 1;
+          const int first = p.causal ? key0 : __ldg(p.cu + doc_of(p.cu, p.ndoc, key0));
+          const int end = __ldg(p.cu + doc_of(p.cu, p.ndoc, last) + 1);
+          // (a multiple of a tile's tokens: the row vectors are read in whole tiles)
+          it.q_lo = (first << a.shift) & ~127;
+          it.n_q = ((end << a.shift) - it.q_lo + 127) >> 7;
+          it.pairs = (G >> a.shift) * it.n_q;
         }
         const uint32_t slot = it_count & 1;
         if (it_count >= 2 && !mbar_wait(&sm.item_empty[slot], ((it_count >> 1) - 1) & 1, wc, hdr))
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           tma_load_2d(sm.v + cb * kBlk, &tm_v, &sm.kv_full, it.g * D + cb * 64, it.ktile * 128);
         }
         ++kv_count;
-        int h = it.g * G, i = it.i_lo;
+        int h = it.g * G, i = 0;
         for (int n = 0; n < it.pairs && ok; ++n) {
           const uint32_t fill = qc >> 1;
 #pragma unroll
@@ -225,12 +229,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             mbar_arrive_expect_tx(&sm.slot_full[s], kLoad);
 #pragma unroll
             for (int cb = 0; cb < kBlocks; ++cb)
-              tma_load_2d(sm.qd[s] + cb * kBlk, t == 0 ? &tm_q : &tm_do, &sm.slot_full[s],
-                          h * D + cb * 64, i * 128);
+              tma_load_3d(sm.qd[s] + cb * kBlk, t == 0 ? &tm_q : &tm_do, &sm.slot_full[s], cb * 64, h,
+                          (it.q_lo + i * 128) >> a.shift);
             ++loads;
           }
           ++qc;
-          if (++i == it.i_lo + it.n_q) { i = it.i_lo; ++h; }
+          if (++i == it.n_q) { i = 0; h += 1 << a.shift; }
         }
       }
       // leaving, normally or on an abort: every issued copy lands first
@@ -253,9 +257,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_arrive(&sm.item_empty[slot]);
         ++it_count;
         if (it.pairs < 0) break;
-        int h = it.g * G, i = it.i_lo;
+        int h = it.g * G, i = 0;
         for (int n = 0; n < it.pairs; ++n) {
-          const int64_t r1 = (int64_t)(2 * h) * a.Tp + (int64_t)i * 128, r2 = r1 + a.Tp;
+          const int64_t hg = h >> a.shift, np = a.Tp << a.shift, q0 = it.q_lo + (int64_t)i * 128;
+          const int64_t r1 = 2 * hg * np + q0, r2 = r1 + np;
           if (n1 >= 1 && !mbar_wait(&sm.ds_ready, (n1 - 1) & 1, wc, hdr)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.first_full, 2 * 512);
           bulk_load(sm.first[0], a.nlse2 + r1, 512, &sm.first_full);
@@ -264,11 +269,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           if (n2 >= 1 && !mbar_wait(&sm.p_ready, (n2 - 1) & 1, wc, hdr)) { ok = false; break; }
           mbar_arrive_expect_tx(&sm.second_full, 3 * 512);
           bulk_load(sm.second[0], a.nlse2 + r2, 512, &sm.second_full);
-          const int64_t rc = (int64_t)h * a.Tp + (int64_t)i * 128;
+          const int64_t rc = hg * np + q0;
           bulk_load(sm.second[1], a.cndelta + rc, 512, &sm.second_full);
           bulk_load(sm.second[2], a.coef + rc, 512, &sm.second_full);
           ++n2;
-          if (++i == it.i_lo + it.n_q) { i = it.i_lo; ++h; }
+          if (++i == it.n_q) { i = 0; h += 1 << a.shift; }
         }
       }
       if (n1 >= 1) drain_wait(&sm.first_full, (n1 - 1) & 1);
@@ -384,15 +389,15 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       mbar_arrive_warp(&sm.item_empty[slot], lane);
       ++it_count;
       if (it.pairs < 0) break;
-      int qlo[4], qhi[4];                                  // queries that see fragment row i
+      int qlo[4], qhi[4];                                  // query rows that see fragment row i
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t key = (int64_t)it.ktile * 128 + wq * 32 + tr + 8 * i;
         qlo[i] = qhi[i] = 0;
         if (key < p.kv_len) {
           const int b = doc_of(p.cu, p.ndoc, key);
-          qlo[i] = p.causal ? (int)key : __ldg(p.cu + b);
-          qhi[i] = (int)min((int64_t)__ldg(p.cu + b + 1), p.q_len);
+          qlo[i] = (p.causal ? (int)key : __ldg(p.cu + b)) << a.shift;
+          qhi[i] = (int)min((int64_t)__ldg(p.cu + b + 1), p.q_len) << a.shift;
         }
       }
       // queries that see every row of the thread
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       const int all_hi = min(min(qhi[0], qhi[1]), min(qhi[2], qhi[3]));
       int n_in = 0;                                        // query tile of the pair, 0 .. n_q - 1
       for (int n = 0; n < it.pairs; ++n) {
-        const int q0 = (it.i_lo + n_in) * 128 + cg * 32;
+        const int q0 = it.q_lo + n_in * 128 + cg * 32;
         if (++n_in == it.n_q) n_in = 0;
         const uint32_t rb = qc & 1;
         const uint32_t s_tm = tmem + lane_base + 128 * rb + cg * 32;
@@ -763,13 +768,13 @@ __global__ void __launch_bounds__(kQThreads, 1)
       if (row < p.q_len) {
         lo = doc.first;
         hi = p.causal ? (int)row + 1 : (int)min((int64_t)doc.last, p.kv_len);
-        const int h = it.h0 + hr;
-        const int64_t v1 = (int64_t)(2 * h) * a.Tp + row;
+        const int64_t hg = it.h0 >> a.shift, np = a.Tp << a.shift, j = ((int64_t)it.t0 << a.shift) + r;
+        const int64_t v1 = 2 * hg * np + j;
         nl[0] = __ldg(a.nlse2 + v1);
-        nl[1] = __ldg(a.nlse2 + v1 + a.Tp);
+        nl[1] = __ldg(a.nlse2 + v1 + np);
         nd[0] = __ldg(a.ndelta + v1);
-        nd[1] = __ldg(a.cndelta + (int64_t)h * a.Tp + row);
-        c = __ldg(a.coef + (int64_t)h * a.Tp + row);
+        nd[1] = __ldg(a.cndelta + hg * np + j);
+        c = __ldg(a.coef + hg * np + j);
       }
       return true;
     };
@@ -875,27 +880,24 @@ __global__ void __launch_bounds__(kQThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mqh,
-                     const CUtensorMap& mdoh, const CUtensorMap& mk, const CUtensorMap& mv, const BwdArgs& a,
-                     cudaStream_t s) {
+cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
+                     const CUtensorMap& mv, const BwdArgs& a, cudaStream_t s) {
   const cudaError_t e = launch_persistent<2 * D>(diff_bwd_dkdv_tc_kernel<D>, kKvThreads,
                                                  smem_bytes<SmemKV>(), s, mq, mdo, mk, mv, a);
   if (e != cudaSuccess) return e;
-  return launch_persistent<2 * D + 1>(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), s, mqh,
-                                      mdoh, mk, mv, a);
+  return launch_persistent<2 * D + 1>(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), s, mq,
+                                      mdo, mk, mv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char* ws, cudaStream_t s) {
   const AttnProblem& p = d.p;
-  CUtensorMap mq, mdo, mk, mv, mqh, mdoh;
-  const int shift = item_shift(p.Hq / p.Hkv);
-  const int64_t qc = (int64_t)p.Hq * p.d, kc = (int64_t)p.Hkv * p.d;
-  if (!diff_tile_map(&mq, p.q, p.q_len, qc) || !diff_tile_map(&mdo, d.dout, p.q_len, qc) ||
-      !diff_tile_map(&mk, p.k, p.kv_len, kc) || !diff_tile_map(&mv, p.v, p.kv_len, kc) ||
-      !diff_heads_map(&mqh, p.q, p.q_len, p.Hq, p.d, 1 << shift) ||
-      !diff_heads_map(&mdoh, d.dout, p.q_len, p.Hq, p.d, 1 << shift))
+  CUtensorMap mq, mdo, mk, mv;
+  const int64_t kc = (int64_t)p.Hkv * p.d;
+  if (!diff_tile_map(&mk, p.k, p.kv_len, kc) || !diff_tile_map(&mv, p.v, p.kv_len, kc) ||
+      !diff_heads_map(&mq, p.q, p.q_len, p.Hq, p.d, 1 << d.shift) ||
+      !diff_heads_map(&mdo, d.dout, p.q_len, p.Hq, p.d, 1 << d.shift))
     return cudaErrorNotSupported;
   BwdArgs a;
   a.p = p;
@@ -903,12 +905,10 @@ cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char*
   a.dq = reinterpret_cast<__nv_bfloat16*>(d.dq);
   a.dk = reinterpret_cast<__nv_bfloat16*>(d.dk);
   a.dv = reinterpret_cast<__nv_bfloat16*>(d.dv);
-  a.shift = shift;
+  a.shift = d.shift;
   a.qorder = reinterpret_cast<const int*>(ws + L.qorder);
-  a.ktiles = reinterpret_cast<const int2*>(ws + L.ktiles);
   a.korder = reinterpret_cast<const int*>(ws + L.korder);
-  return p.d == 128 ? launch_d<128>(mq, mdo, mqh, mdoh, mk, mv, a, s)
-                    : launch_d<64>(mq, mdo, mqh, mdoh, mk, mv, a, s);
+  return p.d == 128 ? launch_d<128>(mq, mdo, mk, mv, a, s) : launch_d<64>(mq, mdo, mk, mv, a, s);
 }
 
 }  // namespace nsp

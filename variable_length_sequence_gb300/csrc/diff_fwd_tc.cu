@@ -522,7 +522,7 @@ bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols)
 cudaError_t launch_diff_fwd_tc(const DiffProblem& d, const FwdWsLayout& L, char* ws, cudaStream_t s) {
   const AttnProblem& p = d.p;
   CUtensorMap mq, mk, mv, mo, mo2;
-  const int shift = item_shift(p.Hq / p.Hkv);
+  const int shift = d.shift;
   if (!diff_heads_map(&mq, p.q, p.q_len, p.Hq, p.d, 1 << shift) ||
       !diff_tile_map(&mk, p.k, p.kv_len, (int64_t)p.Hkv * p.d) ||
       !diff_tile_map(&mv, p.v, p.kv_len, (int64_t)p.Hkv * p.d) ||

@@ -5,9 +5,9 @@
 // O_2 saved by the forward:
 //   delta_2 = <dout, out2>,  delta_1 = <dout, out> + lambda delta_2,
 //   dlambda = -delta_2 (of each token), or its sum over the tokens.
-// Written as [2 Hq][Tp] rows (-delta, -lse log2 e) and [Hq][Tp] (c = -lambda, the
-// factor of the second map's probabilities, and -c delta_2), padded with zeros to whole
-// 128-row tiles.  Bound: HBM, one read of out, out2 and dout: 201 MB of 16384 tokens,
+// Written as [Hq / P][2][Tp][P] (-delta, -lse log2 e) and [Hq / P][Tp][P] (c = -lambda,
+// the factor of the second map's probabilities, and -c delta_2) for the P = 2^shift
+// heads of a query item, padded with zeros to whole 128-row tiles.  Bound: HBM, one read of out, out2 and dout: 201 MB of 16384 tokens,
 // 16 heads, d = 128 in 37 us, 5.5 TB/s.
 #include <algorithm>
 
@@ -19,14 +19,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A warp takes kTokens consecutive tokens of one head (its warps the next heads'),
+// Rows in the order of the vectors: row j of a head group is token j >> shift, head
+// j % 2^shift.  A warp takes kRows consecutive ones (its neighbours the next groups'),
 // so that the values it writes are neighbours.
 template <typename T, int D>
 struct PrepShape {
   static constexpr int TPR = D / Vec<T>::N;                       // threads of a row
   static constexpr int RPW = 32 / TPR;                            // rows of a warp at once
   static constexpr int ROWS = 4;                                  // rows of a thread in flight
-  static constexpr int kTokens = RPW * ROWS;
+  static constexpr int kRows = RPW * ROWS;
 };
 
 template <typename T, int D>
@@ -39,26 +40,30 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
   const int lane = threadIdx.x & 31, sub = lane / S::TPR, part = lane % S::TPR;
   const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
-  const int64_t T_ = p.q_len, units = (T_ + S::kTokens - 1) / S::kTokens * p.Hq;
+  const int64_t T_ = p.q_len, n = T_ << a.shift, np = a.Tp << a.shift;
+  const int groups = p.Hq >> a.shift, last = (1 << a.shift) - 1;
+  const int64_t units = (n + S::kRows - 1) / S::kRows * groups;
   const T* O = reinterpret_cast<const T*>(a.fout);
   const T* O2 = reinterpret_cast<const T*>(a.out2);
   const T* G = reinterpret_cast<const T*>(a.dout);
   const T* L = reinterpret_cast<const T*>(a.lambda);
   for (int64_t u = warp; u < units; u += nwarps) {
-    const int64_t chunk = u / p.Hq, t0 = chunk * S::kTokens;
-    const int h = (int)(u - chunk * p.Hq);
+    const int64_t chunk = u / groups, j0 = chunk * S::kRows;
+    const int hg = (int)(u - chunk * groups);
     uint4 x[S::ROWS], y[S::ROWS], z[S::ROWS];
 #pragma unroll
     for (int k = 0; k < S::ROWS; ++k) {
-      const int64_t t = t0 + k * S::RPW + sub, off = (t * p.Hq + h) * D + part * N;
+      const int64_t j = j0 + k * S::RPW + sub;
+      const int h = (hg << a.shift) + (int)(j & last);
+      const int64_t off = ((j >> a.shift) * p.Hq + h) * D + part * N;
       x[k] = y[k] = z[k] = make_uint4(0, 0, 0, 0);
-      if (t < T_) {
+      if (j < n) {
         x[k] = ld_once(O + off);
         y[k] = ld_once(O2 + off);
         z[k] = ld_once(G + off);
       }
     }
-    float m0 = 0.f, m2 = 0.f;                      // of token t0 + lane (lanes below kTokens)
+    float m0 = 0.f, m2 = 0.f;                      // of row j0 + lane (lanes below kRows)
 #pragma unroll
     for (int k = 0; k < S::ROWS; ++k) {
       float v[N], w[N], g[N];
@@ -83,10 +88,11 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
         m2 = d2;
       }
     }
-    const int64_t t = t0 + lane;
-    if (lane >= S::kTokens || t >= T_) continue;
+    const int64_t j = j0 + lane, t = j >> a.shift;
+    const int h = (hg << a.shift) + (int)(j & last);
+    if (lane >= S::kRows || j >= n) continue;
     const float lam = to_f(L[(int64_t)h * a.n_lambda + (a.n_lambda > 1 ? t : 0)]);
-    const int64_t v1 = (int64_t)h * 2 * a.Tp + t, v2 = v1 + a.Tp, vc = (int64_t)h * a.Tp + t;
+    const int64_t v1 = (int64_t)hg * 2 * np + j, v2 = v1 + np, vc = (int64_t)hg * np + j;
     a.ndelta[v1] = -fmaf(lam, m2, m0);
     a.ndelta[v2] = -m2;
     a.nlse2[v1] = -kLog2e * __ldg(p.lse + (int64_t)h * 2 * T_ + t);
@@ -96,26 +102,27 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
     if (a.n_lambda > 1) st_out(reinterpret_cast<T*>(a.dlambda) + (int64_t)h * T_ + t, -m2);
   }
   // zero padding of the last tile's rows
-  const int pad = (int)(a.Tp - T_);
+  const int64_t pad = np - n;
   const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  for (int64_t e = tid; e < (int64_t)pad * p.Hq; e += (int64_t)gridDim.x * kThreads) {
-    const int64_t h = e / pad, t = T_ + (e - h * pad);
-    a.ndelta[h * 2 * a.Tp + t] = a.ndelta[(h * 2 + 1) * a.Tp + t] = 0.f;
-    a.nlse2[h * 2 * a.Tp + t] = a.nlse2[(h * 2 + 1) * a.Tp + t] = 0.f;
-    a.coef[h * a.Tp + t] = a.cndelta[h * a.Tp + t] = 0.f;
+  for (int64_t e = tid; e < pad * groups; e += (int64_t)gridDim.x * kThreads) {
+    const int64_t hg = e / pad, j = n + (e - hg * pad);
+    a.ndelta[hg * 2 * np + j] = a.ndelta[(hg * 2 + 1) * np + j] = 0.f;
+    a.nlse2[hg * 2 * np + j] = a.nlse2[(hg * 2 + 1) * np + j] = 0.f;
+    a.coef[hg * np + j] = a.cndelta[hg * np + j] = 0.f;
   }
 }
 
 // dlambda[h] = sum_t -delta_2, one block of a head, in one fixed order.
 template <typename T>
 __global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restrict__ ndelta,
-                                                            int64_t tokens, int64_t Tp, T* dlambda,
-                                                            const WsHeader* hdr) {
+                                                            int64_t tokens, int64_t Tp, int shift,
+                                                            T* dlambda, const WsHeader* hdr) {
   __shared__ float s[32];
   if (status_bad(hdr)) return;
-  const float* row = ndelta + ((int64_t)blockIdx.x * 2 + 1) * Tp;
+  const int hg = blockIdx.x >> shift;
+  const float* row = ndelta + (((int64_t)hg * 2 + 1) * Tp << shift) + (blockIdx.x - (hg << shift));
   float x = 0.f;
-  for (int64_t t = threadIdx.x; t < tokens; t += 1024) x += __ldcg(row + t);
+  for (int64_t t = threadIdx.x; t < tokens; t += 1024) x += __ldcg(row + (t << shift));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restr
 
 template <typename T, int D>
 cudaError_t prep_d(const DiffProblem& a, cudaStream_t s) {
-  const int64_t units = ceil_div(a.p.q_len, PrepShape<T, D>::kTokens) * a.p.Hq;
+  const int64_t units = ceil_div(a.p.q_len << a.shift, PrepShape<T, D>::kRows) * (a.p.Hq >> a.shift);
   const int64_t blocks = std::min<int64_t>(ceil_div(units, kThreads / 32), (int64_t)num_sms() * 8);
   diff_prep_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(a);
   count_launches(1);
@@ -143,7 +150,7 @@ cudaError_t prep(const DiffProblem& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t dlambda(const DiffProblem& a, cudaStream_t s) {
-  diff_dlambda_kernel<T><<<a.p.Hq, 1024, 0, s>>>(a.ndelta, a.p.q_len, a.Tp,
+  diff_dlambda_kernel<T><<<a.p.Hq, 1024, 0, s>>>(a.ndelta, a.p.q_len, a.Tp, a.shift,
                                                  reinterpret_cast<T*>(a.dlambda), a.p.hdr);
   count_launches(1);
   return cudaGetLastError();

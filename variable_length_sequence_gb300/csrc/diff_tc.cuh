@@ -93,17 +93,10 @@ __device__ __forceinline__ Span32 document_of_rows(const int32_t* __restrict__ c
 // group at 128 >> shift consecutive tokens (row r is token t0 + (r >> shift), head
 // h0 + r % 2^shift), against n_kv 128-key tiles from key lo, the start of the first
 // token's document; n_kv = -1 stops.
-constexpr int kMaxItemHeads = 8;
 struct QueryItem {
   int t0, h0, g, lo, n_kv;
   int pad[3];
 };
-
-inline int item_shift(int group) {
-  int shift = 0;
-  while ((2 << shift) <= kMaxItemHeads && group % (2 << shift) == 0) ++shift;
-  return shift;
-}
 
 // Item idx (128-token tiles in `order`, Hq items each); false when its tokens lie past
 // the stream (the last tile may be short).

@@ -70,15 +70,27 @@ struct DiffProblem {
   void* out2;                        // second map's output (forward: may be null)
   const void *fout, *dout;           // backward
   void *dq, *dk, *dv, *dlambda;
-  float *ndelta, *nlse2;             // backward workspace: [2 Hq][Tp]
-  float *coef, *cndelta;             // [Hq][Tp]
+  int shift;                         // log2 of the heads P of a query item (0 for float32)
+  float *ndelta, *nlse2;             // backward workspace: [Hq / P][2][Tp][P]
+  float *coef, *cndelta;             // [Hq / P][Tp][P]
   int64_t Tp;
   float *dk_heads, *dv_heads;        // float32 backward, Hq > Hkv: [T, Hq, d] shares of the heads
 };
+// Heads of a tensor-core query item: the power of two in a group's heads, 8 at most
+// (16 gained no more), and rows that 32 bits count.
+constexpr int kMaxItemHeads = 8;
+inline int item_shift(int group, int64_t T) {
+  int shift = 0;
+  while ((2 << shift) <= kMaxItemHeads && group % (2 << shift) == 0 &&
+         (T << (shift + 1)) <= ((int64_t)1 << 30))
+    ++shift;
+  return shift;
+}
 cudaError_t launch_diff_fwd_tc(const DiffProblem& a, const FwdWsLayout& L, char* ws, cudaStream_t s);
 // A map of [rows, cols] bf16 whose copies are 128 rows of 64 columns, 128-byte
 // swizzled; false without tensor-map support in the driver.
 bool diff_tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols);
+// The same of [T, H, d] in copies of `heads` heads at 128 / heads tokens.
 bool diff_heads_map(CUtensorMap* m, const void* base, int64_t T, int64_t H, int64_t d, int heads);
 cudaError_t launch_diff_fwd_simt(const DiffProblem& a, cudaStream_t s);
 cudaError_t launch_diff_bwd_tc(const DiffProblem& a, const BwdWsLayout& L, char* ws, cudaStream_t s);

@@ -294,6 +294,7 @@ static DiffProblem diff_problem(const void* q, const void* k, const void* v, con
   p.wait_budget = wait_budget_cycles();
   a.lambda = lambda;
   a.n_lambda = n_lambda;
+  a.shift = io_dtype == NSP_BF16 ? item_shift(Hq / Hkv, T) : 0;
   return a;
 }
 
