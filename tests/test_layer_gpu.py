@@ -360,6 +360,42 @@ def test_diff_attention(nsp, dt, causal, tokens, lens, hq, hkv, d):
         assert torch.equal(a, b)                      # one fixed order of sums
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,hq,hkv,d", [
+    ([1], 8, 1, 64), ([17, 1, 0, 140, 3, 30], 8, 1, 128), ([9, 8, 7, 6, 5, 4, 3, 2, 1], 16, 2, 128),
+    ([130, 200], 16, 1, 64), ([70, 77], 6, 1, 128), ([250, 7], 24, 2, 64), ([16, 16, 15, 1, 81, 127], 8, 1, 64),
+])
+def test_diff_attention_heads_of_a_group(nsp, lens, hq, hkv, d, causal):
+    """Groups whose heads go into one query tile, 2, 4 or 8 at a time, with documents
+    that begin and end inside its few tokens."""
+    test_diff_attention(nsp, BF16, causal, True, lens, hq, hkv, d)
+
+
+def test_diff_attention_heads_many_documents(nsp):
+    """Every head of a packed group alone (one head a group, whole tiles of tokens):
+    the same values to the rounding of sums in another order of keys."""
+    rng = np.random.default_rng(11)
+    lens = [int(n) for n in rng.choice([0, 1, 2, 5, 16, 40, 131], size=400)]
+    q, k, v, lam, do, cu = diff_inputs(145, lens, 8, 1, 128, BF16, True)
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    dq, dk, dv, dlam = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+    kv = [np.zeros(k.shape) for _ in range(2)]
+    for h in range(8):
+        one = [t[:, h:h + 1].contiguous() for t in (q, do)]
+        o, o2, ls = nsp.diff_attn_fwd(one[0], k, v, lam[h:h + 1].clone(), cu, save=True)
+        g = nsp.diff_attn_bwd(one[0], k, v, lam[h:h + 1].clone(), o, o2, one[1], ls, cu)
+        # P, dS and the outputs are rounded to bf16 on both sides, sums of bf16 products in float32
+        for a, b in ((out[:, h], o[:, 0]), (out2[:, h], o2[:, 0]), (dq[:, h], g[0][:, 0]), (dlam[h], g[3][0])):
+            a, b = f64(a), f64(b)
+            assert np.linalg.norm(a - b) <= 4 * half_step(BF16) * np.linalg.norm(b)
+        np.testing.assert_allclose(f64(lse[h]), f64(ls[0]), rtol=0, atol=2e-5)
+        for t, x in zip(kv, g[1:3]):
+            t += f64(x)
+    for a, b in zip((dk, dv), kv):                    # eight rounded shares against one rounded sum
+        a = f64(a)
+        assert np.linalg.norm(a - b) <= 4 * half_step(BF16) * np.linalg.norm(b)
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_diff_attention_growing_scores(nsp, dt):
     """Scores that climb along the document (the running maximum is replaced
