@@ -11,8 +11,9 @@
 //
 // dK/dV kernel (key-stationary).  Work item: one 128-key tile of one KV head;
 // it walks every pair (2^shift query heads of the group, tile of 128 >> shift
-// tokens of them that can see the keys).  A pair costs four 128 x 128 x 128 products' worth: S_1 and
-// S_2 (half the columns each), dP, dV (both maps in one product, their
+// tokens of them that can see the keys).  With few key tiles an item is some of a tile's
+// pairs, and the join kernel sums the parts' float32 shares in order (key_parts).  A pair
+// costs four 128 x 128 x 128 products' worth: S_1 and S_2 (half the columns each), dP, dV (both maps in one product, their
 // combination is its operand), dK_1 and dK_2 (half the columns each); treating
 // the maps as two heads would cost six.  TMEM: two 128-column regions [0,256),
 // dV [256,256+D), dK_1 | dK_2 [384,384+D).  Pair n puts S_1^T in region A = n & 1,
@@ -23,9 +24,9 @@
 // tiles' copies and dS_1 take about 2900 cycles of it a pair).  The next pair swaps
 // the regions, so its S_1 is computed into B, while the softmax is on this pair's
 // second map.  A pair's 40 instructions take the tensor core 2560 cycles at least
-// (64 for 128 columns, 62 for the 64 of a dK_m); it measures 5200: dS_1 waits for S_1
-// and dP, dK_2 and dV for both, and the two regions hold no third pair.  404 us for
-// 16384 tokens in 19 causal documents, 16 heads on 4, d = 128 (540 TFLOP/s of the
+// (64 for 128 columns, 62 for the 64 of a dK_m); it measures some 5200: dS_1 waits for
+// S_1 and dP, dK_2 and dV for both, and the two regions hold no third pair.  393 us for
+// 16384 tokens in 19 causal documents, 16 heads on 4, d = 128 (555 TFLOP/s of the
 // visible pairs' 8 d).
 //
 // dQ kernel (query-stationary).  Work item: 128 query rows, several heads of a group
@@ -37,8 +38,8 @@
 // product to issue: 32 instructions of a tile take 3500 cycles, 110 each, against
 // 68 to 76 of independent ones back to back (dP of the next tile between dQ_1's or
 // dQ_2's, instruction by instruction or half by half, is 2 to 4 % slower: 600 us
-// for both kernels against 581).  227 us for the same documents (720
-// TFLOP/s of their 6 d).
+// for both kernels against 581, with 128-token tiles of one head).  212 us for the same
+// documents (770 TFLOP/s of their 6 d).
 //
 // Roles, dK/dV: 16 softmax warps (four column groups of four lane quadrants;
 // with 8 warps of 64 columns the loop is 18 KB of instructions and waits for
@@ -59,6 +60,8 @@ struct BwdArgs {
   const float *coef, *cndelta;      // [Hq / P][Tp][P]: c, -c delta_2
   int64_t Tp;
   __nv_bfloat16 *dq, *dk, *dv;
+  float* parts;                     // n_parts > 1: [part][dV, dK][T, Hkv, d] of the key tiles' parts
+  int n_parts;
   const int* qorder;                // 128-token tiles of queries, most keys first
   int shift;                        // log2 of the heads of a query item
   const int* korder;
@@ -73,9 +76,29 @@ constexpr int kKvRegsControl = 64, kKvRegsSoftmax = 104;   // 128 x 64 + 512 x 1
 
 struct KvItem {
   // n_q query tiles (128 >> shift tokens of 2^shift heads) from row q_lo = token << shift on;
-  // pairs = head groups * n_q; -1 stops
-  int ktile, g, q_lo, n_q, pairs, pad[3];
+  // pairs n0 .. n0 + pairs - 1 of the key tile's (head group, query tile) are this item's; -1 stops
+  int ktile, g, q_lo, n_q, n0, pairs, part, whole;
 };
+
+// The query rows that a key tile sees, and its pairs.
+__device__ __forceinline__ int key_tile_pairs(const AttnProblem& p, int ktile, int shift, int& q_lo, int& n_q) {
+  const int key0 = ktile * 128;
+  const int64_t last = min((int64_t)key0 + 128, p.kv_len) - 1;
+  const int first = p.causal ? key0 : __ldg(p.cu + doc_of(p.cu, p.ndoc, key0));
+  const int end = __ldg(p.cu + doc_of(p.cu, p.ndoc, last) + 1);
+  // (a multiple of a tile's tokens: the row vectors are read in whole tiles)
+  q_lo = (first << shift) & ~127;
+  n_q = ((end << shift) - q_lo + 127) >> 7;
+  return (p.Hq / p.Hkv >> shift) * n_q;
+}
+
+// Parts of a key tile of so many pairs, four at least in each: a tile of few pairs is written
+// whole (2000 tokens in short documents, 64 key tiles: 76 us; split in 8 parts each, 97; one
+// document of 2000: 103 us, with 16 pairs at least 133).
+constexpr int kPartPairs = 4;
+__device__ __forceinline__ int parts_of(const BwdArgs& a, int pairs) {
+  return min(a.n_parts, max(1, pairs / kPartPairs));
+}
 
 struct __align__(1024) SmemKV {
   uint8_t k[kTile];
@@ -174,7 +197,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   WaitCtl* const wc = &sm.wait;
   const int G = p.Hq / p.Hkv;
-  const int n_items = hdr->n_items2 * p.Hkv;
+  const int n_items = hdr->n_items2 * p.Hkv * a.n_parts;
   constexpr int kBlocks = D / 64;                        // 64-column blocks of a row
   constexpr uint32_t kLoad = kBlocks * kBlk;             // one Q, dOut, K or V tile
 
@@ -189,16 +212,16 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         KvItem it = {};
         it.pairs = -1;
         if (idx < n_items) {
-          it.ktile = a.korder[idx / p.Hkv];
-          it.g = idx % p.Hkv;
-          const int key0 = it.ktile * 128;
-          const int64_t last = min((int64_t)key0 + 128, p.kv_len) - 1;
-          const int first = p.causal ? key0 : __ldg(p.cu + doc_of(p.cu, p.ndoc, key0));
-          const int end = __ldg(p.cu + doc_of(p.cu, p.ndoc, last) + 1);
-          // (a multiple of a tile's tokens: the row vectors are read in whole tiles)
-          it.q_lo = (first << a.shift) & ~127;
-          it.n_q = ((end << a.shift) - it.q_lo + 127) >> 7;
-          it.pairs = (G >> a.shift) * it.n_q;
+          const int rest = idx % (p.Hkv * a.n_parts);
+          it.ktile = a.korder[idx / (p.Hkv * a.n_parts)];
+          it.g = rest % p.Hkv;
+          it.part = rest / p.Hkv;
+          const int all = key_tile_pairs(p, it.ktile, a.shift, it.q_lo, it.n_q);
+          const int parts = parts_of(a, all);
+          if (it.part >= parts) continue;
+          it.whole = parts == 1;
+          it.n0 = (int)((int64_t)all * it.part / parts);
+          it.pairs = (int)((int64_t)all * (it.part + 1) / parts) - it.n0;
         }
         const uint32_t slot = it_count & 1;
         if (it_count >= 2 && !mbar_wait(&sm.item_empty[slot], ((it_count >> 1) - 1) & 1, wc, hdr))
@@ -215,7 +238,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           tma_load_2d(sm.v + cb * kBlk, &tm_v, &sm.kv_full, it.g * D + cb * 64, it.ktile * 128);
         }
         ++kv_count;
-        int h = it.g * G, i = 0;
+        int h = it.g * G + ((it.n0 / it.n_q) << a.shift), i = it.n0 % it.n_q;
         for (int n = 0; n < it.pairs && ok; ++n) {
           const uint32_t fill = qc >> 1;
 #pragma unroll
@@ -257,7 +280,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_arrive(&sm.item_empty[slot]);
         ++it_count;
         if (it.pairs < 0) break;
-        int h = it.g * G, i = 0;
+        int h = it.g * G + ((it.n0 / it.n_q) << a.shift), i = it.n0 % it.n_q;
         for (int n = 0; n < it.pairs; ++n) {
           const int64_t hg = h >> a.shift, np = a.Tp << a.shift, q0 = it.q_lo + (int64_t)i * 128;
           const int64_t r1 = 2 * hg * np + q0, r2 = r1 + np;
@@ -403,7 +426,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       // queries that see every row of the thread
       const int all_lo = max(max(qlo[0], qlo[1]), max(qlo[2], qlo[3]));
       const int all_hi = min(min(qhi[0], qhi[1]), min(qhi[2], qhi[3]));
-      int n_in = 0;                                        // query tile of the pair, 0 .. n_q - 1
+      int n_in = it.n0 % it.n_q;                           // query tile of the pair, 0 .. n_q - 1
       for (int n = 0; n < it.pairs; ++n) {
         const int q0 = it.q_lo + n_in * 128 + cg * 32;
         if (++n_in == it.n_q) n_in = 0;
@@ -522,13 +545,23 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       if (c0 < D) {
         const int64_t key = (int64_t)it.ktile * 128 + r;
         const bool is_dk = cg >= 2;
-        __nv_bfloat16* dst = (is_dk ? a.dk : a.dv) + (key * p.Hkv + it.g) * D + c0;
+        const int64_t at = (key * p.Hkv + it.g) * D + c0;
+        __nv_bfloat16* dst = (is_dk ? a.dk : a.dv) + at;
+        float* part = a.parts + (it.part * 2 + is_dk) * (p.kv_len * p.Hkv * D) + at;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t v[32];
           tmem_ld32(tmem + lane_base + (is_dk ? 384u : 256u) + c0 + c * 32, v);
           tmem_wait_ld();
-          if (key < p.kv_len) store_row32(dst + c * 32, v, is_dk ? p.scale : 1.f);
+          if (key >= p.kv_len) continue;
+          if (it.whole) {
+            store_row32(dst + c * 32, v, is_dk ? p.scale : 1.f);
+            continue;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_global_v8(part + c * 32 + 8 * i, v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
+                         v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
         }
       }
       tc_fence_before();
@@ -879,14 +912,52 @@ __global__ void __launch_bounds__(kQThreads, 1)
   grid_dep_wait();
 }
 
+// dV, dK = sums of the parts' shares, in order.  One block for 128 keys of a KV head and one of
+// the two.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) diff_bwd_join_kernel(const BwdArgs a) {
+  const AttnProblem& p = a.p;
+  if (status_bad(p.hdr)) return;
+  const bool is_dk = blockIdx.y & 1;
+  const int g = blockIdx.y >> 1;
+  int q_lo, n_q;
+  const int parts = parts_of(a, key_tile_pairs(p, blockIdx.x, a.shift, q_lo, n_q));
+  if (parts == 1) return;                          // written whole
+  const int64_t size = p.kv_len * p.Hkv * D;
+  __nv_bfloat16* const out = is_dk ? a.dk : a.dv;
+  const float f = is_dk ? p.scale : 1.f;
+  for (int e = threadIdx.x; e < 128 * (D / 8); e += kJoinThreads) {
+    const int64_t key = (int64_t)blockIdx.x * 128 + e / (D / 8);
+    if (key >= p.kv_len) break;
+    const int64_t at = (key * p.Hkv + g) * D + e % (D / 8) * 8;
+    const float* src = a.parts + (int64_t)is_dk * size + at;
+    float x[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s, src += 2 * size) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + 1);
+      x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+      x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= f;
+    *reinterpret_cast<uint4*>(out + at) = Vec<__nv_bfloat16>::pack(x);
+  }
+}
+
 template <int D>
 cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
                      const CUtensorMap& mv, const BwdArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_persistent<2 * D>(diff_bwd_dkdv_tc_kernel<D>, kKvThreads,
+  cudaError_t e = launch_persistent<2 * D>(diff_bwd_dkdv_tc_kernel<D>, kKvThreads,
                                                  smem_bytes<SmemKV>(), s, mq, mdo, mk, mv, a);
   if (e != cudaSuccess) return e;
-  return launch_persistent<2 * D + 1>(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), s, mq,
-                                      mdo, mk, mv, a);
+  e = launch_persistent<2 * D + 1>(diff_bwd_dq_tc_kernel<D>, kQThreads, smem_bytes<SmemQ>(), s, mq, mdo,
+                                   mk, mv, a);
+  if (e != cudaSuccess || a.n_parts == 1) return e;
+  diff_bwd_join_kernel<D><<<dim3((unsigned)ceil_div(a.p.kv_len, 128), 2 * a.p.Hkv), kJoinThreads, 0, s>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -906,6 +977,8 @@ cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char*
   a.dk = reinterpret_cast<__nv_bfloat16*>(d.dk);
   a.dv = reinterpret_cast<__nv_bfloat16*>(d.dv);
   a.shift = d.shift;
+  a.parts = d.parts;
+  a.n_parts = key_parts(p.kv_len, p.Hkv);
   a.qorder = reinterpret_cast<const int*>(ws + L.qorder);
   a.korder = reinterpret_cast<const int*>(ws + L.korder);
   return p.d == 128 ? launch_d<128>(mq, mdo, mk, mv, a, s) : launch_d<64>(mq, mdo, mk, mv, a, s);

@@ -74,6 +74,7 @@ struct DiffProblem {
   float *ndelta, *nlse2;             // backward workspace: [Hq / P][2][Tp][P]
   float *coef, *cndelta;             // [Hq / P][Tp][P]
   int64_t Tp;
+  float* parts;                      // bf16 backward: shares of dV and dK of a key tile's parts
   float *dk_heads, *dv_heads;        // float32 backward, Hq > Hkv: [T, Hq, d] shares of the heads
 };
 // Heads of a tensor-core query item: the power of two in a group's heads, 8 at most
@@ -85,6 +86,18 @@ inline int item_shift(int group, int64_t T) {
          (T << (shift + 1)) <= ((int64_t)1 << 30))
     ++shift;
   return shift;
+}
+// Most parts that the bf16 backward splits a key tile into, each some of the tile's (head
+// group, query tile) pairs: as many as give each of 152 SMs one (not the device's count: the
+// workspace's size depends on it).  One document of 4000 tokens, 4 heads on 1: 358 us whole,
+// 146 in 8 parts; 8000 tokens in documents around 1024, 8 heads on 2: 369 whole, 231 in 2;
+// 16384 tokens, 16 heads on 4, 512 key tiles: 555 whole, 618 in 2 (the shares' way through
+// memory).
+inline int key_parts(int64_t T, int Hkv) {
+  const int64_t items = ceil_div(T, 128) * Hkv;
+  int n = 1;
+  while (n < 8 && items * n < 152 && T > 256) n *= 2;
+  return n;
 }
 cudaError_t launch_diff_fwd_tc(const DiffProblem& a, const FwdWsLayout& L, char* ws, cudaStream_t s);
 // A map of [rows, cols] bf16 whose copies are 128 rows of 64 columns, 128-byte

@@ -331,8 +331,8 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
 }
 
 // Backward workspace: the attention backward's layout for 2 Hq rows of -delta
-// and -lse log2 e, then -lambda and lambda delta_2 [Hq, Tp], and for float32 with grouped heads each
-// query head's share of dk and dv.
+// and -lse log2 e, then -lambda and lambda delta_2 [Hq, Tp], then shares of dk and dv: for
+// float32 with grouped heads each query head's, for bf16 each part's of a split key tile.
 struct DiffBwdLayout {
   BwdWsLayout attn;
   size_t coef, heads, total;
@@ -345,6 +345,8 @@ static DiffBwdLayout diff_bwd_layout(int64_t T, int32_t Hq, int32_t Hkv, int32_t
   L.heads = align_up(L.coef + 2 * sizeof(float) * (size_t)Hq * (size_t)L.attn.Tp, 256);
   const bool shares = io_dtype == NSP_F32 && Hq > Hkv;
   L.total = L.heads + (shares ? 2 * sizeof(float) * (size_t)T * (size_t)Hq * (size_t)d : 0);
+  const int parts = io_dtype == NSP_BF16 ? key_parts(T, Hkv) : 1;
+  if (parts > 1) L.total += 2 * sizeof(float) * (size_t)parts * (size_t)T * (size_t)Hkv * (size_t)d;
   return L;
 }
 
@@ -386,7 +388,8 @@ int32_t nsp_diff_attn_bwd(const void* q, const void* k, const void* v, const voi
   a.nlse2 = reinterpret_cast<float*>(ws + L.nlse2);
   a.coef = reinterpret_cast<float*>(ws + W.coef);
   a.cndelta = a.coef + (size_t)Hq * (size_t)L.Tp;
-  a.dk_heads = reinterpret_cast<float*>(ws + W.heads);
+  a.parts = reinterpret_cast<float*>(ws + W.heads);
+  a.dk_heads = a.parts;
   a.dv_heads = a.dk_heads + (size_t)T * (size_t)Hq * (size_t)d;
   a.Tp = L.Tp;
   if (launch_bwd_schedules(a.p, L, ws, s) != cudaSuccess) return NSP_ERR_CUDA;
