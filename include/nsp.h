@@ -669,7 +669,7 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
  *   dlambda = -delta^2 of each token, or its sum over the tokens.
  * Every output is written whole, and sums run in one fixed order: results are
  * the same bits on every run.  A non-finite value in one document's q, k or
- * dout may reach rows of documents that share a 128-token tile with it. */
+ * dout may reach rows of documents less than 128 tokens away from it. */
 size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t d,
                                         int32_t io_dtype);
 

@@ -371,6 +371,24 @@ def test_diff_attention_heads_of_a_group(nsp, lens, hq, hkv, d, causal):
     test_diff_attention(nsp, BF16, causal, True, lens, hq, hkv, d)
 
 
+@pytest.mark.parametrize("lens", [[2500], [300, 1, 900, 0, 60]])
+def test_diff_attention_split_key_tiles(nsp, lens):
+    """Few key tiles: each is split in parts, whose float32 shares lie in a workspace
+    with no more than its documented 16-byte alignment."""
+    hq, hkv, d, T = 8, 1, 128, sum(lens)
+    q, k, v, lam, do, cu = diff_inputs(160, lens, hq, hkv, d, BF16, False)
+    out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    n = nsp.load().nsp_diff_attn_bwd_workspace_size(T, hq, hkv, d, nsp.NSP_BF16)
+    ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")[16:]
+    assert ws.data_ptr() % 32 == 16
+    grads = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu, workspace=ws)
+    ref = L.diff_attn_bwd(*(f64(t) for t in (q, k, v, lam, do)), cu.cpu().numpy(), (d // 2) ** -0.5, True)
+    for name, a, b in zip(("dq", "dk", "dv", "dlam"), grads, ref):
+        assert np.linalg.norm(f64(a) - b) <= 1e-2 * np.linalg.norm(b), name
+    for a, b in zip(grads, nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)):
+        assert torch.equal(a, b)
+
+
 def test_diff_attention_heads_many_documents(nsp):
     """Every head of a packed group alone (one head a group, whole tiles of tokens):
     the same values to the rounding of sums in another order of keys."""

@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             continue;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            st_global_v8(part + c * 32 + 8 * i, v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3],
-                         v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+          for (int i = 0; i < 8; ++i)                      // (a workspace is 16-byte aligned)
+            *reinterpret_cast<uint4*>(part + c * 32 + 4 * i) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
       }
       tc_fence_before();
