@@ -10,9 +10,9 @@
 //   dS_1 = P_1 (dP - delta_1),  dS_2 = -lambda P_2 (dP - delta_2),
 //   dQ_m = scale dS_m K_m,  dK_m = scale dS_m^T Q_m,  dV = (P_1 - lambda P_2)^T dout.
 //
-// Bound: the 128 bytes a clock that shared memory fills registers with (a
-// 16-byte read costs a warp 4 clocks of it, broadcast or not) beside the FP32
-// pipes (a warp's FMA costs 1/4).  Every product is tiled in registers, 16
+// Bound: reads of shared memory beside the FP32 pipes, with the two blocks of four
+// warps of an SM that 255 registers a thread leave (FMA pipes 50 to 55 % busy, issue
+// slots 60 to 67 %).  Every product is tiled in registers, 16
 // threads wide, from float32 tiles in shared memory, rows padded by 4 floats so
 // that 16 rows read at one column fall into different banks; a thread's 8 rows by
 // 4 keys take 12 reads for 128 FMAs (8 x 4 x d = 64; 4 x 4, 8 for 64, took 625 us
