@@ -47,6 +47,11 @@
 // dK and dV: products of one thread run in order, so those that wait for the
 // softmax must not hold up the others), warp 19 producer of the row vectors.
 // dQ: 8 softmax warps, warp 8 producer, warp 9 MMA.  All waits are bounded.
+//
+// Rounding: P_1 + c P_2 and dS_m are rounded to bf16, as the tensor core's operands
+// next to bf16 inputs; scores, exponentials, delta, sums and shares are float32.
+// Against exact arithmetic dQ and dK are off by 0.0026 (relative norm), where outputs
+// rounded to bf16 alone leave 0.0018.
 #include "diff_tc.cuh"
 
 namespace nsp {
