@@ -389,6 +389,45 @@ def test_diff_attention_split_key_tiles(nsp, lens):
         assert torch.equal(a, b)
 
 
+def test_diff_attention_split_captured_and_on_two_streams(nsp):
+    """The split backward replayed from a graph on new values, and two of them in
+    flight at once."""
+    lens = [1200, 77]
+    ins = [diff_inputs(163 + i, lens, 8, 2, 64, BF16, True) for i in range(2)]
+
+    def step(x):
+        q, k, v, lam, do, cu = x
+        out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+        return (out,) + nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)
+
+    want = [step(x) for x in ins]
+    held = tuple(t.clone() for t in ins[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(held)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(held)
+    for i in (1, 0, 1):
+        for a, b in zip(held, ins[i]):
+            a.copy_(b)
+        graph.replay()
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    streams, both = [torch.cuda.Stream() for _ in ins], [None, None]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                both[i] = step(ins[i])
+    torch.cuda.synchronize()
+    for a, b in zip(want, both):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
 def test_diff_attention_heads_many_documents(nsp):
     """Every head of a packed group alone (one head a group, whole tiles of tokens):
     the same values to the rounding of sums in another order of keys."""
