@@ -13,8 +13,8 @@
 // it walks every pair (2^shift query heads of the group, tile of 128 >> shift
 // tokens of them that can see the keys).  With few key tiles an item is some of a tile's
 // pairs, and the join kernel sums the parts' float32 shares in order (key_parts).  A pair
-// costs four 128 x 128 x 128 products' worth: S_1 and S_2 (half the columns each), dP, dV (both maps in one product, their
-// combination is its operand), dK_1 and dK_2 (half the columns each); treating
+// costs four 128 x 128 x 128 products' worth: S_1 and S_2 (half the columns each), dP,
+// dV (both maps in one product, their combination is its operand), dK_1 and dK_2 (half the columns each); treating
 // the maps as two heads would cost six.  TMEM: two 128-column regions [0,256),
 // dV [256,256+D), dK_1 | dK_2 [384,384+D).  Pair n puts S_1^T in region A = n & 1,
 // dP^T in the other one, B; S_2^T follows into A when the softmax warps have

@@ -7,8 +7,8 @@
 //   dlambda = -delta_2 (of each token), or its sum over the tokens.
 // Written as [Hq / P][2][Tp][P] (-delta, -lse log2 e) and [Hq / P][Tp][P] (c = -lambda,
 // the factor of the second map's probabilities, and -c delta_2) for the P = 2^shift
-// heads of a query item, padded with zeros to whole 128-row tiles.  Bound: HBM, one read of out, out2 and dout: 201 MB of 16384 tokens,
-// 16 heads, d = 128 in 37 us, 5.5 TB/s.
+// heads of a query item, padded with zeros to whole 128-row tiles.  Bound: HBM, one read
+// of out, out2 and dout: 201 MB of 16384 tokens, 16 heads, d = 128 in 37 us, 5.5 TB/s.
 #include <algorithm>
 
 #include "layer.cuh"
