@@ -371,6 +371,53 @@ def test_diff_attention_heads_of_a_group(nsp, lens, hq, hkv, d, causal):
     test_diff_attention(nsp, BF16, causal, True, lens, hq, hkv, d)
 
 
+def lambda_grad_bounds(q, k, v, lam, do, cu, scale, causal, dt):
+    """-sum_j P_2 dP of every token and head [Hq, T], how far each may be off in
+    float32, and how far their sum over the tokens may be, by roundings that are
+    independent of one another (eight standard deviations): a score is a sum of d/2
+    products and dP one of d, each off by e times the square root of their number
+    and the terms' magnitudes; exp and the row's lse are off by 16 e and 8 e |lse|, the
+    same for a whole row; T sums of a row add e of its terms' magnitudes each."""
+    T, Hq, d = q.shape
+    P, lse = L.diff_maps(q, k, cu, scale, causal)
+    val, var, common = (np.zeros((Hq, T)) for _ in range(3))
+    for h in range(Hq):
+        g = h // (Hq // k.shape[1])
+        p, dp = P[1, h], do[:, h] @ v[:, g].T
+        mag = scale * np.abs(q[:, h, d // 2:]) @ np.abs(k[:, g, d // 2:]).T
+        each = (p * dp * E * (np.sqrt(d // 2 + 2) * mag + 8)) ** 2
+        each += (p * E * np.sqrt(d) * (np.abs(do[:, h]) @ np.abs(v[:, g]).T)) ** 2
+        val[h] = -(p * dp).sum(-1)
+        var[h] = each.sum(-1) + T * (E * np.abs(p * dp).sum(-1)) ** 2
+        common[h] = E * (16 + 8 * np.abs(np.where(np.isfinite(lse[h, 1]), lse[h, 1], 0))) * np.abs(val[h])
+    one = 8 * np.sqrt(var) + common
+    total = 8 * np.sqrt(var.sum(-1)) + (common + 32 * E * np.abs(val)).sum(-1)
+    h = half_step(dt)
+    return val, one + h * np.abs(val), total + h * np.abs(val.sum(-1))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("lens,hq,d", [([300], 4, 128), ([170, 131, 40], 4, 128), ([600], 3, 64), ([33] * 9, 8, 128)])
+def test_diff_attention_lambda_gradient_cancels(nsp, lens, hq, d, dt):
+    """A head's gradient of lambda is a sum over the tokens whose terms cancel: with
+    either type it is as exact as float32 arithmetic and one rounding to the type."""
+    cu = cu_of(lens)
+    for seed in range(300, 380, 10):
+        q, k, v, lam, do, _ = diff_inputs(seed, lens, hq, 1, d, dt, False)
+        ref = [f64(t) for t in (q, k, v, lam, do)]
+        val, one, total = lambda_grad_bounds(*ref, cu.cpu().numpy(), (d // 2) ** -0.5, True, dt)
+        want = val.sum(-1)
+        assert (np.abs(want) > 2 * total).mean() > 0.9            # (zeros would not pass)
+        out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+        got = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu)[3]
+        assert_within(got, want[:, None], total[:, None], f"dlam {seed}")
+        if dt == BF16:
+            # and of each token
+            many = lam.expand(hq, sum(lens)).contiguous()
+            got = nsp.diff_attn_bwd(q, k, v, many, out, out2, do, lse, cu)[3]
+            assert_within(got, val, one, f"dlam of tokens {seed}")
+
+
 @pytest.mark.parametrize("lens", [[2500], [300, 1, 900, 0, 60]])
 def test_diff_attention_split_key_tiles(nsp, lens):
     """Few key tiles: each is split in parts, whose float32 shares lie in a workspace

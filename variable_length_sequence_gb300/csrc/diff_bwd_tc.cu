@@ -40,6 +40,9 @@
 // dQ_2's, instruction by instruction or half by half, is 2 to 4 % slower: 600 us
 // for both kernels against 581, with 128-token tiles of one head).  212 us for the same
 // documents (770 TFLOP/s of their 6 d).
+// The gradient of lambda comes from here too, -sum_j P_2 dP of each row, from the
+// float32 values before any of them is rounded: its terms cancel over the tokens, and
+// <dout, out2> with the saved bf16 out2 is off by 1 % and more where they do.
 //
 // Roles, dK/dV: 16 softmax warps (four column groups of four lane quadrants;
 // with 8 warps of 64 columns the loop is 18 KB of instructions and waits for
@@ -49,7 +52,8 @@
 // dQ: 8 softmax warps, warp 8 producer, warp 9 MMA.  All waits are bounded.
 //
 // Rounding: P_1 + c P_2 and dS_m are rounded to bf16, as the tensor core's operands
-// next to bf16 inputs; scores, exponentials, delta, sums and shares are float32.
+// next to bf16 inputs; delta_m are float32 sums over the bf16 out and out2 of the
+// forward; scores, exponentials, sums and shares are float32.
 // Against exact arithmetic dQ and dK are off by 0.0026 (relative norm), where outputs
 // rounded to bf16 alone leave 0.0018.
 #include "diff_tc.cuh"
@@ -65,6 +69,8 @@ struct BwdArgs {
   const float *coef, *cndelta;      // [Hq / P][Tp][P]: c, -c delta_2
   int64_t Tp;
   __nv_bfloat16 *dq, *dk, *dv;
+  float* dlam_rows;                 // ndelta's second map: -sum_j P_2 dP of each row, or
+  __nv_bfloat16* dlam;              // (one lambda a token) written as its gradient [Hq][T]
   float* parts;                     // n_parts > 1: [part][dV, dK][T, Hkv, d] of the key tiles' parts
   int n_parts;
   const int* qorder;                // 128-token tiles of queries, most keys first
@@ -597,7 +603,9 @@ struct __align__(1024) SmemQ {
   uint64_t k_full[K_NS], k_empty[K_NS], v_full, v_empty;
   uint64_t s_full[2], p_full[2], dp_full, dp_free, o_full, o_free;
   uint64_t item_full[2], item_empty[2];
+  uint64_t sum_full;
   QueryItem items[2];
+  float sum[2][128];                       // [item parity][row]: sum of P_2 dP over columns 64-127 of every tile
   uint64_t drain;
   uint32_t tmem_base;
   WaitCtl wait;
@@ -649,6 +657,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     mbar_init(&sm.dp_free, 8);
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, 8);
+    mbar_init(&sm.sum_full, 8);
     mbar_init(&sm.drain, 1);
     wait_ctl_init(&sm.wait, p.wait_budget);
     fence_mbar_init();
@@ -819,6 +828,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
     if (!next_item(0)) it.n_kv = -1;
     bool ok = true;
     while (it.n_kv >= 0) {
+      float pdp = 0.f;                                       // sum of P_2 dP over the thread's columns
       for (int jj = 0; jj < it.n_kv; ++jj, ++jc) {
         const int key0 = it.lo + jj * 128 + wg * 64;
         const bool full_w = __all_sync(0xffffffffu, lo <= key0 && key0 + 64 <= hi);
@@ -856,20 +866,30 @@ __global__ void __launch_bounds__(kQThreads, 1)
           // is taken in with dP - delta: c dP - c delta
           const float f = m == 0 ? 1.f : c, g = nd[m];
           const uint64_t f2 = f2_pack(f, f), g2 = f2_pack(g, g);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
+            const uint32_t bits = column_bits(lo - key0 - 32 * cc, hi - key0 - 32 * cc);
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int i = 32 * cc + 2 * e;
+              const uint64_t pe = f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              const uint64_t de = f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1]));
               float u0, u1;
-              f2_unpack(f2_mul(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                               f2_fma(f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])), f2,
-                                      g2)), u0, u1);
+              if (m == 1) {                // P_2 dP (a masked column's is dropped, whatever it is)
+                if (full_w) {
+                  sum[e & 1] = f2_fma(pe, de, sum[e & 1]);
+                } else {
+                  f2_unpack(f2_mul(pe, de), u0, u1);
+                  sum[e & 1] = f2_add(sum[e & 1], f2_pack(bits & (1u << (2 * e)) ? u0 : 0.f,
+                                                          bits & (2u << (2 * e)) ? u1 : 0.f));
+                }
+              }
+              f2_unpack(f2_mul(pe, f2_fma(de, f2, g2)), u0, u1);
               w[e] = pack_bf16x2(u0, u1);
             }
             if (!full_w) {
-              const uint32_t bits = column_bits(lo - key0 - 32 * cc, hi - key0 - 32 * cc);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {                // pairs of columns 8 j + 2 i
                 uint32_t mask[4];
@@ -883,14 +903,34 @@ __global__ void __launch_bounds__(kQThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive_warp(&sm.p_full[m], lane);
+          if (m == 1) {
+            float u0, u1;
+            f2_unpack(f2_add(sum[0], sum[1]), u0, u1);
+            pdp += u0 + u1;
+          }
         }
         if (!ok) break;
       }
       if (!ok) break;
-      // epilogue: map wg of the row's gradient
+      // epilogue: map wg of the row's gradient, and lambda's
       const int64_t row = (int64_t)it.t0 + tr;
-      __nv_bfloat16* const dst = a.dq + (row * p.Hq + it.h0 + hr) * D + wg * (D / 2);
+      const int h = it.h0 + hr;
+      __nv_bfloat16* const dst = a.dq + (row * p.Hq + h) * D + wg * (D / 2);
+      const int64_t sum_at = (2 * (int64_t)(it.h0 >> a.shift) + 1) * (a.Tp << a.shift) +
+                             ((int64_t)it.t0 << a.shift) + r;
+      if (wg == 1) sm.sum[it_count & 1][r] = pdp;
+      // (every warp arrives, so that the next item's phase cannot end before a warp
+      // that waits for this one)
+      mbar_arrive_warp(&sm.sum_full, lane);
       if (!next_item(it_count + 1)) break;
+      if (wg == 0) {                       // (read before o_free, which the slot's next writer follows)
+        if (!mbar_wait_warp(&sm.sum_full, it_count & 1, wc, hdr)) break;
+        const float s = -(pdp + sm.sum[it_count & 1][r]);
+        if (row < p.q_len) {
+          if (a.dlam != nullptr) st_out(a.dlam + (int64_t)h * p.q_len + row, s);
+          else a.dlam_rows[sum_at] = s;
+        }
+      }
       if (!mbar_wait_warp(&sm.o_full, it_count & 1, wc, hdr)) break;
       tc_fence_after();
 #pragma unroll
@@ -982,6 +1022,8 @@ cudaError_t launch_diff_bwd_tc(const DiffProblem& d, const BwdWsLayout& L, char*
   a.dk = reinterpret_cast<__nv_bfloat16*>(d.dk);
   a.dv = reinterpret_cast<__nv_bfloat16*>(d.dv);
   a.shift = d.shift;
+  a.dlam_rows = d.ndelta;
+  a.dlam = d.n_lambda > 1 ? reinterpret_cast<__nv_bfloat16*>(d.dlambda) : nullptr;
   a.parts = d.parts;
   a.n_parts = key_parts(p.kv_len, p.Hkv);
   a.qorder = reinterpret_cast<const int*>(ws + L.qorder);

@@ -5,6 +5,8 @@
 // O_2 saved by the forward:
 //   delta_2 = <dout, out2>,  delta_1 = <dout, out> + lambda delta_2,
 //   dlambda = -delta_2 (of each token), or its sum over the tokens.
+// With bf16 tensors dlambda is not taken from here: out2 is rounded, and a head's sum
+// over the tokens cancels; the dQ kernel puts -sum_j P_2 dP in float32 in delta_2's place.
 // Written as [Hq / P][2][Tp][P] (-delta, -lse log2 e) and [Hq / P][Tp][P] (c = -lambda,
 // the factor of the second map's probabilities, and -c delta_2) for the P = 2^shift
 // heads of a query item, padded with zeros to whole 128-row tiles.  Bound: HBM, one read
@@ -94,12 +96,14 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
     const float lam = to_f(L[(int64_t)h * a.n_lambda + (a.n_lambda > 1 ? t : 0)]);
     const int64_t v1 = (int64_t)hg * 2 * np + j, v2 = v1 + np, vc = (int64_t)hg * np + j;
     a.ndelta[v1] = -fmaf(lam, m2, m0);
-    a.ndelta[v2] = -m2;
     a.nlse2[v1] = -kLog2e * __ldg(p.lse + (int64_t)h * 2 * T_ + t);
     a.nlse2[v2] = -kLog2e * __ldg(p.lse + ((int64_t)h * 2 + 1) * T_ + t);
     a.coef[vc] = -lam;
     a.cndelta[vc] = lam * m2;
-    if (a.n_lambda > 1) st_out(reinterpret_cast<T*>(a.dlambda) + (int64_t)h * T_ + t, -m2);
+    if constexpr (sizeof(T) == 4) {
+      a.ndelta[v2] = -m2;
+      if (a.n_lambda > 1) st_out(reinterpret_cast<T*>(a.dlambda) + (int64_t)h * T_ + t, -m2);
+    }
   }
   // zero padding of the last tile's rows
   const int64_t pad = np - n;
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) diff_prep_kernel(const DiffProblem a
   }
 }
 
-// dlambda[h] = sum_t -delta_2, one block of a head, in one fixed order.
+// dlambda[h] = sum_t -delta_2 (float32 rows), one block of a head, in one fixed order.
 template <typename T>
 __global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restrict__ ndelta,
                                                             int64_t tokens, int64_t Tp, int shift,
