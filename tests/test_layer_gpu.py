@@ -574,6 +574,40 @@ def test_diff_attention_status(nsp):
     assert torch.equal(a, nsp.diff_attn_fwd(q, k, v, lam, cu_of([30, 70]), causal=False))
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("T,hq,hkv,d", [(100, 2, 1, 64), (333, 8, 1, 128), (1000, 8, 2, 64), (129, 5, 5, 128),
+                                        (20000, 8, 1, 64)])
+@pytest.mark.parametrize("past", [1, 1000, 2 ** 31 - 1])
+def test_diff_attention_stream_ends_inside_a_document(nsp, dt, causal, T, hq, hkv, d, past):
+    """cu_seqlens longer than the stream: its start, bit for bit, with key tiles whole
+    and in parts, heads of a group together and alone, and nothing written around the
+    workspace."""
+    if dt == F32 and T > 1000:
+        T = 1500
+    first = T // 3
+    cut = cu_of([first, T - first])
+    long = torch.tensor([0, first, min(T + past, 2 ** 31 - 1), 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    q, k, v, lam, do, _ = diff_inputs(190, [T], hq, hkv, d, dt, False)
+    n = nsp.load().nsp_diff_attn_bwd_workspace_size(T, hq, hkv, d, nsp._DTYPES[dt])
+    got = []
+    for cu in (cut, long):
+        out, out2, lse = nsp.diff_attn_fwd(q, k, v, lam, cu, causal=causal, save=True)
+        buf = torch.full((n + 2 * 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+        ws = buf[65536:65536 + n]
+        grads = nsp.diff_attn_bwd(q, k, v, lam, out, out2, do, lse, cu, causal=causal, workspace=ws)
+        assert nsp.nsp_status_query(ws) == nsp.NSP_OK
+        assert (buf[:65536] == 0xA5).all() and (buf[65536 + n:] == 0xA5).all()
+        got.append((out, out2, lse) + grads)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    if T <= 333:
+        scale = (d // 2) ** -0.5
+        ref, tol = diff_bounds(*(f64(t) for t in (q, k, v, lam, do)), cut.cpu().numpy(), scale, causal, dt)
+        for name, a, b, t in zip(("out", "out2", "lse", "dq", "dk", "dv", "dlam"), got[1], ref, tol):
+            assert_within(a, b, t, name)
+
+
 def test_diff_attention_empty_stream(nsp):
     q, k, v, lam, do, _ = diff_inputs(110, [0], 2, 1, 64, BF16, False)
     cu = cu_of([0])

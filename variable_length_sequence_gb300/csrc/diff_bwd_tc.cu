@@ -96,7 +96,8 @@ __device__ __forceinline__ int key_tile_pairs(const AttnProblem& p, int ktile, i
   const int key0 = ktile * 128;
   const int64_t last = min((int64_t)key0 + 128, p.kv_len) - 1;
   const int first = p.causal ? key0 : __ldg(p.cu + doc_of(p.cu, p.ndoc, key0));
-  const int end = __ldg(p.cu + doc_of(p.cu, p.ndoc, last) + 1);
+  // (the stream may end inside a document: no row vectors are past its rows)
+  const int end = (int)min((int64_t)__ldg(p.cu + doc_of(p.cu, p.ndoc, last) + 1), p.q_len);
   // (a multiple of a tile's tokens: the row vectors are read in whole tiles)
   q_lo = (first << shift) & ~127;
   n_q = ((end << shift) - q_lo + 127) >> 7;

@@ -109,7 +109,7 @@ __device__ __forceinline__ bool query_item(QueryItem& it, const AttnProblem& p, 
   it.g = it.h0 / (p.Hq / p.Hkv);
   const int end = (int)min((int64_t)it.t0 + tokens, p.q_len);
   it.lo = __ldg(p.cu + doc_of(p.cu, p.ndoc, it.t0));
-  const int hi = p.causal ? end : __ldg(p.cu + doc_of(p.cu, p.ndoc, end - 1) + 1);
+  const int hi = p.causal ? end : (int)min((int64_t)__ldg(p.cu + doc_of(p.cu, p.ndoc, end - 1) + 1), p.kv_len);
   it.n_kv = (hi - it.lo + 127) / 128;
   return true;
 }
