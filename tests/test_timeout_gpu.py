@@ -74,3 +74,46 @@ def test_backward_wait_expires_then_recovers(nsp):
     ref = oracle.attn_bwd(q, k, v, do, w.cu_seqlens, scale, True)
     for name, g, r in zip(("dq", "dk", "dv"), (dq, dk, dv), ref):
         assert rel_l2(f64(g), r) <= TOL_GRAD, name
+
+
+@pytest.mark.parametrize("bound", [100, 1000, 4000, 16000, 64000])
+def test_waits_that_expire_while_other_blocks_start(nsp, bound):
+    """Waits that run out at different points of a call, with more blocks starting at
+    that time (the dQ kernels start while their dK/dV kernel ends): every call ends,
+    with the status it recorded, and the next one on the same workspace is right."""
+    lens, hq, hkv, d = [2500, 40, 1800, 700], 8, 2, 128
+    w = make_custom(lens, hq, hkv, d, seed=83)
+    x = to_dev(w)
+    q, k, v, do, cu = x["q"], x["k"], x["v"], x["dout"], x["cu"]
+    T, scale = w.T, d ** -0.5
+    lam = torch.full((hq, 1), 0.4, dtype=q.dtype, device="cuda")
+    out, lse = nsp.attn_fwd(q, k, v, cu, scale=scale)
+    o1, o2, l2 = nsp.diff_attn_fwd(q, k, v, lam, cu, save=True)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (
+        nsp.nsp_attn_fwd_workspace_size(T, T, hq, hkv, d),
+        nsp.nsp_attn_bwd_workspace_size(T, hq, hkv, d, nsp_mod.NSP_BF16),
+        nsp.load().nsp_diff_attn_fwd_workspace_size(T),
+        nsp.load().nsp_diff_attn_bwd_workspace_size(T, hq, hkv, d, nsp_mod.NSP_BF16))]
+    cached = nsp.bwd_workspace(T, hq, hkv, d, q.device,
+                               ds_cache_bytes=nsp.nsp_attn_bwd_ds_cache_size(w.cu_seqlens, hq))
+    calls = [
+        lambda: nsp.attn_fwd(q, k, v, cu, scale=scale, workspace=ws[0]),
+        lambda: nsp.attn_bwd(q, k, v, out, do, lse, cu, scale=scale, workspace=ws[1]),
+        lambda: nsp.diff_attn_fwd(q, k, v, lam, cu, save=True, workspace=ws[2]),
+        lambda: nsp.diff_attn_bwd(q, k, v, lam, o1, o2, do, l2, cu, workspace=ws[3]),
+        lambda: nsp.attn_bwd(q, k, v, out, do, lse, cu, scale=scale, workspace=cached),
+    ]
+    for call, space in zip(calls, ws + [cached]):
+        want = call()
+        for _ in range(5):
+            prev = nsp.nsp_set_wait_timeout_cycles(bound)
+            try:
+                call()
+            finally:
+                nsp.nsp_set_wait_timeout_cycles(prev)
+            status = nsp.nsp_status_query(space)
+            assert status == nsp_mod.NSP_ERR_TIMEOUT or (bound > SHORT_BOUND and status == nsp_mod.NSP_OK)
+            got = call()
+            assert nsp.nsp_status_query(space) == nsp_mod.NSP_OK
+            for a, b in zip(want, got):
+                assert torch.equal(a, b)

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   WsHeader* hdr = p.hdr;
   grid_dep_wait();                          // delta and -lse log2(e) of bwd_delta_kernel
   grid_dep_trigger();                       // the dQ kernel may launch on SMs this one frees
-  if (status_bad(hdr)) return;
+  if (block_leaves(status_bad(hdr))) return;
   SmemKV* smp = smem_view<SmemKV>(smem_raw, hdr);
   if (smp == nullptr) return;
   SmemKV& sm = *smp;
@@ -864,8 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // SMs that kernel frees and waits for it only before it exits (work after
   // this call in the stream then also follows the dK/dV kernel).
   // (with the dS cache in use, the cache's dQ kernel does this call's dQ)
-  if (status_bad(hdr) ||
-      (a.ds_cache != nullptr && *((volatile const int32_t*)&hdr->ds_on) != 0)) {
+  if (block_leaves(status_bad(hdr) ||
+                   (a.ds_cache != nullptr && *((volatile const int32_t*)&hdr->ds_on) != 0))) {
     grid_dep_wait();
     return;
   }
@@ -1284,7 +1284,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   const AttnProblem& p = a.p;
   WsHeader* hdr = p.hdr;
   grid_dep_wait();                          // the dK/dV kernel (and its cache copies) are done
-  if (status_bad(hdr) || *((volatile const int32_t*)&hdr->ds_on) == 0) return;
+  if (block_leaves(status_bad(hdr) || *((volatile const int32_t*)&hdr->ds_on) == 0)) return;
   SmemCQ* smp = smem_view<SmemCQ>(smem_raw, hdr);
   if (smp == nullptr) return;
   SmemCQ& sm = *smp;

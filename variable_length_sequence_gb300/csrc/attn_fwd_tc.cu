@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WsHeader* hdr = p.hdr;
   grid_dep_wait();                          // the schedule kernel's lists and status
-  if (status_bad(hdr)) return;
+  if (block_leaves(status_bad(hdr))) return;
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, 1);

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   WsHeader* hdr = p.hdr;
   grid_dep_wait();                          // the prepared row vectors
   grid_dep_trigger();                       // the dQ kernel may launch on SMs this one frees
-  if (status_bad(hdr)) return;
+  if (block_leaves(status_bad(hdr))) return;
   SmemKV* smp = smem_view<SmemKV>(smem_raw, hdr);
   if (smp == nullptr) return;
   SmemKV& sm = *smp;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
   // everything this kernel reads is complete.  It starts on the SMs that kernel
   // frees and waits for it only before it exits, so that what follows in the
   // stream follows both.
-  if (status_bad(hdr)) {
+  if (block_leaves(status_bad(hdr))) {
     grid_dep_wait();
     return;
   }

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const AttnProblem& p = a.p;
   WsHeader* hdr = p.hdr;
   grid_dep_wait();                          // the schedule kernel's lists and status
-  if (status_bad(hdr)) return;
+  if (block_leaves(status_bad(hdr))) return;
   Smem* smp = smem_view<Smem>(smem_raw, hdr);
   if (smp == nullptr) return;
   Smem& sm = *smp;

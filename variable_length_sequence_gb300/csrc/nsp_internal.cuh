@@ -317,6 +317,13 @@ __device__ __forceinline__ bool status_bad(const WsHeader* hdr) {
   return *((volatile const int32_t*)&hdr->status) != 0;
 }
 
+// Whether the whole block leaves at its start: `leave` of any thread.  The status
+// word is read by every thread for itself, and may change between two reads: another
+// block of the grid, or of the kernel that this one was launched behind, records an
+// expired wait.  Threads that left alone would take a block's barriers, wait bound and
+// tensor memory with them.  Every thread of the block calls it.
+__device__ __forceinline__ bool block_leaves(bool leave) { return __syncthreads_or(leave) != 0; }
+
 // Programmatic dependent launch.  A kernel launched with launch_dependent may
 // start while the kernel before it in the stream is still running, as soon as
 // every CTA of that kernel has executed grid_dep_trigger() (or exited); it
