@@ -532,6 +532,24 @@ def test_diff_attention_equals_attention(nsp):
         assert (f64(out[..., 64 * half:64 * half + 64]) - f64(o)).max() <= 4 * 2.0 ** -8 * 4
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_diff_attention_equals_attention_on_both_sides(nsp, causal):
+    """The same, neither larger nor smaller than the roundings allow: both round P (u of
+    the terms each) and the result, element by element."""
+    lens, scale = [200, 3, 57], 0.125
+    q, k, v, lam, do, cu = diff_inputs(70, lens, 4, 2, 128, BF16, False)
+    lam = torch.zeros_like(lam)
+    out = f64(nsp.diff_attn_fwd(q, k, v, lam, cu, causal=causal))
+    (ref, _, _), (tol, _, _) = diff_bounds(*(f64(t) for t in (q, k, v, lam)), None, cu.cpu().numpy(), scale, causal,
+                                           BF16)
+    assert np.linalg.norm(tol) < 0.05 * np.linalg.norm(ref)
+    for half in range(2):
+        c = slice(64 * half, 64 * half + 64)
+        o, _ = nsp.attn_fwd(q[..., :64].contiguous(), k[..., :64].contiguous(), v[..., c].contiguous(), cu,
+                            scale=scale, causal=causal)
+        assert_within(out[..., c], f64(o), 2 * tol[..., c], "out")
+
+
 def test_diff_attention_differences(nsp):
     """Directional differences of the float32 forward: the step h leaves an
     h^2 / 6 third-derivative term (third derivatives of this loss along a unit
