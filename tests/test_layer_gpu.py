@@ -244,6 +244,42 @@ def test_head_norm(nsp, dt, gate, weight, tokens, heads, d):
         assert dg is None
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128, 512])
+def test_head_norm_far_gates(nsp, dt, d):
+    """Gates far from zero, on both sides: sigmoid and 1 - sigmoid are exact to
+    float32's roundings of their own values, however small they are (and bf16's exp to
+    2 + 1.2 |g| ulp more)."""
+    T, H = 65, 3
+    x, dy, w = randn(34, T, H, d, dt=dt), randn(35, T, H, d, dt=dt), randn(36, d, dt=dt)
+    g = (torch.linspace(-60, 60, T * H * d).view(T, H, d)).to(dt).cuda()
+    kw = dict(eps=1e-5, scale=0.2)
+    rx, rdy, rw, rg = (f64(t) for t in (x, dy, w, g))
+    # as in the test above: 64 e for the norm and the products, exp 2 ulp, the sum,
+    # the reciprocal and the product of the rest: 8 e
+    c = (72 + (4 * np.abs(rg) if dt == BF16 else 0)) * E
+    y = nsp.head_norm(x, w, g, **kw)
+    ref = L.head_norm(rx, rw, rg, 1e-5, 0.2)
+    assert_within(y, ref, (half_step(dt) + c) * np.abs(ref), "y")
+    dg = nsp.head_norm_bwd(x, dy, w, g, **kw)[2]
+    # (the oracle's 1 - s cancels for a large gate as well: sigmoid(-g) does not)
+    s, rest = 1 / (1 + np.exp(-rg)), 1 / (1 + np.exp(rg))
+    ref = 0.2 * rdy * rw * rx / np.sqrt((rx * rx).mean(-1, keepdims=True) + 1e-5) * s * rest
+    assert_within(dg, ref, (half_step(dt) + 2 * c) * np.abs(ref), "dgate")
+
+
+def test_head_norm_infinite_gates(nsp):
+    """A gate of minus infinity closes, one of plus infinity opens; neither has a gradient,
+    and a NaN stays one."""
+    x = randn(37, 5, 2, 64, dt=F32)
+    dy, g = randn(38, 5, 2, 64, dt=F32), torch.zeros_like(x)
+    g[0], g[1], g[2, 0, 0] = float("-inf"), float("inf"), float("nan")
+    y, (dx, _, dg) = nsp.head_norm(x, gate=g), nsp.head_norm_bwd(x, dy, gate=g)
+    assert (y[0] == 0).all() and torch.equal(y[1], nsp.head_norm(x)[1])
+    assert (dg[:2] == 0).all() and (dx[0] == 0).all() and torch.isfinite(dx[1]).all()
+    assert torch.isnan(y[2, 0, 0]) and torch.isnan(dg[2, 0, 0]) and torch.isfinite(y[3:]).all()
+
+
 def test_head_norm_views_and_edges(nsp):
     """Columns of a fused tensor; zero rows and extreme gates; no rows; results
     the same bits twice."""

@@ -13,6 +13,7 @@
 // second small kernel, always in the same order.  32768 x 16 rows of 128 bf16 columns
 // with gate and weight: 61.8 us, 6.5 TB/s; backward of 16383 x 16 such rows: 56.7 us,
 // 5.9 TB/s (some 2.5 of them the second kernel).
+#include <cfloat>
 #include <algorithm>
 
 #include "layer.cuh"
@@ -25,10 +26,15 @@ using namespace tc;
 
 constexpr int kThreads = 256;
 
-// exp to 2 ulp, the reciprocal to 1 (of 1 at least; the largest give zero)
-__device__ __forceinline__ float sigmoid(float g) {
+// 1 / (1 + exp(-g)), and exp(-g).  With float32 tensors exp is off by 2 ulp at most; with
+// bf16 ones the short form is off by some 2 + 1.2 |g| ulp, 2^-16 of the value for the
+// smallest gates that do not give zero, next to a rounding of 2^-8.  The reciprocal (of 1
+// at least) is off by 1 ulp; below 2^-126 (a gate under -87) it is zero.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g, float& e) {
+  e = sizeof(T) == 4 ? expf(-g) : __expf(-g);
   float x;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(1.f + __expf(-g)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(1.f + e));
   return x;
 }
 
@@ -47,10 +53,15 @@ __device__ __forceinline__ uint4 pack2(const uint64_t (&x)[Vec<T>::N / 2]) {
   for (int i = 0; i < Vec<T>::N / 2; ++i) f2_unpack(x[i], t[2 * i], t[2 * i + 1]);
   return Vec<T>::pack(t);
 }
-__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
-  float a, b;
+// A pair's sigmoids; `rest` becomes 1 - sigmoid = exp(-g) sigmoid, which a difference
+// from 1 would not have for a large gate.  (exp may be infinite where sigmoid is zero.)
+template <typename T>
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g, uint64_t& rest) {
+  float a, b, ea, eb;
   f2_unpack(g, a, b);
-  return f2_pack(sigmoid(a), sigmoid(b));
+  const uint64_t s = f2_pack(sigmoid<T>(a, ea), sigmoid<T>(b, eb));
+  rest = f2_mul(f2_pack(fminf(ea, FLT_MAX), fminf(eb, FLT_MAX)), s);
+  return s;
 }
 
 __device__ __forceinline__ float group_sum(float x, int lanes) {
@@ -128,7 +139,8 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const NormArgs a, i
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           t[i] = t[i] * r * w[v][i];
-          if (G != nullptr) t[i] *= sigmoid(q[i]);
+          float e;
+          if (G != nullptr) t[i] *= sigmoid<T>(q[i], e);
         }
         st_once(Y + row * a.d + c * N, Vec<T>::pack(t));
       }
@@ -208,8 +220,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) head_norm_bwd_kernel
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           if (G != nullptr) {
-            sg[v][i] = sigmoid2(sg[v][i]);
-            us[v][i] = f2_mul(us[v][i], sg[v][i]);
+            us[v][i] = f2_mul(us[v][i], sigmoid2<T>(sg[v][i], sg[v][i]));   // (sg: 1 - sigmoid from here on)
           }
           uw[v][i] = f2_mul(us[v][i], w[v][i]);
           ss = f2_fma(t[v][i], t[v][i], ss);
@@ -223,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) head_norm_bwd_kernel
       const float mean = group_sum(u0 + u1, lanes) * r * inv_d;      // mean(u n) / s
       const float sr = a.scale * r;
       const uint64_t sr2 = f2_pack(sr, sr), nm2 = f2_pack(-sr * mean * r, -sr * mean * r);
-      const uint64_t one = f2_pack(1.f, 1.f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = lane + v * lanes;
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) head_norm_bwd_kernel
         for (int i = 0; i < P; ++i) {
           const uint64_t st = f2_mul(t[v][i], sr2);                  // s n
           dw[v][i] = f2_fma(st, us[v][i], dw[v][i]);
-          if (G != nullptr) sg[v][i] = f2_mul(f2_mul(st, uw[v][i]), f2_sub(one, sg[v][i]));
+          if (G != nullptr) sg[v][i] = f2_mul(f2_mul(st, uw[v][i]), sg[v][i]);
           t[v][i] = f2_fma(uw[v][i], sr2, f2_mul(t[v][i], nm2));
         }
         st_once(DX + row * a.d + c * N, pack2<T>(t[v]));
