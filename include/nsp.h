@@ -647,9 +647,12 @@ int32_t nsp_diff_lambda_bwd(const void* dlambda, const void* q1, const void* k1,
  *     [Hq][2][T], or NULL likewise.  out and out2 are of io_dtype.
  * All pointers 16-byte aligned, bf16 out and out2 32-byte aligned.  Outputs
  * must not overlap any input or one another (not checked).  Errors and the
- * status word as nsp_attn_fwd.  A non-finite value in one document's
- * v may reach rows of documents less than 128 tokens away from it (the
- * product with a zero probability is not finite).
+ * status word as nsp_attn_fwd; a cu_seqlens that reaches past T is cut there.
+ * v has to be finite in every row, those of padding documents too: masked
+ * keys have probability zero, which times a non-finite value is NaN, so that
+ * such a value makes NaN of rows that do not see it, in its own document and in
+ * those around it that share its tiles of 128 rows or keys, or a neighbour's.
+ * A non-finite q or k reaches the rows that have or see it and no others.
  * ---------------------------------------------------------------------- */
 size_t nsp_diff_attn_fwd_workspace_size(int64_t T);
 
@@ -666,10 +669,11 @@ int32_t nsp_diff_attn_fwd(const void* q, const void* k, const void* v, const voi
  *   ds^1 = p^1 (dp - delta^1),  ds^2 = -lambda p^2 (dp - delta^2),
  *   dq^m = scale sum_j ds^m_j k^m_j,  dk^m = scale sum_t ds^m_t q^m_t,
  *   dv = sum_t (p^1_t - lambda p^2_t) dout_t  (dk, dv over the group's heads),
- *   dlambda = -delta^2 of each token, or its sum over the tokens.
- * Every output is written whole, and sums run in one fixed order: results are
- * the same bits on every run.  A non-finite value in one document's q, k or
- * dout may reach rows of documents less than 128 tokens away from it. */
+ *   dlambda = -sum_j p^2_j dp_j of each token, or its sum over the tokens.
+ * bf16: delta^m are sums over the rounded out and out2, dlambda is summed in
+ * float32 from p and dp before they are rounded.  Every output is written whole,
+ * and sums run in one fixed order: results are the same bits on every run.
+ * q, k, v and dout have to be finite in every row, for the forward's reason. */
 size_t nsp_diff_attn_bwd_workspace_size(int64_t T, int32_t Hq, int32_t Hkv, int32_t d,
                                         int32_t io_dtype);
 

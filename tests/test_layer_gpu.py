@@ -748,6 +748,39 @@ def test_diff_attention_masked_neighbours(nsp):
     assert torch.isnan(got[50:80]).any()
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 128), (8, 1, 64), (3, 3, 64)])
+def test_diff_attention_non_finite_queries_and_keys(nsp, dt, hq, hkv, d):
+    """A NaN query is its own row's, a NaN or infinite key those rows' that see it: rows
+    before it in its document and all other documents keep their bits.  Whatever a stream
+    holds, the call ends without an error and leaves nothing behind for the next."""
+    lens = [150, 300, 40]
+    q, k, v, lam, do, cu = diff_inputs(155, lens, hq, hkv, d, dt, True)
+    n = nsp.load().nsp_diff_attn_bwd_workspace_size(sum(lens), hq, hkv, d, nsp._DTYPES[dt])
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def step(x):
+        out, out2, lse = nsp.diff_attn_fwd(*x, lam, cu, save=True, workspace=ws)
+        assert nsp.nsp_status_query(ws) == nsp.NSP_OK
+        grads = nsp.diff_attn_bwd(*x, lam, out, out2, do, lse, cu, workspace=ws)
+        assert nsp.nsp_status_query(ws) == nsp.NSP_OK
+        return (out, out2, lse) + grads
+
+    want = step((q, k, v))
+    keys, queries = k.clone(), q.clone()
+    keys[290], keys[300, :, ::2] = float("nan"), float("inf")
+    queries[200] = float("nan")
+    out, out2, lse = step((queries, keys, v))[:3]
+    same = [r for r in range(sum(lens)) if r != 200 and not 290 <= r < 450]
+    for a, b in zip((out, out2, lse.permute(2, 0, 1)), (want[0], want[1], want[2].permute(2, 0, 1))):
+        assert torch.equal(a[same], b[same])
+        assert torch.isnan(a[200]).all() and torch.isnan(a[290:450]).all()
+    bad = [torch.full_like(t, float("nan")) for t in (q, k, v)]
+    assert torch.isnan(step(bad)[0]).all()
+    for a, b in zip(step((q, k, v)), want):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("backward", [False, True])
 def test_diff_attention_timeout(nsp, backward):
     """A wait that runs out is recorded, the context stays usable and the same
