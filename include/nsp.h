@@ -578,8 +578,9 @@ int32_t nsp_seq2head_permute_groups(const void* in, void* out, int32_t B, int64_
  *     The contents of cu_seqlens are not checked here (there is no status
  *     word); they never lead outside the buffers.
  *   freqs: device float64 [rot / 2], radians per position.  The angle's whole
- *     turns are taken off in integer arithmetic: it is exact to 2^-32 turns
- *     at any position.
+ *     turns are taken off in integer arithmetic, at any position; what is left is
+ *     off by 2^-52 of the whole angle (the float64 frequency as a fraction of a
+ *     turn) and by its own rounding to float32, 2^-26 turns at most.
  *   d in 2..1024; rot even, 2..d; sums and products in float32.  Pointers
  *     need their element's alignment; 16-byte aligned ones with strides, d
  *     and rot (halves: rot / 2) of whole 16-byte pieces are several times

@@ -10,8 +10,10 @@
 // converted once per block to a fixed-point fraction of a turn, 2^-64 turns
 // per unit, so that position x frequency is one integer product whose wrap
 // modulo 2^64 is the reduction modulo whole turns, exactly; its top 32 bits,
-// signed, are the angle in [-1/2, 1/2) turns, off by at most 2^-32 turns (and
-// by the float64 frequency's own 2^-53 relative error).
+// signed, are the angle in [-1/2, 1/2) turns, cut off by at most 2^-32 turns.  Two
+// errors are larger: the frequency as a fraction of a turn is a float64 product,
+// 2^-52 of the whole angle (2^-36 turns at position 400000 and frequency 1), and the 32
+// bits are rounded to float32 for the sine, 2^-26 turns at most.
 //
 // Bound: HBM, one read and one write of every element.  A team of threads
 // owns one token and a 16-byte piece of a head each (both pieces of the pair
