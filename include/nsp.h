@@ -577,7 +577,7 @@ int32_t nsp_seq2head_permute_groups(const void* in, void* out, int32_t B, int64_
  *     positions is given).  Rows at or past cu_seqlens[ndoc] are not written.
  *     The contents of cu_seqlens are not checked here (there is no status
  *     word); they never lead outside the buffers.
- *   freqs: device float64 [rot / 2], radians per position.  The angle's whole
+ *   freqs: device float64 [rot / 2], finite, radians per position.  The angle's whole
  *     turns are taken off in integer arithmetic, at any position; what is left is
  *     off by 2^-52 of the whole angle (the float64 frequency as a fraction of a
  *     turn) and by its own rounding to float32, 2^-26 turns at most.

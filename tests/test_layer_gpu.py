@@ -97,6 +97,23 @@ def test_rope_far_positions(nsp):
                "far", err)
 
 
+@pytest.mark.parametrize("d", [64, 6])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rope_angle(nsp, d, sign):
+    """Sine and cosine themselves, of pairs (1, 0): off by the angle's 2^-26 turns and
+    2^-52 of the whole angle, whichever way a frequency turns, and by 4 e (2 ulp of
+    sincospi)."""
+    pos = np.array([0, 1, 399999, 2 ** 30 + 7, 2 ** 31 - 1, -5, -2 ** 31], np.int64)
+    fr = sign * np.logspace(-8, 0.5, d // 2)
+    x = torch.zeros((len(pos), 1, d), device="cuda")
+    x[..., :d // 2] = 1
+    got, _ = nsp.rope(x, None, None, torch.from_numpy(fr).cuda(), positions=torch.from_numpy(pos).int().cuda())
+    a = L.rope_angles(pos, fr)
+    tol = 4 * E + 2 * np.pi * 2.0 ** -26 + np.abs(pos[:, None] * fr) * 2.0 ** -52
+    ref = np.concatenate([np.cos(a), np.sin(a)], -1)[:, None]
+    assert_within(got, ref, np.concatenate([tol, tol], -1)[:, None], "angle")
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_rope_fused_views_in_place_groups(nsp, inter):
     """Columns of a fused projection in, packed, head-grouped and in-place out;

@@ -43,10 +43,12 @@ __device__ __forceinline__ int64_t row_offset(int64_t t, int h, int64_t stride, 
   return (((int64_t)g * len + t) * hpg + (h - g * hpg)) * d;
 }
 
+// (of the magnitude, then negated: 1 minus a small fraction would lose its bits)
 __device__ __forceinline__ uint64_t fixed_turns(double f) {
-  double x = f * 0.15915494309189533576888;          // 1 / (2 pi)
+  double x = fabs(f) * 0.15915494309189533576888;    // 1 / (2 pi)
   x -= floor(x);
-  return __double2ull_rn(x * 18446744073709551616.0);
+  const uint64_t u = __double2ull_rn(x * 18446744073709551616.0);
+  return f < 0 ? 0 - u : u;
 }
 
 __device__ __forceinline__ void turn(int64_t pos, uint64_t fx, float m, bool inverse, float& c,
