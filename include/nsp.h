@@ -567,8 +567,8 @@ int32_t nsp_seq2head_permute_groups(const void* in, void* out, int32_t B, int64_
  *     out device [len, heads, d] of io_dtype, tokens in_stride / out_stride
  *     elements apart (0: heads * d), so that in or out can be columns of a
  *     fused projection's tensor.  in and out may be the same buffer with the
- *     same stride (in place); any other overlap of an input or an output with
- *     an output is NSP_ERR_INVALID.  groups = P > 1: the rotated side (out,
+ *     same stride (in place); any other overlap of an output with another
+ *     array of the call is NSP_ERR_INVALID.  groups = P > 1: the rotated side (out,
  *     or in when inverse = 1) is in the head-group-major layout
  *     [P][len][heads / P][d] of nsp_attn_fwd_headgroups, packed.
  *   positions: device int32 [len], or NULL: row r is then global token

@@ -154,6 +154,21 @@ X, Y = A + (1 << 20), A + (2 << 20)
 INVALID, UNSUPPORTED, ALIGN = nsp.NSP_ERR_INVALID, nsp.NSP_ERR_UNSUPPORTED, nsp.NSP_ERR_ALIGN
 
 
+@pytest.mark.parametrize("kw", [
+    {"pos": Y + 64}, {"pos": Y - 36}, {"pos": Y + 10 * 1024 - 4}, {"freqs": Y}, {"freqs": Y - 504}, {"cu": Y + 4},
+    {"cu": Y - 8}, {"cu": Y + 2048 * 9, "tensors": [(X, Y, 0, 1024, 4, 1)]},
+    {"freqs": Y, "tensors": [(Y, Y, 0, 0, 4, 1)]},                      # (in place as well)
+])
+def test_rope_outputs_over_what_it_reads(lib, kw):
+    """An output over the positions, the frequencies or the documents is refused."""
+    assert _rope(lib, **kw) == INVALID
+
+
+def test_rope_outputs_beside_what_it_reads(lib):
+    """Neighbours are not (checked with no rows, which launches nothing)."""
+    assert _rope(lib, len=0, pos=Y, freqs=Y, cu=Y) == nsp.NSP_OK
+
+
 @pytest.mark.parametrize("kw,expect", [
     ({"n": 0}, INVALID), ({"n": 5}, INVALID), ({"cu": None}, INVALID), ({"ndoc": 0}, INVALID),
     ({"len": -1}, INVALID), ({"start": -1}, INVALID), ({"rot": 63}, INVALID), ({"rot": 130}, INVALID),

@@ -119,6 +119,11 @@ int32_t nsp_rope(const nsp_rope_tensor_t* tensors, int32_t n, const int32_t* cu_
       if (!in_place && overlap(in[i], out[j])) return NSP_ERR_INVALID;
       if (i < j && overlap(out[i], out[j])) return NSP_ERR_INVALID;
     }
+  const Span read[] = {packed(positions, 1, len * 4), packed(freqs, 1, rot / 2 * 8),
+                       packed(positions ? nullptr : cu_seqlens, 1, ((int64_t)ndoc + 1) * 4)};
+  for (int32_t j = 0; j < n; ++j)
+    for (const Span& r : read)
+      if (overlap(r, out[j])) return NSP_ERR_INVALID;
   if (len == 0) return NSP_OK;
   a.n = n;
   a.cu = cu_seqlens; a.ndoc = ndoc; a.positions = positions;
