@@ -622,8 +622,9 @@ int32_t nsp_rope_freqs(int32_t rot, double base, int32_t scaling, double factor,
  * The backward writes dq1 = g e1 k1, dk1 = g e1 q1, dq2 = -g e2 k2,
  * dk2 = -g e2 q2 ([n][dl], io_dtype), e1, e2 the two exponentials and g =
  * dlambda[h] (io_dtype), or its sum over the heads when n = 1.  Sums in
- * float32.  Pointers need their element's alignment.  A gradient that overlaps
- * an input or another gradient is NSP_ERR_INVALID.
+ * float32.  Pointers need their element's alignment.  A lambda that overlaps a
+ * vector, or a gradient that overlaps an input or another gradient, is
+ * NSP_ERR_INVALID.
  * ---------------------------------------------------------------------- */
 int32_t nsp_diff_lambda_fwd(const void* q1, const void* k1, const void* q2, const void* k2,
                             int32_t n, int32_t dl, int32_t heads, float init, int32_t io_dtype,

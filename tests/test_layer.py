@@ -211,6 +211,13 @@ def test_lambda_refusals(lib, kw, expect):
                                        A + 20480, A + 24576, A + 28672, A + 32768, None) == expect
 
 
+@pytest.mark.parametrize("lam", [A, A + 508, A + 4096 + 64, A + 8192 + 510, A + 12288 - 6])
+def test_lambda_over_a_vector(lib, lam):
+    """Vectors of 4 x 64 bf16 (512 bytes), lambda of 4 (8 bytes)."""
+    assert lib.nsp_diff_lambda_fwd(A, A + 4096, A + 8192, A + 12288, 4, 64, 4, 0.8, nsp.NSP_BF16, lam,
+                                   None) == INVALID
+
+
 @pytest.mark.parametrize("kw,expect", [
     ({"heads": 0}, INVALID), ({"d": 0}, INVALID), ({"d": 60}, UNSUPPORTED), ({"d": 1024}, UNSUPPORTED),
     ({"tokens": -1}, INVALID), ({"tokens": 1 << 31}, UNSUPPORTED), ({"eps": 0.0}, INVALID),

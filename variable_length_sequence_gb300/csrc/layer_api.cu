@@ -155,6 +155,9 @@ int32_t nsp_diff_lambda_fwd(const void* q1, const void* k1, const void* q2, cons
   const int32_t st = lambda_check(v, lambda, n, dl, heads, io_dtype);
   if (st != NSP_OK) return st;
   if (!std::isfinite(init)) return NSP_ERR_INVALID;
+  const int64_t es = elem_bytes(io_dtype);
+  for (int i = 0; i < 4; ++i)
+    if (overlap(packed(lambda, 1, heads * es), packed(v[i], n, dl * es))) return NSP_ERR_INVALID;
   return launch_diff_lambda(v, n, dl, heads, init, io_dtype, lambda,
                             reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? NSP_OK
