@@ -38,11 +38,14 @@
 // product to issue: 32 instructions of a tile take 3500 cycles, 110 each, against
 // 68 to 76 of independent ones back to back (dP of the next tile between dQ_1's or
 // dQ_2's, instruction by instruction or half by half, is 2 to 4 % slower: 600 us
-// for both kernels against 581, with 128-token tiles of one head).  212 us for the same
-// documents (770 TFLOP/s of their 6 d).
+// for both kernels against 581, with 128-token tiles of one head).
 // The gradient of lambda comes from here too, -sum_j P_2 dP of each row, from the
 // float32 values before any of them is rounded: its terms cancel over the tokens, and
-// <dout, out2> with the saved bf16 out2 is off by 1 % and more where they do.
+// <dout, out2> with the saved bf16 out2 is off by 1 % and more where they do.  236 us for
+// the same documents (693 TFLOP/s of their 6 d), 213 without that sum: its 32 packed
+// instructions a warp and tile, 128 with a mask, stand in the issue slots of the softmax
+// (behind the arrival that the products wait for they cost the same, or registers: 834 us
+// of the step against 761).
 //
 // Roles, dK/dV: 16 softmax warps (four column groups of four lane quadrants;
 // with 8 warps of 64 columns the loop is 18 KB of instructions and waits for
@@ -54,8 +57,8 @@
 // Rounding: P_1 + c P_2 and dS_m are rounded to bf16, as the tensor core's operands
 // next to bf16 inputs; delta_m are float32 sums over the bf16 out and out2 of the
 // forward; scores, exponentials, sums and shares are float32.
-// Against exact arithmetic dQ and dK are off by 0.0026 (relative norm), where outputs
-// rounded to bf16 alone leave 0.0018.
+// Against exact arithmetic dQ and dK are off by 0.0025 (relative norm) and dV by 0.0024,
+// where outputs rounded to bf16 alone leave 0.0017; dlambda by its rounding.
 #include "diff_tc.cuh"
 
 namespace nsp {

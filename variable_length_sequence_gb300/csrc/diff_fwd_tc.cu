@@ -47,7 +47,7 @@
 // Rounding: P is rounded to bf16 as the product's operand; the row sums use
 // the unrounded float32 values.  The running output is rescaled only when a
 // row's maximum has grown by more than 2^8 (exact either way: numerator and
-// denominator share the reference).
+// denominator share the reference).  lse takes the short logarithm, 2^-22 or 2 ulp of it.
 #include <cudaTypedefs.h>
 
 #include "diff_tc.cuh"

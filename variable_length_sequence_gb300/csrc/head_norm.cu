@@ -11,8 +11,8 @@
 // The weight's gradient is summed by every thread for its own columns over
 // its rows, then over the block in shared memory, and over the blocks by a
 // second small kernel, always in the same order.  32768 x 16 rows of 128 bf16 columns
-// with gate and weight: 61.8 us, 6.5 TB/s; backward of 16383 x 16 such rows: 56.7 us,
-// 5.9 TB/s (some 2.5 of them the second kernel).
+// with gate and weight: 61.7 us, 6.5 TB/s; backward of 16383 x 16 such rows: 58.5 us a
+// call, 5.7 TB/s (some 2.5 of them the second kernel).
 #include <cfloat>
 #include <algorithm>
 

@@ -92,7 +92,9 @@ inline int item_shift(int group, int64_t T) {
 // workspace's size depends on it).  One document of 4000 tokens, 4 heads on 1: 358 us whole,
 // 146 in 8 parts; 8000 tokens in documents around 1024, 8 heads on 2: 369 whole, 231 in 2;
 // 16384 tokens, 16 heads on 4, 512 key tiles: 555 whole, 618 in 2 (the shares' way through
-// memory).
+// memory).  The rule counts tiles, not their work: one causal document loses some 15 % just
+// past the border, where the first tiles, with twice the mean work, are whole again (8 heads
+// on 2: 752 us at 9600 tokens, 895 at 9728; 16 on 4: 420 at 4736, 478 at 4864).
 inline int key_parts(int64_t T, int Hkv) {
   const int64_t items = ceil_div(T, 128) * Hkv;
   int n = 1;

@@ -875,7 +875,8 @@ def diff_attn_fwd(q, k, v, lam, cu_seqlens, scale=None, causal=True, save=False,
     """Differential attention of a packed stream: q [T, Hq, d], k and v
     [T, Hkv, d], map m of a head in columns [m d/2, (m + 1) d/2) of q and k,
     lam [Hq], [Hq, 1] or [Hq, T].  Returns out [T, Hq, d]; with save=True
-    (out, out2, lse), what diff_attn_bwd needs."""
+    (out, out2, lse), what diff_attn_bwd needs.  v has to be finite in every row,
+    those of padding documents too (see nsp_diff_attn_fwd)."""
     fn = "diff_attn_fwd"
     io, dev, T, Hq, Hkv, d, n = _diff_shapes(fn, q, k, v, lam, cu_seqlens)
     scale = (d // 2) ** -0.5 if scale is None else scale
@@ -896,7 +897,7 @@ def diff_attn_fwd(q, k, v, lam, cu_seqlens, scale=None, causal=True, save=False,
 def diff_attn_bwd(q, k, v, lam, out, out2, dout, lse, cu_seqlens, scale=None, causal=True,
                   workspace=None, stream=None):
     """Gradients (dq, dk, dv, dlam) of diff_attn_fwd(save=True); dlam is
-    [Hq, 1] or [Hq, T]."""
+    [Hq, 1] or [Hq, T].  q, k, v and dout have to be finite in every row."""
     fn = "diff_attn_bwd"
     io, dev, T, Hq, Hkv, d, n = _diff_shapes(fn, q, k, v, lam, cu_seqlens, out=out, out2=out2,
                                              dout=dout)
