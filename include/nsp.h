@@ -10,7 +10,11 @@
  *   - the Ulysses seq-sharded -> head-sharded layout permutation;
  *   - a differential attention layer's operators: rotary positions, the
  *     learned difference weight, differential attention forward and backward,
- *     and the norm of each head's output.
+ *     and the norm of each head's output;
+ *   - a packed post-training step's operators next to attention: the norm of
+ *     query and key heads with the rotation in the same pass, log-probabilities
+ *     of given tokens, the clipped policy loss, the preference loss over pairs of
+ *     documents, and the norm and clipping of many gradients.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -715,6 +719,63 @@ int32_t nsp_head_norm_bwd(const void* x, int64_t x_stride, const void* weight, c
                           const void* dy, int64_t tokens, int32_t heads, int32_t d, float eps,
                           float scale, int32_t io_dtype, void* dx, void* dgate, void* dweight,
                           void* workspace, size_t workspace_bytes, nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The operators of a packed post-training step next to attention.  No page has
+ * a counterpart of them; they follow the conventions above.
+ *
+ * Norm of query and key heads with the rotation in the same pass
+ * --------------------------------------------------------------
+ * Every head's row is normed by its root mean square, weighted, and rotated by
+ * its token's position as nsp_rope does:
+ *   r = 1 / sqrt(mean(x^2) + eps),  n = x r,  y = rotated(weight * n).
+ *   tensors: HOST array of n (1..4) descriptors, read during the call: x device
+ *     [len, heads, d] and y of io_dtype, tokens x_stride / y_stride elements
+ *     apart (0: heads * d), so that x can be columns of a fused projection;
+ *     weight device [d] of io_dtype or NULL (ones).  groups = P > 1: y is in the
+ *     head-group-major layout [P][len][heads / P][d], packed.  y may take x's
+ *     place (the same buffer and stride, groups = 1).
+ *   cu_seqlens, ndoc, positions, start, len, rot, freqs, interleaved, mscale:
+ *     as nsp_rope, rows at or past cu_seqlens[ndoc] not written among them.
+ *   d in 2..512, eps > 0; statistics, sums and products in float32.  Pointers
+ *     need their element's alignment; 16-byte aligned ones with strides, d
+ *     and rot (halves: rot / 2) of whole 16-byte pieces are several times
+ *     faster.
+ * The backward reads x and the gradient dy of y (y's stride and groups) and
+ * writes, with z = dy rotated back and u = weight * z,
+ *   dx = r (u - n mean(u n)), tokens dx_stride elements apart, and, unless
+ *   NULL, dweight [d] = sum over rows of n z.
+ * dx may take x's place, or with groups = 1 dy's (the same buffer and stride).
+ * The workspace (nsp_qk_norm_rope_bwd_workspace_size bytes, which reads only
+ * the descriptors' heads; required) holds dweight's partial sums, added in one
+ * fixed order.  Rows at or past cu_seqlens[ndoc] are not written and add
+ * nothing.  Any other overlap of an output or the workspace with another array
+ * of the call is NSP_ERR_INVALID.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const void* x;
+  const void* weight;
+  void* y;              /* forward */
+  const void* dy;       /* backward */
+  void* dx;
+  void* dweight;
+  int64_t x_stride, y_stride, dx_stride;
+  int32_t heads, groups;
+} nsp_qk_tensor_t;
+
+int32_t nsp_qk_norm_rope_fwd(const nsp_qk_tensor_t* tensors, int32_t n, const int32_t* cu_seqlens,
+                             int32_t ndoc, const int32_t* positions, int64_t start, int64_t len,
+                             int32_t d, int32_t rot, const double* freqs, int32_t interleaved,
+                             float mscale, float eps, int32_t io_dtype, nsp_stream_t stream);
+
+size_t nsp_qk_norm_rope_bwd_workspace_size(const nsp_qk_tensor_t* tensors, int32_t n, int64_t len,
+                                           int32_t d);
+
+int32_t nsp_qk_norm_rope_bwd(const nsp_qk_tensor_t* tensors, int32_t n, const int32_t* cu_seqlens,
+                             int32_t ndoc, const int32_t* positions, int64_t start, int64_t len,
+                             int32_t d, int32_t rot, const double* freqs, int32_t interleaved,
+                             float mscale, float eps, int32_t io_dtype, void* workspace,
+                             size_t workspace_bytes, nsp_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Status word of the last call that used `workspace`.  Synchronises `stream`

@@ -87,6 +87,11 @@ _SIGNATURES = {
     "nsp_head_norm_bwd_workspace_size": (_sz, [_i64, _i32, _i32]),
     "nsp_head_norm_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _i32, _vp,
                                  _vp, _vp, _vp, _sz, _vp]),
+    "nsp_qk_norm_rope_fwd": (_i32, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _vp, _i32,
+                                    _f32, _f32, _i32, _vp]),
+    "nsp_qk_norm_rope_bwd_workspace_size": (_sz, [_vp, _i32, _i64, _i32]),
+    "nsp_qk_norm_rope_bwd": (_i32, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _vp, _i32,
+                                    _f32, _f32, _i32, _vp, _sz, _vp]),
     "nsp_status_query": (_i32, [_vp, _vp]),
     "nsp_attn_bwd_ds_cache_size": (_sz, [_vp, _i32, _i32, _i32]),
     "nsp_attn_bwd_blocks_ds_cache_size": (_sz, [_vp, _i32, _i32, _vp, _i32, _i32]),
@@ -113,6 +118,14 @@ class RopeTensor(C.Structure):
     """nsp_rope_tensor_t: one tensor of a rotation."""
     _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("in_stride", C.c_int64),
                 ("out_stride", C.c_int64), ("heads", C.c_int32), ("groups", C.c_int32)]
+
+
+class QkTensor(C.Structure):
+    """nsp_qk_tensor_t: one tensor of a head norm with rotation."""
+    _fields_ = [("x", C.c_void_p), ("weight", C.c_void_p), ("y", C.c_void_p), ("dy", C.c_void_p),
+                ("dx", C.c_void_p), ("dweight", C.c_void_p), ("x_stride", C.c_int64),
+                ("y_stride", C.c_int64), ("dx_stride", C.c_int64), ("heads", C.c_int32),
+                ("groups", C.c_int32)]
 
 
 class AttnCost(C.Structure):
@@ -957,3 +970,134 @@ def head_norm_bwd(x, dy, weight=None, gate=None, eps=1e-6, scale=1.0, workspace=
                                0 if ws is None else ws.numel(), _stream_of(stream, dev))
     _check("nsp_head_norm_bwd", st)
     return dx, dw, dg
+
+
+# ----------------------------------------------------------------------------- packed post-training step
+
+_Qk1, _Qk2 = QkTensor * 1, QkTensor * 2
+
+
+def _qk_shapes(fn, q, k, cu_seqlens, freqs, wq, wk, layout, positions, q_groups, **more):
+    """Checks of q, k and what rotates them; `more`: more tensors of their type."""
+    io = _io(fn, q.dtype)
+    dev = _on_device(fn, q.dtype, q=q, k=k, wq=wq, wk=wk, **more)
+    _on_device(fn, torch.int32, cu_seqlens=cu_seqlens, positions=positions)
+    _on_device(fn, torch.float64, freqs=freqs)
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"{fn}: unknown layout {layout!r}")
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError(f"{fn}: q is [T, Hq, d], k [T, Hkv, d]")
+    T, Hq, d = q.shape
+    if k is not None:
+        _shape(fn, "k", k, (T, k.shape[1], d))
+    elif wk is not None:
+        raise ValueError(f"{fn}: wk without k")
+    if q_groups < 1 or Hq % q_groups != 0:
+        raise ValueError(f"{fn}: q_groups does not divide the heads")
+    _shape(fn, "wq", wq, (d,))
+    _shape(fn, "wk", wk, (d,))
+    _shape(fn, "positions", positions, (T,))
+    if freqs.dim() != 1:
+        raise ValueError(f"{fn}: freqs is [rot / 2]")
+    if positions is None and (cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
+        raise ValueError(f"{fn}: cu_seqlens [documents + 1] or positions are needed")
+    return io, dev, T, Hq, d
+
+
+def qk_norm_rope(q, k, cu_seqlens, freqs, wq=None, wk=None, layout="half", mscale=1.0, eps=1e-6,
+                 start=0, positions=None, q_groups=1, out=None, stream=None):
+    """Norm every head's row of q [T, Hq, d] and k [T, Hkv, d] (k may be None) by
+    its root mean square, weight it by wq and wk [d] (None: ones) and rotate it
+    by its token's position, in one pass: rope(head_norm(q, wq), head_norm(k,
+    wk), ...) without the rounding in between.
+
+    The other arguments are those of `rope`: q and k may have tokens any stride
+    apart, q_groups = P > 1 returns q as [P, T, Hq / P, d], out = (q_out, k_out)
+    may be q and k themselves, and rows at or past cu_seqlens[-1] are not
+    written."""
+    fn = "qk_norm_rope"
+    P = int(q_groups)
+    qo, ko = out if out is not None else (None, None)
+    io, dev, T, Hq, d = _qk_shapes(fn, q, k, cu_seqlens, freqs, wq, wk, layout, positions, P,
+                                   q_out=qo, k_out=ko)
+    q_shape = (P, T, Hq // P, d) if P > 1 else (T, Hq, d)
+    qo_stride = ko_stride = 0                     # (0: packed)
+    if qo is None:
+        qo = _new(stream, q, q_shape)
+    else:
+        _shape(fn, "q_out", qo, q_shape)
+        if P > 1:
+            _ptr(qo)
+        else:
+            qo_stride = _token_stride(fn, "q_out", qo)
+    one = (q.data_ptr(), _ptr(wq), qo.data_ptr(), None, None, None, _token_stride(fn, "q", q),
+           qo_stride, 0, Hq, P)
+    if k is None:
+        ko, n, arr = None, 1, _Qk1(one)
+    else:
+        if ko is None:
+            ko = _new(stream, k, k.shape)
+        else:
+            _shape(fn, "k_out", ko, k.shape)
+            ko_stride = _token_stride(fn, "k_out", ko)
+        n, arr = 2, _Qk2(one, (k.data_ptr(), _ptr(wk), ko.data_ptr(), None, None, None,
+                               _token_stride(fn, "k", k), ko_stride, 0, k.shape[1], 1))
+    st = load().nsp_qk_norm_rope_fwd(C.addressof(arr), n, _ptr(cu_seqlens),
+                                     0 if cu_seqlens is None else cu_seqlens.numel() - 1,
+                                     _ptr(positions), int(start), T, d, 2 * freqs.numel(), _ptr(freqs),
+                                     layout == "interleaved", mscale, eps, io, _stream_of(stream, dev))
+    _check("nsp_qk_norm_rope_fwd", st)
+    return qo, ko
+
+
+def qk_norm_rope_bwd(q, k, dqr, dkr, cu_seqlens, freqs, wq=None, wk=None, layout="half", mscale=1.0,
+                     eps=1e-6, start=0, positions=None, q_groups=1, out=None, workspace=None,
+                     stream=None):
+    """Gradients (dq, dk, dwq, dwk) of qk_norm_rope from those of its results, dqr
+    ([P, T, Hq / P, d] with q_groups = P > 1) and dkr; q and k as the forward
+    took them.  None for a k or a weight that is not there.  out: (dq, dk) to
+    write, tokens any stride apart (columns of the fused projection's gradient),
+    or q and k, or dqr and dkr themselves.  Rows at or past cu_seqlens[-1] are
+    not written and add nothing to the weights' gradients."""
+    fn = "qk_norm_rope_bwd"
+    P = int(q_groups)
+    dq, dk = out if out is not None else (None, None)
+    io, dev, T, Hq, d = _qk_shapes(fn, q, k, cu_seqlens, freqs, wq, wk, layout, positions, P, dqr=dqr,
+                                   dkr=dkr, dq=dq, dk=dk)
+    _shape(fn, "dqr", dqr, (P, T, Hq // P, d) if P > 1 else (T, Hq, d))
+    dq_stride = dk_stride = 0
+    if dq is None:
+        dq = _new(stream, q, q.shape)
+    else:
+        _shape(fn, "dq", dq, q.shape)
+        dq_stride = _token_stride(fn, "dq", dq)
+    dwq = None if wq is None else _new(stream, q, (d,))
+    dwk = None if wk is None else _new(stream, q, (d,))
+    one = (q.data_ptr(), _ptr(wq), None, _ptr(dqr) if P > 1 else dqr.data_ptr(), dq.data_ptr(),
+           _ptr(dwq), _token_stride(fn, "q", q), 0 if P > 1 else _token_stride(fn, "dqr", dqr),
+           dq_stride, Hq, P)
+    if k is None:
+        if dkr is not None:
+            raise ValueError(f"{fn}: dkr without k")
+        dk, n, arr = None, 1, _Qk1(one)
+    else:
+        if dkr is None:
+            raise ValueError(f"{fn}: k without dkr")
+        _shape(fn, "dkr", dkr, k.shape)
+        if dk is None:
+            dk = _new(stream, k, k.shape)
+        else:
+            _shape(fn, "dk", dk, k.shape)
+            dk_stride = _token_stride(fn, "dk", dk)
+        n, arr = 2, _Qk2(one, (k.data_ptr(), _ptr(wk), None, dkr.data_ptr(), dk.data_ptr(), _ptr(dwk),
+                               _token_stride(fn, "k", k), _token_stride(fn, "dkr", dkr), dk_stride,
+                               k.shape[1], 1))
+    lib, at = load(), C.addressof(arr)
+    ws = _workspace(fn, stream, q, lib.nsp_qk_norm_rope_bwd_workspace_size(at, n, T, d), workspace)
+    st = lib.nsp_qk_norm_rope_bwd(at, n, _ptr(cu_seqlens),
+                                  0 if cu_seqlens is None else cu_seqlens.numel() - 1, _ptr(positions),
+                                  int(start), T, d, 2 * freqs.numel(), _ptr(freqs),
+                                  layout == "interleaved", mscale, eps, io, _ptr(ws), ws.numel(),
+                                  _stream_of(stream, dev))
+    _check("nsp_qk_norm_rope_bwd", st)
+    return dq, dk, dwq, dwk
