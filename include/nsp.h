@@ -778,6 +778,154 @@ int32_t nsp_qk_norm_rope_bwd(const nsp_qk_tensor_t* tensors, int32_t n, const in
                              size_t workspace_bytes, nsp_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Log-probability of a given token of every row of logits:
+ *   x_j = scale * logits[t][j],  lse[t] = ln sum_j exp(x_j),
+ *   logp[t] = x_{targets[t]} - lse[t].
+ *   logits: device [rows][vocab] of io_dtype, rows row_stride elements apart (0:
+ *     vocab); targets: device int32 [rows]; a negative target is none: the row is
+ *     not read, whatever it holds, its logp and lse are 0.  A target at or past
+ *     vocab makes its logp NaN.  scale > 0: the inverse of a sampling temperature.
+ *   logp, lse: device float32 [rows]; lse may be NULL.
+ * Logits of minus infinity have probability zero (a row of nothing else, a NaN or
+ * a plus infinity in a row give NaN).  Statistics in float32.
+ * The backward writes
+ *   dlogits[t][j] = scale * dlogp[t] * ([j = targets[t]] - exp(x_j - lse[t])),
+ * rows out_stride elements apart (0: vocab), zeros for a row without a target (whose
+ * dlogp is not used) and NaN for a target at or past vocab.  lse as the forward
+ * wrote it, dlogp device float32 [rows].  dlogits may be the logits' own buffer
+ * with the same stride.  Columns past vocab of a strided tensor are neither read
+ * nor written.
+ * vocab <= 2^20.  Pointers need their element's alignment; logits and dlogits at
+ * the same distance from a 16-byte border, row by row, are several times faster.
+ * Any other overlap of an output with another array is NSP_ERR_INVALID.
+ * ---------------------------------------------------------------------- */
+int32_t nsp_token_logp_fwd(const void* logits, int64_t row_stride, const int32_t* targets, int64_t rows,
+                           int32_t vocab, float scale, int32_t io_dtype, float* logp, float* lse,
+                           nsp_stream_t stream);
+
+int32_t nsp_token_logp_bwd(const void* logits, int64_t row_stride, const int32_t* targets,
+                           const float* lse, const float* dlogp, int64_t rows, int32_t vocab,
+                           float scale, int32_t io_dtype, void* dlogits, int64_t out_stride,
+                           nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Clipped policy loss of a packed stream, with its gradient.  A row is scored if
+ * it has a target (targets[t] >= 0) and lies in a document.  With rho =
+ * exp(logp - old_logp), A the advantage and z = ref_logp - logp:
+ *   surrogate = -min(rho A, min(max(rho, 1 - clip_low), 1 + clip_high) A),
+ *   kl = exp(z) - z - 1 (0 without ref_logp),
+ *   loss = sum over scored rows of w (surrogate + kl_coef kl),
+ * w = 1 / N (mean = NSP_MEAN_TOKENS, N scored rows) or 1 / (D n) (NSP_MEAN_DOCUMENTS:
+ * n scored rows of the row's document, D documents that have one); total > 0
+ * takes the place of N or D (the whole batch's, where a step has several calls).
+ *   logp: device float32 [rows]; old_logp, ref_logp likewise (ref_logp may be NULL
+ *     if kl_coef = 0); advantages: device float32 [ndoc], or [rows] (per_token = 1).
+ *     What rows without a score hold is not used.
+ *   stats: device float32 [4]: loss, and the weighted sums of surrogate, kl and
+ *     clipped (1 where the clip decides: A > 0 and rho > 1 + clip_high, or A < 0
+ *     and rho < 1 - clip_low; such a row's surrogate has no gradient).
+ *   dlogp: device float32 [rows], the loss's gradient; 0 for rows not scored.
+ * nsp_policy_loss_logits does nsp_token_logp_fwd, this and nsp_token_logp_bwd in
+ * one pass over the logits: logp (may be NULL; 0 for rows not scored) and dlogits
+ * as they write them, dlogits the loss's gradient, zeros for rows not scored; it
+ * may be the logits' buffer with the same stride.
+ *   rows: of all arrays; a cu_seqlens that reaches past it is cut there.  A bad
+ *   cu_seqlens sets the status word, and nothing else is written.
+ *   workspace: nsp_policy_loss_workspace_size(rows, ndoc, logits = 0 / 1) bytes.
+ *   0 <= clip_low <= 1, clip_high >= 0.  Sums in one fixed order, to more than
+ *   float32's precision.  An output or workspace that overlaps another array (but
+ *   dlogits as said) is NSP_ERR_INVALID.
+ * ---------------------------------------------------------------------- */
+typedef enum { NSP_MEAN_TOKENS = 0, NSP_MEAN_DOCUMENTS = 1 } nsp_mean;
+
+typedef struct {
+  const float* old_logp;
+  const float* ref_logp;
+  const float* advantages;
+  int32_t per_token;
+  int32_t mean;
+  float clip_low, clip_high, kl_coef, total;
+} nsp_policy_t;
+
+size_t nsp_policy_loss_workspace_size(int64_t rows, int32_t ndoc, int32_t logits);
+
+int32_t nsp_policy_loss(const float* logp, const int32_t* targets, const int32_t* cu_seqlens,
+                        int32_t ndoc, int64_t rows, const nsp_policy_t* policy, float* stats,
+                        float* dlogp, void* workspace, size_t workspace_bytes, nsp_stream_t stream);
+
+int32_t nsp_policy_loss_logits(const void* logits, int64_t row_stride, const int32_t* targets,
+                               const int32_t* cu_seqlens, int32_t ndoc, int64_t rows, int32_t vocab,
+                               float scale, int32_t io_dtype, const nsp_policy_t* policy, float* stats,
+                               float* logp, void* dlogits, int64_t out_stride, void* workspace,
+                               size_t workspace_bytes, nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Preference loss over pairs of documents, with its gradient: documents 2 i and
+ * 2 i + 1 are the chosen and the rejected answer of pair i.
+ *   score_b = sum over document b's scored rows of (logp - ref_logp), divided by
+ *   their number if average = 1 (0 without any),
+ *   rewards[b] = beta score_b,  h = rewards[2 i] - rewards[2 i + 1] - margin,
+ *   loss = mean over pairs of
+ *     NSP_PREFERENCE_SIGMOID: -(1 - smoothing) ln sigma(h) - smoothing ln sigma(-h),
+ *     NSP_PREFERENCE_HINGE:   max(0, 1 - h),
+ *     NSP_PREFERENCE_SQUARE:  (h / beta - 1 / (2 beta))^2.
+ *   logp, ref_logp (NULL: zeros): device float32 [rows]; targets: device int32
+ *   [rows], only their sign is used; ndoc even.
+ *   stats: device float32 [2]: the loss, and the share of pairs whose chosen
+ *   answer's reward is the larger; rewards: device float32 [ndoc]; dlogp: device
+ *   float32 [rows], 0 for rows not scored.
+ * Rows, cu_seqlens, status word, sums and overlaps as nsp_policy_loss (after a bad
+ * cu_seqlens the outputs are unspecified).
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  NSP_PREFERENCE_SIGMOID = 0, NSP_PREFERENCE_HINGE = 1, NSP_PREFERENCE_SQUARE = 2
+} nsp_preference;
+
+size_t nsp_preference_loss_workspace_size(int32_t ndoc);
+
+int32_t nsp_preference_loss(const float* logp, const float* ref_logp, const int32_t* targets,
+                            const int32_t* cu_seqlens, int32_t ndoc, int64_t rows, int32_t kind,
+                            float beta, float smoothing, float margin, int32_t average, float* stats,
+                            float* rewards, float* dlogp, void* workspace, size_t workspace_bytes,
+                            nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Norm of many gradients taken together, and their clipping:
+ *   norm = |unscale| (sum of all g^2)^(1/2) (NSP_NORM_2) or |unscale| max |g|
+ *   (NSP_NORM_INF),
+ *   out = g * unscale * min(1, max_norm / (norm + eps)).
+ *   grads, out, counts, dtypes, out_dtypes: HOST arrays of n (1..16384) device
+ *     pointers, element counts (0 to 2^40) and nsp_dtypes, read during the call.
+ *     Gradients of both types may be mixed, and out may be of the other type
+ *     than its gradient; out[i] may be grads[i] (same type: in place).
+ *   unscale: what the gradients have to be multiplied by (1 / the number of
+ *     micro-batches summed in them, or 1 / a loss scale).
+ *   norm: device float32 [1].  The norm of no elements is 0.
+ * One multiplication in float32 and one rounding to out's type; in place, where the
+ * factor is 1, nothing is read or written again.  The factor is decided on the
+ * device.  A NaN anywhere makes the norm and every output NaN; an infinite norm
+ * makes finite gradients 0 and infinite ones NaN.  Squares are float32: a
+ * gradient past 1.8e19 makes an infinite norm, one below 1e-23 adds nothing.
+ * Sums in one fixed order.  max_norm >= 0, eps > 0.  Pointers need their element's
+ * alignment; grads[i] and out[i] at the same number of elements from a 16-byte
+ * border are faster.  An output, the norm or the workspace
+ * (nsp_grad_norm_workspace_size) that overlaps another array of the call is
+ * NSP_ERR_INVALID (the same gradient twice among them, where it is written).
+ * ---------------------------------------------------------------------- */
+typedef enum { NSP_NORM_2 = 0, NSP_NORM_INF = 1 } nsp_norm;
+
+size_t nsp_grad_norm_workspace_size(const int64_t* counts, int32_t n);
+
+int32_t nsp_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int32_t n,
+                      int32_t kind, float unscale, float* norm, void* workspace, size_t workspace_bytes,
+                      nsp_stream_t stream);
+
+int32_t nsp_grad_clip(const void* const* grads, void* const* out, const int64_t* counts,
+                      const int32_t* dtypes, const int32_t* out_dtypes, int32_t n, int32_t kind,
+                      float unscale, float max_norm, float eps, float* norm, void* workspace,
+                      size_t workspace_bytes, nsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Status word of the last call that used `workspace`.  Synchronises `stream`
  * first (the only synchronising call).  Returns NSP_OK, the recorded device
  * error (NSP_ERR_INVALID for bad cu_seqlens, NSP_ERR_TIMEOUT), or

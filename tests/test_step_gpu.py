@@ -239,3 +239,473 @@ def test_qk_norm_rope_is_norm_then_rope(nsp):
     rdx, rdw, _ = nsp.head_norm_bwd(x, nsp.rope(g, None, cu, fr, inverse=True)[0], w)
     torch.testing.assert_close(dx, rdx, rtol=0, atol=400 * E * float(rdx.abs().max()))
     torch.testing.assert_close(dw, rdw, rtol=0, atol=400 * E * float((x.abs() * g.abs()).sum((0, 1)).max()) * 3)
+
+
+# ----------------------------------------------------------------------------- log-probabilities
+
+SCALE = 0.75                     # (exact in float32)
+
+
+def logits_of(seed, T, V, dt, spread=2.5):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn((T, V), generator=g) * spread).to(dt)
+    y = torch.randint(0, V, (T,), generator=g, dtype=torch.int32)
+    y[torch.rand(T, generator=g) < 0.25] = -1
+    return x.cuda(), y.cuda()
+
+
+def lse_error(x, scale=SCALE):
+    """Absolute error of a row's log sum: an argument's roundings (of the scaled maximum,
+    the scale and the difference: 8 E of the largest magnitude), exp 2 ulp, the
+    terms' sums (a thread's terms one after the other, of 512 threads at least, then 40
+    more), log."""
+    top = scale * np.abs(np.where(np.isfinite(x), x, 0)).max(-1)
+    return E * (8 * top + 64 + x.shape[-1] / 512)
+
+
+def check_logp(x, y, logp, lse, scale=SCALE):
+    x, y = f64(x), y.cpu().numpy()
+    rl, rs = S.token_logp(x, y, scale)
+    err = np.where(y >= 0, lse_error(x, scale), 0)
+    assert_within(logp, rl, err + 2 * E * np.abs(rl), "logp")
+    if lse is not None:
+        assert_within(lse, rs, err + 2 * E * np.abs(rs), "lse")
+
+
+def check_dlogits(x, y, dlogp, got, dt, scale=SCALE, dlogp_err=0.0):
+    x, y = f64(x), y.cpu().numpy()
+    g = f64(dlogp) if isinstance(dlogp, torch.Tensor) else dlogp
+    ref = S.token_logp_bwd(x, y, g, scale)
+    p = np.abs(S.token_logp_bwd(x, y, np.ones(len(y)), scale)) / scale       # p, or 1 - p of the target
+    c = (lse_error(x, scale) + 8 * E)[:, None]
+    # the target's own column is 1 - p: p's error there is c (1 - (1 - p))
+    col = np.where(np.arange(x.shape[1])[None] == y[:, None], 1.0, p)
+    tol = half_step(dt) * np.abs(ref) + np.abs(scale * g)[:, None] * (c * col + 4 * E * p + 2.0 ** -126)
+    tol = tol + np.broadcast_to(np.asarray(dlogp_err), (len(y),))[:, None] * p
+    assert_within(got, ref, np.where(y[:, None] >= 0, tol, 0), "dlogits")
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("T,V", [(1, 1), (3, 2), (7, 8), (5, 31), (4, 257), (9, 1000), (3, 1024), (6, 4096), (5, 4103),
+                                 (2, 16384), (3, 32003), (2, 65536), (2, 100001), (1, 131072), (2, 200000),
+                                 (1, 1 << 20), (700, 264), (400, 1001)])
+def test_token_logp(nsp, dt, T, V):
+    x, y = logits_of(60, T, V, dt)
+    y[0] = V - 1
+    logp, lse = nsp.token_logp(x, y, scale=SCALE)
+    check_logp(x, y, logp, lse)
+    g = randn(61, T, dt=F32)
+    dx = nsp.token_logp_bwd(x, y, lse, g, scale=SCALE)
+    check_dlogits(x, y, g, dx, dt)
+    again, _ = nsp.token_logp(x, y, scale=SCALE)
+    assert torch.equal(again, logp)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("V,stride,shift", [(1000, 1024, 0), (1000, 1001, 0), (999, 1024, 8), (1001, 1003, 1), (40000, 40008, 3),
+                                            (40001, 40001, 5)])
+def test_token_logp_strides(nsp, dt, V, stride, shift):
+    """Padded vocabularies, rows at any distance from a 16-byte border, outputs at the
+    same or at another one, in place: columns behind the vocabulary stay as they were."""
+    T = 6
+    x, y = logits_of(62, T, V, dt)
+    flat = torch.full((T * stride + shift + 64,), float("nan"), dtype=dt, device="cuda")
+    wide = flat[shift:shift + T * stride].view(T, stride)
+    wide[:, :V] = x
+    view = wide[:, :V]
+    logp, lse = nsp.token_logp(view, y, scale=SCALE)
+    check_logp(x, y, logp, lse)
+    g = randn(63, T, dt=F32)
+    for off in (shift, shift + 1):
+        out = torch.full((T * stride + 72,), 7.0, dtype=dt, device="cuda")
+        ov = out[off:off + T * stride].view(T, stride)[:, :V]
+        nsp.token_logp_bwd(view, y, lse, g, scale=SCALE, out=ov)
+        check_dlogits(x, y, g, ov, dt)
+        ov[:] = 7.0
+        assert (out == 7).all()
+    ref = nsp.token_logp_bwd(view, y, lse, g, scale=SCALE)
+    nsp.token_logp_bwd(view, y, lse, g, scale=SCALE, out=view)
+    assert torch.equal(view, ref)
+    view[:] = float("nan")
+    assert torch.isnan(flat).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("V", [40, 1001, 70000])
+def test_token_logp_masked_logits(nsp, dt, V):
+    """Minus infinity has probability zero, wherever it stands (all but one, the
+    target's own); rows without a target may hold anything; NaN, plus infinity and a
+    target past the vocabulary give NaN in their row alone; large magnitudes do not
+    overflow."""
+    x, y = logits_of(64, 8, V, dt)
+    y[:] = torch.arange(8, dtype=torch.int32)
+    inf = float("inf")
+    x[0, 1:] = -inf                       # only the target
+    x[1, 5:] = -inf
+    x[2, 2], x[2, 9:30] = -inf, -inf      # the target itself
+    x[3] = float("nan")
+    y[3] = -1
+    x[4] *= 3e4
+    x[5, 3], x[6, V - 1] = float("nan"), inf
+    y[7] = V
+    logp, lse = nsp.token_logp(x, y, scale=SCALE)
+    g = torch.full((8,), 0.5, device="cuda")
+    g[3] = float("nan")
+    dx = nsp.token_logp_bwd(x, y, lse, g, scale=SCALE)
+    good = [0, 1, 4]
+    check_logp(x[good], y[good], logp[good], lse[good])
+    check_dlogits(x[good], y[good], g[good], dx[good], dt)
+    # (1 - p of a certain target: x_y - lse is off by lse's own rounding)
+    assert logp[0] <= 0 and (dx[0, 1:] == 0).all() and abs(float(dx[0, 0])) <= E * (2 * abs(float(x[0, 0])) + 4)
+    assert logp[2] == -inf and torch.isfinite(lse[2]) and torch.isfinite(dx[2]).all()
+    assert logp[3] == 0 and lse[3] == 0 and (dx[3] == 0).all()
+    assert torch.isnan(logp[5:]).all() and torch.isnan(dx[7]).all()
+    assert torch.isnan(lse[5]) and torch.isnan(lse[6]) and torch.isfinite(lse[7])
+    x[0] = -inf
+    assert torch.isnan(nsp.token_logp(x, y)[0][0])
+
+
+def test_token_logp_no_rows_and_far_rows(nsp):
+    """No rows; offsets past 32 bits."""
+    x = torch.empty((0, 50), device="cuda")
+    y = torch.empty(0, dtype=torch.int32, device="cuda")
+    logp, lse = nsp.token_logp(x, y)
+    assert logp.shape == (0,) and nsp.token_logp_bwd(x, y, lse, logp).shape == (0, 50)
+    T, V = 34000, 65536                   # 2.2e9 elements
+    big = torch.zeros((T, V), dtype=BF16, device="cuda")
+    few, y5 = logits_of(65, 5, V, BF16)
+    big[-5:] = few
+    y = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    y[-5:] = y5
+    logp, lse = nsp.token_logp(big, y, scale=SCALE)
+    assert (logp[:-5] == 0).all()
+    check_logp(few, y5, logp[-5:], lse[-5:])
+    g = randn(66, T, dt=F32)
+    nsp.token_logp_bwd(big, y, lse, g, scale=SCALE, out=big)
+    check_dlogits(few, y5, g[-5:], big[-5:], BF16)
+    assert not big[:-5].any()
+
+
+# ----------------------------------------------------------------------------- losses
+
+# (an empty document, ones without a scored row, a row behind the last one)
+DOCS = [5, 0, 1, 40, 33, 1, 300, 2, 0, 64]
+
+
+def step_inputs(seed, lens, behind=3, T=None):
+    """Targets, log-probabilities and what a policy loss reads, off the clip's borders."""
+    T = sum(lens) + behind if T is None else T
+    rng = np.random.default_rng(seed)
+    y = rng.integers(0, 50, T)
+    y[rng.random(T) < 0.3] = -1
+    logp = -rng.uniform(0.01, 6, T)
+    d = rng.normal(size=T) * 0.3          # log of the ratio
+    for border in (np.log(0.8), np.log(1.25)):
+        d = np.where(np.abs(d - border) < 1e-3, border + 2e-3, d)
+    cuda = lambda a: torch.tensor(a, dtype=torch.float32, device="cuda")  # noqa: E731
+    return (torch.tensor(y, dtype=torch.int32, device="cuda"), cuda(logp), cuda(logp - d),
+            cuda(logp + rng.normal(size=T) * 0.5), rng)
+
+
+def check_policy(logp, y, old, ref, adv, cu, stats, dlogp, kw, logp_err=0.0):
+    """logp_err: of each log-probability."""
+    l, o, a = f64(logp), f64(old), f64(adv)
+    r = None if ref is None else f64(ref)
+    y, cu = y.cpu().numpy(), cu.cpu().numpy()
+    args = dict(clip_low=float(np.float32(kw["clip_low"])), clip_high=float(np.float32(kw["clip_high"])),
+                kl_coef=float(np.float32(kw["kl_coef"])), mean=kw["mean"], total=kw.get("total", 0.0))
+    rs, rg = S.policy_loss(l, o, r, a, y, cu, **args)
+    # one row's terms without their weights: sums of magnitudes times their roundings (the
+    # log ratio's own and its exp: (|d| + 8) E; the weight 3 E)
+    d = np.where(y >= 0, l - o, 0)
+    T = len(l)
+    weight = np.zeros(T)
+    rows_adv = np.zeros(T)
+    live = [[t for t in range(min(cu[b], T), min(cu[b + 1], T)) if y[t] >= 0] for b in range(len(cu) - 1)]
+    nt, nd = sum(map(len, live)), sum(len(x) > 0 for x in live)
+    for b, rows in enumerate(live):
+        for t in rows:
+            n = args["total"] or (nt if args["mean"] == "tokens" else nd)
+            weight[t] = 1 / n if args["mean"] == "tokens" else 1 / (n * len(rows))
+            rows_adv[t] = a[t] if len(a) == T and len(a) != len(live) else a[b]
+    g = np.abs(rows_adv) * np.exp(d)
+    e_rel = (np.abs(d) + 12) * E + logp_err
+    tol = weight * g * e_rel
+    kl_tol = 0.0
+    if r is not None:
+        z = np.where(y >= 0, r - l, 0)
+        big = np.exp(z) + 1 + np.abs(z)
+        kl_tol = weight * big * ((np.abs(z) + 12) * E + logp_err)
+        tol = tol + args["kl_coef"] * kl_tol
+    assert_within(dlogp, rg, tol + 2 * E * np.abs(rg), "dlogp")
+    pg_tol = (weight * g * e_rel).sum()
+    k = np.sum(kl_tol)
+    assert_within(stats, rs, np.array([pg_tol + args["kl_coef"] * k, pg_tol, k, 6 * E * rs[3]]) + 2 * E * np.abs(rs),
+                  "stats")
+
+
+@pytest.mark.parametrize("mean", ["tokens", "documents"])
+@pytest.mark.parametrize("per_token", [False, True])
+@pytest.mark.parametrize("kl", [0.0, 0.07])
+@pytest.mark.parametrize("lens", [DOCS, [1], [2000], [3] * 700, [0, 0, 40000, 0, 17]])
+def test_policy_loss(nsp, mean, per_token, kl, lens):
+    y, logp, old, ref, rng = step_inputs(70, lens)
+    cu = cu_of(lens)
+    T = len(y)
+    adv = torch.tensor(rng.normal(size=T if per_token else len(lens)), dtype=torch.float32, device="cuda")
+    kw = dict(clip_low=0.2, clip_high=0.25, kl_coef=kl, mean=mean)
+    # rows without a score may hold anything
+    out = (y < 0) | (torch.arange(T, device="cuda") >= int(cu[-1]))
+    for t in (logp, old, ref) + ((adv,) if per_token else ()):
+        t[out] = float("nan")
+    r = ref if kl else None
+    stats, dlogp = nsp.policy_loss(logp, y, old, adv, cu, ref=r, **kw)
+    clean = [t.clone() for t in (logp, old, ref, adv)]
+    for t in clean[:3] + ([clean[3]] if per_token else []):
+        t[out] = 0.0
+    c_logp, c_old, c_ref, c_adv = clean
+    check_policy(c_logp, y, c_old, c_ref if kl else None, c_adv, cu, stats, dlogp, kw)
+    assert (dlogp[out] == 0).all()
+    again, d2 = nsp.policy_loss(logp, y, old, adv, cu, ref=r, **kw)
+    assert torch.equal(again, stats) and torch.equal(d2, dlogp)
+
+
+@pytest.mark.parametrize("mean", ["tokens", "documents"])
+def test_policy_loss_total_and_parts(nsp, mean):
+    """Two calls over halves of the documents with the whole's number are the whole."""
+    y, logp, old, ref, rng = step_inputs(71, DOCS, behind=0)
+    cu = cu_of(DOCS)
+    adv = torch.tensor(rng.normal(size=len(DOCS)), dtype=torch.float32, device="cuda")
+    kw = dict(clip_low=0.2, clip_high=0.25, kl_coef=0.1, mean=mean)
+    stats, dlogp = nsp.policy_loss(logp, y, old, adv, cu, ref=ref, **kw)
+    at = int(cu[5])
+    yh = y.cpu().numpy()
+    cuh = cu.cpu().numpy()
+    total = float((yh >= 0).sum() if mean == "tokens" else sum((yh[a:b] >= 0).any() for a, b in zip(cuh, cuh[1:])))
+    parts = [nsp.policy_loss(logp[s], y[s], old[s], adv[d], c, ref=ref[s], total=total, **kw)
+             for s, d, c in ((slice(0, at), slice(0, 5), cu[:6]), (slice(at, None), slice(5, None), cu[5:] - cu[5]))]
+    assert torch.equal(torch.cat([p[1] for p in parts]), dlogp)
+    torch.testing.assert_close(parts[0][0] + parts[1][0], stats, rtol=0, atol=8 * E * float(stats.abs().max()) + 1e-7)
+
+
+def test_policy_loss_nothing_scored(nsp):
+    cu = cu_of([4, 0, 3])
+    y = torch.full((7,), -1, dtype=torch.int32, device="cuda")
+    nan = torch.full((7,), float("nan"), device="cuda")
+    x = torch.full((7, 33), float("nan"), device="cuda")
+    for mean in ("tokens", "documents"):
+        stats, dlogp = nsp.policy_loss(nan, y, nan, nan[:3], cu, ref=nan, kl_coef=0.1, mean=mean)
+        assert (stats == 0).all() and (dlogp == 0).all()
+        stats, logp, dx = nsp.policy_loss_logits(x, y, nan, nan[:3], cu, ref=nan, kl_coef=0.1, mean=mean)
+        assert (stats == 0).all() and (logp == 0).all() and (dx == 0).all()
+    e = x[:0]
+    stats, logp, dx = nsp.policy_loss_logits(e, y[:0], nan[:0], nan[:3], cu)
+    assert (stats == 0).all() and logp.shape == (0,) and dx.shape == (0, 33)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("V,lens,kl,mean", [(50, DOCS, 0.07, "documents"), (1003, [5, 0, 7, 1], 0.0, "tokens"),
+                                            (32768, [3, 9], 0.07, "tokens"), (131072, [4], 0.07, "documents"),
+                                            (70001, [2, 5], 0.07, "documents"), (300000, [3], 0.07, "tokens"),
+                                            (8, [1000, 1000], 0.1, "tokens")])
+def test_policy_loss_logits(nsp, dt, V, lens, kl, mean):
+    """Against the oracle, and the three calls that it does in one."""
+    y, _, _, _, rng = step_inputs(72, lens)
+    T, cu = len(y), cu_of(lens)
+    x, _ = logits_of(73, T, V, dt)
+    y = torch.where(y >= 0, torch.tensor(rng.integers(0, V, T), dtype=torch.int32, device="cuda"), y)
+    logp64, _ = S.token_logp(f64(x), y.cpu().numpy(), SCALE)
+    d = rng.normal(size=T) * 0.3
+    for border in (np.log(0.8), np.log(1.25)):
+        d = np.where(np.abs(d - border) < 1e-3, border + 2e-3, d)
+    old, ref = (torch.tensor(logp64 + o, dtype=torch.float32, device="cuda") for o in (-d, rng.normal(size=T) * 0.5))
+    adv = torch.tensor(rng.normal(size=len(lens)), dtype=torch.float32, device="cuda")
+    kw = dict(clip_low=0.2, clip_high=0.25, kl_coef=kl, mean=mean)
+    r = ref if kl else None
+    behind = torch.arange(T, device="cuda") >= int(cu[-1])
+    x[y < 0], x[behind] = float("nan"), float("nan")
+    stats, logp, dx = nsp.policy_loss_logits(x, y, old, adv, cu, ref=r, scale=SCALE, **kw)
+    scored = torch.where(behind, torch.full_like(y, -1), y)
+    x0 = torch.nan_to_num(x, nan=0.0)
+    check_logp(x0, scored, logp, None)
+    err = lse_error(f64(x0)) + 2 * E * np.abs(logp64)
+    lw = torch.tensor(np.where(scored.cpu().numpy() >= 0, logp64, 0), device="cuda")
+    dl_ref = S.policy_loss(f64(lw), f64(old), None if r is None else f64(r), f64(adv), scored.cpu().numpy(),
+                           cu.cpu().numpy(), float(np.float32(0.2)), 0.25, float(np.float32(kl)), mean)[1]
+    two, dl = nsp.policy_loss(logp, y, old, adv, cu, ref=r, **kw)
+    check_policy(lw, scored, old, r, adv, cu, stats, dl, kw, logp_err=err)
+    dl_err = np.abs(f64(dl) - dl_ref) + 4 * E * np.abs(dl_ref)
+    check_dlogits(x0, scored, dl_ref, dx, dt, dlogp_err=SCALE * dl_err)
+    torch.testing.assert_close(stats, two, rtol=8 * E, atol=8 * E * float(two.abs().max()))
+    # in place, into padded rows, and twice: the same bits
+    wide = torch.full((T, V + 16 // x.element_size()), 7.0, dtype=dt, device="cuda")
+    wide[:, :V] = x
+    s2, l2, d2 = nsp.policy_loss_logits(wide[:, :V], y, old, adv, cu, ref=r, scale=SCALE, out=wide[:, :V], **kw)
+    assert torch.equal(s2, stats) and torch.equal(l2, logp) and torch.equal(d2, dx) and (wide[:, V:] == 7).all()
+    s3, _, d3 = nsp.policy_loss_logits(x, y, old, adv, cu, ref=r, scale=SCALE, **kw)
+    assert torch.equal(s3, stats) and torch.equal(d3, dx)
+
+
+@pytest.mark.parametrize("bad", [[1, 3, 6], [0, 5, 3], [0, -1, 6], [0, 3, 2]])
+def test_losses_bad_documents(nsp, bad):
+    """The status word says so, and the next call is a clean one."""
+    T = 6
+    cu, good = torch.tensor(bad, dtype=torch.int32, device="cuda"), cu_of([3, 3])
+    y = torch.tensor([0, 1, -1, 2, 0, 1], dtype=torch.int32, device="cuda")
+    v, x = randn(80, T, dt=F32), randn(81, T, 9, dt=F32)
+    ws = torch.empty(8192, dtype=torch.uint8, device="cuda")
+    for call in (lambda c: nsp.policy_loss(v, y, v, v[:2], c, workspace=ws),
+                 lambda c: nsp.policy_loss_logits(x, y, v, v[:2], c, workspace=ws),
+                 lambda c: nsp.preference_loss(v, y, c, workspace=ws)):
+        call(cu)
+        assert nsp.nsp_status_query(ws) == nsp.NSP_ERR_INVALID
+        first = call(good)
+        assert nsp.nsp_status_query(ws) == nsp.NSP_OK
+        for a, b in zip(first, call(good)):
+            assert torch.equal(a, b)
+    # a cu_seqlens that reaches past the rows is cut there
+    long = cu_of([3, 300])
+    for a, b in zip(nsp.policy_loss(v, y, v, v[:2], long, workspace=ws), nsp.policy_loss(v, y, v, v[:2], good)):
+        assert torch.equal(a, b)
+    for a, b in zip(nsp.preference_loss(v, y, long, workspace=ws), nsp.preference_loss(v, y, good)):
+        assert torch.equal(a, b)
+    assert nsp.nsp_status_query(ws) == nsp.NSP_OK
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "square"])
+@pytest.mark.parametrize("average", [False, True])
+@pytest.mark.parametrize("lens", [DOCS, [1, 1], [0, 0], [3000, 4097], [3] * 900, [0, 70000, 3, 1], [20000, 1, 1, 20000]])
+def test_preference_loss(nsp, kind, average, lens):
+    y, logp, _, ref, _ = step_inputs(74, lens, behind=5)
+    cu, T = cu_of(lens), len(y)
+    out = (y < 0) | (torch.arange(T, device="cuda") >= int(cu[-1]))
+    logp[out], ref[out] = float("nan"), float("nan")
+    kw = dict(kind=kind, beta=0.125, smoothing=0.0625, margin=0.25, average=average)     # (exact in float32)
+    for r in (ref, None):
+        stats, rewards, dlogp = nsp.preference_loss(logp, y, cu, ref=r, **kw)
+        l0 = torch.where(out, 0.0, logp)
+        r0 = None if r is None else f64(torch.where(out, 0.0, r))
+        scored = torch.where(out, torch.full_like(y, -1), y).cpu().numpy()
+        rs, rr, rg = S.preference_loss(f64(l0), r0, scored, cu.cpu().numpy(), **kw)
+        # scores are exact to 2^-40 of their terms' magnitudes, the rest is float64
+        mag = np.abs(f64(l0)).sum() * 2.0 ** -38
+        assert_within(rewards, rr, 2 * E * np.abs(rr) + mag, "rewards")
+        # the loss's slope in h is at most 1, or (square) 2 |off| / beta^2
+        slope = 1.0 if kind != "square" else 2 * (np.abs(rr).max() * 2 + 5) / 0.125 ** 2
+        assert_within(stats[:1], rs[:1], 4 * E * np.abs(rs[:1]) + slope * mag, "loss")
+        assert stats[1] == np.float32(rs[1])
+        assert_within(dlogp, rg, 3 * E * np.abs(rg) + slope * mag, "dlogp")
+        assert (dlogp[out] == 0).all()
+        for a, b in zip(nsp.preference_loss(logp, y, cu, ref=r, **kw), (stats, rewards, dlogp)):
+            assert torch.equal(a, b)
+
+
+def test_preference_loss_far_scores(nsp):
+    """Scores that differ by thousands: the sigmoid's tails keep their own precision."""
+    cu = cu_of([1, 1, 1, 1, 1, 1])
+    y = torch.zeros(6, dtype=torch.int32, device="cuda")
+    logp = torch.tensor([-1.0, -4001.0, -4001.0, -1.0, -1.0, -301.0], device="cuda")
+    stats, rewards, dlogp = nsp.preference_loss(logp, y, cu, beta=0.125)
+    rs, rr, rg = S.preference_loss(f64(logp), None, np.zeros(6), cu.cpu().numpy(), beta=0.125)
+    np.testing.assert_allclose(f64(rewards), rr, rtol=2e-7)
+    np.testing.assert_allclose(f64(stats), rs, rtol=2e-7)
+    np.testing.assert_allclose(f64(dlogp), rg, rtol=4e-7, atol=1e-38)
+
+
+# ----------------------------------------------------------------------------- many gradients
+
+def grads_of(seed, sizes, types, shift=0, scale=1.0):
+    out = []
+    for i, n in enumerate(sizes):
+        dt = types[i % len(types)]
+        base = torch.zeros(n + 16, dtype=dt, device="cuda")
+        t = base[shift * i % 9:][:n]
+        t.copy_(randn(seed + i, n, dt=F32, scale=scale))
+        out.append(t)
+    return out
+
+
+def check_norm(grads, norm, unscale=1.0, kind=2):
+    ref = S.grad_norm([f64(g) for g in grads], unscale, kind)
+    # a square's rounding and at most 126 float32 sums of squares, halved by the root
+    assert_within(norm, [ref], (64 if kind == 2 else 1) * E * ref, "norm")
+    return ref
+
+
+SIZES = [[1], [7, 0, 300], [32768], [32769, 5], [40000, 1, 1, 1, 65536, 3000], [1000003], [17] * 70, [5] * 900 + [40001] * 3]
+
+
+@pytest.mark.parametrize("types", [[BF16], [F32], [BF16, F32]])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("sizes", SIZES)
+def test_grad_norm_and_clip(nsp, types, shift, sizes):
+    grads = grads_of(90, sizes, types, shift)
+    norm = nsp.grad_norm(grads, unscale=-0.25)
+    ref = check_norm(grads, norm, -0.25)
+    assert torch.equal(nsp.grad_norm(grads, unscale=-0.25), norm)
+    check_norm(grads, nsp.grad_norm(grads, float("inf"), unscale=0.5), 0.5, np.inf)
+    max_norm = float(np.float32(0.3 * ref))
+    factor = -0.25 * max_norm / (ref + 1e-6)
+    for other in (False, True):
+        out = [torch.full((n + 8,), 7.0, dtype=types[(i + other) % len(types)], device="cuda") for i, n in enumerate(sizes)]
+        views = [o[1 + shift * (i % 3):][:n] for i, (o, n) in enumerate(zip(out, sizes))]
+        got = nsp.clip_grads(grads, max_norm, unscale=-0.25, out=views)
+        assert torch.equal(got, norm)
+        for i, (g, v) in enumerate(zip(grads, views)):
+            want = f64(g) * factor
+            # (float32 values below 2^-126 aside)
+            assert_within(v, want, (half_step(v.dtype) + 80 * E) * np.abs(want) + 2.0 ** -126, i)
+            v[:] = 7.0
+        assert all([(o == 7).all() for o in out])
+    keep = [g.clone() for g in grads]
+    assert torch.equal(nsp.clip_grads(grads, max_norm, unscale=-0.25), norm)
+    for g, k in zip(grads, keep):
+        want = f64(k) * factor
+        assert_within(g, want, (half_step(g.dtype) + 80 * E) * np.abs(want) + 2.0 ** -126, "in place")
+
+
+def test_clip_does_nothing_below_the_norm(nsp):
+    grads = grads_of(91, [1000, 77], [F32, BF16])
+    keep = [g.clone() for g in grads]
+    norm = nsp.clip_grads(grads, 1e6)
+    check_norm(grads, norm)
+    for g, k in zip(grads, keep):
+        assert torch.equal(g, k)
+    nsp.clip_grads(grads, 1e6, unscale=0.5)
+    for g, k in zip(grads, keep):
+        assert torch.equal(g, k * 0.5)
+    nsp.clip_grads(grads, 0.0)
+    assert all([(g == 0).all() for g in grads])
+
+
+def test_grad_norm_special_values(nsp):
+    """NaN and infinity anywhere; zeros; no elements; magnitudes near the ends."""
+    for kind in (2, float("inf")):
+        for at in (0, 999, 40000):
+            g = grads_of(92, [40001, 30], [F32])
+            g[0][at] = float("inf")
+            assert nsp.grad_norm(g, kind) == float("inf")
+            keep = g[1].clone()
+            assert nsp.clip_grads(g, 1.0, kind) == float("inf")
+            assert torch.isnan(g[0][at]) and (g[1] == 0).all() and keep.any()
+            g[1][3] = float("nan")
+            assert torch.isnan(nsp.grad_norm(g, kind))
+            nsp.clip_grads(g, 1.0, kind)
+            assert all([torch.isnan(t).all() for t in g])
+    z = [torch.zeros(500, device="cuda"), torch.zeros(0, device="cuda")]
+    assert nsp.grad_norm(z) == 0 and nsp.grad_norm(z[1:]) == 0 and nsp.clip_grads(z, 1.0) == 0
+    big = [torch.full((4,), 1e18, device="cuda"), torch.full((4,), 1e-18, device="cuda")]
+    check_norm(big[:1], nsp.grad_norm(big[:1]))
+    check_norm(big[1:], nsp.grad_norm(big[1:]))
+    check_norm(big, nsp.grad_norm(big))
+
+
+def test_grad_norm_far_elements(nsp):
+    """Offsets past 32 bits in one tensor."""
+    n = (1 << 31) + 5000
+    t = torch.zeros(n, dtype=BF16, device="cuda")
+    t[-3:] = 4.0
+    t[0] = 1.0
+    assert nsp.grad_norm([t]) == 7.0
+    nsp.clip_grads([t], 3.5)
+    assert abs(float(t[-1]) - 2.0) < 0.01 and abs(float(t[0]) - 0.5) < 0.01 and not t[1:-3].any()

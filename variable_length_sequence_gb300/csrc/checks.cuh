@@ -25,7 +25,8 @@ struct Span {
 // Whether two spans share a byte.  Spans of the same step (views of one
 // tensor's columns) are compared column by column; others by their extents.
 inline bool overlap(const Span& a, const Span& b) {
-  if (a.rows < 1 || b.rows < 1 || a.end() <= b.base || b.end() <= a.base) return false;
+  if (a.rows < 1 || b.rows < 1 || a.row < 1 || b.row < 1) return false;
+  if (a.end() <= b.base || b.end() <= a.base) return false;
   if (a.step != b.step || a.row > a.step || b.row > b.step) return true;
   const int64_t off = ((int64_t)(b.base - a.base) % a.step + a.step) % a.step;
   return off < a.row || off + b.row > a.step;

@@ -1,0 +1,261 @@
+// Losses of a packed stream over the log-probabilities of its scored rows (those
+// with a target): the clipped policy loss and the preference loss over pairs of
+// documents, each with its gradient.
+#include <algorithm>
+
+#include "policy.cuh"
+#include "sums.cuh"
+
+namespace nsp {
+namespace {
+
+constexpr int kPrepThreads = 1024;
+constexpr int kThreads = 256;
+constexpr int kPolicyBlocks = 304;
+
+// Scored rows before row x.
+__device__ __forceinline__ int scored_before(const LossArgs& a, int64_t x) {
+  x = min(x, a.rows);
+  const int64_t w = x >> 5;
+  int n = w > 0 ? a.before[w - 1] : 0;               // (before[w]: up to the end of word w)
+  if ((x & 31) != 0) n += __popc(a.bits[w] & ((1u << (x & 31)) - 1));
+  return n;
+}
+
+__global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const LossArgs a) {
+  __shared__ int s_warp[32], s_bad, s_base, s_docs;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_bad = a.cu[0] != 0, s_base = 0, s_docs = 0;
+  __syncthreads();
+  for (int i = tid; i < a.ndoc; i += kPrepThreads)
+    if (a.cu[i] > a.cu[i + 1]) s_bad = 1;
+  __syncthreads();
+  if (tid == 0) a.hdr->status = s_bad ? NSP_ERR_INVALID : NSP_OK;
+  if (s_bad) return;
+  const int64_t end = min((int64_t)a.cu[a.ndoc], a.rows);
+  const int64_t words = (a.rows + 31) >> 5;
+  for (int64_t w0 = 0; w0 < words; w0 += kPrepThreads) {
+    // a warp's 32 words, a word a turn; lane i keeps word i
+    uint32_t mine = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const int64_t t = (w0 + warp * 32 + i) * 32 + lane;
+      const uint32_t b = __ballot_sync(0xffffffffu, t < end && __ldg(a.targets + t) >= 0);
+      if (lane == i) mine = b;
+    }
+    int n = __popc(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += v;
+    }
+    if (lane == 31) s_warp[warp] = n;
+    __syncthreads();
+    int base = s_base;
+    for (int w = 0; w < warp; ++w) base += s_warp[w];
+    const int64_t w = w0 + tid;
+    if (w < words) {
+      a.bits[w] = mine;
+      a.before[w] = base + n;
+    }
+    __syncthreads();
+    if (tid == kPrepThreads - 1) s_base = base + n;
+  }
+  __syncthreads();
+  int docs = 0;
+  for (int i = tid; i < a.ndoc; i += kPrepThreads) {
+    const int n = scored_before(a, a.cu[i + 1]) - scored_before(a, a.cu[i]);
+    a.weight[i] = (float)n;
+    docs += n > 0;
+  }
+  atomicAdd(&s_docs, docs);
+  __syncthreads();
+  const float tokens = a.total > 0.f ? a.total : (float)s_base;
+  const float many = a.total > 0.f ? a.total : (float)s_docs;
+  for (int i = tid; i < a.ndoc; i += kPrepThreads) {
+    const float n = a.weight[i];
+    a.weight[i] = n == 0.f ? 0.f : a.mean == NSP_MEAN_TOKENS ? 1.f / tokens : 1.f / (many * n);
+  }
+}
+
+// stats from sums of surrogate, kl and clipped.
+__device__ __forceinline__ void write_stats(float* stats, float kl_coef, double pg, double kl, double cut) {
+  stats[0] = (float)(pg + (double)kl_coef * kl);
+  stats[1] = (float)pg;
+  stats[2] = (float)kl;
+  stats[3] = (float)cut;
+}
+
+__global__ void __launch_bounds__(kThreads) policy_kernel(const __grid_constant__ PolicyArgs a) {
+  __shared__ Sum2 s_sum[3][kThreads / 32];
+  if (status_bad(a.p.hdr)) return;
+  const int64_t end = min((int64_t)__ldg(a.p.cu + a.p.ndoc), a.rows);
+  Sum2 pg = {0.f, 0.f}, kl = pg, cut = pg;
+  for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < a.rows;
+       t += (int64_t)gridDim.x * kThreads) {
+    float g = 0.f;
+    if (t < end && __ldg(a.targets + t) >= 0) {
+      const PolicyRow r = policy_row(a.p, t, doc_of(a.p.cu, a.p.ndoc, t), __ldg(a.logp + t));
+      pg.add(r.surrogate);
+      kl.add(r.kl);
+      cut.add(r.clipped);
+      g = r.grad;
+    }
+    a.dlogp[t] = g;
+  }
+  constexpr int W = kThreads / 32;
+  pg = block_sum<W>(pg, s_sum[0]);
+  kl = block_sum<W>(kl, s_sum[1]);
+  cut = block_sum<W>(cut, s_sum[2]);
+  if (threadIdx.x == 0) {
+    float* const o = a.p.terms + blockIdx.x;
+    o[0] = (float)pg.value();
+    o[gridDim.x] = (float)kl.value();
+    o[2 * gridDim.x] = (float)cut.value();
+  }
+}
+
+// stats from n terms of each of the three.
+__global__ void __launch_bounds__(kPrepThreads) policy_stats_kernel(const float* __restrict__ terms,
+                                                                    int64_t n, float kl_coef,
+                                                                    const WsHeader* hdr, float* stats) {
+  __shared__ Sum2 s_sum[3][kPrepThreads / 32];
+  if (status_bad(hdr)) return;
+  Sum2 sum[3] = {};
+  for (int i = 0; i < 3; ++i) {
+    for (int64_t t = threadIdx.x; t < n; t += kPrepThreads) sum[i].add(terms[i * n + t]);
+    sum[i] = block_sum<kPrepThreads / 32>(sum[i], s_sum[i]);
+  }
+  if (threadIdx.x == 0) write_stats(stats, kl_coef, sum[0].value(), sum[1].value(), sum[2].value());
+}
+
+// One pair of documents a block: both sums, the pair's loss, and its gradient over the
+// documents' rows; the blocks together clear the rows behind the last document.
+__global__ void __launch_bounds__(kThreads) preference_kernel(const __grid_constant__ PreferenceArgs a) {
+  __shared__ Sum2 s_sum[2][kThreads / 32];
+  __shared__ int s_count[2][kThreads / 32];
+  const int pairs = a.ndoc / 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = blockIdx.x; i < pairs; i += gridDim.x) {
+    const int64_t at[3] = {__ldg(a.cu + 2 * i), __ldg(a.cu + 2 * i + 1), __ldg(a.cu + 2 * i + 2)};
+    const bool bad = at[0] > at[1] || at[1] > at[2] || at[0] < 0 || (i == 0 && at[0] != 0);
+    if (threadIdx.x == 0) a.terms[2 * (int64_t)pairs + i] = bad ? 1.f : 0.f;
+    if (bad) continue;
+    double score[2];
+    int count[2];
+    __syncthreads();                   // (the last pair's sums have been read)
+    for (int k = 0; k < 2; ++k) {
+      const int64_t hi = min(at[k + 1], a.rows);
+      Sum2 x = {0.f, 0.f};
+      int n = 0;
+      for (int64_t t = at[k] + threadIdx.x; t < hi; t += kThreads)
+        if (__ldg(a.targets + t) >= 0) {
+          x.add(__ldg(a.logp + t));
+          if (a.ref_logp) x.add(-__ldg(a.ref_logp + t));
+          ++n;
+        }
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) s_count[k][warp] = n;
+      score[k] = block_sum<kThreads / 32>(x, s_sum[k]).value();
+      count[k] = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? s_count[k][lane] : 0);
+      if (a.average) score[k] /= max(1, count[k]);
+    }
+    const double beta = a.beta, h = beta * (score[0] - score[1]) - a.margin;
+    double loss, dh;
+    if (a.kind == NSP_PREFERENCE_SIGMOID) {
+      const double e = exp(-fabs(h)), low = log1p(e);          // log(1 + exp(-|h|))
+      const double down = low + fmax(-h, 0.0), up = low + fmax(h, 0.0);   // -log sigmoid(+-h)
+      loss = (1.0 - a.smoothing) * down + a.smoothing * up;
+      dh = a.smoothing - (h > 0 ? e : 1.0) / (1.0 + e);        // smoothing - sigmoid(-h)
+    } else if (a.kind == NSP_PREFERENCE_HINGE) {
+      loss = h < 1.0 ? 1.0 - h : (h >= 1.0 ? 0.0 : h);         // (NaN stays)
+      dh = h < 1.0 ? -1.0 : (h >= 1.0 ? 0.0 : h);
+    } else {
+      const double off = h / beta - 0.5 / beta;
+      loss = off * off;
+      dh = 2.0 * off / beta;
+    }
+    if (threadIdx.x == 0) {
+      a.terms[i] = (float)loss;
+      a.terms[pairs + i] = score[0] > score[1] ? 1.f : 0.f;
+      a.rewards[2 * (int64_t)i] = (float)(beta * score[0]);
+      a.rewards[2 * (int64_t)i + 1] = (float)(beta * score[1]);
+    }
+    for (int k = 0; k < 2; ++k) {
+      const int64_t hi = min(at[k + 1], a.rows);
+      const float g = (float)((k ? -dh : dh) * beta / pairs / (a.average ? max(1, count[k]) : 1));
+      for (int64_t t = at[k] + threadIdx.x; t < hi; t += kThreads)
+        a.dlogp[t] = __ldg(a.targets + t) >= 0 ? g : 0.f;
+    }
+  }
+  for (int64_t t = max((int64_t)0, (int64_t)__ldg(a.cu + a.ndoc)) + (int64_t)blockIdx.x * kThreads + threadIdx.x;
+       t < a.rows; t += (int64_t)gridDim.x * kThreads)
+    a.dlogp[t] = 0.f;
+}
+
+__global__ void __launch_bounds__(kPrepThreads) preference_stats_kernel(const float* __restrict__ terms,
+                                                                        int pairs, WsHeader* hdr,
+                                                                        float* stats) {
+  __shared__ Sum2 s_sum[3][kPrepThreads / 32];
+  grid_dep_wait();
+  Sum2 sum[3] = {};
+  for (int i = 0; i < 3; ++i) {
+    for (int t = threadIdx.x; t < pairs; t += kPrepThreads) sum[i].add(__ldcg(terms + (int64_t)i * pairs + t));
+    sum[i] = block_sum<kPrepThreads / 32>(sum[i], s_sum[i]);
+  }
+  if (threadIdx.x != 0) return;
+  hdr->status = sum[2].hi != 0.f ? NSP_ERR_INVALID : NSP_OK;
+  stats[0] = (float)(sum[0].value() / pairs);
+  stats[1] = (float)(sum[1].value() / pairs);
+}
+
+}  // namespace
+
+LossWsLayout loss_ws_layout(int64_t rows, int32_t ndoc, bool logits) {
+  LossWsLayout L;
+  const size_t words = (size_t)ceil_div(rows, 32);
+  L.before = sizeof(WsHeader);
+  L.bits = align_up(L.before + 4 * words, 256);
+  L.weight = align_up(L.bits + 4 * words, 256);
+  L.terms = align_up(L.weight + 4 * (size_t)ndoc, 256);
+  L.total = align_up(L.terms + 12 * (logits ? (size_t)rows : (size_t)kPolicyBlocks), 256);
+  return L;
+}
+
+cudaError_t launch_loss_prep(const LossArgs& a, cudaStream_t s) {
+  loss_prep_kernel<<<1, kPrepThreads, 0, s>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+static int policy_blocks(int64_t rows) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kPolicyBlocks, ceil_div(rows, kThreads)));
+}
+
+cudaError_t launch_policy(const PolicyArgs& a, cudaStream_t s) {
+  const int blocks = policy_blocks(a.rows);
+  policy_kernel<<<blocks, kThreads, 0, s>>>(a);
+  policy_stats_kernel<<<1, kPrepThreads, 0, s>>>(a.p.terms, blocks, a.p.kl_coef, a.p.hdr, a.stats);
+  count_launches(2);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_policy_stats(const RowArgs& a, float* stats, cudaStream_t s) {
+  policy_stats_kernel<<<1, kPrepThreads, 0, s>>>(a.p.terms, a.rows, a.p.kl_coef, a.p.hdr, stats);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_preference(const PreferenceArgs& a, cudaStream_t s) {
+  const int pairs = a.ndoc / 2;
+  const int blocks = (int)std::min<int64_t>(pairs, (int64_t)num_sms() * 8);
+  preference_kernel<<<blocks, kThreads, 0, s>>>(a);
+  count_launches(1);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(preference_stats_kernel, dim3(1), dim3(kPrepThreads), 0, s,
+                       (const float*)a.terms, pairs, a.hdr, a.stats);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace nsp

@@ -35,4 +35,100 @@ int qk_bwd_blocks(int64_t rows);
 cudaError_t launch_qk_norm_rope(const QkArgs& a, int32_t io_dtype, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, int32_t io_dtype, cudaStream_t s);
 
+// ---- log-probabilities of given tokens (token_logp.cu)
+constexpr int32_t kMaxVocab = 1 << 20;
+
+// A policy loss on top of the rows: what each row's weight and loss are made of.
+struct PolicyRows {
+  const float *old_logp, *ref_logp, *advantages;
+  int32_t per_token;                       // advantages of each row, or of each document
+  float clip_low, clip_high, kl_coef;
+  const int32_t* cu;
+  int32_t ndoc;
+  const WsHeader* hdr;
+  const float* doc_weight;                 // [ndoc] weight of a row of the document
+  float* terms;                            // [3][rows]: weighted surrogate, kl, clipped
+};
+
+struct RowArgs {
+  const void* logits;
+  int64_t row_stride;                      // elements
+  const int32_t* targets;
+  int64_t rows;
+  int32_t vocab;
+  float scale;
+  float *logp, *lse;                       // forward and policy: written (may be null)
+  const float *in_lse, *dlogp;             // backward
+  void* dlogits;
+  int64_t out_stride;
+  PolicyRows p;
+};
+enum RowMode { kRowForward, kRowBackward, kRowPolicy };
+cudaError_t launch_rows(const RowArgs& a, RowMode mode, int32_t io_dtype, cudaStream_t s);
+
+// ---- losses (loss.cu)
+// Workspace of a loss: header; per 32 rows the number of scored ones before them and
+// which of them are; each document's weight; terms or partial sums.
+struct LossWsLayout {
+  size_t before, bits, weight, terms, total;
+};
+LossWsLayout loss_ws_layout(int64_t rows, int32_t ndoc, bool logits);
+
+struct LossArgs {
+  const int32_t* targets;
+  const int32_t* cu;
+  int32_t ndoc;
+  int64_t rows;
+  int32_t mean;
+  float total;
+  WsHeader* hdr;
+  uint32_t* bits;
+  int32_t* before;
+  float* weight;
+};
+// Checks cu_seqlens (status word), counts each document's scored rows and writes
+// the documents' weights.
+cudaError_t launch_loss_prep(const LossArgs& a, cudaStream_t s);
+
+struct PolicyArgs {
+  const float* logp;
+  const int32_t* targets;
+  int64_t rows;
+  PolicyRows p;                            // (p.terms: partial sums of the blocks)
+  float *stats, *dlogp;
+};
+cudaError_t launch_policy(const PolicyArgs& a, cudaStream_t s);
+// stats from the rows' terms of a kRowPolicy pass
+cudaError_t launch_policy_stats(const RowArgs& a, float* stats, cudaStream_t s);
+
+struct PreferenceArgs {
+  const float *logp, *ref_logp;
+  const int32_t *targets, *cu;
+  int32_t ndoc;
+  int64_t rows;
+  int32_t kind;
+  float beta, smoothing, margin;
+  int32_t average;
+  WsHeader* hdr;
+  float* terms;                            // [3][pairs]: loss, ahead, bad cu_seqlens
+  float *stats, *rewards, *dlogp;
+};
+cudaError_t launch_preference(const PreferenceArgs& a, cudaStream_t s);
+
+// ---- norm and clipping of many gradients (grad_norm.cu)
+constexpr int32_t kMaxGrads = 16384;
+struct GradArgs {
+  int32_t n;
+  const void* const* in;                   // HOST arrays
+  void* const* out;                        // null: the norm alone
+  const int64_t* counts;
+  const int32_t *in_dtypes, *out_dtypes;
+  int32_t kind;
+  float unscale, max_norm, eps;
+  float* norm;
+  char* workspace;
+};
+size_t grad_ws_size(const int64_t* counts, int32_t n);
+cudaError_t launch_grads(const GradArgs& a, cudaStream_t s);
+
 }  // namespace nsp

@@ -92,6 +92,18 @@ _SIGNATURES = {
     "nsp_qk_norm_rope_bwd_workspace_size": (_sz, [_vp, _i32, _i64, _i32]),
     "nsp_qk_norm_rope_bwd": (_i32, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _vp, _i32,
                                     _f32, _f32, _i32, _vp, _sz, _vp]),
+    "nsp_token_logp_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _f32, _i32, _vp, _vp, _vp]),
+    "nsp_token_logp_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _f32, _i32, _vp, _i64, _vp]),
+    "nsp_policy_loss_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "nsp_policy_loss": (_i32, [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nsp_policy_loss_logits": (_i32, [_vp, _i64, _vp, _vp, _i32, _i64, _i32, _f32, _i32, _vp, _vp, _vp,
+                                      _vp, _i64, _vp, _sz, _vp]),
+    "nsp_preference_loss_workspace_size": (_sz, [_i32]),
+    "nsp_preference_loss": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _f32, _f32, _f32, _i32, _vp,
+                                   _vp, _vp, _vp, _sz, _vp]),
+    "nsp_grad_norm_workspace_size": (_sz, [_vp, _i32]),
+    "nsp_grad_norm": (_i32, [_vp, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _sz, _vp]),
+    "nsp_grad_clip": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _f32, _f32, _f32, _vp, _vp, _sz, _vp]),
     "nsp_status_query": (_i32, [_vp, _vp]),
     "nsp_attn_bwd_ds_cache_size": (_sz, [_vp, _i32, _i32, _i32]),
     "nsp_attn_bwd_blocks_ds_cache_size": (_sz, [_vp, _i32, _i32, _vp, _i32, _i32]),
@@ -126,6 +138,13 @@ class QkTensor(C.Structure):
                 ("dx", C.c_void_p), ("dweight", C.c_void_p), ("x_stride", C.c_int64),
                 ("y_stride", C.c_int64), ("dx_stride", C.c_int64), ("heads", C.c_int32),
                 ("groups", C.c_int32)]
+
+
+class Policy(C.Structure):
+    """nsp_policy_t: what a clipped policy loss goes by."""
+    _fields_ = [("old_logp", C.c_void_p), ("ref_logp", C.c_void_p), ("advantages", C.c_void_p),
+                ("per_token", C.c_int32), ("mean", C.c_int32), ("clip_low", C.c_float),
+                ("clip_high", C.c_float), ("kl_coef", C.c_float), ("total", C.c_float)]
 
 
 class AttnCost(C.Structure):
@@ -1101,3 +1120,236 @@ def qk_norm_rope_bwd(q, k, dqr, dkr, cu_seqlens, freqs, wq=None, wk=None, layout
                                   _stream_of(stream, dev))
     _check("nsp_qk_norm_rope_bwd", st)
     return dq, dk, dwq, dwk
+
+
+def _logit_rows(fn, name, x, shape=None):
+    """Row stride of logits [T, V] whose rows are packed."""
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: {name} is [T, vocabulary]")
+    if shape is not None:
+        _shape(fn, name, x, shape)
+    if x.is_contiguous():
+        return x.shape[1]
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{fn}: the rows of {name} are not packed")
+    if x.shape[0] <= 1:
+        return x.shape[1]
+    if x.stride(0) < x.shape[1]:
+        raise ValueError(f"{fn}: the rows of {name} overlap")
+    return x.stride(0)
+
+
+def token_logp(logits, targets, scale=1.0, stream=None):
+    """Log-probabilities of targets (int32 [T]; negative: none, the row is not read
+    and gives zeros) under the rows of scale * logits [T, vocabulary] (rows any
+    stride apart), and the rows' log sums of exponentials: (logp, lse), float32 [T]."""
+    fn = "token_logp"
+    io = _io(fn, logits.dtype)
+    dev = _on_device(fn, logits.dtype, logits=logits)
+    _on_device(fn, torch.int32, targets=targets)
+    stride = _logit_rows(fn, "logits", logits)
+    T, V = logits.shape
+    _shape(fn, "targets", targets, (T,))
+    logp, lse = _new(stream, logits, (T,), torch.float32), _new(stream, logits, (T,), torch.float32)
+    st = load().nsp_token_logp_fwd(logits.data_ptr(), stride, _ptr(targets), T, V, scale, io,
+                                   _ptr(logp), _ptr(lse), _stream_of(stream, dev))
+    _check("nsp_token_logp_fwd", st)
+    return logp, lse
+
+
+def token_logp_bwd(logits, targets, lse, dlogp, scale=1.0, out=None, stream=None):
+    """Gradient of the logits from that of token_logp's logp (dlogp float32 [T]; not
+    used where there is no target: such rows get zeros).  out: where to write it,
+    logits themselves allowed; default a new packed tensor."""
+    fn = "token_logp_bwd"
+    io = _io(fn, logits.dtype)
+    dev = _on_device(fn, logits.dtype, logits=logits, out=out)
+    _on_device(fn, torch.int32, targets=targets)
+    _on_device(fn, torch.float32, lse=lse, dlogp=dlogp)
+    stride = _logit_rows(fn, "logits", logits)
+    T, V = logits.shape
+    for name, t in (("targets", targets), ("lse", lse), ("dlogp", dlogp)):
+        _shape(fn, name, t, (T,))
+    if out is None:
+        out = _new(stream, logits, (T, V))
+    out_stride = _logit_rows(fn, "out", out, (T, V))
+    st = load().nsp_token_logp_bwd(logits.data_ptr(), stride, _ptr(targets), _ptr(lse), _ptr(dlogp), T, V,
+                                   scale, io, out.data_ptr(), out_stride, _stream_of(stream, dev))
+    _check("nsp_token_logp_bwd", st)
+    return out
+
+
+MEANS = {"tokens": 0, "documents": 1}
+PREFERENCES = {"sigmoid": 0, "hinge": 1, "square": 2}
+
+
+def _policy(fn, T, targets, old_logp, advantages, cu_seqlens, ref, clip_low, clip_high, kl_coef, mean,
+            total, per_token):
+    """nsp_policy_t of a call, and its number of documents."""
+    _on_device(fn, torch.int32, targets=targets, cu_seqlens=cu_seqlens)
+    _on_device(fn, torch.float32, old_logp=old_logp, advantages=advantages, ref=ref)
+    if mean not in MEANS:
+        raise ValueError(f"{fn}: unknown mean {mean!r}")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError(f"{fn}: cu_seqlens is [documents + 1]")
+    docs = cu_seqlens.numel() - 1
+    _shape(fn, "targets", targets, (T,))
+    _shape(fn, "old_logp", old_logp, (T,))
+    _shape(fn, "ref", ref, (T,))
+    if per_token is None:
+        per_token = advantages.numel() != docs
+    _shape(fn, "advantages", advantages, (T if per_token else docs,))
+    if ref is None:
+        kl_coef = 0.0
+    return Policy(_ptr(old_logp), _ptr(ref), _ptr(advantages), bool(per_token), MEANS[mean], clip_low,
+                  clip_high, kl_coef, total), docs
+
+
+def policy_loss(logp, targets, old_logp, advantages, cu_seqlens, ref=None, clip_low=0.2, clip_high=0.2,
+                kl_coef=0.0, mean="tokens", total=0.0, per_token=None, workspace=None, stream=None):
+    """Clipped policy loss of a packed stream and its gradient: (stats, dlogp).
+
+    logp, old_logp, ref (None: no KL term): float32 [T]; targets int32 [T], negative
+    where a row is not scored; advantages float32 [documents] or [T] (told apart by
+    their number, documents where both are the same; per_token says which).  mean:
+    "tokens" or "documents"; total: the number of scored tokens or of documents
+    with one, where the mean is over more than this call.  stats float32 [4]: loss,
+    and the means of the surrogate, the KL term and the clipped share; dlogp float32
+    [T], zero for rows not scored (see nsp_policy_loss)."""
+    fn = "policy_loss"
+    dev = _on_device(fn, torch.float32, logp=logp)
+    if logp.dim() != 1:
+        raise ValueError(f"{fn}: logp is [T]")
+    T = logp.shape[0]
+    p, docs = _policy(fn, T, targets, old_logp, advantages, cu_seqlens, ref, clip_low, clip_high, kl_coef,
+                      mean, total, per_token)
+    lib = load()
+    stats, dlogp = _new(stream, logp, (4,)), _new(stream, logp, (T,))
+    ws = _workspace(fn, stream, logp, lib.nsp_policy_loss_workspace_size(T, docs, 0), workspace)
+    st = lib.nsp_policy_loss(_ptr(logp), _ptr(targets), _ptr(cu_seqlens), docs, T, C.addressof(p),
+                             _ptr(stats), _ptr(dlogp), _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    _check("nsp_policy_loss", st)
+    return stats, dlogp
+
+
+def policy_loss_logits(logits, targets, old_logp, advantages, cu_seqlens, ref=None, clip_low=0.2,
+                       clip_high=0.2, kl_coef=0.0, mean="tokens", scale=1.0, total=0.0, per_token=None,
+                       out=None, workspace=None, stream=None):
+    """token_logp, policy_loss and token_logp_bwd in one pass over logits [T,
+    vocabulary]: (stats, logp, dlogits), logp zero for rows not scored.  out: where
+    dlogits go, logits themselves allowed; the other arguments are policy_loss's."""
+    fn = "policy_loss_logits"
+    io = _io(fn, logits.dtype)
+    dev = _on_device(fn, logits.dtype, logits=logits, out=out)
+    stride = _logit_rows(fn, "logits", logits)
+    T, V = logits.shape
+    p, docs = _policy(fn, T, targets, old_logp, advantages, cu_seqlens, ref, clip_low, clip_high, kl_coef,
+                      mean, total, per_token)
+    if out is None:
+        out = _new(stream, logits, (T, V))
+    out_stride = _logit_rows(fn, "out", out, (T, V))
+    lib = load()
+    stats, logp = _new(stream, logits, (4,), torch.float32), _new(stream, logits, (T,), torch.float32)
+    ws = _workspace(fn, stream, logits, lib.nsp_policy_loss_workspace_size(T, docs, 1), workspace)
+    st = lib.nsp_policy_loss_logits(logits.data_ptr(), stride, _ptr(targets), _ptr(cu_seqlens), docs, T, V,
+                                    scale, io, C.addressof(p), _ptr(stats), _ptr(logp), out.data_ptr(),
+                                    out_stride, _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    _check("nsp_policy_loss_logits", st)
+    return stats, logp, out
+
+
+def preference_loss(logp, targets, cu_seqlens, ref=None, kind="sigmoid", beta=0.1, smoothing=0.0,
+                    margin=0.0, average=False, workspace=None, stream=None):
+    """Preference loss over pairs of documents (2 i chosen, 2 i + 1 rejected) and its
+    gradient: (stats, rewards, dlogp).
+
+    logp, ref (None: zeros) float32 [T]; targets int32 [T], negative where a row is
+    not scored.  kind: "sigmoid", "hinge" or "square"; average: scores are means over
+    a document's scored rows instead of sums.  stats float32 [2]: the loss and the
+    share of pairs whose chosen answer has the larger reward; rewards float32
+    [documents]; dlogp float32 [T] (see nsp_preference_loss)."""
+    fn = "preference_loss"
+    dev = _on_device(fn, torch.float32, logp=logp, ref=ref)
+    _on_device(fn, torch.int32, targets=targets, cu_seqlens=cu_seqlens)
+    if kind not in PREFERENCES:
+        raise ValueError(f"{fn}: unknown kind {kind!r}")
+    if logp.dim() != 1:
+        raise ValueError(f"{fn}: logp is [T]")
+    T = logp.shape[0]
+    _shape(fn, "targets", targets, (T,))
+    _shape(fn, "ref", ref, (T,))
+    docs = cu_seqlens.numel() - 1
+    if cu_seqlens.dim() != 1 or docs < 2 or docs % 2 != 0:
+        raise ValueError(f"{fn}: cu_seqlens is [documents + 1] of an even number of documents")
+    lib = load()
+    stats, rewards, dlogp = _new(stream, logp, (2,)), _new(stream, logp, (docs,)), _new(stream, logp, (T,))
+    ws = _workspace(fn, stream, logp, lib.nsp_preference_loss_workspace_size(docs), workspace)
+    st = lib.nsp_preference_loss(_ptr(logp), _ptr(ref), _ptr(targets), _ptr(cu_seqlens), docs, T,
+                                 PREFERENCES[kind], beta, smoothing, margin, bool(average), _ptr(stats),
+                                 _ptr(rewards), _ptr(dlogp), _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    _check("nsp_preference_loss", st)
+    return stats, rewards, dlogp
+
+
+NORMS = {2: 0, 2.0: 0, float("inf"): 1}
+
+
+def _gradients(fn, grads, dev=None):
+    """HOST arrays of the gradients' pointers, counts and types, and their device."""
+    n = len(grads)
+    if n == 0:
+        raise ValueError(f"{fn}: no gradients")
+    at = {t.get_device() for t in grads}
+    if dev is None:
+        if -1 in at:
+            raise ValueError(f"{fn}: a gradient is not on a CUDA device")
+        dev = torch.cuda.current_device()
+    if at != {dev}:
+        raise ValueError(f"{fn}: a gradient is not on the current device {dev}")
+    if not all([t.is_contiguous() for t in grads]):
+        raise ValueError(f"{fn}: libnsp takes contiguous tensors only")
+    try:
+        types = [_DTYPES[t.dtype] for t in grads]
+    except KeyError as e:
+        raise TypeError(f"{fn}: unsupported dtype {e.args[0]}") from None
+    return ((_vp * n)(*[t.data_ptr() for t in grads]), (_i64 * n)(*[t.numel() for t in grads]),
+            (_i32 * n)(*types), n, dev)
+
+
+def grad_norm(grads, norm_type=2, unscale=1.0, workspace=None, stream=None):
+    """Norm (norm_type 2 or inf) of all gradients of a list taken together, times
+    |unscale|: float32 [1].  Contiguous tensors of both types, any sizes."""
+    fn = "grad_norm"
+    if norm_type not in NORMS:
+        raise ValueError(f"{fn}: unknown norm {norm_type!r}")
+    ptrs, counts, types, n, dev = _gradients(fn, grads)
+    lib = load()
+    norm = _new(stream, grads[0], (1,), torch.float32)
+    ws = _workspace(fn, stream, norm, lib.nsp_grad_norm_workspace_size(counts, n), workspace)
+    st = lib.nsp_grad_norm(ptrs, counts, types, n, NORMS[norm_type], unscale, norm.data_ptr(), _ptr(ws),
+                           ws.numel(), _stream_of(stream, dev))
+    _check("nsp_grad_norm", st)
+    return norm
+
+
+def clip_grads(grads, max_norm, norm_type=2, unscale=1.0, eps=1e-6, out=None, workspace=None,
+               stream=None):
+    """Scale all gradients of a list by unscale * min(1, max_norm / (norm + eps)),
+    norm their grad_norm, which is returned (before clipping; float32 [1]).  In
+    place, or into `out`: a list of tensors of the same sizes, of either type."""
+    fn = "clip_grads"
+    if norm_type not in NORMS:
+        raise ValueError(f"{fn}: unknown norm {norm_type!r}")
+    ptrs, counts, types, n, dev = _gradients(fn, grads)
+    out_ptrs, out_types = ptrs, types
+    if out is not None:
+        if len(out) != n or any([a.shape != b.shape for a, b in zip(grads, out)]):
+            raise ValueError(f"{fn}: out are as many tensors of the gradients' shapes")
+        out_ptrs, _, out_types, _, _ = _gradients(fn, out, dev)
+    lib = load()
+    norm = _new(stream, grads[0], (1,), torch.float32)
+    ws = _workspace(fn, stream, norm, lib.nsp_grad_norm_workspace_size(counts, n), workspace)
+    st = lib.nsp_grad_clip(ptrs, out_ptrs, counts, types, out_types, n, NORMS[norm_type], unscale, max_norm,
+                           eps, norm.data_ptr(), _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    _check("nsp_grad_clip", st)
+    return norm
