@@ -4,114 +4,272 @@
 // g the gradient of logp: given (backward), or the policy loss's own, of the logp
 // just computed (the row is then read once for both).  A row without a target
 // (y < 0) is not read; its logp, lse and gradient are zero.
+//
+// All in base 2: with c = s log2(e), a range's state is M = c max x (rounded once)
+// and S = sum 2^(c x - M), each term's argument one FMA of the unrounded c x; ranges
+// join by S1 2^(M1 - M) + S2 2^(M2 - M).  The same M serves the sum, logp and the
+// gradient, so that its rounding cancels.
+//
+// A row is split over the blocks of a cluster, and a block's slice lives in its
+// threads' registers: one read of the logits, the sum, one exchange of (M, S)
+// through the cluster's shared memory, and the gradient from the same registers.
+#include <algorithm>
 #include <cmath>
 
 #include "policy.cuh"
+#include "tc_ptx.cuh"
 
 namespace nsp {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+using namespace tc;
 
-// m and s of sum exp(x - m): the sum of both ranges'.
+constexpr int kMaxRanks = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// The sum of both ranges, in the first.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
   const float ref = top == -INFINITY ? 0.f : top;
-  s = s * expf(m - ref) + s2 * expf(m2 - ref);
+  s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
   m = top;
 }
 
-template <typename T, RowMode MODE>
-__global__ void __launch_bounds__(kThreads) row_kernel(const __grid_constant__ RowArgs a) {
-  __shared__ float s_m[kWarps], s_s[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (MODE == kRowPolicy && status_bad(a.p.hdr)) return;
-  for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    const int y = __ldg(a.targets + t);
-    const T* const x = reinterpret_cast<const T*>(a.logits) + t * a.row_stride;
-    T* const dx = reinterpret_cast<T*>(a.dlogits) + t * a.out_stride;
-    int doc = 0;
-    bool scored = y >= 0;
-    if (MODE == kRowPolicy) {
-      scored = scored && t < (int64_t)__ldg(a.p.cu + a.p.ndoc);
-      if (scored) doc = doc_of(a.p.cu, a.p.ndoc, t);
-    }
-    if (!scored) {
-      if (MODE != kRowForward)
-        for (int j = threadIdx.x; j < a.vocab; j += kThreads) st_out(dx + j, 0.f);
-      if (MODE != kRowBackward && threadIdx.x == 0) {
-        if (a.logp) a.logp[t] = 0.f;
-        if (a.lse) a.lse[t] = 0.f;
-        if (MODE == kRowPolicy)
-          for (int i = 0; i < 3; ++i) a.p.terms[i * a.rows + t] = 0.f;
-      }
-      continue;
-    }
-    float lse, g;
-    if constexpr (MODE == kRowBackward) {
-      lse = __ldg(a.in_lse + t);
-      g = __ldg(a.dlogp + t);
-    } else {
-      float m = -INFINITY, s = 0.f;
-      for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
-        const float v = a.scale * to_f(x[j]);
-        if (v > m) {
-          s *= expf(m - v);
-          m = v;
-        }
-        s += v == -INFINITY ? 0.f : expf(v - m);
-      }
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  __device__ static __forceinline__ float top(const uint4& u) {
+    return fmaxf(max3f(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z)),
+                 __uint_as_float(u.w));
+  }
+};
+template <> struct Raw<__nv_bfloat16> {
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+  __device__ static __forceinline__ float top(const uint4& u) {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(u.x), "r"(u.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(u.z), "r"(u.w));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
+};
+
+// sum of 2^(c x + n) over a vector, added to acc pair by pair
+template <typename T>
+__device__ __forceinline__ uint64_t add_exps(const uint4& u, uint64_t c2, uint64_t n2, uint64_t acc) {
+  float x[Vec<T>::N];
+  Vec<T>::unpack(u, x);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-      __syncthreads();
-      if (lane == 0) {
-        s_m[warp] = m;
-        s_s[warp] = s;
-      }
-      __syncthreads();
-      m = s_m[0];
-      s = s_s[0];
-      for (int w = 1; w < kWarps; ++w) join(m, s, s_m[w], s_s[w]);
-      const float rest = logf(s);
-      lse = m + rest;
-      float logp = y < a.vocab ? a.scale * to_f(x[y]) - m - rest : NAN;
-      if (logp > 0.f) logp = 0.f;      // (by its rounding)
-      if (threadIdx.x == 0) {
-        if (a.logp) a.logp[t] = logp;
-        if (a.lse) a.lse[t] = lse;
-      }
-      if constexpr (MODE == kRowPolicy) {
-        const PolicyRow r = policy_row(a.p, t, doc, logp);
-        g = r.grad;
-        if (threadIdx.x == 0) {
-          a.p.terms[t] = r.surrogate;
-          a.p.terms[a.rows + t] = r.kl;
-          a.p.terms[2 * a.rows + t] = r.clipped;
-        }
-        __syncthreads();               // (in place: x[y] has been read)
-      }
+  for (int i = 0; i < Vec<T>::N / 2; ++i) {
+    float a, b;
+    f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), c2, n2), a, b);
+    acc = f2_add(acc, f2_pack(ex2(a), ex2(b)));
+  }
+  return acc;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_peer(const float2* p, int rank, float2 v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// VPT: vectors of a thread held in registers; what a slice has more is read again.
+template <typename T, RowMode MODE, int THREADS, int VPT>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __grid_constant__ RowArgs a,
+                                                                      const int ranks) {
+  constexpr int N = Vec<T>::N, kWarps = THREADS / 32;
+  __shared__ float2 s_part[kMaxRanks * kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t = blockIdx.x / (unsigned)ranks;
+  const int rank = (int)(blockIdx.x - (unsigned)t * ranks);
+  if (MODE == kRowPolicy && status_bad(a.p.hdr)) return;
+  const int y = __ldg(a.targets + t);
+  const T* const x = reinterpret_cast<const T*>(a.logits) + t * a.row_stride;
+  T* const dx = reinterpret_cast<T*>(a.dlogits) + t * a.out_stride;
+  bool scored = y >= 0;
+  if (MODE == kRowPolicy) scored = scored && t < (int64_t)__ldg(a.p.cu + a.p.ndoc);
+  // The row's whole vectors start at its first 16-byte border; the elements before and
+  // behind them are rank 0's first threads'.
+  const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T), a.vocab);
+  const int nvec = (a.vocab - head) / N, rest = a.vocab - nvec * N;
+  const int per = (nvec + ranks - 1) / ranks, v0 = rank * per, v1 = min(v0 + per, nvec);
+  const bool extra = rank == 0 && tid < rest;
+  const int ecol = tid < head ? tid : nvec * N + tid;
+  const uint4* const xv = reinterpret_cast<const uint4*>(x + head);
+  const bool whole = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
+  auto store = [&](int v, const float (&o)[N]) {
+    if (whole) {
+      st_once(dx + head + (int64_t)v * N, Vec<T>::pack(o));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) st_out(dx + head + (int64_t)v * N + i, o[i]);
     }
-    if constexpr (MODE != kRowForward) {
-      if (y >= a.vocab) g = NAN;
-      const float sg = a.scale * g;
-      for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
-        const float p = expf(a.scale * to_f(x[j]) - lse);
-        st_out(dx + j, sg * ((j == y ? 1.f : 0.f) - p));
+  };
+  if (!scored) {
+    if (MODE != kRowForward) {
+      const float zero[N] = {};
+      for (int v = v0 + tid; v < v1; v += THREADS) store(v, zero);
+      if (extra) st_out(dx + ecol, 0.f);
+    }
+    if (MODE != kRowBackward && rank == 0 && tid == 0) {
+      if (a.logp) a.logp[t] = 0.f;
+      if (a.lse) a.lse[t] = 0.f;
+      if (MODE == kRowPolicy)
+        for (int i = 0; i < 3; ++i) a.p.terms[i * a.rows + t] = 0.f;
+    }
+    return;
+  }
+  if (MODE != kRowBackward && ranks > 1) cluster_arrive();
+  uint4 reg[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = v0 + i * THREADS + tid;
+    reg[i] = v < v1 ? ld_once(xv + v)
+                    : make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
+  }
+  const float xe = extra ? to_f(x[ecol]) : -INFINITY;
+  const float c = a.scale * kLog2e;
+  const uint64_t c2 = f2_pack(c, c);
+  float n, k, g;                     // p = 2^(c x + n) k;  d logit = s g ([j = y] - p)
+  if constexpr (MODE == kRowBackward) {
+    n = -__ldg(a.in_lse + t) * kLog2e;
+    k = 1.f;
+    g = __ldg(a.dlogp + t);
+  } else {
+    // (read before the barrier: a gradient in place is written behind it)
+    const float xy = y < a.vocab ? to_f(x[y]) : NAN;
+    const int doc = MODE == kRowPolicy ? doc_of(a.p.cu, a.p.ndoc, t) : 0;
+    float top = xe;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) top = fmaxf(top, Raw<T>::top(reg[i]));
+    float m = top * c;
+    auto ref = [](float m) { return m == -INFINITY ? 0.f : -m; };
+    const uint64_t n2 = f2_pack(ref(m), ref(m));
+    uint64_t acc[2] = {f2_pack(ex2(fmaf(xe, c, ref(m))), 0.f), 0};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) acc[i & 1] = add_exps<T>(reg[i], c2, n2, acc[i & 1]);
+    float s, s1;
+    f2_unpack(f2_add(acc[0], acc[1]), s, s1);
+    s += s1;
+    for (int v = v0 + VPT * THREADS + tid; v < v1; v += THREADS) {
+      const uint4 u = ld_once(xv + v);
+      const float m1 = Raw<T>::top(u) * c;
+      const uint64_t one = add_exps<T>(u, c2, f2_pack(ref(m1), ref(m1)), 0);
+      float p0, p1;
+      f2_unpack(one, p0, p1);
+      join(m, s, m1, p0 + p1);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    // every warp's state to every block of the cluster
+    if (ranks > 1) {
+      cluster_wait();
+      if (lane < ranks) st_peer(&s_part[rank * kWarps + warp], lane, make_float2(m, s));
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      if (lane == 0) s_part[warp] = make_float2(m, s);
+      __syncthreads();
+    }
+    m = -INFINITY;
+    s = 0.f;
+    for (int i = lane; i < ranks * kWarps; i += 32) join(m, s, s_part[i].x, s_part[i].y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    const float rest2 = log2f(s);
+    float logp = (fmaf(xy, c, -m) - rest2) * kLn2;
+    if (logp > 0.f) logp = 0.f;      // (by its rounding)
+    const bool writes = rank == 0 && tid == 0;
+    if (writes) {
+      if (a.logp) a.logp[t] = logp;
+      if (a.lse) a.lse[t] = (m + rest2) * kLn2;
+    }
+    if constexpr (MODE == kRowPolicy) {
+      const PolicyRow r = policy_row(a.p, t, doc, logp);
+      g = r.grad;
+      if (writes) {
+        a.p.terms[t] = r.surrogate;
+        a.p.terms[a.rows + t] = r.kl;
+        a.p.terms[2 * a.rows + t] = r.clipped;
       }
+      n = ref(m);
+      k = 1.f / s;
     }
   }
+  if constexpr (MODE != kRowForward) {
+    if (y >= a.vocab) g = NAN;
+    const float sg = a.scale * g, f = -sg * k;
+    const uint64_t n2 = f2_pack(n, n), f2 = f2_pack(f, f);
+    const int yv = y < head ? -1 : (y - head) / N, yi = y - head - yv * N;
+    auto gradient = [&](int v, const uint4& u) {
+      float o[N];
+      Vec<T>::unpack(u, o);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        float p, q;
+        f2_unpack(f2_fma(f2_pack(o[2 * i], o[2 * i + 1]), c2, n2), p, q);
+        f2_unpack(f2_mul(f2_pack(ex2(p), ex2(q)), f2), o[2 * i], o[2 * i + 1]);
+      }
+      if (v == yv) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] += i == yi ? sg : 0.f;
+      }
+      store(v, o);
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = v0 + i * THREADS + tid;
+      if (v < v1) gradient(v, reg[i]);
+    }
+    for (int v = v0 + VPT * THREADS + tid; v < v1; v += THREADS) gradient(v, ld_once(xv + v));
+    if (extra) st_out(dx + ecol, ex2(fmaf(xe, c, n)) * f + (ecol == y ? sg : 0.f));
+  }
+}
+
+template <typename T, RowMode MODE, int THREADS, int VPT>
+cudaError_t go(const RowArgs& a, int ranks, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.rows * ranks));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = MODE != kRowBackward && ranks > 1 ? 1 : 0;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, row_kernel<T, MODE, THREADS, VPT>, a, ranks);
+}
+
+template <typename T, RowMode MODE>
+cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
+  const int64_t nvec = a.vocab / (16 / (int)sizeof(T)) + 1;
+  if (nvec <= 128) return go<T, MODE, 128, 1>(a, 1, s);
+  if (nvec <= 256) return go<T, MODE, 128, 2>(a, 1, s);
+  if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
+  int ranks = 1;
+  while (ranks < kMaxRanks && nvec > (int64_t)ranks * 4096) ranks *= 2;
+  while (ranks < kMaxRanks && a.rows * ranks < (int64_t)num_sms() * 2 && nvec > (int64_t)ranks * 512) ranks *= 2;
+  if (a.rows * ranks > INT32_MAX) ranks = 1;
+  const int64_t per = ceil_div(nvec, ranks);
+  if (per <= 512) return go<T, MODE, 512, 1>(a, ranks, s);
+  if (per <= 1024) return go<T, MODE, 512, 2>(a, ranks, s);
+  if (per <= 2048) return go<T, MODE, 512, 4>(a, ranks, s);
+  return go<T, MODE, 512, 8>(a, ranks, s);
 }
 
 template <typename T>
 cudaError_t launch_typed(const RowArgs& a, RowMode mode, cudaStream_t s) {
-  const unsigned blocks = (unsigned)(a.rows < 65536 ? a.rows : 65536);
-  if (mode == kRowForward) row_kernel<T, kRowForward><<<blocks, kThreads, 0, s>>>(a);
-  else if (mode == kRowBackward) row_kernel<T, kRowBackward><<<blocks, kThreads, 0, s>>>(a);
-  else row_kernel<T, kRowPolicy><<<blocks, kThreads, 0, s>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  if (mode == kRowForward) return launch_mode<T, kRowForward>(a, s);
+  if (mode == kRowBackward) return launch_mode<T, kRowBackward>(a, s);
+  return launch_mode<T, kRowPolicy>(a, s);
 }
 
 }  // namespace
