@@ -78,6 +78,17 @@ __global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const LossArgs 
   }
 }
 
+// Weight and advantage of every row, for a kernel that has no time for a search a row.
+__global__ void __launch_bounds__(kThreads) loss_rows_kernel(const __grid_constant__ RowArgs a) {
+  grid_dep_wait();
+  if (status_bad(a.p.hdr)) return;
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= a.rows || t >= (int64_t)__ldg(a.p.cu + a.p.ndoc) || __ldg(a.targets + t) < 0) return;
+  const int doc = doc_of(a.p.cu, a.p.ndoc, t);
+  a.p.row_scalars[t] = make_float2(__ldcg(a.p.doc_weight + doc),
+                                   __ldg(a.p.advantages + (a.p.per_token ? t : (int64_t)doc)));
+}
+
 // stats from sums of surrogate, kl and clipped.
 __device__ __forceinline__ void write_stats(float* stats, float kl_coef, double pg, double kl, double cut) {
   stats[0] = (float)(pg + (double)kl_coef * kl);
@@ -95,7 +106,8 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const __grid_constant_
        t += (int64_t)gridDim.x * kThreads) {
     float g = 0.f;
     if (t < end && __ldg(a.targets + t) >= 0) {
-      const PolicyRow r = policy_row(a.p, t, doc_of(a.p.cu, a.p.ndoc, t), __ldg(a.logp + t));
+      const PolicyScalars v = policy_scalars(a.p, t, doc_of(a.p.cu, a.p.ndoc, t));
+      const PolicyRow r = policy_row(a.p, v, __ldg(a.logp + t));
       pg.add(r.surrogate);
       kl.add(r.kl);
       cut.add(r.clipped);
@@ -217,7 +229,8 @@ LossWsLayout loss_ws_layout(int64_t rows, int32_t ndoc, bool logits) {
   L.bits = align_up(L.before + 4 * words, 256);
   L.weight = align_up(L.bits + 4 * words, 256);
   L.terms = align_up(L.weight + 4 * (size_t)ndoc, 256);
-  L.total = align_up(L.terms + 12 * (logits ? (size_t)rows : (size_t)kPolicyBlocks), 256);
+  L.scalars = align_up(L.terms + 12 * (logits ? (size_t)rows : (size_t)kPolicyBlocks), 256);
+  L.total = align_up(L.scalars + (logits ? 8 * (size_t)rows : 0), 256);
   return L;
 }
 
@@ -225,6 +238,11 @@ cudaError_t launch_loss_prep(const LossArgs& a, cudaStream_t s) {
   loss_prep_kernel<<<1, kPrepThreads, 0, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
+}
+
+cudaError_t launch_loss_rows(const RowArgs& a, cudaStream_t s) {
+  count_launches(1);
+  return launch_dependent(loss_rows_kernel, dim3((unsigned)ceil_div(a.rows, kThreads)), dim3(kThreads), 0, s, a);
 }
 
 static int policy_blocks(int64_t rows) {

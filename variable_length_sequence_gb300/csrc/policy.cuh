@@ -17,10 +17,19 @@ struct PolicyRow {
   float surrogate, kl, clipped, grad;      // grad: of logp, all four times the row's weight
 };
 
-__device__ __forceinline__ PolicyRow policy_row(const PolicyRows& p, int64_t t, int doc, float logp) {
-  const float w = __ldg(p.doc_weight + doc);
-  const float adv = __ldg(p.advantages + (p.per_token ? t : (int64_t)doc));
-  const float rho = expf(logp - __ldg(p.old_logp + t));
+// What a row's loss is made of, besides its logp.
+struct PolicyScalars {
+  float weight, advantage, old_logp, ref_logp;
+};
+
+__device__ __forceinline__ PolicyScalars policy_scalars(const PolicyRows& p, int64_t t, int doc) {
+  return {__ldg(p.doc_weight + doc), __ldg(p.advantages + (p.per_token ? t : (int64_t)doc)),
+          __ldg(p.old_logp + t), p.ref_logp != nullptr ? __ldg(p.ref_logp + t) : 0.f};
+}
+
+__device__ __forceinline__ PolicyRow policy_row(const PolicyRows& p, const PolicyScalars& v, float logp) {
+  const float w = v.weight, adv = v.advantage;
+  const float rho = expf(logp - v.old_logp);
   const bool cut = (adv > 0.f && rho > 1.f + p.clip_high) || (adv < 0.f && rho < 1.f - p.clip_low);
   PolicyRow r;
   const float bound = adv > 0.f ? 1.f + p.clip_high : 1.f - p.clip_low;
@@ -29,7 +38,7 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyRows& p, int64_t t, 
   r.clipped = cut ? w : 0.f;
   r.kl = 0.f;
   if (p.ref_logp != nullptr) {
-    const float z = __ldg(p.ref_logp + t) - logp, e = expm1f(z);
+    const float z = v.ref_logp - logp, e = expm1f(z);
     r.kl = w * (e - z);
     r.grad = fmaf(-p.kl_coef, e, r.grad);
   }

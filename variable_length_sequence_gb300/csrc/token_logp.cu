@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
       if (a.lse) a.lse[t] = (m + rest2) * kLn2;
     }
     if constexpr (MODE == kRowPolicy) {
-      const PolicyRow r = policy_row(a.p, t, doc, logp);
+      const PolicyRow r = policy_row(a.p, policy_scalars(a.p, t, doc), logp);
       g = r.grad;
       if (writes) {
         a.p.terms[t] = r.surrogate;
@@ -232,6 +232,333 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
   }
 }
 
+// ---- many long rows: persistent blocks behind a ring of asynchronous copies
+//
+// A block (a cluster of them, where a row is longer than 128 KB) walks its rows.  Every
+// thread copies its own vectors of the rows ahead into shared memory, kRing chunks of
+// kChunk vectors at any time, and reads only what it copied itself, so that the ring
+// needs no barrier.  A scored row is read from there into registers, which the gradient
+// is taken from.
+constexpr int kRingThreads = 512, kRingWarps = kRingThreads / 32;
+constexpr int kChunk = 4, kRing = 6;
+constexpr int kRingBytes = kRing * kChunk * kRingThreads * 16;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// NCH: chunks of a row (policy), held in registers; 0: any number, not held (forward).
+template <typename T, RowMode MODE, int NCH>
+__global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_constant__ RowArgs a,
+                                                               const int ranks, const int chunks) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ __align__(16) uint4 s_ring[];
+  __shared__ float2 s_part[2][kMaxRanks * kRingWarps];
+  __shared__ float2 s_target[2];                     // x: the target's logit
+  __shared__ int2 s_queue[kRingWarps][8];            // rows copied ahead, a warp's own copy
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = ranks > 1 ? (int)(blockIdx.x % (unsigned)ranks) : 0;
+  const int64_t first = blockIdx.x / (unsigned)ranks, step = gridDim.x / (unsigned)ranks;
+  if (MODE == kRowPolicy) {
+    grid_dep_wait();
+    if (status_bad(a.p.hdr)) return;
+  }
+  const int64_t end = MODE == kRowPolicy ? min(a.rows, (int64_t)__ldg(a.p.cu + a.p.ndoc)) : a.rows;
+  const uint32_t ring = smem_u32(s_ring) + tid * 16;
+  const float c = a.scale * kLog2e;
+  const uint64_t c2 = f2_pack(c, c);
+
+  struct Row {
+    const T* x;
+    int head, nvec, v0, v1;
+  };
+  auto row_of = [&](int64_t t) {
+    Row r;
+    r.x = reinterpret_cast<const T*>(a.logits) + t * a.row_stride;
+    r.head = min((int)((16 - (reinterpret_cast<uintptr_t>(r.x) & 15)) & 15) / (int)sizeof(T), a.vocab);
+    r.nvec = (a.vocab - r.head) / N;
+    const int per = (r.nvec + ranks - 1) / ranks;
+    r.v0 = rank * per;
+    r.v1 = min(r.v0 + per, r.nvec);
+    return r;
+  };
+  auto store = [&](T* dx, int head, bool whole, int v, const float (&o)[N]) {
+    if (whole) {
+      st_once(dx + head + (int64_t)v * N, Vec<T>::pack(o));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) st_out(dx + head + (int64_t)v * N + i, o[i]);
+    }
+  };
+  auto gradient_row = [&](int64_t t, const T* x, bool& whole) {
+    T* const dx = reinterpret_cast<T*>(a.dlogits) + t * a.out_stride;
+    whole = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
+    return dx;
+  };
+  // a row without a score: zeros
+  auto skip = [&](int64_t t) {
+    if constexpr (MODE == kRowPolicy) {
+      const Row r = row_of(t);
+      bool whole;
+      T* const dx = gradient_row(t, r.x, whole);
+      const float zero[N] = {};
+      for (int v = r.v0 + tid; v < r.v1; v += kRingThreads) store(dx, r.head, whole, v, zero);
+      if (rank == 0 && tid < a.vocab - r.nvec * N) st_out(dx + (tid < r.head ? tid : r.nvec * N + tid), 0.f);
+    }
+    if (rank == 0 && tid == 0) {
+      if (a.logp) a.logp[t] = 0.f;
+      if (a.lse) a.lse[t] = 0.f;
+      if (MODE == kRowPolicy)
+        for (int i = 0; i < 3; ++i) a.p.terms[i * a.rows + t] = 0.f;
+    }
+  };
+
+  // The block's rows in order, 32 targets at a time in a warp's lanes, the next 32 on
+  // their way.
+  auto target = [&](int64_t i) {
+    const int64_t t = first + i * step;
+    return t < end ? __ldg(a.targets + t) : -1;
+  };
+  int64_t base = 0;
+  int y32 = target(lane), y_next = target(32 + lane);
+  uint32_t left = __ballot_sync(0xffffffffu, y32 >= 0);
+  int at = 0;                                        // rows of the 32 that are done with
+  auto next = [&](int64_t& t, int& y) {
+    for (;;) {
+      const int bit = left ? __ffs(left) - 1 : 32;
+      for (; at < bit; ++at) {
+        const int64_t u = first + (base + at) * step;
+        if (u >= a.rows) return false;
+        skip(u);
+      }
+      if (bit < 32) {
+        left &= left - 1;
+        at = bit + 1;
+        t = first + (base + bit) * step;
+        y = __shfl_sync(0xffffffffu, y32, bit);
+        return true;
+      }
+      base += 32;
+      y32 = y_next;
+      y_next = target(base + 32 + lane);
+      left = __ballot_sync(0xffffffffu, y32 >= 0);
+      at = 0;
+    }
+  };
+  int queued = 0, taken = 0, ch_ahead = chunks;
+  Row ahead = {};
+  bool more = true;
+  auto copy_next = [&](int slot) {
+    if (more && ch_ahead == chunks) {
+      int64_t t;
+      int y;
+      more = next(t, y);
+      if (more) {
+        ahead = row_of(t);
+        ch_ahead = 0;
+        if (lane == 0) s_queue[warp][queued & 7] = make_int2((int)t, y);
+        ++queued;
+      }
+    }
+    if (more) {
+      const uint4* const xv = reinterpret_cast<const uint4*>(ahead.x + ahead.head);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) {
+        const int v = ahead.v0 + (ch_ahead * kChunk + i) * kRingThreads + tid;
+        if (v < ahead.v1) copy16(ring + (slot * kChunk + i) * kRingThreads * 16, xv + v);
+      }
+      ++ch_ahead;
+    }
+    copy_commit();
+  };
+  for (int i = 0; i < kRing; ++i) copy_next(i);
+  if (ranks > 1) {                                   // (every block of the cluster runs)
+    cluster_arrive();
+    cluster_wait();
+  }
+  int slot = 0;
+  for (; taken < queued; ++taken) {
+    __syncwarp();
+    const int2 item = s_queue[warp][taken & 7];
+    __syncwarp();
+    const int64_t t = item.x;
+    const int y = item.y, par = taken & 1;
+    const Row r = row_of(t);
+    const int rest = a.vocab - r.nvec * N;
+    const bool extra = rank == 0 && tid < rest;
+    const int ecol = tid < r.head ? tid : r.nvec * N + tid;
+    const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
+    const int yv = y < r.head ? -1 : (y - r.head) / N, yi = y - r.head - yv * N;
+    auto publish = [&](float x) {
+      if (ranks > 1) {
+        for (int k = 0; k < ranks; ++k) st_peer(&s_target[par], k, make_float2(x, 0.f));
+      } else {
+        s_target[par].x = x;
+      }
+    };
+    uint4 reg[NCH > 0 ? NCH * kChunk : kChunk];
+    float m = -INFINITY, s = 0.f;
+    auto take = [&](int ch, uint4* u) {
+      copy_wait<kRing - 1>();
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) {
+        const int v = r.v0 + (ch * kChunk + i) * kRingThreads + tid;
+        u[i] = v < r.v1 ? s_ring[(slot * kChunk + i) * kRingThreads + tid]
+                        : make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
+        top = fmaxf(top, Raw<T>::top(u[i]));
+        if (v == yv && v < r.v1) {
+          float e[N], xy = 0.f;
+          Vec<T>::unpack(u[i], e);
+#pragma unroll
+          for (int j = 0; j < N; ++j) xy = j == yi ? e[j] : xy;
+          publish(xy);
+        }
+      }
+      const float m1 = fmaxf(m, top * c), n1 = m1 == -INFINITY ? 0.f : -m1;
+      const uint64_t n2 = f2_pack(n1, n1);
+      uint64_t acc[2] = {f2_pack(s * ex2(m + n1), 0.f), 0};
+      m = m1;
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) acc[i & 1] = add_exps<T>(u[i], c2, n2, acc[i & 1]);
+      float s1;
+      f2_unpack(f2_add(acc[0], acc[1]), s, s1);
+      s += s1;
+      copy_next(slot);
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+    };
+    if constexpr (NCH > 0) {
+#pragma unroll
+      for (int ch = 0; ch < NCH; ++ch) take(ch, reg + ch * kChunk);
+    } else {
+      for (int ch = 0; ch < chunks; ++ch) take(ch, reg);
+    }
+    PolicyScalars sc = {};
+    if constexpr (MODE == kRowPolicy) {
+      const float2 w = __ldg(a.p.row_scalars + t);
+      sc = {w.x, w.y, __ldg(a.p.old_logp + t), a.p.ref_logp != nullptr ? __ldg(a.p.ref_logp + t) : 0.f};
+    }
+    if (extra) {
+      join(m, s, xe * c, isinf(xe) && xe < 0.f ? 0.f : 1.f);
+      if (ecol == y) publish(xe);
+    }
+    if (tid == 0 && rank == 0 && y >= a.vocab) publish(NAN);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    // (two sets of states in turn: a block that writes the next row's has seen every block
+    // behind this row's barrier, and so behind reading the last row's)
+    if (ranks > 1) {
+      if (lane < ranks) st_peer(&s_part[par][rank * kRingWarps + warp], lane, make_float2(m, s));
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      if (lane == 0) s_part[par][warp] = make_float2(m, s);
+      __syncthreads();
+    }
+    if (MODE == kRowForward && warp != 0) continue;
+    m = -INFINITY;
+    s = 0.f;
+    for (int i = lane; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    const float rest2 = log2f(s);
+    float logp = (fmaf(s_target[par].x, c, -m) - rest2) * kLn2;
+    if (logp > 0.f) logp = 0.f;      // (by its rounding)
+    const bool writes = rank == 0 && tid == 0;
+    if (writes) {
+      if (a.logp) a.logp[t] = logp;
+      if (a.lse) a.lse[t] = (m + rest2) * kLn2;
+    }
+    if constexpr (MODE == kRowPolicy) {
+      const PolicyRow pr = policy_row(a.p, sc, logp);
+      if (writes) {
+        a.p.terms[t] = pr.surrogate;
+        a.p.terms[a.rows + t] = pr.kl;
+        a.p.terms[2 * a.rows + t] = pr.clipped;
+      }
+      const float g = y < a.vocab ? pr.grad : NAN;
+      const float sg = a.scale * g, f = -sg / s, n = m == -INFINITY ? 0.f : -m;
+      const uint64_t n2 = f2_pack(n, n), ff = f2_pack(f, f);
+      bool whole;
+      T* const dx = gradient_row(t, r.x, whole);
+#pragma unroll
+      for (int i = 0; i < NCH * kChunk; ++i) {
+        const int v = r.v0 + i * kRingThreads + tid;
+        if (v >= r.v1) break;
+        float o[N];
+        Vec<T>::unpack(reg[i], o);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          float p, q;
+          f2_unpack(f2_fma(f2_pack(o[2 * j], o[2 * j + 1]), c2, n2), p, q);
+          f2_unpack(f2_mul(f2_pack(ex2(p), ex2(q)), ff), o[2 * j], o[2 * j + 1]);
+        }
+        if (v == yv) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) o[j] += j == yi ? sg : 0.f;
+        }
+        store(dx, r.head, whole, v, o);
+      }
+      if (extra) st_out(dx + ecol, ex2(fmaf(xe, c, n)) * f + (ecol == y ? sg : 0.f));
+    }
+  }
+}
+
+template <typename T, RowMode MODE, int NCH>
+cudaError_t go_ring(const RowArgs& a, int ranks, int chunks, cudaStream_t s) {
+  static bool allowed[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  auto kern = ring_kernel<T, MODE, NCH>;
+  if (dev >= 64 || !allowed[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(num_sms() / ranks * ranks));
+  cfg.blockDim = dim3(kRingThreads);
+  cfg.dynamicSmemBytes = kRingBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (ranks > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)ranks;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+    // the clusters that run at once: one that had to wait for others would double the time
+    static int resident[64][kMaxRanks + 1] = {};
+    int fit = dev < 64 ? resident[dev][ranks] : 0;
+    if (fit == 0) {
+      cfg.attrs = attr;
+      cfg.numAttrs = n;
+      e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      if (fit < 1) return cudaErrorInvalidConfiguration;
+      if (dev < 64) resident[dev][ranks] = fit;
+    }
+    cfg.gridDim.x = (unsigned)(std::min<int64_t>(fit, num_sms() / ranks) * ranks);
+  }
+  if (a.rows * ranks < cfg.gridDim.x) cfg.gridDim.x = (unsigned)(a.rows * ranks);
+  if (MODE == kRowPolicy) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kern, a, ranks, chunks);
+}
+
 template <typename T, RowMode MODE, int THREADS, int VPT>
 cudaError_t go(const RowArgs& a, int ranks, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -254,6 +581,25 @@ cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
   if (nvec <= 128) return go<T, MODE, 128, 1>(a, 1, s);
   if (nvec <= 256) return go<T, MODE, 128, 2>(a, 1, s);
   if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
+  constexpr int kHeld = 4 * kChunk * kRingThreads;   // vectors of a block's registers
+  if constexpr (MODE != kRowBackward) {
+    int r = 1;
+    if (MODE == kRowPolicy)
+      while (r < kMaxRanks && nvec > (int64_t)r * kHeld) r *= 2;
+    const int chunks = (int)ceil_div(ceil_div(nvec, r), kChunk * kRingThreads);
+    if (a.rows * r >= (int64_t)num_sms() * 4 && (MODE == kRowForward || chunks <= 4)) {
+      if constexpr (MODE == kRowForward) {
+        return go_ring<T, MODE, 0>(a, 1, chunks, s);
+      } else {
+        const cudaError_t e = launch_loss_rows(a, s);
+        if (e != cudaSuccess) return e;
+        if (chunks == 1) return go_ring<T, MODE, 1>(a, r, chunks, s);
+        if (chunks == 2) return go_ring<T, MODE, 2>(a, r, chunks, s);
+        if (chunks == 3) return go_ring<T, MODE, 3>(a, r, chunks, s);
+        return go_ring<T, MODE, 4>(a, r, chunks, s);
+      }
+    }
+  }
   int ranks = 1;
   while (ranks < kMaxRanks && nvec > (int64_t)ranks * 4096) ranks *= 2;
   while (ranks < kMaxRanks && a.rows * ranks < (int64_t)num_sms() * 2 && nvec > (int64_t)ranks * 512) ranks *= 2;

@@ -48,6 +48,7 @@ struct PolicyRows {
   const WsHeader* hdr;
   const float* doc_weight;                 // [ndoc] weight of a row of the document
   float* terms;                            // [3][rows]: weighted surrogate, kl, clipped
+  float2* row_scalars;                     // [rows] weight and advantage (launch_loss_rows)
 };
 
 struct RowArgs {
@@ -68,9 +69,10 @@ cudaError_t launch_rows(const RowArgs& a, RowMode mode, int32_t io_dtype, cudaSt
 
 // ---- losses (loss.cu)
 // Workspace of a loss: header; per 32 rows the number of scored ones before them and
-// which of them are; each document's weight; terms or partial sums.
+// which of them are; each document's weight; terms or partial sums; with logits, each
+// row's weight and advantage.
 struct LossWsLayout {
-  size_t before, bits, weight, terms, total;
+  size_t before, bits, weight, terms, scalars, total;
 };
 LossWsLayout loss_ws_layout(int64_t rows, int32_t ndoc, bool logits);
 
@@ -89,6 +91,8 @@ struct LossArgs {
 // Checks cu_seqlens (status word), counts each document's scored rows and writes
 // the documents' weights.
 cudaError_t launch_loss_prep(const LossArgs& a, cudaStream_t s);
+// each scored row's weight and advantage, behind launch_loss_prep
+cudaError_t launch_loss_rows(const RowArgs& a, cudaStream_t s);
 
 struct PolicyArgs {
   const float* logp;

@@ -172,6 +172,7 @@ int32_t policy_check(const nsp_policy_t* policy, const int32_t* cu, int32_t ndoc
   p.hdr = reinterpret_cast<WsHeader*>(ws);
   p.doc_weight = reinterpret_cast<float*>(ws + L.weight);
   p.terms = reinterpret_cast<float*>(ws + L.terms);
+  p.row_scalars = reinterpret_cast<float2*>(ws + L.scalars);
   l.cu = cu; l.ndoc = ndoc; l.rows = rows;
   l.mean = policy->mean; l.total = policy->total;
   l.hdr = reinterpret_cast<WsHeader*>(ws);
