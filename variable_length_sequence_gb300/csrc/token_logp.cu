@@ -250,6 +250,16 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// The sum of a warp's 32 ranges, in every lane.
+__device__ __forceinline__ void join_warp(float& m, float& s) {
+  float top;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
+  s *= ex2(m - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  m = top;
+}
+
 // NCH: chunks of a row (policy), held in registers; 0: any number, not held (forward).
 template <typename T, RowMode MODE, int NCH>
 __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_constant__ RowArgs a,
@@ -267,13 +277,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     if (status_bad(a.p.hdr)) return;
   }
   const int64_t end = MODE == kRowPolicy ? min(a.rows, (int64_t)__ldg(a.p.cu + a.p.ndoc)) : a.rows;
-  const uint32_t ring = smem_u32(s_ring) + tid * 16;
+  uint4* const ring = s_ring + tid;
   const float c = a.scale * kLog2e;
   const uint64_t c2 = f2_pack(c, c);
 
+  // A row's whole vectors start at its first 16-byte border, the thread's own ones at
+  // `first_vec` of them, kRingThreads apart, while `left` > 0 of the block's slice; the
+  // elements before and behind the vectors are rank 0's first threads'.
   struct Row {
     const T* x;
-    int head, nvec, v0, v1;
+    int head, nvec, first_vec, left;
   };
   auto row_of = [&](int64_t t) {
     Row r;
@@ -281,16 +294,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     r.head = min((int)((16 - (reinterpret_cast<uintptr_t>(r.x) & 15)) & 15) / (int)sizeof(T), a.vocab);
     r.nvec = (a.vocab - r.head) / N;
     const int per = (r.nvec + ranks - 1) / ranks;
-    r.v0 = rank * per;
-    r.v1 = min(r.v0 + per, r.nvec);
+    r.first_vec = rank * per + tid;
+    r.left = min(rank * per + per, r.nvec) - r.first_vec;
     return r;
   };
-  auto store = [&](T* dx, int head, bool whole, int v, const float (&o)[N]) {
+  auto store = [&](T* dx, bool whole, const float (&o)[N]) {
     if (whole) {
-      st_once(dx + head + (int64_t)v * N, Vec<T>::pack(o));
+      st_once(dx, Vec<T>::pack(o));
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) st_out(dx + head + (int64_t)v * N + i, o[i]);
+      for (int i = 0; i < N; ++i) st_out(dx + i, o[i]);
     }
   };
   auto gradient_row = [&](int64_t t, const T* x, bool& whole) {
@@ -305,7 +318,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       bool whole;
       T* const dx = gradient_row(t, r.x, whole);
       const float zero[N] = {};
-      for (int v = r.v0 + tid; v < r.v1; v += kRingThreads) store(dx, r.head, whole, v, zero);
+      for (int i = 0; i < r.left; i += kRingThreads)
+        store(dx + r.head + (int64_t)(r.first_vec + i) * N, whole, zero);
       if (rank == 0 && tid < a.vocab - r.nvec * N) st_out(dx + (tid < r.head ? tid : r.nvec * N + tid), 0.f);
     }
     if (rank == 0 && tid == 0) {
@@ -348,33 +362,40 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       at = 0;
     }
   };
-  int queued = 0, taken = 0, ch_ahead = chunks;
-  Row ahead = {};
+  int queued = 0, taken = 0, ahead_left = 0;
+  const uint4* ahead = nullptr;                      // the thread's first vector of the row ahead
   bool more = true;
-  auto copy_next = [&](int slot) {
-    if (more && ch_ahead == chunks) {
-      int64_t t;
-      int y;
-      more = next(t, y);
-      if (more) {
-        ahead = row_of(t);
-        ch_ahead = 0;
-        if (lane == 0) s_queue[warp][queued & 7] = make_int2((int)t, y);
-        ++queued;
-      }
-    }
+  auto next_row = [&] {
+    int64_t t;
+    int y;
+    more = more && next(t, y);
+    ahead_left = 0;
+    if (!more) return;
+    const Row r = row_of(t);
+    ahead = reinterpret_cast<const uint4*>(r.x + r.head) + r.first_vec;
+    ahead_left = r.left;
+    if (lane == 0) s_queue[warp][queued & 7] = make_int2((int)t, y);
+    ++queued;
+  };
+  // chunk ch of the row ahead; where the row has no vector the ring holds -infinity
+  auto copy_chunk = [&](int slot, int ch) {
     if (more) {
-      const uint4* const xv = reinterpret_cast<const uint4*>(ahead.x + ahead.head);
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {
-        const int v = ahead.v0 + (ch_ahead * kChunk + i) * kRingThreads + tid;
-        if (v < ahead.v1) copy16(ring + (slot * kChunk + i) * kRingThreads * 16, xv + v);
+        uint4* const to = ring + (slot * kChunk + i) * kRingThreads;
+        const int v = (ch * kChunk + i) * kRingThreads;
+        if (v < ahead_left) copy16(smem_u32(to), ahead + v);
+        else *to = make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
       }
-      ++ch_ahead;
     }
     copy_commit();
   };
-  for (int i = 0; i < kRing; ++i) copy_next(i);
+  int ch_ahead = 0;
+  for (int i = 0; i < kRing; ++i) {
+    if (ch_ahead == 0) next_row();
+    copy_chunk(i, ch_ahead);
+    ch_ahead = ch_ahead + 1 == chunks ? 0 : ch_ahead + 1;
+  }
   if (ranks > 1) {                                   // (every block of the cluster runs)
     cluster_arrive();
     cluster_wait();
@@ -391,7 +412,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     const bool extra = rank == 0 && tid < rest;
     const int ecol = tid < r.head ? tid : r.nvec * N + tid;
     const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
-    const int yv = y < r.head ? -1 : (y - r.head) / N, yi = y - r.head - yv * N;
+    // the thread's vector with the target (its number in the thread's), and where in it
+    const int ydist = (y < r.head ? -1 : (y - r.head) / N) - r.first_vec;
+    const int mine = ydist >= 0 && ydist < r.left && ydist % kRingThreads == 0 ? ydist / kRingThreads : -1;
+    const int yi = (y - r.head) & (N - 1);
     auto publish = [&](float x) {
       if (ranks > 1) {
         for (int k = 0; k < ranks; ++k) st_peer(&s_target[par], k, make_float2(x, 0.f));
@@ -406,11 +430,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {
-        const int v = r.v0 + (ch * kChunk + i) * kRingThreads + tid;
-        u[i] = v < r.v1 ? s_ring[(slot * kChunk + i) * kRingThreads + tid]
-                        : make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
+        u[i] = ring[(slot * kChunk + i) * kRingThreads];
         top = fmaxf(top, Raw<T>::top(u[i]));
-        if (v == yv && v < r.v1) {
+        if (mine == ch * kChunk + i) {
           float e[N], xy = 0.f;
           Vec<T>::unpack(u[i], e);
 #pragma unroll
@@ -427,14 +449,24 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       float s1;
       f2_unpack(f2_add(acc[0], acc[1]), s, s1);
       s += s1;
-      copy_next(slot);
-      slot = slot + 1 == kRing ? 0 : slot + 1;
     };
+    auto advance = [&] { slot = slot + 1 == kRing ? 0 : slot + 1; };
     if constexpr (NCH > 0) {
 #pragma unroll
-      for (int ch = 0; ch < NCH; ++ch) take(ch, reg + ch * kChunk);
+      for (int ch = 0; ch < NCH; ++ch) {
+        take(ch, reg + ch * kChunk);
+        if ((ch + kRing) % NCH == 0) next_row();
+        copy_chunk(slot, (ch + kRing) % NCH);
+        advance();
+      }
     } else {
-      for (int ch = 0; ch < chunks; ++ch) take(ch, reg);
+      for (int ch = 0; ch < chunks; ++ch) {
+        take(ch, reg);
+        if (ch_ahead == 0) next_row();
+        copy_chunk(slot, ch_ahead);
+        ch_ahead = ch_ahead + 1 == chunks ? 0 : ch_ahead + 1;
+        advance();
+      }
     }
     PolicyScalars sc = {};
     if constexpr (MODE == kRowPolicy) {
@@ -446,9 +478,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       if (ecol == y) publish(xe);
     }
     if (tid == 0 && rank == 0 && y >= a.vocab) publish(NAN);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    join_warp(m, s);
     // (two sets of states in turn: a block that writes the next row's has seen every block
     // behind this row's barrier, and so behind reading the last row's)
     if (ranks > 1) {
@@ -463,10 +493,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
     if (MODE == kRowForward && warp != 0) continue;
     m = -INFINITY;
     s = 0.f;
-    for (int i = lane; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    if (lane < ranks * kRingWarps) {
+      m = s_part[par][lane].x;
+      s = s_part[par][lane].y;
+    }
+    for (int i = lane + 32; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
+    join_warp(m, s);
     const float rest2 = log2f(s);
     float logp = (fmaf(s_target[par].x, c, -m) - rest2) * kLn2;
     if (logp > 0.f) logp = 0.f;      // (by its rounding)
@@ -487,10 +519,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       const uint64_t n2 = f2_pack(n, n), ff = f2_pack(f, f);
       bool whole;
       T* const dx = gradient_row(t, r.x, whole);
+      T* const out = dx + r.head + (int64_t)r.first_vec * N;
 #pragma unroll
       for (int i = 0; i < NCH * kChunk; ++i) {
-        const int v = r.v0 + i * kRingThreads + tid;
-        if (v >= r.v1) break;
+        if (i * kRingThreads >= r.left) break;
         float o[N];
         Vec<T>::unpack(reg[i], o);
 #pragma unroll
@@ -499,11 +531,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
           f2_unpack(f2_fma(f2_pack(o[2 * j], o[2 * j + 1]), c2, n2), p, q);
           f2_unpack(f2_mul(f2_pack(ex2(p), ex2(q)), ff), o[2 * j], o[2 * j + 1]);
         }
-        if (v == yv) {
+        if (i == mine) {
 #pragma unroll
           for (int j = 0; j < N; ++j) o[j] += j == yi ? sg : 0.f;
         }
-        store(dx, r.head, whole, v, o);
+        store(out + i * kRingThreads * N, whole, o);
       }
       if (extra) st_out(dx + ecol, ex2(fmaf(xe, c, n)) * f + (ecol == y ? sg : 0.f));
     }
@@ -577,7 +609,7 @@ cudaError_t go(const RowArgs& a, int ranks, cudaStream_t s) {
 
 template <typename T, RowMode MODE>
 cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
-  const int64_t nvec = a.vocab / (16 / (int)sizeof(T)) + 1;
+  const int64_t nvec = std::max(1, a.vocab / (16 / (int)sizeof(T)));
   if (nvec <= 128) return go<T, MODE, 128, 1>(a, 1, s);
   if (nvec <= 256) return go<T, MODE, 128, 2>(a, 1, s);
   if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
