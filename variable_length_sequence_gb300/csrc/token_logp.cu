@@ -234,17 +234,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
 
 // ---- many long rows: persistent blocks behind a ring of asynchronous copies
 //
-// A block (a cluster of them, where a row is longer than 128 KB) walks its rows.  Every
-// thread copies its own vectors of the rows ahead into shared memory, kRing chunks of
-// kChunk vectors at any time, and reads only what it copied itself, so that the ring
-// needs no barrier.  A scored row is read from there into registers, which the gradient
-// is taken from.
+// Two blocks of an SM walk their rows (policy: a cluster of blocks a row, a slice of it
+// each).  Every thread copies its own vectors of the rows ahead into its own places of
+// shared memory, kSlots of them at any time, and reads only what it copied itself, so
+// that the ring needs no barrier and no wait but the copies' own.
 constexpr int kRingThreads = 512, kRingWarps = kRingThreads / 32;
-constexpr int kChunk = 4, kRing = 6;
-constexpr int kRingBytes = kRing * kChunk * kRingThreads * 16;
+constexpr int kSlots = 12;                           // 16-byte places of a thread
+constexpr int kRingBytes = kSlots * kRingThreads * 16;
+constexpr int kMaxSlice = 8;                         // vectors of a thread in a policy row
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -260,66 +260,80 @@ __device__ __forceinline__ void join_warp(float& m, float& s) {
   m = top;
 }
 
-// NCH: chunks of a row (policy), held in registers; 0: any number, not held (forward).
-template <typename T, RowMode MODE, int NCH>
-__global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_constant__ RowArgs a,
-                                                               const int ranks, const int chunks) {
-  constexpr int N = Vec<T>::N;
-  extern __shared__ __align__(16) uint4 s_ring[];
-  __shared__ float2 s_part[2][kMaxRanks * kRingWarps];
-  __shared__ float2 s_target[2];                     // x: the target's logit
-  __shared__ int2 s_queue[kRingWarps][8];            // rows copied ahead, a warp's own copy
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = ranks > 1 ? (int)(blockIdx.x % (unsigned)ranks) : 0;
-  const int64_t first = blockIdx.x / (unsigned)ranks, step = gridDim.x / (unsigned)ranks;
-  if (MODE == kRowPolicy) {
-    grid_dep_wait();
-    if (status_bad(a.p.hdr)) return;
-  }
-  const int64_t end = MODE == kRowPolicy ? min(a.rows, (int64_t)__ldg(a.p.cu + a.p.ndoc)) : a.rows;
-  uint4* const ring = s_ring + tid;
-  const float c = a.scale * kLog2e;
-  const uint64_t c2 = f2_pack(c, c);
+// A row's whole vectors start at its first 16-byte border, the thread's own ones at
+// `vec` of them, kRingThreads apart, while `left` > 0 of the block's slice; the elements
+// before and behind the vectors are rank 0's first threads'.
+template <typename T>
+struct Row {
+  const T* x;
+  int head, nvec, vec, left;
+};
 
-  // A row's whole vectors start at its first 16-byte border, the thread's own ones at
-  // `first_vec` of them, kRingThreads apart, while `left` > 0 of the block's slice; the
-  // elements before and behind the vectors are rank 0's first threads'.
-  struct Row {
-    const T* x;
-    int head, nvec, first_vec, left;
-  };
-  auto row_of = [&](int64_t t) {
-    Row r;
-    r.x = reinterpret_cast<const T*>(a.logits) + t * a.row_stride;
-    r.head = min((int)((16 - (reinterpret_cast<uintptr_t>(r.x) & 15)) & 15) / (int)sizeof(T), a.vocab);
-    r.nvec = (a.vocab - r.head) / N;
-    const int per = (r.nvec + ranks - 1) / ranks;
-    r.first_vec = rank * per + tid;
-    r.left = min(rank * per + per, r.nvec) - r.first_vec;
-    return r;
-  };
-  auto store = [&](T* dx, bool whole, const float (&o)[N]) {
-    if (whole) {
-      st_once(dx, Vec<T>::pack(o));
-    } else {
+template <typename T>
+__device__ __forceinline__ Row<T> row_of(const RowArgs& a, int64_t t, int rank, int log_ranks) {
+  constexpr int N = Vec<T>::N;
+  Row<T> r;
+  r.x = reinterpret_cast<const T*>(a.logits) + t * a.row_stride;
+  r.head = min((int)((16 - (reinterpret_cast<uintptr_t>(r.x) & 15)) & 15) / (int)sizeof(T), a.vocab);
+  r.nvec = (a.vocab - r.head) / N;
+  const int per = (r.nvec + (1 << log_ranks) - 1) >> log_ranks;
+  r.vec = rank * per + (int)threadIdx.x;
+  r.left = min(rank * per + per, r.nvec) - r.vec;
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* dx, bool whole, const float (&o)[Vec<T>::N]) {
+  if (whole) {
+    st_once(dx, Vec<T>::pack(o));
+  } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) st_out(dx + i, o[i]);
-    }
-  };
-  auto gradient_row = [&](int64_t t, const T* x, bool& whole) {
-    T* const dx = reinterpret_cast<T*>(a.dlogits) + t * a.out_stride;
-    whole = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
-    return dx;
-  };
-  // a row without a score: zeros
-  auto skip = [&](int64_t t) {
+    for (int i = 0; i < Vec<T>::N; ++i) st_out(dx + i, o[i]);
+  }
+}
+
+// Where row t's gradient goes; whole: its vectors are vectors there as well.
+template <typename T>
+__device__ __forceinline__ T* gradient_row(const RowArgs& a, int64_t t, const T* x, bool& whole) {
+  T* const dx = reinterpret_cast<T*>(a.dlogits) + t * a.out_stride;
+  whole = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
+  return dx;
+}
+
+// The scored rows of a block (rows first, first + step, ...), in order; the rows passed
+// over get their zeros on the way.  A warp's lanes hold 32 targets, the next 32 on their
+// way; all warps of a block walk alike.
+template <typename T, RowMode MODE>
+struct RowWalk {
+  const RowArgs& a;
+  const int rank, log_ranks;
+  const int64_t first, step, end;
+  int64_t base = 0;
+  int y32, y_next, at = 0;                           // at: rows of the 32 that are done with
+  uint32_t scored;
+
+  __device__ __forceinline__ RowWalk(const RowArgs& a, int rank, int log_ranks)
+      : a(a), rank(rank), log_ranks(log_ranks), first(blockIdx.x >> log_ranks),
+        step(gridDim.x >> log_ranks),
+        end(MODE == kRowPolicy ? min(a.rows, (int64_t)__ldg(a.p.cu + a.p.ndoc)) : a.rows) {
+    y32 = target(threadIdx.x & 31);
+    y_next = target(32 + (threadIdx.x & 31));
+    scored = __ballot_sync(0xffffffffu, y32 >= 0);
+  }
+  __device__ __forceinline__ int target(int64_t i) const {
+    const int64_t t = first + i * step;
+    return t < end ? __ldg(a.targets + t) : -1;
+  }
+  __device__ __forceinline__ void skip(int64_t t) const {
+    const int tid = threadIdx.x;
     if constexpr (MODE == kRowPolicy) {
-      const Row r = row_of(t);
+      constexpr int N = Vec<T>::N;
+      const Row<T> r = row_of<T>(a, t, rank, log_ranks);
       bool whole;
-      T* const dx = gradient_row(t, r.x, whole);
+      T* const dx = gradient_row<T>(a, t, r.x, whole);
       const float zero[N] = {};
       for (int i = 0; i < r.left; i += kRingThreads)
-        store(dx + r.head + (int64_t)(r.first_vec + i) * N, whole, zero);
+        store_vec<T>(dx + r.head + (int64_t)(r.vec + i) * N, whole, zero);
       if (rank == 0 && tid < a.vocab - r.nvec * N) st_out(dx + (tid < r.head ? tid : r.nvec * N + tid), 0.f);
     }
     if (rank == 0 && tid == 0) {
@@ -328,28 +342,17 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       if (MODE == kRowPolicy)
         for (int i = 0; i < 3; ++i) a.p.terms[i * a.rows + t] = 0.f;
     }
-  };
-
-  // The block's rows in order, 32 targets at a time in a warp's lanes, the next 32 on
-  // their way.
-  auto target = [&](int64_t i) {
-    const int64_t t = first + i * step;
-    return t < end ? __ldg(a.targets + t) : -1;
-  };
-  int64_t base = 0;
-  int y32 = target(lane), y_next = target(32 + lane);
-  uint32_t left = __ballot_sync(0xffffffffu, y32 >= 0);
-  int at = 0;                                        // rows of the 32 that are done with
-  auto next = [&](int64_t& t, int& y) {
+  }
+  __device__ __forceinline__ bool next(int64_t& t, int& y) {
     for (;;) {
-      const int bit = left ? __ffs(left) - 1 : 32;
+      const int bit = scored ? __ffs(scored) - 1 : 32;
       for (; at < bit; ++at) {
         const int64_t u = first + (base + at) * step;
         if (u >= a.rows) return false;
         skip(u);
       }
       if (bit < 32) {
-        left &= left - 1;
+        scored &= scored - 1;
         at = bit + 1;
         t = first + (base + bit) * step;
         y = __shfl_sync(0xffffffffu, y32, bit);
@@ -357,64 +360,195 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       }
       base += 32;
       y32 = y_next;
-      y_next = target(base + 32 + lane);
-      left = __ballot_sync(0xffffffffu, y32 >= 0);
+      y_next = target(base + 32 + (threadIdx.x & 31));
+      scored = __ballot_sync(0xffffffffu, y32 >= 0);
       at = 0;
     }
-  };
-  int queued = 0, taken = 0, ahead_left = 0;
-  const uint4* ahead = nullptr;                      // the thread's first vector of the row ahead
+  }
+};
+
+// The copies: `row` is the thread's first vector of the row ahead.  The rows on their way
+// wait in a queue of every warp's own.
+template <typename T, RowMode MODE>
+struct RowCopies {
+  RowWalk<T, MODE> walk;
+  uint4* const ring;                                 // the thread's first place
+  int2* const queue;                                 // the warp's [16]
+  const uint4* row = nullptr;
+  int left = 0, queued = 0;
   bool more = true;
-  auto next_row = [&] {
+
+  __device__ __forceinline__ RowCopies(const RowArgs& a, int rank, int log_ranks, uint4* ring, int2* queue)
+      : walk(a, rank, log_ranks), ring(ring), queue(queue) {}
+  __device__ __forceinline__ void next_row() {
     int64_t t;
     int y;
-    more = more && next(t, y);
-    ahead_left = 0;
+    more = more && walk.next(t, y);
+    left = 0;
     if (!more) return;
-    const Row r = row_of(t);
-    ahead = reinterpret_cast<const uint4*>(r.x + r.head) + r.first_vec;
-    ahead_left = r.left;
-    if (lane == 0) s_queue[warp][queued & 7] = make_int2((int)t, y);
+    const Row<T> r = row_of<T>(walk.a, t, walk.rank, walk.log_ranks);
+    row = reinterpret_cast<const uint4*>(r.x + r.head) + r.vec;
+    left = r.left;
+    if ((threadIdx.x & 31) == 0) queue[queued & 15] = make_int2((int)t, y);
     ++queued;
-  };
-  // chunk ch of the row ahead; where the row has no vector the ring holds -infinity
-  auto copy_chunk = [&](int slot, int ch) {
-    if (more) {
+  }
+  // vector i of the row ahead; where it has none the place holds -infinity
+  __device__ __forceinline__ void copy(int slot, int i) {
+    if (!more) return;
+    uint4* const to = ring + slot * kRingThreads;
+    if (i * kRingThreads < left) copy16(to, row + i * kRingThreads);
+    else *to = make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
+  }
+};
+
+// A thread's part of a row's sum, and the logit of the row's target if it is the thread's.
+template <typename T>
+struct RowSum {
+  float m = -INFINITY, s = 0.f;
+
+  // G vectors more
+  template <int G>
+  __device__ __forceinline__ void add(const uint4 (&u)[G], float c, uint64_t c2) {
+    float top = Raw<T>::top(u[0]);
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        uint4* const to = ring + (slot * kChunk + i) * kRingThreads;
-        const int v = (ch * kChunk + i) * kRingThreads;
-        if (v < ahead_left) copy16(smem_u32(to), ahead + v);
-        else *to = make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
-      }
-    }
+    for (int i = 1; i < G; ++i) top = fmaxf(top, Raw<T>::top(u[i]));
+    const float m1 = fmaxf(m, top * c), n1 = m1 == -INFINITY ? 0.f : -m1;
+    const uint64_t n2 = f2_pack(n1, n1);
+    uint64_t acc[2] = {f2_pack(s * ex2(m + n1), 0.f), 0};
+    m = m1;
+#pragma unroll
+    for (int i = 0; i < G; ++i) acc[i & 1] = add_exps<T>(u[i], c2, n2, acc[i & 1]);
+    float s1;
+    f2_unpack(f2_add(acc[0], acc[1]), s, s1);
+    s += s1;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float element(const uint4& u, int k) {
+  float e[Vec<T>::N], x = 0.f;
+  Vec<T>::unpack(u, e);
+#pragma unroll
+  for (int j = 0; j < Vec<T>::N; ++j) x = j == k ? e[j] : x;
+  return x;
+}
+
+// Scores alone: a row a block, in groups of kGroup vectors of a thread.
+constexpr int kGroup = 4, kGroups = kSlots / kGroup;
+template <typename T>
+__global__ void __launch_bounds__(kRingThreads, 2) score_ring_kernel(const __grid_constant__ RowArgs a,
+                                                                     const int groups) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ __align__(16) uint4 s_ring[];
+  __shared__ float2 s_part[2][kRingWarps];
+  __shared__ float s_target[2];
+  __shared__ int2 s_queue[kRingWarps][16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c = a.scale * kLog2e;
+  const uint64_t c2 = f2_pack(c, c);
+  RowCopies<T, kRowForward> ahead(a, 0, 0, s_ring + tid, s_queue[warp]);
+  int g_ahead = 0;
+  auto copy_group = [&](int slot) {
+    if (g_ahead == 0) ahead.next_row();
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) ahead.copy(slot + i, g_ahead * kGroup + i);
     copy_commit();
+    g_ahead = g_ahead + 1 == groups ? 0 : g_ahead + 1;
   };
-  int ch_ahead = 0;
-  for (int i = 0; i < kRing; ++i) {
-    if (ch_ahead == 0) next_row();
-    copy_chunk(i, ch_ahead);
-    ch_ahead = ch_ahead + 1 == chunks ? 0 : ch_ahead + 1;
+  for (int i = 0; i < kGroups; ++i) copy_group(i * kGroup);
+  int slot = 0;
+  for (int taken = 0; taken < ahead.queued; ++taken) {
+    __syncwarp();
+    const int2 item = s_queue[warp][taken & 15];
+    __syncwarp();
+    const int64_t t = item.x;
+    const int y = item.y, par = taken & 1;
+    const Row<T> r = row_of<T>(a, t, 0, 0);
+    const bool extra = tid < a.vocab - r.nvec * N;
+    const int ecol = tid < r.head ? tid : r.nvec * N + tid;
+    const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
+    // the target's vector among the thread's, if it is one of them, and where in it
+    const int dist = (y < r.head ? -1 : (y - r.head) / N) - tid;
+    const int mine = dist >= 0 && dist < r.left && dist % kRingThreads == 0 ? dist / kRingThreads : -1;
+    RowSum<T> sum;
+    for (int g = 0; g < groups; ++g) {
+      copy_wait<kGroups - 1>();
+      uint4 u[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        u[i] = ahead.ring[(slot + i) * kRingThreads];
+        if (mine == g * kGroup + i) s_target[par] = element<T>(u[i], (y - r.head) & (N - 1));
+      }
+      sum.add(u, c, c2);
+      copy_group(slot);
+      slot = slot + kGroup == kSlots ? 0 : slot + kGroup;
+    }
+    float m = sum.m, s = sum.s;
+    if (extra) {
+      join(m, s, xe * c, xe == -INFINITY ? 0.f : 1.f);
+      if (ecol == y) s_target[par] = xe;
+    }
+    if (tid == 0 && y >= a.vocab) s_target[par] = NAN;
+    join_warp(m, s);
+    // (two sets of states in turn: a warp that writes the next row's but one has passed the
+    // next row's barrier, and so has warp 0, behind reading this row's)
+    if (lane == 0) s_part[par][warp] = make_float2(m, s);
+    __syncthreads();
+    if (warp != 0) continue;
+    const float2 part = lane < kRingWarps ? s_part[par][lane] : make_float2(-INFINITY, 0.f);
+    m = part.x;
+    s = part.y;
+    join_warp(m, s);
+    const float rest2 = log2f(s);
+    float logp = (fmaf(s_target[par], c, -m) - rest2) * kLn2;
+    if (logp > 0.f) logp = 0.f;      // (by its rounding)
+    if (lane == 0) {
+      a.logp[t] = logp;
+      if (a.lse) a.lse[t] = (m + rest2) * kLn2;
+    }
+  }
+}
+
+// The policy loss: a cluster of blocks a row, SLICE vectors of a thread, which stay in
+// their places of the ring until the gradient has been taken from them.
+template <typename T, int SLICE>
+__global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __grid_constant__ RowArgs a,
+                                                                      const int log_ranks) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ __align__(16) uint4 s_ring[];
+  __shared__ float2 s_part[2][kMaxRanks * kRingWarps];
+  __shared__ float2 s_target[2];                     // x: the target's logit
+  __shared__ int2 s_queue[kRingWarps][16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ranks = 1 << log_ranks;
+  const int rank = (int)(blockIdx.x & (unsigned)(ranks - 1));
+  grid_dep_wait();
+  if (status_bad(a.p.hdr)) return;
+  const float c = a.scale * kLog2e;
+  const uint64_t c2 = f2_pack(c, c);
+  RowCopies<T, kRowPolicy> ahead(a, rank, log_ranks, s_ring + tid, s_queue[warp]);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    if (i % SLICE == 0) ahead.next_row();
+    ahead.copy(i, i % SLICE);
+    copy_commit();
   }
   if (ranks > 1) {                                   // (every block of the cluster runs)
     cluster_arrive();
     cluster_wait();
   }
-  int slot = 0;
-  for (; taken < queued; ++taken) {
+  int slot0 = 0;                                     // the row's first place
+  for (int taken = 0; taken < ahead.queued; ++taken) {
     __syncwarp();
-    const int2 item = s_queue[warp][taken & 7];
+    const int2 item = s_queue[warp][taken & 15];
     __syncwarp();
     const int64_t t = item.x;
     const int y = item.y, par = taken & 1;
-    const Row r = row_of(t);
-    const int rest = a.vocab - r.nvec * N;
-    const bool extra = rank == 0 && tid < rest;
+    const Row<T> r = row_of<T>(a, t, rank, log_ranks);
+    const bool extra = rank == 0 && tid < a.vocab - r.nvec * N;
     const int ecol = tid < r.head ? tid : r.nvec * N + tid;
     const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
-    // the thread's vector with the target (its number in the thread's), and where in it
-    const int ydist = (y < r.head ? -1 : (y - r.head) / N) - r.first_vec;
-    const int mine = ydist >= 0 && ydist < r.left && ydist % kRingThreads == 0 ? ydist / kRingThreads : -1;
+    const int dist = (y < r.head ? -1 : (y - r.head) / N) - r.vec;
+    const int mine = dist >= 0 && dist < r.left && dist % kRingThreads == 0 ? dist / kRingThreads : -1;
     const int yi = (y - r.head) & (N - 1);
     auto publish = [&](float x) {
       if (ranks > 1) {
@@ -423,64 +557,46 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
         s_target[par].x = x;
       }
     };
-    uint4 reg[NCH > 0 ? NCH * kChunk : kChunk];
-    float m = -INFINITY, s = 0.f;
-    auto take = [&](int ch, uint4* u) {
-      copy_wait<kRing - 1>();
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        u[i] = ring[(slot * kChunk + i) * kRingThreads];
-        top = fmaxf(top, Raw<T>::top(u[i]));
-        if (mine == ch * kChunk + i) {
-          float e[N], xy = 0.f;
-          Vec<T>::unpack(u[i], e);
-#pragma unroll
-          for (int j = 0; j < N; ++j) xy = j == yi ? e[j] : xy;
-          publish(xy);
-        }
-      }
-      const float m1 = fmaxf(m, top * c), n1 = m1 == -INFINITY ? 0.f : -m1;
-      const uint64_t n2 = f2_pack(n1, n1);
-      uint64_t acc[2] = {f2_pack(s * ex2(m + n1), 0.f), 0};
-      m = m1;
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) acc[i & 1] = add_exps<T>(u[i], c2, n2, acc[i & 1]);
-      float s1;
-      f2_unpack(f2_add(acc[0], acc[1]), s, s1);
-      s += s1;
+    auto place = [&](int i) {
+      const int p = slot0 + i;
+      return p >= kSlots ? p - kSlots : p;
     };
-    auto advance = [&] { slot = slot + 1 == kRing ? 0 : slot + 1; };
-    if constexpr (NCH > 0) {
+    RowSum<T> sum;
+    constexpr int G = SLICE % 2 == 0 ? 2 : 1;
+    // (kSlots - 1 - i groups are behind vector i of the row)
+    auto add = [&](int i) {
+      uint4 u[G];
 #pragma unroll
-      for (int ch = 0; ch < NCH; ++ch) {
-        take(ch, reg + ch * kChunk);
-        if ((ch + kRing) % NCH == 0) next_row();
-        copy_chunk(slot, (ch + kRing) % NCH);
-        advance();
+      for (int j = 0; j < G; ++j) {
+        u[j] = ahead.ring[place(i + j) * kRingThreads];
+        if (mine == i + j) publish(element<T>(u[j], yi));
       }
+      sum.add(u, c, c2);
+    };
+#define NSP_WAIT_ADD(i)                          \
+  if constexpr ((i) < SLICE) {                   \
+    copy_wait<kSlots - (i) - G>();               \
+    add(i);                                      \
+  }
+    if constexpr (G == 2) {
+      NSP_WAIT_ADD(0) NSP_WAIT_ADD(2) NSP_WAIT_ADD(4) NSP_WAIT_ADD(6)
     } else {
-      for (int ch = 0; ch < chunks; ++ch) {
-        take(ch, reg);
-        if (ch_ahead == 0) next_row();
-        copy_chunk(slot, ch_ahead);
-        ch_ahead = ch_ahead + 1 == chunks ? 0 : ch_ahead + 1;
-        advance();
-      }
+      NSP_WAIT_ADD(0) NSP_WAIT_ADD(1) NSP_WAIT_ADD(2) NSP_WAIT_ADD(3)
+      NSP_WAIT_ADD(4) NSP_WAIT_ADD(5) NSP_WAIT_ADD(6) NSP_WAIT_ADD(7)
     }
-    PolicyScalars sc = {};
-    if constexpr (MODE == kRowPolicy) {
-      const float2 w = __ldg(a.p.row_scalars + t);
-      sc = {w.x, w.y, __ldg(a.p.old_logp + t), a.p.ref_logp != nullptr ? __ldg(a.p.ref_logp + t) : 0.f};
-    }
+#undef NSP_WAIT_ADD
+    const float2 wa = __ldg(a.p.row_scalars + t);
+    const PolicyScalars sc = {wa.x, wa.y, __ldg(a.p.old_logp + t),
+                              a.p.ref_logp != nullptr ? __ldg(a.p.ref_logp + t) : 0.f};
+    float m = sum.m, s = sum.s;
     if (extra) {
-      join(m, s, xe * c, isinf(xe) && xe < 0.f ? 0.f : 1.f);
+      join(m, s, xe * c, xe == -INFINITY ? 0.f : 1.f);
       if (ecol == y) publish(xe);
     }
     if (tid == 0 && rank == 0 && y >= a.vocab) publish(NAN);
     join_warp(m, s);
-    // (two sets of states in turn: a block that writes the next row's has seen every block
-    // behind this row's barrier, and so behind reading the last row's)
+    // (two sets of states in turn: a block that writes the next row's but one has passed the
+    // next row's barrier, and so has every block of the cluster, behind reading this row's)
     if (ranks > 1) {
       if (lane < ranks) st_peer(&s_part[par][rank * kRingWarps + warp], lane, make_float2(m, s));
       __syncwarp();
@@ -490,41 +606,32 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
       if (lane == 0) s_part[par][warp] = make_float2(m, s);
       __syncthreads();
     }
-    if (MODE == kRowForward && warp != 0) continue;
     m = -INFINITY;
     s = 0.f;
-    if (lane < ranks * kRingWarps) {
-      m = s_part[par][lane].x;
-      s = s_part[par][lane].y;
-    }
-    for (int i = lane + 32; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
+    for (int i = lane; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
     join_warp(m, s);
     const float rest2 = log2f(s);
     float logp = (fmaf(s_target[par].x, c, -m) - rest2) * kLn2;
     if (logp > 0.f) logp = 0.f;      // (by its rounding)
-    const bool writes = rank == 0 && tid == 0;
-    if (writes) {
+    const PolicyRow pr = policy_row(a.p, sc, logp);
+    if (rank == 0 && tid == 0) {
       if (a.logp) a.logp[t] = logp;
-      if (a.lse) a.lse[t] = (m + rest2) * kLn2;
+      a.p.terms[t] = pr.surrogate;
+      a.p.terms[a.rows + t] = pr.kl;
+      a.p.terms[2 * a.rows + t] = pr.clipped;
     }
-    if constexpr (MODE == kRowPolicy) {
-      const PolicyRow pr = policy_row(a.p, sc, logp);
-      if (writes) {
-        a.p.terms[t] = pr.surrogate;
-        a.p.terms[a.rows + t] = pr.kl;
-        a.p.terms[2 * a.rows + t] = pr.clipped;
-      }
-      const float g = y < a.vocab ? pr.grad : NAN;
-      const float sg = a.scale * g, f = -sg / s, n = m == -INFINITY ? 0.f : -m;
-      const uint64_t n2 = f2_pack(n, n), ff = f2_pack(f, f);
-      bool whole;
-      T* const dx = gradient_row(t, r.x, whole);
-      T* const out = dx + r.head + (int64_t)r.first_vec * N;
+    const float sg = y < a.vocab ? a.scale * pr.grad : NAN;
+    const float f = -sg / s, n = m == -INFINITY ? 0.f : -m;
+    const uint64_t n2 = f2_pack(n, n), ff = f2_pack(f, f);
+    bool whole;
+    T* const dx = gradient_row<T>(a, t, r.x, whole);
+    T* const out = dx + r.head + (int64_t)r.vec * N;
 #pragma unroll
-      for (int i = 0; i < NCH * kChunk; ++i) {
-        if (i * kRingThreads >= r.left) break;
+    for (int i = 0; i < SLICE; ++i) {
+      if (i * kRingThreads < r.left) {
+        const uint4 u = ahead.ring[place(i) * kRingThreads];
         float o[N];
-        Vec<T>::unpack(reg[i], o);
+        Vec<T>::unpack(u, o);
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
           float p, q;
@@ -535,60 +642,76 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < N; ++j) o[j] += j == yi ? sg : 0.f;
         }
-        store(out + i * kRingThreads * N, whole, o);
+        store_vec<T>(out + i * kRingThreads * N, whole, o);
       }
-      if (extra) st_out(dx + ecol, ex2(fmaf(xe, c, n)) * f + (ecol == y ? sg : 0.f));
+      // the place takes the vector kSlots further on
+      if ((kSlots + i) % SLICE == 0) ahead.next_row();
+      ahead.copy(place(i), (kSlots + i) % SLICE);
+      copy_commit();
     }
+    if (extra) st_out(dx + ecol, ex2(fmaf(xe, c, n)) * f + (ecol == y ? sg : 0.f));
+    slot0 = place(SLICE);
   }
 }
 
-template <typename T, RowMode MODE, int NCH>
-cudaError_t go_ring(const RowArgs& a, int ranks, int chunks, cudaStream_t s) {
+// Dynamic shared memory of a ring kernel, allowed once a device.
+template <typename K>
+cudaError_t allow_ring(K kern, bool (&allowed)[64], int& dev) {
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && allowed[dev])) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e == cudaSuccess && dev < 64) allowed[dev] = true;
+  return e;
+}
+
+template <typename T>
+cudaError_t go_score_ring(const RowArgs& a, cudaStream_t s) {
   static bool allowed[64] = {};
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_ring(score_ring_kernel<T>, allowed, dev);
   if (e != cudaSuccess) return e;
-  auto kern = ring_kernel<T, MODE, NCH>;
-  if (dev >= 64 || !allowed[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) allowed[dev] = true;
-  }
+  const int64_t nvec = std::max(1, a.vocab / Vec<T>::N);
+  const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)num_sms() * 2);
+  score_ring_kernel<T><<<(unsigned)blocks, kRingThreads, kRingBytes, s>>>(
+      a, (int)ceil_div(nvec, kGroup * kRingThreads));
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int SLICE>
+cudaError_t go_policy_ring(const RowArgs& a, int log_ranks, cudaStream_t s) {
+  static bool allowed[64] = {};
+  static int resident[64][4] = {};
+  auto kern = policy_ring_kernel<T, SLICE>;
+  int dev = 0;
+  cudaError_t e = allow_ring(kern, allowed, dev);
+  if (e != cudaSuccess) return e;
+  const int ranks = 1 << log_ranks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(num_sms() / ranks * ranks));
+  cfg.gridDim = dim3((unsigned)(num_sms() * 2 / ranks * ranks));
   cfg.blockDim = dim3(kRingThreads);
   cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (ranks > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = (unsigned)ranks;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-    // the clusters that run at once: one that had to wait for others would double the time
-    static int resident[64][kMaxRanks + 1] = {};
-    int fit = dev < 64 ? resident[dev][ranks] : 0;
-    if (fit == 0) {
-      cfg.attrs = attr;
-      cfg.numAttrs = n;
-      e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
-      if (e != cudaSuccess) return e;
-      if (fit < 1) return cudaErrorInvalidConfiguration;
-      if (dev < 64) resident[dev][ranks] = fit;
-    }
-    cfg.gridDim.x = (unsigned)(std::min<int64_t>(fit, num_sms() / ranks) * ranks);
-  }
-  if (a.rows * ranks < cfg.gridDim.x) cfg.gridDim.x = (unsigned)(a.rows * ranks);
-  if (MODE == kRowPolicy) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = n;
+  // the clusters that run at once: one that had to wait for others would double the time
+  int fit = dev < 64 ? resident[dev][log_ranks] : 0;
+  if (fit == 0) {
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (fit < 1) return cudaErrorInvalidConfiguration;
+    if (dev < 64) resident[dev][log_ranks] = fit;
+  }
+  cfg.gridDim.x = (unsigned)(std::min<int64_t>(std::min<int64_t>(fit, num_sms() * 2 / ranks), a.rows) * ranks);
+  cfg.numAttrs = 2;
   count_launches(1);
-  return cudaLaunchKernelEx(&cfg, kern, a, ranks, chunks);
+  return cudaLaunchKernelEx(&cfg, kern, a, log_ranks);
 }
 
 template <typename T, RowMode MODE, int THREADS, int VPT>
@@ -613,23 +736,20 @@ cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
   if (nvec <= 128) return go<T, MODE, 128, 1>(a, 1, s);
   if (nvec <= 256) return go<T, MODE, 128, 2>(a, 1, s);
   if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
-  constexpr int kHeld = 4 * kChunk * kRingThreads;   // vectors of a block's registers
-  if constexpr (MODE != kRowBackward) {
-    int r = 1;
-    if (MODE == kRowPolicy)
-      while (r < kMaxRanks && nvec > (int64_t)r * kHeld) r *= 2;
-    const int chunks = (int)ceil_div(ceil_div(nvec, r), kChunk * kRingThreads);
-    if (a.rows * r >= (int64_t)num_sms() * 4 && (MODE == kRowForward || chunks <= 4)) {
-      if constexpr (MODE == kRowForward) {
-        return go_ring<T, MODE, 0>(a, 1, chunks, s);
-      } else {
-        const cudaError_t e = launch_loss_rows(a, s);
-        if (e != cudaSuccess) return e;
-        if (chunks == 1) return go_ring<T, MODE, 1>(a, r, chunks, s);
-        if (chunks == 2) return go_ring<T, MODE, 2>(a, r, chunks, s);
-        if (chunks == 3) return go_ring<T, MODE, 3>(a, r, chunks, s);
-        return go_ring<T, MODE, 4>(a, r, chunks, s);
-      }
+  if constexpr (MODE == kRowForward) {
+    if (a.rows >= (int64_t)num_sms() * 4) return go_score_ring<T>(a, s);
+  }
+  if constexpr (MODE == kRowPolicy) {
+    int log_ranks = 0;
+    while (log_ranks < 3 && nvec > ((int64_t)kMaxSlice * kRingThreads << log_ranks)) ++log_ranks;
+    const int64_t slice = ceil_div(ceil_div(nvec, 1 << log_ranks), kRingThreads);
+    if ((a.rows << log_ranks) >= (int64_t)num_sms() * 4 && slice <= kMaxSlice) {
+      const cudaError_t e = launch_loss_rows(a, s);
+      if (e != cudaSuccess) return e;
+      if (slice <= 2) return go_policy_ring<T, 2>(a, log_ranks, s);
+      if (slice <= 4) return go_policy_ring<T, 4>(a, log_ranks, s);
+      if (slice <= 6) return go_policy_ring<T, 6>(a, log_ranks, s);
+      return go_policy_ring<T, 8>(a, log_ranks, s);
     }
   }
   int ranks = 1;
