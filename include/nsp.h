@@ -786,6 +786,7 @@ int32_t nsp_qk_norm_rope_bwd(const nsp_qk_tensor_t* tensors, int32_t n, const in
  *     not read, whatever it holds, its logp and lse are 0.  A target at or past
  *     vocab makes its logp NaN.  scale > 0: the inverse of a sampling temperature.
  *   logp, lse: device float32 [rows]; lse may be NULL.
+ *   workspace: nsp_token_logp_workspace_size(rows) bytes.
  * Logits of minus infinity have probability zero (a row of nothing else, a NaN or
  * a plus infinity in a row give NaN).  Statistics in float32.
  * The backward writes
@@ -799,9 +800,11 @@ int32_t nsp_qk_norm_rope_bwd(const nsp_qk_tensor_t* tensors, int32_t n, const in
  * the same distance from a 16-byte border, row by row, are several times faster.
  * Any other overlap of an output with another array is NSP_ERR_INVALID.
  * ---------------------------------------------------------------------- */
+size_t nsp_token_logp_workspace_size(int64_t rows);
+
 int32_t nsp_token_logp_fwd(const void* logits, int64_t row_stride, const int32_t* targets, int64_t rows,
                            int32_t vocab, float scale, int32_t io_dtype, float* logp, float* lse,
-                           nsp_stream_t stream);
+                           void* workspace, size_t workspace_bytes, nsp_stream_t stream);
 
 int32_t nsp_token_logp_bwd(const void* logits, int64_t row_stride, const int32_t* targets,
                            const float* lse, const float* dlogp, int64_t rows, int32_t vocab,

@@ -230,10 +230,11 @@ LG, TG, LP, LS, DL, GO = (A + (i << 20) for i in range(1, 7))
 
 def _fwd(lib, **kw):
     """10 rows of 100 bf16 logits."""
-    a = dict(x=LG, stride=0, y=TG, rows=10, vocab=100, scale=1.0, io=nsp.NSP_BF16, logp=LP, lse=LS)
+    a = dict(x=LG, stride=0, y=TG, rows=10, vocab=100, scale=1.0, io=nsp.NSP_BF16, logp=LP, lse=LS, ws=A + (14 << 20),
+             n=4096)
     a.update(kw)
     return lib.nsp_token_logp_fwd(a["x"], a["stride"], a["y"], a["rows"], a["vocab"], a["scale"], a["io"],
-                                  a["logp"], a["lse"], None)
+                                  a["logp"], a["lse"], a["ws"], a["n"], None)
 
 
 def _bwd(lib, **kw):
@@ -257,6 +258,9 @@ def test_token_logp_refusals(lib, kw, expect):
 
 def test_token_logp_outputs(lib):
     assert _fwd(lib, logp=None) == INVALID and _fwd(lib, logp=LP + 2) == ALIGN
+    assert _fwd(lib, ws=None) == WORKSPACE and _fwd(lib, n=300) == WORKSPACE and _fwd(lib, ws=A + 8) == ALIGN
+    assert _fwd(lib, ws=LG + 1600) == INVALID and _fwd(lib, ws=LP - 320) == INVALID
+    assert lib.nsp_token_logp_workspace_size(-1) == 0 and lib.nsp_token_logp_workspace_size(0) > 0
     for kw in (dict(logp=LG + 1996), dict(lse=LP + 36), dict(lse=TG), dict(logp=LG + 200, stride=108)):
         assert _fwd(lib, **kw) == INVALID, kw
     for kw in (dict(lse=None), dict(dlogp=None), dict(out=None), dict(out=LG + 2), dict(out=LG, out_stride=108),

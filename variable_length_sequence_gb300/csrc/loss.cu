@@ -22,25 +22,27 @@ __device__ __forceinline__ int scored_before(const LossArgs& a, int64_t x) {
   return n;
 }
 
-__global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const LossArgs a) {
-  __shared__ int s_warp[32], s_bad, s_base, s_docs;
+// Walks the rows of a stream in a block's order: which are scored (below `end`, with a
+// target), how many up to the end of each 32 (bits, before), and the list of both kinds
+// (RowArgs::list); what is null is not wanted.  Returns the number of scored rows.
+struct RowScan {
+  int warp_sum[32];
+  int base;
+};
+__device__ __forceinline__ int scan_rows(const int32_t* __restrict__ targets, int64_t rows, int64_t end,
+                                         uint32_t* bits, int32_t* before, int2* list, float* logp,
+                                         float* lse, RowScan& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_bad = a.cu[0] != 0, s_base = 0, s_docs = 0;
-  __syncthreads();
-  for (int i = tid; i < a.ndoc; i += kPrepThreads)
-    if (a.cu[i] > a.cu[i + 1]) s_bad = 1;
-  __syncthreads();
-  if (tid == 0) a.hdr->status = s_bad ? NSP_ERR_INVALID : NSP_OK;
-  if (s_bad) return;
-  const int64_t end = min((int64_t)a.cu[a.ndoc], a.rows);
-  const int64_t words = (a.rows + 31) >> 5;
-  for (int64_t w0 = 0; w0 < words; w0 += kPrepThreads) {
-    // a warp's 32 words, a word a turn; lane i keeps word i
-    uint32_t mine = 0;
+  const int64_t words = (rows + 31) >> 5;
+  const int per = (int)min((int64_t)32, (words + 31) >> 5);    // words of a warp and turn
+  if (tid == 0) sh.base = 0;
+  for (int64_t w0 = 0; w0 < words; w0 += 32 * per) {
+    const int64_t first = w0 + warp * per;
+    uint32_t mine = 0;                                         // lane i keeps word i
 #pragma unroll 8
-    for (int i = 0; i < 32; ++i) {
-      const int64_t t = (w0 + warp * 32 + i) * 32 + lane;
-      const uint32_t b = __ballot_sync(0xffffffffu, t < end && __ldg(a.targets + t) >= 0);
+    for (int i = 0; i < per; ++i) {
+      const int64_t t = (first + i) * 32 + lane;
+      const uint32_t b = __ballot_sync(0xffffffffu, t < end && __ldg(targets + t) >= 0);
       if (lane == i) mine = b;
     }
     int n = __popc(mine);
@@ -49,18 +51,62 @@ __global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const LossArgs 
       const int v = __shfl_up_sync(0xffffffffu, n, o);
       if (lane >= o) n += v;
     }
-    if (lane == 31) s_warp[warp] = n;
+    if (lane == 31) sh.warp_sum[warp] = n;
     __syncthreads();
-    int base = s_base;
-    for (int w = 0; w < warp; ++w) base += s_warp[w];
-    const int64_t w = w0 + tid;
-    if (w < words) {
-      a.bits[w] = mine;
-      a.before[w] = base + n;
+    const int others = sh.warp_sum[lane];
+    n += sh.base + __reduce_add_sync(0xffffffffu, lane < warp ? others : 0);
+    if (lane < per && first + lane < words && bits != nullptr) {
+      bits[first + lane] = mine;
+      before[first + lane] = n;
     }
+    if (list != nullptr) {
+#pragma unroll 4
+      for (int i = 0; i < per; ++i) {
+        const uint32_t b = __shfl_sync(0xffffffffu, mine, i);
+        const int start = __shfl_sync(0xffffffffu, n, i) - __popc(b);
+        const int64_t t = (first + i) * 32 + lane;
+        const int k = start + __popc(b & ((1u << lane) - 1));  // scored rows before t
+        if (t >= rows) continue;
+        if (b >> lane & 1) {
+          list[k] = make_int2((int)t, __ldg(targets + t));
+        } else {
+          list[rows - 1 - (t - k)] = make_int2((int)t, -1);
+          if (logp) logp[t] = 0.f;
+          if (lse) lse[t] = 0.f;
+        }
+      }
+    }
+    const int turn = __reduce_add_sync(0xffffffffu, others);
     __syncthreads();
-    if (tid == kPrepThreads - 1) s_base = base + n;
+    if (tid == 0) sh.base += turn;
+    __syncthreads();
   }
+  __syncthreads();
+  return sh.base;
+}
+
+__global__ void __launch_bounds__(kPrepThreads) row_list_kernel(const __grid_constant__ RowArgs a) {
+  __shared__ RowScan sh;
+  grid_dep_trigger();
+  const int n = scan_rows(a.targets, a.rows, a.rows, nullptr, nullptr, a.list, a.logp, a.lse, sh);
+  if (threadIdx.x == 0) a.hdr->n_items = n;
+}
+
+__global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const LossArgs a) {
+  __shared__ RowScan sh;
+  __shared__ int s_bad, s_docs;
+  const int tid = threadIdx.x;
+  grid_dep_trigger();
+  if (tid == 0) s_bad = a.cu[0] != 0, s_docs = 0;
+  __syncthreads();
+  for (int i = tid; i < a.ndoc; i += kPrepThreads)
+    if (a.cu[i] > a.cu[i + 1]) s_bad = 1;
+  __syncthreads();
+  if (tid == 0) a.hdr->status = s_bad ? NSP_ERR_INVALID : NSP_OK;
+  if (s_bad) return;
+  const int scored = scan_rows(a.targets, a.rows, min((int64_t)a.cu[a.ndoc], a.rows), a.bits, a.before,
+                               a.list, nullptr, nullptr, sh);
+  if (tid == 0) a.hdr->n_items = scored;
   __syncthreads();
   int docs = 0;
   for (int i = tid; i < a.ndoc; i += kPrepThreads) {
@@ -70,7 +116,7 @@ __global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const LossArgs 
   }
   atomicAdd(&s_docs, docs);
   __syncthreads();
-  const float tokens = a.total > 0.f ? a.total : (float)s_base;
+  const float tokens = a.total > 0.f ? a.total : (float)scored;
   const float many = a.total > 0.f ? a.total : (float)s_docs;
   for (int i = tid; i < a.ndoc; i += kPrepThreads) {
     const float n = a.weight[i];
@@ -78,12 +124,18 @@ __global__ void __launch_bounds__(kPrepThreads) loss_prep_kernel(const LossArgs 
   }
 }
 
-// Weight and advantage of every row, for a kernel that has no time for a search a row.
+// Weight and advantage of every scored row, for a kernel that has no time for a search a
+// row; zeros of the others.
 __global__ void __launch_bounds__(kThreads) loss_rows_kernel(const __grid_constant__ RowArgs a) {
   grid_dep_wait();
   if (status_bad(a.p.hdr)) return;
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (t >= a.rows || t >= (int64_t)__ldg(a.p.cu + a.p.ndoc) || __ldg(a.targets + t) < 0) return;
+  if (t >= a.rows) return;
+  if (t >= (int64_t)__ldg(a.p.cu + a.p.ndoc) || __ldg(a.targets + t) < 0) {
+    if (a.logp) a.logp[t] = 0.f;
+    for (int i = 0; i < 3; ++i) a.p.terms[i * a.rows + t] = 0.f;
+    return;
+  }
   const int doc = doc_of(a.p.cu, a.p.ndoc, t);
   a.p.row_scalars[t] = make_float2(__ldcg(a.p.doc_weight + doc),
                                    __ldg(a.p.advantages + (a.p.per_token ? t : (int64_t)doc)));
@@ -99,6 +151,8 @@ __device__ __forceinline__ void write_stats(float* stats, float kl_coef, double 
 
 __global__ void __launch_bounds__(kThreads) policy_kernel(const __grid_constant__ PolicyArgs a) {
   __shared__ Sum2 s_sum[3][kThreads / 32];
+  grid_dep_trigger();
+  grid_dep_wait();
   if (status_bad(a.p.hdr)) return;
   const int64_t end = min((int64_t)__ldg(a.p.cu + a.p.ndoc), a.rows);
   Sum2 pg = {0.f, 0.f}, kl = pg, cut = pg;
@@ -132,12 +186,13 @@ __global__ void __launch_bounds__(kPrepThreads) policy_stats_kernel(const float*
                                                                     int64_t n, float kl_coef,
                                                                     const WsHeader* hdr, float* stats) {
   __shared__ Sum2 s_sum[3][kPrepThreads / 32];
+  grid_dep_wait();
   if (status_bad(hdr)) return;
   Sum2 sum[3] = {};
-  for (int i = 0; i < 3; ++i) {
-    for (int64_t t = threadIdx.x; t < n; t += kPrepThreads) sum[i].add(terms[i * n + t]);
-    sum[i] = block_sum<kPrepThreads / 32>(sum[i], s_sum[i]);
-  }
+#pragma unroll 4
+  for (int64_t t = threadIdx.x; t < n; t += kPrepThreads)
+    for (int i = 0; i < 3; ++i) sum[i].add(__ldcg(terms + i * n + t));
+  for (int i = 0; i < 3; ++i) sum[i] = block_sum<kPrepThreads / 32>(sum[i], s_sum[i]);
   if (threadIdx.x == 0) write_stats(stats, kl_coef, sum[0].value(), sum[1].value(), sum[2].value());
 }
 
@@ -230,12 +285,19 @@ LossWsLayout loss_ws_layout(int64_t rows, int32_t ndoc, bool logits) {
   L.weight = align_up(L.bits + 4 * words, 256);
   L.terms = align_up(L.weight + 4 * (size_t)ndoc, 256);
   L.scalars = align_up(L.terms + 12 * (logits ? (size_t)rows : (size_t)kPolicyBlocks), 256);
-  L.total = align_up(L.scalars + (logits ? 8 * (size_t)rows : 0), 256);
+  L.list = align_up(L.scalars + (logits ? 8 * (size_t)rows : 0), 256);
+  L.total = align_up(L.list + (logits ? 8 * (size_t)rows : 0), 256);
   return L;
 }
 
 cudaError_t launch_loss_prep(const LossArgs& a, cudaStream_t s) {
   loss_prep_kernel<<<1, kPrepThreads, 0, s>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_row_list(const RowArgs& a, cudaStream_t s) {
+  row_list_kernel<<<1, kPrepThreads, 0, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -251,16 +313,17 @@ static int policy_blocks(int64_t rows) {
 
 cudaError_t launch_policy(const PolicyArgs& a, cudaStream_t s) {
   const int blocks = policy_blocks(a.rows);
-  policy_kernel<<<blocks, kThreads, 0, s>>>(a);
-  policy_stats_kernel<<<1, kPrepThreads, 0, s>>>(a.p.terms, blocks, a.p.kl_coef, a.p.hdr, a.stats);
   count_launches(2);
-  return cudaGetLastError();
+  const cudaError_t e = launch_dependent(policy_kernel, dim3(blocks), dim3(kThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(policy_stats_kernel, dim3(1), dim3(kPrepThreads), 0, s,
+                          (const float*)a.p.terms, (int64_t)blocks, a.p.kl_coef, a.p.hdr, a.stats);
 }
 
 cudaError_t launch_policy_stats(const RowArgs& a, float* stats, cudaStream_t s) {
-  policy_stats_kernel<<<1, kPrepThreads, 0, s>>>(a.p.terms, a.rows, a.p.kl_coef, a.p.hdr, stats);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(policy_stats_kernel, dim3(1), dim3(kPrepThreads), 0, s,
+                          (const float*)a.p.terms, a.rows, a.p.kl_coef, a.p.hdr, stats);
 }
 
 cudaError_t launch_preference(const PreferenceArgs& a, cudaStream_t s) {

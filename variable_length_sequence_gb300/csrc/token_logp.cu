@@ -234,11 +234,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
 
 // ---- many long rows: persistent blocks behind a ring of asynchronous copies
 //
-// Two blocks of an SM walk their rows (policy: a cluster of blocks a row, a slice of it
+// A block of every SM walks its rows (policy: a cluster of blocks a row, a slice of it
 // each).  Every thread copies its own vectors of the rows ahead into its own places of
 // shared memory, kSlots of them at any time, and reads only what it copied itself, so
 // that the ring needs no barrier and no wait but the copies' own.
-constexpr int kRingThreads = 512, kRingWarps = kRingThreads / 32;
+constexpr int kRingThreads = 1024, kRingWarps = kRingThreads / 32;
 constexpr int kSlots = 12;                           // 16-byte places of a thread
 constexpr int kRingBytes = kSlots * kRingThreads * 16;
 constexpr int kMaxSlice = 8;                         // vectors of a thread in a policy row
@@ -300,78 +300,48 @@ __device__ __forceinline__ T* gradient_row(const RowArgs& a, int64_t t, const T*
   return dx;
 }
 
-// The scored rows of a block (rows first, first + step, ...), in order; the rows passed
-// over get their zeros on the way.  A warp's lanes hold 32 targets, the next 32 on their
-// way; all warps of a block walk alike.
-template <typename T, RowMode MODE>
+// A block's share of the list of scored rows: entries first, first + step, ... of it, so
+// that blocks differ by one row at most, wherever the scored ones lie in the stream.  A
+// warp's lanes hold 32 entries, the next 32 on their way; all warps of a block walk alike.
 struct RowWalk {
-  const RowArgs& a;
-  const int rank, log_ranks;
-  const int64_t first, step, end;
+  const int2* const list;
+  const int64_t first, step, count;
   int64_t base = 0;
-  int y32, y_next, at = 0;                           // at: rows of the 32 that are done with
-  uint32_t scored;
+  int2 now, then;
+  int at = 0;
 
-  __device__ __forceinline__ RowWalk(const RowArgs& a, int rank, int log_ranks)
-      : a(a), rank(rank), log_ranks(log_ranks), first(blockIdx.x >> log_ranks),
-        step(gridDim.x >> log_ranks),
-        end(MODE == kRowPolicy ? min(a.rows, (int64_t)__ldg(a.p.cu + a.p.ndoc)) : a.rows) {
-    y32 = target(threadIdx.x & 31);
-    y_next = target(32 + (threadIdx.x & 31));
-    scored = __ballot_sync(0xffffffffu, y32 >= 0);
+  __device__ __forceinline__ RowWalk(const RowArgs& a, int log_ranks)
+      : list(a.list), first(blockIdx.x >> log_ranks), step(gridDim.x >> log_ranks),
+        count(*(volatile const int32_t*)&a.hdr->n_items) {
+    now = entry(threadIdx.x & 31);
+    then = entry(32 + (threadIdx.x & 31));
   }
-  __device__ __forceinline__ int target(int64_t i) const {
-    const int64_t t = first + i * step;
-    return t < end ? __ldg(a.targets + t) : -1;
-  }
-  __device__ __forceinline__ void skip(int64_t t) const {
-    const int tid = threadIdx.x;
-    if constexpr (MODE == kRowPolicy) {
-      constexpr int N = Vec<T>::N;
-      const Row<T> r = row_of<T>(a, t, rank, log_ranks);
-      bool whole;
-      T* const dx = gradient_row<T>(a, t, r.x, whole);
-      const float zero[N] = {};
-      for (int i = 0; i < r.left; i += kRingThreads)
-        store_vec<T>(dx + r.head + (int64_t)(r.vec + i) * N, whole, zero);
-      if (rank == 0 && tid < a.vocab - r.nvec * N) st_out(dx + (tid < r.head ? tid : r.nvec * N + tid), 0.f);
-    }
-    if (rank == 0 && tid == 0) {
-      if (a.logp) a.logp[t] = 0.f;
-      if (a.lse) a.lse[t] = 0.f;
-      if (MODE == kRowPolicy)
-        for (int i = 0; i < 3; ++i) a.p.terms[i * a.rows + t] = 0.f;
-    }
+  __device__ __forceinline__ int2 entry(int64_t i) const {
+    const int64_t k = first + i * step;
+    return k < count ? __ldcg(list + k) : make_int2(-1, -1);
   }
   __device__ __forceinline__ bool next(int64_t& t, int& y) {
-    for (;;) {
-      const int bit = scored ? __ffs(scored) - 1 : 32;
-      for (; at < bit; ++at) {
-        const int64_t u = first + (base + at) * step;
-        if (u >= a.rows) return false;
-        skip(u);
-      }
-      if (bit < 32) {
-        scored &= scored - 1;
-        at = bit + 1;
-        t = first + (base + bit) * step;
-        y = __shfl_sync(0xffffffffu, y32, bit);
-        return true;
-      }
+    if (at == 32) {
       base += 32;
-      y32 = y_next;
-      y_next = target(base + 32 + (threadIdx.x & 31));
-      scored = __ballot_sync(0xffffffffu, y32 >= 0);
+      now = then;
+      then = entry(base + 32 + (threadIdx.x & 31));
       at = 0;
     }
+    t = __shfl_sync(0xffffffffu, now.x, at);
+    y = __shfl_sync(0xffffffffu, now.y, at);
+    if (t < 0) return false;
+    ++at;
+    return true;
   }
 };
 
 // The copies: `row` is the thread's first vector of the row ahead.  The rows on their way
 // wait in a queue of every warp's own.
-template <typename T, RowMode MODE>
+template <typename T>
 struct RowCopies {
-  RowWalk<T, MODE> walk;
+  const RowArgs& a;
+  const int rank, log_ranks;
+  RowWalk walk;
   uint4* const ring;                                 // the thread's first place
   int2* const queue;                                 // the warp's [16]
   const uint4* row = nullptr;
@@ -379,14 +349,14 @@ struct RowCopies {
   bool more = true;
 
   __device__ __forceinline__ RowCopies(const RowArgs& a, int rank, int log_ranks, uint4* ring, int2* queue)
-      : walk(a, rank, log_ranks), ring(ring), queue(queue) {}
+      : a(a), rank(rank), log_ranks(log_ranks), walk(a, log_ranks), ring(ring), queue(queue) {}
   __device__ __forceinline__ void next_row() {
     int64_t t;
     int y;
     more = more && walk.next(t, y);
     left = 0;
     if (!more) return;
-    const Row<T> r = row_of<T>(walk.a, t, walk.rank, walk.log_ranks);
+    const Row<T> r = row_of<T>(a, t, rank, log_ranks);
     row = reinterpret_cast<const uint4*>(r.x + r.head) + r.vec;
     left = r.left;
     if ((threadIdx.x & 31) == 0) queue[queued & 15] = make_int2((int)t, y);
@@ -436,9 +406,9 @@ __device__ __forceinline__ float element(const uint4& u, int k) {
 // Scores alone: a row a block, in groups of kGroup vectors of a thread.
 constexpr int kGroup = 4, kGroups = kSlots / kGroup;
 template <typename T>
-__global__ void __launch_bounds__(kRingThreads, 2) score_ring_kernel(const __grid_constant__ RowArgs a,
+__global__ void __launch_bounds__(kRingThreads, 1) score_ring_kernel(const __grid_constant__ RowArgs a,
                                                                      const int groups) {
-  constexpr int N = Vec<T>::N;
+  constexpr int N = Vec<T>::N, kLogN = N == 8 ? 3 : 2;
   extern __shared__ __align__(16) uint4 s_ring[];
   __shared__ float2 s_part[2][kRingWarps];
   __shared__ float s_target[2];
@@ -446,7 +416,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) score_ring_kernel(const __gri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = a.scale * kLog2e;
   const uint64_t c2 = f2_pack(c, c);
-  RowCopies<T, kRowForward> ahead(a, 0, 0, s_ring + tid, s_queue[warp]);
+  grid_dep_wait();
+  RowCopies<T> ahead(a, 0, 0, s_ring + tid, s_queue[warp]);
   int g_ahead = 0;
   auto copy_group = [&](int slot) {
     if (g_ahead == 0) ahead.next_row();
@@ -468,8 +439,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) score_ring_kernel(const __gri
     const int ecol = tid < r.head ? tid : r.nvec * N + tid;
     const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
     // the target's vector among the thread's, if it is one of them, and where in it
-    const int dist = (y < r.head ? -1 : (y - r.head) / N) - tid;
-    const int mine = dist >= 0 && dist < r.left && dist % kRingThreads == 0 ? dist / kRingThreads : -1;
+    const unsigned dist = (unsigned)((y - r.head) >> kLogN) - (unsigned)tid;
+    const int mine = y >= r.head && (int)dist < r.left && dist % kRingThreads == 0 ? (int)(dist / kRingThreads) : -1;
     RowSum<T> sum;
     for (int g = 0; g < groups; ++g) {
       copy_wait<kGroups - 1>();
@@ -512,12 +483,13 @@ __global__ void __launch_bounds__(kRingThreads, 2) score_ring_kernel(const __gri
 // The policy loss: a cluster of blocks a row, SLICE vectors of a thread, which stay in
 // their places of the ring until the gradient has been taken from them.
 template <typename T, int SLICE>
-__global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __grid_constant__ RowArgs a,
+__global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __grid_constant__ RowArgs a,
                                                                       const int log_ranks) {
-  constexpr int N = Vec<T>::N;
+  constexpr int N = Vec<T>::N, kLogN = N == 8 ? 3 : 2;
   extern __shared__ __align__(16) uint4 s_ring[];
   __shared__ float2 s_part[2][kMaxRanks * kRingWarps];
   __shared__ float2 s_target[2];                     // x: the target's logit
+  __shared__ float4 s_coef;                          // p = 2^(c x + .x), gradient .y p, .z at the target
   __shared__ int2 s_queue[kRingWarps][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ranks = 1 << log_ranks;
   const int rank = (int)(blockIdx.x & (unsigned)(ranks - 1));
@@ -525,7 +497,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __gr
   if (status_bad(a.p.hdr)) return;
   const float c = a.scale * kLog2e;
   const uint64_t c2 = f2_pack(c, c);
-  RowCopies<T, kRowPolicy> ahead(a, rank, log_ranks, s_ring + tid, s_queue[warp]);
+  RowCopies<T> ahead(a, rank, log_ranks, s_ring + tid, s_queue[warp]);
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     if (i % SLICE == 0) ahead.next_row();
@@ -536,6 +508,23 @@ __global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __gr
     cluster_arrive();
     cluster_wait();
   }
+  // The rows without a score get their zeros between the others, evenly.
+  const int64_t others = a.rows - ahead.walk.count;
+  int64_t zeroed = ahead.walk.first;
+  auto zero_rows = [&](int64_t upto) {
+    for (; zeroed < upto; zeroed += ahead.walk.step) {
+      const int64_t t = __ldcg(a.list + a.rows - 1 - zeroed).x;
+      const Row<T> r = row_of<T>(a, t, rank, log_ranks);
+      bool whole;
+      T* const dx = gradient_row<T>(a, t, r.x, whole);
+      const float zero[N] = {};
+      for (int i = 0; i < r.left; i += kRingThreads)
+        store_vec<T>(dx + r.head + (int64_t)(r.vec + i) * N, whole, zero);
+      if (rank == 0 && tid < a.vocab - r.nvec * N) st_out(dx + (tid < r.head ? tid : r.nvec * N + tid), 0.f);
+    }
+  };
+  // (others / count of them a scored row, as the entries of both kinds are spread alike)
+  const float share = ahead.walk.count > 0 ? (float)others / (float)ahead.walk.count : 0.f;
   int slot0 = 0;                                     // the row's first place
   for (int taken = 0; taken < ahead.queued; ++taken) {
     __syncwarp();
@@ -547,9 +536,14 @@ __global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __gr
     const bool extra = rank == 0 && tid < a.vocab - r.nvec * N;
     const int ecol = tid < r.head ? tid : r.nvec * N + tid;
     const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
-    const int dist = (y < r.head ? -1 : (y - r.head) / N) - r.vec;
-    const int mine = dist >= 0 && dist < r.left && dist % kRingThreads == 0 ? dist / kRingThreads : -1;
+    const unsigned dist = (unsigned)((y - r.head) >> kLogN) - (unsigned)r.vec;
+    const int mine = y >= r.head && (int)dist < r.left && dist % kRingThreads == 0 ? (int)(dist / kRingThreads) : -1;
     const int yi = (y - r.head) & (N - 1);
+    PolicyScalars sc = {};
+    if (warp == 0) {
+      const float2 w = __ldg(a.p.row_scalars + t);
+      sc = {w.x, w.y, __ldg(a.p.old_logp + t), a.p.ref_logp != nullptr ? __ldg(a.p.ref_logp + t) : 0.f};
+    }
     auto publish = [&](float x) {
       if (ranks > 1) {
         for (int k = 0; k < ranks; ++k) st_peer(&s_target[par], k, make_float2(x, 0.f));
@@ -585,9 +579,6 @@ __global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __gr
       NSP_WAIT_ADD(4) NSP_WAIT_ADD(5) NSP_WAIT_ADD(6) NSP_WAIT_ADD(7)
     }
 #undef NSP_WAIT_ADD
-    const float2 wa = __ldg(a.p.row_scalars + t);
-    const PolicyScalars sc = {wa.x, wa.y, __ldg(a.p.old_logp + t),
-                              a.p.ref_logp != nullptr ? __ldg(a.p.ref_logp + t) : 0.f};
     float m = sum.m, s = sum.s;
     if (extra) {
       join(m, s, xe * c, xe == -INFINITY ? 0.f : 1.f);
@@ -606,22 +597,29 @@ __global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __gr
       if (lane == 0) s_part[par][warp] = make_float2(m, s);
       __syncthreads();
     }
-    m = -INFINITY;
-    s = 0.f;
-    for (int i = lane; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
-    join_warp(m, s);
-    const float rest2 = log2f(s);
-    float logp = (fmaf(s_target[par].x, c, -m) - rest2) * kLn2;
-    if (logp > 0.f) logp = 0.f;      // (by its rounding)
-    const PolicyRow pr = policy_row(a.p, sc, logp);
-    if (rank == 0 && tid == 0) {
-      if (a.logp) a.logp[t] = logp;
-      a.p.terms[t] = pr.surrogate;
-      a.p.terms[a.rows + t] = pr.kl;
-      a.p.terms[2 * a.rows + t] = pr.clipped;
+    if (warp == 0) {                  // one warp for all: the others' issue slots are dear
+      m = -INFINITY;
+      s = 0.f;
+      for (int i = lane; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
+      join_warp(m, s);
+      const float rest2 = log2f(s);
+      float logp = (fmaf(s_target[par].x, c, -m) - rest2) * kLn2;
+      if (logp > 0.f) logp = 0.f;      // (by its rounding)
+      const PolicyRow pr = policy_row(a.p, sc, logp);
+      if (lane == 0) {
+        const float sg = y < a.vocab ? a.scale * pr.grad : NAN;
+        s_coef = make_float4(m == -INFINITY ? 0.f : -m, -sg / s, sg, 0.f);
+        if (rank == 0) {
+          if (a.logp) a.logp[t] = logp;
+          a.p.terms[t] = pr.surrogate;
+          a.p.terms[a.rows + t] = pr.kl;
+          a.p.terms[2 * a.rows + t] = pr.clipped;
+        }
+      }
     }
-    const float sg = y < a.vocab ? a.scale * pr.grad : NAN;
-    const float f = -sg / s, n = m == -INFINITY ? 0.f : -m;
+    __syncthreads();
+    const float4 coef = s_coef;        // (written again behind the next row's barrier)
+    const float n = coef.x, f = coef.y, sg = coef.z;
     const uint64_t n2 = f2_pack(n, n), ff = f2_pack(f, f);
     bool whole;
     T* const dx = gradient_row<T>(a, t, r.x, whole);
@@ -651,7 +649,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) policy_ring_kernel(const __gr
     }
     if (extra) st_out(dx + ecol, ex2(fmaf(xe, c, n)) * f + (ecol == y ? sg : 0.f));
     slot0 = place(SLICE);
+    zero_rows(min(others, (int64_t)(share * (float)(taken + 1) * (float)ahead.walk.step)));
   }
+  zero_rows(others);
 }
 
 // Dynamic shared memory of a ring kernel, allowed once a device.
@@ -668,14 +668,14 @@ template <typename T>
 cudaError_t go_score_ring(const RowArgs& a, cudaStream_t s) {
   static bool allowed[64] = {};
   int dev = 0;
-  const cudaError_t e = allow_ring(score_ring_kernel<T>, allowed, dev);
+  cudaError_t e = allow_ring(score_ring_kernel<T>, allowed, dev);
+  if (e == cudaSuccess) e = launch_row_list(a, s);
   if (e != cudaSuccess) return e;
   const int64_t nvec = std::max(1, a.vocab / Vec<T>::N);
-  const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)num_sms() * 2);
-  score_ring_kernel<T><<<(unsigned)blocks, kRingThreads, kRingBytes, s>>>(
-      a, (int)ceil_div(nvec, kGroup * kRingThreads));
+  const int64_t blocks = std::min<int64_t>(a.rows, num_sms());
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(score_ring_kernel<T>, dim3((unsigned)blocks), dim3(kRingThreads), kRingBytes, s, a,
+                          (int)ceil_div(nvec, kGroup * kRingThreads));
 }
 
 template <typename T, int SLICE>
@@ -688,7 +688,7 @@ cudaError_t go_policy_ring(const RowArgs& a, int log_ranks, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int ranks = 1 << log_ranks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(num_sms() * 2 / ranks * ranks));
+  cfg.gridDim = dim3((unsigned)(num_sms() / ranks * ranks));
   cfg.blockDim = dim3(kRingThreads);
   cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = s;
@@ -708,7 +708,7 @@ cudaError_t go_policy_ring(const RowArgs& a, int log_ranks, cudaStream_t s) {
     if (fit < 1) return cudaErrorInvalidConfiguration;
     if (dev < 64) resident[dev][log_ranks] = fit;
   }
-  cfg.gridDim.x = (unsigned)(std::min<int64_t>(std::min<int64_t>(fit, num_sms() * 2 / ranks), a.rows) * ranks);
+  cfg.gridDim.x = (unsigned)(std::min<int64_t>(std::min<int64_t>(fit, num_sms() / ranks), a.rows) * ranks);
   cfg.numAttrs = 2;
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, kern, a, log_ranks);
@@ -730,20 +730,34 @@ cudaError_t go(const RowArgs& a, int ranks, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, row_kernel<T, MODE, THREADS, VPT>, a, ranks);
 }
 
+// Blocks of a policy row's cluster, as a power of two, and vectors of a thread; false
+// where the ring has no room for the row.
+bool policy_slice(int64_t nvec, int& log_ranks, int64_t& slice) {
+  log_ranks = 0;
+  while (log_ranks < 3 && nvec > ((int64_t)kMaxSlice * kRingThreads << log_ranks)) ++log_ranks;
+  slice = ceil_div(ceil_div(nvec, 1 << log_ranks), kRingThreads);
+  return slice <= kMaxSlice;
+}
+
+// Many rows of more than 8 KB go through the ring.
+bool listed(const RowArgs& a, RowMode mode, int64_t nvec) {
+  if (mode == kRowBackward || nvec <= 512) return false;
+  int log_ranks = 0;
+  int64_t slice;
+  if (mode == kRowPolicy && !policy_slice(nvec, log_ranks, slice)) return false;
+  return (a.rows << log_ranks) >= (int64_t)num_sms() * 4;
+}
+
 template <typename T, RowMode MODE>
 cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
-  const int64_t nvec = std::max(1, a.vocab / (16 / (int)sizeof(T)));
-  if (nvec <= 128) return go<T, MODE, 128, 1>(a, 1, s);
-  if (nvec <= 256) return go<T, MODE, 128, 2>(a, 1, s);
-  if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
-  if constexpr (MODE == kRowForward) {
-    if (a.rows >= (int64_t)num_sms() * 4) return go_score_ring<T>(a, s);
-  }
-  if constexpr (MODE == kRowPolicy) {
-    int log_ranks = 0;
-    while (log_ranks < 3 && nvec > ((int64_t)kMaxSlice * kRingThreads << log_ranks)) ++log_ranks;
-    const int64_t slice = ceil_div(ceil_div(nvec, 1 << log_ranks), kRingThreads);
-    if ((a.rows << log_ranks) >= (int64_t)num_sms() * 4 && slice <= kMaxSlice) {
+  const int64_t nvec = std::max(1, a.vocab / Vec<T>::N);
+  if (listed(a, MODE, nvec)) {
+    if constexpr (MODE == kRowForward) {
+      return go_score_ring<T>(a, s);
+    } else if constexpr (MODE == kRowPolicy) {
+      int log_ranks;
+      int64_t slice;
+      policy_slice(nvec, log_ranks, slice);
       const cudaError_t e = launch_loss_rows(a, s);
       if (e != cudaSuccess) return e;
       if (slice <= 2) return go_policy_ring<T, 2>(a, log_ranks, s);
@@ -752,6 +766,9 @@ cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
       return go_policy_ring<T, 8>(a, log_ranks, s);
     }
   }
+  if (nvec <= 128) return go<T, MODE, 128, 1>(a, 1, s);
+  if (nvec <= 256) return go<T, MODE, 128, 2>(a, 1, s);
+  if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
   int ranks = 1;
   while (ranks < kMaxRanks && nvec > (int64_t)ranks * 4096) ranks *= 2;
   while (ranks < kMaxRanks && a.rows * ranks < (int64_t)num_sms() * 2 && nvec > (int64_t)ranks * 512) ranks *= 2;
@@ -771,6 +788,10 @@ cudaError_t launch_typed(const RowArgs& a, RowMode mode, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool rows_listed(const RowArgs& a, RowMode mode, int32_t io_dtype) {
+  return listed(a, mode, std::max(1, a.vocab / (io_dtype == NSP_BF16 ? 8 : 4)));
+}
 
 cudaError_t launch_rows(const RowArgs& a, RowMode mode, int32_t io_dtype, cudaStream_t s) {
   return io_dtype == NSP_BF16 ? launch_typed<__nv_bfloat16>(a, mode, s) : launch_typed<float>(a, mode, s);

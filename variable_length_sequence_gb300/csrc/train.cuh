@@ -60,19 +60,24 @@ struct RowArgs {
   float scale;
   float *logp, *lse;                       // forward and policy: written (may be null)
   const float *in_lse, *dlogp;             // backward
+  WsHeader* hdr;                           // forward and policy: workspace, n_items scored rows
+  int2* list;                              // [rows] row and target of the scored rows, in order;
+                                           // from the end backwards the rows not scored
   void* dlogits;
   int64_t out_stride;
   PolicyRows p;
 };
 enum RowMode { kRowForward, kRowBackward, kRowPolicy };
+// Whether launch_rows walks a list of the scored rows.
+bool rows_listed(const RowArgs& a, RowMode mode, int32_t io_dtype);
 cudaError_t launch_rows(const RowArgs& a, RowMode mode, int32_t io_dtype, cudaStream_t s);
 
 // ---- losses (loss.cu)
 // Workspace of a loss: header; per 32 rows the number of scored ones before them and
 // which of them are; each document's weight; terms or partial sums; with logits, each
-// row's weight and advantage.
+// row's weight and advantage, and the list of rows.
 struct LossWsLayout {
-  size_t before, bits, weight, terms, scalars, total;
+  size_t before, bits, weight, terms, scalars, list, total;
 };
 LossWsLayout loss_ws_layout(int64_t rows, int32_t ndoc, bool logits);
 
@@ -87,12 +92,15 @@ struct LossArgs {
   uint32_t* bits;
   int32_t* before;
   float* weight;
+  int2* list;                              // null: not wanted
 };
 // Checks cu_seqlens (status word), counts each document's scored rows and writes
 // the documents' weights.
 cudaError_t launch_loss_prep(const LossArgs& a, cudaStream_t s);
-// each scored row's weight and advantage, behind launch_loss_prep
+// each scored row's weight and advantage, and the other rows' zeros, behind launch_loss_prep
 cudaError_t launch_loss_rows(const RowArgs& a, cudaStream_t s);
+// the list of a forward's scored rows, and the other rows' zeros
+cudaError_t launch_row_list(const RowArgs& a, cudaStream_t s);
 
 struct PolicyArgs {
   const float* logp;

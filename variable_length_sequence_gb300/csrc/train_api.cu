@@ -173,6 +173,7 @@ int32_t policy_check(const nsp_policy_t* policy, const int32_t* cu, int32_t ndoc
   p.doc_weight = reinterpret_cast<float*>(ws + L.weight);
   p.terms = reinterpret_cast<float*>(ws + L.terms);
   p.row_scalars = reinterpret_cast<float2*>(ws + L.scalars);
+  l.list = logits ? reinterpret_cast<int2*>(ws + L.list) : nullptr;
   l.cu = cu; l.ndoc = ndoc; l.rows = rows;
   l.mean = policy->mean; l.total = policy->total;
   l.hdr = reinterpret_cast<WsHeader*>(ws);
@@ -235,20 +236,29 @@ int32_t nsp_qk_norm_rope_bwd(const nsp_qk_tensor_t* tensors, int32_t n, const in
 
 // ---------------------------------------------------------------- token log-probabilities
 
+size_t nsp_token_logp_workspace_size(int64_t rows) {
+  return rows < 0 || rows > kMaxTokens ? 0 : sizeof(WsHeader) + sizeof(int2) * (size_t)rows;
+}
+
 int32_t nsp_token_logp_fwd(const void* logits, int64_t row_stride, const int32_t* targets, int64_t rows,
                            int32_t vocab, float scale, int32_t io_dtype, float* logp, float* lse,
-                           nsp_stream_t stream) {
+                           void* workspace, size_t workspace_bytes, nsp_stream_t stream) {
   RowArgs a;
   const int32_t st = rows_check(logits, row_stride, targets, rows, vocab, scale, io_dtype, a);
   if (st != NSP_OK) return st;
   if (rows > 0 && !logp) return NSP_ERR_INVALID;
   if (!aligned(logp, 4) || !aligned(lse, 4)) return NSP_ERR_ALIGN;
-  const Span outs[] = {packed(logp, 1, rows * 4), packed(lse, 1, rows * 4)};
+  const size_t need = nsp_token_logp_workspace_size(rows);
+  if (!workspace || workspace_bytes < need) return NSP_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return NSP_ERR_ALIGN;
+  const Span outs[] = {packed(logp, 1, rows * 4), packed(lse, 1, rows * 4), packed(workspace, 1, (int64_t)need)};
   const Span ins[] = {logits_span(a, elem_bytes(io_dtype)), packed(targets, 1, rows * 4)};
-  if (clash(outs, 2, ins, 2)) return NSP_ERR_INVALID;
+  if (clash(outs, 3, ins, 2)) return NSP_ERR_INVALID;
   if (rows == 0) return NSP_OK;
   a.logp = logp;
   a.lse = lse;
+  a.hdr = reinterpret_cast<WsHeader*>(workspace);
+  a.list = reinterpret_cast<int2*>(reinterpret_cast<char*>(workspace) + sizeof(WsHeader));
   return status_of(launch_rows(a, kRowForward, io_dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -328,7 +338,10 @@ int32_t nsp_policy_loss_logits(const void* logits, int64_t row_stride, const int
   for (const Span& o : outs)
     if (overlap(o, in) && !(&o == &outs[2] && same_rows(in, out))) return NSP_ERR_INVALID;
   a.logp = logp;
+  a.hdr = l.hdr;
+  a.list = l.list;
   l.targets = targets;
+  if (!rows_listed(a, kRowPolicy, io_dtype)) l.list = nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_loss_prep(l, s);
   if (e == cudaSuccess && rows > 0) e = launch_rows(a, kRowPolicy, io_dtype, s);

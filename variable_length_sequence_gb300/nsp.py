@@ -92,7 +92,8 @@ _SIGNATURES = {
     "nsp_qk_norm_rope_bwd_workspace_size": (_sz, [_vp, _i32, _i64, _i32]),
     "nsp_qk_norm_rope_bwd": (_i32, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _vp, _i32,
                                     _f32, _f32, _i32, _vp, _sz, _vp]),
-    "nsp_token_logp_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _f32, _i32, _vp, _vp, _vp]),
+    "nsp_token_logp_workspace_size": (_sz, [_i64]),
+    "nsp_token_logp_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _f32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "nsp_token_logp_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _f32, _i32, _vp, _i64, _vp]),
     "nsp_policy_loss_workspace_size": (_sz, [_i64, _i32, _i32]),
     "nsp_policy_loss": (_i32, [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -1139,7 +1140,7 @@ def _logit_rows(fn, name, x, shape=None):
     return x.stride(0)
 
 
-def token_logp(logits, targets, scale=1.0, stream=None):
+def token_logp(logits, targets, scale=1.0, workspace=None, stream=None):
     """Log-probabilities of targets (int32 [T]; negative: none, the row is not read
     and gives zeros) under the rows of scale * logits [T, vocabulary] (rows any
     stride apart), and the rows' log sums of exponentials: (logp, lse), float32 [T]."""
@@ -1151,8 +1152,10 @@ def token_logp(logits, targets, scale=1.0, stream=None):
     T, V = logits.shape
     _shape(fn, "targets", targets, (T,))
     logp, lse = _new(stream, logits, (T,), torch.float32), _new(stream, logits, (T,), torch.float32)
-    st = load().nsp_token_logp_fwd(logits.data_ptr(), stride, _ptr(targets), T, V, scale, io,
-                                   _ptr(logp), _ptr(lse), _stream_of(stream, dev))
+    lib = load()
+    ws = _workspace(fn, stream, logits, lib.nsp_token_logp_workspace_size(T), workspace)
+    st = lib.nsp_token_logp_fwd(logits.data_ptr(), stride, _ptr(targets), T, V, scale, io, _ptr(logp),
+                                _ptr(lse), _ptr(ws), ws.numel(), _stream_of(stream, dev))
     _check("nsp_token_logp_fwd", st)
     return logp, lse
 
