@@ -23,7 +23,7 @@ struct PolicyScalars {
 };
 
 __device__ __forceinline__ PolicyScalars policy_scalars(const PolicyRows& p, int64_t t, int doc) {
-  return {__ldg(p.doc_weight + doc), __ldg(p.advantages + (p.per_token ? t : (int64_t)doc)),
+  return {__ldcg(p.doc_weight + doc), __ldg(p.advantages + (p.per_token ? t : (int64_t)doc)),
           __ldg(p.old_logp + t), p.ref_logp != nullptr ? __ldg(p.ref_logp + t) : 0.f};
 }
 

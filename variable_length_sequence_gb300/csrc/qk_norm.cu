@@ -6,13 +6,18 @@
 //   dx = r (u - n mean(u n)),  dw = sum over rows of n z.
 #include <algorithm>
 
+#include "tc_ptx.cuh"
 #include "train.cuh"
 
 namespace nsp {
 namespace {
 
+using namespace tc;
+
 constexpr int kThreads = 256;
+constexpr int kVecThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int64_t kL2Bytes = (int64_t)128 << 20;
 constexpr int kBwdBlocks = 304;
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -21,9 +26,11 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// The blocks of a grid that a tensor's rows are given to.
+// The blocks of a grid that a tensor's rows are given to, and the parts that a token's
+// heads are split in there.
 struct Share {
   int first[kRopeMaxTensors + 1];
+  int hsplit[kRopeMaxTensors], per[kRopeMaxTensors];
 };
 
 // One row a warp, one element (of a pair) a lane and step: any d, stride and
@@ -120,6 +127,367 @@ __global__ void __launch_bounds__(kThreads) qk_element_kernel(const __grid_const
   }
 }
 
+// ---- whole 16-byte pieces
+//
+// A team of lanes owns a token's heads (or a part of them) and computes the sines and
+// cosines of its pairs once; a lane holds U units of two 16-byte vectors of a head: both
+// halves of its pairs, or two neighbours.  The weights enter the turn's coefficients, so
+// that a pair costs two products, two FMAs and the row's factor.
+
+// The columns of a lane's unit; `second`: its second vector is there; turned: bit v, vector
+// v's pairs are rotated.
+template <int N, bool INTER>
+__device__ __forceinline__ bool unit_of(int d, int rot, int u, int& c0, int& c1, bool& second, int& turned) {
+  const int r = rot / 2 / N;
+  if (INTER || u >= r) {
+    c0 = INTER ? 2 * u * N : rot + 2 * (u - r) * N;
+    c1 = c0 + N;
+    second = c1 < d;
+    turned = INTER ? (c0 < rot ? 1 : 0) | (c1 < rot ? 2 : 0) : 0;
+    return c0 < d;
+  }
+  c0 = u * N;
+  c1 = c0 + rot / 2;
+  second = true;
+  turned = 3;
+  return true;
+}
+
+// A lane's part of a head: its units' columns, and which of their vectors there are.
+template <int N, bool INTER, int LANES, int U>
+struct Units {
+  int c0[U], c1[U], turned[U];
+  bool first[U], second[U];
+
+  __device__ __forceinline__ Units(const QkArgs& a, int lane) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      first[i] = unit_of<N, INTER>(a.d, a.rot, lane + i * LANES, c0[i], c1[i], second[i], turned[i]);
+      second[i] = second[i] && first[i];
+      if (!first[i]) turned[i] = 0;
+    }
+  }
+};
+
+// Sum over a team of LANES lanes, which meet here together.
+template <int LANES>
+__device__ __forceinline__ float team_sum(float x, uint32_t mask) {
+#pragma unroll
+  for (int o = LANES >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+  return x;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t team_mask() {
+  return LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1) << (threadIdx.x & 31 & ~(LANES - 1));
+}
+
+// A vector's values as packed pairs.
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4& u, uint64_t* x) {
+  float t[Vec<T>::N];
+  Vec<T>::unpack(u, t);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N / 2; ++i) x[i] = f2_pack(t[2 * i], t[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const uint64_t* x) {
+  float t[Vec<T>::N];
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N / 2; ++i) f2_unpack(x[i], t[2 * i], t[2 * i + 1]);
+  return Vec<T>::pack(t);
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return f2_pack(b, a);
+}
+__device__ __forceinline__ float sum2(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return a + b;
+}
+
+// Cosines and sines of a unit's pairs: halves: pair j of both vectors; neighbours: pairs j
+// of the first, N / 2 + j of the second.  Columns that are not rotated: 1 and 0.
+template <int N, bool INTER>
+__device__ __forceinline__ void turns(const QkArgs& a, const uint64_t* s_fx, int64_t pos, int u, int turned,
+                                      bool inverse, float (&c)[N], float (&s)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    c[j] = 1.f;
+    s[j] = 0.f;
+    const bool on = INTER ? (turned >> (j >= N / 2 ? 1 : 0)) & 1 : turned != 0;
+    if (on) turn(pos, s_fx[u * N + j], a.mscale, inverse, c[j], s[j]);
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load_weight(const void* w, int col, bool there, float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = 1.f;
+  if (w != nullptr && there) Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(w) + col)), x);
+}
+
+// Where a team's part of a token's heads begins; the part lies in one head group.
+struct Item {
+  int64_t t;
+  int h0, h1;
+};
+__device__ __forceinline__ Item item_of(const QkTensor& q, int64_t item, int hsplit, int per) {
+  Item m;
+  m.t = hsplit == 1 ? item : (int64_t)((uint32_t)item / (uint32_t)hsplit);
+  m.h0 = (int)(item - m.t * hsplit) * per;
+  m.h1 = min(m.h0 + per, q.heads);
+  return m;
+}
+
+template <typename T, bool INTER, int LANES, int U>
+__global__ void __launch_bounds__(kVecThreads, U == 1 ? 4 : 2) qk_vec_kernel(const __grid_constant__ QkArgs a,
+                                                                             const Share share) {
+  constexpr int N = Vec<T>::N, P = N / 2, kFlight = U == 1 ? 4 : 2, kTeams = kVecThreads / LANES;
+  __shared__ uint64_t s_fx[kQkMaxDim / 2];
+  for (int i = threadIdx.x; i < a.rot / 2; i += kVecThreads) s_fx[i] = fixed_turns(a.freqs[i]);
+  __syncthreads();
+  int k = 0;
+  while ((int)blockIdx.x >= share.first[k + 1]) ++k;
+  const QkTensor& q = a.t[k];
+  const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
+  const uint32_t mask = team_mask<LANES>();
+  const Units<N, INTER, LANES, U> un(a, lane);
+  const int hsplit = share.hsplit[k], per = share.per[k];
+  const int64_t items = a.len * hsplit;
+  const float inv_d = 1.f / (float)a.d;
+  const int64_t step = (int64_t)(share.first[k + 1] - share.first[k]) * kTeams;
+  for (int64_t item = (int64_t)(blockIdx.x - share.first[k]) * kTeams + team; item < items; item += step) {
+    const Item m = item_of(q, item, hsplit, per);
+    const T* x = reinterpret_cast<const T*>(q.x) + m.t * q.x_stride + (int64_t)m.h0 * a.d;
+    T* y = reinterpret_cast<T*>(q.y) + row_offset(m.t, m.h0, q.y_stride, q.heads, q.groups, a.len, a.d);
+    bool ready = false;
+    uint64_t ca[U][N], cb[U][N];             // [P] for the first output vector, [P] for the second
+    for (int h = m.h0; h < m.h1; h += kFlight) {
+      uint4 v[kFlight][U][2];
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) {
+        const T* const row = x + f * a.d;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          v[f][i][0] = v[f][i][1] = make_uint4(0, 0, 0, 0);
+          if (h + f < m.h1 && un.first[i]) v[f][i][0] = ld_once(row + un.c0[i]);
+          if (h + f < m.h1 && un.second[i]) v[f][i][1] = ld_once(row + un.c1[i]);
+        }
+      }
+      if (!ready) {                          // under the first loads
+        int64_t pos;
+        if (!position_of(Positions{a.positions, a.cu, a.ndoc, a.start}, m.t, pos)) break;
+        ready = true;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          float c[N], s[N], w0[N], w1[N];
+          turns<N, INTER>(a, s_fx, pos, lane + i * LANES, un.turned[i], false, c, s);
+          load_weight<T>(q.weight, un.c0[i], un.first[i], w0);
+          load_weight<T>(q.weight, un.c1[i], un.second[i], w1);
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            if constexpr (INTER) {
+              // out = (x_even, x_odd) ca + (x_odd, x_even) cb
+              ca[i][j] = f2_pack(w0[2 * j] * c[j], w0[2 * j + 1] * c[j]);
+              cb[i][j] = f2_pack(-w0[2 * j + 1] * s[j], w0[2 * j] * s[j]);
+              ca[i][P + j] = f2_pack(w1[2 * j] * c[P + j], w1[2 * j + 1] * c[P + j]);
+              cb[i][P + j] = f2_pack(-w1[2 * j + 1] * s[P + j], w1[2 * j] * s[P + j]);
+            } else {
+              // out0 = x0 ca + x1 cb, out1 = x1 ca' + x0 cb'
+              ca[i][j] = f2_pack(w0[2 * j] * c[2 * j], w0[2 * j + 1] * c[2 * j + 1]);
+              cb[i][j] = f2_pack(-w1[2 * j] * s[2 * j], -w1[2 * j + 1] * s[2 * j + 1]);
+              ca[i][P + j] = f2_pack(w1[2 * j] * c[2 * j], w1[2 * j + 1] * c[2 * j + 1]);
+              cb[i][P + j] = f2_pack(w0[2 * j] * s[2 * j], w0[2 * j + 1] * s[2 * j + 1]);
+            }
+          }
+        }
+      }
+      float r[kFlight];
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) {
+        uint64_t ss = 0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          uint64_t e[N];
+          unpack2<T>(v[f][i][0], e);
+          unpack2<T>(v[f][i][1], e + P);
+#pragma unroll
+          for (int j = 0; j < N; ++j) ss = f2_fma(e[j], e[j], ss);
+        }
+        r[f] = sum2(ss);
+      }
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) r[f] = rsqrtf(fmaf(team_sum<LANES>(r[f], mask), inv_d, a.eps));
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) {
+        if (h + f >= m.h1) break;
+        const uint64_t r2 = f2_pack(r[f], r[f]);
+        T* const row = y + f * a.d;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          uint64_t e[N], o[N];
+          unpack2<T>(v[f][i][0], e);
+          unpack2<T>(v[f][i][1], e + P);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const uint64_t other = INTER ? swap2(e[j]) : e[j < P ? j + P : j - P];
+            o[j] = f2_mul(f2_fma(other, cb[i][j], f2_mul(e[j], ca[i][j])), r2);
+          }
+          if (un.first[i]) st_once(row + un.c0[i], pack2<T>(o));
+          if (un.second[i]) st_once(row + un.c1[i], pack2<T>(o + P));
+        }
+      }
+      x += kFlight * a.d;
+      y += kFlight * a.d;
+    }
+  }
+}
+
+template <typename T, bool INTER, int LANES, int U>
+__global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(const __grid_constant__ QkArgs a,
+                                                                              const Share share) {
+  constexpr int N = Vec<T>::N, P = N / 2, kTeams = kThreads / LANES;
+  extern __shared__ float s_dw[];                  // [kTeams][d]
+  __shared__ uint64_t s_fx[kQkMaxDim / 2];
+  grid_dep_trigger();
+  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) s_fx[i] = fixed_turns(a.freqs[i]);
+  __syncthreads();
+  int k = 0;
+  while ((int)blockIdx.x >= share.first[k + 1]) ++k;
+  const QkTensor& q = a.t[k];
+  const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
+  const uint32_t mask = team_mask<LANES>();
+  const Units<N, INTER, LANES, U> un(a, lane);
+  const int hsplit = share.hsplit[k], per = share.per[k];
+  const int64_t items = a.len * hsplit;
+  const float inv_d = 1.f / (float)a.d;
+  const int64_t step = (int64_t)(share.first[k + 1] - share.first[k]) * kTeams;
+  uint64_t w[U][N], dw[U][N];                      // [P] of the first vector, [P] of the second
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float t[N];
+    load_weight<T>(q.weight, un.c0[i], un.first[i], t);
+#pragma unroll
+    for (int j = 0; j < P; ++j) w[i][j] = f2_pack(t[2 * j], t[2 * j + 1]);
+    load_weight<T>(q.weight, un.c1[i], un.second[i], t);
+#pragma unroll
+    for (int j = 0; j < P; ++j) w[i][P + j] = f2_pack(t[2 * j], t[2 * j + 1]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) dw[i][j] = 0;
+  }
+  for (int64_t item = (int64_t)(blockIdx.x - share.first[k]) * kTeams + team; item < items; item += step) {
+    const Item m = item_of(q, item, hsplit, per);
+    if (m.h0 >= m.h1) continue;
+    const T* x = reinterpret_cast<const T*>(q.x) + m.t * q.x_stride + (int64_t)m.h0 * a.d;
+    const T* dy = reinterpret_cast<const T*>(q.dy) +
+                  row_offset(m.t, m.h0, q.y_stride, q.heads, q.groups, a.len, a.d);
+    T* dx = reinterpret_cast<T*>(q.dx) + m.t * q.dx_stride + (int64_t)m.h0 * a.d;
+    uint4 nx[U][2], ny[U][2];                      // the next head, on its way
+    auto load = [&] {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        nx[i][0] = nx[i][1] = ny[i][0] = ny[i][1] = make_uint4(0, 0, 0, 0);
+        if (un.first[i]) {
+          nx[i][0] = ld_once(x + un.c0[i]);
+          ny[i][0] = ld_once(dy + un.c0[i]);
+        }
+        if (un.second[i]) {
+          nx[i][1] = ld_once(x + un.c1[i]);
+          ny[i][1] = ld_once(dy + un.c1[i]);
+        }
+      }
+      x += a.d;
+      dy += a.d;
+    };
+    load();
+    int64_t pos;
+    if (!position_of(Positions{a.positions, a.cu, a.ndoc, a.start}, m.t, pos)) continue;
+    // halves: c and s of the pairs, packed; neighbours: (c, c) and (-s, s) of each
+    uint64_t c2[U][INTER ? N : P], s2[U][INTER ? N : P];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float c[N], s[N];
+      turns<N, INTER>(a, s_fx, pos, lane + i * LANES, un.turned[i], true, c, s);
+      if constexpr (INTER) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          c2[i][j] = f2_pack(c[j], c[j]);
+          s2[i][j] = f2_pack(-s[j], s[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          c2[i][j] = f2_pack(c[2 * j], c[2 * j + 1]);
+          s2[i][j] = f2_pack(s[2 * j], s[2 * j + 1]);
+        }
+      }
+    }
+    for (int h = m.h0; h < m.h1; ++h) {
+      uint64_t xs[U][N], z[U][N], ss = 0, su = 0;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        uint64_t e[N];
+        unpack2<T>(nx[i][0], xs[i]);
+        unpack2<T>(nx[i][1], xs[i] + P);
+        unpack2<T>(ny[i][0], e);
+        unpack2<T>(ny[i][1], e + P);
+        if constexpr (INTER) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) z[i][j] = f2_fma(swap2(e[j]), s2[i][j], f2_mul(e[j], c2[i][j]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            z[i][j] = f2_sub(f2_mul(e[j], c2[i][j]), f2_mul(e[P + j], s2[i][j]));
+            z[i][P + j] = f2_fma(e[j], s2[i][j], f2_mul(e[P + j], c2[i][j]));
+          }
+        }
+      }
+      if (h + 1 < m.h1) load();
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          ss = f2_fma(xs[i][j], xs[i][j], ss);
+          su = f2_fma(xs[i][j], f2_mul(z[i][j], w[i][j]), su);
+        }
+      const float r = rsqrtf(fmaf(team_sum<LANES>(sum2(ss), mask), inv_d, a.eps));
+      const float mean = team_sum<LANES>(sum2(su), mask) * r * inv_d;          // mean(u n)
+      const uint64_t r2 = f2_pack(r, r), nm2 = f2_pack(-r * mean * r, -r * mean * r);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        uint64_t o[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const uint64_t zr = f2_mul(z[i][j], r2);
+          dw[i][j] = f2_fma(xs[i][j], zr, dw[i][j]);
+          o[j] = f2_fma(zr, w[i][j], f2_mul(xs[i][j], nm2));
+        }
+        if (un.first[i]) st_once(dx + un.c0[i], pack2<T>(o));
+        if (un.second[i]) st_once(dx + un.c1[i], pack2<T>(o + P));
+      }
+      dx += a.d;
+    }
+  }
+  if (q.dweight == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float* const o = s_dw + team * a.d;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      if (un.first[i]) f2_unpack(dw[i][j], o[un.c0[i] + 2 * j], o[un.c0[i] + 2 * j + 1]);
+      if (un.second[i]) f2_unpack(dw[i][P + j], o[un.c1[i] + 2 * j], o[un.c1[i] + 2 * j + 1]);
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.d; c += kThreads) {
+    float x = 0.f;
+    for (int m = 0; m < kTeams; ++m) x += s_dw[m * a.d + c];
+    a.partial[(int64_t)blockIdx.x * a.d + c] = x;
+  }
+}
+
 // dw[c] of a tensor: the sum of its blocks' partial sums, 32 columns of a block,
 // 32 warps taking every 32nd of them.
 constexpr int kSumThreads = 1024;
@@ -144,31 +512,111 @@ __global__ void __launch_bounds__(kSumThreads) qk_weight_grad_kernel(const __gri
   if (lane == 0 && blockIdx.x * 32 + warp < a.d) st_out(dw + blockIdx.x * 32 + warp, x);
 }
 
+// Whether rows are whole 16-byte pieces, and the lanes of a team and units of a lane then.
+template <typename T>
+bool vector_shape(const QkArgs& a, int& lanes, int& units) {
+  constexpr int N = Vec<T>::N;
+  if (a.d % N != 0 || (a.interleaved ? a.rot : a.rot / 2) % N != 0) return false;
+  for (int i = 0; i < a.n; ++i) {
+    const QkTensor& q = a.t[i];
+    const void* const ptrs[] = {q.x, q.weight, q.y, q.dy, q.dx};
+    for (const void* p : ptrs)
+      if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return false;
+    if (q.x_stride % N != 0 || q.y_stride % N != 0 || q.dx_stride % N != 0) return false;
+  }
+  const int vecs = a.d / N, turned = a.rot / N;
+  const int n = a.interleaved ? (vecs + 1) / 2 : turned / 2 + (vecs - turned + 1) / 2;
+  lanes = 4;
+  while (lanes < 32 && lanes < n) lanes *= 2;
+  units = (n + lanes - 1) / lanes;
+  return units <= 2;
+}
+
+// Heads of a part when there are to be `hsplit` parts or more: a part lies in one group.
+int part_heads(const QkTensor& q, int64_t hsplit) {
+  const int hpg = q.heads / q.groups;
+  int per = (int)ceil_div(q.heads, hsplit);
+  if (q.groups == 1) return per;
+  per = std::min(per, hpg);
+  while (hpg % per != 0) --per;
+  return per;
+}
+
+// The kernel of a shape: KERN is a template of <T, INTER, LANES, U>.
+#define NSP_QK_KERNEL(KERN, T, lanes, units, inter, go)                    \
+  do {                                                                     \
+    if (units == 2) {                                                      \
+      if (inter) go(KERN<T, true, 32, 2>); else go(KERN<T, false, 32, 2>); \
+    } else if (lanes == 4) {                                               \
+      if (inter) go(KERN<T, true, 4, 1>); else go(KERN<T, false, 4, 1>);   \
+    } else if (lanes == 8) {                                               \
+      if (inter) go(KERN<T, true, 8, 1>); else go(KERN<T, false, 8, 1>);   \
+    } else if (lanes == 16) {                                              \
+      if (inter) go(KERN<T, true, 16, 1>); else go(KERN<T, false, 16, 1>); \
+    } else {                                                               \
+      if (inter) go(KERN<T, true, 32, 1>); else go(KERN<T, false, 32, 1>); \
+    }                                                                      \
+  } while (0)
+
 template <typename T>
 cudaError_t fwd(const QkArgs& a, cudaStream_t s) {
-  Share share;
-  share.first[0] = 0;
-  for (int i = 0; i < kRopeMaxTensors; ++i) {
-    const int64_t rows = i < a.n ? a.len * a.t[i].heads : 0;
-    const int64_t blocks = std::min<int64_t>(ceil_div(rows, kWarps), (int64_t)num_sms() * 8);
+  Share share = {};
+  int lanes, units;
+  const bool vec = vector_shape<T>(a, lanes, units);
+  const int64_t nsm = num_sms();
+  int total = 0;
+  for (int i = 0; i < a.n; ++i) total += a.t[i].heads;
+  for (int i = 0; i < a.n; ++i) {
+    const int heads = a.t[i].heads;
+    int64_t blocks;
+    if (vec) {
+      // A token's heads are split over several teams, each with its own search and angles,
+      // until every SM has two blocks, and in parts of 12 heads or more of a stream that does
+      // not fit in L2, whose rows in flight then lie closer together (as in rope.cu)
+      const int teams = kVecThreads / lanes;
+      const int64_t bytes = 2 * a.len * total * a.d * (int64_t)sizeof(T);
+      int64_t hsplit = ceil_div(nsm * 2 * teams * heads, a.len * total);
+      if (bytes > kL2Bytes) hsplit = std::max<int64_t>(hsplit, heads / 12);
+      hsplit = std::max<int64_t>(1, std::min<int64_t>(hsplit, heads));
+      if (a.len * hsplit > UINT32_MAX) hsplit = 1;     // the kernel divides split items in 32 bits
+      share.per[i] = part_heads(a.t[i], hsplit);
+      share.hsplit[i] = (int)ceil_div(heads, share.per[i]);
+      blocks = std::min<int64_t>(ceil_div(a.len * share.hsplit[i], teams), nsm * 128);
+    } else {
+      blocks = std::min<int64_t>(ceil_div(a.len * heads, kWarps), nsm * 8);
+    }
     share.first[i + 1] = share.first[i] + (int)blocks;
   }
-  qk_element_kernel<T, false><<<share.first[a.n], kThreads, 0, s>>>(a, share);
+  auto go = [&](auto kern) { kern<<<share.first[a.n], kVecThreads, 0, s>>>(a, share); };
+  if (!vec) qk_element_kernel<T, false><<<share.first[a.n], kThreads, 0, s>>>(a, share);
+  else NSP_QK_KERNEL(qk_vec_kernel, T, lanes, units, a.interleaved, go);
   count_launches(1);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t bwd(const QkArgs& a, cudaStream_t s) {
-  Share share;
-  share.first[0] = 0;
+  Share share = {};
+  int lanes, units;
+  const bool vec = vector_shape<T>(a, lanes, units);
   bool weights = false;
-  for (int i = 0; i < kRopeMaxTensors; ++i) {
-    const int64_t rows = i < a.n ? a.len * a.t[i].heads : 0;
-    share.first[i + 1] = share.first[i] + (i < a.n ? qk_bwd_blocks(rows) : 0);
-    weights = weights || (i < a.n && a.t[i].dweight != nullptr);
+  for (int i = 0; i < a.n; ++i) {
+    const int heads = a.t[i].heads;
+    const int blocks = qk_bwd_blocks(a.t, a.n, i, a.len);
+    share.first[i + 1] = share.first[i] + blocks;
+    if (vec) {
+      int64_t hsplit = std::min<int64_t>(heads, ceil_div((int64_t)blocks * (kThreads / lanes), a.len));
+      if (a.len * hsplit > UINT32_MAX) hsplit = 1;
+      share.per[i] = part_heads(a.t[i], hsplit);
+      share.hsplit[i] = (int)ceil_div(heads, share.per[i]);
+    }
+    weights = weights || a.t[i].dweight != nullptr;
   }
-  qk_element_kernel<T, true><<<share.first[a.n], kThreads, sizeof(float) * kWarps * a.d, s>>>(a, share);
+  auto go = [&](auto kern) {
+    kern<<<share.first[a.n], kThreads, sizeof(float) * (kThreads / lanes) * a.d, s>>>(a, share);
+  };
+  if (!vec) qk_element_kernel<T, true><<<share.first[a.n], kThreads, sizeof(float) * kWarps * a.d, s>>>(a, share);
+  else NSP_QK_KERNEL(qk_vec_bwd_kernel, T, lanes, units, a.interleaved, go);
   count_launches(1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !weights) return e;
@@ -180,9 +628,18 @@ cudaError_t bwd(const QkArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int qk_bwd_blocks(int64_t rows) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(kBwdBlocks, ceil_div(rows, kWarps)));
+// kBwdBlocks blocks, two on each of 152 SMs, shared by the tensors' heads and some for
+// every tensor's searches and angles; fewer for few rows.  The same on every device: the
+// workspace's size, and the order of the weights' sums, go by it.
+template <typename Tensor>
+static int bwd_blocks(const Tensor* t, int n, int i, int64_t len) {
+  int64_t total = 0;
+  for (int k = 0; k < n; ++k) total += t[k].heads + 4;
+  const int64_t share = std::max<int64_t>(1, (int64_t)kBwdBlocks * (t[i].heads + 4) / total);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(share, ceil_div(len * t[i].heads, kWarps)));
 }
+int qk_bwd_blocks(const QkTensor* t, int n, int i, int64_t len) { return bwd_blocks(t, n, i, len); }
+int qk_bwd_blocks(const nsp_qk_tensor_t* t, int n, int i, int64_t len) { return bwd_blocks(t, n, i, len); }
 
 cudaError_t launch_qk_norm_rope(const QkArgs& a, int32_t io_dtype, cudaStream_t s) {
   return io_dtype == NSP_BF16 ? fwd<__nv_bfloat16>(a, s) : fwd<float>(a, s);

@@ -30,8 +30,9 @@ struct QkArgs {
   float mscale, eps;
   float* partial;                          // backward: [blocks of a tensor][d] sums, tensor by tensor
 };
-// Most blocks that the backward gives a tensor, whatever the device.
-int qk_bwd_blocks(int64_t rows);
+// The blocks that the backward gives tensor i of n, whatever the device.
+int qk_bwd_blocks(const QkTensor* t, int n, int i, int64_t len);
+int qk_bwd_blocks(const nsp_qk_tensor_t* t, int n, int i, int64_t len);
 cudaError_t launch_qk_norm_rope(const QkArgs& a, int32_t io_dtype, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, int32_t io_dtype, cudaStream_t s);
 

@@ -206,10 +206,9 @@ size_t nsp_qk_norm_rope_bwd_workspace_size(const nsp_qk_tensor_t* tensors, int32
       d > kQkMaxDim)
     return 0;
   size_t blocks = 0;
-  for (int32_t i = 0; i < n; ++i) {
+  for (int32_t i = 0; i < n; ++i)
     if (tensors[i].heads < 1 || tensors[i].heads > kMaxHeads) return 0;
-    blocks += (size_t)qk_bwd_blocks(len * tensors[i].heads);
-  }
+  for (int32_t i = 0; i < n; ++i) blocks += (size_t)qk_bwd_blocks(tensors, n, i, len);
   return blocks * (size_t)d * sizeof(float);
 }
 
