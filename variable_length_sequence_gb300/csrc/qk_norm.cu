@@ -345,25 +345,128 @@ __global__ void __launch_bounds__(kVecThreads, U == 1 ? 4 : 2) qk_vec_kernel(con
   }
 }
 
+// The backward's rows come through a ring in shared memory: a thread copies its own
+// vectors of the heads ahead, kAhead of them at any time, and reads only what it copied
+// itself.
+constexpr int kAhead = 6;
+template <int U> constexpr int bwd_ring_bytes() { return kAhead / U * U * 4 * 16 * kThreads; }
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// A warp's rows of a tensor, `row` to `end` of them: the heads of TOKENS tokens at a time,
+// a team each, which turn to their next tokens together; all warps have as many, give or
+// take one.  Rows behind the last document (at `live`) are nobody's.
+template <int TOKENS>
+struct WarpRows {
+  int64_t live, row, end;
+
+  __device__ __forceinline__ WarpRows(const QkArgs& a, const QkTensor& q, int64_t warp, int64_t warps) {
+    live = a.len;
+    if (a.positions == nullptr)
+      live = max((int64_t)0, min(live, (int64_t)__ldg(a.cu + a.ndoc) - a.start));
+    const int64_t rows = (live + TOKENS - 1) / TOKENS * q.heads, each = rows / warps;
+    const int64_t more = rows - each * warps;
+    row = warp * each + min(warp, more);
+    end = row + each + (warp < more ? 1 : 0);
+  }
+};
+
+// Positions of a team's tokens: a search where a document ends.
+struct PositionWalk {
+  int64_t start = 0, end = 0;
+  __device__ __forceinline__ int64_t of(const QkArgs& a, int64_t t) {
+    if (a.positions != nullptr) return __ldg(a.positions + t);
+    const int64_t g = a.start + t;
+    if (g >= end) {
+      const int doc = doc_of(a.cu, a.ndoc, g);
+      start = __ldg(a.cu + doc);
+      end = __ldg(a.cu + doc + 1);
+    }
+    return g - start;
+  }
+};
+
+template <typename T, int U, int TOKENS, typename UNITS>
+struct HeadCopies {
+  const QkArgs& a;
+  const QkTensor& q;
+  const UNITS& un;
+  const int64_t live;
+  int64_t left, t;                                 // rows that are not copied yet; token of the next
+  int h;
+  const T *x, *dy;
+
+  __device__ __forceinline__ HeadCopies(const QkArgs& a, const QkTensor& q, const UNITS& un,
+                                        const WarpRows<TOKENS>& rows, int64_t t, int h)
+      : a(a), q(q), un(un), live(rows.live), left(t < live ? rows.end - rows.row : 0), t(t), h(h) {
+    x = reinterpret_cast<const T*>(q.x) + t * q.x_stride + (int64_t)h * a.d;
+    find();
+  }
+  __device__ __forceinline__ void find() {
+    dy = reinterpret_cast<const T*>(q.dy) + row_offset(t, h, q.y_stride, q.heads, q.groups, a.len, a.d);
+  }
+  // the next head into the four places (of every unit) from `to` on
+  __device__ __forceinline__ void copy(uint4* to) {
+    if (left > 0) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        uint4* const p = to + i * 4 * kThreads;
+        if (un.first[i]) {
+          copy16(p, x + un.c0[i]);
+          copy16(p + 2 * kThreads, dy + un.c0[i]);
+        }
+        if (un.second[i]) {
+          copy16(p + kThreads, x + un.c1[i]);
+          copy16(p + 3 * kThreads, dy + un.c1[i]);
+        }
+      }
+      --left;
+      x += a.d;
+      dy += a.d;
+      if (++h == q.heads) {
+        h = 0;
+        t += TOKENS;
+        x += TOKENS * q.x_stride - (int64_t)q.heads * a.d;
+        if (t >= live) left = 0;
+        if (left > 0) find();
+      } else if (q.groups > 1 && left > 0) {
+        find();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
 template <typename T, bool INTER, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(const __grid_constant__ QkArgs a,
                                                                               const Share share) {
-  constexpr int N = Vec<T>::N, P = N / 2, kTeams = kThreads / LANES;
-  extern __shared__ float s_dw[];                  // [kTeams][d]
+  constexpr int N = Vec<T>::N, P = N / 2, kTeams = kThreads / LANES, kHeads = kAhead / U, kTokens = 32 / LANES;
+  using UnitsOf = Units<N, INTER, LANES, U>;
+  extern __shared__ __align__(16) uint4 s_ring[];  // [kHeads][U][4][kThreads]; in the end [kTeams][d] sums
   __shared__ uint64_t s_fx[kQkMaxDim / 2];
   grid_dep_trigger();
-  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) s_fx[i] = fixed_turns(a.freqs[i]);
-  __syncthreads();
   int k = 0;
   while ((int)blockIdx.x >= share.first[k + 1]) ++k;
   const QkTensor& q = a.t[k];
   const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
   const uint32_t mask = team_mask<LANES>();
-  const Units<N, INTER, LANES, U> un(a, lane);
-  const int hsplit = share.hsplit[k], per = share.per[k];
-  const int64_t items = a.len * hsplit;
+  const UnitsOf un(a, lane);
   const float inv_d = 1.f / (float)a.d;
-  const int64_t step = (int64_t)(share.first[k + 1] - share.first[k]) * kTeams;
+  const WarpRows<kTokens> rows(a, q, (int64_t)(blockIdx.x - share.first[k]) * kWarps + threadIdx.x / 32,
+                               (int64_t)(share.first[k + 1] - share.first[k]) * kWarps);
+  int64_t t = rows.row / q.heads;                  // (of the warp's groups of tokens)
+  int h = (int)(rows.row - t * q.heads);
+  t = t * kTokens + team % kTokens;
+  uint4* const ring = s_ring + threadIdx.x;
+  // (vectors that a lane does not have are never copied: zeros)
+  for (int i = 0; i < kHeads * U * 4; ++i) ring[i * kThreads] = make_uint4(0, 0, 0, 0);
+  HeadCopies<T, U, kTokens, UnitsOf> ahead(a, q, un, rows, t, h);
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) ahead.copy(ring + i * U * 4 * kThreads);
+  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) s_fx[i] = fixed_turns(a.freqs[i]);
+  __syncthreads();
   uint64_t w[U][N], dw[U][N];                      // [P] of the first vector, [P] of the second
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -377,33 +480,13 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(co
 #pragma unroll
     for (int j = 0; j < N; ++j) dw[i][j] = 0;
   }
-  for (int64_t item = (int64_t)(blockIdx.x - share.first[k]) * kTeams + team; item < items; item += step) {
-    const Item m = item_of(q, item, hsplit, per);
-    if (m.h0 >= m.h1) continue;
-    const T* x = reinterpret_cast<const T*>(q.x) + m.t * q.x_stride + (int64_t)m.h0 * a.d;
-    const T* dy = reinterpret_cast<const T*>(q.dy) +
-                  row_offset(m.t, m.h0, q.y_stride, q.heads, q.groups, a.len, a.d);
-    T* dx = reinterpret_cast<T*>(q.dx) + m.t * q.dx_stride + (int64_t)m.h0 * a.d;
-    uint4 nx[U][2], ny[U][2];                      // the next head, on its way
-    auto load = [&] {
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        nx[i][0] = nx[i][1] = ny[i][0] = ny[i][1] = make_uint4(0, 0, 0, 0);
-        if (un.first[i]) {
-          nx[i][0] = ld_once(x + un.c0[i]);
-          ny[i][0] = ld_once(dy + un.c0[i]);
-        }
-        if (un.second[i]) {
-          nx[i][1] = ld_once(x + un.c1[i]);
-          ny[i][1] = ld_once(dy + un.c1[i]);
-        }
-      }
-      x += a.d;
-      dy += a.d;
-    };
-    load();
-    int64_t pos;
-    if (!position_of(Positions{a.positions, a.cu, a.ndoc, a.start}, m.t, pos)) continue;
+  int slot = 0;
+  PositionWalk at;
+  for (int64_t row = rows.row; row < rows.end && t < rows.live; t += kTokens, h = 0) {
+    const int h1 = (int)min((int64_t)q.heads, h + (rows.end - row));
+    row += h1 - h;
+    const int64_t pos = at.of(a, t);
+    T* dx = reinterpret_cast<T*>(q.dx) + t * q.dx_stride + (int64_t)h * a.d;
     // halves: c and s of the pairs, packed; neighbours: (c, c) and (-s, s) of each
     uint64_t c2[U][INTER ? N : P], s2[U][INTER ? N : P];
 #pragma unroll
@@ -424,15 +507,19 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(co
         }
       }
     }
-    for (int h = m.h0; h < m.h1; ++h) {
+    for (; h < h1; ++h) {
       uint64_t xs[U][N], z[U][N], ss = 0, su = 0;
+      uint4* const place = ring + slot * U * 4 * kThreads;
+      slot = slot + 1 == kHeads ? 0 : slot + 1;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kHeads - 1) : "memory");
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         uint64_t e[N];
-        unpack2<T>(nx[i][0], xs[i]);
-        unpack2<T>(nx[i][1], xs[i] + P);
-        unpack2<T>(ny[i][0], e);
-        unpack2<T>(ny[i][1], e + P);
+        const uint4* const v = place + i * 4 * kThreads;
+        unpack2<T>(v[0], xs[i]);
+        unpack2<T>(v[kThreads], xs[i] + P);
+        unpack2<T>(v[2 * kThreads], e);
+        unpack2<T>(v[3 * kThreads], e + P);
         if constexpr (INTER) {
 #pragma unroll
           for (int j = 0; j < N; ++j) z[i][j] = f2_fma(swap2(e[j]), s2[i][j], f2_mul(e[j], c2[i][j]));
@@ -444,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(co
           }
         }
       }
-      if (h + 1 < m.h1) load();
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
@@ -454,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(co
         }
       const float r = rsqrtf(fmaf(team_sum<LANES>(sum2(ss), mask), inv_d, a.eps));
       const float mean = team_sum<LANES>(sum2(su), mask) * r * inv_d;          // mean(u n)
+      ahead.copy(place);                           // (the sums have used its last contents)
       const uint64_t r2 = f2_pack(r, r), nm2 = f2_pack(-r * mean * r, -r * mean * r);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -471,6 +558,9 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(co
     }
   }
   if (q.dweight == nullptr) return;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  float* const s_dw = reinterpret_cast<float*>(s_ring);
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     float* const o = s_dw + team * a.d;
@@ -542,20 +632,21 @@ int part_heads(const QkTensor& q, int64_t hsplit) {
   return per;
 }
 
-// The kernel of a shape: KERN is a template of <T, INTER, LANES, U>.
-#define NSP_QK_KERNEL(KERN, T, lanes, units, inter, go)                    \
-  do {                                                                     \
-    if (units == 2) {                                                      \
-      if (inter) go(KERN<T, true, 32, 2>); else go(KERN<T, false, 32, 2>); \
-    } else if (lanes == 4) {                                               \
-      if (inter) go(KERN<T, true, 4, 1>); else go(KERN<T, false, 4, 1>);   \
-    } else if (lanes == 8) {                                               \
-      if (inter) go(KERN<T, true, 8, 1>); else go(KERN<T, false, 8, 1>);   \
-    } else if (lanes == 16) {                                              \
-      if (inter) go(KERN<T, true, 16, 1>); else go(KERN<T, false, 16, 1>); \
-    } else {                                                               \
-      if (inter) go(KERN<T, true, 32, 1>); else go(KERN<T, false, 32, 1>); \
-    }                                                                      \
+// The kernel of a shape, as a type: KERN is a template of <T, INTER, LANES, U>.
+template <auto K> struct Kernel { static constexpr auto value = K; };
+#define NSP_QK_KERNEL(KERN, T, lanes, units, inter, go)                                        \
+  do {                                                                                         \
+    if (units == 2) {                                                                          \
+      if (inter) go(Kernel<KERN<T, true, 32, 2>>{}); else go(Kernel<KERN<T, false, 32, 2>>{}); \
+    } else if (lanes == 4) {                                                                   \
+      if (inter) go(Kernel<KERN<T, true, 4, 1>>{}); else go(Kernel<KERN<T, false, 4, 1>>{});   \
+    } else if (lanes == 8) {                                                                   \
+      if (inter) go(Kernel<KERN<T, true, 8, 1>>{}); else go(Kernel<KERN<T, false, 8, 1>>{});   \
+    } else if (lanes == 16) {                                                                  \
+      if (inter) go(Kernel<KERN<T, true, 16, 1>>{}); else go(Kernel<KERN<T, false, 16, 1>>{}); \
+    } else {                                                                                   \
+      if (inter) go(Kernel<KERN<T, true, 32, 1>>{}); else go(Kernel<KERN<T, false, 32, 1>>{}); \
+    }                                                                                          \
   } while (0)
 
 template <typename T>
@@ -587,7 +678,7 @@ cudaError_t fwd(const QkArgs& a, cudaStream_t s) {
     }
     share.first[i + 1] = share.first[i] + (int)blocks;
   }
-  auto go = [&](auto kern) { kern<<<share.first[a.n], kVecThreads, 0, s>>>(a, share); };
+  auto go = [&](auto tag) { decltype(tag)::value<<<share.first[a.n], kVecThreads, 0, s>>>(a, share); };
   if (!vec) qk_element_kernel<T, false><<<share.first[a.n], kThreads, 0, s>>>(a, share);
   else NSP_QK_KERNEL(qk_vec_kernel, T, lanes, units, a.interleaved, go);
   count_launches(1);
@@ -601,24 +692,26 @@ cudaError_t bwd(const QkArgs& a, cudaStream_t s) {
   const bool vec = vector_shape<T>(a, lanes, units);
   bool weights = false;
   for (int i = 0; i < a.n; ++i) {
-    const int heads = a.t[i].heads;
-    const int blocks = qk_bwd_blocks(a.t, a.n, i, a.len);
-    share.first[i + 1] = share.first[i] + blocks;
-    if (vec) {
-      int64_t hsplit = std::min<int64_t>(heads, ceil_div((int64_t)blocks * (kThreads / lanes), a.len));
-      if (a.len * hsplit > UINT32_MAX) hsplit = 1;
-      share.per[i] = part_heads(a.t[i], hsplit);
-      share.hsplit[i] = (int)ceil_div(heads, share.per[i]);
-    }
+    share.first[i + 1] = share.first[i] + qk_bwd_blocks(a.t, a.n, i, a.len);
     weights = weights || a.t[i].dweight != nullptr;
   }
-  auto go = [&](auto kern) {
-    kern<<<share.first[a.n], kThreads, sizeof(float) * (kThreads / lanes) * a.d, s>>>(a, share);
+  const int smem = units == 2 ? bwd_ring_bytes<2>() : bwd_ring_bytes<1>();
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto tag) {
+    constexpr auto kern = decltype(tag)::value;
+    static bool allowed[64] = {};
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !allowed[dev])) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e == cudaSuccess && dev < 64) allowed[dev] = true;
+    }
+    if (e == cudaSuccess) kern<<<share.first[a.n], kThreads, smem, s>>>(a, share);
   };
   if (!vec) qk_element_kernel<T, true><<<share.first[a.n], kThreads, sizeof(float) * kWarps * a.d, s>>>(a, share);
   else NSP_QK_KERNEL(qk_vec_bwd_kernel, T, lanes, units, a.interleaved, go);
   count_launches(1);
-  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || !weights) return e;
   e = launch_dependent(qk_weight_grad_kernel<T>, dim3((a.d + 31) / 32, a.n), dim3(kSumThreads), 0, s,
                        a, share);
