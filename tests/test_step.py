@@ -359,7 +359,7 @@ def _grads(lib, clip, ptrs=(LG, TG), counts=(100, 50), types=(0, 1), out=None, o
 @pytest.mark.parametrize("clip", [False, True])
 @pytest.mark.parametrize("kw,expect", [
     ({"n": 0}, INVALID), ({"n": 1 << 20}, UNSUPPORTED), ({"kind": 2}, INVALID), ({"unscale": float("inf")}, INVALID),
-    ({"norm": None}, INVALID), ({"norm": A + 2}, ALIGN), ({"ws": None}, WORKSPACE), ({"size": 200}, WORKSPACE),
+    ({"norm": None}, INVALID), ({"norm": A + 2}, ALIGN), ({"ws": None}, WORKSPACE), ({"size": 8}, WORKSPACE),
     ({"ws": A + 8}, ALIGN), ({"types": (0, 2)}, INVALID), ({"counts": (100, -1)}, INVALID),
     ({"counts": (100, (1 << 40) + 1)}, UNSUPPORTED), ({"ptrs": (LG, 0)}, INVALID), ({"ptrs": (LG + 2, TG)}, ALIGN),
     ({"norm": LG + 396}, INVALID), ({"ws": TG + 96}, INVALID), ({"norm": A + (14 << 20) + 8}, INVALID),
@@ -382,7 +382,7 @@ def test_clip_refusals(lib, kw, expect):
 
 def test_grad_workspace(lib):
     size = lib.nsp_grad_norm_workspace_size
-    assert size((C.c_int64 * 2)(5, 0), 2) > 256 and size((C.c_int64 * 1)(-5), 1) == 0 and size(None, 1) == 0
+    assert size((C.c_int64 * 2)(5, 0), 2) > 0 and size((C.c_int64 * 1)(-5), 1) == 0 and size(None, 1) == 0
     assert size((C.c_int64 * 1)(5), 0) == 0
 
 

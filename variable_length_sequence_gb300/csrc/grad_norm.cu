@@ -1,18 +1,31 @@
 // Global norm of many gradients, and the gradients scaled by what is left of it:
 //   norm = |unscale| (sum g^2)^(1/2)  or  |unscale| max |g|,
 //   out = g unscale min(1, max_norm / (norm + eps)).
+//
+// Bound: HBM, one read of every gradient for the norm, one read and one write for the
+// scaling.  All gradients one behind the other are cut in pieces of kPiece elements,
+// and each of kBlocks blocks takes a run of neighbouring pieces, whatever tensors they
+// lie in, so that one launch serves hundreds of tensors and no block has much more than
+// another.  A thread adds 16 float32 squares at a time and those sums in pairs of
+// floats; the blocks' sums are added by every block that scales, or by one more.  The
+// scaling walks each block's run from its end, where L2 still holds what the norm read
+// last.
 #include <algorithm>
 #include <cmath>
 
 #include "sums.cuh"
+#include "tc_ptx.cuh"
 #include "train.cuh"
 
 namespace nsp {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSumThreads = 1024;
-constexpr int64_t kChunk = 32768;          // elements of a partial sum
+using namespace tc;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlocks = 912;               // of a launch, whatever the device: six of an SM
+constexpr int64_t kPiece = 2048;           // elements
+constexpr int kFlight = 4;                 // units of 8 elements that a thread has in flight
 
 // The tensors of one launch travel as a kernel parameter, so that a captured graph
 // of the call carries them.
@@ -20,160 +33,310 @@ struct GradTensor {
   const void* in;
   void* out;
   int64_t count;
-  int32_t chunk0;                          // its first chunk, of the launch's
+  int32_t piece0;                          // its first piece, of the launch's
   int32_t types;                           // 1: bf16 in, 2: bf16 out
 };
 template <int CAP>
 struct GradTable {
   GradTensor t[CAP];
-  int32_t n, chunks;
+  int32_t n, pieces;
 };
 
 template <int CAP>
-__device__ __forceinline__ int tensor_of(const GradTable<CAP>& g, int chunk) {
+__device__ __forceinline__ int tensor_of(const GradTable<CAP>& g, int piece) {
   int lo = 0, hi = g.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (g.t[mid].chunk0 <= chunk) lo = mid; else hi = mid - 1;
+    if (g.t[mid].piece0 <= piece) lo = mid; else hi = mid - 1;
   }
   return lo;
-}
-
-__device__ __forceinline__ float load(const void* p, int64_t i, bool bf16) {
-  return bf16 ? to_f(reinterpret_cast<const __nv_bfloat16*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
 }
 
 // max that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b) { return a > b || isnan(a) ? a : b; }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradTable<CAP> g,
-                                                             int kind, Sum2* __restrict__ partial) {
-  __shared__ Sum2 s_sum[kThreads / 32];
-  for (int c = blockIdx.x; c < g.chunks; c += gridDim.x) {
-    const GradTensor& t = g.t[tensor_of(g, c)];
-    const int64_t first = (int64_t)(c - t.chunk0) * kChunk, last = min(first + kChunk, t.count);
-    Sum2 x = {0.f, 0.f};
-    for (int64_t i = first + threadIdx.x; i < last; i += kThreads) {
-      const float v = load(t.in, i, t.types & 1);
-      if (kind == NSP_NORM_2) x.add(v * v); else x.hi = max_nan(x.hi, fabsf(v));
-    }
-    __syncthreads();
-    if (kind == NSP_NORM_2) {
-      x = block_sum<kThreads / 32>(x, s_sum);
+// Calls f(tensor, first, last) for every tensor's elements in the block's run of pieces,
+// in order or from the end.
+template <int CAP, typename F>
+__device__ __forceinline__ void for_run(const GradTable<CAP>& g, bool backwards, F f) {
+  const int each = g.pieces / (int)gridDim.x, more = g.pieces - each * (int)gridDim.x;
+  const int b = blockIdx.x;
+  int p0 = b * each + min(b, more), p1 = p0 + each + (b < more ? 1 : 0);
+  if (p0 == p1) return;
+  int k = tensor_of(g, backwards ? p1 - 1 : p0);
+  while (p0 < p1) {
+    const GradTensor& t = g.t[k];
+    const int end = k + 1 < g.n ? g.t[k + 1].piece0 : g.pieces;
+    const int a = max(p0, t.piece0), z = min(p1, end);
+    f(t, (int64_t)(a - t.piece0) * kPiece, min((int64_t)(z - t.piece0) * kPiece, t.count));
+    if (backwards) {
+      p1 = a;
+      --k;
     } else {
-      for (int o = 16; o > 0; o >>= 1) x.hi = max_nan(x.hi, __shfl_xor_sync(0xffffffffu, x.hi, o));
-      if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = x;
-      __syncthreads();
-      for (int w = 0; w < kThreads / 32; ++w) x.hi = max_nan(x.hi, s_sum[w].hi);
+      p0 = z;
+      ++k;
     }
-    if (threadIdx.x == 0) partial[c] = x;
   }
 }
 
-// norm, and the factor of the gradients, from the chunks' partial sums.
-__global__ void __launch_bounds__(kSumThreads) grad_total_kernel(const Sum2* __restrict__ partial, int64_t n,
-                                                                 int kind, float unscale, float max_norm,
-                                                                 float eps, float* norm, float* factor) {
-  __shared__ Sum2 s_sum[kSumThreads / 32];
+// Eight elements, 16-byte aligned.
+template <typename T>
+struct Unit {
+  static constexpr int V = 8 / Vec<T>::N;
+  uint4 v[V];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = ld_once(p + i * Vec<T>::N);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float t[Vec<T>::N];
+      Vec<T>::unpack(v[i], t);
+#pragma unroll
+      for (int j = 0; j < Vec<T>::N; ++j) x[i * Vec<T>::N + j] = t[j];
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ void store_unit(T* p, const float (&x)[8]) {
+  constexpr int N = Vec<T>::N;
+#pragma unroll
+  for (int i = 0; i < 8 / N; ++i) {
+    float t[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = x[i * N + j];
+    st_once(p + i * N, Vec<T>::pack(t));
+  }
+}
+
+// Elements before the first 16-byte border, at most n.
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int64_t n) {
+  return (int)min(n, (int64_t)(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T)));
+}
+
+template <typename T, bool MAX>
+__device__ __forceinline__ void take_run(const T* p, int64_t n, Sum2& x) {
+  const int head = head_of(p, n);
+  const int64_t units = (n - head) / 8;
+  const int rest = (int)(n - units * 8);                // before and behind the units: 14 at most
+  if ((int)threadIdx.x < rest) {
+    const float v = to_f(p[(int)threadIdx.x < head ? threadIdx.x : units * 8 + threadIdx.x]);
+    if (MAX) x.hi = max_nan(x.hi, fabsf(v)); else x.add(v * v);
+  }
+  p += head;
+  for (int64_t i = threadIdx.x; i < units; i += kThreads * kFlight) {
+    Unit<T> u[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      if (i + f * kThreads < units) u[f].load(p + (i + f * kThreads) * 8);
+      else u[f].zero();
+    }
+    uint64_t s[2] = {0, 0};
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      float e[8];
+      u[f].get(e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (MAX) {
+          x.hi = max_nan(max_nan(x.hi, fabsf(e[2 * j])), fabsf(e[2 * j + 1]));
+        } else {
+          const uint64_t v = f2_pack(e[2 * j], e[2 * j + 1]);
+          s[f & 1] = f2_fma(v, v, s[f & 1]);
+        }
+      }
+    }
+    if constexpr (!MAX) {
+      float a, b;
+      f2_unpack(f2_add(s[0], s[1]), a, b);
+      x.add(a + b);
+    }
+  }
+}
+
+// Over the block, in every thread.
+template <bool MAX>
+__device__ __forceinline__ Sum2 block_total(Sum2 x, Sum2* s) {
+  if constexpr (!MAX) return block_sum<kWarps>(x, s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x.hi = max_nan(x.hi, __shfl_xor_sync(0xffffffffu, x.hi, o));
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) x.hi = max_nan(x.hi, s[w].hi);
+  return x;
+}
+
+template <int CAP, bool MAX>
+__global__ void __launch_bounds__(kThreads, 6) grad_norm_kernel(const __grid_constant__ GradTable<CAP> g,
+                                                                Sum2* __restrict__ partial) {
+  __shared__ Sum2 s_sum[kWarps];
+  grid_dep_trigger();
   Sum2 x = {0.f, 0.f};
-  for (int64_t i = threadIdx.x; i < n; i += kSumThreads) {
-    if (kind == NSP_NORM_2) x.add(partial[i]); else x.hi = max_nan(x.hi, partial[i].hi);
-  }
-  double v;
-  if (kind == NSP_NORM_2) {
-    v = sqrt(block_sum<kSumThreads / 32>(x, s_sum).value());
-  } else {
-    for (int o = 16; o > 0; o >>= 1) x.hi = max_nan(x.hi, __shfl_xor_sync(0xffffffffu, x.hi, o));
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = x;
-    __syncthreads();
-    for (int w = 0; w < kSumThreads / 32; ++w) x.hi = max_nan(x.hi, s_sum[w].hi);
-    v = x.hi;
-  }
-  if (threadIdx.x != 0) return;
-  v *= fabs((double)unscale);
-  norm[0] = (float)v;
-  const double f = (double)max_norm / (v + (double)eps);
-  factor[0] = (float)((f < 1.0 || isnan(f) ? f : 1.0) * (double)unscale);
+  for_run(g, false, [&](const GradTensor& t, int64_t first, int64_t last) {
+    if (t.types & 1) take_run<__nv_bfloat16, MAX>(reinterpret_cast<const __nv_bfloat16*>(t.in) + first, last - first, x);
+    else take_run<float, MAX>(reinterpret_cast<const float*>(t.in) + first, last - first, x);
+  });
+  x = block_total<MAX>(x, s_sum);
+  if (threadIdx.x == 0) partial[blockIdx.x] = x;
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradTable<CAP> g,
-                                                              const float* __restrict__ factor) {
-  const float f = __ldcg(factor);
-  for (int c = blockIdx.x; c < g.chunks; c += gridDim.x) {
-    const GradTensor& t = g.t[tensor_of(g, c)];
-    if (f == 1.f && t.in == t.out) continue;           // (in place: nothing changes)
-    const int64_t first = (int64_t)(c - t.chunk0) * kChunk, last = min(first + kChunk, t.count);
-    for (int64_t i = first + threadIdx.x; i < last; i += kThreads) {
-      const float v = load(t.in, i, t.types & 1) * f;
-      if (t.types & 2) st_out(reinterpret_cast<__nv_bfloat16*>(t.out) + i, v);
-      else reinterpret_cast<float*>(t.out)[i] = v;
+struct Total {
+  const Sum2* partial;
+  int n;
+  float unscale, max_norm, eps;
+  float* norm;
+};
+
+// The norm, and the factor of the gradients, in every thread.
+template <bool MAX>
+__device__ __forceinline__ float total_of(const Total& t, bool write) {
+  __shared__ Sum2 s_sum[kWarps];
+  __shared__ float s_factor;
+  Sum2 x = {0.f, 0.f};
+#pragma unroll 4
+  for (int i = threadIdx.x; i < t.n; i += kThreads) {
+    const float2 p = __ldcg(reinterpret_cast<const float2*>(t.partial) + i);
+    const Sum2 o = {p.x, p.y};
+    if (MAX) x.hi = max_nan(x.hi, o.hi); else x.add(o);
+  }
+  x = block_total<MAX>(x, s_sum);
+  if (threadIdx.x == 0) {
+    const double v = (MAX ? (double)x.hi : sqrt(x.value())) * fabs((double)t.unscale);
+    const double f = (double)t.max_norm / (v + (double)t.eps);
+    s_factor = (float)((f < 1.0 || isnan(f) ? f : 1.0) * (double)t.unscale);
+    if (write) t.norm[0] = (float)v;
+  }
+  __syncthreads();
+  return s_factor;
+}
+
+template <bool MAX>
+__global__ void __launch_bounds__(kThreads) grad_total_kernel(const __grid_constant__ Total t) {
+  grid_dep_wait();
+  total_of<MAX>(t, true);
+}
+
+template <typename TI, typename TO>
+__device__ __forceinline__ void scale_run(const TI* p, TO* o, int64_t n, float f) {
+  const int head = head_of(p, n);
+  const int64_t units = (n - head) / 8;
+  const int rest = (int)(n - units * 8);
+  if ((int)threadIdx.x < rest) {
+    const int64_t i = (int)threadIdx.x < head ? threadIdx.x : units * 8 + threadIdx.x;
+    st_out(o + i, to_f(p[i]) * f);
+  }
+  p += head;
+  o += head;
+  const bool whole = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+  constexpr int kF = 2;
+  for (int64_t i = units - 1 - threadIdx.x; i >= 0; i -= kThreads * kF) {
+    Unit<TI> u[kF];
+#pragma unroll
+    for (int k = 0; k < kF; ++k)
+      if (i - k * kThreads >= 0) u[k].load(p + (i - k * kThreads) * 8);
+#pragma unroll
+    for (int k = 0; k < kF; ++k) {
+      if (i - k * kThreads < 0) break;
+      float e[8];
+      u[k].get(e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] *= f;
+      TO* const q = o + (i - k * kThreads) * 8;
+      if (whole) {
+        store_unit(q, e);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) st_out(q + j, e[j]);
+      }
     }
   }
 }
 
+template <int CAP, bool MAX>
+__global__ void __launch_bounds__(kThreads, 6) grad_scale_kernel(const __grid_constant__ GradTable<CAP> g,
+                                                                 const __grid_constant__ Total total, bool write) {
+  using B = __nv_bfloat16;
+  grid_dep_wait();
+  const float f = total_of<MAX>(total, write && blockIdx.x == 0);
+  for_run(g, true, [&](const GradTensor& t, int64_t first, int64_t last) {
+    if (f == 1.f && t.in == t.out) return;              // (in place: nothing changes)
+    const int64_t n = last - first;
+    if (t.types == 0) scale_run(reinterpret_cast<const float*>(t.in) + first, reinterpret_cast<float*>(t.out) + first, n, f);
+    else if (t.types == 3) scale_run(reinterpret_cast<const B*>(t.in) + first, reinterpret_cast<B*>(t.out) + first, n, f);
+    else if (t.types == 1) scale_run(reinterpret_cast<const B*>(t.in) + first, reinterpret_cast<float*>(t.out) + first, n, f);
+    else scale_run(reinterpret_cast<const float*>(t.in) + first, reinterpret_cast<B*>(t.out) + first, n, f);
+  });
+}
+
+// Tables of few tensors are a short parameter.
 constexpr int kSmall = 64, kLarge = 768;
 
-// Tables of at most CAP tensors, one launch each.
+// Calls launch(table, number of the launch) for tables of at most CAP tensors.
 template <int CAP, typename F>
 cudaError_t for_tables(const GradArgs& a, F launch) {
   GradTable<CAP> g;
-  int64_t base = 0;
+  int at = 0;
   for (int32_t i = 0; i < a.n;) {
     g.n = 0;
-    g.chunks = 0;
-    while (i < a.n && g.n < CAP) {
-      const int64_t chunks = ceil_div(a.counts[i], kChunk);
-      if (g.n > 0 && g.chunks + chunks > (1 << 30)) break;
-      if (chunks > 0) {
-        g.t[g.n++] = {a.in[i], a.out ? a.out[i] : nullptr, a.counts[i], g.chunks,
-                      (a.in_dtypes[i] == NSP_BF16 ? 1 : 0) |
-                          (a.out && a.out_dtypes[i] == NSP_BF16 ? 2 : 0)};
-        g.chunks += (int32_t)chunks;
-      }
-      ++i;
+    int64_t pieces = 0;
+    for (; i < a.n && g.n < CAP; ++i) {
+      const int64_t more = ceil_div(a.counts[i], kPiece);
+      if (more == 0) continue;
+      if (pieces + more > INT32_MAX) break;             // (one tensor has 2^29 pieces at most)
+      g.t[g.n++] = {a.in[i], a.out ? a.out[i] : nullptr, a.counts[i], (int32_t)pieces,
+                    (a.in_dtypes[i] == NSP_BF16 ? 1 : 0) | (a.out && a.out_dtypes[i] == NSP_BF16 ? 2 : 0)};
+      pieces += more;
     }
-    if (g.chunks == 0) break;
-    launch(g, base);
+    g.pieces = (int32_t)pieces;
+    if (g.n == 0) break;
+    const cudaError_t e = launch(g, at);
     count_launches(1);
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    base += g.chunks;
+    ++at;
   }
   return cudaSuccess;
 }
 
-template <int CAP>
+template <int CAP, bool MAX>
 cudaError_t run(const GradArgs& a, cudaStream_t s) {
-  float* const factor = reinterpret_cast<float*>(a.workspace);
-  Sum2* const partial = reinterpret_cast<Sum2*>(a.workspace + 256);
-  const int64_t most = (int64_t)num_sms() * 8;
-  int64_t chunks = 0;
-  for (int32_t i = 0; i < a.n; ++i) chunks += ceil_div(a.counts[i], kChunk);
-  cudaError_t e = for_tables<CAP>(a, [&](const GradTable<CAP>& g, int64_t base) {
-    grad_norm_kernel<CAP><<<(unsigned)std::min<int64_t>(g.chunks, most), kThreads, 0, s>>>(g, a.kind, partial + base);
+  Sum2* const partial = reinterpret_cast<Sum2*>(a.workspace);
+  Total total = {partial, 0, a.unscale, a.max_norm, a.eps, a.norm};
+  auto blocks = [](const GradTable<CAP>& g) { return (unsigned)std::min(g.pieces, kBlocks); };
+  cudaError_t e = for_tables<CAP>(a, [&](const GradTable<CAP>& g, int) {
+    grad_norm_kernel<CAP, MAX><<<blocks(g), kThreads, 0, s>>>(g, partial + total.n);
+    total.n += (int)blocks(g);
+    return cudaGetLastError();
   });
   if (e != cudaSuccess) return e;
-  grad_total_kernel<<<1, kSumThreads, 0, s>>>(partial, chunks, a.kind, a.unscale, a.max_norm, a.eps, a.norm, factor);
-  count_launches(1);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !a.out) return e;
-  return for_tables<CAP>(a, [&](const GradTable<CAP>& g, int64_t) {
-    grad_scale_kernel<CAP><<<(unsigned)std::min<int64_t>(g.chunks, most), kThreads, 0, s>>>(g, factor);
+  if (!a.out || total.n == 0) {
+    count_launches(1);
+    return launch_dependent(grad_total_kernel<MAX>, dim3(1), dim3(kThreads), 0, s, total);
+  }
+  return for_tables<CAP>(a, [&](const GradTable<CAP>& g, int at) {
+    return launch_dependent(grad_scale_kernel<CAP, MAX>, dim3(blocks(g)), dim3(kThreads), 0, s, g, total, at == 0);
   });
 }
 
 }  // namespace
 
+// Sums of at most kBlocks blocks of each launch: of kSmall tensors or fewer one, then
+// one for kLarge tensors, or for 2^31 pieces.
 size_t grad_ws_size(const int64_t* counts, int32_t n) {
-  size_t chunks = 0;
-  for (int32_t i = 0; i < n; ++i) chunks += (size_t)ceil_div(counts[i], kChunk);
-  return 256 + chunks * sizeof(Sum2);
+  int64_t pieces = 0;
+  for (int32_t i = 0; i < n; ++i) pieces += ceil_div(counts[i], kPiece);
+  const int64_t launches = 1 + n / kLarge + 2 * (pieces >> 31);
+  return (size_t)std::max<int64_t>(1, std::min<int64_t>(launches * kBlocks, pieces)) * sizeof(Sum2);
 }
 
 cudaError_t launch_grads(const GradArgs& a, cudaStream_t s) {
-  return a.n <= kSmall ? run<kSmall>(a, s) : run<kLarge>(a, s);
+  if (a.kind == NSP_NORM_2) return a.n <= kSmall ? run<kSmall, false>(a, s) : run<kLarge, false>(a, s);
+  return a.n <= kSmall ? run<kSmall, true>(a, s) : run<kLarge, true>(a, s);
 }
 
 }  // namespace nsp

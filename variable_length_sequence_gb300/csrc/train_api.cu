@@ -412,36 +412,34 @@ static int32_t grads_check(const GradArgs& a, size_t workspace_bytes) {
 // their addresses, none of which may begin before the end of an earlier output, nor an
 // output before the end of any earlier array.  An output in its own input's place is one.
 static bool grads_clash(const GradArgs& a) {
-  constexpr uint32_t kWorkspace = 2 * kMaxGrads, kNorm = kWorkspace + 1;
-  uint32_t at[2 * kMaxGrads + 2];
-  int32_t n = 0;
-  const int64_t ws = (int64_t)grad_ws_size(a.counts, a.n);
-  auto in_place = [&](uint32_t i) { return a.out && a.out[i] == a.in[i]; };
-  auto base = [&](uint32_t id) {
-    const void* p = id == kWorkspace ? a.workspace
-                    : id == kNorm    ? a.norm
-                    : (id & 1)       ? a.out[id >> 1]
-                                     : a.in[id >> 1];
-    return reinterpret_cast<uintptr_t>(p);
+  struct Extent {
+    uintptr_t base;
+    int64_t bytes;                          // negative: written
   };
+  const int64_t ws = (int64_t)grad_ws_size(a.counts, a.n);
+  const Span outs[] = {packed(a.workspace, 1, ws), packed(a.norm, 1, 4)};
+  if (overlap(outs[0], outs[1])) return true;
+  Extent at[2 * kMaxGrads];
+  int32_t n = 0;
   for (int32_t i = 0; i < a.n; ++i) {
     if (a.counts[i] == 0) continue;
-    at[n++] = 2u * i;
-    if (a.out && !in_place(i)) at[n++] = 2u * i + 1;
-    if (in_place(i) && a.out_dtypes[i] != a.in_dtypes[i]) return true;
+    const bool in_place = a.out && a.out[i] == a.in[i];
+    if (in_place && a.out_dtypes[i] != a.in_dtypes[i]) return true;
+    const Span in = packed(a.in[i], 1, a.counts[i] * elem_bytes(a.in_dtypes[i]));
+    if (overlap(in, outs[0]) || overlap(in, outs[1])) return true;
+    at[n++] = {in.base, in_place ? -in.row : in.row};
+    if (!a.out || in_place) continue;
+    const Span out = packed(a.out[i], 1, a.counts[i] * elem_bytes(a.out_dtypes[i]));
+    if (overlap(out, outs[0]) || overlap(out, outs[1])) return true;
+    at[n++] = {out.base, -out.row};
   }
-  at[n++] = kWorkspace;
-  at[n++] = kNorm;
-  std::sort(at, at + n, [&](uint32_t x, uint32_t y) { return base(x) < base(y); });
+  if (!a.out) return false;                 // nothing else is written
+  std::sort(at, at + n, [](const Extent& x, const Extent& y) { return x.base < y.base; });
   uintptr_t end = 0, written_end = 0;
   for (int32_t i = 0; i < n; ++i) {
-    const uint32_t id = at[i], g = id >> 1;
-    const bool written = id >= kWorkspace || (id & 1) || in_place(g);
-    const int64_t bytes = id == kWorkspace ? ws
-                          : id == kNorm    ? 4
-                          : a.counts[g] * elem_bytes((id & 1) ? a.out_dtypes[g] : a.in_dtypes[g]);
-    if (base(id) < (written ? end : written_end)) return true;
-    const uintptr_t e = base(id) + (uintptr_t)bytes;
+    const bool written = at[i].bytes < 0;
+    if (at[i].base < (written ? end : written_end)) return true;
+    const uintptr_t e = at[i].base + (uintptr_t)(written ? -at[i].bytes : at[i].bytes);
     end = std::max(end, e);
     if (written) written_end = std::max(written_end, e);
   }

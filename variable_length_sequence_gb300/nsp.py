@@ -8,7 +8,9 @@ loudly when the library has not been built.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
+import operator
 import os
 import re
 from typing import Optional, Sequence
@@ -1297,26 +1299,36 @@ def preference_loss(logp, targets, cu_seqlens, ref=None, kind="sigmoid", beta=0.
 NORMS = {2: 0, 2.0: 0, float("inf"): 1}
 
 
+# (hundreds of tensors a call: one C loop over them for each thing looked at)
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+_get_dtype = operator.attrgetter("dtype")
+
+
 def _gradients(fn, grads, dev=None):
     """HOST arrays of the gradients' pointers, counts and types, and their device."""
     n = len(grads)
     if n == 0:
         raise ValueError(f"{fn}: no gradients")
-    at = {t.get_device() for t in grads}
+    at = set(map(_get_device, grads))
     if dev is None:
         if -1 in at:
             raise ValueError(f"{fn}: a gradient is not on a CUDA device")
         dev = torch.cuda.current_device()
     if at != {dev}:
         raise ValueError(f"{fn}: a gradient is not on the current device {dev}")
-    if not all([t.is_contiguous() for t in grads]):
+    if not all(map(_is_contiguous, grads)):
         raise ValueError(f"{fn}: libnsp takes contiguous tensors only")
-    try:
-        types = [_DTYPES[t.dtype] for t in grads]
-    except KeyError as e:
-        raise TypeError(f"{fn}: unsupported dtype {e.args[0]}") from None
-    return ((_vp * n)(*[t.data_ptr() for t in grads]), (_i64 * n)(*[t.numel() for t in grads]),
-            (_i32 * n)(*types), n, dev)
+    types = list(map(_DTYPES.get, map(_get_dtype, grads)))
+    if None in types:
+        raise TypeError(f"{fn}: unsupported dtype {grads[types.index(None)].dtype}")
+    return (array.array("Q", map(_data_ptr, grads)), array.array("q", map(_numel, grads)),
+            array.array("i", types), n, dev)
+
+
+def _at(a) -> int:
+    """Address of an array's elements."""
+    return a.buffer_info()[0]
 
 
 def grad_norm(grads, norm_type=2, unscale=1.0, workspace=None, stream=None):
@@ -1328,8 +1340,8 @@ def grad_norm(grads, norm_type=2, unscale=1.0, workspace=None, stream=None):
     ptrs, counts, types, n, dev = _gradients(fn, grads)
     lib = load()
     norm = _new(stream, grads[0], (1,), torch.float32)
-    ws = _workspace(fn, stream, norm, lib.nsp_grad_norm_workspace_size(counts, n), workspace)
-    st = lib.nsp_grad_norm(ptrs, counts, types, n, NORMS[norm_type], unscale, norm.data_ptr(), _ptr(ws),
+    ws = _workspace(fn, stream, norm, lib.nsp_grad_norm_workspace_size(_at(counts), n), workspace)
+    st = lib.nsp_grad_norm(_at(ptrs), _at(counts), _at(types), n, NORMS[norm_type], unscale, norm.data_ptr(), _ptr(ws),
                            ws.numel(), _stream_of(stream, dev))
     _check("nsp_grad_norm", st)
     return norm
@@ -1346,13 +1358,13 @@ def clip_grads(grads, max_norm, norm_type=2, unscale=1.0, eps=1e-6, out=None, wo
     ptrs, counts, types, n, dev = _gradients(fn, grads)
     out_ptrs, out_types = ptrs, types
     if out is not None:
-        if len(out) != n or any([a.shape != b.shape for a, b in zip(grads, out)]):
-            raise ValueError(f"{fn}: out are as many tensors of the gradients' shapes")
-        out_ptrs, _, out_types, _, _ = _gradients(fn, out, dev)
+        out_ptrs, out_counts, out_types, _, _ = _gradients(fn, out, dev)
+        if out_counts != counts:
+            raise ValueError(f"{fn}: out are as many tensors of the gradients' sizes")
     lib = load()
     norm = _new(stream, grads[0], (1,), torch.float32)
-    ws = _workspace(fn, stream, norm, lib.nsp_grad_norm_workspace_size(counts, n), workspace)
-    st = lib.nsp_grad_clip(ptrs, out_ptrs, counts, types, out_types, n, NORMS[norm_type], unscale, max_norm,
+    ws = _workspace(fn, stream, norm, lib.nsp_grad_norm_workspace_size(_at(counts), n), workspace)
+    st = lib.nsp_grad_clip(_at(ptrs), _at(out_ptrs), _at(counts), _at(types), _at(out_types), n, NORMS[norm_type], unscale, max_norm,
                            eps, norm.data_ptr(), _ptr(ws), ws.numel(), _stream_of(stream, dev))
     _check("nsp_grad_clip", st)
     return norm
