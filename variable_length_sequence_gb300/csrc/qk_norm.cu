@@ -131,20 +131,22 @@ __global__ void __launch_bounds__(kThreads) qk_element_kernel(const __grid_const
 //
 // A team of lanes owns a token's heads (or a part of them) and computes the sines and
 // cosines of its pairs once; a lane holds U units of two 16-byte vectors of a head: both
-// halves of its pairs, or two neighbours.  The weights enter the turn's coefficients, so
+// halves of its pairs, or any two.  The weights enter the turn's coefficients, so
 // that a pair costs two products, two FMAs and the row's factor.
 
 // The columns of a lane's unit; `second`: its second vector is there; turned: bit v, vector
-// v's pairs are rotated.
+// v's pairs are rotated.  (Neighbouring lanes' vectors are neighbours in memory: lanes 32
+// bytes apart would take half of every sector they touch.)
 template <int N, bool INTER>
 __device__ __forceinline__ bool unit_of(int d, int rot, int u, int& c0, int& c1, bool& second, int& turned) {
-  const int r = rot / 2 / N;
-  if (INTER || u >= r) {
-    c0 = INTER ? 2 * u * N : rot + 2 * (u - r) * N;
-    c1 = c0 + N;
-    second = c1 < d;
+  const int r = INTER ? 0 : rot / 2 / N;
+  if (u >= r) {
+    const int first = INTER ? 0 : rot, vecs = (d - first) / N, half = (vecs + 1) / 2, v = u - r;
+    c0 = first + v * N;
+    c1 = c0 + half * N;
+    second = v + half < vecs;
     turned = INTER ? (c0 < rot ? 1 : 0) | (c1 < rot ? 2 : 0) : 0;
-    return c0 < d;
+    return v < half;
   }
   c0 = u * N;
   c1 = c0 + rot / 2;
@@ -210,14 +212,15 @@ __device__ __forceinline__ float sum2(uint64_t x) {
 // Cosines and sines of a unit's pairs: halves: pair j of both vectors; neighbours: pairs j
 // of the first, N / 2 + j of the second.  Columns that are not rotated: 1 and 0.
 template <int N, bool INTER>
-__device__ __forceinline__ void turns(const QkArgs& a, const uint64_t* s_fx, int64_t pos, int u, int turned,
-                                      bool inverse, float (&c)[N], float (&s)[N]) {
+__device__ __forceinline__ void turns(const QkArgs& a, const uint64_t* s_fx, int64_t pos, int c0, int c1,
+                                      int turned, bool inverse, float (&c)[N], float (&s)[N]) {
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     c[j] = 1.f;
     s[j] = 0.f;
     const bool on = INTER ? (turned >> (j >= N / 2 ? 1 : 0)) & 1 : turned != 0;
-    if (on) turn(pos, s_fx[u * N + j], a.mscale, inverse, c[j], s[j]);
+    const int pair = INTER ? (j < N / 2 ? c0 / 2 + j : c1 / 2 + j - N / 2) : c0 + j;
+    if (on) turn(pos, s_fx[pair], a.mscale, inverse, c[j], s[j]);
   }
 }
 
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kVecThreads, U == 1 ? 4 : 2) qk_vec_kernel(con
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           float c[N], s[N], w0[N], w1[N];
-          turns<N, INTER>(a, s_fx, pos, lane + i * LANES, un.turned[i], false, c, s);
+          turns<N, INTER>(a, s_fx, pos, un.c0[i], un.c1[i], un.turned[i], false, c, s);
           load_weight<T>(q.weight, un.c0[i], un.first[i], w0);
           load_weight<T>(q.weight, un.c1[i], un.second[i], w1);
 #pragma unroll
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) qk_vec_bwd_kernel(co
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       float c[N], s[N];
-      turns<N, INTER>(a, s_fx, pos, lane + i * LANES, un.turned[i], true, c, s);
+      turns<N, INTER>(a, s_fx, pos, un.c0[i], un.c1[i], un.turned[i], true, c, s);
       if constexpr (INTER) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {

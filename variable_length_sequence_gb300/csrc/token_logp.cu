@@ -238,10 +238,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
 // each).  Every thread copies its own vectors of the rows ahead into its own places of
 // shared memory, kSlots of them at any time, and reads only what it copied itself, so
 // that the ring needs no barrier and no wait but the copies' own.
-constexpr int kRingThreads = 1024, kRingWarps = kRingThreads / 32;
-constexpr int kSlots = 12;                           // 16-byte places of a thread
-constexpr int kRingBytes = kSlots * kRingThreads * 16;
-constexpr int kMaxSlice = 8;                         // vectors of a thread in a policy row
+constexpr int kScoreThreads = 1024, kScoreSlots = 12;    // 16-byte places of a thread
+constexpr int kPolicyThreads = 1024, kPolicySlots = 12, kMaxSlice = 8;   // vectors of a thread in a row
+constexpr int kRingBytes = 12 * 1024 * 16;
+static_assert(kScoreThreads * kScoreSlots * 16 == kRingBytes && kPolicyThreads * kPolicySlots * 16 == kRingBytes, "");
 
 __device__ __forceinline__ void copy16(uint4* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -261,7 +261,7 @@ __device__ __forceinline__ void join_warp(float& m, float& s) {
 }
 
 // A row's whole vectors start at its first 16-byte border, the thread's own ones at
-// `vec` of them, kRingThreads apart, while `left` > 0 of the block's slice; the elements
+// `vec` of them, the block's threads apart, while `left` > 0 of the block's slice; the elements
 // before and behind the vectors are rank 0's first threads'.
 template <typename T>
 struct Row {
@@ -337,7 +337,7 @@ struct RowWalk {
 
 // The copies: `row` is the thread's first vector of the row ahead.  The rows on their way
 // wait in a queue of every warp's own.
-template <typename T>
+template <typename T, int THREADS>
 struct RowCopies {
   const RowArgs& a;
   const int rank, log_ranks;
@@ -365,8 +365,8 @@ struct RowCopies {
   // vector i of the row ahead; where it has none the place holds -infinity
   __device__ __forceinline__ void copy(int slot, int i) {
     if (!more) return;
-    uint4* const to = ring + slot * kRingThreads;
-    if (i * kRingThreads < left) copy16(to, row + i * kRingThreads);
+    uint4* const to = ring + slot * THREADS;
+    if (i * THREADS < left) copy16(to, row + i * THREADS);
     else *to = make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
   }
 };
@@ -404,20 +404,20 @@ __device__ __forceinline__ float element(const uint4& u, int k) {
 }
 
 // Scores alone: a row a block, in groups of kGroup vectors of a thread.
-constexpr int kGroup = 4, kGroups = kSlots / kGroup;
+constexpr int kGroup = 4, kGroups = kScoreSlots / kGroup;
 template <typename T>
-__global__ void __launch_bounds__(kRingThreads, 1) score_ring_kernel(const __grid_constant__ RowArgs a,
+__global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __grid_constant__ RowArgs a,
                                                                      const int groups) {
   constexpr int N = Vec<T>::N, kLogN = N == 8 ? 3 : 2;
   extern __shared__ __align__(16) uint4 s_ring[];
-  __shared__ float2 s_part[2][kRingWarps];
+  __shared__ float2 s_part[2][(kScoreThreads / 32)];
   __shared__ float s_target[2];
-  __shared__ int2 s_queue[kRingWarps][16];
+  __shared__ int2 s_queue[(kScoreThreads / 32)][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = a.scale * kLog2e;
   const uint64_t c2 = f2_pack(c, c);
   grid_dep_wait();
-  RowCopies<T> ahead(a, 0, 0, s_ring + tid, s_queue[warp]);
+  RowCopies<T, kScoreThreads> ahead(a, 0, 0, s_ring + tid, s_queue[warp]);
   int g_ahead = 0;
   auto copy_group = [&](int slot) {
     if (g_ahead == 0) ahead.next_row();
@@ -440,19 +440,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) score_ring_kernel(const __gri
     const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
     // the target's vector among the thread's, if it is one of them, and where in it
     const unsigned dist = (unsigned)((y - r.head) >> kLogN) - (unsigned)tid;
-    const int mine = y >= r.head && (int)dist < r.left && dist % kRingThreads == 0 ? (int)(dist / kRingThreads) : -1;
+    const int mine = y >= r.head && (int)dist < r.left && dist % kScoreThreads == 0 ? (int)(dist / kScoreThreads) : -1;
     RowSum<T> sum;
     for (int g = 0; g < groups; ++g) {
       copy_wait<kGroups - 1>();
       uint4 u[kGroup];
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
-        u[i] = ahead.ring[(slot + i) * kRingThreads];
+        u[i] = ahead.ring[(slot + i) * kScoreThreads];
         if (mine == g * kGroup + i) s_target[par] = element<T>(u[i], (y - r.head) & (N - 1));
       }
       sum.add(u, c, c2);
       copy_group(slot);
-      slot = slot + kGroup == kSlots ? 0 : slot + kGroup;
+      slot = slot + kGroup == kScoreSlots ? 0 : slot + kGroup;
     }
     float m = sum.m, s = sum.s;
     if (extra) {
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) score_ring_kernel(const __gri
     if (lane == 0) s_part[par][warp] = make_float2(m, s);
     __syncthreads();
     if (warp != 0) continue;
-    const float2 part = lane < kRingWarps ? s_part[par][lane] : make_float2(-INFINITY, 0.f);
+    const float2 part = lane < (kScoreThreads / 32) ? s_part[par][lane] : make_float2(-INFINITY, 0.f);
     m = part.x;
     s = part.y;
     join_warp(m, s);
@@ -483,23 +483,23 @@ __global__ void __launch_bounds__(kRingThreads, 1) score_ring_kernel(const __gri
 // The policy loss: a cluster of blocks a row, SLICE vectors of a thread, which stay in
 // their places of the ring until the gradient has been taken from them.
 template <typename T, int SLICE>
-__global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __grid_constant__ RowArgs a,
+__global__ void __launch_bounds__(kPolicyThreads, 1) policy_ring_kernel(const __grid_constant__ RowArgs a,
                                                                       const int log_ranks) {
   constexpr int N = Vec<T>::N, kLogN = N == 8 ? 3 : 2;
   extern __shared__ __align__(16) uint4 s_ring[];
-  __shared__ float2 s_part[2][kMaxRanks * kRingWarps];
+  __shared__ float2 s_part[2][kMaxRanks * (kPolicyThreads / 32)];
   __shared__ float2 s_target[2];                     // x: the target's logit
   __shared__ float4 s_coef;                          // p = 2^(c x + .x), gradient .y p, .z at the target
-  __shared__ int2 s_queue[kRingWarps][16];
+  __shared__ int2 s_queue[(kPolicyThreads / 32)][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ranks = 1 << log_ranks;
   const int rank = (int)(blockIdx.x & (unsigned)(ranks - 1));
   grid_dep_wait();
   if (status_bad(a.p.hdr)) return;
   const float c = a.scale * kLog2e;
   const uint64_t c2 = f2_pack(c, c);
-  RowCopies<T> ahead(a, rank, log_ranks, s_ring + tid, s_queue[warp]);
+  RowCopies<T, kPolicyThreads> ahead(a, rank, log_ranks, s_ring + tid, s_queue[warp]);
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
+  for (int i = 0; i < kPolicySlots; ++i) {
     if (i % SLICE == 0) ahead.next_row();
     ahead.copy(i, i % SLICE);
     copy_commit();
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __gr
       bool whole;
       T* const dx = gradient_row<T>(a, t, r.x, whole);
       const float zero[N] = {};
-      for (int i = 0; i < r.left; i += kRingThreads)
+      for (int i = 0; i < r.left; i += kPolicyThreads)
         store_vec<T>(dx + r.head + (int64_t)(r.vec + i) * N, whole, zero);
       if (rank == 0 && tid < a.vocab - r.nvec * N) st_out(dx + (tid < r.head ? tid : r.nvec * N + tid), 0.f);
     }
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __gr
     const int ecol = tid < r.head ? tid : r.nvec * N + tid;
     const float xe = extra ? to_f(r.x[ecol]) : -INFINITY;
     const unsigned dist = (unsigned)((y - r.head) >> kLogN) - (unsigned)r.vec;
-    const int mine = y >= r.head && (int)dist < r.left && dist % kRingThreads == 0 ? (int)(dist / kRingThreads) : -1;
+    const int mine = y >= r.head && (int)dist < r.left && dist % kPolicyThreads == 0 ? (int)(dist / kPolicyThreads) : -1;
     const int yi = (y - r.head) & (N - 1);
     PolicyScalars sc = {};
     if (warp == 0) {
@@ -553,23 +553,23 @@ __global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __gr
     };
     auto place = [&](int i) {
       const int p = slot0 + i;
-      return p >= kSlots ? p - kSlots : p;
+      return p >= kPolicySlots ? p - kPolicySlots : p;
     };
     RowSum<T> sum;
     constexpr int G = SLICE % 2 == 0 ? 2 : 1;
-    // (kSlots - 1 - i groups are behind vector i of the row)
+    // (kPolicySlots - 1 - i groups are behind vector i of the row)
     auto add = [&](int i) {
       uint4 u[G];
 #pragma unroll
       for (int j = 0; j < G; ++j) {
-        u[j] = ahead.ring[place(i + j) * kRingThreads];
+        u[j] = ahead.ring[place(i + j) * kPolicyThreads];
         if (mine == i + j) publish(element<T>(u[j], yi));
       }
       sum.add(u, c, c2);
     };
 #define NSP_WAIT_ADD(i)                          \
   if constexpr ((i) < SLICE) {                   \
-    copy_wait<kSlots - (i) - G>();               \
+    copy_wait<kPolicySlots - (i) - G>();               \
     add(i);                                      \
   }
     if constexpr (G == 2) {
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __gr
     // (two sets of states in turn: a block that writes the next row's but one has passed the
     // next row's barrier, and so has every block of the cluster, behind reading this row's)
     if (ranks > 1) {
-      if (lane < ranks) st_peer(&s_part[par][rank * kRingWarps + warp], lane, make_float2(m, s));
+      if (lane < ranks) st_peer(&s_part[par][rank * (kPolicyThreads / 32) + warp], lane, make_float2(m, s));
       __syncwarp();
       cluster_arrive();
       cluster_wait();
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __gr
     if (warp == 0) {                  // one warp for all: the others' issue slots are dear
       m = -INFINITY;
       s = 0.f;
-      for (int i = lane; i < ranks * kRingWarps; i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
+      for (int i = lane; i < ranks * (kPolicyThreads / 32); i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
       join_warp(m, s);
       const float rest2 = log2f(s);
       float logp = (fmaf(s_target[par].x, c, -m) - rest2) * kLn2;
@@ -626,8 +626,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __gr
     T* const out = dx + r.head + (int64_t)r.vec * N;
 #pragma unroll
     for (int i = 0; i < SLICE; ++i) {
-      if (i * kRingThreads < r.left) {
-        const uint4 u = ahead.ring[place(i) * kRingThreads];
+      if (i * kPolicyThreads < r.left) {
+        const uint4 u = ahead.ring[place(i) * kPolicyThreads];
         float o[N];
         Vec<T>::unpack(u, o);
 #pragma unroll
@@ -640,11 +640,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) policy_ring_kernel(const __gr
 #pragma unroll
           for (int j = 0; j < N; ++j) o[j] += j == yi ? sg : 0.f;
         }
-        store_vec<T>(out + i * kRingThreads * N, whole, o);
+        store_vec<T>(out + i * kPolicyThreads * N, whole, o);
       }
-      // the place takes the vector kSlots further on
-      if ((kSlots + i) % SLICE == 0) ahead.next_row();
-      ahead.copy(place(i), (kSlots + i) % SLICE);
+      // the place takes the vector kPolicySlots further on
+      if ((kPolicySlots + i) % SLICE == 0) ahead.next_row();
+      ahead.copy(place(i), (kPolicySlots + i) % SLICE);
       copy_commit();
     }
     if (extra) st_out(dx + ecol, ex2(fmaf(xe, c, n)) * f + (ecol == y ? sg : 0.f));
@@ -674,8 +674,8 @@ cudaError_t go_score_ring(const RowArgs& a, cudaStream_t s) {
   const int64_t nvec = std::max(1, a.vocab / Vec<T>::N);
   const int64_t blocks = std::min<int64_t>(a.rows, num_sms());
   count_launches(1);
-  return launch_dependent(score_ring_kernel<T>, dim3((unsigned)blocks), dim3(kRingThreads), kRingBytes, s, a,
-                          (int)ceil_div(nvec, kGroup * kRingThreads));
+  return launch_dependent(score_ring_kernel<T>, dim3((unsigned)blocks), dim3(kScoreThreads), kRingBytes, s, a,
+                          (int)ceil_div(nvec, kGroup * kScoreThreads));
 }
 
 template <typename T, int SLICE>
@@ -689,7 +689,7 @@ cudaError_t go_policy_ring(const RowArgs& a, int log_ranks, cudaStream_t s) {
   const int ranks = 1 << log_ranks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(num_sms() / ranks * ranks));
-  cfg.blockDim = dim3(kRingThreads);
+  cfg.blockDim = dim3(kPolicyThreads);
   cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -734,8 +734,8 @@ cudaError_t go(const RowArgs& a, int ranks, cudaStream_t s) {
 // where the ring has no room for the row.
 bool policy_slice(int64_t nvec, int& log_ranks, int64_t& slice) {
   log_ranks = 0;
-  while (log_ranks < 3 && nvec > ((int64_t)kMaxSlice * kRingThreads << log_ranks)) ++log_ranks;
-  slice = ceil_div(ceil_div(nvec, 1 << log_ranks), kRingThreads);
+  while (log_ranks < 3 && nvec > ((int64_t)kMaxSlice * kPolicyThreads << log_ranks)) ++log_ranks;
+  slice = ceil_div(ceil_div(nvec, 1 << log_ranks), kPolicyThreads);
   return slice <= kMaxSlice;
 }
 
