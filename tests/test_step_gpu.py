@@ -709,3 +709,148 @@ def test_grad_norm_far_elements(nsp):
     assert nsp.grad_norm([t]) == 7.0
     nsp.clip_grads([t], 3.5)
     assert abs(float(t[-1]) - 2.0) < 0.01 and abs(float(t[0]) - 0.5) < 0.01 and not t[1:-3].any()
+
+
+# ----------------------------------------------------------------------------- many long rows
+
+def scattered(seed, T, V, every=1):
+    """Targets of about half of every `every`-th row: runs of scored and other rows, single ones."""
+    rng = np.random.default_rng(seed)
+    y = np.full(T, -1)
+    at = np.arange(0, T, every)
+    on = np.repeat(rng.random(len(at) // 7 + 1) < 0.6, 7)[:len(at)] ^ (rng.random(len(at)) < 0.1)
+    y[at[on]] = rng.integers(0, V, on.sum())
+    y[at[0]], y[at[-1]] = 0, V - 1
+    return torch.tensor(y, dtype=torch.int32, device="cuda")
+
+
+def logits_on(seed, y, V, dt, stride=None, shift=0):
+    """Logits whose rows without a target are NaN, rows `stride` apart."""
+    T, stride = len(y), stride or V
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    flat = torch.full((T * stride + shift + 64,), float("nan"), dtype=dt, device="cuda")
+    x = flat[shift:shift + T * stride].view(T, stride)[:, :V]
+    rows = torch.nonzero(y >= 0)[:, 0]
+    x[rows] = (torch.randn((len(rows), V), generator=g, device="cuda") * 2.5).to(dt)
+    return x, rows
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("T,V,stride,shift", [(609, 4200, None, 0), (700, 4111, None, 3), (1300, 8192, 8200, 0),
+                                              (640, 20001, None, 1), (650, 33000, None, 0), (5000, 5003, None, 0)])
+def test_token_logp_many_rows(nsp, dt, T, V, stride, shift):
+    y = scattered(100, T, V)
+    x, rows = logits_on(101, y, V, dt, stride, shift)
+    logp, lse = nsp.token_logp(x, y, scale=SCALE)
+    assert (logp[y < 0] == 0).all() and (lse[y < 0] == 0).all()
+    check_logp(x[rows], y[rows], logp[rows], lse[rows])
+    again = nsp.token_logp(x, y, scale=SCALE)
+    assert torch.equal(again[0], logp) and torch.equal(again[1], lse)
+    # whatever the way: one row alone
+    for r in (int(rows[0]), int(rows[-1])):
+        one, _ = nsp.token_logp(x[r:r + 1], y[r:r + 1], scale=SCALE)
+        err = 2 * float(lse_error(f64(x[r:r + 1]))[0]) + 4 * E * abs(float(one[0]))
+        assert abs(float(one[0]) - float(logp[r])) <= err
+    g = randn(102, T, dt=F32)
+    dx = nsp.token_logp_bwd(x, y, lse, g, scale=SCALE)
+    assert not dx[y < 0].any()
+    check_dlogits(x[rows], y[rows], g[rows], dx[rows], dt)
+    none = torch.full_like(y, -1)
+    logp, lse = nsp.token_logp(x, none)
+    assert not logp.any() and not lse.any()
+
+
+def test_token_logp_many_rows_special(nsp):
+    """NaN, infinities and targets past the vocabulary stay in their rows, also where many
+    rows are on their way at once."""
+    T, V = 700, 9000
+    x = randn(103, T, V, dt=F32)
+    y = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(104), dtype=torch.int32).cuda()
+    x[10, 5] = x[200, V - 1] = float("nan")
+    x[11, 17] = float("inf")
+    x[12] = float("-inf")
+    x[13, 40:] = float("-inf")
+    y[13] = 3
+    y[14] = V
+    y[600] = 2 ** 31 - 1
+    logp, lse = nsp.token_logp(x, y)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[[10, 11, 12, 14, 200, 600]] = True
+    assert torch.isnan(logp[bad]).all() and torch.isfinite(logp[~bad]).all() and torch.isfinite(lse[14])
+    check_logp(x[~bad], y[~bad], logp[~bad], lse[~bad], 1.0)
+
+
+@pytest.mark.parametrize("dt,T,V,stride,shift,every", [
+    (BF16, 612, 4200, None, 0, 1), (F32, 700, 4111, None, 3, 1), (BF16, 640, 20001, None, 1, 1),
+    (F32, 620, 12288, None, 0, 1), (BF16, 1000, 33000, 33008, 0, 3), (F32, 310, 50001, None, 0, 2),
+    (BF16, 330, 131072, None, 0, 4), (BF16, 320, 140001, None, 1, 5), (F32, 200, 140000, None, 0, 3),
+    (BF16, 160, 300001, None, 0, 4), (F32, 100, 200000, None, 0, 2), (BF16, 620, 49999, None, 0, 2)])
+@pytest.mark.parametrize("mean", ["documents", "tokens"])
+def test_policy_loss_logits_many_rows(nsp, dt, T, V, stride, shift, every, mean):
+    """Rows shared by up to eight blocks, odd vocabularies at any distance from a 16-byte
+    border; rows behind the last document; outputs whole, in place the same bits."""
+    lens = [T // 3, 0, 1, T // 2, T - T // 3 - T // 2 - 4]
+    cu, y = cu_of(lens), scattered(110, T, V, every)
+    x, _ = logits_on(111, y, V, dt, stride, shift)
+    scored = y.clone()
+    scored[sum(lens):] = -1
+    rows = torch.nonzero(scored >= 0)[:, 0]
+    rng = np.random.default_rng(112)
+    lp = np.zeros(T)
+    r = rows.cpu().numpy()
+    lp[r] = S.token_logp(f64(x[rows]), scored[rows].cpu().numpy(), SCALE)[0]
+    d = rng.normal(size=T) * 0.3
+    for border in (np.log(0.8), np.log(1.25)):
+        d = np.where(np.abs(d - border) < 1e-3, border + 2e-3, d)
+    old, ref = (torch.tensor(lp + o, dtype=torch.float32, device="cuda") for o in (-d, rng.normal(size=T) * 0.5))
+    adv = torch.tensor(rng.normal(size=len(lens)), dtype=torch.float32, device="cuda")
+    kw = dict(clip_low=0.2, clip_high=0.25, kl_coef=0.07, mean=mean)
+    out = torch.full((T * (stride or V) + shift + 64,), 7.0, dtype=dt, device="cuda")
+    view = out[shift:shift + T * (stride or V)].view(T, stride or V)[:, :V]
+    stats, logp, dx = nsp.policy_loss_logits(x, y, old, adv, cu, ref=ref, scale=SCALE, out=view, **kw)
+    assert (logp[scored < 0] == 0).all()
+    check_logp(x[rows], scored[rows], logp[rows], None)
+    dl_ref = S.policy_loss(lp, f64(old), f64(ref), f64(adv), scored.cpu().numpy(), cu.cpu().numpy(),
+                           float(np.float32(0.2)), 0.25, float(np.float32(0.07)), mean)[1]
+    two, dl = nsp.policy_loss(logp, y, old, adv, cu, ref=ref, **kw)
+    err = np.zeros(T)
+    err[r] = lse_error(f64(x[rows])) + 2 * E * np.abs(lp[r])
+    lw = torch.tensor(lp, device="cuda")
+    check_policy(lw, scored, old, ref, adv, cu, stats, dl, kw, logp_err=err)
+    torch.testing.assert_close(stats, two, rtol=8 * E, atol=8 * E * float(two.abs().max()))
+    dl_err = np.abs(f64(dl) - dl_ref) + 4 * E * np.abs(dl_ref)
+    check_dlogits(x[rows], scored[rows], dl_ref[r], dx[rows], dt, dlogp_err=SCALE * dl_err[r])
+    assert not dx[scored < 0].any()
+    keep = view.clone()
+    view[:] = 7.0
+    assert (out == 7).all()
+    # another distance from the border, and in place
+    two, _, other = nsp.policy_loss_logits(x, y, old, adv, cu, ref=ref, scale=SCALE,
+                                           out=torch.empty(T * V + 1, dtype=dt, device="cuda")[1:].view(T, V), **kw)
+    assert torch.equal(other, keep) and torch.equal(two, stats)
+    _, _, same = nsp.policy_loss_logits(x, y, old, adv, cu, ref=ref, scale=SCALE, out=x, **kw)
+    assert torch.equal(same, keep)
+
+
+def test_policy_loss_logits_many_rows_edges(nsp):
+    """Nothing scored, a bad cu_seqlens, a target past the vocabulary."""
+    T, V = 700, 5000
+    x = randn(120, T, V)
+    y = scattered(121, T, V)
+    old, adv = -torch.rand(T, device="cuda"), torch.ones(2, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    none = torch.full_like(y, -1)
+    stats, logp, dx = nsp.policy_loss_logits(x, none, old, adv, cu_of([300, 400]), workspace=ws)
+    assert not stats.any() and not logp.any() and not dx.any()
+    keep = x.clone()
+    bad = torch.tensor([0, 500, 400], dtype=torch.int32, device="cuda")
+    nsp.policy_loss_logits(x, y, old, adv, bad, workspace=ws, out=x)
+    assert nsp.nsp_status_query(ws) == nsp.NSP_ERR_INVALID and torch.equal(x, keep)
+    good, _, dgood = nsp.policy_loss_logits(x, y, old, adv, cu_of([300, 400]), workspace=ws)
+    assert nsp.nsp_status_query(ws) == nsp.NSP_OK
+    y2, row = y.clone(), int(torch.nonzero(y >= 0)[5, 0])
+    y2[row] = V + 3
+    stats, logp, dx = nsp.policy_loss_logits(x, y2, old, adv, cu_of([300, 400]), workspace=ws)
+    assert torch.isnan(stats[0]) and torch.isnan(logp[row]) and torch.isnan(dx[row]).all()
+    rest = torch.arange(T, device="cuda") != row
+    assert torch.equal(dx[rest], dgood[rest])

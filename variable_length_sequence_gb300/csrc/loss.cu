@@ -198,64 +198,89 @@ __global__ void __launch_bounds__(kPrepThreads) policy_stats_kernel(const float*
 
 // One pair of documents a block: both sums, the pair's loss, and its gradient over the
 // documents' rows; the blocks together clear the rows behind the last document.
-__global__ void __launch_bounds__(kThreads) preference_kernel(const __grid_constant__ PreferenceArgs a) {
-  __shared__ Sum2 s_sum[2][kThreads / 32];
-  __shared__ int s_count[2][kThreads / 32];
+constexpr int kPairThreads = 512, kPairWarps = kPairThreads / 32;
+__global__ void __launch_bounds__(kPairThreads) preference_kernel(const __grid_constant__ PreferenceArgs a) {
+  __shared__ Sum2 s_sum[2][kPairWarps];
+  __shared__ int s_count[2][kPairWarps];
+  __shared__ float s_grad[2];
   const int pairs = a.ndoc / 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_trigger();
   for (int i = blockIdx.x; i < pairs; i += gridDim.x) {
     const int64_t at[3] = {__ldg(a.cu + 2 * i), __ldg(a.cu + 2 * i + 1), __ldg(a.cu + 2 * i + 2)};
     const bool bad = at[0] > at[1] || at[1] > at[2] || at[0] < 0 || (i == 0 && at[0] != 0);
     if (threadIdx.x == 0) a.terms[2 * (int64_t)pairs + i] = bad ? 1.f : 0.f;
     if (bad) continue;
-    double score[2];
-    int count[2];
-    __syncthreads();                   // (the last pair's sums have been read)
+    __syncthreads();                   // (the last pair's sums and gradients have been read)
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t hi = min(at[k + 1], a.rows);
       Sum2 x = {0.f, 0.f};
       int n = 0;
-      for (int64_t t = at[k] + threadIdx.x; t < hi; t += kThreads)
-        if (__ldg(a.targets + t) >= 0) {
-          x.add(__ldg(a.logp + t));
-          if (a.ref_logp) x.add(-__ldg(a.ref_logp + t));
-          ++n;
-        }
+      // (loaded whether scored or not, so that the loads do not wait for one another)
+#pragma unroll 4
+      for (int64_t t = at[k] + threadIdx.x; t < hi; t += kPairThreads) {
+        const int y = __ldg(a.targets + t);
+        const float l = __ldg(a.logp + t), r = a.ref_logp ? __ldg(a.ref_logp + t) : 0.f;
+        x.add(y >= 0 ? l : 0.f);
+        x.add(y >= 0 ? -r : 0.f);
+        n += y >= 0;
+      }
       n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) s_count[k][warp] = n;
-      score[k] = block_sum<kThreads / 32>(x, s_sum[k]).value();
-      count[k] = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? s_count[k][lane] : 0);
-      if (a.average) score[k] /= max(1, count[k]);
+      x = warp_sum(x);
+      if (lane == 0) {
+        s_count[k][warp] = n;
+        s_sum[k][warp] = x;
+      }
     }
-    const double beta = a.beta, h = beta * (score[0] - score[1]) - a.margin;
-    double loss, dh;
-    if (a.kind == NSP_PREFERENCE_SIGMOID) {
-      const double e = exp(-fabs(h)), low = log1p(e);          // log(1 + exp(-|h|))
-      const double down = low + fmax(-h, 0.0), up = low + fmax(h, 0.0);   // -log sigmoid(+-h)
-      loss = (1.0 - a.smoothing) * down + a.smoothing * up;
-      dh = a.smoothing - (h > 0 ? e : 1.0) / (1.0 + e);        // smoothing - sigmoid(-h)
-    } else if (a.kind == NSP_PREFERENCE_HINGE) {
-      loss = h < 1.0 ? 1.0 - h : (h >= 1.0 ? 0.0 : h);         // (NaN stays)
-      dh = h < 1.0 ? -1.0 : (h >= 1.0 ? 0.0 : h);
-    } else {
-      const double off = h / beta - 0.5 / beta;
-      loss = off * off;
-      dh = 2.0 * off / beta;
+    __syncthreads();
+    if (warp == 0) {
+      double score[2];
+      int count[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        Sum2 x = {0.f, 0.f};
+        if (lane < kPairWarps) x = s_sum[k][lane];
+        score[k] = warp_sum(x).value();
+        count[k] = max(1, __reduce_add_sync(0xffffffffu, lane < kPairWarps ? s_count[k][lane] : 0));
+        if (a.average) score[k] /= count[k];
+      }
+      // (one thread: float64 units are few)
+      if (lane == 0) {
+        const double beta = a.beta, h = beta * (score[0] - score[1]) - a.margin;
+        double loss, dh;
+        if (a.kind == NSP_PREFERENCE_SIGMOID) {
+          const double e = exp(-fabs(h)), low = log1p(e);          // log(1 + exp(-|h|))
+          const double down = low + fmax(-h, 0.0), up = low + fmax(h, 0.0);   // -log sigmoid(+-h)
+          loss = (1.0 - a.smoothing) * down + a.smoothing * up;
+          dh = a.smoothing - (h > 0 ? e : 1.0) / (1.0 + e);        // smoothing - sigmoid(-h)
+        } else if (a.kind == NSP_PREFERENCE_HINGE) {
+          loss = h < 1.0 ? 1.0 - h : (h >= 1.0 ? 0.0 : h);         // (NaN stays)
+          dh = h < 1.0 ? -1.0 : (h >= 1.0 ? 0.0 : h);
+        } else {
+          const double off = h / beta - 0.5 / beta;
+          loss = off * off;
+          dh = 2.0 * off / beta;
+        }
+        a.terms[i] = (float)loss;
+        a.terms[pairs + i] = score[0] > score[1] ? 1.f : 0.f;
+        a.rewards[2 * (int64_t)i] = (float)(beta * score[0]);
+        a.rewards[2 * (int64_t)i + 1] = (float)(beta * score[1]);
+        for (int k = 0; k < 2; ++k)
+          s_grad[k] = (float)((k ? -dh : dh) * beta / pairs / (a.average ? count[k] : 1));
+      }
     }
-    if (threadIdx.x == 0) {
-      a.terms[i] = (float)loss;
-      a.terms[pairs + i] = score[0] > score[1] ? 1.f : 0.f;
-      a.rewards[2 * (int64_t)i] = (float)(beta * score[0]);
-      a.rewards[2 * (int64_t)i + 1] = (float)(beta * score[1]);
-    }
+    __syncthreads();
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t hi = min(at[k + 1], a.rows);
-      const float g = (float)((k ? -dh : dh) * beta / pairs / (a.average ? max(1, count[k]) : 1));
-      for (int64_t t = at[k] + threadIdx.x; t < hi; t += kThreads)
+      const float g = s_grad[k];
+#pragma unroll 4
+      for (int64_t t = at[k] + threadIdx.x; t < hi; t += kPairThreads)
         a.dlogp[t] = __ldg(a.targets + t) >= 0 ? g : 0.f;
     }
   }
-  for (int64_t t = max((int64_t)0, (int64_t)__ldg(a.cu + a.ndoc)) + (int64_t)blockIdx.x * kThreads + threadIdx.x;
-       t < a.rows; t += (int64_t)gridDim.x * kThreads)
+  for (int64_t t = max((int64_t)0, (int64_t)__ldg(a.cu + a.ndoc)) + (int64_t)blockIdx.x * kPairThreads + threadIdx.x;
+       t < a.rows; t += (int64_t)gridDim.x * kPairThreads)
     a.dlogp[t] = 0.f;
 }
 
@@ -265,10 +290,10 @@ __global__ void __launch_bounds__(kPrepThreads) preference_stats_kernel(const fl
   __shared__ Sum2 s_sum[3][kPrepThreads / 32];
   grid_dep_wait();
   Sum2 sum[3] = {};
-  for (int i = 0; i < 3; ++i) {
-    for (int t = threadIdx.x; t < pairs; t += kPrepThreads) sum[i].add(__ldcg(terms + (int64_t)i * pairs + t));
-    sum[i] = block_sum<kPrepThreads / 32>(sum[i], s_sum[i]);
-  }
+#pragma unroll 2
+  for (int t = threadIdx.x; t < pairs; t += kPrepThreads)
+    for (int i = 0; i < 3; ++i) sum[i].add(__ldcg(terms + (int64_t)i * pairs + t));
+  for (int i = 0; i < 3; ++i) sum[i] = block_sum<kPrepThreads / 32>(sum[i], s_sum[i]);
   if (threadIdx.x != 0) return;
   hdr->status = sum[2].hi != 0.f ? NSP_ERR_INVALID : NSP_OK;
   stats[0] = (float)(sum[0].value() / pairs);
@@ -328,8 +353,8 @@ cudaError_t launch_policy_stats(const RowArgs& a, float* stats, cudaStream_t s) 
 
 cudaError_t launch_preference(const PreferenceArgs& a, cudaStream_t s) {
   const int pairs = a.ndoc / 2;
-  const int blocks = (int)std::min<int64_t>(pairs, (int64_t)num_sms() * 8);
-  preference_kernel<<<blocks, kThreads, 0, s>>>(a);
+  const int blocks = (int)std::min<int64_t>(pairs, (int64_t)num_sms() * 4);
+  preference_kernel<<<blocks, kPairThreads, 0, s>>>(a);
   count_launches(1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -403,16 +403,27 @@ __device__ __forceinline__ float element(const uint4& u, int k) {
   return x;
 }
 
-// Scores alone: a row a block, in groups of kGroup vectors of a thread.
+// Scores alone: a row a block, in groups of kGroup vectors of a thread.  A warp leaves its
+// part of a row in shared memory and goes on; one warp of the block, another for every
+// row, waits for the others' parts at one of kOpen barriers and joins them.  Before a
+// barrier and its places are used again the whole block meets.
+constexpr int kOpen = 8;
+__device__ __forceinline__ void arrive_at(int barrier, int threads) {
+  asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void wait_at(int barrier, int threads) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+}
 constexpr int kGroup = 4, kGroups = kScoreSlots / kGroup;
 template <typename T>
 __global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __grid_constant__ RowArgs a,
                                                                      const int groups) {
   constexpr int N = Vec<T>::N, kLogN = N == 8 ? 3 : 2;
   extern __shared__ __align__(16) uint4 s_ring[];
-  __shared__ float2 s_part[2][(kScoreThreads / 32)];
-  __shared__ float s_target[2];
-  __shared__ int2 s_queue[(kScoreThreads / 32)][16];
+  constexpr int kWarps = kScoreThreads / 32;
+  __shared__ float2 s_part[kOpen][kWarps];
+  __shared__ float s_target[kOpen];
+  __shared__ int2 s_queue[kWarps][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = a.scale * kLog2e;
   const uint64_t c2 = f2_pack(c, c);
@@ -429,11 +440,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __gr
   for (int i = 0; i < kGroups; ++i) copy_group(i * kGroup);
   int slot = 0;
   for (int taken = 0; taken < ahead.queued; ++taken) {
+    if (taken > 0 && taken % kOpen == 0) __syncthreads();
     __syncwarp();
     const int2 item = s_queue[warp][taken & 15];
     __syncwarp();
     const int64_t t = item.x;
-    const int y = item.y, par = taken & 1;
+    const int y = item.y, par = taken % kOpen;
     const Row<T> r = row_of<T>(a, t, 0, 0);
     const bool extra = tid < a.vocab - r.nvec * N;
     const int ecol = tid < r.head ? tid : r.nvec * N + tid;
@@ -461,14 +473,19 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __gr
     }
     if (tid == 0 && y >= a.vocab) s_target[par] = NAN;
     join_warp(m, s);
-    // (two sets of states in turn: a warp that writes the next row's but one has passed the
-    // next row's barrier, and so has warp 0, behind reading this row's)
     if (lane == 0) s_part[par][warp] = make_float2(m, s);
-    __syncthreads();
-    if (warp != 0) continue;
-    const float2 part = lane < (kScoreThreads / 32) ? s_part[par][lane] : make_float2(-INFINITY, 0.f);
-    m = part.x;
-    s = part.y;
+    __syncwarp();
+    if (warp != taken % kWarps) {
+      arrive_at(1 + par, kScoreThreads);
+      continue;
+    }
+    wait_at(1 + par, kScoreThreads);
+    m = -INFINITY;
+    s = 0.f;
+    if (lane < kWarps) {
+      m = s_part[par][lane].x;
+      s = s_part[par][lane].y;
+    }
     join_warp(m, s);
     const float rest2 = log2f(s);
     float logp = (fmaf(s_target[par], c, -m) - rest2) * kLn2;
