@@ -687,6 +687,9 @@ def _io(fn: str, dtype) -> int:
     return io
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on_device(fn: str, dtype, **tensors) -> int:
     """Every given tensor is of `dtype` and on the current CUDA device (the
     library takes bare pointers).  Returns that device's index."""
@@ -698,7 +701,7 @@ def _on_device(fn: str, dtype, **tensors) -> int:
         if at != dev:
             if at < 0:
                 raise ValueError(f"{fn}: {name} is not on a CUDA device")
-            dev = torch.cuda.current_device()
+            dev = _current_device()
             if at != dev:
                 raise ValueError(f"{fn}: {name} is on device {at}, the current one is {dev}")
         if t.dtype is not dtype:
@@ -734,6 +737,13 @@ def _new(stream, like, shape, dtype=None):
         with _owner(stream):
             return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
     return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+
+
+def _new_like(stream, like):
+    """A new packed tensor of `like`'s shape and type that belongs to `stream`."""
+    if stream is not None:
+        return _new(stream, like, like.shape)
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _token_stride(fn: str, name: str, t) -> int:
@@ -996,7 +1006,16 @@ def head_norm_bwd(x, dy, weight=None, gate=None, eps=1e-6, scale=1.0, workspace=
 
 # ----------------------------------------------------------------------------- packed post-training step
 
-_Qk1, _Qk2 = QkTensor * 1, QkTensor * 2
+
+def _at(a) -> int:
+    """Address of an array's elements."""
+    return a.buffer_info()[0]
+
+
+def _qk_words(x, weight, y, dy, dx, dweight, x_stride, y_stride, dx_stride, heads, groups):
+    """One nsp_qk_tensor_t as 64-bit words (built in a fraction of a structure's time)."""
+    return (x, weight or 0, y or 0, dy or 0, dx or 0, dweight or 0, x_stride, y_stride, dx_stride,
+            heads | groups << 32)
 
 
 def _qk_shapes(fn, q, k, cu_seqlens, freqs, wq, wk, layout, positions, q_groups, **more):
@@ -1045,26 +1064,29 @@ def qk_norm_rope(q, k, cu_seqlens, freqs, wq=None, wk=None, layout="half", mscal
     q_shape = (P, T, Hq // P, d) if P > 1 else (T, Hq, d)
     qo_stride = ko_stride = 0                     # (0: packed)
     if qo is None:
-        qo = _new(stream, q, q_shape)
+        qo = _new_like(stream, q) if P == 1 else _new(stream, q, q_shape)
     else:
         _shape(fn, "q_out", qo, q_shape)
         if P > 1:
             _ptr(qo)
         else:
             qo_stride = _token_stride(fn, "q_out", qo)
-    one = (q.data_ptr(), _ptr(wq), qo.data_ptr(), None, None, None, _token_stride(fn, "q", q),
-           qo_stride, 0, Hq, P)
+    words = _qk_words(q.data_ptr(), _ptr(wq), qo.data_ptr(), 0, 0, 0, _token_stride(fn, "q", q),
+                      qo_stride, 0, Hq, P)
+    n = 1
     if k is None:
-        ko, n, arr = None, 1, _Qk1(one)
+        ko = None
     else:
         if ko is None:
-            ko = _new(stream, k, k.shape)
+            ko = _new_like(stream, k)
         else:
             _shape(fn, "k_out", ko, k.shape)
             ko_stride = _token_stride(fn, "k_out", ko)
-        n, arr = 2, _Qk2(one, (k.data_ptr(), _ptr(wk), ko.data_ptr(), None, None, None,
-                               _token_stride(fn, "k", k), ko_stride, 0, k.shape[1], 1))
-    st = load().nsp_qk_norm_rope_fwd(C.addressof(arr), n, _ptr(cu_seqlens),
+        n = 2
+        words += _qk_words(k.data_ptr(), _ptr(wk), ko.data_ptr(), 0, 0, 0, _token_stride(fn, "k", k),
+                           ko_stride, 0, k.shape[1], 1)
+    arr = array.array("q", words)
+    st = load().nsp_qk_norm_rope_fwd(_at(arr), n, _ptr(cu_seqlens),
                                      0 if cu_seqlens is None else cu_seqlens.numel() - 1,
                                      _ptr(positions), int(start), T, d, 2 * freqs.numel(), _ptr(freqs),
                                      layout == "interleaved", mscale, eps, io, _stream_of(stream, dev))
@@ -1089,32 +1111,34 @@ def qk_norm_rope_bwd(q, k, dqr, dkr, cu_seqlens, freqs, wq=None, wk=None, layout
     _shape(fn, "dqr", dqr, (P, T, Hq // P, d) if P > 1 else (T, Hq, d))
     dq_stride = dk_stride = 0
     if dq is None:
-        dq = _new(stream, q, q.shape)
+        dq = _new_like(stream, q)
     else:
         _shape(fn, "dq", dq, q.shape)
         dq_stride = _token_stride(fn, "dq", dq)
-    dwq = None if wq is None else _new(stream, q, (d,))
-    dwk = None if wk is None else _new(stream, q, (d,))
-    one = (q.data_ptr(), _ptr(wq), None, _ptr(dqr) if P > 1 else dqr.data_ptr(), dq.data_ptr(),
-           _ptr(dwq), _token_stride(fn, "q", q), 0 if P > 1 else _token_stride(fn, "dqr", dqr),
-           dq_stride, Hq, P)
+    dwq = None if wq is None else _new_like(stream, wq)
+    dwk = None if wk is None else _new_like(stream, wk)
+    n = 1
+    words = _qk_words(q.data_ptr(), _ptr(wq), 0, _ptr(dqr) if P > 1 else dqr.data_ptr(), dq.data_ptr(),
+                      _ptr(dwq), _token_stride(fn, "q", q),
+                      0 if P > 1 else _token_stride(fn, "dqr", dqr), dq_stride, Hq, P)
     if k is None:
         if dkr is not None:
             raise ValueError(f"{fn}: dkr without k")
-        dk, n, arr = None, 1, _Qk1(one)
+        dk = None
     else:
         if dkr is None:
             raise ValueError(f"{fn}: k without dkr")
         _shape(fn, "dkr", dkr, k.shape)
         if dk is None:
-            dk = _new(stream, k, k.shape)
+            dk = _new_like(stream, k)
         else:
             _shape(fn, "dk", dk, k.shape)
             dk_stride = _token_stride(fn, "dk", dk)
-        n, arr = 2, _Qk2(one, (k.data_ptr(), _ptr(wk), None, dkr.data_ptr(), dk.data_ptr(), _ptr(dwk),
-                               _token_stride(fn, "k", k), _token_stride(fn, "dkr", dkr), dk_stride,
-                               k.shape[1], 1))
-    lib, at = load(), C.addressof(arr)
+        n = 2
+        words += _qk_words(k.data_ptr(), _ptr(wk), 0, dkr.data_ptr(), dk.data_ptr(), _ptr(dwk),
+                           _token_stride(fn, "k", k), _token_stride(fn, "dkr", dkr), dk_stride, k.shape[1], 1)
+    arr = array.array("q", words)
+    lib, at = load(), _at(arr)
     ws = _workspace(fn, stream, q, lib.nsp_qk_norm_rope_bwd_workspace_size(at, n, T, d), workspace)
     st = lib.nsp_qk_norm_rope_bwd(at, n, _ptr(cu_seqlens),
                                   0 if cu_seqlens is None else cu_seqlens.numel() - 1, _ptr(positions),
@@ -1314,7 +1338,7 @@ def _gradients(fn, grads, dev=None):
     if dev is None:
         if -1 in at:
             raise ValueError(f"{fn}: a gradient is not on a CUDA device")
-        dev = torch.cuda.current_device()
+        dev = _current_device()
     if at != {dev}:
         raise ValueError(f"{fn}: a gradient is not on the current device {dev}")
     if not all(map(_is_contiguous, grads)):
@@ -1324,11 +1348,6 @@ def _gradients(fn, grads, dev=None):
         raise TypeError(f"{fn}: unsupported dtype {grads[types.index(None)].dtype}")
     return (array.array("Q", map(_data_ptr, grads)), array.array("q", map(_numel, grads)),
             array.array("i", types), n, dev)
-
-
-def _at(a) -> int:
-    """Address of an array's elements."""
-    return a.buffer_info()[0]
 
 
 def grad_norm(grads, norm_type=2, unscale=1.0, workspace=None, stream=None):
