@@ -854,3 +854,313 @@ def test_policy_loss_logits_many_rows_edges(nsp):
     assert torch.isnan(stats[0]) and torch.isnan(logp[row]) and torch.isnan(dx[row]).all()
     rest = torch.arange(T, device="cuda") != row
     assert torch.equal(dx[rest], dgood[rest])
+
+
+def test_qk_norm_rope_far_rows(nsp):
+    """Offsets past 32 bits, both directions, in place."""
+    T, h, d = 270000, 64, 128                 # 2.2e9 elements
+    cu, fr, w = cu_of([T - 7, 7]), nsp.rope_freqs(d, device="cuda"), randn(60, d)
+    x = torch.zeros((T, h, d), dtype=BF16, device="cuda")
+    x[-9:] = few = randn(61, 9, h, d)
+    pos = torch.tensor([T - 9, T - 8, 0, 1, 2, 3, 4, 5, 6], dtype=torch.int32, device="cuda")
+    y, _ = nsp.qk_norm_rope(x, None, cu, fr, w)
+    ref, _ = nsp.qk_norm_rope(few, None, None, fr, w, positions=pos)
+    assert torch.equal(y[-9:], ref) and not y[:-9].any()
+    dx = nsp.qk_norm_rope_bwd(x, None, y, None, cu, fr, w, out=(y, None))[0]
+    ref = nsp.qk_norm_rope_bwd(few, None, ref, None, None, fr, w, positions=pos)[0]
+    assert torch.equal(dx[-9:], ref) and not dx[:-9].any()
+
+
+# ----------------------------------------------------------------------------- all of them
+
+def step_calls(nsp, seed, T=700, V=4200, ws=None, stream=None):
+    """The operators on one set of inputs: [(name, call, outputs' number)]; ws: a workspace for each."""
+    lens = [T // 2, 0, T // 4, T - T // 2 - T // 4]
+    cu = cu_of(lens)
+    q, k = randn(seed, T, 6, 64), randn(seed + 1, T, 2, 64)
+    gq, gk, wq, wk = randn(seed + 2, T, 6, 64), randn(seed + 3, T, 2, 64), randn(seed + 4, 64), randn(seed + 5, 64)
+    fr = nsp.rope_freqs(64, device="cuda")
+    y = scattered(seed + 6, T, V)
+    x, few = randn(seed + 7, T, V), randn(seed + 8, 40, V)
+    y40, cu40 = y[:40].clone(), cu_of([13, 20])
+    logp = -torch.rand(T, generator=torch.Generator().manual_seed(seed)).cuda()
+    adv = randn(seed + 9, 4, dt=F32)
+    grads = [randn(seed + 10 + i, n, dt=(F32, BF16)[i % 2]) for i, n in enumerate((70000, 5, 4097, 33))]
+    st = dict(stream=stream)
+
+    def w(i):
+        return dict(st, workspace=None if ws is None else ws[i])
+    lse = nsp.token_logp(x, y)[1]
+    torch.cuda.synchronize()
+    return [lambda: nsp.qk_norm_rope(q, k, cu, fr, wq, wk, **st),
+            lambda: nsp.qk_norm_rope_bwd(q, k, gq, gk, cu, fr, wq, wk, **w(0)),
+            lambda: nsp.token_logp(x, y, **w(1)),
+            lambda: nsp.token_logp(few, y40, **w(2)),
+            lambda: (nsp.token_logp_bwd(x, y, lse, logp, **st),),
+            lambda: nsp.policy_loss(logp, y, logp * 0.9, adv, cu, ref=logp * 1.1, kl_coef=0.1, **w(3)),
+            lambda: nsp.policy_loss_logits(x, y, logp, adv, cu, ref=logp, kl_coef=0.1, **w(4)),
+            lambda: nsp.policy_loss_logits(few, y40, logp[:40], adv[:2], cu40, **w(5)),
+            lambda: nsp.preference_loss(logp, y, cu, ref=logp * 0.5, **w(6)),
+            lambda: (nsp.grad_norm(grads, **w(7)),),
+            lambda: (lambda o: (nsp.clip_grads(grads, 0.5, out=o, **w(8)), *o))([torch.empty_like(g) for g in grads])]
+
+
+def test_step_guard_zones(nsp):
+    """Workspaces of exactly the asked size, and what lies behind them and the outputs, in
+    arrays of one buffer one behind the other, stays as it was."""
+    import ctypes as C
+    lib = nsp.load()
+    T, V, lens = 700, 4200, [350, 0, 175, 175]
+    cu, y, x = cu_of(lens), scattered(130, T, V), randn(131, T, V)
+    logp, adv = -torch.rand(T, device="cuda"), torch.ones(4, device="cuda")
+    zone = 4096
+
+    def guarded(nbytes):
+        buf = torch.full((nbytes + 2 * zone,), 0xA5, dtype=torch.uint8, device="cuda")
+        return buf, buf[zone:zone + nbytes]
+
+    def intact(buf):
+        return bool((buf[:zone] == 0xA5).all()) and bool((buf[-zone:] == 0xA5).all())
+
+    q, gq, w = randn(132, T, 6, 64), randn(133, T, 6, 64), randn(134, 64)
+    fr = nsp.rope_freqs(64, device="cuda")
+    desc = (nsp.QkTensor * 1)(nsp.QkTensor(heads=6))
+    sizes = {"qk": lib.nsp_qk_norm_rope_bwd_workspace_size(C.addressof(desc), 1, T, 64),
+             "logp": lib.nsp_token_logp_workspace_size(T),
+             "policy": lib.nsp_policy_loss_workspace_size(T, 4, 0), "logits": lib.nsp_policy_loss_workspace_size(T, 4, 1),
+             "preference": lib.nsp_preference_loss_workspace_size(4)}
+    ws = {n: guarded(s) for n, s in sizes.items()}
+    ob, o = guarded(T * V * 2)
+    dx = o.view(torch.bfloat16).view(T, V)
+    qb, qo = guarded(T * 6 * 64 * 2)
+    dq = qo.view(torch.bfloat16).view(T, 6, 64)
+    nsp.qk_norm_rope_bwd(q, None, gq, None, cu, fr, w, out=(dq, None), workspace=ws["qk"][1])
+    nsp.token_logp(x, y, workspace=ws["logp"][1])
+    nsp.policy_loss(logp, y, logp, adv, cu, workspace=ws["policy"][1])
+    nsp.policy_loss_logits(x, y, logp, adv, cu, out=dx, workspace=ws["logits"][1])
+    nsp.preference_loss(logp, y, cu, workspace=ws["preference"][1])
+    grads = [randn(135, n) for n in (3, 5000, 40001)]
+    counts = (C.c_int64 * 3)(3, 5000, 40001)
+    ws["grad"] = guarded(lib.nsp_grad_norm_workspace_size(counts, 3))
+    outs = [guarded(g.numel() * 2) for g in grads]
+    nsp.clip_grads(grads, 0.1, out=[v.view(torch.bfloat16) for _, v in outs], workspace=ws["grad"][1])
+    torch.cuda.synchronize()
+    assert all([intact(b) for b, _ in list(ws.values()) + outs]) and intact(ob) and intact(qb)
+
+
+def test_step_captured_and_replayed(nsp):
+    """Every operator in one captured graph, replayed while eager calls run between: the
+    bits of the eager calls, as often as it is replayed."""
+    calls = step_calls(nsp, 140)
+    eager = [c() for c in calls]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for c in calls:
+            c()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [c() for c in calls]
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                if t is not None:
+                    t.fill_(-3.0)
+        graph.replay()
+        for c in calls:
+            c()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, eager)):
+            for s, t in zip(a, b):
+                assert (s is None and t is None) or torch.equal(s, t), i
+
+
+def test_step_two_streams(nsp):
+    """Two sets of inputs on two streams at once, each with its own workspaces, several times:
+    the bits of each alone."""
+    sets = [step_calls(nsp, 150), step_calls(nsp, 180, T=900, V=5001)]
+    alone = [[c() for c in calls] for calls in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [[], []]
+        for i in range(len(sets[0])):
+            for j in (0, 1):
+                with torch.cuda.stream(streams[j]):
+                    got[j].append(sets[j][i]())
+        torch.cuda.synchronize()
+        for j in (0, 1):
+            for i, (a, b) in enumerate(zip(got[j], alone[j])):
+                for s, t in zip(a, b):
+                    assert (s is None and t is None) or torch.equal(s, t), (j, i)
+
+
+def test_step_stream_argument(nsp):
+    """A given stream in place of the current one."""
+    side = torch.cuda.Stream()
+    alone = [c() for c in step_calls(nsp, 200)]
+    torch.cuda.synchronize()
+    got = [c() for c in step_calls(nsp, 200, stream=side)]
+    side.synchronize()
+    for a, b in zip(got, alone):
+        for s, t in zip(a, b):
+            assert (s is None and t is None) or torch.equal(s, t)
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+import test_step_gpu as t
+from variable_length_sequence_gb300 import nsp
+g = torch.cuda.CUDAGraph()
+q, w = t.randn(1, 300, 4, 64), t.randn(2, 64)
+cu, fr = t.cu_of([200, 100]), nsp.rope_freqs(64, device="cuda")
+x, y = t.randn(3, 700, 4200), t.scattered(4, 700, 4200)
+logp, adv, docs = -torch.rand(700, device="cuda"), torch.ones(2, device="cuda"), t.cu_of([300, 400])
+grads = [t.randn(5, 5000)]
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    a = nsp.qk_norm_rope_bwd(q, None, q, None, cu, fr, w)[0]
+    b = nsp.token_logp(x, y)[0]
+    c = nsp.policy_loss_logits(x, y, logp, adv, docs)[2]
+    d = nsp.preference_loss(logp, y, docs)[2]
+    e = nsp.grad_norm(grads)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(a, nsp.qk_norm_rope_bwd(q, None, q, None, cu, fr, w)[0])
+assert torch.equal(b, nsp.token_logp(x, y)[0])
+assert torch.equal(c, nsp.policy_loss_logits(x, y, logp, adv, docs)[2])
+assert torch.equal(d, nsp.preference_loss(logp, y, docs)[2])
+assert torch.equal(e, nsp.grad_norm(grads))
+print("same bits")
+"""
+
+
+def test_step_first_call_captured():
+    """A process whose first call of an operator is a captured one."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0 and "same bits" in r.stdout, r.stderr[-2000:]
+
+
+def model64(p, tokens, lens, heads, loss):
+    """An attention layer and its logits in float64; loss(logits) and its gradients."""
+    p = {n: v.detach().cpu().double().requires_grad_() for n, v in p.items()}
+    hq, hkv, d = heads
+    x = p["embed"][tokens]
+    T = len(tokens)
+    qkv = (x @ p["qkv"]).view(T, hq + 2 * hkv, d)
+    pos = torch.cat([torch.arange(n, dtype=torch.float64) for n in lens])
+    freqs = 10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
+    turn = torch.polar(torch.ones(T, d // 2, dtype=torch.float64), torch.outer(pos, freqs))[:, None]
+
+    def norm_rope(v, w):
+        n = v / torch.sqrt((v * v).mean(-1, keepdim=True) + 1e-6) * w
+        z = torch.complex(n[..., :d // 2], n[..., d // 2:]) * turn
+        return torch.cat([z.real, z.imag], -1)
+    q, k, v = norm_rope(qkv[:, :hq], p["wq"]), norm_rope(qkv[:, hq:hq + hkv], p["wk"]), qkv[:, hq + hkv:]
+    k, v = (t.repeat_interleave(hq // hkv, 1) for t in (k, v))
+    doc = torch.cat([torch.full((n,), i) for i, n in enumerate(lens)])
+    seen = (doc[:, None] == doc[None]) & torch.ones(T, T).tril().bool()
+    a = torch.einsum("thd,jhd->htj", q, k) * d ** -0.5
+    a = torch.softmax(a.masked_fill(~seen, float("-inf")), -1)
+    o = torch.einsum("htj,jhd->thd", a, v).reshape(T, hq * d)
+    value = loss((x + o @ p["out"]) @ p["embed"].T)
+    return value, dict(zip(p, torch.autograd.grad(value, list(p.values()))))
+
+
+@pytest.mark.parametrize("kind", ["policy", "preference"])
+def test_step_of_a_model(nsp, kind):
+    """A training step as it would be run, float32: fused projection, norm and rotation from
+    its columns, attention, logits, loss, all the way back into the fused projection's
+    gradient, and all gradients clipped: against float64 autograd of the whole, and against
+    differences of the float64 loss.  Everything is float32 with sums of at most 500 terms,
+    six matrix products deep: 1e-4 of each gradient's norm is 50 times the roundings of
+    such a sum of random terms (sqrt(500) E a product)."""
+    torch.backends.cuda.matmul.allow_tf32 = False
+    hq, hkv, d, D, V, lens = 4, 2, 64, 96, 300, [40, 1, 70, 33]
+    T = sum(lens)
+    gen = torch.Generator().manual_seed(7)
+    rand = lambda *s, scale=1.0: (torch.randn(s, generator=gen) * scale).cuda()  # noqa: E731
+    p = {"embed": rand(V, D), "qkv": rand(D, (hq + 2 * hkv) * d, scale=D ** -0.5), "out": rand(hq * d, D, scale=(hq * d) ** -0.5),
+         "wq": 1 + rand(d, scale=0.1), "wk": 1 + rand(d, scale=0.1)}
+    tokens = torch.randint(0, V, (T,), generator=gen)
+    cu = cu_of(lens)
+    targets = torch.cat([tokens[1:], tokens[:1]]).to(torch.int32)
+    first = 0
+    for n in lens:                          # prompts, and rows without a next token
+        targets[first:first + n // 3] = -1
+        targets[first + n - 1] = -1
+        first += n
+    fr = nsp.rope_freqs(d, device="cuda")
+    old, ref = rand(T, scale=0.1) - 6, rand(T, scale=0.3) - 6
+    adv = rand(len(lens))
+
+    x = p["embed"][tokens.cuda()]
+    qkv = (x @ p["qkv"]).view(T, hq + 2 * hkv, d)
+    q, k = nsp.qk_norm_rope(qkv[:, :hq], qkv[:, hq:hq + hkv], cu, fr, p["wq"], p["wk"])
+    v = qkv[:, hq + hkv:].contiguous()
+    out, lse = nsp.attn_fwd(q, k, v, cu)
+    h = x + out.view(T, -1) @ p["out"]
+    logits = h @ p["embed"].T
+    y = targets.cuda()
+    if kind == "policy":
+        old = nsp.token_logp(logits, y)[0] + 0.1 * (old + 6)
+        ref = old + 0.3 * (ref + 6)
+        stats, _, dlogits = nsp.policy_loss_logits(logits, y, old, adv, cu, ref=ref, kl_coef=0.1, mean="documents")
+    else:
+        logp, row_lse = nsp.token_logp(logits, y)
+        stats, _, dlogp = nsp.preference_loss(logp, y, cu, ref=ref, beta=0.1, smoothing=0.1)
+        dlogits = nsp.token_logp_bwd(logits, y, row_lse, dlogp)
+    dh = dlogits @ p["embed"]
+    grads = {"embed": dlogits.T @ h, "out": out.view(T, -1).T @ dh}
+    dout = (dh @ p["out"].T).view(T, hq, d).contiguous()
+    dq, dk, dv = nsp.attn_bwd(q, k, v, out, dout, lse, cu)
+    dqkv = torch.empty_like(qkv)
+    dqkv[:, hq + hkv:] = dv
+    _, _, grads["wq"], grads["wk"] = nsp.qk_norm_rope_bwd(
+        qkv[:, :hq], qkv[:, hq:hq + hkv], dq, dk, cu, fr, p["wq"], p["wk"], out=(dqkv[:, :hq], dqkv[:, hq:hq + hkv]))
+    dqkv = dqkv.view(T, -1)
+    grads["qkv"] = x.T @ dqkv
+    grads["embed"].index_add_(0, tokens.cuda(), dh + dqkv @ p["qkv"].T)
+    norm = nsp.clip_grads(list(grads.values()), 0.25, unscale=0.5)
+
+    yc, o64, r64, a64 = targets.long(), old.cpu().double(), ref.cpu().double(), adv.cpu().double()
+
+    def loss(z):
+        lp = torch.log_softmax(z, -1).gather(1, yc.clamp(min=0)[:, None])[:, 0]
+        parts, first, scores = [], 0, []
+        for b, n in enumerate(lens):
+            rows = [t for t in range(first, first + n) if yc[t] >= 0]
+            first += n
+            scores.append((lp[rows] - r64[rows]).sum())
+            if rows:
+                rho = torch.exp(lp[rows] - o64[rows])
+                far = r64[rows] - lp[rows]
+                pg = -torch.min(rho * a64[b], rho.clamp(0.8, 1.2) * a64[b])
+                parts.append((pg + 0.1 * (torch.exp(far) - far - 1)).mean())
+        if kind == "policy":
+            return torch.stack(parts).mean()
+        hs = 0.1 * (torch.stack(scores[0::2]) - torch.stack(scores[1::2]))
+        ls = torch.nn.functional.logsigmoid
+        return -(0.9 * ls(hs) + 0.1 * ls(-hs)).mean()
+
+    heads = (hq, hkv, d)
+    value, want = model64(p, tokens, lens, heads, loss)
+    assert abs(float(stats[0]) - float(value)) <= 1e-4 * max(1.0, abs(float(value)))
+    total = 0.5 * float(torch.sqrt(sum((g ** 2).sum() for g in want.values())))
+    assert abs(float(norm) - total) <= 1e-4 * total
+    factor = 0.5 * min(1.0, 0.25 / (total + 1e-6))
+    for n, g in want.items():
+        off = (grads[n].cpu().double() - factor * g).norm() / (factor * g).norm()
+        assert off <= 1e-4, (n, float(off))
+    # differences of the whole along a random direction of all parameters
+    dirs = {n: torch.randn(v.shape, generator=gen).double() for n, v in p.items()}
+    f = [float(model64({n: v.cpu().double() + s * dirs[n] for n, v in p.items()}, tokens, lens, heads, loss)[0])
+         for s in (1e-6, -1e-6)]
+    along = sum(float((grads[n].cpu().double() * dirs[n]).sum()) for n in p) / factor
+    size = sum(float((grads[n].cpu().double() * dirs[n]).norm()) for n in p) / factor
+    assert abs((f[0] - f[1]) / 2e-6 - along) <= 1e-3 * size
