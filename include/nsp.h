@@ -784,7 +784,7 @@ int32_t nsp_qk_norm_rope_bwd(const nsp_qk_tensor_t* tensors, int32_t n, const in
  *   logits: device [rows][vocab] of io_dtype, rows row_stride elements apart (0:
  *     vocab); targets: device int32 [rows]; a negative target is none: the row is
  *     not read, whatever it holds, its logp and lse are 0.  A target at or past
- *     vocab makes its logp NaN.  scale > 0: the inverse of a sampling temperature.
+ *     vocab makes its logp NaN.  scale in [1e-30, 1e30]: the inverse of a sampling temperature.
  *   logp, lse: device float32 [rows]; lse may be NULL.
  *   workspace: nsp_token_logp_workspace_size(rows) bytes.
  * Logits of minus infinity have probability zero (a row of nothing else, a NaN or
@@ -803,12 +803,12 @@ int32_t nsp_qk_norm_rope_bwd(const nsp_qk_tensor_t* tensors, int32_t n, const in
 size_t nsp_token_logp_workspace_size(int64_t rows);
 
 int32_t nsp_token_logp_fwd(const void* logits, int64_t row_stride, const int32_t* targets, int64_t rows,
-                           int32_t vocab, float scale, int32_t io_dtype, float* logp, float* lse,
+                           int32_t vocab, double scale, int32_t io_dtype, float* logp, float* lse,
                            void* workspace, size_t workspace_bytes, nsp_stream_t stream);
 
 int32_t nsp_token_logp_bwd(const void* logits, int64_t row_stride, const int32_t* targets,
                            const float* lse, const float* dlogp, int64_t rows, int32_t vocab,
-                           float scale, int32_t io_dtype, void* dlogits, int64_t out_stride,
+                           double scale, int32_t io_dtype, void* dlogits, int64_t out_stride,
                            nsp_stream_t stream);
 
 /* ------------------------------------------------------------------------
@@ -858,7 +858,7 @@ int32_t nsp_policy_loss(const float* logp, const int32_t* targets, const int32_t
 
 int32_t nsp_policy_loss_logits(const void* logits, int64_t row_stride, const int32_t* targets,
                                const int32_t* cu_seqlens, int32_t ndoc, int64_t rows, int32_t vocab,
-                               float scale, int32_t io_dtype, const nsp_policy_t* policy, float* stats,
+                               double scale, int32_t io_dtype, const nsp_policy_t* policy, float* stats,
                                float* logp, void* dlogits, int64_t out_stride, void* workspace,
                                size_t workspace_bytes, nsp_stream_t stream);
 

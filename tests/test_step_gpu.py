@@ -280,7 +280,9 @@ def check_dlogits(x, y, dlogp, got, dt, scale=SCALE, dlogp_err=0.0):
     c = (lse_error(x, scale) + 8 * E)[:, None]
     # the target's own column is 1 - p: p's error there is c (1 - (1 - p))
     col = np.where(np.arange(x.shape[1])[None] == y[:, None], 1.0, p)
-    tol = half_step(dt) * np.abs(ref) + np.abs(scale * g)[:, None] * (c * col + 4 * E * p + 2.0 ** -126)
+    # (a power of two below 2^-126 is zero; the sum that divides it is 1/2 or more, as its
+    # largest term's exponent is in (-1, 0]: a p below 2^-125 may be zero)
+    tol = half_step(dt) * np.abs(ref) + np.abs(scale * g)[:, None] * (c * col + 4 * E * p + 2.0 ** -125)
     tol = tol + np.broadcast_to(np.asarray(dlogp_err), (len(y),))[:, None] * p
     assert_within(got, ref, np.where(y[:, None] >= 0, tol, 0), "dlogits")
 
@@ -758,6 +760,43 @@ def test_token_logp_many_rows(nsp, dt, T, V, stride, shift):
     none = torch.full_like(y, -1)
     logp, lse = nsp.token_logp(x, none)
     assert not logp.any() and not lse.any()
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.8, float(np.log(2)), 2 * float(np.log(2)), 0.1, 1 / 3, 1.7, 3.0, 1e-3, 40.0])
+@pytest.mark.parametrize("T,V", [(5, 999), (2, 20000), (620, 4999)])
+def test_token_logp_scales(nsp, scale, T, V):
+    """Any temperature, whichever way its factor rounds; masked logits; forward and backward."""
+    x = randn(105, T, V, dt=F32, scale=2.0)
+    x[:, 7:40] = float("-inf")
+    y = torch.randint(0, V - 40, (T,), generator=torch.Generator().manual_seed(106), dtype=torch.int32).cuda()
+    y = torch.where(y < 7, y, y + 33)
+    logp, lse = nsp.token_logp(x, y, scale=scale)
+    check_logp(x, y, logp, lse, scale)
+    g = randn(107, T, dt=F32)
+    check_dlogits(x, y, g, nsp.token_logp_bwd(x, y, lse, g, scale=scale), F32, scale)
+    cu = cu_of([T])
+    stats, lp, dx = nsp.policy_loss_logits(x, y, logp, torch.ones(1, device="cuda"), cu, scale=scale)
+    check_logp(x, y, lp, None, scale)
+    # rho = 1 but for the log-probabilities' own errors: the gradient of -mean(logp)
+    err = 2 * lse_error(f64(x) * (np.abs(f64(x)) < 1e9), scale) + 8 * E * np.abs(f64(lp))
+    check_dlogits(x, y, np.full(T, -1.0 / T), dx, F32, scale, dlogp_err=scale * err / T)
+
+
+def test_token_logp_errors_do_not_lean(nsp):
+    """The mean error of thousands of log-probabilities, which a document's sum multiplies by
+    their number, is below one's own.  One is off by 3e-7 rms (the roundings of values near
+    10); what is the same for all is ex2's mean error, which is taken off as it is over
+    uniform arguments, and differs from that by at most its whole, 1e-7, elsewhere.  (One-
+    sided roundings of the scale or of the powers of two gave 2e-7 to 3e-7.)"""
+    T, V = 3000, 5001
+    x, _ = logits_of(108, T, V, BF16)
+    y = torch.arange(T, dtype=torch.int32, device="cuda")
+    for scale in (1.0, 0.8, 1 / 3, 0.9):
+        ref = S.token_logp(f64(x), y.cpu().numpy(), scale)[0]
+        for part in (slice(0, T), slice(0, 500)):
+            got = nsp.token_logp(x[part], y[part], scale=scale)[0]
+            lean = np.mean(f64(got) - ref[part])
+            assert abs(lean) <= 1e-7 + 3 * 3e-7 / np.sqrt(len(got)), (scale, part, lean)
 
 
 def test_token_logp_many_rows_special(nsp):

@@ -5,10 +5,10 @@
 // just computed (the row is then read once for both).  A row without a target
 // (y < 0) is not read; its logp, lse and gradient are zero.
 //
-// All in base 2: with c = s log2(e), a range's state is M = c max x (rounded once)
-// and S = sum 2^(c x - M), each term's argument one FMA of the unrounded c x; ranges
-// join by S1 2^(M1 - M) + S2 2^(M2 - M).  The same M serves the sum, logp and the
-// gradient, so that its rounding cancels.
+// All in base 2: with c = s log2(e) in two floats, a range's state is a whole number M
+// just above c max x and S = sum 2^(c x - M), each term's argument two FMAs; ranges join
+// by S1 2^(M1 - M) + S2 2^(M2 - M), whose powers are exact.  (c in one float and M = c max
+// x: every logp of a document was off to the same side, by 2e-7 to 3e-7.)
 //
 // A row is split over the blocks of a cluster, and a block's slice lives in its
 // threads' registers: one read of the logits, the sum, one exchange of (M, S)
@@ -27,12 +27,29 @@ using namespace tc;
 constexpr int kMaxRanks = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// 2^d of a whole d <= 0 (0 where it would be a denormal, and of -infinity).
+__device__ __forceinline__ float pow2(float d) {
+  return d >= -126.f ? __int_as_float(((int)d + 127) << 23) : 0.f;
+}
+
 // The sum of both ranges, in the first.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
   const float ref = top == -INFINITY ? 0.f : top;
-  s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
+  s = s * pow2(m - ref) + s2 * pow2(m2 - ref);
   m = top;
+}
+
+// logp and lse of a row whose sum is s 2^m.  Sums of a document's thousands of them are
+// what they are wanted for, so that their errors must not lean to one side: ex2 is too
+// small by 5.1e-8 of its value in the mean below zero (measured over [-30, 0]), and ln 2
+// is taken in two floats.
+constexpr float kBias = 5.1e-8f, kLn2Lo = (float)(0.69314718055994530942 - (double)kLn2);
+__device__ __forceinline__ float finish(float xy, const RowArgs& a, float m, float s, float& lse) {
+  const float l = log2f(s), d = fmaf(xy, a.c_lo, fmaf(xy, a.c, -m)) - l;
+  const float logp = d == -INFINITY ? d : fmaf(d, kLn2, fmaf(d, kLn2Lo, -kBias));
+  lse = fmaf(m + l, kLn2, fmaf(m + l, kLn2Lo, kBias));
+  return logp > 0.f ? 0.f : logp;  // (by its rounding; NaN stays)
 }
 
 template <typename T> struct Raw;
@@ -54,18 +71,33 @@ template <> struct Raw<__nv_bfloat16> {
   }
 };
 
+// c = s log2(e) in two floats, each twice.
+struct Scale2 {
+  uint64_t hi, lo;
+  __device__ __forceinline__ explicit Scale2(const RowArgs& a)
+      : hi(f2_pack(a.c, a.c)), lo(f2_pack(a.c_lo, a.c_lo)) {}
+};
+
 // sum of 2^(c x + n) over a vector, added to acc pair by pair
 template <typename T>
-__device__ __forceinline__ uint64_t add_exps(const uint4& u, uint64_t c2, uint64_t n2, uint64_t acc) {
+__device__ __forceinline__ uint64_t add_exps(const uint4& u, const Scale2& c, uint64_t n2, uint64_t acc) {
   float x[Vec<T>::N];
   Vec<T>::unpack(u, x);
 #pragma unroll
   for (int i = 0; i < Vec<T>::N / 2; ++i) {
+    const uint64_t v = f2_pack(x[2 * i], x[2 * i + 1]);
     float a, b;
-    f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), c2, n2), a, b);
+    f2_unpack(f2_fma(v, c.lo, f2_fma(v, c.hi, n2)), a, b);
     acc = f2_add(acc, f2_pack(ex2(a), ex2(b)));
   }
   return acc;
+}
+
+// c x + n for a gradient: bf16 ones need no more than c's first float.
+template <typename T>
+__device__ __forceinline__ uint64_t exponents(uint64_t v, const Scale2& c, uint64_t n2) {
+  const uint64_t z = f2_fma(v, c.hi, n2);
+  return sizeof(T) == 4 ? f2_fma(v, c.lo, z) : z;
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -131,8 +163,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
                     : make_uint4(Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf, Raw<T>::kNegInf);
   }
   const float xe = extra ? to_f(x[ecol]) : -INFINITY;
-  const float c = a.scale * kLog2e;
-  const uint64_t c2 = f2_pack(c, c);
+  const float c = a.c;
+  const Scale2 c2(a);
   float n, k, g;                     // p = 2^(c x + n) k;  d logit = s g ([j = y] - p)
   if constexpr (MODE == kRowBackward) {
     n = -__ldg(a.in_lse + t) * kLog2e;
@@ -145,10 +177,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
     float top = xe;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) top = fmaxf(top, Raw<T>::top(reg[i]));
-    float m = top * c;
+    float m = ceilf(top * c);
     auto ref = [](float m) { return m == -INFINITY ? 0.f : -m; };
     const uint64_t n2 = f2_pack(ref(m), ref(m));
-    uint64_t acc[2] = {f2_pack(ex2(fmaf(xe, c, ref(m))), 0.f), 0};
+    uint64_t acc[2] = {f2_pack(ex2(fmaf(xe, a.c_lo, fmaf(xe, c, ref(m)))), 0.f), 0};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) acc[i & 1] = add_exps<T>(reg[i], c2, n2, acc[i & 1]);
     float s, s1;
@@ -156,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
     s += s1;
     for (int v = v0 + VPT * THREADS + tid; v < v1; v += THREADS) {
       const uint4 u = ld_once(xv + v);
-      const float m1 = Raw<T>::top(u) * c;
+      const float m1 = ceilf(Raw<T>::top(u) * c);
       const uint64_t one = add_exps<T>(u, c2, f2_pack(ref(m1), ref(m1)), 0);
       float p0, p1;
       f2_unpack(one, p0, p1);
@@ -182,13 +214,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-    const float rest2 = log2f(s);
-    float logp = (fmaf(xy, c, -m) - rest2) * kLn2;
-    if (logp > 0.f) logp = 0.f;      // (by its rounding)
     const bool writes = rank == 0 && tid == 0;
+    float lse;
+    const float logp = finish(xy, a, m, s, lse);
     if (writes) {
       if (a.logp) a.logp[t] = logp;
-      if (a.lse) a.lse[t] = (m + rest2) * kLn2;
+      if (a.lse) a.lse[t] = lse;
     }
     if constexpr (MODE == kRowPolicy) {
       const PolicyRow r = policy_row(a.p, policy_scalars(a.p, t, doc), logp);
@@ -213,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
         float p, q;
-        f2_unpack(f2_fma(f2_pack(o[2 * i], o[2 * i + 1]), c2, n2), p, q);
+        f2_unpack(exponents<T>(f2_pack(o[2 * i], o[2 * i + 1]), c2, n2), p, q);
         f2_unpack(f2_mul(f2_pack(ex2(p), ex2(q)), f2), o[2 * i], o[2 * i + 1]);
       }
       if (v == yv) {
@@ -254,7 +285,7 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 __device__ __forceinline__ void join_warp(float& m, float& s) {
   float top;
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
-  s *= ex2(m - (top == -INFINITY ? 0.f : top));
+  s *= pow2(m - (top == -INFINITY ? 0.f : top));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   m = top;
@@ -371,6 +402,12 @@ struct RowCopies {
   }
 };
 
+// One element more.
+__device__ __forceinline__ void join_element(float& m, float& s, float x, const RowArgs& a) {
+  const float m1 = ceilf(x * a.c);
+  join(m, s, m1, m1 == -INFINITY ? 0.f : ex2(fmaf(x, a.c_lo, fmaf(x, a.c, -m1))));
+}
+
 // A thread's part of a row's sum, and the logit of the row's target if it is the thread's.
 template <typename T>
 struct RowSum {
@@ -378,13 +415,13 @@ struct RowSum {
 
   // G vectors more
   template <int G>
-  __device__ __forceinline__ void add(const uint4 (&u)[G], float c, uint64_t c2) {
+  __device__ __forceinline__ void add(const uint4 (&u)[G], float c, const Scale2& c2) {
     float top = Raw<T>::top(u[0]);
 #pragma unroll
     for (int i = 1; i < G; ++i) top = fmaxf(top, Raw<T>::top(u[i]));
-    const float m1 = fmaxf(m, top * c), n1 = m1 == -INFINITY ? 0.f : -m1;
+    const float m1 = fmaxf(m, ceilf(top * c)), n1 = m1 == -INFINITY ? 0.f : -m1;
     const uint64_t n2 = f2_pack(n1, n1);
-    uint64_t acc[2] = {f2_pack(s * ex2(m + n1), 0.f), 0};
+    uint64_t acc[2] = {f2_pack(s * pow2(m + n1), 0.f), 0};
     m = m1;
 #pragma unroll
     for (int i = 0; i < G; ++i) acc[i & 1] = add_exps<T>(u[i], c2, n2, acc[i & 1]);
@@ -425,8 +462,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __gr
   __shared__ float s_target[kOpen];
   __shared__ int2 s_queue[kWarps][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float c = a.scale * kLog2e;
-  const uint64_t c2 = f2_pack(c, c);
+  const float c = a.c;
+  const Scale2 c2(a);
   grid_dep_wait();
   RowCopies<T, kScoreThreads> ahead(a, 0, 0, s_ring + tid, s_queue[warp]);
   int g_ahead = 0;
@@ -468,7 +505,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __gr
     }
     float m = sum.m, s = sum.s;
     if (extra) {
-      join(m, s, xe * c, xe == -INFINITY ? 0.f : 1.f);
+      join_element(m, s, xe, a);
       if (ecol == y) s_target[par] = xe;
     }
     if (tid == 0 && y >= a.vocab) s_target[par] = NAN;
@@ -487,12 +524,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __gr
       s = s_part[par][lane].y;
     }
     join_warp(m, s);
-    const float rest2 = log2f(s);
-    float logp = (fmaf(s_target[par], c, -m) - rest2) * kLn2;
-    if (logp > 0.f) logp = 0.f;      // (by its rounding)
     if (lane == 0) {
-      a.logp[t] = logp;
-      if (a.lse) a.lse[t] = (m + rest2) * kLn2;
+      float row_lse;
+      a.logp[t] = finish(s_target[par], a, m, s, row_lse);
+      if (a.lse) a.lse[t] = row_lse;
     }
   }
 }
@@ -512,8 +547,8 @@ __global__ void __launch_bounds__(kPolicyThreads, 1) policy_ring_kernel(const __
   const int rank = (int)(blockIdx.x & (unsigned)(ranks - 1));
   grid_dep_wait();
   if (status_bad(a.p.hdr)) return;
-  const float c = a.scale * kLog2e;
-  const uint64_t c2 = f2_pack(c, c);
+  const float c = a.c;
+  const Scale2 c2(a);
   RowCopies<T, kPolicyThreads> ahead(a, rank, log_ranks, s_ring + tid, s_queue[warp]);
 #pragma unroll
   for (int i = 0; i < kPolicySlots; ++i) {
@@ -598,7 +633,7 @@ __global__ void __launch_bounds__(kPolicyThreads, 1) policy_ring_kernel(const __
 #undef NSP_WAIT_ADD
     float m = sum.m, s = sum.s;
     if (extra) {
-      join(m, s, xe * c, xe == -INFINITY ? 0.f : 1.f);
+      join_element(m, s, xe, a);
       if (ecol == y) publish(xe);
     }
     if (tid == 0 && rank == 0 && y >= a.vocab) publish(NAN);
@@ -619,9 +654,8 @@ __global__ void __launch_bounds__(kPolicyThreads, 1) policy_ring_kernel(const __
       s = 0.f;
       for (int i = lane; i < ranks * (kPolicyThreads / 32); i += 32) join(m, s, s_part[par][i].x, s_part[par][i].y);
       join_warp(m, s);
-      const float rest2 = log2f(s);
-      float logp = (fmaf(s_target[par].x, c, -m) - rest2) * kLn2;
-      if (logp > 0.f) logp = 0.f;      // (by its rounding)
+      float row_lse;
+      const float logp = finish(s_target[par].x, a, m, s, row_lse);
       const PolicyRow pr = policy_row(a.p, sc, logp);
       if (lane == 0) {
         const float sg = y < a.vocab ? a.scale * pr.grad : NAN;
@@ -650,7 +684,7 @@ __global__ void __launch_bounds__(kPolicyThreads, 1) policy_ring_kernel(const __
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
           float p, q;
-          f2_unpack(f2_fma(f2_pack(o[2 * j], o[2 * j + 1]), c2, n2), p, q);
+          f2_unpack(exponents<T>(f2_pack(o[2 * j], o[2 * j + 1]), c2, n2), p, q);
           f2_unpack(f2_mul(f2_pack(ex2(p), ex2(q)), ff), o[2 * j], o[2 * j + 1]);
         }
         if (i == mine) {

@@ -58,7 +58,7 @@ struct RowArgs {
   const int32_t* targets;
   int64_t rows;
   int32_t vocab;
-  float scale;
+  float scale, c, c_lo;                    // s; s log2(e) in two floats
   float *logp, *lse;                       // forward and policy: written (may be null)
   const float *in_lse, *dlogp;             // backward
   WsHeader* hdr;                           // forward and policy: workspace, n_items scored rows

@@ -101,8 +101,9 @@ int32_t qk_check(const nsp_qk_tensor_t* tensors, int32_t n, const int32_t* cu, i
 
 // Rows of logits and of their gradient.
 int32_t rows_check(const void* logits, int64_t row_stride, const int32_t* targets, int64_t rows,
-                   int32_t vocab, float scale, int32_t io_dtype, RowArgs& a) {
-  if (!dtype_ok(io_dtype) || rows < 0 || vocab < 1 || !scale_ok(scale)) return NSP_ERR_INVALID;
+                   int32_t vocab, double scale, int32_t io_dtype, RowArgs& a) {
+  // (what a float holds of it without loss of precision)
+  if (!dtype_ok(io_dtype) || rows < 0 || vocab < 1 || !(scale >= 1e-30) || !(scale <= 1e30)) return NSP_ERR_INVALID;
   if (rows > kMaxTokens || vocab > kMaxVocab) return NSP_ERR_UNSUPPORTED;
   if (row_stride == 0) row_stride = vocab;
   if (row_stride < vocab) return NSP_ERR_INVALID;
@@ -111,7 +112,12 @@ int32_t rows_check(const void* logits, int64_t row_stride, const int32_t* target
   if (!aligned(logits, elem_bytes(io_dtype)) || !aligned(targets, 4)) return NSP_ERR_ALIGN;
   a = {};
   a.logits = logits; a.row_stride = row_stride; a.targets = targets;
-  a.rows = rows; a.vocab = vocab; a.scale = scale;
+  a.rows = rows; a.vocab = vocab; a.scale = (float)scale;
+  const double c = scale * 1.44269504088896340736;
+  // (a remainder above zero: it meets logits of minus infinity)
+  a.c = (float)c;
+  while ((double)a.c >= c) a.c = std::nextafterf(a.c, 0.f);
+  a.c_lo = (float)(c - (double)a.c);
   return NSP_OK;
 }
 
@@ -240,7 +246,7 @@ size_t nsp_token_logp_workspace_size(int64_t rows) {
 }
 
 int32_t nsp_token_logp_fwd(const void* logits, int64_t row_stride, const int32_t* targets, int64_t rows,
-                           int32_t vocab, float scale, int32_t io_dtype, float* logp, float* lse,
+                           int32_t vocab, double scale, int32_t io_dtype, float* logp, float* lse,
                            void* workspace, size_t workspace_bytes, nsp_stream_t stream) {
   RowArgs a;
   const int32_t st = rows_check(logits, row_stride, targets, rows, vocab, scale, io_dtype, a);
@@ -263,7 +269,7 @@ int32_t nsp_token_logp_fwd(const void* logits, int64_t row_stride, const int32_t
 
 int32_t nsp_token_logp_bwd(const void* logits, int64_t row_stride, const int32_t* targets,
                            const float* lse, const float* dlogp, int64_t rows, int32_t vocab,
-                           float scale, int32_t io_dtype, void* dlogits, int64_t out_stride,
+                           double scale, int32_t io_dtype, void* dlogits, int64_t out_stride,
                            nsp_stream_t stream) {
   RowArgs a;
   int32_t st = rows_check(logits, row_stride, targets, rows, vocab, scale, io_dtype, a);
@@ -315,7 +321,7 @@ int32_t nsp_policy_loss(const float* logp, const int32_t* targets, const int32_t
 
 int32_t nsp_policy_loss_logits(const void* logits, int64_t row_stride, const int32_t* targets,
                                const int32_t* cu_seqlens, int32_t ndoc, int64_t rows, int32_t vocab,
-                               float scale, int32_t io_dtype, const nsp_policy_t* policy, float* stats,
+                               double scale, int32_t io_dtype, const nsp_policy_t* policy, float* stats,
                                float* logp, void* dlogits, int64_t out_stride, void* workspace,
                                size_t workspace_bytes, nsp_stream_t stream) {
   RowArgs a;

@@ -95,11 +95,11 @@ _SIGNATURES = {
     "nsp_qk_norm_rope_bwd": (_i32, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _vp, _i32,
                                     _f32, _f32, _i32, _vp, _sz, _vp]),
     "nsp_token_logp_workspace_size": (_sz, [_i64]),
-    "nsp_token_logp_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _f32, _i32, _vp, _vp, _vp, _sz, _vp]),
-    "nsp_token_logp_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _f32, _i32, _vp, _i64, _vp]),
+    "nsp_token_logp_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _f64, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "nsp_token_logp_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _f64, _i32, _vp, _i64, _vp]),
     "nsp_policy_loss_workspace_size": (_sz, [_i64, _i32, _i32]),
     "nsp_policy_loss": (_i32, [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
-    "nsp_policy_loss_logits": (_i32, [_vp, _i64, _vp, _vp, _i32, _i64, _i32, _f32, _i32, _vp, _vp, _vp,
+    "nsp_policy_loss_logits": (_i32, [_vp, _i64, _vp, _vp, _i32, _i64, _i32, _f64, _i32, _vp, _vp, _vp,
                                       _vp, _i64, _vp, _sz, _vp]),
     "nsp_preference_loss_workspace_size": (_sz, [_i32]),
     "nsp_preference_loss": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _f32, _f32, _f32, _i32, _vp,
