@@ -30,6 +30,10 @@ online softmax, no fusion), citing the page passage it follows:
   from R^{n x H x d} per rank to R^{N x h x d}, h = H/P (HSAP Sec. 2.2.2;
   BASP Sec. II-C "DeepSpeed Ulysses").
 
+* ``layer`` and ``step`` -- the operators of a differential attention layer and
+  of a packed post-training step, which no page has; their definitions are
+  those of the C header.
+
 Parity pins: every function here is checked by ``tests/test_oracle_*.py``
 against closed forms, invariants, library special cases and finite
 differences; none is "parity unpinned".

@@ -1,6 +1,12 @@
 // Losses of a packed stream over the log-probabilities of its scored rows (those
 // with a target): the clipped policy loss and the preference loss over pairs of
 // documents, each with its gradient.
+//
+// A few bytes a row: bound by launches and the latency of dependent loads.  One block
+// counts the scored rows (32 rows a word, a running count a word, so that any document's
+// count is two lookups) and writes the documents' weights: 6 us of 8192 rows.  A pair of
+// documents is one block: both sums, the loss in float64 by one thread, the gradient over
+// the rows: 10 us of 4099 rows.
 #include <algorithm>
 
 #include "policy.cuh"
