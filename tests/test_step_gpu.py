@@ -739,7 +739,10 @@ def logits_on(seed, y, V, dt, stride=None, shift=0):
 
 @pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("T,V,stride,shift", [(609, 4200, None, 0), (700, 4111, None, 3), (1300, 8192, 8200, 0),
-                                              (640, 20001, None, 1), (650, 33000, None, 0), (5000, 5003, None, 0)])
+                                              (640, 20001, None, 1), (650, 33000, None, 0), (5000, 5003, None, 0),
+                                              (609, 500, None, 0), (620, 1000, 1016, 5), (612, 6001, None, 0),
+                                              (611, 12000, None, 0), (610, 24000, None, 0), (640, 66000, None, 0),
+                                              (800, 40001, 40016, 2)])
 def test_token_logp_many_rows(nsp, dt, T, V, stride, shift):
     y = scattered(100, T, V)
     x, rows = logits_on(101, y, V, dt, stride, shift)
@@ -763,7 +766,7 @@ def test_token_logp_many_rows(nsp, dt, T, V, stride, shift):
 
 
 @pytest.mark.parametrize("scale", [1.0, 0.8, float(np.log(2)), 2 * float(np.log(2)), 0.1, 1 / 3, 1.7, 3.0, 1e-3, 40.0])
-@pytest.mark.parametrize("T,V", [(5, 999), (2, 20000), (620, 4999)])
+@pytest.mark.parametrize("T,V", [(5, 999), (2, 20000), (620, 4999), (610, 16500)])
 def test_token_logp_scales(nsp, scale, T, V):
     """Any temperature, whichever way its factor rounds; masked logits; forward and backward."""
     x = randn(105, T, V, dt=F32, scale=2.0)
@@ -778,7 +781,7 @@ def test_token_logp_scales(nsp, scale, T, V):
     stats, lp, dx = nsp.policy_loss_logits(x, y, logp, torch.ones(1, device="cuda"), cu, scale=scale)
     check_logp(x, y, lp, None, scale)
     # rho = 1 but for the log-probabilities' own errors: the gradient of -mean(logp)
-    err = 2 * lse_error(f64(x) * (np.abs(f64(x)) < 1e9), scale) + 8 * E * np.abs(f64(lp))
+    err = 2 * lse_error(f64(x), scale) + 8 * E * np.abs(f64(lp))
     check_dlogits(x, y, np.full(T, -1.0 / T), dx, F32, scale, dlogp_err=scale * err / T)
 
 
@@ -802,7 +805,7 @@ def test_token_logp_errors_do_not_lean(nsp):
 def test_token_logp_many_rows_special(nsp):
     """NaN, infinities and targets past the vocabulary stay in their rows, also where many
     rows are on their way at once."""
-    T, V = 700, 9000
+    T, V = 700, 17000
     x = randn(103, T, V, dt=F32)
     y = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(104), dtype=torch.int32).cuda()
     x[10, 5] = x[200, V - 1] = float("nan")
@@ -823,7 +826,10 @@ def test_token_logp_many_rows_special(nsp):
     (BF16, 612, 4200, None, 0, 1), (F32, 700, 4111, None, 3, 1), (BF16, 640, 20001, None, 1, 1),
     (F32, 620, 12288, None, 0, 1), (BF16, 1000, 33000, 33008, 0, 3), (F32, 310, 50001, None, 0, 2),
     (BF16, 330, 131072, None, 0, 4), (BF16, 320, 140001, None, 1, 5), (F32, 200, 140000, None, 0, 3),
-    (BF16, 160, 300001, None, 0, 4), (F32, 100, 200000, None, 0, 2), (BF16, 620, 49999, None, 0, 2)])
+    (BF16, 160, 300001, None, 0, 4), (F32, 100, 200000, None, 0, 2), (BF16, 620, 49999, None, 0, 2),
+    (F32, 640, 16389, None, 1, 3), (BF16, 620, 500, None, 0, 1), (BF16, 700, 1001, 1016, 3, 1),
+    (F32, 610, 1000, None, 0, 1), (F32, 612, 3001, None, 2, 1), (BF16, 615, 8190, None, 0, 1),
+    (F32, 612, 6002, None, 0, 2), (BF16, 611, 24001, 24008, 1, 2), (F32, 609, 16000, None, 0, 3)])
 @pytest.mark.parametrize("mean", ["documents", "tokens"])
 def test_policy_loss_logits_many_rows(nsp, dt, T, V, stride, shift, every, mean):
     """Rows shared by up to eight blocks, odd vocabularies at any distance from a 16-byte
@@ -873,7 +879,7 @@ def test_policy_loss_logits_many_rows(nsp, dt, T, V, stride, shift, every, mean)
 
 def test_policy_loss_logits_many_rows_edges(nsp):
     """Nothing scored, a bad cu_seqlens, a target past the vocabulary."""
-    T, V = 700, 5000
+    T, V = 700, 33000
     x = randn(120, T, V)
     y = scattered(121, T, V)
     old, adv = -torch.rand(T, device="cuda"), torch.ones(2, device="cuda")
@@ -912,7 +918,7 @@ def test_qk_norm_rope_far_rows(nsp):
 
 # ----------------------------------------------------------------------------- all of them
 
-def step_calls(nsp, seed, T=700, V=4200, ws=None, stream=None):
+def step_calls(nsp, seed, T=700, V=33000, ws=None, stream=None):
     """The operators on one set of inputs: [(name, call, outputs' number)]; ws: a workspace for each."""
     lens = [T // 2, 0, T // 4, T - T // 2 - T // 4]
     cu = cu_of(lens)
@@ -949,7 +955,7 @@ def test_step_guard_zones(nsp):
     arrays of one buffer one behind the other, stays as it was."""
     import ctypes as C
     lib = nsp.load()
-    T, V, lens = 700, 4200, [350, 0, 175, 175]
+    T, V, lens = 700, 33000, [350, 0, 175, 175]
     cu, y, x = cu_of(lens), scattered(130, T, V), randn(131, T, V)
     logp, adv = -torch.rand(T, device="cuda"), torch.ones(4, device="cuda")
     zone = 4096
@@ -1017,7 +1023,7 @@ def test_step_captured_and_replayed(nsp):
 def test_step_two_streams(nsp):
     """Two sets of inputs on two streams at once, each with its own workspaces, several times:
     the bits of each alone."""
-    sets = [step_calls(nsp, 150), step_calls(nsp, 180, T=900, V=5001)]
+    sets = [step_calls(nsp, 150), step_calls(nsp, 180, T=900, V=33001)]
     alone = [[c() for c in calls] for calls in sets]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -1053,7 +1059,7 @@ from variable_length_sequence_gb300 import nsp
 g = torch.cuda.CUDAGraph()
 q, w = t.randn(1, 300, 4, 64), t.randn(2, 64)
 cu, fr = t.cu_of([200, 100]), nsp.rope_freqs(64, device="cuda")
-x, y = t.randn(3, 700, 4200), t.scattered(4, 700, 4200)
+x, y = t.randn(3, 700, 33000), t.scattered(4, 700, 33000)
 logp, adv, docs = -torch.rand(700, device="cuda"), torch.ones(2, device="cuda"), t.cu_of([300, 400])
 grads = [t.randn(5, 5000)]
 torch.cuda.synchronize()
@@ -1189,7 +1195,8 @@ def test_step_of_a_model(nsp, kind):
 
     heads = (hq, hkv, d)
     value, want = model64(p, tokens, lens, heads, loss)
-    assert abs(float(stats[0]) - float(value)) <= 1e-4 * max(1.0, abs(float(value)))
+    value = float(value.detach())
+    assert abs(float(stats[0]) - value) <= 1e-4 * max(1.0, abs(value))
     total = 0.5 * float(torch.sqrt(sum((g ** 2).sum() for g in want.values())))
     assert abs(float(norm) - total) <= 1e-4 * total
     factor = 0.5 * min(1.0, 0.25 / (total + 1e-6))

@@ -801,9 +801,13 @@ bool policy_slice(int64_t nvec, int& log_ranks, int64_t& slice) {
   return slice <= kMaxSlice;
 }
 
-// Many rows of more than 8 KB go through the ring.
+// Many rows of more than 64 KB go through the ring.  Scores and policy step of rows 30 %
+// unscored, in us, ring against registers: 8000 rows of 1024 vectors 85 and 132 against 25
+// and 55; 4000 of 4096 50 and 115 against 44 and 99; 4000 of 5000 69 and 131 against 87 and
+// 161; 2000 of 16384 76 and 181 against 101 and 214 (bf16; float32 alike).
+constexpr int64_t kRingVectors = 4096;
 bool listed(const RowArgs& a, RowMode mode, int64_t nvec) {
-  if (mode == kRowBackward || nvec <= 512) return false;
+  if (mode == kRowBackward || nvec <= kRingVectors) return false;
   int log_ranks = 0;
   int64_t slice;
   if (mode == kRowPolicy && !policy_slice(nvec, log_ranks, slice)) return false;
@@ -822,15 +826,25 @@ cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
       policy_slice(nvec, log_ranks, slice);
       const cudaError_t e = launch_loss_rows(a, s);
       if (e != cudaSuccess) return e;
-      if (slice <= 2) return go_policy_ring<T, 2>(a, log_ranks, s);
-      if (slice <= 4) return go_policy_ring<T, 4>(a, log_ranks, s);
+      // (a ring's row is longer than four vectors of a thread)
       if (slice <= 6) return go_policy_ring<T, 6>(a, log_ranks, s);
       return go_policy_ring<T, 8>(a, log_ranks, s);
     }
   }
+  // Many rows: as few threads a row as hold it in eight vectors each, so that many rows are
+  // on an SM at once; a row longer than 64 KB over a cluster.
+  if (a.rows >= (int64_t)num_sms() * 4) {
+    if (nvec <= 64) return go<T, MODE, 32, 2>(a, 1, s);
+    if (nvec <= 128) return go<T, MODE, 32, 4>(a, 1, s);
+    if (nvec <= 256) return go<T, MODE, 64, 4>(a, 1, s);
+    if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
+    if (nvec <= 768) return go<T, MODE, 128, 6>(a, 1, s);
+    if (nvec <= 1024) return go<T, MODE, 128, 8>(a, 1, s);
+    if (nvec <= 1536) return go<T, MODE, 256, 6>(a, 1, s);
+    if (nvec <= 2048) return go<T, MODE, 256, 8>(a, 1, s);
+  }
   if (nvec <= 128) return go<T, MODE, 128, 1>(a, 1, s);
-  if (nvec <= 256) return go<T, MODE, 128, 2>(a, 1, s);
-  if (nvec <= 512) return go<T, MODE, 128, 4>(a, 1, s);
+  // Few: every SM a part of them.
   int ranks = 1;
   while (ranks < kMaxRanks && nvec > (int64_t)ranks * 4096) ranks *= 2;
   while (ranks < kMaxRanks && a.rows * ranks < (int64_t)num_sms() * 2 && nvec > (int64_t)ranks * 512) ranks *= 2;
@@ -839,6 +853,7 @@ cudaError_t launch_mode(const RowArgs& a, cudaStream_t s) {
   if (per <= 512) return go<T, MODE, 512, 1>(a, ranks, s);
   if (per <= 1024) return go<T, MODE, 512, 2>(a, ranks, s);
   if (per <= 2048) return go<T, MODE, 512, 4>(a, ranks, s);
+  if (per <= 512 * 6) return go<T, MODE, 512, 6>(a, ranks, s);
   return go<T, MODE, 512, 8>(a, ranks, s);
 }
 
