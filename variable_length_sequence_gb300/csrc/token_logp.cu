@@ -273,10 +273,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_kernel(const __gr
 // each).  Every thread copies its own vectors of the rows ahead into its own places of
 // shared memory, 192 KB of them at any time, and reads only what it copied itself, so
 // that the ring needs no barrier and no wait but the copies' own.
-// 8192 rows of 65536 bf16 logits (5730 scored): 129 us a call, 5.8 TB/s; a policy step on
+// 8192 rows of 65536 bf16 logits (5730 scored): 127 us a call, 5.9 TB/s; a policy step on
 // 8192 x 131072 of them, 30 % without a score: 656 us, 5.6 TB/s of logits read and
 // gradients written (row by row from registers: 344 and 1491 us).  In the way of more:
-// some 15 instructions an element, two exponentials among them, and a row's chain from
+// 10 instructions an element of the scores (80 % of the issue slots), twice that and two
+// exponentials of the policy step (60 %), and a row's chain from
 // its last vector over the cluster's exchange to the first gradient, under which a block
 // only copies.  512 threads and clusters twice as large: 718 us of the step; a row held in
 // registers in place of the ring: 867 us.
@@ -508,8 +509,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_ring_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
         u[i] = ahead.ring[(slot + i) * kScoreThreads];
-        if (mine == g * kGroup + i) s_target[par] = element<T>(u[i], (y - r.head) & (N - 1));
+
       }
+      if (mine >= g * kGroup && mine < (g + 1) * kGroup)
+        s_target[par] = element<T>(ahead.ring[(slot + mine - g * kGroup) * kScoreThreads], (y - r.head) & (N - 1));
       sum.add(u, c, c2);
       copy_group(slot);
       slot = slot + kGroup == kScoreSlots ? 0 : slot + kGroup;
