@@ -741,6 +741,8 @@ int32_t nsp_head_norm_bwd(const void* x, int64_t x_stride, const void* weight, c
  *     need their element's alignment; 16-byte aligned ones with strides, d
  *     and rot (halves: rot / 2) of whole 16-byte pieces are several times
  *     faster.
+ * A non-finite element makes its own row's results non-finite or zero, in any
+ * column, and in the backward dweight; no other row's.
  * The backward reads x and the gradient dy of y (y's stride and groups) and
  * writes, with z = dy rotated back and u = weight * z,
  *   dx = r (u - n mean(u n)), tokens dx_stride elements apart, and, unless
